@@ -70,7 +70,11 @@ enum {
     BASED_ERR_DEVICE_TIMEOUT = -9, /* a kernel gave up a bounded wait (based_device_status) */
     BASED_ERR_NO_DEVICE = -10,     /* no sm_103 device is current */
     BASED_ERR_BAD_ARGUMENT = -11,  /* any other invalid argument */
-    BASED_ERR_SCRATCH_LIMIT = -12  /* shape needs more than BASED_NOALLOC_SCRATCH_BYTES of scratch */
+    BASED_ERR_SCRATCH_LIMIT = -12, /* shape needs more than BASED_NOALLOC_SCRATCH_BYTES of scratch */
+    /* of the operators in based_ops.h */
+    BASED_ERR_UNSUPPORTED_TYPE = -13, /* an element type, or a pair of them, that the operator lacks */
+    BASED_ERR_BAD_SIZE = -14,         /* a size that is < 1, too large, or not a multiple where it must be */
+    BASED_ERR_BAD_STRIDE = -15        /* a negative stride */
 };
 
 /*

@@ -9,12 +9,13 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbased_gb300.so")
-SOURCES = [os.path.join(CSRC, "based_fwd.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("based_fwd.cu", "based_scan.cu", "based_norm.cu", "based_embed.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "based_kernels.cuh"), os.path.join(CSRC, "sm103_ptx.cuh"),
-                  os.path.join(CSRC, "based_plan.h"),
-                  os.path.join(ROOT, "include", "based.h")]
+                  os.path.join(CSRC, "based_plan.h"), os.path.join(CSRC, "ops_common.cuh"),
+                  os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-Xcompiler", "-fvisibility=hidden"]
+              "-Xcompiler", "-fPIC", "-shared", "-Xcompiler", "-fvisibility=hidden",
+              "--threads", "0"]  # the sources compile side by side
 
 
 def nvcc() -> str:

@@ -425,6 +425,17 @@ int noalloc_scratch(int dev, void **ptr) {
 
 }  // namespace
 
+namespace based {
+// What the other operators' host code shares with this file (ops_common.cuh).
+int host_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+int host_device(int *sms) {
+    int dev;
+    const int rc = current_device(&dev);
+    if (rc == BASED_OK) *sms = g_dev[dev].sms;
+    return rc;
+}
+}  // namespace based
+
 extern "C" {
 
 int based_fwd(const uint16_t *q, const uint16_t *k, const uint16_t *v, int B, int T, int H, int K,
@@ -665,6 +676,9 @@ const char *based_fwd_strerror(int code) {
         case BASED_ERR_BAD_ARGUMENT: return "invalid argument";
         case BASED_ERR_SCRATCH_LIMIT:
             return "shape needs more scratch than the fixed BASED_NOALLOC_SCRATCH_BYTES array";
+        case BASED_ERR_UNSUPPORTED_TYPE: return "element type, or pair of types, not supported";
+        case BASED_ERR_BAD_SIZE: return "size out of range";
+        case BASED_ERR_BAD_STRIDE: return "negative stride";
         default: return "unknown error code";
     }
 }
