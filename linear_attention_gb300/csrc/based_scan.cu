@@ -3,23 +3,31 @@
 //     h_t = a_t h_{t-1} + u_t    per batch entry and channel
 //
 // A stretch of rows acts on the state as the affine map h -> A h + H with A the product of its
-// decays and H the state it ends in from zero; two stretches compose as (A2 A1, A2 H1 + H2). The
-// kernels cut time into tiles, a tile's rows among the warps of a CTA, take each warp's map in one
-// pass over registers, compose the maps in front of each warp, and then run the rows from the
-// right state. Nothing but the inputs is read and nothing but the outputs is written.
+// decays and H the state it ends in from zero; two stretches compose as (A2 A1, A2 H1 + H2). Time
+// is cut into tiles of 64 rows. The CTAs of a cluster take the tiles in turn; each warp of a CTA
+// takes its rows' map in one pass over registers, the maps of a CTA's warps and of the cluster's
+// CTAs are exchanged through (distributed) shared memory, and every warp then runs its rows from
+// the state in front of them. So each input is read once and each output written once, however
+// few channels there are, and no CTA waits for one that may not be resident.
+#include <mutex>
+
 #include "ops_common.cuh"
 
 namespace based {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kSave = BASED_SCAN_SAVE_ROWS;
+constexpr int kTile = kSave;       // rows of a tile: one saved state each
+constexpr int kRowBytes = 128;     // a tile's row: 64 channels of 16 bits or 32 of 32
+constexpr int kMaxCluster = 16;
 
 struct ScanParams {
     const void *gate, *x, *dy;
     int64_t gate_sb, gate_st, x_sb, x_st, dy_sb, dy_st;
     int B, T, D, slabs;
+    int cluster;          // CTAs of a cluster
+    int word;             // bytes of a copy to shared memory that every row's start allows: 16, 4 or 2
+    int pair;             // two 16-bit outputs can be stored as one word
     const float *state;   // forward: h_{-1}; backward: dfinal
     const int32_t *lengths;
     void *y;              // forward: h; backward: dgate
@@ -40,201 +48,424 @@ __device__ __forceinline__ void decay(float g, float x, float &a, float &u) {
     }
 }
 
-// One CTA: 32 N channels of one batch entry, tiles of kWarps * R rows in turn. Lane: N channels;
-// warp w: rows [w R, w R + R) of a tile.
-template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) based_scan_fwd_kernel(const ScanParams p) {
-    constexpr int R = 16;
-    constexpr int kTile = R * kWarps;
-    using W = Pack<T, N>;
-    __shared__ float agg[2][kWarps][2 * N][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.slabs, c = (blockIdx.x % p.slabs) * 32 * N + lane * N;
-    const bool on = c < p.D;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    const int64_t plane = static_cast<int64_t>(b) * p.D + c;
-    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c;
-    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
-    const int n_saved = (p.T + kSave - 1) / kSave;
-    float carry[N];
+// ------------------------------------------------------------------------------------------------
+// Copies of a tile's rows into shared memory
+// ------------------------------------------------------------------------------------------------
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows [0, rows) of channels [0, cols) of a tensor at src into the tile at dst, by all THREADS
+// threads of the CTA. The other places keep what they held; nothing that is stored depends on it.
+template <typename T, int THREADS, int BYTES>
+__device__ __forceinline__ void copy_words(uint8_t *dst, const T *src, int64_t stride, int rows, int cols) {
+    constexpr int kPer = BYTES / static_cast<int>(sizeof(T)), kWords = kRowBytes / BYTES, kStep = THREADS / kWords;
+    const int col = static_cast<int>(threadIdx.x) % kWords, row0 = static_cast<int>(threadIdx.x) / kWords;
+    if (col * kPer >= cols) return;
+    const T *from = src + row0 * stride + col * kPer;
+    const uint32_t to = smem_u32(dst) + row0 * kRowBytes + col * BYTES;
 #pragma unroll
-    for (int j = 0; j < N; ++j) carry[j] = on && p.state ? p.state[plane + j] : 0.0f;
-    const int tiles = (p.T + kTile - 1) / kTile;
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int row0 = tile * kTile + warp * R;
-        float a[R][N], u[R][N], A[N], H[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) A[j] = 1.0f, H[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (on && row0 + i < len) {
-                const W g = *reinterpret_cast<const W *>(gate + (row0 + i) * p.gate_st);
-                const W v = *reinterpret_cast<const W *>(x + (row0 + i) * p.x_st);
-#pragma unroll
-                for (int j = 0; j < N; ++j) decay<MODE>(to_f32(g.v[j]), to_f32(v.v[j]), a[i][j], u[i][j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) a[i][j] = 1.0f, u[i][j] = 0.0f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                H[j] = fmaf(a[i][j], H[j], u[i][j]);
-                A[j] *= a[i][j];
-            }
-        float(&slot)[kWarps][2 * N][32] = agg[tile & 1];
-#pragma unroll
-        for (int j = 0; j < N; ++j) slot[warp][j][lane] = A[j], slot[warp][N + j][lane] = H[j];
-        __syncthreads();  // the two buffers alternate: one barrier a tile is enough
-        float h[N];
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (w == warp) h[j] = carry[j];
-                carry[j] = fmaf(slot[w][j][lane], carry[j], slot[w][N + j][lane]);
-            }
-        }
-        if (!on) continue;
-        if (p.saved && row0 % kSave == 0 && row0 < p.T) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                p.saved[(static_cast<int64_t>(b) * n_saved + row0 / kSave) * p.D + c + j] = h[j];
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if (row0 + i < p.T) {
-                W o;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    h[j] = fmaf(a[i][j], h[j], u[i][j]);
-                    o.v[j] = from_f32<T>(row0 + i < len ? h[j] : 0.0f);
-                }
-                *reinterpret_cast<W *>(y + static_cast<int64_t>(row0 + i) * p.D) = o;
-            }
-        }
+    for (int k = 0; k < kTile / kStep; ++k) {
+        if (row0 + k * kStep < rows) cp_async<BYTES>(to + k * kStep * kRowBytes, from);
+        from += kStep * stride;
     }
-    if (on && warp == 0 && p.final_state) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) p.final_state[plane + j] = carry[j];
+}
+template <typename T, int THREADS>
+__device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t stride, int rows, int cols, int word) {
+    if (word == 16) {
+        copy_words<T, THREADS, 16>(dst, src, stride, rows, cols);
+    } else if (word == 4) {
+        copy_words<T, THREADS, 4>(dst, src, stride, rows, cols);
+    } else {
+        // rows that start on an odd 16-bit element: no asynchronous copy is that narrow
+        constexpr int kCols = kRowBytes / sizeof(T);
+        for (int i = threadIdx.x; i < rows * kCols; i += THREADS)
+            if (i % kCols < cols) reinterpret_cast<T *>(dst)[i] = src[(i / kCols) * stride + i % kCols];
     }
 }
 
-// Backward: the tiles from the last to the first. With mu = what the rows after a row pass back to
-// it, lam_t = dy_t + mu and mu <- a_t lam_t: the map of a stretch in reversed time is mu -> A mu + M
-// with the same A. h inside a tile is rebuilt from the state saved before it.
-template <typename T, int N, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) based_scan_bwd_kernel(const ScanParams p) {
-    constexpr int R = kSave / kWarps;
+// ------------------------------------------------------------------------------------------------
+// Clusters
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The map h -> a h + b of N channels.
+template <int N>
+struct alignas(8 * N) Map {
+    float a[N], b[N];
+};
+template <int N>
+__device__ __forceinline__ void send(Map<N> *slot, uint32_t rank, const Map<N> &m) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(slot)), "r"(rank));
+    if (N == 2)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(m.a[0]), "f"(m.a[N - 1]),
+                     "f"(m.b[0]), "f"(m.b[N - 1])
+                     : "memory");
+    else
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m.a[0]), "f"(m.b[0]) : "memory");
+}
+// The maps of the cluster's CTAs, in the order of their tiles: `at` becomes the value in front of
+// tile `rank`, `carry` the one behind the last.
+template <int N>
+__device__ __forceinline__ void fold(const Map<N> (*maps)[32], int cluster, int rank, int lane, float (&at)[N], float (&carry)[N]) {
+    for (int r = 0; r < cluster; ++r) {
+        const Map<N> m = maps[r][lane];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            at[j] = r == rank ? carry[j] : at[j];
+            carry[j] = fmaf(m.a[j], carry[j], m.b[j]);
+        }
+    }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_channels(T *dst, const float (&v)[N], int n, int pair) {
+    if (N == 2 && pair) {
+        Pack<T, N> w;
+#pragma unroll
+        for (int j = 0; j < N; ++j) w.v[j] = from_f32<T>(v[j]);
+        *reinterpret_cast<Pack<T, N> *>(dst) = w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n) dst[j] = from_f32<T>(v[j]);
+    }
+}
+
+// Shared memory: the stages of the copies, the warps' maps, the cluster's maps (two of each, used in
+// turn, so that one barrier a tile orders their reuse).
+template <int N, int WARPS, int TENSORS, int STAGES>
+struct ScanSmem {
+    uint8_t tile[STAGES][TENSORS][kTile * kRowBytes];
+    Map<N> warp[2][WARPS][32];
+    float rev[2][WARPS][N][32];  // backward: the reversed map's increment
+    static constexpr size_t bytes(int cluster) { return sizeof(ScanSmem) + (cluster > 1 ? 2 * cluster * 32 * sizeof(Map<N>) : 0); }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Forward
+// ------------------------------------------------------------------------------------------------
+constexpr int kFwdWarps = 4, kFwdStages = 2;
+template <typename T>
+struct ScanCfg {
+    static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
+    using Fwd = ScanSmem<N, kFwdWarps, 2, kFwdStages>;
+};
+
+// A cluster: 32 N channels of one batch entry. Lane: N channels; warp w of the CTA: rows
+// [16 w, 16 w + 16) of its tile.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
+    constexpr int N = ScanCfg<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
+    using Smem = typename ScanCfg<T>::Fwd;
     using W = Pack<T, N>;
-    __shared__ float agg[2][kWarps][3 * N][32];
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    Map<N>(*maps)[32] = reinterpret_cast<Map<N>(*)[32]>(raw + sizeof(Smem));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.slabs, c = (blockIdx.x % p.slabs) * 32 * N + lane * N;
-    const bool on = c < p.D;
+    const int cs = p.cluster, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int slab = static_cast<int>(blockIdx.x / cs), b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
+    const int n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
     griddep_wait();
     griddep_launch_dependents();
     const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
     const int64_t plane = static_cast<int64_t>(b) * p.D + c;
-    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c;
-    const T *dy = static_cast<const T *>(p.dy) + b * p.dy_sb + c;
-    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
-    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(b) * p.T * p.D + c;
-    const int tiles = (p.T + kSave - 1) / kSave;
+    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c0;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c0;
+    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
+    const int tiles = (p.T + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;
     float carry[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) carry[j] = on && p.state ? p.state[plane + j] : 0.0f;
-    for (int tile = tiles - 1; tile >= 0; --tile) {
-        const int row0 = tile * kSave + warp * R;
-        float a[R][N], rest[R][N], v[R][N], d[R][N], before[R][N], h[N], A[N], H[N], M[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            A[j] = 1.0f, H[j] = 0.0f, M[j] = 0.0f;
-            h[j] = on ? p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] : 0.0f;
+    for (int j = 0; j < N; ++j) carry[j] = j < n && p.state ? p.state[plane + j] : 0.0f;
+    auto fetch = [&](int step) {
+        const int row = (step * cs + rank) * kTile, rows = min(len - row, kTile);
+        if (rows > 0) {
+            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, cols, p.word);
+            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, cols, p.word);
         }
+    };
+#pragma unroll
+    for (int k = 0; k < kFwdStages - 1; ++k) {
+        if (k < steps) fetch(k);
+        cp_async_commit();
+    }
+    if (cs > 1) {  // every CTA of the cluster runs before another one writes to its shared memory
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int step = 0; step < steps; ++step) {
+        const int tile = step * cs + rank, row0 = tile * kTile + warp * R;
+        cp_async_wait<kFwdStages - 2>();
+        __syncthreads();  // the tile has landed, and the stage before it is free
+        if (step + kFwdStages - 1 < steps) fetch(step + kFwdStages - 1);
+        cp_async_commit();
+        const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
+        const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * kRowBytes + lane * 4;
+        float a[R][N], u[R][N];
+        Map<N> m;
+#pragma unroll
+        for (int j = 0; j < N; ++j) m.a[j] = 1.0f, m.b[j] = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            if (on && row0 + i < len) {
-                const W wg = *reinterpret_cast<const W *>(gate + (row0 + i) * p.gate_st);
-                const W wx = *reinterpret_cast<const W *>(x + (row0 + i) * p.x_st);
-                const W wd = *reinterpret_cast<const W *>(dy + (row0 + i) * p.dy_st);
+            const W g = *reinterpret_cast<const W *>(sg + i * kRowBytes);
+            const W v = *reinterpret_cast<const W *>(sx + i * kRowBytes);
+            const bool live = row0 + i < len;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                decay<MODE>(to_f32(g.v[j]), to_f32(v.v[j]), a[i][j], u[i][j]);
+                a[i][j] = live ? a[i][j] : 1.0f;
+                u[i][j] = live ? u[i][j] : 0.0f;
+                m.b[j] = fmaf(a[i][j], m.b[j], u[i][j]);
+                m.a[j] *= a[i][j];
+            }
+        }
+        sm.warp[step & 1][warp][lane] = m;
+        __syncthreads();
+        // this warp's start as a map of the tile's start, then the tile's start itself
+        Map<N> pre, all;
+#pragma unroll
+        for (int j = 0; j < N; ++j) all.a[j] = 1.0f, all.b[j] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFwdWarps; ++w) {
+            const Map<N> o = sm.warp[step & 1][w][lane];
+            if (w == warp) pre = all;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                all.b[j] = fmaf(o.a[j], all.b[j], o.b[j]);
+                all.a[j] *= o.a[j];
+            }
+        }
+        float h[N];
+        if (cs > 1) {
+            Map<N>(*mine)[32] = maps + (step & 1) * cs;
+            for (int r = warp; r < cs; r += kFwdWarps) send(&mine[rank][lane], r, all);
+            cluster_arrive();
+            cluster_wait();
+            fold<N>(mine, cs, rank, lane, h, carry);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                h[j] = carry[j];
+                carry[j] = fmaf(all.a[j], carry[j], all.b[j]);
+            }
+        }
+        if (warp == 0 && p.saved && row0 < p.T) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n) p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] = h[j];
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[j] = fmaf(pre.a[j], h[j], pre.b[j]);
+        if (n > 0) {
+            T *to = y + static_cast<int64_t>(row0) * p.D;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float o[N];
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    if (MODE == BASED_GATE_LOG)
-                        a[i][j] = expf(to_f32(wg.v[j])), rest[i][j] = 1.0f;
-                    else
-                        sigmoid_pair(to_f32(wg.v[j]), a[i][j], rest[i][j]);
-                    v[i][j] = to_f32(wx.v[j]);
-                    d[i][j] = to_f32(wd.v[j]);
+                    h[j] = fmaf(a[i][j], h[j], u[i][j]);
+                    o[j] = row0 + i < len ? h[j] : 0.0f;
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) a[i][j] = 1.0f, rest[i][j] = 0.0f, v[i][j] = 0.0f, d[i][j] = 0.0f;
+                if (row0 + i < p.T) store_channels<T, N>(to, o, n, p.pair);
+                to += p.D;
             }
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                H[j] = fmaf(a[i][j], H[j], rest[i][j] * v[i][j]);
-                A[j] *= a[i][j];
-                const int k = R - 1 - i;
-                M[j] = a[k][j] * (d[k][j] + M[j]);
-            }
-        float(&slot)[kWarps][3 * N][32] = agg[tile & 1];
+    }
+    if (warp == 0 && rank == 0 && p.final_state) {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            slot[warp][j][lane] = A[j], slot[warp][N + j][lane] = H[j], slot[warp][2 * N + j][lane] = M[j];
-        __syncthreads();
-        float mu[N];
+            if (j < n) p.final_state[plane + j] = carry[j];
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Backward
+// ------------------------------------------------------------------------------------------------
+// The tiles from the last to the first. With mu = what the rows after a row pass back to it,
+// lam_t = dy_t + mu and mu <- a_t lam_t: the map of a stretch in reversed time is mu -> A mu + M
+// with the same A. h inside a tile is rebuilt from the state saved before it.
+constexpr int kBwdWarps = 8, kBwdStages = 3;
+template <typename T, int MODE>
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const ScanParams p) {
+    constexpr int N = ScanCfg<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
+    using Smem = ScanSmem<N, kBwdWarps, 3, kBwdStages>;
+    using W = Pack<T, N>;
+    extern __shared__ __align__(128) uint8_t raw[];
+    Smem &sm = *reinterpret_cast<Smem *>(raw);
+    Map<N>(*maps)[32] = reinterpret_cast<Map<N>(*)[32]>(raw + sizeof(Smem));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cs = p.cluster, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int slab = static_cast<int>(blockIdx.x / cs), b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
+    const int n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
+    griddep_wait();
+    griddep_launch_dependents();
+    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+    const int64_t plane = static_cast<int64_t>(b) * p.D + c;
+    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c0;
+    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c0;
+    const T *dy = static_cast<const T *>(p.dy) + b * p.dy_sb + c0;
+    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
+    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(b) * p.T * p.D + c;
+    const int tiles = (p.T + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;
+    float carry[N];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int k = kWarps - 1 - w;
+    for (int j = 0; j < N; ++j) carry[j] = j < n && p.state ? p.state[plane + j] : 0.0f;
+    auto fetch = [&](int step) {
+        const int row = (tiles - 1 - (step * cs + rank)) * kTile, rows = min(len - row, kTile);
+        if (row >= 0 && rows > 0) {
+            uint8_t(*to)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
+            copy_tile<T, kThreads>(to[0], gate + row * p.gate_st, p.gate_st, rows, cols, p.word);
+            copy_tile<T, kThreads>(to[1], x + row * p.x_st, p.x_st, rows, cols, p.word);
+            copy_tile<T, kThreads>(to[2], dy + row * p.dy_st, p.dy_st, rows, cols, p.word);
+        }
+    };
+    float next[N];  // the state in front of the next tile
+    auto fetch_state = [&](int step) {
+        const int tile = tiles - 1 - (step * cs + rank);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            next[j] = tile >= 0 && j < n ? p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] : 0.0f;
+    };
+    fetch_state(0);
+#pragma unroll
+    for (int k = 0; k < kBwdStages - 1; ++k) {
+        if (k < steps) fetch(k);
+        cp_async_commit();
+    }
+    if (cs > 1) {  // every CTA of the cluster runs before another one writes to its shared memory
+        cluster_arrive();
+        cluster_wait();
+    }
+    for (int step = 0; step < steps; ++step) {
+        const int tile = tiles - 1 - (step * cs + rank), row0 = tile * kTile + warp * R;
+        float h[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) h[j] = next[j];
+        cp_async_wait<kBwdStages - 2>();
+        __syncthreads();
+        if (step + kBwdStages - 1 < steps) fetch(step + kBwdStages - 1);
+        cp_async_commit();
+        fetch_state(step + 1);
+        const uint8_t(*st)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
+        const int off = warp * R * kRowBytes + lane * 4;
+        float a[R][N], rest[R][N], rev[N];
+        W v[R], d[R];
+        Map<N> m;
+#pragma unroll
+        for (int j = 0; j < N; ++j) m.a[j] = 1.0f, m.b[j] = 0.0f, rev[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const W g = *reinterpret_cast<const W *>(st[0] + off + i * kRowBytes);
+            v[i] = *reinterpret_cast<const W *>(st[1] + off + i * kRowBytes);
+            d[i] = *reinterpret_cast<const W *>(st[2] + off + i * kRowBytes);
+            const bool live = tile >= 0 && row0 + i < len;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (w < warp) h[j] = fmaf(slot[w][j][lane], h[j], slot[w][N + j][lane]);
-                if (k == warp) mu[j] = carry[j];
-                carry[j] = fmaf(slot[k][j][lane], carry[j], slot[k][2 * N + j][lane]);
+                if (MODE == BASED_GATE_LOG)
+                    a[i][j] = expf(to_f32(g.v[j])), rest[i][j] = 1.0f;
+                else
+                    sigmoid_pair(to_f32(g.v[j]), a[i][j], rest[i][j]);
+                if (!live) {
+                    a[i][j] = 1.0f, rest[i][j] = 0.0f;
+                    v[i].v[j] = from_f32<T>(0.0f);
+                    d[i].v[j] = from_f32<T>(0.0f);
+                }
+                m.b[j] = fmaf(a[i][j], m.b[j], rest[i][j] * to_f32(v[i].v[j]));
+                m.a[j] *= a[i][j];
             }
         }
-        if (!on) continue;
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) rev[j] = a[i][j] * (to_f32(d[i].v[j]) + rev[j]);
+        sm.warp[step & 1][warp][lane] = m;
+#pragma unroll
+        for (int j = 0; j < N; ++j) sm.rev[step & 1][warp][j][lane] = rev[j];
+        __syncthreads();
+        // the rows behind this warp's as a map, and the tile's map
+        Map<N> pre, all;
+#pragma unroll
+        for (int j = 0; j < N; ++j) all.a[j] = 1.0f, all.b[j] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kBwdWarps; ++k) {
+            const int w = kBwdWarps - 1 - k;
+            const Map<N> o = sm.warp[step & 1][w][lane], f = sm.warp[step & 1][k][lane];
+            if (w == warp) pre = all;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                all.b[j] = fmaf(o.a[j], all.b[j], sm.rev[step & 1][w][j][lane]);
+                all.a[j] *= o.a[j];
+                h[j] = k < warp ? fmaf(f.a[j], h[j], f.b[j]) : h[j];
+            }
+        }
+        float mu[N];
+        if (cs > 1) {
+            Map<N>(*mine)[32] = maps + (step & 1) * cs;
+            for (int r = warp; r < cs; r += kBwdWarps) send(&mine[rank][lane], r, all);
+            cluster_arrive();
+            cluster_wait();
+            fold<N>(mine, cs, rank, lane, mu, carry);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                mu[j] = carry[j];
+                carry[j] = fmaf(all.a[j], carry[j], all.b[j]);
+            }
+        }
+        float before[R][N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) mu[j] = fmaf(pre.a[j], mu[j], pre.b[j]);
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 before[i][j] = h[j];
-                h[j] = fmaf(a[i][j], h[j], rest[i][j] * v[i][j]);
+                h[j] = fmaf(a[i][j], h[j], rest[i][j] * to_f32(v[i].v[j]));
             }
+        if (n > 0 && tile >= 0) {
+            const int64_t at = static_cast<int64_t>(row0) * p.D;
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) {
-            if (row0 + i < p.T) {
-                W og, ox;
+            for (int i = R - 1; i >= 0; --i) {
+                float og[N], ox[N];
                 const bool live = row0 + i < len;
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    const float lam = d[i][j] + mu[j];
+                    const float lam = to_f32(d[i].v[j]) + mu[j];
                     mu[j] = a[i][j] * lam;
-                    float dg, dv;
                     if (MODE == BASED_GATE_LOG)
-                        dg = mu[j] * before[i][j], dv = lam;
+                        og[j] = mu[j] * before[i][j], ox[j] = lam;
                     else
-                        dg = mu[j] * rest[i][j] * (before[i][j] - v[i][j]), dv = rest[i][j] * lam;
-                    og.v[j] = from_f32<T>(live ? dg : 0.0f);
-                    ox.v[j] = from_f32<T>(live ? dv : 0.0f);
+                        og[j] = mu[j] * rest[i][j] * (before[i][j] - to_f32(v[i].v[j])), ox[j] = rest[i][j] * lam;
+                    og[j] = live ? og[j] : 0.0f;
+                    ox[j] = live ? ox[j] : 0.0f;
                 }
-                *reinterpret_cast<W *>(dgate + static_cast<int64_t>(row0 + i) * p.D) = og;
-                *reinterpret_cast<W *>(dx + static_cast<int64_t>(row0 + i) * p.D) = ox;
+                if (row0 + i < p.T) {
+                    store_channels<T, N>(dgate + at + static_cast<int64_t>(i) * p.D, og, n, p.pair);
+                    store_channels<T, N>(dx + at + static_cast<int64_t>(i) * p.D, ox, n, p.pair);
+                }
             }
         }
     }
-    if (on && warp == 0 && p.final_state) {
+    if (warp == 0 && rank == 0 && p.final_state) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) p.final_state[plane + j] = carry[j];
+        for (int j = 0; j < N; ++j)
+            if (j < n) p.final_state[plane + j] = carry[j];
     }
 }
 
@@ -283,7 +514,7 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
     if (!type_ok(dtype)) return BASED_ERR_UNSUPPORTED_TYPE;
     if (mode != BASED_GATE_LOG && mode != BASED_GATE_SIGMOID) return BASED_ERR_BAD_ARGUMENT;
     if (p.B < 1 || p.T < 1 || p.D < 1) return BASED_ERR_BAD_SIZE;
-    if (static_cast<int64_t>(p.B) * p.D >= (1ll << 31) || p.T > (1 << 30)) return BASED_ERR_BAD_SIZE;
+    if (static_cast<int64_t>(p.B) * p.D >= (1ll << 30) || p.T > (1 << 30)) return BASED_ERR_BAD_SIZE;
     if (p.gate_sb < 0 || p.gate_st < 0 || p.x_sb < 0 || p.x_st < 0 || p.dy_sb < 0 || p.dy_st < 0)
         return BASED_ERR_BAD_STRIDE;
     const size_t es = elem_size(dtype);
@@ -308,32 +539,60 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
     return BASED_OK;
 }
 
-template <typename T, int N>
-int launch_scan(ScanParams &p, int mode, bool bwd, cudaStream_t st) {
-    p.slabs = (p.D + 32 * N - 1) / (32 * N);
-    const dim3 grid(static_cast<unsigned>(p.slabs) * p.B);
-    if (bwd)
-        OPS_CUDA(launch_op(mode == BASED_GATE_LOG ? based_scan_bwd_kernel<T, N, BASED_GATE_LOG>
-                                                  : based_scan_bwd_kernel<T, N, BASED_GATE_SIGMOID>,
-                           grid, kThreads, 0, st, p));
-    else
-        OPS_CUDA(launch_op(mode == BASED_GATE_LOG ? based_scan_fwd_kernel<T, N, BASED_GATE_LOG>
-                                                  : based_scan_fwd_kernel<T, N, BASED_GATE_SIGMOID>,
-                           grid, kThreads, 0, st, p));
+// Once per kernel and process: its shared memory above 48 KB and clusters of 16.
+template <typename K>
+cudaError_t allow(K *kernel, size_t smem) {
+    static std::mutex m;
+    static K *done[32];
+    std::lock_guard<std::mutex> lk(m);
+    int i = 0;
+    for (; i < 32 && done[i]; ++i)
+        if (done[i] == kernel) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && i < 32) done[i] = kernel;
+    return e;
+}
+
+// per_sm: CTAs that an SM holds. Time is shared out among as many CTAs as there are slots and
+// tiles for, so that few channels fill the GPU too.
+template <typename T, typename Smem>
+int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int per_sm, int sms, cudaStream_t st) {
+    p.slabs = (p.D + 32 * ScanCfg<T>::N - 1) / (32 * ScanCfg<T>::N);
+    const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
+    p.cluster = 1;
+    while (p.cluster < kMaxCluster && p.cluster < tiles && blocks * p.cluster * 2 <= static_cast<int64_t>(sms) * per_sm)
+        p.cluster *= 2;
+    OPS_CUDA(allow(kernel, Smem::bytes(kMaxCluster)));
+    OPS_CUDA(launch_op(kernel, dim3(static_cast<unsigned>(blocks * p.cluster)), threads, Smem::bytes(p.cluster), st, p, p.cluster));
     return BASED_OK;
+}
+template <typename T>
+int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
+    const bool log = mode == BASED_GATE_LOG;
+    if (bwd)
+        return launch_scan<T, ScanSmem<ScanCfg<T>::N, kBwdWarps, 3, kBwdStages>>(
+            p, log ? based_scan_bwd_kernel<T, BASED_GATE_LOG> : based_scan_bwd_kernel<T, BASED_GATE_SIGMOID>,
+            32 * kBwdWarps, 2, sms, st);
+    return launch_scan<T, typename ScanCfg<T>::Fwd>(
+        p, log ? based_scan_fwd_kernel<T, BASED_GATE_LOG> : based_scan_fwd_kernel<T, BASED_GATE_SIGMOID>,
+        32 * kFwdWarps, 4, sms, st);
 }
 
 int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream) {
     int rc = check_scan(p, dtype, mode, bwd), sms;
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (dtype == BASED_F32) return launch_scan<float, 1>(p, mode, bwd, st);
-    // two 16-bit channels a lane where every row starts on a 4-byte boundary
-    const bool pair = ((p.D | p.gate_sb | p.gate_st | p.x_sb | p.x_st | p.dy_sb | p.dy_st) & 1) == 0 &&
-                      aligned(p.gate, 4) && aligned(p.x, 4) && aligned(p.dy, 4) && aligned(p.y, 4) && aligned(p.dx, 4);
-    if (dtype == BASED_BF16)
-        return pair ? launch_scan<__nv_bfloat16, 2>(p, mode, bwd, st) : launch_scan<__nv_bfloat16, 1>(p, mode, bwd, st);
-    return pair ? launch_scan<__half, 2>(p, mode, bwd, st) : launch_scan<__half, 1>(p, mode, bwd, st);
+    // the widest word that every row of every input starts on, and ends on
+    const int64_t es = static_cast<int64_t>(elem_size(dtype));
+    const int64_t bits = (p.D | p.gate_sb | p.gate_st | p.x_sb | p.x_st | p.dy_sb | p.dy_st) * es |
+                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.gate) | reinterpret_cast<uintptr_t>(p.x) |
+                                              reinterpret_cast<uintptr_t>(p.dy));
+    p.word = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    p.pair = p.D % 2 == 0 && aligned(p.y, 4) && aligned(p.dx, 4);
+    if (dtype == BASED_F32) return launch_scan<float>(p, mode, bwd, sms, st);
+    if (dtype == BASED_BF16) return launch_scan<__nv_bfloat16>(p, mode, bwd, sms, st);
+    return launch_scan<__half>(p, mode, bwd, sms, st);
 }
 
 template <typename T, int N>
