@@ -15,6 +15,7 @@
 #include "../../include/based.h"
 #include "based_kernels.cuh"
 #include "based_plan.h"
+#include "ops_common.cuh"
 
 namespace {
 
@@ -630,6 +631,9 @@ int based_device_status(int device, unsigned int *status, int clear) {
         const unsigned int zero = 0;
         e = cudaMemcpyToSymbol(based::g_status, &zero, sizeof(unsigned int));
     }
+    unsigned int scan = 0;
+    if (e == cudaSuccess) e = based::scan_status(&scan, clear != 0);
+    if (e == cudaSuccess && scan && !*status) *status = 1u | (64u << 8);  // the recurrence's cluster exchange: site 64
     if (device != prev) cudaSetDevice(prev);
     if (e != cudaSuccess) return cuda_fail(e, "status word");
     return BASED_OK;

@@ -9,7 +9,9 @@
 // CTAs are exchanged through (distributed) shared memory, and every warp then runs its rows from
 // the state in front of them. So each input is read once and each output written once, however
 // few channels there are, and no CTA waits for one that may not be resident.
+#include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -36,16 +38,21 @@ struct ScanParams {
     float *saved;         // forward: written; backward: read
 };
 
-template <int MODE>
-__device__ __forceinline__ void decay(float g, float x, float &a, float &u) {
+// The decay a and its complement 1 - a (unused for log decays), and the increment u.
+template <int MODE, int N>
+__device__ __forceinline__ void decay(Vec<N> g, Vec<N> &a, Vec<N> &rest) {
     if (MODE == BASED_GATE_LOG) {
-        a = expf(g);
-        u = x;
+#pragma unroll
+        for (int j = 0; j < N; ++j) g.v[j] = at_least(g.v[j], -120.0f);  // exp is 0 there
+        a = vexp(g, 1.0f);
+        rest = splat<N>(1.0f);
     } else {
-        float rest;
-        sigmoid_pair(g, a, rest);
-        u = rest * x;
+        vsigmoid(g, a, rest);
     }
+}
+template <int MODE, int N>
+__device__ __forceinline__ Vec<N> increment(const Vec<N> &rest, const Vec<N> &x) {
+    return MODE == BASED_GATE_LOG ? x : vmul(rest, x);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -94,204 +101,228 @@ __device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t st
 }
 
 // ------------------------------------------------------------------------------------------------
-// Clusters
+// Maps h -> a h + b of N channels, and their exchange in a cluster
 // ------------------------------------------------------------------------------------------------
+template <int N>
+struct alignas(8 * N) Map {
+    Vec<N> a, b;
+};
+template <int N>
+__device__ __forceinline__ Vec<N> apply(const Map<N> &m, const Vec<N> &h) {
+    return vfma(m.a, h, m.b);
+}
+template <int N>  // first `in`, then `m`
+__device__ __forceinline__ Map<N> compose(const Map<N> &m, const Map<N> &in) {
+    return {vmul(m.a, in.a), vfma(m.a, in.b, m.b)};
+}
+
+__device__ unsigned int g_scan_status;  // bit 0: a wait on the cluster's maps gave up
+constexpr uint64_t kScanWaitNs = 1000000000ull;
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// The map h -> a h + b of N channels.
-template <int N>
-struct alignas(8 * N) Map {
-    float a[N], b[N];
-};
-template <int N>
-__device__ __forceinline__ void send(Map<N> *slot, uint32_t rank, const Map<N> &m) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(slot)), "r"(rank));
-    if (N == 2)
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(m.a[0]), "f"(m.a[N - 1]),
-                     "f"(m.b[0]), "f"(m.b[N - 1])
-                     : "memory");
-    else
-        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m.a[0]), "f"(m.b[0]) : "memory");
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The maps of the cluster's CTAs, in the order of their tiles: `at` becomes the value in front of
-// tile `rank`, `carry` the one behind the last.
+
+// The maps of a cluster's tiles, two sets in turn. A CTA's warp sends its tile's map into every CTA
+// of the cluster with stores that count their bytes on that CTA's mbarrier: nothing else has to be
+// ordered or flushed, as a barrier of the whole cluster would.
 template <int N>
-__device__ __forceinline__ void fold(const Map<N> (*maps)[32], int cluster, int rank, int lane, float (&at)[N], float (&carry)[N]) {
-    for (int r = 0; r < cluster; ++r) {
-        const Map<N> m = maps[r][lane];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            at[j] = r == rank ? carry[j] : at[j];
-            carry[j] = fmaf(m.a[j], carry[j], m.b[j]);
+struct Exchange {
+    uint64_t full[2];
+    Map<N> maps[1][32];  // (2, cluster, 32)
+
+    static constexpr size_t bytes(int cluster) { return 16 + 2 * cluster * 32 * sizeof(Map<N>); }
+
+    __device__ __forceinline__ void init() {
+        mbar_init(smem_u32(&full[0]), 1);
+        mbar_init(smem_u32(&full[1]), 1);
+        fence_mbar_init();
+    }
+    // one warp: sends `m`, waits for the set of this step; returns false where the wait gave up
+    __device__ __forceinline__ bool swap(int step, int cluster, int rank, int lane, const Map<N> &m) {
+        const uint32_t bar = smem_u32(&full[step & 1]), slot = smem_u32(&maps[(step & 1) * cluster + rank][lane]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, cluster * 32 * sizeof(Map<N>));
+        for (int r = 0; r < cluster; ++r) {
+            uint32_t to, to_bar;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(slot), "r"(r));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
+            if (N == 2)
+                asm volatile(
+                    "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                    "f"(m.a.v[0]), "f"(m.a.v[N - 1]), "f"(m.b.v[0]), "f"(m.b.v[N - 1]), "r"(to_bar)
+                    : "memory");
+            else
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                             "f"(m.a.v[0]), "f"(m.b.v[0]), "r"(to_bar)
+                             : "memory");
+        }
+        const uint32_t parity = (step >> 1) & 1;
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t began = global_timer_ns();
+        while (!mbar_try_wait(bar, parity))
+            if (global_timer_ns() - began > kScanWaitNs) {
+                atomicOr(&g_scan_status, 1u);
+                return false;
+            }
+        return true;
+    }
+    // `at`: the value in front of tile `rank`; `carry` becomes the one behind the last tile
+    __device__ __forceinline__ void fold(int step, int cluster, int rank, int lane, Vec<N> &at, Vec<N> &carry) {
+        const Map<N>(*set)[32] = maps + (step & 1) * cluster;
+        at = carry;
+#pragma unroll 4
+        for (int r = 0; r < cluster; ++r) {
+            carry = apply(set[r][lane], carry);
+            if (r + 1 == rank) at = carry;
         }
     }
-}
+};
 
 template <typename T, int N>
-__device__ __forceinline__ void store_channels(T *dst, const float (&v)[N], int n, int pair) {
-    if (N == 2 && pair) {
-        Pack<T, N> w;
+__device__ __forceinline__ void store_some(T *dst, const Vec<N> &v, int n) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) w.v[j] = from_f32<T>(v[j]);
-        *reinterpret_cast<Pack<T, N> *>(dst) = w;
-    } else {
+    for (int j = 0; j < N; ++j)
+        if (j < n) dst[j] = from_f32<T>(v.v[j]);
+}
+template <int N>
+__device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < n) dst[j] = from_f32<T>(v[j]);
-    }
+    for (int j = 0; j < N; ++j) v.v[j] = src && j < n ? src[j] : 0.0f;
 }
 
-// Shared memory: the stages of the copies, the warps' maps, the cluster's maps (two of each, used in
-// turn, so that one barrier a tile orders their reuse).
-template <int N, int WARPS, int TENSORS, int STAGES>
-struct ScanSmem {
-    uint8_t tile[STAGES][TENSORS][kTile * kRowBytes];
-    Map<N> warp[2][WARPS][32];
-    float rev[2][WARPS][N][32];  // backward: the reversed map's increment
-    static constexpr size_t bytes(int cluster) { return sizeof(ScanSmem) + (cluster > 1 ? 2 * cluster * 32 * sizeof(Map<N>) : 0); }
+// What both kernels know about their place: 32 N channels of one batch entry for a cluster, N
+// channels for a lane; the cluster's CTAs take the tiles in turn.
+template <typename T>
+struct Place {
+    static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
+    int lane, warp, rank, b, c0, c, n, cols, tiles, steps;
+    __device__ __forceinline__ explicit Place(const ScanParams &p) {
+        lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+        const int slab = static_cast<int>(blockIdx.x) / p.cluster;
+        b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
+        n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
+        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) / p.cluster;
+    }
 };
 
 // ------------------------------------------------------------------------------------------------
 // Forward
 // ------------------------------------------------------------------------------------------------
+// Warp w of a CTA: rows [16 w, 16 w + 16) of its tile.
 constexpr int kFwdWarps = 4, kFwdStages = 2;
-template <typename T>
-struct ScanCfg {
-    static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
-    using Fwd = ScanSmem<N, kFwdWarps, 2, kFwdStages>;
+template <int N>
+struct FwdSmem {
+    uint8_t tile[kFwdStages][2][kTile * kRowBytes];
+    Map<N> warp[kFwdWarps][32];
+    Vec<N> start[kFwdWarps][32];
+    Exchange<N> ex;
+    static constexpr size_t bytes(int cluster) { return offsetof(FwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
 
-// A cluster: 32 N channels of one batch entry. Lane: N channels; warp w of the CTA: rows
-// [16 w, 16 w + 16) of its tile.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
-    constexpr int N = ScanCfg<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
-    using Smem = typename ScanCfg<T>::Fwd;
+    constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
     using W = Pack<T, N>;
     extern __shared__ __align__(128) uint8_t raw[];
-    Smem &sm = *reinterpret_cast<Smem *>(raw);
-    Map<N>(*maps)[32] = reinterpret_cast<Map<N>(*)[32]>(raw + sizeof(Smem));
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int cs = p.cluster, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int slab = static_cast<int>(blockIdx.x / cs), b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
-    const int n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
+    FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
+    const Place<T> at(p);
+    const int lane = at.lane, warp = at.warp, cs = p.cluster;
+    if (cs > 1) {
+        if (threadIdx.x == 0) sm.ex.init();
+        cluster_sync();  // every CTA's mbarriers are there before another CTA counts on them
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    const int64_t plane = static_cast<int64_t>(b) * p.D + c;
-    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c0;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c0;
-    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
-    const int tiles = (p.T + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;
-    float carry[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) carry[j] = j < n && p.state ? p.state[plane + j] : 0.0f;
+    const int len = p.lengths ? min(max(p.lengths[at.b], 0), p.T) : p.T;
+    const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
+    const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
+    const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
+    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
+    const bool wide = p.pair && at.n == N;
+    Vec<N> carry;  // warp 0's: the state in front of the cluster's tiles
+    load_state(p.state ? p.state + plane : nullptr, at.n, carry);
+    bool waiting = true;
     auto fetch = [&](int step) {
-        const int row = (step * cs + rank) * kTile, rows = min(len - row, kTile);
-        if (rows > 0) {
-            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, cols, p.word);
-            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, cols, p.word);
+        const int row = (step * cs + at.rank) * kTile, rows = min(len - row, kTile);
+        if (step < at.steps && rows > 0) {
+            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
         }
+        cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kFwdStages - 1; ++k) {
-        if (k < steps) fetch(k);
-        cp_async_commit();
-    }
-    if (cs > 1) {  // every CTA of the cluster runs before another one writes to its shared memory
-        cluster_arrive();
-        cluster_wait();
-    }
-    for (int step = 0; step < steps; ++step) {
-        const int tile = step * cs + rank, row0 = tile * kTile + warp * R;
-        cp_async_wait<kFwdStages - 2>();
-        __syncthreads();  // the tile has landed, and the stage before it is free
-        if (step + kFwdStages - 1 < steps) fetch(step + kFwdStages - 1);
-        cp_async_commit();
+    for (int k = 0; k < kFwdStages; ++k) fetch(k);
+    cp_async_wait<kFwdStages - 1>();
+    __syncthreads();
+    for (int step = 0; step < at.steps; ++step) {
+        const int tile = step * cs + at.rank, row0 = tile * kTile + warp * R;
         const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
         const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * kRowBytes + lane * 4;
-        float a[R][N], u[R][N];
-        Map<N> m;
-#pragma unroll
-        for (int j = 0; j < N; ++j) m.a[j] = 1.0f, m.b[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const W g = *reinterpret_cast<const W *>(sg + i * kRowBytes);
-            const W v = *reinterpret_cast<const W *>(sx + i * kRowBytes);
-            const bool live = row0 + i < len;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                decay<MODE>(to_f32(g.v[j]), to_f32(v.v[j]), a[i][j], u[i][j]);
-                a[i][j] = live ? a[i][j] : 1.0f;
-                u[i][j] = live ? u[i][j] : 0.0f;
-                m.b[j] = fmaf(a[i][j], m.b[j], u[i][j]);
-                m.a[j] *= a[i][j];
-            }
-        }
-        sm.warp[step & 1][warp][lane] = m;
-        __syncthreads();
-        // this warp's start as a map of the tile's start, then the tile's start itself
-        Map<N> pre, all;
-#pragma unroll
-        for (int j = 0; j < N; ++j) all.a[j] = 1.0f, all.b[j] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kFwdWarps; ++w) {
-            const Map<N> o = sm.warp[step & 1][w][lane];
-            if (w == warp) pre = all;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                all.b[j] = fmaf(o.a[j], all.b[j], o.b[j]);
-                all.a[j] *= o.a[j];
-            }
-        }
-        float h[N];
-        if (cs > 1) {
-            Map<N>(*mine)[32] = maps + (step & 1) * cs;
-            for (int r = warp; r < cs; r += kFwdWarps) send(&mine[rank][lane], r, all);
-            cluster_arrive();
-            cluster_wait();
-            fold<N>(mine, cs, rank, lane, h, carry);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                h[j] = carry[j];
-                carry[j] = fmaf(all.a[j], carry[j], all.b[j]);
-            }
-        }
-        if (warp == 0 && p.saved && row0 < p.T) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (j < n) p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] = h[j];
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j) h[j] = fmaf(pre.a[j], h[j], pre.b[j]);
-        if (n > 0) {
-            T *to = y + static_cast<int64_t>(row0) * p.D;
+        Vec<N> a[R], u[R];
+        const bool full = row0 + R <= len;
+        Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
+        auto rows = [&](auto all_live) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                float o[N];
+                Vec<N> rest;
+                decay<MODE>(to_vec(*reinterpret_cast<const W *>(sg + i * kRowBytes)), a[i], rest);
+                u[i] = increment<MODE>(rest, to_vec(*reinterpret_cast<const W *>(sx + i * kRowBytes)));
+                if (!decltype(all_live)::value && row0 + i >= len) a[i] = splat<N>(1.0f), u[i] = splat<N>(0.0f);
+                m = compose(Map<N>{a[i], u[i]}, m);
+            }
+        };
+        if (full)
+            rows(std::true_type());
+        else
+            rows(std::false_type());
+        sm.warp[warp][lane] = m;
+        __syncthreads();  // the maps are there, and this step's stage is free
+        fetch(step + kFwdStages);
+        if (warp == 0) {
+            Vec<N> h = carry;
+            Map<N> all[kFwdWarps];  // of the tile's rows up to each warp's last
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    h[j] = fmaf(a[i][j], h[j], u[i][j]);
-                    o[j] = row0 + i < len ? h[j] : 0.0f;
-                }
-                if (row0 + i < p.T) store_channels<T, N>(to, o, n, p.pair);
+            for (int w = 0; w < kFwdWarps; ++w) all[w] = w ? compose(sm.warp[w][lane], all[w - 1]) : sm.warp[w][lane];
+            if (cs > 1) {
+                if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[kFwdWarps - 1]);
+                sm.ex.fold(step, cs, at.rank, lane, h, carry);
+            } else {
+                carry = apply(all[kFwdWarps - 1], carry);
+            }
+            if (p.saved && tile < at.tiles)
+                store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, h, at.n);
+            sm.start[0][lane] = h;
+#pragma unroll
+            for (int w = 1; w < kFwdWarps; ++w) sm.start[w][lane] = apply(all[w - 1], h);
+        }
+        cp_async_wait<kFwdStages - 1>();
+        __syncthreads();  // the starts are there, and the next step's tile
+        Vec<N> h = sm.start[warp][lane];
+        T *to = y + static_cast<int64_t>(row0) * p.D;
+        if (full && wide) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                h = vfma(a[i], h, u[i]);
+                *reinterpret_cast<W *>(to) = pack_vec(h, T());
+                to += p.D;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                h = vfma(a[i], h, u[i]);
+                if (row0 + i < p.T) store_some(to, row0 + i < len ? h : splat<N>(0.0f), at.n);
                 to += p.D;
             }
         }
     }
-    if (warp == 0 && rank == 0 && p.final_state) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < n) p.final_state[plane + j] = carry[j];
-    }
+    if (warp == 0 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
+    if (cs > 1) cluster_sync();  // no CTA leaves while another one may still write to it
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -300,173 +331,156 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
 // The tiles from the last to the first. With mu = what the rows after a row pass back to it,
 // lam_t = dy_t + mu and mu <- a_t lam_t: the map of a stretch in reversed time is mu -> A mu + M
 // with the same A. h inside a tile is rebuilt from the state saved before it.
+// Warp w of a CTA: rows [8 w, 8 w + 8) of its tile.
 constexpr int kBwdWarps = 8, kBwdStages = 3;
+template <int N>
+struct BwdSmem {
+    uint8_t tile[kBwdStages][3][kTile * kRowBytes];
+    Map<N> warp[kBwdWarps][32];
+    Vec<N> rev[kBwdWarps][32];  // the reversed map's increment
+    Vec<N> start[kBwdWarps][32], mu[kBwdWarps][32];
+    Exchange<N> ex;
+    static constexpr size_t bytes(int cluster) { return offsetof(BwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
+};
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const ScanParams p) {
-    constexpr int N = ScanCfg<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
-    using Smem = ScanSmem<N, kBwdWarps, 3, kBwdStages>;
+    constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
     using W = Pack<T, N>;
     extern __shared__ __align__(128) uint8_t raw[];
-    Smem &sm = *reinterpret_cast<Smem *>(raw);
-    Map<N>(*maps)[32] = reinterpret_cast<Map<N>(*)[32]>(raw + sizeof(Smem));
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int cs = p.cluster, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int slab = static_cast<int>(blockIdx.x / cs), b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
-    const int n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
+    BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
+    const Place<T> at(p);
+    const int lane = at.lane, warp = at.warp, cs = p.cluster;
+    if (cs > 1) {
+        if (threadIdx.x == 0) sm.ex.init();
+        cluster_sync();
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    const int64_t plane = static_cast<int64_t>(b) * p.D + c;
-    const T *gate = static_cast<const T *>(p.gate) + b * p.gate_sb + c0;
-    const T *x = static_cast<const T *>(p.x) + b * p.x_sb + c0;
-    const T *dy = static_cast<const T *>(p.dy) + b * p.dy_sb + c0;
-    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.D + c;
-    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(b) * p.T * p.D + c;
-    const int tiles = (p.T + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;
-    float carry[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) carry[j] = j < n && p.state ? p.state[plane + j] : 0.0f;
+    const int len = p.lengths ? min(max(p.lengths[at.b], 0), p.T) : p.T;
+    const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
+    const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
+    const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
+    const T *dy = static_cast<const T *>(p.dy) + at.b * p.dy_sb + at.c0;
+    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
+    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
+    const bool wide = p.pair && at.n == N;
+    Vec<N> carry;  // warp 1's: mu behind the cluster's tiles
+    load_state(p.state ? p.state + plane : nullptr, at.n, carry);
+    bool waiting = true;
+    auto tile_of = [&](int step) { return at.tiles - 1 - (step * cs + at.rank); };
     auto fetch = [&](int step) {
-        const int row = (tiles - 1 - (step * cs + rank)) * kTile, rows = min(len - row, kTile);
+        const int row = tile_of(step) * kTile, rows = min(len - row, kTile);
         if (row >= 0 && rows > 0) {
             uint8_t(*to)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
-            copy_tile<T, kThreads>(to[0], gate + row * p.gate_st, p.gate_st, rows, cols, p.word);
-            copy_tile<T, kThreads>(to[1], x + row * p.x_st, p.x_st, rows, cols, p.word);
-            copy_tile<T, kThreads>(to[2], dy + row * p.dy_st, p.dy_st, rows, cols, p.word);
+            copy_tile<T, kThreads>(to[0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads>(to[1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads>(to[2], dy + row * p.dy_st, p.dy_st, rows, at.cols, p.word);
         }
+        cp_async_commit();
     };
-    float next[N];  // the state in front of the next tile
+    Vec<N> saved;  // warp 0's: the state in front of the next tile
     auto fetch_state = [&](int step) {
-        const int tile = tiles - 1 - (step * cs + rank);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            next[j] = tile >= 0 && j < n ? p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] : 0.0f;
+        const int tile = tile_of(step);
+        load_state(tile >= 0 ? p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c : nullptr, at.n, saved);
     };
-    fetch_state(0);
+    if (warp == 0) fetch_state(0);
 #pragma unroll
-    for (int k = 0; k < kBwdStages - 1; ++k) {
-        if (k < steps) fetch(k);
-        cp_async_commit();
-    }
-    if (cs > 1) {  // every CTA of the cluster runs before another one writes to its shared memory
-        cluster_arrive();
-        cluster_wait();
-    }
-    for (int step = 0; step < steps; ++step) {
-        const int tile = tiles - 1 - (step * cs + rank), row0 = tile * kTile + warp * R;
-        float h[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) h[j] = next[j];
-        cp_async_wait<kBwdStages - 2>();
-        __syncthreads();
-        if (step + kBwdStages - 1 < steps) fetch(step + kBwdStages - 1);
-        cp_async_commit();
-        fetch_state(step + 1);
+    for (int k = 0; k < kBwdStages; ++k) fetch(k);
+    cp_async_wait<kBwdStages - 1>();
+    __syncthreads();
+    for (int step = 0; step < at.steps; ++step) {
+        const int tile = tile_of(step), row0 = tile * kTile + warp * R;
         const uint8_t(*st)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
         const int off = warp * R * kRowBytes + lane * 4;
-        float a[R][N], rest[R][N], rev[N];
+        const bool full = tile >= 0 && row0 + R <= len;
+        Vec<N> a[R], rest[R], rev = splat<N>(0.0f);
         W v[R], d[R];
-        Map<N> m;
+        Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
+        auto rows = [&](auto all_live) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) m.a[j] = 1.0f, m.b[j] = 0.0f, rev[j] = 0.0f;
+            for (int i = 0; i < R; ++i) {
+                decay<MODE>(to_vec(*reinterpret_cast<const W *>(st[0] + off + i * kRowBytes)), a[i], rest[i]);
+                v[i] = *reinterpret_cast<const W *>(st[1] + off + i * kRowBytes);
+                d[i] = *reinterpret_cast<const W *>(st[2] + off + i * kRowBytes);
+                if (!decltype(all_live)::value && !(tile >= 0 && row0 + i < len)) {
+                    a[i] = splat<N>(1.0f), rest[i] = splat<N>(0.0f);
+                    v[i] = d[i] = pack_vec(splat<N>(0.0f), T());
+                }
+                m = compose(Map<N>{a[i], increment<MODE>(rest[i], to_vec(v[i]))}, m);
+            }
+        };
+        if (full)
+            rows(std::true_type());
+        else
+            rows(std::false_type());
+#pragma unroll
+        for (int i = R - 1; i >= 0; --i) rev = vmul(a[i], vadd(to_vec(d[i]), rev));
+        sm.warp[warp][lane] = m;
+        sm.rev[warp][lane] = rev;
+        __syncthreads();  // the maps are there, and this step's stage is free
+        fetch(step + kBwdStages);
+        if (warp == 0) {
+            Vec<N> h = saved;
+#pragma unroll
+            for (int w = 0; w < kBwdWarps; ++w) {
+                sm.start[w][lane] = h;
+                h = apply(sm.warp[w][lane], h);
+            }
+            fetch_state(step + 1);
+        } else if (warp == 1) {
+            Map<N> all[kBwdWarps];  // of the tile's rows from each warp's first on, in reversed time
+#pragma unroll
+            for (int w = kBwdWarps - 1; w >= 0; --w) {
+                const Map<N> o = {sm.warp[w][lane].a, sm.rev[w][lane]};
+                all[w] = w < kBwdWarps - 1 ? compose(o, all[w + 1 < kBwdWarps ? w + 1 : w]) : o;
+            }
+            Vec<N> mu = carry;
+            if (cs > 1) {
+                if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[0]);
+                sm.ex.fold(step, cs, at.rank, lane, mu, carry);
+            } else {
+                carry = apply(all[0], carry);
+            }
+            sm.mu[kBwdWarps - 1][lane] = mu;
+#pragma unroll
+            for (int w = 0; w < kBwdWarps - 1; ++w) sm.mu[w][lane] = apply(all[w + 1], mu);
+        }
+        cp_async_wait<kBwdStages - 1>();
+        __syncthreads();  // the starts are there, and the next step's tile
+        if (tile < 0) continue;
+        Vec<N> h = sm.start[warp][lane], mu = sm.mu[warp][lane], before[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const W g = *reinterpret_cast<const W *>(st[0] + off + i * kRowBytes);
-            v[i] = *reinterpret_cast<const W *>(st[1] + off + i * kRowBytes);
-            d[i] = *reinterpret_cast<const W *>(st[2] + off + i * kRowBytes);
-            const bool live = tile >= 0 && row0 + i < len;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (MODE == BASED_GATE_LOG)
-                    a[i][j] = expf(to_f32(g.v[j])), rest[i][j] = 1.0f;
-                else
-                    sigmoid_pair(to_f32(g.v[j]), a[i][j], rest[i][j]);
-                if (!live) {
-                    a[i][j] = 1.0f, rest[i][j] = 0.0f;
-                    v[i].v[j] = from_f32<T>(0.0f);
-                    d[i].v[j] = from_f32<T>(0.0f);
-                }
-                m.b[j] = fmaf(a[i][j], m.b[j], rest[i][j] * to_f32(v[i].v[j]));
-                m.a[j] *= a[i][j];
-            }
+            before[i] = h;
+            h = vfma(a[i], h, increment<MODE>(rest[i], to_vec(v[i])));
         }
+        const int64_t last = static_cast<int64_t>(row0 + R - 1) * p.D;
+        T *to_g = dgate + last, *to_x = dx + last;
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) rev[j] = a[i][j] * (to_f32(d[i].v[j]) + rev[j]);
-        sm.warp[step & 1][warp][lane] = m;
-#pragma unroll
-        for (int j = 0; j < N; ++j) sm.rev[step & 1][warp][j][lane] = rev[j];
-        __syncthreads();
-        // the rows behind this warp's as a map, and the tile's map
-        Map<N> pre, all;
-#pragma unroll
-        for (int j = 0; j < N; ++j) all.a[j] = 1.0f, all.b[j] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kBwdWarps; ++k) {
-            const int w = kBwdWarps - 1 - k;
-            const Map<N> o = sm.warp[step & 1][w][lane], f = sm.warp[step & 1][k][lane];
-            if (w == warp) pre = all;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                all.b[j] = fmaf(o.a[j], all.b[j], sm.rev[step & 1][w][j][lane]);
-                all.a[j] *= o.a[j];
-                h[j] = k < warp ? fmaf(f.a[j], h[j], f.b[j]) : h[j];
+        for (int i = R - 1; i >= 0; --i) {
+            const Vec<N> lam = vadd(to_vec(d[i]), mu);
+            mu = vmul(a[i], lam);
+            Vec<N> og, ox;
+            if (MODE == BASED_GATE_LOG) {
+                og = vmul(mu, before[i]), ox = lam;
+            } else {
+                og = vmul(vmul(mu, rest[i]), vadd(before[i], vneg(to_vec(v[i]))));
+                ox = vmul(rest[i], lam);
             }
-        }
-        float mu[N];
-        if (cs > 1) {
-            Map<N>(*mine)[32] = maps + (step & 1) * cs;
-            for (int r = warp; r < cs; r += kBwdWarps) send(&mine[rank][lane], r, all);
-            cluster_arrive();
-            cluster_wait();
-            fold<N>(mine, cs, rank, lane, mu, carry);
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                mu[j] = carry[j];
-                carry[j] = fmaf(all.a[j], carry[j], all.b[j]);
+            if (full && wide) {
+                *reinterpret_cast<W *>(to_g) = pack_vec(og, T());
+                *reinterpret_cast<W *>(to_x) = pack_vec(ox, T());
+            } else if (row0 + i < p.T) {
+                store_some(to_g, row0 + i < len ? og : splat<N>(0.0f), at.n);
+                store_some(to_x, row0 + i < len ? ox : splat<N>(0.0f), at.n);
             }
-        }
-        float before[R][N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) mu[j] = fmaf(pre.a[j], mu[j], pre.b[j]);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                before[i][j] = h[j];
-                h[j] = fmaf(a[i][j], h[j], rest[i][j] * to_f32(v[i].v[j]));
-            }
-        if (n > 0 && tile >= 0) {
-            const int64_t at = static_cast<int64_t>(row0) * p.D;
-#pragma unroll
-            for (int i = R - 1; i >= 0; --i) {
-                float og[N], ox[N];
-                const bool live = row0 + i < len;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float lam = to_f32(d[i].v[j]) + mu[j];
-                    mu[j] = a[i][j] * lam;
-                    if (MODE == BASED_GATE_LOG)
-                        og[j] = mu[j] * before[i][j], ox[j] = lam;
-                    else
-                        og[j] = mu[j] * rest[i][j] * (before[i][j] - to_f32(v[i].v[j])), ox[j] = rest[i][j] * lam;
-                    og[j] = live ? og[j] : 0.0f;
-                    ox[j] = live ? ox[j] : 0.0f;
-                }
-                if (row0 + i < p.T) {
-                    store_channels<T, N>(dgate + at + static_cast<int64_t>(i) * p.D, og, n, p.pair);
-                    store_channels<T, N>(dx + at + static_cast<int64_t>(i) * p.D, ox, n, p.pair);
-                }
-            }
+            to_g -= p.D;
+            to_x -= p.D;
         }
     }
-    if (warp == 0 && rank == 0 && p.final_state) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < n) p.final_state[plane + j] = carry[j];
-    }
+    if (warp == 1 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
+    if (cs > 1) cluster_sync();
 }
 
 struct StepParams {
@@ -495,9 +509,9 @@ __global__ void __launch_bounds__(128) based_scan_step_kernel(const StepParams p
             Pack<float, N> h = *reinterpret_cast<const Pack<float, N> *>(p.pool + s * p.D + c);
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                float a, u;
-                decay<MODE>(to_f32(g.v[j]), to_f32(v.v[j]), a, u);
-                h.v[j] = fmaf(a, h.v[j], u);
+                Vec<1> a, rest;
+                decay<MODE>(Vec<1>{{to_f32(g.v[j])}}, a, rest);
+                h.v[j] = fmaf(a.v[0], h.v[j], increment<MODE>(rest, Vec<1>{{to_f32(v.v[j])}}).v[0]);
                 o.v[j] = from_f32<T>(h.v[j]);
             }
             *reinterpret_cast<Pack<float, N> *>(p.pool + s * p.D + c) = h;
@@ -558,7 +572,7 @@ cudaError_t allow(K *kernel, size_t smem) {
 // tiles for, so that few channels fill the GPU too.
 template <typename T, typename Smem>
 int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int per_sm, int sms, cudaStream_t st) {
-    p.slabs = (p.D + 32 * ScanCfg<T>::N - 1) / (32 * ScanCfg<T>::N);
+    p.slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
     const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
     p.cluster = 1;
     while (p.cluster < kMaxCluster && p.cluster < tiles && blocks * p.cluster * 2 <= static_cast<int64_t>(sms) * per_sm)
@@ -571,10 +585,10 @@ template <typename T>
 int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
     const bool log = mode == BASED_GATE_LOG;
     if (bwd)
-        return launch_scan<T, ScanSmem<ScanCfg<T>::N, kBwdWarps, 3, kBwdStages>>(
+        return launch_scan<T, BwdSmem<Place<T>::N>>(
             p, log ? based_scan_bwd_kernel<T, BASED_GATE_LOG> : based_scan_bwd_kernel<T, BASED_GATE_SIGMOID>,
             32 * kBwdWarps, 2, sms, st);
-    return launch_scan<T, typename ScanCfg<T>::Fwd>(
+    return launch_scan<T, FwdSmem<Place<T>::N>>(
         p, log ? based_scan_fwd_kernel<T, BASED_GATE_LOG> : based_scan_fwd_kernel<T, BASED_GATE_SIGMOID>,
         32 * kFwdWarps, 4, sms, st);
 }
@@ -606,6 +620,15 @@ int launch_step(const StepParams &p, int mode, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t scan_status(unsigned int *status, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_scan_status, sizeof(unsigned int));
+    if (e == cudaSuccess && clear && *status) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_scan_status, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
 }  // namespace based
 
 extern "C" {

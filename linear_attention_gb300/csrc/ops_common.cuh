@@ -14,6 +14,8 @@ namespace based {
 // defined in based_fwd.cu
 int host_cuda_fail(cudaError_t e, const char *what);
 int host_device(int *sms);  // checks that the current device is an sm_103 GPU
+// defined in based_scan.cu: the current device's status word of the scan kernels
+cudaError_t scan_status(unsigned int *status, bool clear);
 
 #define OPS_CUDA(call)                                            \
     do {                                                          \
@@ -88,22 +90,131 @@ struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Pack {
     T v[N];
 };
 
-// exp and the logistic function to about one unit of float32's last place: the recurrence
-// multiplies thousands of decays, so that the error of a faster approximation would add up.
-// 1 / d by the hardware's approximation and one step of Newton's method.
-__device__ __forceinline__ float recip(float d) {
+// ------------------------------------------------------------------------------------------------
+// Device: float32 vectors of one or two elements. Two go through the packed instructions, which
+// take one issue slot for both.
+// ------------------------------------------------------------------------------------------------
+template <int N>
+struct Vec;
+template <>
+struct Vec<1> {
+    float v[1];
+};
+template <>
+struct alignas(8) Vec<2> {
+    float v[2];
+};
+template <int N>
+__device__ __forceinline__ Vec<N> splat(float s) {
+    Vec<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = s;
+    return r;
+}
+__device__ __forceinline__ uint64_t bits2(const Vec<2> &a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.v[0]), "f"(a.v[1]));
+    return r;
+}
+__device__ __forceinline__ Vec<2> from_bits2(uint64_t b) {
+    Vec<2> r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.v[0]), "=f"(r.v[1]) : "l"(b));
+    return r;
+}
+__device__ __forceinline__ Vec<1> vfma(const Vec<1> &a, const Vec<1> &b, const Vec<1> &c) { return {fmaf(a.v[0], b.v[0], c.v[0])}; }
+__device__ __forceinline__ Vec<1> vmul(const Vec<1> &a, const Vec<1> &b) { return {a.v[0] * b.v[0]}; }
+__device__ __forceinline__ Vec<1> vadd(const Vec<1> &a, const Vec<1> &b) { return {a.v[0] + b.v[0]}; }
+__device__ __forceinline__ Vec<2> vfma(const Vec<2> &a, const Vec<2> &b, const Vec<2> &c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ Vec<2> vmul(const Vec<2> &a, const Vec<2> &b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+__device__ __forceinline__ Vec<2> vadd(const Vec<2> &a, const Vec<2> &b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from_bits2(r);
+}
+template <int N>
+__device__ __forceinline__ Vec<N> vneg(const Vec<N> &a) {
+    Vec<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = -a.v[j];
+    return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ Vec<N> to_vec(const Pack<T, N> &w) {
+    Vec<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = to_f32(w.v[j]);
+    return r;
+}
+__device__ __forceinline__ Pack<float, 1> pack_vec(const Vec<1> &a, float) { return {{a.v[0]}}; }
+__device__ __forceinline__ Pack<__nv_bfloat16, 2> pack_vec(const Vec<2> &a, __nv_bfloat16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a.v[0], a.v[1]);
+    return {{p.x, p.y}};
+}
+__device__ __forceinline__ Pack<__half, 2> pack_vec(const Vec<2> &a, __half) {
+    const __half2 p = __floats2half2_rn(a.v[0], a.v[1]);
+    return {{p.x, p.y}};
+}
+
+// ------------------------------------------------------------------------------------------------
+// Device: exp and the logistic function, to about 2^-22 relative
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ float ex2(float t) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+    return r;
+}
+__device__ __forceinline__ float rcp(float d) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-    return fmaf(r, fmaf(-d, r, 1.0f), r);
+    return r;
 }
-// p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy. Below g = -87, where p
-// is under 2e-38, g counts as -87, so that exp(-g) and its reciprocal stay in range; NaN stays NaN.
+// x limited to [lo, hi]; NaN stays NaN
+__device__ __forceinline__ float at_least(float x, float lo) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float at_most(float x, float hi) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(hi));
+    return r;
+}
+// e^(sign x) = 2^t (1 + r ln 2) with t = x log2(e) rounded and r what the rounding left out, which
+// for |x| of 10 is as much as 2^-21 of the result and would add up over the rows of a recurrence.
+// |x| must be below 126 ln 2 on the side that grows and 1000 on the other.
+template <int N>
+__device__ __forceinline__ Vec<N> vexp(const Vec<N> &x, float sign) {
+    const Vec<N> log2e = splat<N>(sign * 1.4426950408889634f);
+    const Vec<N> t = vmul(x, log2e), r = vmul(vfma(x, log2e, vneg(t)), splat<N>(0.6931471805599453f));
+    Vec<N> e;
+#pragma unroll
+    for (int j = 0; j < N; ++j) e.v[j] = ex2(t.v[j]);
+    return vfma(e, r, e);
+}
+// p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy. g counts as -87 below
+// that, where p is under 2e-38, and as 104 above, where q is 0 in float32; NaN stays NaN.
+template <int N>
+__device__ __forceinline__ void vsigmoid(Vec<N> g, Vec<N> &p, Vec<N> &q) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) g.v[j] = at_most(at_least(g.v[j], -87.0f), 104.0f);
+    const Vec<N> e = vexp(g, -1.0f), d = vadd(e, splat<N>(1.0f));
+#pragma unroll
+    for (int j = 0; j < N; ++j) p.v[j] = rcp(d.v[j]);
+    q = vmul(e, p);
+}
 __device__ __forceinline__ void sigmoid_pair(float g, float &p, float &q) {
-    float c;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(g), "f"(-87.0f));
-    const float e = expf(-c);
-    p = recip(1.0f + e);
-    q = e * p;
+    Vec<1> vp, vq;
+    vsigmoid(Vec<1>{{g}}, vp, vq);
+    p = vp.v[0], q = vq.v[0];
 }
 
 }  // namespace based
