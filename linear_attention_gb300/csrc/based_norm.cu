@@ -54,15 +54,15 @@ struct Row {
     __device__ __forceinline__ T &at(int i) { return w[i / kPer].v[i % kPer]; }
 };
 
-// Sums of K values over the threads of a group. For groups of more than a warp, `red` holds
-// 16 K floats, and calls in a row use different ones.
-template <int K>
+// Sums of K values over the threads of a group. BIG: groups may span warps (then they are the whole
+// CTA); `red` holds 16 K floats, and calls in a row use different ones.
+template <int K, bool BIG>
 __device__ __forceinline__ void group_sum(float (&v)[K], int tpg, float *red) {
-    for (int d = min(tpg, 32) >> 1; d > 0; d >>= 1) {
+    for (int d = BIG ? min(tpg, 32) >> 1 : tpg >> 1; d > 0; d >>= 1) {
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(~0u, v[k], d);
     }
-    if (tpg <= 32) return;
+    if (!BIG || tpg <= 32) return;
     const int warps = tpg >> 5;
     if ((threadIdx.x & 31) == 0) {
 #pragma unroll
@@ -75,23 +75,36 @@ __device__ __forceinline__ void group_sum(float (&v)[K], int tpg, float *red) {
         for (int w = 0; w < warps; ++w) v[k] += red[k * 16 + w];
     }
 }
-
-// act(v) and act'(v)
-__device__ __forceinline__ void activate(int act, float v, float &f, float &df) {
-    if (act == BASED_ACT_NONE) {
-        f = v, df = 1.0f;
-        return;
-    }
-    float s, t;
-    sigmoid_pair(v, s, t);
-    if (act == BASED_ACT_SIGMOID)
-        f = s, df = s * t;
-    else
-        f = v * s, df = fmaf(f, t, s);
+__device__ __forceinline__ float total(const Vec<2> (&v)[kElems / 2]) {
+    const Vec<2> s = vadd(vadd(v[0], v[1]), vadd(v[2], v[3]));
+    return s.v[0] + s.v[1];
 }
 
-template <typename TX, typename TY, bool VEC, bool GATED, bool BWD>
-__global__ void __launch_bounds__(512) based_norm_kernel(const NormParams p) {
+// act(v) and act'(v)
+__device__ __forceinline__ void activate(int act, const Vec<2> &v, Vec<2> &f, Vec<2> &df) {
+    if (act == BASED_ACT_NONE) {
+        f = v, df = splat<2>(1.0f);
+        return;
+    }
+    Vec<2> s, t;
+    vsigmoid(v, s, t);
+    if (act == BASED_ACT_SIGMOID)
+        f = s, df = vmul(s, t);
+    else
+        f = vmul(v, s), df = vfma(f, t, s);
+}
+
+// Two elements of a row in float32, 0 where the thread holds none.
+template <typename T, bool VEC>
+__device__ __forceinline__ Vec<2> two(Row<T, VEC> &r, int k, bool in0, bool in1) {
+    return {{in0 ? to_f32(r.at(2 * k)) : 0.0f, in1 ? to_f32(r.at(2 * k + 1)) : 0.0f}};
+}
+
+// Registers: the forward kernel fits 64, 1024 threads an SM; the backward kernel, which also holds
+// the sums for dweight and dbias, takes about 100. BIG ones may have 512 threads.
+template <typename TX, typename TY, bool VEC, bool GATED, bool BWD, bool BIG>
+__global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_norm_kernel(const NormParams p) {
+    constexpr int P = kElems / 2;
     extern __shared__ float smem[];
     const int slot = threadIdx.x / p.tpg, l = threadIdx.x % p.tpg;
     const int r = slot / p.gpb, g = blockIdx.y * p.gpb + slot % p.gpb;
@@ -100,91 +113,115 @@ __global__ void __launch_bounds__(512) based_norm_kernel(const NormParams p) {
     const int n = on ? p.Cg - first : 0;  // > 0: this thread holds channels
     const int64_t c = static_cast<int64_t>(g) * p.Cg + first;
     const float inv = 1.0f / p.Cg;
+    auto holds = [&](int i, int m) { return VEC ? m > 0 : i * step < m; };  // element i of a row with m channels
     griddep_wait();
     griddep_launch_dependents();
-    float w[kElems], b[kElems], dw[kElems], db[kElems];
-    bool in[kElems];
+    Vec<2> w[P], b[P], dw[P], db[P];
 #pragma unroll
     for (int i = 0; i < kElems; ++i) {
-        const int o = VEC ? i : i * step;
-        in[i] = VEC ? n > 0 : o < n;
-        w[i] = in[i] ? load_param(p.weight, p.p_dtype, static_cast<int>(c) + o, 1.0f) : 0.0f;
-        b[i] = in[i] ? load_param(p.bias, p.p_dtype, static_cast<int>(c) + o, 0.0f) : 0.0f;
-        dw[i] = db[i] = 0.0f;
+        const int o = static_cast<int>(c) + (VEC ? i : i * step);
+        w[i / 2].v[i % 2] = holds(i, n) ? load_param(p.weight, p.p_dtype, o, 1.0f) : 0.0f;
+        b[i / 2].v[i % 2] = holds(i, n) ? load_param(p.bias, p.p_dtype, o, 0.0f) : 0.0f;
     }
-    // every thread takes part in the sums of every turn: the bound is the CTA's first row
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * p.rp; base < p.R; base += static_cast<int64_t>(gridDim.x) * p.rp) {
-        const int64_t row = base + r;
-        const int m = row < p.R ? n : 0;
-        Row<TX, VEC> rx;
-        Row<TY, VEC> rz, rd;
-        rx.load(static_cast<const TX *>(p.x) + row * p.x_sr + c, m, step);
-        if (GATED) rz.load(static_cast<const TY *>(p.gate) + row * p.gate_sr + c, m, step);
-        if (BWD) rd.load(static_cast<const TY *>(p.dy) + row * p.dy_sr + c, m, step);
-        float h[kElems];
-        float s1[1] = {0.0f}, s2[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) {
-            in[i] = VEC ? m > 0 : i * step < m;
-            h[i] = in[i] ? to_f32(rx.at(i)) : 0.0f;
-            s1[0] += h[i];
-        }
-        group_sum(s1, p.tpg, smem);
+    for (int k = 0; k < P; ++k) dw[k] = db[k] = splat<2>(0.0f);
+    // the next row is loaded while a row is worked on
+    Row<TX, VEC> nx;
+    Row<TY, VEC> nz, nd;
+    auto fetch = [&](int64_t row, int m) {
+        nx.load(static_cast<const TX *>(p.x) + row * p.x_sr + c, m, step);
+        if (GATED) nz.load(static_cast<const TY *>(p.gate) + row * p.gate_sr + c, m, step);
+        if (BWD) nd.load(static_cast<const TY *>(p.dy) + row * p.dy_sr + c, m, step);
+    };
+    const int64_t turn = static_cast<int64_t>(gridDim.x) * p.rp;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * p.rp + r;
+    int m = row < p.R ? n : 0;
+    fetch(row, m);
+    // every thread takes part in the sums of every turn: the bound is the CTA's first row
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * p.rp; base < p.R; base += turn) {
+        Row<TX, VEC> rx = nx;
+        Row<TY, VEC> rz, rd;
+        if (GATED) rz = nz;
+        if (BWD) rd = nd;
+        const int64_t here = row;
+        const int mh = m;
+        row += turn;
+        m = row < p.R ? n : 0;
+        fetch(row, m);
+        Vec<2> h[P], sq[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k) h[k] = two(rx, k, holds(2 * k, mh), holds(2 * k + 1, mh));
+        float s1[1] = {total(h)};
+        group_sum<1, BIG>(s1, p.tpg, smem);
         const float mean = s1[0] * inv;
 #pragma unroll
-        for (int i = 0; i < kElems; ++i) {
-            h[i] = in[i] ? h[i] - mean : 0.0f;
-            s2[0] = fmaf(h[i], h[i], s2[0]);
+        for (int k = 0; k < P; ++k) {
+            h[k] = vadd(h[k], splat<2>(-mean));
+            if (!holds(2 * k, mh)) h[k].v[0] = 0.0f;
+            if (!holds(2 * k + 1, mh)) h[k].v[1] = 0.0f;
+            sq[k] = vmul(h[k], h[k]);
         }
-        group_sum(s2, p.tpg, smem + 16);
+        float s2[1] = {total(sq)};
+        group_sum<1, BIG>(s2, p.tpg, smem + 16);
         const float rstd = rsqrtf(fmaf(s2[0], inv, p.eps));
         if (!BWD) {
             Row<TY, VEC> ry;
 #pragma unroll
-            for (int i = 0; i < kElems; ++i) {
-                const float v = fmaf(h[i] * rstd, w[i], b[i]);
-                float f, df;
-                activate(p.act, GATED ? to_f32(rz.at(i)) : v, f, df);
-                ry.at(i) = from_f32<TY>(GATED ? v * f : f);
+            for (int k = 0; k < P; ++k) {
+                const Vec<2> v = vfma(vmul(h[k], splat<2>(rstd)), w[k], b[k]);
+                Vec<2> f, df;
+                activate(p.act, GATED ? two(rz, k, true, true) : v, f, df);
+                const Vec<2> y = GATED ? vmul(v, f) : f;
+                ry.at(2 * k) = from_f32<TY>(y.v[0]);
+                ry.at(2 * k + 1) = from_f32<TY>(y.v[1]);
             }
-            ry.store(static_cast<TY *>(p.y) + row * p.C + c, m, step);
+            ry.store(static_cast<TY *>(p.y) + here * p.C + c, mh, step);
         } else {
             Row<TY, VEC> oz;
             Row<TX, VEC> ox;
-            float q[kElems], s[2] = {0.0f, 0.0f};
+            Vec<2> q[P], s0 = splat<2>(0.0f), sh = splat<2>(0.0f);
 #pragma unroll
-            for (int i = 0; i < kElems; ++i) {
-                h[i] *= rstd;
-                const float v = fmaf(h[i], w[i], b[i]);
-                const float d = in[i] ? to_f32(rd.at(i)) : 0.0f;
-                float f, df;
-                activate(p.act, GATED ? (in[i] ? to_f32(rz.at(i)) : 0.0f) : v, f, df);
-                const float dv = d * (GATED ? f : df);
-                if (GATED) oz.at(i) = from_f32<TY>(d * v * df);
-                dw[i] = fmaf(dv, h[i], dw[i]);
-                db[i] += dv;
-                q[i] = dv * w[i];
-                s[0] += q[i];
-                s[1] = fmaf(q[i], h[i], s[1]);
+            for (int k = 0; k < P; ++k) {
+                const bool in0 = holds(2 * k, mh), in1 = holds(2 * k + 1, mh);
+                h[k] = vmul(h[k], splat<2>(rstd));
+                const Vec<2> v = vfma(h[k], w[k], b[k]), d = two(rd, k, in0, in1);
+                Vec<2> f, df;
+                activate(p.act, GATED ? two(rz, k, in0, in1) : v, f, df);
+                const Vec<2> dv = vmul(d, GATED ? f : df);
+                if (GATED) {
+                    const Vec<2> dz = vmul(vmul(d, v), df);
+                    oz.at(2 * k) = from_f32<TY>(dz.v[0]);
+                    oz.at(2 * k + 1) = from_f32<TY>(dz.v[1]);
+                }
+                dw[k] = vfma(dv, h[k], dw[k]);
+                db[k] = vadd(db[k], dv);
+                q[k] = vmul(dv, w[k]);
+                s0 = vadd(s0, q[k]);
+                sh = vfma(q[k], h[k], sh);
             }
-            group_sum(s, p.tpg, smem + 32);
+            if (GATED) oz.store(static_cast<TY *>(p.dgate) + here * p.C + c, mh, step);
+            float s[2] = {s0.v[0] + s0.v[1], sh.v[0] + sh.v[1]};
+            group_sum<2, BIG>(s, p.tpg, smem + 32);
+            const Vec<2> m0 = splat<2>(-s[0] * inv), m1 = splat<2>(-s[1] * inv), scale = splat<2>(rstd);
 #pragma unroll
-            for (int i = 0; i < kElems; ++i)
-                ox.at(i) = from_f32<TX>(rstd * (q[i] - s[0] * inv - h[i] * (s[1] * inv)));
-            ox.store(static_cast<TX *>(p.dx) + row * p.C + c, m, step);
-            if (GATED) oz.store(static_cast<TY *>(p.dgate) + row * p.C + c, m, step);
+            for (int k = 0; k < P; ++k) {
+                const Vec<2> dx = vmul(scale, vfma(h[k], m1, vadd(q[k], m0)));
+                ox.at(2 * k) = from_f32<TX>(dx.v[0]);
+                ox.at(2 * k + 1) = from_f32<TX>(dx.v[1]);
+            }
+            ox.store(static_cast<TX *>(p.dx) + here * p.C + c, mh, step);
         }
     }
     if (BWD && p.partial) {
         // the CTA's rows side by side are added in shared memory, in order
         float *part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
         const int per = p.gpb * p.tpg;  // threads of a row
-        float *sum = smem + 64;
+        Vec<2> *sum = reinterpret_cast<Vec<2> *>(smem + 64);
         for (int k = 1; k < p.rp; ++k) {
             __syncthreads();
             if (r == k && on) {
 #pragma unroll
-                for (int i = 0; i < kElems; ++i) {
+                for (int i = 0; i < P; ++i) {
                     sum[(i * 2) * per + threadIdx.x % per] = dw[i];
                     sum[(i * 2 + 1) * per + threadIdx.x % per] = db[i];
                 }
@@ -192,9 +229,9 @@ __global__ void __launch_bounds__(512) based_norm_kernel(const NormParams p) {
             __syncthreads();
             if (r == 0 && on) {
 #pragma unroll
-                for (int i = 0; i < kElems; ++i) {
-                    dw[i] += sum[(i * 2) * per + threadIdx.x];
-                    db[i] += sum[(i * 2 + 1) * per + threadIdx.x];
+                for (int i = 0; i < P; ++i) {
+                    dw[i] = vadd(dw[i], sum[(i * 2) * per + threadIdx.x]);
+                    db[i] = vadd(db[i], sum[(i * 2 + 1) * per + threadIdx.x]);
                 }
             }
         }
@@ -202,9 +239,9 @@ __global__ void __launch_bounds__(512) based_norm_kernel(const NormParams p) {
 #pragma unroll
             for (int i = 0; i < kElems; ++i) {
                 const int o = VEC ? i : i * step;
-                if (VEC ? n > 0 : o < n) {
-                    part[c + o] = dw[i];
-                    part[p.C + c + o] = db[i];
+                if (holds(i, n)) {
+                    part[c + o] = dw[i / 2].v[i % 2];
+                    part[p.C + c + o] = db[i / 2].v[i % 2];
                 }
             }
         }
@@ -217,20 +254,23 @@ struct NormSumParams {
     void *dweight, *dbias;
 };
 
-// dweight and dbias from the CTAs' sums: 32 columns a CTA, eight rows of partials at a time.
-__global__ void __launch_bounds__(256) based_norm_sum_kernel(const NormSumParams p) {
-    __shared__ float red[8][32];
+// dweight and dbias from the CTAs' sums: 32 columns a CTA, one row of partial sums a warp.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) based_norm_sum_kernel(const NormSumParams p) {
+    __shared__ float red[kSumWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;  // 0 .. 2 C - 1: dweight, then dbias
     griddep_wait();
     griddep_launch_dependents();
     float s = 0.0f;
-    if (c < 2 * p.C)
-        for (int k = warp; k < p.parts; k += 8) s += p.partial[static_cast<int64_t>(k) * 2 * p.C + c];
+    if (c < 2 * p.C) {
+#pragma unroll 8
+        for (int k = warp; k < p.parts; k += kSumWarps) s += p.partial[static_cast<int64_t>(k) * 2 * p.C + c];
+    }
     red[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= 2 * p.C) return;
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
+    for (int w = 1; w < kSumWarps; ++w) s += red[w][lane];
     void *out = c < p.C ? p.dweight : p.dbias;
     const int o = c < p.C ? c : c - p.C;
     if (!out) return;
@@ -254,13 +294,15 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd) {
         s.gpb = s.rp = 1;
         s.threads = s.tpg;
     } else {
-        s.gpb = 256 / s.tpg < G ? 256 / s.tpg : G;
-        s.rp = 256 / (s.gpb * s.tpg);
+        // columns in blocks of about equal width, rows side by side where one block is narrow
+        const int limit = bwd ? 128 : 256, blocks = (G * s.tpg + limit - 1) / limit;
+        s.gpb = (G + blocks - 1) / blocks;
+        s.rp = limit / (s.gpb * s.tpg);
         s.threads = (s.gpb * s.rp * s.tpg + 31) / 32 * 32;
     }
     s.grid_y = (G + s.gpb - 1) / s.gpb;
     // as many CTAs as are resident at once, in whole turns over the column blocks
-    const int resident = sms * ((bwd ? 1024 : 2048) / (s.threads > 256 ? 512 : 256));
+    const int resident = sms * ((bwd ? 640 : 1024) / s.threads);
     const int64_t turns = (R + s.rp - 1) / s.rp, most = resident / s.grid_y > 1 ? resident / s.grid_y : 1;
     s.grid_x = static_cast<int>(turns < most ? turns : most);
     return s;
@@ -310,10 +352,12 @@ int launch_norm(const NormParams &p, const NormShape &s, cudaStream_t st) {
     const dim3 grid(s.grid_x, s.grid_y);
     const size_t smem = (64 + (BWD && s.rp > 1 ? 2 * kElems * s.gpb * s.tpg : 0)) * sizeof(float);
     void (*kernel)(NormParams);
-    if (p.gate)
-        kernel = vec ? based_norm_kernel<TX, TY, true, true, BWD> : based_norm_kernel<TX, TY, false, true, BWD>;
+    if (!vec)
+        kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, true> : based_norm_kernel<TX, TY, false, false, BWD, true>;
+    else if (s.tpg > 32)
+        kernel = p.gate ? based_norm_kernel<TX, TY, true, true, BWD, true> : based_norm_kernel<TX, TY, true, false, BWD, true>;
     else
-        kernel = vec ? based_norm_kernel<TX, TY, true, false, BWD> : based_norm_kernel<TX, TY, false, false, BWD>;
+        kernel = p.gate ? based_norm_kernel<TX, TY, true, true, BWD, false> : based_norm_kernel<TX, TY, true, false, BWD, false>;
     OPS_CUDA(launch_op(kernel, grid, s.threads, smem, st, p));
     return BASED_OK;
 }
@@ -389,7 +433,7 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if ((rc = dispatch_norm<true>(p, s, x_dtype, dtype, st)) != BASED_OK || !sums) return rc;
     const NormSumParams q = {p.partial, s.grid_x, C, p_dtype, dweight, dbias};
-    OPS_CUDA(launch_op(based_norm_sum_kernel, dim3((2 * C + 31) / 32), 256, 0, st, q));
+    OPS_CUDA(launch_op(based_norm_sum_kernel, dim3((2 * C + 31) / 32), 32 * kSumWarps, 0, st, q));
     return BASED_OK;
 }
 
