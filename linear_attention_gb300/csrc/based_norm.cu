@@ -35,23 +35,56 @@ __device__ __forceinline__ float load_param(const void *p, int dtype, int i, flo
 }
 
 // Eight channels of a row. VEC: consecutive ones, loaded as 16-byte words; otherwise channels
-// l, l + tpg, ... of the group. n: the channels of the group from this thread's first on.
+// l, l + tpg, ... of the group. n: the channels of the group from this thread's first on. What the
+// thread does not hold is zero.
 template <typename T, bool VEC>
-struct Row {
-    static constexpr int kPer = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;  // channels of a word
-    using Word = Pack<T, kPer>;
-    Word w[kElems / kPer];
+struct Row;
+template <typename T>
+struct Row<T, true> {
+    static constexpr int kQuads = sizeof(T) * kElems / 16;
+    uint32_t w[kQuads * 4];
+    __device__ __forceinline__ void load(const T *p, int n, int) {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const uint4 q = n > 0 ? reinterpret_cast<const uint4 *>(p)[k] : make_uint4(0, 0, 0, 0);
+            w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+        }
+    }
+    __device__ __forceinline__ void store(T *p, int n, int) const {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k)
+            if (n > 0) reinterpret_cast<uint4 *>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    __device__ __forceinline__ Vec<2> get(int k) const {
+        if constexpr (sizeof(T) == 4)
+            return {{__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])}};
+        else
+            return unpack<T>(w[k]);
+    }
+    __device__ __forceinline__ void set(int k, const Vec<2> &v) {
+        if constexpr (sizeof(T) == 4)
+            w[2 * k] = __float_as_uint(v.v[0]), w[2 * k + 1] = __float_as_uint(v.v[1]);
+        else
+            w[k] = pack<T>(v);
+    }
+};
+template <typename T>
+struct Row<T, false> {
+    T w[kElems];
     __device__ __forceinline__ void load(const T *p, int n, int step) {
 #pragma unroll
-        for (int k = 0; k < kElems / kPer; ++k)
-            if (VEC ? n > 0 : k * step < n) w[k] = *reinterpret_cast<const Word *>(p + k * (VEC ? kPer : step));
+        for (int k = 0; k < kElems; ++k) w[k] = k * step < n ? p[k * step] : from_f32<T>(0.0f);
     }
     __device__ __forceinline__ void store(T *p, int n, int step) const {
 #pragma unroll
-        for (int k = 0; k < kElems / kPer; ++k)
-            if (VEC ? n > 0 : k * step < n) *reinterpret_cast<Word *>(p + k * (VEC ? kPer : step)) = w[k];
+        for (int k = 0; k < kElems; ++k)
+            if (k * step < n) p[k * step] = w[k];
     }
-    __device__ __forceinline__ T &at(int i) { return w[i / kPer].v[i % kPer]; }
+    __device__ __forceinline__ Vec<2> get(int k) const { return {{to_f32(w[2 * k]), to_f32(w[2 * k + 1])}}; }
+    __device__ __forceinline__ void set(int k, const Vec<2> &v) {
+        w[2 * k] = from_f32<T>(v.v[0]);
+        w[2 * k + 1] = from_f32<T>(v.v[1]);
+    }
 };
 
 // Sums of K values over the threads of a group. BIG: groups may span warps (then they are the whole
@@ -87,28 +120,23 @@ __device__ __forceinline__ void activate(int act, const Vec<2> &v, Vec<2> &f, Ve
         return;
     }
     Vec<2> s, t;
-    vsigmoid(v, s, t);
+    vsigmoid<false>(v, s, t);
     if (act == BASED_ACT_SIGMOID)
         f = s, df = vmul(s, t);
     else
         f = vmul(v, s), df = vfma(f, t, s);
 }
 
-// Two elements of a row in float32, 0 where the thread holds none.
-template <typename T, bool VEC>
-__device__ __forceinline__ Vec<2> two(Row<T, VEC> &r, int k, bool in0, bool in1) {
-    return {{in0 ? to_f32(r.at(2 * k)) : 0.0f, in1 ? to_f32(r.at(2 * k + 1)) : 0.0f}};
-}
-
-// Registers: the forward kernel fits 64, 1024 threads an SM; the backward kernel, which also holds
-// the sums for dweight and dbias, takes about 100. BIG ones may have 512 threads.
+// Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
+// and dbias, 80: weight and bias wait in shared memory, four 16-byte reads a row. BIG ones may have
+// 512 threads.
 template <typename TX, typename TY, bool VEC, bool GATED, bool BWD, bool BIG>
-__global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(BIG ? 512 : BWD ? 128 : 256, BIG ? 1 : BWD ? 6 : 4) based_norm_kernel(const NormParams p) {
     constexpr int P = kElems / 2;
     extern __shared__ float smem[];
     const int slot = threadIdx.x / p.tpg, l = threadIdx.x % p.tpg;
     const int r = slot / p.gpb, g = blockIdx.y * p.gpb + slot % p.gpb;
-    const int first = VEC ? l * kElems : l, step = p.tpg;
+    const int first = VEC ? l * kElems : l, step = p.tpg, per = p.gpb * p.tpg;
     const bool on = r < p.rp && g < p.G;
     const int n = on ? p.Cg - first : 0;  // > 0: this thread holds channels
     const int64_t c = static_cast<int64_t>(g) * p.Cg + first;
@@ -116,13 +144,22 @@ __global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_
     auto holds = [&](int i, int m) { return VEC ? m > 0 : i * step < m; };  // element i of a row with m channels
     griddep_wait();
     griddep_launch_dependents();
-    Vec<2> w[P], b[P], dw[P], db[P];
+    // (4, per) quads: elements 0-3 and 4-7 of the weights, then of the biases, of a row's threads
+    float4 *params = reinterpret_cast<float4 *>(smem + 64);
+    const float4 *mine = params + threadIdx.x % per;
+    if (r == 0) {
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) {
-        const int o = static_cast<int>(c) + (VEC ? i : i * step);
-        w[i / 2].v[i % 2] = holds(i, n) ? load_param(p.weight, p.p_dtype, o, 1.0f) : 0.0f;
-        b[i / 2].v[i % 2] = holds(i, n) ? load_param(p.bias, p.p_dtype, o, 0.0f) : 0.0f;
+        for (int q = 0; q < 4; ++q) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = (q & 1) * 4 + j, o = static_cast<int>(c) + (VEC ? i : i * step);
+                v[j] = holds(i, n) ? load_param(q < 2 ? p.weight : p.bias, p.p_dtype, o, q < 2 ? 1.0f : 0.0f) : 0.0f;
+            }
+            params[q * per + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+        }
     }
+    Vec<2> dw[P], db[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) dw[k] = db[k] = splat<2>(0.0f);
     // the next row is loaded while a row is worked on
@@ -137,9 +174,10 @@ __global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_
     int64_t row = static_cast<int64_t>(blockIdx.x) * p.rp + r;
     int m = row < p.R ? n : 0;
     fetch(row, m);
+    __syncthreads();
     // every thread takes part in the sums of every turn: the bound is the CTA's first row
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * p.rp; base < p.R; base += turn) {
-        Row<TX, VEC> rx = nx;
+        const Row<TX, VEC> rx = nx;
         Row<TY, VEC> rz, rd;
         if (GATED) rz = nz;
         if (BWD) rd = nd;
@@ -150,30 +188,36 @@ __global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_
         fetch(row, m);
         Vec<2> h[P], sq[P];
 #pragma unroll
-        for (int k = 0; k < P; ++k) h[k] = two(rx, k, holds(2 * k, mh), holds(2 * k + 1, mh));
+        for (int k = 0; k < P; ++k) h[k] = rx.get(k);
         float s1[1] = {total(h)};
         group_sum<1, BIG>(s1, p.tpg, smem);
-        const float mean = s1[0] * inv;
+        const Vec<2> mean = splat<2>(-s1[0] * inv);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-            h[k] = vadd(h[k], splat<2>(-mean));
-            if (!holds(2 * k, mh)) h[k].v[0] = 0.0f;
-            if (!holds(2 * k + 1, mh)) h[k].v[1] = 0.0f;
+            h[k] = vadd(h[k], mean);
+            if (!VEC) {
+                if (!holds(2 * k, mh)) h[k].v[0] = 0.0f;
+                if (!holds(2 * k + 1, mh)) h[k].v[1] = 0.0f;
+            }
             sq[k] = vmul(h[k], h[k]);
         }
         float s2[1] = {total(sq)};
+        if (VEC && mh <= 0) s2[0] = 0.0f;
         group_sum<1, BIG>(s2, p.tpg, smem + 16);
-        const float rstd = rsqrtf(fmaf(s2[0], inv, p.eps));
+        // a thread without channels scales by 0, so that nothing it adds to a sum is NaN where eps is 0
+        const float rstd = mh > 0 ? rsqrtf(fmaf(s2[0], inv, p.eps)) : 0.0f;
+        auto param = [&](int k, int which) {  // pair k of the weights (0) or biases (1)
+            const float4 q = mine[(2 * which + k / 2) * per];
+            return k % 2 ? Vec<2>{{q.z, q.w}} : Vec<2>{{q.x, q.y}};
+        };
         if (!BWD) {
             Row<TY, VEC> ry;
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                const Vec<2> v = vfma(vmul(h[k], splat<2>(rstd)), w[k], b[k]);
+                const Vec<2> v = vfma(vmul(h[k], splat<2>(rstd)), param(k, 0), param(k, 1));
                 Vec<2> f, df;
-                activate(p.act, GATED ? two(rz, k, true, true) : v, f, df);
-                const Vec<2> y = GATED ? vmul(v, f) : f;
-                ry.at(2 * k) = from_f32<TY>(y.v[0]);
-                ry.at(2 * k + 1) = from_f32<TY>(y.v[1]);
+                activate(p.act, GATED ? rz.get(k) : v, f, df);
+                ry.set(k, GATED ? vmul(v, f) : f);
             }
             ry.store(static_cast<TY *>(p.y) + here * p.C + c, mh, step);
         } else {
@@ -182,20 +226,15 @@ __global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_
             Vec<2> q[P], s0 = splat<2>(0.0f), sh = splat<2>(0.0f);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                const bool in0 = holds(2 * k, mh), in1 = holds(2 * k + 1, mh);
                 h[k] = vmul(h[k], splat<2>(rstd));
-                const Vec<2> v = vfma(h[k], w[k], b[k]), d = two(rd, k, in0, in1);
+                const Vec<2> w = param(k, 0), v = vfma(h[k], w, param(k, 1)), d = rd.get(k);
                 Vec<2> f, df;
-                activate(p.act, GATED ? two(rz, k, in0, in1) : v, f, df);
+                activate(p.act, GATED ? rz.get(k) : v, f, df);
                 const Vec<2> dv = vmul(d, GATED ? f : df);
-                if (GATED) {
-                    const Vec<2> dz = vmul(vmul(d, v), df);
-                    oz.at(2 * k) = from_f32<TY>(dz.v[0]);
-                    oz.at(2 * k + 1) = from_f32<TY>(dz.v[1]);
-                }
+                if (GATED) oz.set(k, vmul(vmul(d, v), df));
                 dw[k] = vfma(dv, h[k], dw[k]);
                 db[k] = vadd(db[k], dv);
-                q[k] = vmul(dv, w[k]);
+                q[k] = vmul(dv, w);
                 s0 = vadd(s0, q[k]);
                 sh = vfma(q[k], h[k], sh);
             }
@@ -204,19 +243,14 @@ __global__ void __launch_bounds__(BIG ? 512 : 256, BIG ? 1 : BWD ? 2 : 4) based_
             group_sum<2, BIG>(s, p.tpg, smem + 32);
             const Vec<2> m0 = splat<2>(-s[0] * inv), m1 = splat<2>(-s[1] * inv), scale = splat<2>(rstd);
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const Vec<2> dx = vmul(scale, vfma(h[k], m1, vadd(q[k], m0)));
-                ox.at(2 * k) = from_f32<TX>(dx.v[0]);
-                ox.at(2 * k + 1) = from_f32<TX>(dx.v[1]);
-            }
+            for (int k = 0; k < P; ++k) ox.set(k, vmul(scale, vfma(h[k], m1, vadd(q[k], m0))));
             ox.store(static_cast<TX *>(p.dx) + here * p.C + c, mh, step);
         }
     }
     if (BWD && p.partial) {
         // the CTA's rows side by side are added in shared memory, in order
         float *part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
-        const int per = p.gpb * p.tpg;  // threads of a row
-        Vec<2> *sum = reinterpret_cast<Vec<2> *>(smem + 64);
+        Vec<2> *sum = reinterpret_cast<Vec<2> *>(params + 4 * per);
         for (int k = 1; k < p.rp; ++k) {
             __syncthreads();
             if (r == k && on) {
@@ -302,7 +336,7 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd) {
     }
     s.grid_y = (G + s.gpb - 1) / s.gpb;
     // as many CTAs as are resident at once, in whole turns over the column blocks
-    const int resident = sms * ((bwd ? 640 : 1024) / s.threads);
+    const int resident = sms * ((bwd ? 768 : 1024) / s.threads);
     const int64_t turns = (R + s.rp - 1) / s.rp, most = resident / s.grid_y > 1 ? resident / s.grid_y : 1;
     s.grid_x = static_cast<int>(turns < most ? turns : most);
     return s;
@@ -350,7 +384,8 @@ int launch_norm(const NormParams &p, const NormShape &s, cudaStream_t st) {
     const bool vec = p.Cg % kElems == 0 && wide(p.x, p.x_sr, xs) && wide(p.gate, p.gate_sr, es) &&
                      wide(p.dy, p.dy_sr, es) && aligned(p.y, 16) && aligned(p.dx, 16) && aligned(p.dgate, 16);
     const dim3 grid(s.grid_x, s.grid_y);
-    const size_t smem = (64 + (BWD && s.rp > 1 ? 2 * kElems * s.gpb * s.tpg : 0)) * sizeof(float);
+    // the sums' 64 floats, weight and bias, and where rows lie side by side their dweight and dbias
+    const size_t smem = (64 + (BWD && s.rp > 1 ? 4 : 2) * kElems * s.gpb * s.tpg) * sizeof(float);
     void (*kernel)(NormParams);
     if (!vec)
         kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, true> : based_norm_kernel<TX, TY, false, false, BWD, true>;

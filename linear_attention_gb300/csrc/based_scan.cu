@@ -47,7 +47,7 @@ __device__ __forceinline__ void decay(Vec<N> g, Vec<N> &a, Vec<N> &rest) {
         a = vexp(g, 1.0f);
         rest = splat<N>(1.0f);
     } else {
-        vsigmoid(g, a, rest);
+        vsigmoid<true>(g, a, rest);
     }
 }
 template <int MODE, int N>
@@ -228,7 +228,6 @@ struct FwdSmem {
 template <typename T, int MODE>
 __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
-    using W = Pack<T, N>;
     extern __shared__ __align__(128) uint8_t raw[];
     FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
     const Place<T> at(p);
@@ -271,8 +270,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<N> rest;
-                decay<MODE>(to_vec(*reinterpret_cast<const W *>(sg + i * kRowBytes)), a[i], rest);
-                u[i] = increment<MODE>(rest, to_vec(*reinterpret_cast<const W *>(sx + i * kRowBytes)));
+                decay<MODE>(unpack<T>(*reinterpret_cast<const uint32_t *>(sg + i * kRowBytes)), a[i], rest);
+                u[i] = increment<MODE>(rest, unpack<T>(*reinterpret_cast<const uint32_t *>(sx + i * kRowBytes)));
                 if (!decltype(all_live)::value && row0 + i >= len) a[i] = splat<N>(1.0f), u[i] = splat<N>(0.0f);
                 m = compose(Map<N>{a[i], u[i]}, m);
             }
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
-                *reinterpret_cast<W *>(to) = pack_vec(h, T());
+                *reinterpret_cast<uint32_t *>(to) = pack<T>(h);
                 to += p.D;
             }
         } else {
@@ -346,7 +345,6 @@ struct BwdSmem {
 template <typename T, int MODE>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
-    using W = Pack<T, N>;
     extern __shared__ __align__(128) uint8_t raw[];
     BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
     const Place<T> at(p);
@@ -395,19 +393,19 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
         const int off = warp * R * kRowBytes + lane * 4;
         const bool full = tile >= 0 && row0 + R <= len;
         Vec<N> a[R], rest[R], rev = splat<N>(0.0f);
-        W v[R], d[R];
+        uint32_t v[R], d[R];
         Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
         auto rows = [&](auto all_live) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                decay<MODE>(to_vec(*reinterpret_cast<const W *>(st[0] + off + i * kRowBytes)), a[i], rest[i]);
-                v[i] = *reinterpret_cast<const W *>(st[1] + off + i * kRowBytes);
-                d[i] = *reinterpret_cast<const W *>(st[2] + off + i * kRowBytes);
+                decay<MODE>(unpack<T>(*reinterpret_cast<const uint32_t *>(st[0] + off + i * kRowBytes)), a[i], rest[i]);
+                v[i] = *reinterpret_cast<const uint32_t *>(st[1] + off + i * kRowBytes);
+                d[i] = *reinterpret_cast<const uint32_t *>(st[2] + off + i * kRowBytes);
                 if (!decltype(all_live)::value && !(tile >= 0 && row0 + i < len)) {
                     a[i] = splat<N>(1.0f), rest[i] = splat<N>(0.0f);
-                    v[i] = d[i] = pack_vec(splat<N>(0.0f), T());
+                    v[i] = d[i] = 0;
                 }
-                m = compose(Map<N>{a[i], increment<MODE>(rest[i], to_vec(v[i]))}, m);
+                m = compose(Map<N>{a[i], increment<MODE>(rest[i], unpack<T>(v[i]))}, m);
             }
         };
         if (full)
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
         else
             rows(std::false_type());
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) rev = vmul(a[i], vadd(to_vec(d[i]), rev));
+        for (int i = R - 1; i >= 0; --i) rev = vmul(a[i], vadd(unpack<T>(d[i]), rev));
         sm.warp[warp][lane] = m;
         sm.rev[warp][lane] = rev;
         __syncthreads();  // the maps are there, and this step's stage is free
@@ -453,24 +451,24 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             before[i] = h;
-            h = vfma(a[i], h, increment<MODE>(rest[i], to_vec(v[i])));
+            h = vfma(a[i], h, increment<MODE>(rest[i], unpack<T>(v[i])));
         }
         const int64_t last = static_cast<int64_t>(row0 + R - 1) * p.D;
         T *to_g = dgate + last, *to_x = dx + last;
 #pragma unroll
         for (int i = R - 1; i >= 0; --i) {
-            const Vec<N> lam = vadd(to_vec(d[i]), mu);
+            const Vec<N> lam = vadd(unpack<T>(d[i]), mu);
             mu = vmul(a[i], lam);
             Vec<N> og, ox;
             if (MODE == BASED_GATE_LOG) {
                 og = vmul(mu, before[i]), ox = lam;
             } else {
-                og = vmul(vmul(mu, rest[i]), vadd(before[i], vneg(to_vec(v[i]))));
+                og = vmul(vmul(mu, rest[i]), vadd(before[i], vneg(unpack<T>(v[i]))));
                 ox = vmul(rest[i], lam);
             }
             if (full && wide) {
-                *reinterpret_cast<W *>(to_g) = pack_vec(og, T());
-                *reinterpret_cast<W *>(to_x) = pack_vec(ox, T());
+                *reinterpret_cast<uint32_t *>(to_g) = pack<T>(og);
+                *reinterpret_cast<uint32_t *>(to_x) = pack<T>(ox);
             } else if (row0 + i < p.T) {
                 store_some(to_g, row0 + i < len ? og : splat<N>(0.0f), at.n);
                 store_some(to_x, row0 + i < len ? ox : splat<N>(0.0f), at.n);

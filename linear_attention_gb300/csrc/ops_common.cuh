@@ -147,21 +147,42 @@ __device__ __forceinline__ Vec<N> vneg(const Vec<N> &a) {
     return r;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ Vec<N> to_vec(const Pack<T, N> &w) {
-    Vec<N> r;
-#pragma unroll
-    for (int j = 0; j < N; ++j) r.v[j] = to_f32(w.v[j]);
+// A 32-bit word as one float32 or two 16-bit elements, the first in the low half.
+template <typename T>
+__device__ __forceinline__ Vec<4 / sizeof(T)> unpack(uint32_t w);
+template <>
+__device__ __forceinline__ Vec<1> unpack<float>(uint32_t w) {
+    return {{__uint_as_float(w)}};
+}
+template <>
+__device__ __forceinline__ Vec<2> unpack<__nv_bfloat16>(uint32_t w) {
+    return {{__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}};
+}
+template <>
+__device__ __forceinline__ Vec<2> unpack<__half>(uint32_t w) {
+    Vec<2> r;
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}"
+        : "=f"(r.v[0]), "=f"(r.v[1])
+        : "r"(w));
     return r;
 }
-__device__ __forceinline__ Pack<float, 1> pack_vec(const Vec<1> &a, float) { return {{a.v[0]}}; }
-__device__ __forceinline__ Pack<__nv_bfloat16, 2> pack_vec(const Vec<2> &a, __nv_bfloat16) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a.v[0], a.v[1]);
-    return {{p.x, p.y}};
+template <typename T>
+__device__ __forceinline__ uint32_t pack(const Vec<4 / sizeof(T)> &a);
+template <>
+__device__ __forceinline__ uint32_t pack<float>(const Vec<1> &a) {
+    return __float_as_uint(a.v[0]);
 }
-__device__ __forceinline__ Pack<__half, 2> pack_vec(const Vec<2> &a, __half) {
-    const __half2 p = __floats2half2_rn(a.v[0], a.v[1]);
-    return {{p.x, p.y}};
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(const Vec<2> &a) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(a.v[1]), "f"(a.v[0]));
+    return w;
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(const Vec<2> &a) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(a.v[1]), "f"(a.v[0]));
+    return w;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -202,19 +223,27 @@ __device__ __forceinline__ Vec<N> vexp(const Vec<N> &x, float sign) {
 }
 // p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy. g counts as -87 below
 // that, where p is under 2e-38, and as 104 above, where q is 0 in float32; NaN stays NaN.
-template <int N>
+// LONG: to 2^-20.5, for values that add up over the rows of a recurrence. Otherwise exp(-g) is taken
+// without the correction of its rounded argument, good to 2^-22 + |g| 2^-24: a fifth fewer instructions for
+// values that are used once.
+template <bool LONG, int N>
 __device__ __forceinline__ void vsigmoid(Vec<N> g, Vec<N> &p, Vec<N> &q) {
+    Vec<N> e;
 #pragma unroll
-    for (int j = 0; j < N; ++j) g.v[j] = at_most(at_least(g.v[j], -87.0f), 104.0f);
-    const Vec<N> e = vexp(g, -1.0f), d = vadd(e, splat<N>(1.0f));
+    for (int j = 0; j < N; ++j) g.v[j] = at_least(g.v[j], -87.0f);
+    if (LONG) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) g.v[j] = at_most(g.v[j], 104.0f);
+        e = vexp(g, -1.0f);
+    } else {
+        e = vmul(g, splat<N>(-1.4426950408889634f));
+#pragma unroll
+        for (int j = 0; j < N; ++j) e.v[j] = ex2(e.v[j]);
+    }
+    const Vec<N> d = vadd(e, splat<N>(1.0f));
 #pragma unroll
     for (int j = 0; j < N; ++j) p.v[j] = rcp(d.v[j]);
     q = vmul(e, p);
-}
-__device__ __forceinline__ void sigmoid_pair(float g, float &p, float &q) {
-    Vec<1> vp, vq;
-    vsigmoid(Vec<1>{{g}}, vp, vq);
-    p = vp.v[0], q = vq.v[0];
 }
 
 }  // namespace based
