@@ -195,19 +195,43 @@ __device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
     for (int j = 0; j < N; ++j) v.v[j] = src && j < n ? src[j] : 0.0f;
 }
 
+// The rows of sequence b before its padding. Kernels without lengths (RAGGED false) are instances of
+// their own: a bound that comes from memory makes the loop over the tiles one of threads that might
+// diverge, which costs the forward pass over 16384 x 2048 a third more time (62 us, not 45).
+template <bool RAGGED>
+__device__ __forceinline__ int sequence_length(const ScanParams &p, int b) {
+    return RAGGED ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+
+// Zeros in the rows [row0, T) of an output's columns of this cluster, by all threads of its CTAs.
+template <typename T, int THREADS>
+__device__ __forceinline__ void zero_rows(T *out, int row0, const ScanParams &p, int n, int rank, int lane, int warp) {
+    if (n <= 0) return;
+    constexpr int N = 4 / sizeof(T), kWarps = THREADS / 32;
+    const int step = p.cluster * kWarps;
+    T *to = out + static_cast<int64_t>(row0 + rank * kWarps + warp) * p.D;
+    for (int row = row0 + rank * kWarps + warp; row < p.T; row += step) {
+        if (p.pair && n == N)
+            *reinterpret_cast<uint32_t *>(to) = 0;
+        else
+            store_some(to, splat<N>(0.0f), n);
+        to += static_cast<int64_t>(step) * p.D;
+    }
+}
+
 // What both kernels know about their place: 32 N channels of one batch entry for a cluster, N
 // channels for a lane; the cluster's CTAs take the tiles in turn.
 template <typename T>
 struct Place {
     static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
-    int lane, warp, rank, b, c0, c, n, cols, tiles, steps;
+    int lane, warp, rank, b, c0, c, n, cols, tiles;
     __device__ __forceinline__ explicit Place(const ScanParams &p) {
         lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
         const int slab = static_cast<int>(blockIdx.x) / p.cluster;
         b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
         n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
-        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) / p.cluster;
+        tiles = (p.T + kTile - 1) / kTile;
     }
 };
 
@@ -225,7 +249,7 @@ struct FwdSmem {
     static constexpr size_t bytes(int cluster) { return offsetof(FwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
@@ -238,7 +262,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     }
     griddep_wait();
     griddep_launch_dependents();
-    const int len = p.lengths ? min(max(p.lengths[at.b], 0), p.T) : p.T;
+    const int len = sequence_length<RAGGED>(p, at.b);
     const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
     const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
     const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
@@ -249,7 +273,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     bool waiting = true;
     auto fetch = [&](int step) {
         const int row = (step * cs + at.rank) * kTile, rows = min(len - row, kTile);
-        if (step < at.steps && rows > 0) {
+        if (rows > 0) {
             copy_tile<T, kThreads>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
             copy_tile<T, kThreads>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
         }
@@ -259,7 +283,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     for (int k = 0; k < kFwdStages; ++k) fetch(k);
     cp_async_wait<kFwdStages - 1>();
     __syncthreads();
-    for (int step = 0; step < at.steps; ++step) {
+    const int live = (len + kTile * cs - 1) / (kTile * cs);  // steps with rows before the padding
+    for (int step = 0; step < live; ++step) {
         const int tile = step * cs + at.rank, row0 = tile * kTile + warp * R;
         const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
         const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * kRowBytes + lane * 4;
@@ -320,7 +345,13 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
             }
         }
     }
-    if (warp == 0 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
+    if (RAGGED) zero_rows<T, kThreads>(y, live * kTile * cs, p, at.n, at.rank, lane, warp);
+    if (warp == 0) {
+        if (RAGGED && p.saved)
+            for (int tile = live * cs + at.rank; tile < at.tiles; tile += cs)
+                store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, carry, at.n);
+        if (at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
+    }
     if (cs > 1) cluster_sync();  // no CTA leaves while another one may still write to it
 }
 
@@ -342,7 +373,7 @@ struct BwdSmem {
     static constexpr size_t bytes(int cluster) { return offsetof(BwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool RAGGED>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
@@ -355,7 +386,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
     }
     griddep_wait();
     griddep_launch_dependents();
-    const int len = p.lengths ? min(max(p.lengths[at.b], 0), p.T) : p.T;
+    const int len = sequence_length<RAGGED>(p, at.b);
     const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
     const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
     const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
@@ -366,7 +397,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
     Vec<N> carry;  // warp 1's: mu behind the cluster's tiles
     load_state(p.state ? p.state + plane : nullptr, at.n, carry);
     bool waiting = true;
-    auto tile_of = [&](int step) { return at.tiles - 1 - (step * cs + at.rank); };
+    const int tiles = (len + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;  // those before the padding
+    auto tile_of = [&](int step) { return tiles - 1 - (step * cs + at.rank); };
     auto fetch = [&](int step) {
         const int row = tile_of(step) * kTile, rows = min(len - row, kTile);
         if (row >= 0 && rows > 0) {
@@ -387,7 +419,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
     for (int k = 0; k < kBwdStages; ++k) fetch(k);
     cp_async_wait<kBwdStages - 1>();
     __syncthreads();
-    for (int step = 0; step < at.steps; ++step) {
+    for (int step = 0; step < steps; ++step) {
         const int tile = tile_of(step), row0 = tile * kTile + warp * R;
         const uint8_t(*st)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
         const int off = warp * R * kRowBytes + lane * 4;
@@ -477,6 +509,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
             to_x -= p.D;
         }
     }
+    if (RAGGED) zero_rows<T, kThreads>(dgate, tiles * kTile, p, at.n, at.rank, lane, warp);
+    if (RAGGED) zero_rows<T, kThreads>(dx, tiles * kTile, p, at.n, at.rank, lane, warp);
     if (warp == 1 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
     if (cs > 1) cluster_sync();
 }
@@ -566,15 +600,31 @@ cudaError_t allow(K *kernel, size_t smem) {
     return e;
 }
 
-// per_sm: CTAs that an SM holds. Time is shared out among as many CTAs as there are slots and
-// tiles for, so that few channels fill the GPU too.
+// CTAs of a cluster: those whose estimated time is least. A step of a CTA takes `step_us` by its
+// own latencies, or longer where the resident CTAs' copies exceed the memory's rate; a CTA has two steps'
+// worth of start and end besides its share of the tiles. slots: CTAs that the GPU holds at once.
+int choose_cluster(int64_t blocks, int64_t tiles, int64_t slots, double step_us, double step_bytes) {
+    auto step = [&](int64_t resident) {
+        const double us = resident * step_bytes / 6.4e6;  // bytes per us that the memory gives a kernel
+        return us > step_us ? us : step_us;
+    };
+    int best = 1;
+    double least = 0.0;
+    for (int cs = 1; cs <= kMaxCluster && (cs == 1 || cs / 2 < tiles); cs *= 2) {
+        const int64_t n = blocks * cs, waves = n / slots, rest = n % slots;
+        const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots) + (rest ? step(rest) : 0.0));
+        // a larger cluster for a clear gain alone: its exchange costs what the estimate leaves out
+        if (cs == 1 || us < 0.9 * least) best = cs, least = us;
+    }
+    return best;
+}
+
 template <typename T, typename Smem>
-int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int per_sm, int sms, cudaStream_t st) {
+int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int64_t slots, double step_us, int tensors,
+                cudaStream_t st) {
     p.slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
     const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
-    p.cluster = 1;
-    while (p.cluster < kMaxCluster && p.cluster < tiles && blocks * p.cluster * 2 <= static_cast<int64_t>(sms) * per_sm)
-        p.cluster *= 2;
+    p.cluster = choose_cluster(blocks, tiles, slots, step_us, static_cast<double>(tensors) * kTile * kRowBytes);
     OPS_CUDA(allow(kernel, Smem::bytes(kMaxCluster)));
     OPS_CUDA(launch_op(kernel, dim3(static_cast<unsigned>(blocks * p.cluster)), threads, Smem::bytes(p.cluster), st, p, p.cluster));
     return BASED_OK;
@@ -582,13 +632,15 @@ int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int per_
 template <typename T>
 int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
     const bool log = mode == BASED_GATE_LOG;
-    if (bwd)
-        return launch_scan<T, BwdSmem<Place<T>::N>>(
-            p, log ? based_scan_bwd_kernel<T, BASED_GATE_LOG> : based_scan_bwd_kernel<T, BASED_GATE_SIGMOID>,
-            32 * kBwdWarps, 2, sms, st);
-    return launch_scan<T, FwdSmem<Place<T>::N>>(
-        p, log ? based_scan_fwd_kernel<T, BASED_GATE_LOG> : based_scan_fwd_kernel<T, BASED_GATE_SIGMOID>,
-        32 * kFwdWarps, 4, sms, st);
+    constexpr int kLog = BASED_GATE_LOG, kSig = BASED_GATE_SIGMOID;
+    if (bwd) {
+        void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_bwd_kernel<T, kLog, true> : based_scan_bwd_kernel<T, kSig, true>)
+                                                : (log ? based_scan_bwd_kernel<T, kLog, false> : based_scan_bwd_kernel<T, kSig, false>);
+        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, 2 * sms, 1.9, 5, st);
+    }
+    void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_fwd_kernel<T, kLog, true> : based_scan_fwd_kernel<T, kSig, true>)
+                                            : (log ? based_scan_fwd_kernel<T, kLog, false> : based_scan_fwd_kernel<T, kSig, false>);
+    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, 4 * sms, 1.7, 3, st);
 }
 
 int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream) {
