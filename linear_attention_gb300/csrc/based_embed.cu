@@ -2,21 +2,23 @@
 //
 //     y_i = s E[id_i],    dE_v = s sum over i with id_i = v of dy_i
 //
-// The gradient is summed by sorted tokens. The (id, position) pairs are sorted by id with a stable
-// counting sort, digit by digit; the sorted order is cut into tiles, a CTA sums the runs of equal
-// ids in its tile, and runs that cross tiles are joined from float32 partial sums. The order of
-// every sum follows from the ids alone, so that results repeat bit for bit, and a token that
+// The gradient is summed by sorted tokens, in three launches. One cluster sorts the (id, position)
+// pairs by id with a stable counting sort, digit by digit, while the other clusters of the same
+// launch write the zeros of the gradient. The sorted order is cut into tiles, a CTA sums the runs of
+// equal ids in its tile, and runs that cross tiles are joined from float32 partial sums. The order
+// of every sum follows from the ids alone, so that results repeat bit for bit, and a token that
 // occurs thousands of times is spread over many CTAs.
 #include "ops_common.cuh"
 
 namespace based {
 namespace {
 
-constexpr int kSortThreads = 256;
-constexpr int kSortChunk = 1024;    // keys a CTA ranks at a time, 128 a warp
-constexpr int kMaxSortBlocks = 128;
-constexpr int kMaxDigits = 1024;
-constexpr int kTileRows = 32;       // sorted positions of a tile
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+constexpr int kSortRounds = 4;                             // keys of a thread at a time
+constexpr int kSortChunk = kSortThreads * kSortRounds;
+constexpr int kMaxBits = 9;                                // of a digit
+constexpr int kTileRows = 32;                              // sorted positions of a tile
 
 struct EmbedParams {
     const void *ids, *table;
@@ -53,137 +55,128 @@ __global__ void __launch_bounds__(256) based_embed_fwd_kernel(const EmbedParams 
 }
 
 struct SortParams {
-    const void *ids;       // the first pass reads ids, the others key_in and pos_in
-    const int32_t *key_in, *pos_in;
-    int32_t *key_out, *pos_out, *hist;  // hist: (blocks, digits)
-    int N, V, ids64, per;  // per: keys of a CTA, a multiple of kSortChunk
-    int shift, digits;
+    const void *ids;
+    int32_t *key0, *key1, *pos0, *pos1;  // pass i writes lists i & 1; the first reads ids
+    int N, V, ids64, passes, bits;
+    void *out;                 // the gradient: `words` 16-byte words, then bytes up to `bytes`
+    int64_t words, bytes;
 };
 
-__device__ __forceinline__ int sort_key(const SortParams &p, int i) {
-    return p.ids ? load_id(p.ids, p.ids64, i, p.V) : p.key_in[i];
+__device__ __forceinline__ int load_remote(const int *p, int rank) {
+    uint32_t at;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
-// How often each digit occurs among a CTA's keys.
-__global__ void __launch_bounds__(kSortThreads) based_embed_count_kernel(const SortParams p) {
-    __shared__ int cnt[kMaxDigits];
-    griddep_wait();
-    griddep_launch_dependents();
-    for (int d = threadIdx.x; d < p.digits; d += kSortThreads) cnt[d] = 0;
-    __syncthreads();
-    const int64_t begin = static_cast<int64_t>(blockIdx.x) * p.per, end = min(begin + p.per, static_cast<int64_t>(p.N));
-    for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads)
-        atomicAdd(&cnt[(sort_key(p, static_cast<int>(i)) >> p.shift) & (p.digits - 1)], 1);
-    __syncthreads();
-    for (int d = threadIdx.x; d < p.digits; d += kSortThreads)
-        p.hist[static_cast<int64_t>(blockIdx.x) * p.digits + d] = cnt[d];
-}
+struct SortSmem {
+    int hist[1 << kMaxBits];   // digits of this CTA's keys
+    int base[1 << kMaxBits];   // where the next key of each digit goes
+    int warp_sum[kSortWarps];
+    int cnt[kSortWarps][1 << kMaxBits];
+};
 
-// Moves a CTA's keys to their places: those of smaller digits, then those of the same digit in
-// earlier CTAs, earlier warps, earlier rounds and lower lanes come first.
-__global__ void __launch_bounds__(kSortThreads) based_embed_place_kernel(const SortParams p) {
-    __shared__ int base[kMaxDigits];
-    __shared__ int cnt[kSortThreads / 32][kMaxDigits];
-    __shared__ int warp_sum[kSortThreads / 32];
+// The first cluster sorts: each of its CTAs takes an eighth of the keys. Per pass and CTA: count the
+// digits; read the other CTAs' counts through distributed shared memory; move each key behind those
+// of smaller digits, then those of the same digit in earlier CTAs, warps, rounds and lanes. On one
+// cluster a pass costs barriers of a few hundred nanoseconds where launches of their own cost microseconds,
+// and the sort of 32768 tokens is done before the zeros of a 50000 x 1024 gradient are written.
+__global__ void __launch_bounds__(kSortThreads, 1) based_embed_sort_kernel(const SortParams p) {
+    extern __shared__ int raw[];
+    SortSmem &sm = *reinterpret_cast<SortSmem *>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
     griddep_launch_dependents();
-    const int blocks = gridDim.x, me = blockIdx.x;
-    for (int d = threadIdx.x; d < kMaxDigits; d += kSortThreads) {
+    if (blockIdx.x >= kSortCluster) {
+        const int64_t step = static_cast<int64_t>(gridDim.x - kSortCluster) * kSortThreads;
+        const int64_t at = static_cast<int64_t>(blockIdx.x - kSortCluster) * kSortThreads + threadIdx.x;
+        for (int64_t i = at; i < p.words; i += step) static_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
+        // the rest, or all of a table that starts off a 16-byte boundary, in the 2 bytes of the smallest type
+        for (int64_t i = p.words * 8 + at; i < p.bytes / 2; i += step) static_cast<uint16_t *>(p.out)[i] = 0;
+        return;
+    }
+    const int rank = static_cast<int>(cluster_rank()), digits = 1 << p.bits;
+    const int64_t begin = static_cast<int64_t>(p.N) * rank / kSortCluster, end = static_cast<int64_t>(p.N) * (rank + 1) / kSortCluster;
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        const int32_t *key_in = pass & 1 ? p.key0 : p.key1, *pos_in = pass & 1 ? p.pos0 : p.pos1;
+        int32_t *key_out = pass & 1 ? p.key1 : p.key0, *pos_out = pass & 1 ? p.pos1 : p.pos0;
+        auto key_at = [&](int64_t i) { return pass == 0 ? load_id(p.ids, p.ids64, i, p.V) : __ldcg(key_in + i); };
+        auto digit = [&](int key) { return (key >> shift) & (digits - 1); };
+        if (threadIdx.x < digits) sm.hist[threadIdx.x] = 0;
+        __syncthreads();
+        for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&sm.hist[digit(key_at(i))], 1);
+        cluster_sync();
         int total = 0, before = 0;
-        if (d < p.digits) {
-#pragma unroll 8
-            for (int k = 0; k < blocks; ++k) {
-                const int v = p.hist[static_cast<int64_t>(k) * p.digits + d];
+        if (threadIdx.x < digits) {
+#pragma unroll
+            for (int r = 0; r < kSortCluster; ++r) {
+                const int v = load_remote(&sm.hist[threadIdx.x], r);
                 total += v;
-                before += k < me ? v : 0;
+                before += r < rank ? v : 0;
             }
         }
-        base[d] = before;
-        cnt[0][d] = total;
-    }
-    __syncthreads();
-    {
-        // exclusive sum of the digits' totals, four digits a thread
-        int v[4], s = 0;
+        // exclusive sum of the totals over the digits
+        int incl = total;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = cnt[0][threadIdx.x * 4 + j], s += v[j];
-        int incl = s;
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(~0u, incl, d);
             if (lane >= d) incl += o;
         }
-        if (lane == 31) warp_sum[warp] = incl;
+        if (lane == 31) sm.warp_sum[warp] = incl;
         __syncthreads();
-        int off = incl - s;
-        for (int w = 0; w < warp; ++w) off += warp_sum[w];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            base[threadIdx.x * 4 + j] += off;
-            off += v[j];
+        if (threadIdx.x < digits) {
+            int off = incl - total + before;
+            for (int w = 0; w < warp; ++w) off += sm.warp_sum[w];
+            sm.base[threadIdx.x] = off;
         }
-    }
-    const int64_t begin = static_cast<int64_t>(me) * p.per, end = min(begin + p.per, static_cast<int64_t>(p.N));
-    for (int64_t chunk = begin; chunk < end; chunk += kSortChunk) {
-        __syncthreads();
-        for (int d = threadIdx.x; d < p.digits; d += kSortThreads) {
+        for (int64_t chunk = begin; chunk < end; chunk += kSortChunk) {
+            for (int i = threadIdx.x; i < kSortWarps * digits; i += kSortThreads) sm.cnt[i >> p.bits][i & (digits - 1)] = 0;
+            __syncthreads();
+            int key[kSortRounds], rank_in[kSortRounds];
+            // a warp's keys are consecutive
+            const int64_t first = chunk + warp * (32 * kSortRounds) + lane;
 #pragma unroll
-            for (int w = 0; w < kSortThreads / 32; ++w) cnt[w][d] = 0;
-        }
-        __syncthreads();
-        constexpr int kRounds = kSortChunk / kSortThreads;
-        int key[kRounds], rank[kRounds];
+            for (int r = 0; r < kSortRounds; ++r) key[r] = first + r * 32 < end ? key_at(first + r * 32) : -1;
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            const int64_t i = chunk + warp * (32 * kRounds) + r * 32 + lane;
-            key[r] = i < end ? sort_key(p, static_cast<int>(i)) : -1;
-            const int d = key[r] < 0 ? -1 : (key[r] >> p.shift) & (p.digits - 1);
-            const unsigned same = __match_any_sync(~0u, d);
-            const int leader = __ffs(same) - 1;
-            int old = 0;
-            if (lane == leader && d >= 0) {
-                old = cnt[warp][d];
-                cnt[warp][d] = old + __popc(same);
+            for (int r = 0; r < kSortRounds; ++r) {
+                const int d = key[r] < 0 ? -1 : digit(key[r]);
+                const unsigned same = __match_any_sync(~0u, d);
+                const int leader = __ffs(same) - 1;
+                int old = 0;
+                if (lane == leader && d >= 0) {
+                    old = sm.cnt[warp][d];
+                    sm.cnt[warp][d] = old + __popc(same);
+                }
+                rank_in[r] = __shfl_sync(~0u, old, leader) + __popc(same & ((1u << lane) - 1));
+                __syncwarp();
             }
-            rank[r] = __shfl_sync(~0u, old, leader) + __popc(same & ((1u << lane) - 1));
-            __syncwarp();
-        }
-        __syncthreads();
-        for (int d = threadIdx.x; d < p.digits; d += kSortThreads) {
-            int off = base[d];
-#pragma unroll
-            for (int w = 0; w < kSortThreads / 32; ++w) {
-                const int t = cnt[w][d];
-                cnt[w][d] = off;
-                off += t;
+            __syncthreads();
+            if (threadIdx.x < digits) {
+                int off = sm.base[threadIdx.x];
+#pragma unroll 8
+                for (int w = 0; w < kSortWarps; ++w) {
+                    const int t = sm.cnt[w][threadIdx.x];
+                    sm.cnt[w][threadIdx.x] = off;
+                    off += t;
+                }
+                sm.base[threadIdx.x] = off;
             }
-            base[d] = off;
-        }
-        __syncthreads();
+            __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            if (key[r] < 0) continue;
-            const int i = static_cast<int>(chunk) + warp * (32 * kRounds) + r * 32 + lane;
-            const int at = cnt[warp][(key[r] >> p.shift) & (p.digits - 1)] + rank[r];
-            p.key_out[at] = key[r];
-            p.pos_out[at] = p.ids ? i : p.pos_in[i];
+            for (int r = 0; r < kSortRounds; ++r) {
+                if (key[r] < 0) continue;
+                const int at = sm.cnt[warp][digit(key[r])] + rank_in[r];
+                const int i = static_cast<int>(first) + r * 32;
+                key_out[at] = key[r];
+                pos_out[at] = pass == 0 ? i : __ldcg(pos_in + i);
+            }
+            __syncthreads();
         }
+        // the counts were read and the keys are in place everywhere before the next pass
+        cluster_sync();
     }
-}
-
-struct FillParams {
-    void *out;
-    int64_t words;  // 16-byte words
-    int64_t bytes;
-};
-
-__global__ void __launch_bounds__(256) based_embed_zero_kernel(const FillParams p) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 256, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    for (int64_t i = at; i < p.words; i += step) static_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
-    // the rest, or all of a table that starts off a 16-byte boundary, in the 2 bytes of the smallest type
-    for (int64_t i = p.words * 8 + at; i < p.bytes / 2; i += step) static_cast<uint16_t *>(p.out)[i] = 0;
 }
 
 struct SumParams {
@@ -225,7 +218,8 @@ __global__ void __launch_bounds__(256) based_embed_sum_kernel(const SumParams p)
         key[i] = at >= 0 && at < p.N ? p.key[at] : -1;
         if (i < n) pos[i] = p.pos[begin + i];
     }
-    __syncthreads();
+    // padding sorts last: the rows in front of it
+    const int live = __syncthreads_count(static_cast<int>(threadIdx.x) < n && p.key[begin + threadIdx.x] < p.V);
     if (c >= p.D) return;
     const T *dy = static_cast<const T *>(p.dy) + c;
     float acc[N];
@@ -233,84 +227,97 @@ __global__ void __launch_bounds__(256) based_embed_sum_kernel(const SumParams p)
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
     bool before = key[0] == key[1];  // the run began in an earlier tile
     float *partial = p.partial + (static_cast<int64_t>(tile) * 2) * p.D + c;
-    for (int i0 = 0; i0 < n; i0 += kAhead) {
+    for (int i0 = 0; i0 < live; i0 += kAhead) {
+        // loads that depend on no condition (past the end the last row again), so that all are under way at once
         W w[kAhead][kWords];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            if (i0 + k < n && key[i0 + k + 1] < p.V) {
-                const T *row = dy + pos[i0 + k] * p.dy_sr;
+            const T *row = dy + pos[min(i0 + k, live - 1)] * p.dy_sr;
 #pragma unroll
-                for (int q = 0; q < kWords; ++q) w[k][q] = *reinterpret_cast<const W *>(row + q * kPer);
-            }
+            for (int q = 0; q < kWords; ++q) w[k][q] = *reinterpret_cast<const W *>(row + q * kPer);
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int i = i0 + k;
-            if (i >= n || key[i + 1] >= p.V) break;  // padding sorts last
+            if (i < live) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += to_f32(w[k][j / kPer].v[j % kPer]);
-            const bool last = i == n - 1;
-            if (!last && key[i + 2] == key[i + 1]) continue;
-            const bool after = last && key[i + 2] == key[i + 1];
-            if (!before && !after) {
-                store_row<G, N>(p, key[i + 1], c, acc);
-            } else {
-                float *to = partial + (before ? 0 : p.D);
+                for (int j = 0; j < N; ++j) acc[j] += to_f32(w[k][j / kPer].v[j % kPer]);
+                const bool same = key[i + 2] == key[i + 1];
+                if (!same || i == n - 1) {
+                    if (!before && !same) {
+                        store_row<G, N>(p, key[i + 1], c, acc);
+                    } else {
+                        float *to = partial + (before ? 0 : p.D);
 #pragma unroll
-                for (int j = 0; j < N; ++j) to[j] = acc[j];
+                        for (int j = 0; j < N; ++j) to[j] = acc[j];
+                    }
+                    before = false;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                }
             }
-            before = false;
-#pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] = 0.0f;
         }
     }
 }
 
-// Joins each run that crosses tiles, in the CTA of the tile it begins in.
+// Joins each run that crosses tiles, in the CTAs of the tile it begins in: 32 N columns each, the
+// run's partial sums shared out among the warps.
+constexpr int kJoinWarps = 8;
 template <typename G, int N>
-__global__ void __launch_bounds__(256) based_embed_join_kernel(const SumParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) based_embed_join_kernel(const SumParams p) {
+    __shared__ float red[kJoinWarps][N][32];
     griddep_wait();
     griddep_launch_dependents();
-    const int tile = blockIdx.x, c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
-    const int64_t begin = static_cast<int64_t>(tile) * kTileRows, end = begin + kTileRows;
-    if (end >= p.N || c >= p.D) return;  // nothing goes on after the last tile
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t tile = blockIdx.x, begin = tile * kTileRows, end = begin + kTileRows;
+    const int c = (blockIdx.y * 32 + lane) * N;
+    if (end >= p.N) return;  // nothing goes on after the last tile
     const int k = p.key[end - 1];
     if (k >= p.V || p.key[end] != k) return;
     if (begin > 0 && p.key[begin] == k && p.key[begin - 1] == k) return;  // it began earlier
+    int64_t last = tile;  // the run's last tile: 32 of the tiles' first keys at a time
+    for (unsigned same = ~0u; same == ~0u;) {
+        const int64_t at = (last + 1 + lane) * kTileRows;
+        same = __ballot_sync(~0u, at < p.N && p.key[at < p.N ? at : 0] == k);
+        last += same == ~0u ? 32 : __ffs(~same) - 1;
+    }
     float acc[N];
-    const float *from = p.partial + (static_cast<int64_t>(tile) * 2 + 1) * p.D + c;
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = from[j];
-    for (int64_t t = tile + 1; t * kTileRows < p.N && p.key[t * kTileRows] == k; ++t) {
-        from = p.partial + t * 2 * p.D + c;
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    if (c < p.D) {
+#pragma unroll 4
+        for (int64_t t = tile + warp; t <= last; t += kJoinWarps) {
+            const float *from = p.partial + (t * 2 + (t == tile ? 1 : 0)) * p.D + c;
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] += from[j];
+            for (int j = 0; j < N; ++j) acc[j] += from[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) red[warp][j][lane] = acc[j];
+    __syncthreads();
+    if (warp != 0 || c >= p.D) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] += red[w][j][lane];
     }
     store_row<G, N>(p, k, c, acc);
 }
 
 // Where the parts of based_embed_bwd's workspace lie.
 struct EmbedPlan {
-    int passes, bits, blocks, per, tiles;
-    size_t key, pos, hist, partial, bytes;  // key and pos: two buffers each
+    int passes, bits, tiles;
+    size_t list, partial, bytes;  // two lists of keys, two of positions, the partial sums
 };
 bool embed_plan(int64_t N, int V, int D, EmbedPlan &e) {
     if (N < 1 || V < 1 || D < 1 || N >= (1ll << 30)) return false;
     int bits = 1;
     while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;  // V itself is the key of padding
-    e.passes = (bits + 9) / 10;                              // at most kMaxDigits digits a pass
+    e.passes = (bits + kMaxBits - 1) / kMaxBits;
     e.bits = (bits + e.passes - 1) / e.passes;
-    int64_t per = (N + kMaxSortBlocks - 1) / kMaxSortBlocks;
-    per = (per + kSortChunk - 1) / kSortChunk * kSortChunk;
-    e.per = static_cast<int>(per);
-    e.blocks = static_cast<int>((N + per - 1) / per);
     e.tiles = static_cast<int>((N + kTileRows - 1) / kTileRows);
-    auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
-    const size_t list = up(static_cast<size_t>(N) * 4);
-    e.key = 0;
-    e.pos = 2 * list;
-    e.hist = 4 * list;
-    e.partial = e.hist + up(static_cast<size_t>(e.blocks) * (1 << e.bits) * 4);
+    e.list = (static_cast<size_t>(N) * 4 + 255) & ~static_cast<size_t>(255);
+    e.partial = 4 * e.list;
     e.bytes = e.partial + static_cast<size_t>(e.tiles) * 2 * D * 4;
     return true;
 }
@@ -320,7 +327,7 @@ int launch_sums(const SumParams &p, int tiles, cudaStream_t st) {
     const int need = (p.D + N - 1) / N, threads = need >= 256 ? 256 : (need + 31) / 32 * 32;
     const dim3 grid(tiles, (need + threads - 1) / threads);
     OPS_CUDA(launch_op(based_embed_sum_kernel<T, G, N>, grid, threads, 0, st, p));
-    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, grid, threads, 0, st, p));
+    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, dim3(tiles, (need + 31) / 32), 32 * kJoinWarps, 0, st, p));
     return BASED_OK;
 }
 template <typename T>
@@ -402,32 +409,20 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     if (rc != BASED_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    int32_t *key[2], *pos[2];
-    for (int i = 0; i < 2; ++i) {
-        key[i] = reinterpret_cast<int32_t *>(ws + e.key + i * (e.pos / 2));
-        pos[i] = reinterpret_cast<int32_t *>(ws + e.pos + i * (e.pos / 2));
-    }
+    int32_t *lists[4];
+    for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<int32_t *>(ws + i * e.list);
     const int64_t out_bytes = static_cast<int64_t>(V) * D * gs;
-    const FillParams f = {dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
-    OPS_CUDA(launch_op(based_embed_zero_kernel, dim3(sms * 8), 256, 0, st, f));
-    for (int i = 0; i < e.passes; ++i) {
-        const SortParams s = {i == 0 ? ids : nullptr,
-                              key[(i + 1) & 1],
-                              pos[(i + 1) & 1],
-                              key[i & 1],
-                              pos[i & 1],
-                              reinterpret_cast<int32_t *>(ws + e.hist),
-                              static_cast<int>(N),
-                              V,
-                              ids64 ? 1 : 0,
-                              e.per,
-                              i * e.bits,
-                              1 << e.bits};
-        OPS_CUDA(launch_op(based_embed_count_kernel, dim3(e.blocks), kSortThreads, 0, st, s));
-        OPS_CUDA(launch_op(based_embed_place_kernel, dim3(e.blocks), kSortThreads, 0, st, s));
-    }
+    const SortParams s = {ids, lists[0], lists[1], lists[2], lists[3], static_cast<int>(N), V, ids64 ? 1 : 0, e.passes,
+                          e.bits, dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
+    // one cluster sorts; enough others write the zeros: the rest of the GPU, or 16 words a thread
+    int64_t fill = (out_bytes / 16 + kSortCluster * kSortThreads * 16 - 1) / (kSortCluster * kSortThreads * 16);
+    const int64_t most = sms / kSortCluster - 4;  // clusters of eight whole SMs that the GPU holds at once
+    fill = fill < 1 ? 1 : fill < most ? fill : most;
+    OPS_CUDA(allow(based_embed_sort_kernel, sizeof(SortSmem)));
+    OPS_CUDA(launch_op(based_embed_sort_kernel, dim3(static_cast<unsigned>((fill + 1) * kSortCluster)), kSortThreads,
+                       sizeof(SortSmem), st, s, kSortCluster));
     const int done = (e.passes - 1) & 1;
-    const SumParams p = {key[done], pos[done], dy, dy_sr, static_cast<int>(N), V, D, scale,
+    const SumParams p = {lists[done], lists[2 + done], dy, dy_sr, static_cast<int>(N), V, D, scale,
                          reinterpret_cast<float *>(ws + e.partial), dtable};
     const bool wide = D % 8 == 0 && aligned(dy, 16) && dy_sr * es % 16 == 0 && aligned(dtable, 16);
     if (dtype == BASED_F32) return launch_sums<float>(p, g_dtype, wide, e.tiles, st);

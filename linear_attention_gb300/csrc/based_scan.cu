@@ -10,7 +10,6 @@
 // the state in front of them. So each input is read once and each output written once, however
 // few channels there are, and no CTA waits for one that may not be resident.
 #include <cstddef>
-#include <mutex>
 #include <type_traits>
 
 #include "ops_common.cuh"
@@ -118,15 +117,6 @@ __device__ __forceinline__ Map<N> compose(const Map<N> &m, const Map<N> &in) {
 
 __device__ unsigned int g_scan_status;  // bit 0: a wait on the cluster's maps gave up
 constexpr uint64_t kScanWaitNs = 1000000000ull;
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // The maps of a cluster's tiles, two sets in turn. A CTA's warp sends its tile's map into every CTA
 // of the cluster with stores that count their bytes on that CTA's mbarrier: nothing else has to be
@@ -583,21 +573,6 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
             if (overlap(out[i], out[k])) return BASED_ERR_ALIASING;
     }
     return BASED_OK;
-}
-
-// Once per kernel and process: its shared memory above 48 KB and clusters of 16.
-template <typename K>
-cudaError_t allow(K *kernel, size_t smem) {
-    static std::mutex m;
-    static K *done[32];
-    std::lock_guard<std::mutex> lk(m);
-    int i = 0;
-    for (; i < 32 && done[i]; ++i)
-        if (done[i] == kernel) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && i < 32) done[i] = kernel;
-    return e;
 }
 
 // CTAs of a cluster: those whose estimated time is least. A step of a CTA takes `step_us` by its

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/based_ops.h"
 #include "sm103_ptx.cuh"
@@ -61,6 +62,40 @@ cudaError_t launch_op(void (*kernel)(P), dim3 grid, int block, size_t smem, cuda
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
+// Lets a kernel have `smem` bytes of dynamic shared memory and clusters of 16; once per kernel and
+// device. K: a kernel's function type.
+template <typename K>
+cudaError_t allow(K *kernel, size_t smem) {
+    struct Done {
+        K *kernel;
+        uint64_t devices;
+    };
+    static std::mutex m;
+    static Done done[64];
+    int dev, i = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(m);
+    while (i < 63 && done[i].kernel && done[i].kernel != kernel) ++i;
+    if (done[i].kernel == kernel && (done[i].devices >> (dev & 63) & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done[i] = {kernel, (done[i].kernel == kernel ? done[i].devices : 0) | 1ull << (dev & 63)};
+    return e;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Device: clusters
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------------------------------
