@@ -13,9 +13,9 @@
 namespace based {
 namespace {
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;  // two CTAs an SM
 constexpr int kSortCluster = 8;
-constexpr int kSortRounds = 4;                             // keys of a thread at a time
+constexpr int kSortRounds = 8;                             // keys that a thread holds, at most
 constexpr int kSortChunk = kSortThreads * kSortRounds;
 constexpr int kMaxBits = 9;                                // of a digit
 constexpr int kTileRows = 32;                              // sorted positions of a tile
@@ -77,44 +77,169 @@ struct SortSmem {
     int cnt[kSortWarps][1 << kMaxBits];
 };
 
+constexpr int kFillBytes = 16384;  // zeros that one copy writes
+static_assert(sizeof(SortSmem) >= kFillBytes, "the zeros lie in the sort's shared memory");
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// A chunk of a CTA's keys in registers: `rounds` keys a thread, a warp's keys consecutive.
+struct SortChunk {
+    int key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
+    int rounds;
+    int64_t first;
+
+    __device__ __forceinline__ void load(const SortParams &p, int pass, int64_t begin, int64_t end) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int64_t n = min(end - begin, static_cast<int64_t>(kSortChunk)), last = begin + n;
+        rounds = static_cast<int>((n + kSortThreads - 1) / kSortThreads);
+        first = begin + warp * 32 * rounds + lane;
+        if (n <= 0) return;
+        // loads that depend on nothing (past the end the last key again), so that all are under way at once
+        int64_t at[kSortRounds];
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) at[r] = min(first + r * 32, last - 1);
+        if (pass > 0) {
+            const int32_t *key_in = pass & 1 ? p.key0 : p.key1, *pos_in = pass & 1 ? p.pos0 : p.pos1;
+#pragma unroll
+            for (int r = 0; r < kSortRounds; ++r) key[r] = __ldcg(key_in + at[r]);
+#pragma unroll
+            for (int r = 0; r < kSortRounds; ++r) pos[r] = __ldcg(pos_in + at[r]);
+        } else {
+            int64_t id[kSortRounds];
+            if (p.ids64) {
+#pragma unroll
+                for (int r = 0; r < kSortRounds; ++r) id[r] = static_cast<const int64_t *>(p.ids)[at[r]];
+            } else {
+#pragma unroll
+                for (int r = 0; r < kSortRounds; ++r) id[r] = static_cast<const int32_t *>(p.ids)[at[r]];
+            }
+#pragma unroll
+            for (int r = 0; r < kSortRounds; ++r) {
+                key[r] = id[r] >= 0 && id[r] < p.V ? static_cast<int>(id[r]) : p.V;
+                pos[r] = static_cast<int>(at[r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r)
+            if (r >= rounds || first + r * 32 >= last) key[r] = -1;
+    }
+    // rank: how many earlier keys of the warp have the key's digit; cnt[warp]: the warp's digits
+    __device__ __forceinline__ void count(SortSmem &sm, int shift, int digits) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        for (int d = lane; d < digits; d += 32) sm.cnt[warp][d] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) {
+            if (r >= rounds) break;
+            // lanes with the same digit, bit by bit: nine votes, where matching whole digits takes
+            // far longer (27 us instead of 16 for the sort of 32768 tokens)
+            const int d = (key[r] >> shift) & (digits - 1);
+            unsigned same = __ballot_sync(~0u, key[r] >= 0);
+#pragma unroll
+            for (int b = 0; b < kMaxBits; ++b) {
+                const unsigned set = __ballot_sync(~0u, d >> b & 1);
+                same &= d >> b & 1 ? set : ~set;
+            }
+            const int leader = same ? __ffs(same) - 1 : 0;
+            int old = 0;
+            if (lane == leader && key[r] >= 0) {
+                old = sm.cnt[warp][d];
+                sm.cnt[warp][d] = old + __popc(same);
+            }
+            rank[r] = __shfl_sync(~0u, old, leader) + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+        }
+    }
+    // cnt[warp][d] becomes the count in earlier warps, counted from `start`; returns the end
+    __device__ __forceinline__ static int scan_warps(SortSmem &sm, int d, int start) {
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int t = sm.cnt[w][d];
+            sm.cnt[w][d] = start;
+            start += t;
+        }
+        return start;
+    }
+    // base: added to the counts (where a chunk is a CTA's only one), or NULL
+    __device__ __forceinline__ void place(const SortParams &p, const SortSmem &sm, int pass, int shift, int digits, const int *base) {
+        int32_t *key_out = pass & 1 ? p.key1 : p.key0, *pos_out = pass & 1 ? p.pos1 : p.pos0;
+        const int warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int r = 0; r < kSortRounds; ++r) {
+            if (r >= rounds || key[r] < 0) continue;
+            const int d = (key[r] >> shift) & (digits - 1), at = sm.cnt[warp][d] + rank[r] + (base ? base[d] : 0);
+            key_out[at] = key[r];
+            pos_out[at] = pos[r];
+        }
+    }
+};
+
 // The first cluster sorts: each of its CTAs takes an eighth of the keys. Per pass and CTA: count the
 // digits; read the other CTAs' counts through distributed shared memory; move each key behind those
 // of smaller digits, then those of the same digit in earlier CTAs, warps, rounds and lanes. On one
-// cluster a pass costs barriers of a few hundred nanoseconds where launches of their own cost microseconds,
-// and the sort of 32768 tokens is done before the zeros of a 50000 x 1024 gradient are written.
-__global__ void __launch_bounds__(kSortThreads, 1) based_embed_sort_kernel(const SortParams p) {
+// cluster a pass costs barriers of a few hundred nanoseconds where launches of their own cost
+// microseconds. Up to 32768 tokens every key is loaded once a pass; more go through twice, in chunks.
+__global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const SortParams p) {
     extern __shared__ int raw[];
     SortSmem &sm = *reinterpret_cast<SortSmem *>(raw);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x >= kSortCluster) {
         const int64_t step = static_cast<int64_t>(gridDim.x - kSortCluster) * kSortThreads;
-        const int64_t at = static_cast<int64_t>(blockIdx.x - kSortCluster) * kSortThreads + threadIdx.x;
-        for (int64_t i = at; i < p.words; i += step) static_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
+        const int64_t at = static_cast<int64_t>(blockIdx.x - kSortCluster) * kSortThreads + tid;
+        // bulk copies of zeros from shared memory, by one thread
+        for (int i = tid; i < kFillBytes / 16; i += kSortThreads) reinterpret_cast<uint4 *>(raw)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (tid == 0) {
+            const int64_t n = p.words * 16;
+            for (int64_t i = static_cast<int64_t>(blockIdx.x - kSortCluster) * kFillBytes; i < n;
+                 i += static_cast<int64_t>(gridDim.x - kSortCluster) * kFillBytes)
+                bulk_store(static_cast<uint8_t *>(p.out) + i, smem_u32(raw), static_cast<int>(min(n - i, static_cast<int64_t>(kFillBytes))));
+            bulk_commit_group();
+            bulk_wait_group_all();
+        }
         // the rest, or all of a table that starts off a 16-byte boundary, in the 2 bytes of the smallest type
         for (int64_t i = p.words * 8 + at; i < p.bytes / 2; i += step) static_cast<uint16_t *>(p.out)[i] = 0;
         return;
     }
     const int rank = static_cast<int>(cluster_rank()), digits = 1 << p.bits;
     const int64_t begin = static_cast<int64_t>(p.N) * rank / kSortCluster, end = static_cast<int64_t>(p.N) * (rank + 1) / kSortCluster;
+    const bool once = end - begin <= kSortChunk;
+    SortChunk ch;
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * p.bits;
-        const int32_t *key_in = pass & 1 ? p.key0 : p.key1, *pos_in = pass & 1 ? p.pos0 : p.pos1;
-        int32_t *key_out = pass & 1 ? p.key1 : p.key0, *pos_out = pass & 1 ? p.pos1 : p.pos0;
-        auto key_at = [&](int64_t i) { return pass == 0 ? load_id(p.ids, p.ids64, i, p.V) : __ldcg(key_in + i); };
-        auto digit = [&](int key) { return (key >> shift) & (digits - 1); };
-        if (threadIdx.x < digits) sm.hist[threadIdx.x] = 0;
-        __syncthreads();
-        for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) atomicAdd(&sm.hist[digit(key_at(i))], 1);
+        if (once) {
+            ch.load(p, pass, begin, end);
+            ch.count(sm, shift, digits);
+            __syncthreads();
+            if (tid < digits) sm.hist[tid] = SortChunk::scan_warps(sm, tid, 0);
+        } else {
+            int mine = 0;
+            for (int64_t chunk = begin; chunk < end; chunk += kSortChunk) {
+                ch.load(p, pass, chunk, end);
+                ch.count(sm, shift, digits);
+                __syncthreads();
+                if (tid < digits) {
+#pragma unroll
+                    for (int w = 0; w < kSortWarps; ++w) mine += sm.cnt[w][tid];
+                }
+                __syncthreads();
+            }
+            if (tid < digits) sm.hist[tid] = mine;
+        }
         cluster_sync();
         int total = 0, before = 0;
-        if (threadIdx.x < digits) {
+        if (tid < digits) {
+            int v[kSortCluster];
+#pragma unroll
+            for (int r = 0; r < kSortCluster; ++r) v[r] = load_remote(&sm.hist[tid], r);
 #pragma unroll
             for (int r = 0; r < kSortCluster; ++r) {
-                const int v = load_remote(&sm.hist[threadIdx.x], r);
-                total += v;
-                before += r < rank ? v : 0;
+                total += v[r];
+                before += r < rank ? v[r] : 0;
             }
         }
         // exclusive sum of the totals over the digits
@@ -126,53 +251,24 @@ __global__ void __launch_bounds__(kSortThreads, 1) based_embed_sort_kernel(const
         }
         if (lane == 31) sm.warp_sum[warp] = incl;
         __syncthreads();
-        if (threadIdx.x < digits) {
+        if (tid < digits) {
             int off = incl - total + before;
             for (int w = 0; w < warp; ++w) off += sm.warp_sum[w];
-            sm.base[threadIdx.x] = off;
+            sm.base[tid] = off;
         }
-        for (int64_t chunk = begin; chunk < end; chunk += kSortChunk) {
-            for (int i = threadIdx.x; i < kSortWarps * digits; i += kSortThreads) sm.cnt[i >> p.bits][i & (digits - 1)] = 0;
-            __syncthreads();
-            int key[kSortRounds], rank_in[kSortRounds];
-            // a warp's keys are consecutive
-            const int64_t first = chunk + warp * (32 * kSortRounds) + lane;
-#pragma unroll
-            for (int r = 0; r < kSortRounds; ++r) key[r] = first + r * 32 < end ? key_at(first + r * 32) : -1;
-#pragma unroll
-            for (int r = 0; r < kSortRounds; ++r) {
-                const int d = key[r] < 0 ? -1 : digit(key[r]);
-                const unsigned same = __match_any_sync(~0u, d);
-                const int leader = __ffs(same) - 1;
-                int old = 0;
-                if (lane == leader && d >= 0) {
-                    old = sm.cnt[warp][d];
-                    sm.cnt[warp][d] = old + __popc(same);
-                }
-                rank_in[r] = __shfl_sync(~0u, old, leader) + __popc(same & ((1u << lane) - 1));
-                __syncwarp();
+        __syncthreads();
+        if (once) {
+            ch.place(p, sm, pass, shift, digits, sm.base);
+        } else {
+            for (int64_t chunk = begin; chunk < end; chunk += kSortChunk) {
+                ch.load(p, pass, chunk, end);
+                ch.count(sm, shift, digits);
+                __syncthreads();
+                if (tid < digits) sm.base[tid] = SortChunk::scan_warps(sm, tid, sm.base[tid]);
+                __syncthreads();
+                ch.place(p, sm, pass, shift, digits, nullptr);
+                __syncthreads();
             }
-            __syncthreads();
-            if (threadIdx.x < digits) {
-                int off = sm.base[threadIdx.x];
-#pragma unroll 8
-                for (int w = 0; w < kSortWarps; ++w) {
-                    const int t = sm.cnt[w][threadIdx.x];
-                    sm.cnt[w][threadIdx.x] = off;
-                    off += t;
-                }
-                sm.base[threadIdx.x] = off;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < kSortRounds; ++r) {
-                if (key[r] < 0) continue;
-                const int at = sm.cnt[warp][digit(key[r])] + rank_in[r];
-                const int i = static_cast<int>(first) + r * 32;
-                key_out[at] = key[r];
-                pos_out[at] = pass == 0 ? i : __ldcg(pos_in + i);
-            }
-            __syncthreads();
         }
         // the counts were read and the keys are in place everywhere before the next pass
         cluster_sync();
@@ -260,48 +356,69 @@ __global__ void __launch_bounds__(256) based_embed_sum_kernel(const SumParams p)
     }
 }
 
-// Joins each run that crosses tiles, in the CTAs of the tile it begins in: 32 N columns each, the
-// run's partial sums shared out among the warps.
-constexpr int kJoinWarps = 8;
+// Joins each run that crosses tiles: a warp looks at one tile and 32 N columns, and sums the run that begins
+// there and goes on after it; the CTA's warps share a run of more than kJoinAlone tiles.
+constexpr int kJoinWarps = 8, kJoinAlone = 8;
 template <typename G, int N>
 __global__ void __launch_bounds__(32 * kJoinWarps) based_embed_join_kernel(const SumParams p) {
     __shared__ float red[kJoinWarps][N][32];
+    __shared__ int64_t last_of[kJoinWarps];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t tile = blockIdx.x, begin = tile * kTileRows, end = begin + kTileRows;
     const int c = (blockIdx.y * 32 + lane) * N;
-    if (end >= p.N) return;  // nothing goes on after the last tile
-    const int k = p.key[end - 1];
-    if (k >= p.V || p.key[end] != k) return;
-    if (begin > 0 && p.key[begin] == k && p.key[begin - 1] == k) return;  // it began earlier
-    int64_t last = tile;  // the run's last tile: 32 of the tiles' first keys at a time
-    for (unsigned same = ~0u; same == ~0u;) {
-        const int64_t at = (last + 1 + lane) * kTileRows;
-        same = __ballot_sync(~0u, at < p.N && p.key[at < p.N ? at : 0] == k);
-        last += same == ~0u ? 32 : __ffs(~same) - 1;
-    }
-    float acc[N];
+    // lane i: the partial sums of tiles first + i, first + i + step, ... up to last
+    auto add = [&](float (&acc)[N], int64_t tile, int64_t first, int64_t last, int step) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-    if (c < p.D) {
+        for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+        if (c >= p.D) return;
 #pragma unroll 4
-        for (int64_t t = tile + warp; t <= last; t += kJoinWarps) {
+        for (int64_t t = first; t <= last; t += step) {
             const float *from = p.partial + (t * 2 + (t == tile ? 1 : 0)) * p.D + c;
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] += from[j];
         }
+    };
+    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps, tile = tile0 + warp;
+    const int64_t begin = tile * kTileRows, end = begin + kTileRows;
+    int64_t last = -1;  // the last tile of the run that begins in this one and goes on; -1: none does
+    if (end < p.N) {
+        // the tile's last key, the next one, its first and the one before; then the first keys of the tiles after the next
+        const int k = p.key[end], in = p.key[end - 1], first = p.key[begin], earlier = begin > 0 ? p.key[begin - 1] : -1;
+        if (k < p.V && in == k && !(first == k && earlier == k)) {
+            last = tile;
+            for (unsigned same = ~0u; same == ~0u;) {  // 32 tiles at a time
+                const int64_t at = (last + 1 + lane) * kTileRows;
+                same = __ballot_sync(~0u, at < p.N && p.key[at < p.N ? at : 0] == k);
+                last += same == ~0u ? 32 : __ffs(~same) - 1;
+            }
+            if (last - tile < kJoinAlone) {
+                float acc[N];
+                add(acc, tile, tile, last, 1);
+                if (c < p.D) store_row<G, N>(p, k, c, acc);
+                last = -1;
+            }
+        }
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) red[warp][j][lane] = acc[j];
+    if (lane == 0) last_of[warp] = last;
     __syncthreads();
-    if (warp != 0 || c >= p.D) return;
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (last_of[w] < 0) continue;
+        float acc[N];
+        add(acc, tile0 + w, tile0 + w + warp, last_of[w], kJoinWarps);
 #pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) {
+        for (int j = 0; j < N; ++j) red[warp][j][lane] = acc[j];
+        __syncthreads();
+        if (warp == 0 && c < p.D) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] += red[w][j][lane];
+            for (int i = 1; i < kJoinWarps; ++i) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += red[i][j][lane];
+            }
+            store_row<G, N>(p, p.key[(tile0 + w + 1) * kTileRows], c, acc);
+        }
+        __syncthreads();
     }
-    store_row<G, N>(p, k, c, acc);
 }
 
 // Where the parts of based_embed_bwd's workspace lie.
@@ -327,7 +444,7 @@ int launch_sums(const SumParams &p, int tiles, cudaStream_t st) {
     const int need = (p.D + N - 1) / N, threads = need >= 256 ? 256 : (need + 31) / 32 * 32;
     const dim3 grid(tiles, (need + threads - 1) / threads);
     OPS_CUDA(launch_op(based_embed_sum_kernel<T, G, N>, grid, threads, 0, st, p));
-    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, dim3(tiles, (need + 31) / 32), 32 * kJoinWarps, 0, st, p));
+    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, dim3((tiles + kJoinWarps - 1) / kJoinWarps, (need + 31) / 32), 32 * kJoinWarps, 0, st, p));
     return BASED_OK;
 }
 template <typename T>
@@ -416,7 +533,8 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
                           e.bits, dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
     // one cluster sorts; enough others write the zeros: the rest of the GPU, or 16 words a thread
     int64_t fill = (out_bytes / 16 + kSortCluster * kSortThreads * 16 - 1) / (kSortCluster * kSortThreads * 16);
-    const int64_t most = sms / kSortCluster - 4;  // clusters of eight whole SMs that the GPU holds at once
+    // no more clusters than are resident at once (a cluster's CTAs share a part of the GPU, which leaves some SMs over)
+    const int64_t most = 2 * sms / kSortCluster * 4 / 5;
     fill = fill < 1 ? 1 : fill < most ? fill : most;
     OPS_CUDA(allow(based_embed_sort_kernel, sizeof(SortSmem)));
     OPS_CUDA(launch_op(based_embed_sort_kernel, dim3(static_cast<unsigned>((fill + 1) * kSortCluster)), kSortThreads,
