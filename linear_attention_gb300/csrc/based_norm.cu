@@ -8,6 +8,8 @@
 // registers: one read of x serves the mean, the squared deviations and the result. Up to 32
 // threads reduce by shuffles; larger groups take a whole CTA. A CTA keeps its channels and walks
 // over rows, so that weights are loaded once and their gradients add up in registers.
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace based {
@@ -35,18 +37,23 @@ __device__ __forceinline__ float load_param(const void *p, int dtype, int i, flo
 }
 
 // Eight channels of a row. VEC: consecutive ones, loaded as 16-byte words; otherwise channels
-// l, l + tpg, ... of the group. n: the channels of the group from this thread's first on. What the
-// thread does not hold is zero.
+// l, l + tpg, ... of the group. n: the channels of the group from this thread's first on. A load
+// leaves what the thread does not hold as it is (zero from clear()).
 template <typename T, bool VEC>
 struct Row;
 template <typename T>
 struct Row<T, true> {
     static constexpr int kQuads = sizeof(T) * kElems / 16;
     uint32_t w[kQuads * 4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < 4 * kQuads; ++k) w[k] = 0;
+    }
     __device__ __forceinline__ void load(const T *p, int n, int) {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
-            const uint4 q = n > 0 ? reinterpret_cast<const uint4 *>(p)[k] : make_uint4(0, 0, 0, 0);
+            if (n <= 0) continue;
+            const uint4 q = reinterpret_cast<const uint4 *>(p)[k];
             w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
         }
     }
@@ -71,9 +78,14 @@ struct Row<T, true> {
 template <typename T>
 struct Row<T, false> {
     T w[kElems];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kElems; ++k) w[k] = from_f32<T>(0.0f);
+    }
     __device__ __forceinline__ void load(const T *p, int n, int step) {
 #pragma unroll
-        for (int k = 0; k < kElems; ++k) w[k] = k * step < n ? p[k * step] : from_f32<T>(0.0f);
+        for (int k = 0; k < kElems; ++k)
+            if (k * step < n) w[k] = p[k * step];
     }
     __device__ __forceinline__ void store(T *p, int n, int step) const {
 #pragma unroll
@@ -91,7 +103,9 @@ struct Row<T, false> {
 // CTA); `red` holds 16 K floats, and calls in a row use different ones.
 template <int K, bool BIG>
 __device__ __forceinline__ void group_sum(float (&v)[K], int tpg, float *red) {
-    for (int d = BIG ? min(tpg, 32) >> 1 : tpg >> 1; d > 0; d >>= 1) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        if (tpg <= d) continue;
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(~0u, v[k], d);
     }
@@ -114,17 +128,29 @@ __device__ __forceinline__ float total(const Vec<2> (&v)[kElems / 2]) {
 }
 
 // act(v) and act'(v)
-__device__ __forceinline__ void activate(int act, const Vec<2> &v, Vec<2> &f, Vec<2> &df) {
-    if (act == BASED_ACT_NONE) {
+template <int ACT>
+__device__ __forceinline__ void activate(const Vec<2> &v, Vec<2> &f, Vec<2> &df) {
+    if (ACT == BASED_ACT_NONE) {
         f = v, df = splat<2>(1.0f);
         return;
     }
     Vec<2> s, t;
     vsigmoid<false>(v, s, t);
-    if (act == BASED_ACT_SIGMOID)
+    if (ACT == BASED_ACT_SIGMOID)
         f = s, df = vmul(s, t);
     else
         f = vmul(v, s), df = vfma(f, t, s);
+}
+
+// f with the activation as a compile-time constant
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    if (act == BASED_ACT_SILU)
+        f(std::integral_constant<int, BASED_ACT_SILU>());
+    else if (act == BASED_ACT_SIGMOID)
+        f(std::integral_constant<int, BASED_ACT_SIGMOID>());
+    else
+        f(std::integral_constant<int, BASED_ACT_NONE>());
 }
 
 // Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
@@ -165,15 +191,20 @@ __global__ void __launch_bounds__(BIG ? 512 : BWD ? 128 : 256, BIG ? 1 : BWD ? 6
     // the next row is loaded while a row is worked on
     Row<TX, VEC> nx;
     Row<TY, VEC> nz, nd;
-    auto fetch = [&](int64_t row, int m) {
-        nx.load(static_cast<const TX *>(p.x) + row * p.x_sr + c, m, step);
-        if (GATED) nz.load(static_cast<const TY *>(p.gate) + row * p.gate_sr + c, m, step);
-        if (BWD) nd.load(static_cast<const TY *>(p.dy) + row * p.dy_sr + c, m, step);
-    };
+    nx.clear(), nz.clear(), nd.clear();
     const int64_t turn = static_cast<int64_t>(gridDim.x) * p.rp;
     int64_t row = static_cast<int64_t>(blockIdx.x) * p.rp + r;
-    int m = row < p.R ? n : 0;
-    fetch(row, m);
+    const TX *px = static_cast<const TX *>(p.x) + row * p.x_sr + c;
+    const TY *pz = static_cast<const TY *>(p.gate) + row * p.gate_sr + c, *pd = static_cast<const TY *>(p.dy) + row * p.dy_sr + c;
+    int64_t out = row * p.C + c;
+    // past the last row the registers keep an earlier one
+    auto fetch = [&] {
+        const int m = row < p.R ? n : 0;
+        nx.load(px, m, step);
+        if (GATED) nz.load(pz, m, step);
+        if (BWD) nd.load(pd, m, step);
+    };
+    fetch();
     __syncthreads();
     // every thread takes part in the sums of every turn: the bound is the CTA's first row
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * p.rp; base < p.R; base += turn) {
@@ -181,11 +212,11 @@ __global__ void __launch_bounds__(BIG ? 512 : BWD ? 128 : 256, BIG ? 1 : BWD ? 6
         Row<TY, VEC> rz, rd;
         if (GATED) rz = nz;
         if (BWD) rd = nd;
-        const int64_t here = row;
-        const int mh = m;
+        const int mh = row < p.R ? n : 0;
         row += turn;
-        m = row < p.R ? n : 0;
-        fetch(row, m);
+        px += turn * p.x_sr, pz += turn * p.gate_sr, pd += turn * p.dy_sr;
+        fetch();
+        if (BWD && mh <= 0) rd.clear();  // adds nothing to dweight and dbias
         Vec<2> h[P], sq[P];
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = rx.get(k);
@@ -212,40 +243,45 @@ __global__ void __launch_bounds__(BIG ? 512 : BWD ? 128 : 256, BIG ? 1 : BWD ? 6
         };
         if (!BWD) {
             Row<TY, VEC> ry;
+            with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const Vec<2> v = vfma(vmul(h[k], splat<2>(rstd)), param(k, 0), param(k, 1));
-                Vec<2> f, df;
-                activate(p.act, GATED ? rz.get(k) : v, f, df);
-                ry.set(k, GATED ? vmul(v, f) : f);
-            }
-            ry.store(static_cast<TY *>(p.y) + here * p.C + c, mh, step);
+                for (int k = 0; k < P; ++k) {
+                    const Vec<2> v = vfma(vmul(h[k], splat<2>(rstd)), param(k, 0), param(k, 1));
+                    Vec<2> f, df;
+                    activate<decltype(act)::value>(GATED ? rz.get(k) : v, f, df);
+                    ry.set(k, GATED ? vmul(v, f) : f);
+                }
+            });
+            ry.store(static_cast<TY *>(p.y) + out, mh, step);
         } else {
             Row<TY, VEC> oz;
             Row<TX, VEC> ox;
             Vec<2> q[P], s0 = splat<2>(0.0f), sh = splat<2>(0.0f);
+            with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                h[k] = vmul(h[k], splat<2>(rstd));
-                const Vec<2> w = param(k, 0), v = vfma(h[k], w, param(k, 1)), d = rd.get(k);
-                Vec<2> f, df;
-                activate(p.act, GATED ? rz.get(k) : v, f, df);
-                const Vec<2> dv = vmul(d, GATED ? f : df);
-                if (GATED) oz.set(k, vmul(vmul(d, v), df));
-                dw[k] = vfma(dv, h[k], dw[k]);
-                db[k] = vadd(db[k], dv);
-                q[k] = vmul(dv, w);
-                s0 = vadd(s0, q[k]);
-                sh = vfma(q[k], h[k], sh);
-            }
-            if (GATED) oz.store(static_cast<TY *>(p.dgate) + here * p.C + c, mh, step);
+                for (int k = 0; k < P; ++k) {
+                    h[k] = vmul(h[k], splat<2>(rstd));
+                    const Vec<2> w = param(k, 0), v = vfma(h[k], w, param(k, 1)), d = rd.get(k);
+                    Vec<2> f, df;
+                    activate<decltype(act)::value>(GATED ? rz.get(k) : v, f, df);
+                    const Vec<2> dv = vmul(d, GATED ? f : df);
+                    if (GATED) oz.set(k, vmul(vmul(d, v), df));
+                    dw[k] = vfma(dv, h[k], dw[k]);
+                    db[k] = vadd(db[k], dv);
+                    q[k] = vmul(dv, w);
+                    s0 = vadd(s0, q[k]);
+                    sh = vfma(q[k], h[k], sh);
+                }
+            });
+            if (GATED) oz.store(static_cast<TY *>(p.dgate) + out, mh, step);
             float s[2] = {s0.v[0] + s0.v[1], sh.v[0] + sh.v[1]};
             group_sum<2, BIG>(s, p.tpg, smem + 32);
             const Vec<2> m0 = splat<2>(-s[0] * inv), m1 = splat<2>(-s[1] * inv), scale = splat<2>(rstd);
 #pragma unroll
             for (int k = 0; k < P; ++k) ox.set(k, vmul(scale, vfma(h[k], m1, vadd(q[k], m0))));
-            ox.store(static_cast<TX *>(p.dx) + here * p.C + c, mh, step);
+            ox.store(static_cast<TX *>(p.dx) + out, mh, step);
         }
+        out += turn * p.C;
     }
     if (BWD && p.partial) {
         // the CTA's rows side by side are added in shared memory, in order
