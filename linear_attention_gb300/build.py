@@ -1,8 +1,9 @@
-"""Builds the CUDA library in-tree with nvcc (sm_103a only)."""
+"""Builds the CUDA library in-tree with nvcc (sm_103a only), and the operators' Python binding with g++."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -13,6 +14,9 @@ SOURCES = [os.path.join(CSRC, f) for f in ("based_fwd.cu", "based_scan.cu", "bas
 DEPS = SOURCES + [os.path.join(CSRC, "based_kernels.cuh"), os.path.join(CSRC, "sm103_ptx.cuh"),
                   os.path.join(CSRC, "based_plan.h"), os.path.join(CSRC, "ops_common.cuh"),
                   os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]
+BINDING_PATH = os.path.join(LIB_DIR, "based_ops_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "ops_binding.cpp")
+BINDING_DEPS = [BINDING_SOURCE, os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-Xcompiler", "-fvisibility=hidden",
               "--threads", "0"]  # the sources compile side by side
@@ -23,19 +27,55 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _fresh(path: str, deps) -> bool:
+    """Whether path exists and is not older than any of deps."""
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def _binding_commands(obj: str, out: str):
+    """The compilation of the binding, and its link against the built library."""
+    import torch
+
+    top = os.path.dirname(torch.__file__)
+    include = [os.path.join(top, "include"), os.path.join(top, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"), sysconfig.get_paths()["include"]]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in include:
+        compile_ += ["-isystem", d]
+    link = ["g++", "-shared", obj, "-o", out, "-L" + LIB_DIR, "-lbased_gb300", "-Wl,-rpath,$ORIGIN",
+            "-L" + os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return compile_ + ["-c", BINDING_SOURCE, "-o", obj], link
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the shared library if it is missing or older than any of its sources."""
+    """Compile the shared library, and the operators' binding to it, where they are missing or older
+    than any of their sources."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB_PATH):
-        t = os.path.getmtime(LIB_PATH)
-        if all(os.path.getmtime(p) <= t for p in DEPS):
-            return LIB_PATH
-    tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc()] + NVCC_FLAGS + SOURCES + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB_PATH)
+    obj = BINDING_PATH[:-3] + ".o"
+    compile_, link = _binding_commands(obj, BINDING_PATH + ".tmp")
+    compiler = None
+    if force or not _fresh(BINDING_PATH, BINDING_DEPS):
+        if verbose:
+            print(" ".join(compile_))
+        compiler = subprocess.Popen(compile_)  # beside nvcc
+    try:
+        if force or not _fresh(LIB_PATH, DEPS):
+            tmp = LIB_PATH + ".tmp"
+            cmd = [nvcc()] + NVCC_FLAGS + SOURCES + ["-o", tmp]
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.run(cmd, check=True)
+            os.replace(tmp, LIB_PATH)
+    finally:
+        failed = compiler is not None and compiler.wait() != 0
+    if failed:
+        raise subprocess.CalledProcessError(compiler.returncode, compile_)
+    if compiler is not None:
+        if verbose:
+            print(" ".join(link))
+        subprocess.run(link, check=True)
+        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
 

@@ -333,9 +333,16 @@ __global__ void __launch_bounds__(32 * kSumWarps) based_norm_sum_kernel(const No
     griddep_wait();
     griddep_launch_dependents();
     float s = 0.0f;
-    if (c < 2 * p.C) {
-#pragma unroll 8
-        for (int k = warp; k < p.parts; k += kSumWarps) s += p.partial[static_cast<int64_t>(k) * 2 * p.C + c];
+    constexpr int kAhead = 20;  // loads under way at once: the sums of 640 CTAs, the most there are, in one go
+    for (int k0 = warp; k0 < p.parts && c < 2 * p.C; k0 += kAhead * kSumWarps) {
+        float v[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int k = k0 + i * kSumWarps;
+            v[i] = k < p.parts ? p.partial[static_cast<int64_t>(k) * 2 * p.C + c] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) s += v[i];
     }
     red[warp][lane] = s;
     __syncthreads();
