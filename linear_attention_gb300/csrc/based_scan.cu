@@ -185,27 +185,25 @@ __device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
     for (int j = 0; j < N; ++j) v.v[j] = src && j < n ? src[j] : 0.0f;
 }
 
-// The rows of sequence b before its padding. Kernels without lengths (RAGGED false) are instances of
-// their own: a bound that comes from memory makes the loop over the tiles one of threads that might
-// diverge, which costs the forward pass over 16384 x 2048 a third more time (62 us, not 45).
+// The rows of sequence b before its padding. The loops over the tiles run to T all the same, and steps in
+// the padding skip their work between the barriers: a bound that comes from memory makes the loop one
+// of threads that might diverge, which costs a third more time. Kernels without lengths (RAGGED
+// false) are instances of their own.
 template <bool RAGGED>
 __device__ __forceinline__ int sequence_length(const ScanParams &p, int b) {
     return RAGGED ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
-// Zeros in the rows [row0, T) of an output's columns of this cluster, by all threads of its CTAs.
-template <typename T, int THREADS>
-__device__ __forceinline__ void zero_rows(T *out, int row0, const ScanParams &p, int n, int rank, int lane, int warp) {
-    if (n <= 0) return;
-    constexpr int N = 4 / sizeof(T), kWarps = THREADS / 32;
-    const int step = p.cluster * kWarps;
-    T *to = out + static_cast<int64_t>(row0 + rank * kWarps + warp) * p.D;
-    for (int row = row0 + rank * kWarps + warp; row < p.T; row += step) {
+// Zeros in an output's rows [row0, row0 + R).
+template <int R, typename T>
+__device__ __forceinline__ void zero_rows(T *to, const ScanParams &p, int row0, int n) {
+    constexpr int N = 4 / sizeof(T);
+    for (int i = 0; i < R && row0 + i < p.T; ++i) {
         if (p.pair && n == N)
             *reinterpret_cast<uint32_t *>(to) = 0;
         else
             store_some(to, splat<N>(0.0f), n);
-        to += static_cast<int64_t>(step) * p.D;
+        to += p.D;
     }
 }
 
@@ -214,14 +212,14 @@ __device__ __forceinline__ void zero_rows(T *out, int row0, const ScanParams &p,
 template <typename T>
 struct Place {
     static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
-    int lane, warp, rank, b, c0, c, n, cols, tiles;
+    int lane, warp, rank, b, c0, c, n, cols, tiles, steps;
     __device__ __forceinline__ explicit Place(const ScanParams &p) {
         lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
         const int slab = static_cast<int>(blockIdx.x) / p.cluster;
         b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
         n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
-        tiles = (p.T + kTile - 1) / kTile;
+        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) / p.cluster;
     }
 };
 
@@ -273,9 +271,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     for (int k = 0; k < kFwdStages; ++k) fetch(k);
     cp_async_wait<kFwdStages - 1>();
     __syncthreads();
-    const int live = (len + kTile * cs - 1) / (kTile * cs);  // steps with rows before the padding
-    for (int step = 0; step < live; ++step) {
+    for (int step = 0; step < at.steps; ++step) {
         const int tile = step * cs + at.rank, row0 = tile * kTile + warp * R;
+        const bool live = !RAGGED || step * cs * kTile < len;  // some row of the cluster's tiles is no padding
         const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
         const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * kRowBytes + lane * 4;
         Vec<N> a[R], u[R];
@@ -293,55 +291,54 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         };
         if (full)
             rows(std::true_type());
-        else
+        else if (row0 < len)
             rows(std::false_type());
         sm.warp[warp][lane] = m;
         __syncthreads();  // the maps are there, and this step's stage is free
         fetch(step + kFwdStages);
         if (warp == 0) {
             Vec<N> h = carry;
-            Map<N> all[kFwdWarps];  // of the tile's rows up to each warp's last
+            if (live) {
+                Map<N> all[kFwdWarps];  // of the tile's rows up to each warp's last
 #pragma unroll
-            for (int w = 0; w < kFwdWarps; ++w) all[w] = w ? compose(sm.warp[w][lane], all[w - 1]) : sm.warp[w][lane];
-            if (cs > 1) {
-                if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[kFwdWarps - 1]);
-                sm.ex.fold(step, cs, at.rank, lane, h, carry);
-            } else {
-                carry = apply(all[kFwdWarps - 1], carry);
+                for (int w = 0; w < kFwdWarps; ++w) all[w] = w ? compose(sm.warp[w][lane], all[w - 1]) : sm.warp[w][lane];
+                if (cs > 1) {
+                    if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[kFwdWarps - 1]);
+                    sm.ex.fold(step, cs, at.rank, lane, h, carry);
+                } else {
+                    carry = apply(all[kFwdWarps - 1], carry);
+                }
+                sm.start[0][lane] = h;
+#pragma unroll
+                for (int w = 1; w < kFwdWarps; ++w) sm.start[w][lane] = apply(all[w - 1], h);
             }
             if (p.saved && tile < at.tiles)
                 store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, h, at.n);
-            sm.start[0][lane] = h;
-#pragma unroll
-            for (int w = 1; w < kFwdWarps; ++w) sm.start[w][lane] = apply(all[w - 1], h);
         }
         cp_async_wait<kFwdStages - 1>();
         __syncthreads();  // the starts are there, and the next step's tile
-        Vec<N> h = sm.start[warp][lane];
         T *to = y + static_cast<int64_t>(row0) * p.D;
         if (full && wide) {
+            Vec<N> h = sm.start[warp][lane];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
                 *reinterpret_cast<uint32_t *>(to) = pack<T>(h);
                 to += p.D;
             }
-        } else {
+        } else if (row0 < len) {
+            Vec<N> h = sm.start[warp][lane];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
                 if (row0 + i < p.T) store_some(to, row0 + i < len ? h : splat<N>(0.0f), at.n);
                 to += p.D;
             }
+        } else if (RAGGED) {
+            zero_rows<R>(to, p, row0, at.n);
         }
     }
-    if (RAGGED) zero_rows<T, kThreads>(y, live * kTile * cs, p, at.n, at.rank, lane, warp);
-    if (warp == 0) {
-        if (RAGGED && p.saved)
-            for (int tile = live * cs + at.rank; tile < at.tiles; tile += cs)
-                store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, carry, at.n);
-        if (at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
-    }
+    if (warp == 0 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
     if (cs > 1) cluster_sync();  // no CTA leaves while another one may still write to it
 }
 
@@ -351,8 +348,11 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
 // The tiles from the last to the first. With mu = what the rows after a row pass back to it,
 // lam_t = dy_t + mu and mu <- a_t lam_t: the map of a stretch in reversed time is mu -> A mu + M
 // with the same A. h inside a tile is rebuilt from the state saved before it.
-// Warp w of a CTA: rows [8 w, 8 w + 8) of its tile.
-constexpr int kBwdWarps = 8, kBwdStages = 3;
+// Warp w of a CTA: rows [16 w, 16 w + 16) of its tile. A thread keeps its rows' decays and what the mode
+// needs besides: 1 - a for logistic gates, the states in front of the rows for log decays. The rest stays in
+// shared memory, where the differences h_{t-1} - x_t of logistic gates take the places of the gate and x (each thread
+// reads and writes its own words alone).
+constexpr int kBwdWarps = 4, kBwdStages = 2;
 template <int N>
 struct BwdSmem {
     uint8_t tile[kBwdStages][3][kTile * kRowBytes];
@@ -364,7 +364,7 @@ struct BwdSmem {
 };
 
 template <typename T, int MODE, bool RAGGED>
-__global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
     BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
     Vec<N> carry;  // warp 1's: mu behind the cluster's tiles
     load_state(p.state ? p.state + plane : nullptr, at.n, carry);
     bool waiting = true;
-    const int tiles = (len + kTile - 1) / kTile, steps = (tiles + cs - 1) / cs;  // those before the padding
-    auto tile_of = [&](int step) { return tiles - 1 - (step * cs + at.rank); };
+    int exchanges = 0;
+    auto tile_of = [&](int step) { return at.tiles - 1 - (step * cs + at.rank); };
     auto fetch = [&](int step) {
         const int row = tile_of(step) * kTile, rows = min(len - row, kTile);
         if (row >= 0 && rows > 0) {
@@ -405,41 +405,41 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
         load_state(tile >= 0 ? p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c : nullptr, at.n, saved);
     };
     if (warp == 0) fetch_state(0);
-#pragma unroll
-    for (int k = 0; k < kBwdStages; ++k) fetch(k);
-    cp_async_wait<kBwdStages - 1>();
-    __syncthreads();
-    for (int step = 0; step < steps; ++step) {
+    fetch(0);
+    for (int step = 0; step < at.steps; ++step) {
         const int tile = tile_of(step), row0 = tile * kTile + warp * R;
-        const uint8_t(*st)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
-        const int off = warp * R * kRowBytes + lane * 4;
-        const bool full = tile >= 0 && row0 + R <= len;
-        Vec<N> a[R], rest[R], rev = splat<N>(0.0f);
-        uint32_t v[R], d[R];
+        const bool live = !RAGGED || (at.tiles - (step + 1) * cs) * kTile < len;  // some row of the cluster's tiles is no padding
+        cp_async_wait<0>();
+        __syncthreads();  // the tile has landed
+        uint8_t *sg = sm.tile[step % kBwdStages][0] + warp * R * kRowBytes + lane * 4;
+        uint8_t *sx = sg + kTile * kRowBytes, *sd = sx + kTile * kRowBytes;
+        auto word = [&](uint8_t *s, int i) -> uint32_t & { return *reinterpret_cast<uint32_t *>(s + i * kRowBytes); };
+        const bool full = tile >= 0 && row0 + R <= len, some = tile >= 0 && row0 < len;
+        Vec<N> a[R], other[R], rev = splat<N>(0.0f);  // other: 1 - a, or the states in front of the rows
         Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
         auto rows = [&](auto all_live) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                decay<MODE>(unpack<T>(*reinterpret_cast<const uint32_t *>(st[0] + off + i * kRowBytes)), a[i], rest[i]);
-                v[i] = *reinterpret_cast<const uint32_t *>(st[1] + off + i * kRowBytes);
-                d[i] = *reinterpret_cast<const uint32_t *>(st[2] + off + i * kRowBytes);
-                if (!decltype(all_live)::value && !(tile >= 0 && row0 + i < len)) {
-                    a[i] = splat<N>(1.0f), rest[i] = splat<N>(0.0f);
-                    v[i] = d[i] = 0;
+                Vec<N> rest;
+                decay<MODE>(unpack<T>(word(sg, i)), a[i], rest);
+                if (!decltype(all_live)::value && row0 + i >= len) {
+                    a[i] = splat<N>(1.0f), rest = splat<N>(0.0f);
+                    word(sx, i) = word(sd, i) = 0;
                 }
-                m = compose(Map<N>{a[i], increment<MODE>(rest[i], unpack<T>(v[i]))}, m);
+                if (MODE == BASED_GATE_SIGMOID) other[i] = rest;
+                m = compose(Map<N>{a[i], increment<MODE>(rest, unpack<T>(word(sx, i)))}, m);
             }
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) rev = vmul(a[i], vadd(unpack<T>(word(sd, i)), rev));
         };
         if (full)
             rows(std::true_type());
-        else
+        else if (some)
             rows(std::false_type());
-#pragma unroll
-        for (int i = R - 1; i >= 0; --i) rev = vmul(a[i], vadd(unpack<T>(d[i]), rev));
         sm.warp[warp][lane] = m;
         sm.rev[warp][lane] = rev;
-        __syncthreads();  // the maps are there, and this step's stage is free
-        fetch(step + kBwdStages);
+        __syncthreads();  // the maps are there, and the other stage is free
+        fetch(step + 1);
         if (warp == 0) {
             Vec<N> h = saved;
 #pragma unroll
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
                 h = apply(sm.warp[w][lane], h);
             }
             fetch_state(step + 1);
-        } else if (warp == 1) {
+        } else if (warp == 1 && live) {
             Map<N> all[kBwdWarps];  // of the tile's rows from each warp's first on, in reversed time
 #pragma unroll
             for (int w = kBwdWarps - 1; w >= 0; --w) {
@@ -457,8 +457,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
             }
             Vec<N> mu = carry;
             if (cs > 1) {
-                if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[0]);
-                sm.ex.fold(step, cs, at.rank, lane, mu, carry);
+                if (waiting) waiting = sm.ex.swap(exchanges, cs, at.rank, lane, all[0]);
+                sm.ex.fold(exchanges, cs, at.rank, lane, mu, carry);
+                ++exchanges;
             } else {
                 carry = apply(all[0], carry);
             }
@@ -466,41 +467,59 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) based_scan_bwd_kernel(const
 #pragma unroll
             for (int w = 0; w < kBwdWarps - 1; ++w) sm.mu[w][lane] = apply(all[w + 1], mu);
         }
-        cp_async_wait<kBwdStages - 1>();
-        __syncthreads();  // the starts are there, and the next step's tile
-        if (tile < 0) continue;
-        Vec<N> h = sm.start[warp][lane], mu = sm.mu[warp][lane], before[R];
+        __syncthreads();  // the starts are there
+        const int64_t first = static_cast<int64_t>(row0) * p.D, last = first + static_cast<int64_t>(R - 1) * p.D;
+        if (some) {
+            Vec<N> h = sm.start[warp][lane], mu = sm.mu[warp][lane];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            before[i] = h;
-            h = vfma(a[i], h, increment<MODE>(rest[i], unpack<T>(v[i])));
-        }
-        const int64_t last = static_cast<int64_t>(row0 + R - 1) * p.D;
-        T *to_g = dgate + last, *to_x = dx + last;
+            for (int i = 0; i < R; ++i) {
+                const Vec<N> v = unpack<T>(word(sx, i));
+                if constexpr (MODE == BASED_GATE_LOG) {
+                    other[i] = h;
+                    h = vfma(a[i], h, v);
+                } else {
+                    const Vec<N> diff = vfma(v, splat<N>(-1.0f), h);
+                    h = vfma(a[i], h, vmul(other[i], v));
+                    word(sg, i) = __float_as_uint(diff.v[0]);
+                    if (N == 2) word(sx, i) = __float_as_uint(diff.v[N - 1]);
+                }
+            }
+            T *to_g = dgate + last, *to_x = dx + last;
+            auto back = [&](auto all_live) {
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) {
-            const Vec<N> lam = vadd(unpack<T>(d[i]), mu);
-            mu = vmul(a[i], lam);
-            Vec<N> og, ox;
-            if (MODE == BASED_GATE_LOG) {
-                og = vmul(mu, before[i]), ox = lam;
-            } else {
-                og = vmul(vmul(mu, rest[i]), vadd(before[i], vneg(unpack<T>(v[i]))));
-                ox = vmul(rest[i], lam);
-            }
-            if (full && wide) {
-                *reinterpret_cast<uint32_t *>(to_g) = pack<T>(og);
-                *reinterpret_cast<uint32_t *>(to_x) = pack<T>(ox);
-            } else if (row0 + i < p.T) {
-                store_some(to_g, row0 + i < len ? og : splat<N>(0.0f), at.n);
-                store_some(to_x, row0 + i < len ? ox : splat<N>(0.0f), at.n);
-            }
-            to_g -= p.D;
-            to_x -= p.D;
+                for (int i = R - 1; i >= 0; --i) {
+                    const Vec<N> lam = vadd(unpack<T>(word(sd, i)), mu);
+                    mu = vmul(a[i], lam);
+                    Vec<N> og, ox;
+                    if constexpr (MODE == BASED_GATE_LOG) {
+                        og = vmul(mu, other[i]), ox = lam;
+                    } else {
+                        Vec<N> diff;
+                        diff.v[0] = __uint_as_float(word(sg, i));
+                        if (N == 2) diff.v[N - 1] = __uint_as_float(word(sx, i));
+                        og = vmul(vmul(mu, other[i]), diff);
+                        ox = vmul(other[i], lam);
+                    }
+                    if (decltype(all_live)::value) {
+                        *reinterpret_cast<uint32_t *>(to_g) = pack<T>(og);
+                        *reinterpret_cast<uint32_t *>(to_x) = pack<T>(ox);
+                    } else if (row0 + i < p.T) {
+                        store_some(to_g, row0 + i < len ? og : splat<N>(0.0f), at.n);
+                        store_some(to_x, row0 + i < len ? ox : splat<N>(0.0f), at.n);
+                    }
+                    to_g -= p.D;
+                    to_x -= p.D;
+                }
+            };
+            if (full && wide)
+                back(std::true_type());
+            else
+                back(std::false_type());
+        } else if (RAGGED && tile >= 0) {
+            zero_rows<R>(dgate + first, p, row0, at.n);
+            zero_rows<R>(dx + first, p, row0, at.n);
         }
     }
-    if (RAGGED) zero_rows<T, kThreads>(dgate, tiles * kTile, p, at.n, at.rank, lane, warp);
-    if (RAGGED) zero_rows<T, kThreads>(dx, tiles * kTile, p, at.n, at.rank, lane, warp);
     if (warp == 1 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
     if (cs > 1) cluster_sync();
 }
@@ -611,7 +630,7 @@ int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
     if (bwd) {
         void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_bwd_kernel<T, kLog, true> : based_scan_bwd_kernel<T, kSig, true>)
                                                 : (log ? based_scan_bwd_kernel<T, kLog, false> : based_scan_bwd_kernel<T, kSig, false>);
-        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, 2 * sms, 1.9, 5, st);
+        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, 4 * sms, 2.4, 5, st);
     }
     void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_fwd_kernel<T, kLog, true> : based_scan_fwd_kernel<T, kSig, true>)
                                             : (log ? based_scan_fwd_kernel<T, kLog, false> : based_scan_fwd_kernel<T, kSig, false>);

@@ -250,10 +250,11 @@ __device__ __forceinline__ float at_most(float x, float hi) {
 template <int N>
 __device__ __forceinline__ Vec<N> vexp(const Vec<N> &x, float sign) {
     const Vec<N> log2e = splat<N>(sign * 1.4426950408889634f);
-    const Vec<N> t = vmul(x, log2e), r = vmul(vfma(x, log2e, vneg(t)), splat<N>(0.6931471805599453f));
+    const Vec<N> t = vmul(x, splat<N>(sign * -1.4426950408889634f));  // negated
+    const Vec<N> r = vmul(vfma(x, log2e, t), splat<N>(0.6931471805599453f));
     Vec<N> e;
 #pragma unroll
-    for (int j = 0; j < N; ++j) e.v[j] = ex2(t.v[j]);
+    for (int j = 0; j < N; ++j) e.v[j] = ex2(-t.v[j]);
     return vfma(e, r, e);
 }
 // p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy. g counts as -87 below
