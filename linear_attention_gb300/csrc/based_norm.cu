@@ -135,7 +135,7 @@ __device__ __forceinline__ void activate(const Vec<2> &v, Vec<2> &f, Vec<2> &df)
         return;
     }
     Vec<2> s, t;
-    vsigmoid<false>(v, s, t);
+    vsigmoid(v, s, t);
     if (ACT == BASED_ACT_SIGMOID)
         f = s, df = vmul(s, t);
     else

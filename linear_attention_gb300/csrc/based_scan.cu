@@ -21,13 +21,15 @@ constexpr int kSave = BASED_SCAN_SAVE_ROWS;
 constexpr int kTile = kSave;       // rows of a tile: one saved state each
 constexpr int kRowBytes = 128;     // a tile's row: 64 channels of 16 bits or 32 of 32
 constexpr int kMaxCluster = 16;
+constexpr int kMaxGridY = 65535;   // batch entries along y, then z
+constexpr int kMaxD = 1 << 22;     // channels: a tile of an output spans less than 2^32 bytes
 
 struct ScanParams {
     const void *gate, *x, *dy;
     int64_t gate_sb, gate_st, x_sb, x_st, dy_sb, dy_st;
     int B, T, D, slabs;
-    int cluster;          // CTAs of a cluster
-    int word;             // bytes of a copy to shared memory that every row's start allows: 16, 4 or 2
+    int cluster, log2_cluster;  // CTAs of a cluster, a power of two
+    int word;             // bytes of a copy to shared memory that every row's start allows: 16 or 4; 0: neither
     int pair;             // two 16-bit outputs can be stored as one word
     const float *state;   // forward: h_{-1}; backward: dfinal
     const int32_t *lengths;
@@ -41,12 +43,10 @@ struct ScanParams {
 template <int MODE, int N>
 __device__ __forceinline__ void decay(Vec<N> g, Vec<N> &a, Vec<N> &rest) {
     if (MODE == BASED_GATE_LOG) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) g.v[j] = at_least(g.v[j], -120.0f);  // exp is 0 there
-        a = vexp(g, 1.0f);
+        a = vexp(g);
         rest = splat<N>(1.0f);
     } else {
-        vsigmoid<true>(g, a, rest);
+        vsigmoid(g, a, rest);
     }
 }
 template <int MODE, int N>
@@ -70,30 +70,40 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows [0, rows) of channels [0, cols) of a tensor at src into the tile at dst, by all THREADS
-// threads of the CTA. The other places keep what they held; nothing that is stored depends on it.
-template <typename T, int THREADS, int BYTES>
-__device__ __forceinline__ void copy_words(uint8_t *dst, const T *src, int64_t stride, int rows, int cols) {
-    constexpr int kPer = BYTES / static_cast<int>(sizeof(T)), kWords = kRowBytes / BYTES, kStep = THREADS / kWords;
+// Rows [0, rows) of the first `cols` bytes of rows at src, `stride` bytes apart, into the tile at dst, by
+// all THREADS threads of the CTA. The other places keep what they held; nothing that is stored depends
+// on it. src is the same for all threads and their offsets from it fit 32 bits: one addition a copy.
+template <int THREADS, int BYTES>
+__device__ __forceinline__ void copy_words(uint8_t *dst, const uint8_t *src, uint32_t stride, int rows, int cols) {
+    constexpr int kWords = kRowBytes / BYTES, kStep = THREADS / kWords;
     const int col = static_cast<int>(threadIdx.x) % kWords, row0 = static_cast<int>(threadIdx.x) / kWords;
-    if (col * kPer >= cols) return;
-    const T *from = src + row0 * stride + col * kPer;
+    if (col * BYTES >= cols) return;
+    uint32_t off = row0 * stride + col * BYTES;
     const uint32_t to = smem_u32(dst) + row0 * kRowBytes + col * BYTES;
+    if (rows == kTile) {
 #pragma unroll
-    for (int k = 0; k < kTile / kStep; ++k) {
-        if (row0 + k * kStep < rows) cp_async<BYTES>(to + k * kStep * kRowBytes, from);
-        from += kStep * stride;
+        for (int k = 0; k < kTile / kStep; ++k) {
+            cp_async<BYTES>(to + k * kStep * kRowBytes, src + off);
+            off += kStep * stride;
+        }
+    } else {
+        for (int k = 0; k < kTile / kStep && row0 + k * kStep < rows; ++k) {
+            cp_async<BYTES>(to + k * kStep * kRowBytes, src + off);
+            off += kStep * stride;
+        }
     }
 }
+// T: the element; stride in elements, cols in channels.
 template <typename T, int THREADS>
 __device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t stride, int rows, int cols, int word) {
+    constexpr int es = sizeof(T);
     if (word == 16) {
-        copy_words<T, THREADS, 16>(dst, src, stride, rows, cols);
+        copy_words<THREADS, 16>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
     } else if (word == 4) {
-        copy_words<T, THREADS, 4>(dst, src, stride, rows, cols);
+        copy_words<THREADS, 4>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
     } else {
-        // rows that start on an odd 16-bit element: no asynchronous copy is that narrow
-        constexpr int kCols = kRowBytes / sizeof(T);
+        // rows that start on an odd 16-bit element (no asynchronous copy is that narrow), or far apart
+        constexpr int kCols = kRowBytes / es;
         for (int i = threadIdx.x; i < rows * kCols; i += THREADS)
             if (i % kCols < cols) reinterpret_cast<T *>(dst)[i] = src[(i / kCols) * stride + i % kCols];
     }
@@ -215,11 +225,11 @@ struct Place {
     int lane, warp, rank, b, c0, c, n, cols, tiles, steps;
     __device__ __forceinline__ explicit Place(const ScanParams &p) {
         lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        rank = p.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
-        const int slab = static_cast<int>(blockIdx.x) / p.cluster;
-        b = slab / p.slabs, c0 = (slab % p.slabs) * 32 * N, c = c0 + lane * N;
+        rank = static_cast<int>(blockIdx.x) & (p.cluster - 1);
+        b = static_cast<int>(blockIdx.z * kMaxGridY + blockIdx.y);
+        c0 = static_cast<int>(blockIdx.x >> p.log2_cluster) * 32 * N, c = c0 + lane * N;
         n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
-        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) / p.cluster;
+        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) >> p.log2_cluster;
     }
 };
 
@@ -244,6 +254,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
+    if (at.b >= p.B) return;
     if (cs > 1) {
         if (threadIdx.x == 0) sm.ex.init();
         cluster_sync();  // every CTA's mbarriers are there before another CTA counts on them
@@ -254,7 +265,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
     const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
     const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
-    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
+    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
+    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = p.pair && at.n == N;
     Vec<N> carry;  // warp 0's: the state in front of the cluster's tiles
     load_state(p.state ? p.state + plane : nullptr, at.n, carry);
@@ -317,25 +329,26 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         }
         cp_async_wait<kFwdStages - 1>();
         __syncthreads();  // the starts are there, and the next step's tile
-        T *to = y + static_cast<int64_t>(row0) * p.D;
+        uint8_t *to = reinterpret_cast<uint8_t *>(y + static_cast<int64_t>(tile) * kTile * p.D);
+        uint32_t off = off0;
         if (full && wide) {
             Vec<N> h = sm.start[warp][lane];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
-                *reinterpret_cast<uint32_t *>(to) = pack<T>(h);
-                to += p.D;
+                *reinterpret_cast<uint32_t *>(to + off) = pack<T>(h);
+                off += off_row;
             }
         } else if (row0 < len) {
             Vec<N> h = sm.start[warp][lane];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
-                if (row0 + i < p.T) store_some(to, row0 + i < len ? h : splat<N>(0.0f), at.n);
-                to += p.D;
+                if (row0 + i < p.T) store_some(reinterpret_cast<T *>(to + off), row0 + i < len ? h : splat<N>(0.0f), at.n);
+                off += off_row;
             }
         } else if (RAGGED) {
-            zero_rows<R>(to, p, row0, at.n);
+            zero_rows<R>(reinterpret_cast<T *>(to + off0), p, row0, at.n);
         }
     }
     if (warp == 0 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
@@ -370,6 +383,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
     BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
+    if (at.b >= p.B) return;
     if (cs > 1) {
         if (threadIdx.x == 0) sm.ex.init();
         cluster_sync();
@@ -381,8 +395,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
     const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
     const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
     const T *dy = static_cast<const T *>(p.dy) + at.b * p.dy_sb + at.c0;
-    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
-    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D + at.c;
+    T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
+    T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D;
+    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = p.pair && at.n == N;
     Vec<N> carry;  // warp 1's: mu behind the cluster's tiles
     load_state(p.state ? p.state + plane : nullptr, at.n, carry);
@@ -410,7 +425,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
         const int tile = tile_of(step), row0 = tile * kTile + warp * R;
         const bool live = !RAGGED || (at.tiles - (step + 1) * cs) * kTile < len;  // some row of the cluster's tiles is no padding
         cp_async_wait<0>();
-        __syncthreads();  // the tile has landed
+        __syncthreads();  // the tile has landed, and the other stage is free
+        fetch(step + 1);
         uint8_t *sg = sm.tile[step % kBwdStages][0] + warp * R * kRowBytes + lane * 4;
         uint8_t *sx = sg + kTile * kRowBytes, *sd = sx + kTile * kRowBytes;
         auto word = [&](uint8_t *s, int i) -> uint32_t & { return *reinterpret_cast<uint32_t *>(s + i * kRowBytes); };
@@ -438,8 +454,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
             rows(std::false_type());
         sm.warp[warp][lane] = m;
         sm.rev[warp][lane] = rev;
-        __syncthreads();  // the maps are there, and the other stage is free
-        fetch(step + 1);
+        __syncthreads();  // the maps are there
         if (warp == 0) {
             Vec<N> h = saved;
 #pragma unroll
@@ -468,7 +483,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
             for (int w = 0; w < kBwdWarps - 1; ++w) sm.mu[w][lane] = apply(all[w + 1], mu);
         }
         __syncthreads();  // the starts are there
-        const int64_t first = static_cast<int64_t>(row0) * p.D, last = first + static_cast<int64_t>(R - 1) * p.D;
+        uint8_t *const to_g = reinterpret_cast<uint8_t *>(dgate + static_cast<int64_t>(tile) * kTile * p.D);
+        uint8_t *const to_x = reinterpret_cast<uint8_t *>(dx + static_cast<int64_t>(tile) * kTile * p.D);
         if (some) {
             Vec<N> h = sm.start[warp][lane], mu = sm.mu[warp][lane];
 #pragma unroll
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
                     if (N == 2) word(sx, i) = __float_as_uint(diff.v[N - 1]);
                 }
             }
-            T *to_g = dgate + last, *to_x = dx + last;
+            uint32_t off = off0 + (R - 1) * off_row;
             auto back = [&](auto all_live) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
@@ -501,14 +517,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
                         ox = vmul(other[i], lam);
                     }
                     if (decltype(all_live)::value) {
-                        *reinterpret_cast<uint32_t *>(to_g) = pack<T>(og);
-                        *reinterpret_cast<uint32_t *>(to_x) = pack<T>(ox);
+                        *reinterpret_cast<uint32_t *>(to_g + off) = pack<T>(og);
+                        *reinterpret_cast<uint32_t *>(to_x + off) = pack<T>(ox);
                     } else if (row0 + i < p.T) {
-                        store_some(to_g, row0 + i < len ? og : splat<N>(0.0f), at.n);
-                        store_some(to_x, row0 + i < len ? ox : splat<N>(0.0f), at.n);
+                        store_some(reinterpret_cast<T *>(to_g + off), row0 + i < len ? og : splat<N>(0.0f), at.n);
+                        store_some(reinterpret_cast<T *>(to_x + off), row0 + i < len ? ox : splat<N>(0.0f), at.n);
                     }
-                    to_g -= p.D;
-                    to_x -= p.D;
+                    off -= off_row;
                 }
             };
             if (full && wide)
@@ -516,8 +531,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
             else
                 back(std::false_type());
         } else if (RAGGED && tile >= 0) {
-            zero_rows<R>(dgate + first, p, row0, at.n);
-            zero_rows<R>(dx + first, p, row0, at.n);
+            zero_rows<R>(reinterpret_cast<T *>(to_g + off0), p, row0, at.n);
+            zero_rows<R>(reinterpret_cast<T *>(to_x + off0), p, row0, at.n);
         }
     }
     if (warp == 1 && at.rank == 0 && p.final_state) store_some(p.final_state + plane, carry, at.n);
@@ -569,7 +584,7 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
     if (!type_ok(dtype)) return BASED_ERR_UNSUPPORTED_TYPE;
     if (mode != BASED_GATE_LOG && mode != BASED_GATE_SIGMOID) return BASED_ERR_BAD_ARGUMENT;
     if (p.B < 1 || p.T < 1 || p.D < 1) return BASED_ERR_BAD_SIZE;
-    if (static_cast<int64_t>(p.B) * p.D >= (1ll << 30) || p.T > (1 << 30)) return BASED_ERR_BAD_SIZE;
+    if (static_cast<int64_t>(p.B) * p.D >= (1ll << 30) || p.T > (1 << 30) || p.D > kMaxD) return BASED_ERR_BAD_SIZE;
     if (p.gate_sb < 0 || p.gate_st < 0 || p.x_sb < 0 || p.x_st < 0 || p.dy_sb < 0 || p.dy_st < 0)
         return BASED_ERR_BAD_STRIDE;
     const size_t es = elem_size(dtype);
@@ -619,8 +634,10 @@ int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int64_t 
     p.slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
     const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
     p.cluster = choose_cluster(blocks, tiles, slots, step_us, static_cast<double>(tensors) * kTile * kRowBytes);
+    for (p.log2_cluster = 0; 1 << p.log2_cluster < p.cluster;) ++p.log2_cluster;
     OPS_CUDA(allow(kernel, Smem::bytes(kMaxCluster)));
-    OPS_CUDA(launch_op(kernel, dim3(static_cast<unsigned>(blocks * p.cluster)), threads, Smem::bytes(p.cluster), st, p, p.cluster));
+    const dim3 grid(static_cast<unsigned>(p.slabs) * p.cluster, p.B < kMaxGridY ? p.B : kMaxGridY, (p.B + kMaxGridY - 1) / kMaxGridY);
+    OPS_CUDA(launch_op(kernel, grid, threads, Smem::bytes(p.cluster), st, p, p.cluster));
     return BASED_OK;
 }
 template <typename T>
@@ -646,7 +663,8 @@ int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream
     const int64_t bits = (p.D | p.gate_sb | p.gate_st | p.x_sb | p.x_st | p.dy_sb | p.dy_st) * es |
                          static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.gate) | reinterpret_cast<uintptr_t>(p.x) |
                                               reinterpret_cast<uintptr_t>(p.dy));
-    p.word = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    const bool near = (p.gate_st | p.x_st | p.dy_st) < (1 << 24);  // a tile's rows within 2^32 bytes
+    p.word = !near ? 0 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
     p.pair = p.D % 2 == 0 && aligned(p.y, 4) && aligned(p.dx, 4);
     if (dtype == BASED_F32) return launch_scan<float>(p, mode, bwd, sms, st);
     if (dtype == BASED_BF16) return launch_scan<__nv_bfloat16>(p, mode, bwd, sms, st);

@@ -174,14 +174,6 @@ __device__ __forceinline__ Vec<2> vadd(const Vec<2> &a, const Vec<2> &b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
     return from_bits2(r);
 }
-template <int N>
-__device__ __forceinline__ Vec<N> vneg(const Vec<N> &a) {
-    Vec<N> r;
-#pragma unroll
-    for (int j = 0; j < N; ++j) r.v[j] = -a.v[j];
-    return r;
-}
-
 // A 32-bit word as one float32 or two 16-bit elements, the first in the low half.
 template <typename T>
 __device__ __forceinline__ Vec<4 / sizeof(T)> unpack(uint32_t w);
@@ -221,7 +213,7 @@ __device__ __forceinline__ uint32_t pack<__half>(const Vec<2> &a) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Device: exp and the logistic function, to about 2^-22 relative
+// Device: exp and the logistic function
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ float ex2(float t) {
     float r;
@@ -233,49 +225,25 @@ __device__ __forceinline__ float rcp(float d) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     return r;
 }
-// x limited to [lo, hi]; NaN stays NaN
-__device__ __forceinline__ float at_least(float x, float lo) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float at_most(float x, float hi) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(hi));
-    return r;
-}
-// e^(sign x) = 2^t (1 + r ln 2) with t = x log2(e) rounded and r what the rounding left out, which
-// for |x| of 10 is as much as 2^-21 of the result and would add up over the rows of a recurrence.
-// |x| must be below 126 ln 2 on the side that grows and 1000 on the other.
+// e^x = 2^t with t = x log2(e) rounded once: off by 2^-22 (the approximation of 2^t) and |x| 2^-24.
+// The second part is what a recurrence does not notice: where a decay e^x is near 1 and errors add
+// up over many rows, |x| is small, and where |x| is large nothing is left after a few rows.
 template <int N>
-__device__ __forceinline__ Vec<N> vexp(const Vec<N> &x, float sign) {
-    const Vec<N> log2e = splat<N>(sign * 1.4426950408889634f);
-    const Vec<N> t = vmul(x, splat<N>(sign * -1.4426950408889634f));  // negated
-    const Vec<N> r = vmul(vfma(x, log2e, t), splat<N>(0.6931471805599453f));
-    Vec<N> e;
+__device__ __forceinline__ Vec<N> vexp(const Vec<N> &x) {
+    Vec<N> t = vmul(x, splat<N>(1.4426950408889634f));
 #pragma unroll
-    for (int j = 0; j < N; ++j) e.v[j] = ex2(-t.v[j]);
-    return vfma(e, r, e);
+    for (int j = 0; j < N; ++j) t.v[j] = ex2(t.v[j]);
+    return t;
 }
-// p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy. g counts as -87 below
-// that, where p is under 2e-38, and as 104 above, where q is 0 in float32; NaN stays NaN.
-// LONG: to 2^-20.5, for values that add up over the rows of a recurrence. Otherwise exp(-g) is taken
-// without the correction of its rounded argument, good to 2^-22 + |g| 2^-24: a fifth fewer instructions for
-// values that are used once.
-template <bool LONG, int N>
+// p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy (q = e^-g p, not 1 - p). Below
+// g = -87, where p is under 2e-38, g counts as -87, so that e^-g stays finite; NaN stays NaN.
+template <int N>
 __device__ __forceinline__ void vsigmoid(Vec<N> g, Vec<N> &p, Vec<N> &q) {
-    Vec<N> e;
 #pragma unroll
-    for (int j = 0; j < N; ++j) g.v[j] = at_least(g.v[j], -87.0f);
-    if (LONG) {
+    for (int j = 0; j < N; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(g.v[j]) : "f"(g.v[j]), "f"(-87.0f));
+    Vec<N> e = vmul(g, splat<N>(-1.4426950408889634f));
 #pragma unroll
-        for (int j = 0; j < N; ++j) g.v[j] = at_most(g.v[j], 104.0f);
-        e = vexp(g, -1.0f);
-    } else {
-        e = vmul(g, splat<N>(-1.4426950408889634f));
-#pragma unroll
-        for (int j = 0; j < N; ++j) e.v[j] = ex2(e.v[j]);
-    }
+    for (int j = 0; j < N; ++j) e.v[j] = ex2(e.v[j]);
     const Vec<N> d = vadd(e, splat<N>(1.0f));
 #pragma unroll
     for (int j = 0; j < N; ++j) p.v[j] = rcp(d.v[j]);
