@@ -93,19 +93,33 @@ __device__ __forceinline__ void copy_words(uint8_t *dst, const uint8_t *src, uin
         }
     }
 }
-// T: the element; stride in elements, cols in channels.
-template <typename T, int THREADS>
+// T: the element; stride in elements, cols in channels. FAST: some word can be copied asynchronously.
+template <typename T, int THREADS, bool FAST>
 __device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t stride, int rows, int cols, int word) {
     constexpr int es = sizeof(T);
-    if (word == 16) {
+    if (FAST && word == 16) {
         copy_words<THREADS, 16>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
-    } else if (word == 4) {
+    } else if (FAST) {
         copy_words<THREADS, 4>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
     } else {
-        // rows that start on an odd 16-bit element (no asynchronous copy is that narrow), or far apart
-        constexpr int kCols = kRowBytes / es;
-        for (int i = threadIdx.x; i < rows * kCols; i += THREADS)
-            if (i % kCols < cols) reinterpret_cast<T *>(dst)[i] = src[(i / kCols) * stride + i % kCols];
+        // Rows that start on an odd 16-bit element (no asynchronous copy is that narrow), or far apart:
+        // element by element through registers, the loads of four words at a time under way together.
+        constexpr int kPer = 4 / es, kStep = THREADS / 32, kAhead = 4;
+        const int col = static_cast<int>(threadIdx.x & 31) * kPer, row0 = threadIdx.x >> 5;
+        const T *from = src + row0 * stride + col;
+#pragma unroll 1
+        for (int k = 0; k < kTile / kStep; k += kAhead) {
+            Pack<T, kPer> w[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (row0 + (k + i) * kStep < rows && col + j < cols) w[i].v[j] = from[(k + i) * (kStep * stride) + j];
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                *reinterpret_cast<Pack<T, kPer> *>(dst + (row0 + (k + i) * kStep) * kRowBytes + col * es) = w[i];
+        }
     }
 }
 
@@ -198,10 +212,11 @@ __device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
 // The rows of sequence b before its padding. The loops over the tiles run to T all the same, and steps in
 // the padding skip their work between the barriers: a bound that comes from memory makes the loop one
 // of threads that might diverge, which costs a third more time. Kernels without lengths (RAGGED
-// false) are instances of their own.
+// false) and those whose rows need the slow copy (FAST false, which take lengths or none) are
+// instances of their own, as both cost the others registers.
 template <bool RAGGED>
 __device__ __forceinline__ int sequence_length(const ScanParams &p, int b) {
-    return RAGGED ? min(max(p.lengths[b], 0), p.T) : p.T;
+    return RAGGED && p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
 // Zeros in an output's rows [row0, row0 + R).
@@ -241,13 +256,13 @@ constexpr int kFwdWarps = 4, kFwdStages = 2;
 template <int N>
 struct FwdSmem {
     uint8_t tile[kFwdStages][2][kTile * kRowBytes];
-    Map<N> warp[kFwdWarps][32];
-    Vec<N> start[kFwdWarps][32];
+    Map<N> warp[kFwdWarps][32];  // each warp's rows; then the tile's rows in front of them
+    Vec<N> start[32];            // the state in front of the tile
     Exchange<N> ex;
     static constexpr size_t bytes(int cluster) { return offsetof(FwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
 
-template <typename T, int MODE, bool RAGGED>
+template <typename T, int MODE, bool RAGGED, bool FAST>
 __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
@@ -274,8 +289,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     auto fetch = [&](int step) {
         const int row = (step * cs + at.rank) * kTile, rows = min(len - row, kTile);
         if (rows > 0) {
-            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads, FAST>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads, FAST>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
         }
         cp_async_commit();
     };
@@ -311,18 +326,20 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         if (warp == 0) {
             Vec<N> h = carry;
             if (live) {
-                Map<N> all[kFwdWarps];  // of the tile's rows up to each warp's last
+                Map<N> all = {splat<N>(1.0f), splat<N>(0.0f)};
 #pragma unroll
-                for (int w = 0; w < kFwdWarps; ++w) all[w] = w ? compose(sm.warp[w][lane], all[w - 1]) : sm.warp[w][lane];
+                for (int w = 0; w < kFwdWarps; ++w) {
+                    const Map<N> o = sm.warp[w][lane];
+                    sm.warp[w][lane] = all;
+                    all = compose(o, all);
+                }
                 if (cs > 1) {
-                    if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all[kFwdWarps - 1]);
+                    if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all);
                     sm.ex.fold(step, cs, at.rank, lane, h, carry);
                 } else {
-                    carry = apply(all[kFwdWarps - 1], carry);
+                    carry = apply(all, carry);
                 }
-                sm.start[0][lane] = h;
-#pragma unroll
-                for (int w = 1; w < kFwdWarps; ++w) sm.start[w][lane] = apply(all[w - 1], h);
+                sm.start[lane] = h;
             }
             if (p.saved && tile < at.tiles)
                 store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, h, at.n);
@@ -332,7 +349,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         uint8_t *to = reinterpret_cast<uint8_t *>(y + static_cast<int64_t>(tile) * kTile * p.D);
         uint32_t off = off0;
         if (full && wide) {
-            Vec<N> h = sm.start[warp][lane];
+            Vec<N> h = apply(sm.warp[warp][lane], sm.start[lane]);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
                 off += off_row;
             }
         } else if (row0 < len) {
-            Vec<N> h = sm.start[warp][lane];
+            Vec<N> h = apply(sm.warp[warp][lane], sm.start[lane]);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
@@ -370,13 +387,13 @@ template <int N>
 struct BwdSmem {
     uint8_t tile[kBwdStages][3][kTile * kRowBytes];
     Map<N> warp[kBwdWarps][32];
-    Vec<N> rev[kBwdWarps][32];  // the reversed map's increment
-    Vec<N> start[kBwdWarps][32], mu[kBwdWarps][32];
+    Vec<N> rev[kBwdWarps][32];   // the reversed map's increment
+    Vec<N> start[32], mu[32];    // the state in front of the tile, mu behind it
     Exchange<N> ex;
     static constexpr size_t bytes(int cluster) { return offsetof(BwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
 
-template <typename T, int MODE, bool RAGGED>
+template <typename T, int MODE, bool RAGGED, bool FAST>
 __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
@@ -408,9 +425,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
         const int row = tile_of(step) * kTile, rows = min(len - row, kTile);
         if (row >= 0 && rows > 0) {
             uint8_t(*to)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
-            copy_tile<T, kThreads>(to[0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads>(to[1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads>(to[2], dy + row * p.dy_st, p.dy_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads, FAST>(to[0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads, FAST>(to[1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
+            copy_tile<T, kThreads, FAST>(to[2], dy + row * p.dy_st, p.dy_st, rows, at.cols, p.word);
         }
         cp_async_commit();
     };
@@ -456,37 +473,34 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
         sm.rev[warp][lane] = rev;
         __syncthreads();  // the maps are there
         if (warp == 0) {
-            Vec<N> h = saved;
-#pragma unroll
-            for (int w = 0; w < kBwdWarps; ++w) {
-                sm.start[w][lane] = h;
-                h = apply(sm.warp[w][lane], h);
-            }
+            sm.start[lane] = saved;
             fetch_state(step + 1);
         } else if (warp == 1 && live) {
-            Map<N> all[kBwdWarps];  // of the tile's rows from each warp's first on, in reversed time
-#pragma unroll
-            for (int w = kBwdWarps - 1; w >= 0; --w) {
-                const Map<N> o = {sm.warp[w][lane].a, sm.rev[w][lane]};
-                all[w] = w < kBwdWarps - 1 ? compose(o, all[w + 1 < kBwdWarps ? w + 1 : w]) : o;
-            }
             Vec<N> mu = carry;
             if (cs > 1) {
-                if (waiting) waiting = sm.ex.swap(exchanges, cs, at.rank, lane, all[0]);
+                Map<N> all = {sm.warp[kBwdWarps - 1][lane].a, sm.rev[kBwdWarps - 1][lane]};  // the tile's, in reversed time
+#pragma unroll
+                for (int w = kBwdWarps - 2; w >= 0; --w) all = compose(Map<N>{sm.warp[w][lane].a, sm.rev[w][lane]}, all);
+                if (waiting) waiting = sm.ex.swap(exchanges, cs, at.rank, lane, all);
                 sm.ex.fold(exchanges, cs, at.rank, lane, mu, carry);
                 ++exchanges;
             } else {
-                carry = apply(all[0], carry);
-            }
-            sm.mu[kBwdWarps - 1][lane] = mu;
 #pragma unroll
-            for (int w = 0; w < kBwdWarps - 1; ++w) sm.mu[w][lane] = apply(all[w + 1], mu);
+                for (int w = kBwdWarps - 1; w >= 0; --w) carry = vfma(sm.warp[w][lane].a, carry, sm.rev[w][lane]);
+            }
+            sm.mu[lane] = mu;
         }
         __syncthreads();  // the starts are there
         uint8_t *const to_g = reinterpret_cast<uint8_t *>(dgate + static_cast<int64_t>(tile) * kTile * p.D);
         uint8_t *const to_x = reinterpret_cast<uint8_t *>(dx + static_cast<int64_t>(tile) * kTile * p.D);
         if (some) {
-            Vec<N> h = sm.start[warp][lane], mu = sm.mu[warp][lane];
+            // through the tile's rows in front of this warp's, and those behind it
+            Vec<N> h = sm.start[lane], mu = sm.mu[lane];
+#pragma unroll
+            for (int w = 0; w < kBwdWarps; ++w) {
+                if (w < warp) h = apply(sm.warp[w][lane], h);
+                if (kBwdWarps - 1 - w > warp) mu = vfma(sm.warp[kBwdWarps - 1 - w][lane].a, mu, sm.rev[kBwdWarps - 1 - w][lane]);
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const Vec<N> v = unpack<T>(word(sx, i));
@@ -504,6 +518,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
             auto back = [&](auto all_live) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
+                    // shared memory is read four rows ahead at most: all 16 at once spill registers, which
+                    // costs a third of the time
+                    if (i % 4 == 3) asm volatile("" ::: "memory");
                     const Vec<N> lam = vadd(unpack<T>(word(sd, i)), mu);
                     mu = vmul(a[i], lam);
                     Vec<N> og, ox;
@@ -611,8 +628,10 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
 
 // CTAs of a cluster: those whose estimated time is least. A step of a CTA takes `step_us` by its
 // own latencies, or longer where the resident CTAs' copies exceed the memory's rate; a CTA has two steps'
-// worth of start and end besides its share of the tiles. slots: CTAs that the GPU holds at once.
-int choose_cluster(int64_t blocks, int64_t tiles, int64_t slots, double step_us, double step_bytes) {
+// worth of start and end besides its share of the tiles. smem(cs): shared memory of a CTA, which
+// decides with the registers (four CTAs) how many an SM holds.
+template <typename F>
+int choose_cluster(int64_t blocks, int64_t tiles, int sms, F smem, double step_us, double step_bytes) {
     auto step = [&](int64_t resident) {
         const double us = resident * step_bytes / 6.4e6;  // bytes per us that the memory gives a kernel
         return us > step_us ? us : step_us;
@@ -620,6 +639,7 @@ int choose_cluster(int64_t blocks, int64_t tiles, int64_t slots, double step_us,
     int best = 1;
     double least = 0.0;
     for (int cs = 1; cs <= kMaxCluster && (cs == 1 || cs / 2 < tiles); cs *= 2) {
+        const int64_t per_sm = 228 * 1024 / (static_cast<int64_t>(smem(cs)) + 1024), slots = sms * (per_sm < 4 ? per_sm : 4);
         const int64_t n = blocks * cs, waves = n / slots, rest = n % slots;
         const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots) + (rest ? step(rest) : 0.0));
         // a larger cluster for a clear gain alone: its exchange costs what the estimate leaves out
@@ -629,29 +649,40 @@ int choose_cluster(int64_t blocks, int64_t tiles, int64_t slots, double step_us,
 }
 
 template <typename T, typename Smem>
-int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int64_t slots, double step_us, int tensors,
+int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms, double step_us, int tensors,
                 cudaStream_t st) {
     p.slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
     const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
-    p.cluster = choose_cluster(blocks, tiles, slots, step_us, static_cast<double>(tensors) * kTile * kRowBytes);
+    p.cluster = choose_cluster(blocks, tiles, sms, Smem::bytes, step_us, static_cast<double>(tensors) * kTile * kRowBytes);
     for (p.log2_cluster = 0; 1 << p.log2_cluster < p.cluster;) ++p.log2_cluster;
-    OPS_CUDA(allow(kernel, Smem::bytes(kMaxCluster)));
+    // CTAs that are all resident at once spread evenly where no SM can take more than its share: each asks for
+    // that share of the shared memory (8 x 3000 x 1536 backward: 84 us with up to four on an SM, 69 us with three)
+    constexpr int64_t kMost = 227 * 1024;
+    // One more with clusters of 16, which have to find their SMs within a part of the GPU.
+    const int64_t per_sm = (blocks * p.cluster + sms - 1) / sms + (p.cluster == kMaxCluster ? 1 : 0), share = per_sm < 4 ? 228 * 1024 / per_sm - 1024 : 0;
+    size_t smem = Smem::bytes(p.cluster);
+    if (share > static_cast<int64_t>(smem)) smem = static_cast<size_t>(share < kMost ? share : kMost);
+    OPS_CUDA(allow(kernel, kMost));
     const dim3 grid(static_cast<unsigned>(p.slabs) * p.cluster, p.B < kMaxGridY ? p.B : kMaxGridY, (p.B + kMaxGridY - 1) / kMaxGridY);
-    OPS_CUDA(launch_op(kernel, grid, threads, Smem::bytes(p.cluster), st, p, p.cluster));
+    OPS_CUDA(launch_op(kernel, grid, threads, smem, st, p, p.cluster));
     return BASED_OK;
 }
 template <typename T>
 int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
-    const bool log = mode == BASED_GATE_LOG;
     constexpr int kLog = BASED_GATE_LOG, kSig = BASED_GATE_SIGMOID;
+    const bool log = mode == BASED_GATE_LOG, fast = p.word != 0, ragged = p.lengths;
     if (bwd) {
-        void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_bwd_kernel<T, kLog, true> : based_scan_bwd_kernel<T, kSig, true>)
-                                                : (log ? based_scan_bwd_kernel<T, kLog, false> : based_scan_bwd_kernel<T, kSig, false>);
-        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, 4 * sms, 2.4, 5, st);
+        void (*const k)(ScanParams) =
+            !fast    ? (log ? based_scan_bwd_kernel<T, kLog, true, false> : based_scan_bwd_kernel<T, kSig, true, false>)
+            : ragged ? (log ? based_scan_bwd_kernel<T, kLog, true, true> : based_scan_bwd_kernel<T, kSig, true, true>)
+                     : (log ? based_scan_bwd_kernel<T, kLog, false, true> : based_scan_bwd_kernel<T, kSig, false, true>);
+        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, sms, 2.4, 5, st);
     }
-    void (*const k)(ScanParams) = p.lengths ? (log ? based_scan_fwd_kernel<T, kLog, true> : based_scan_fwd_kernel<T, kSig, true>)
-                                            : (log ? based_scan_fwd_kernel<T, kLog, false> : based_scan_fwd_kernel<T, kSig, false>);
-    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, 4 * sms, 1.7, 3, st);
+    void (*const k)(ScanParams) =
+        !fast    ? (log ? based_scan_fwd_kernel<T, kLog, true, false> : based_scan_fwd_kernel<T, kSig, true, false>)
+        : ragged ? (log ? based_scan_fwd_kernel<T, kLog, true, true> : based_scan_fwd_kernel<T, kSig, true, true>)
+                 : (log ? based_scan_fwd_kernel<T, kLog, false, true> : based_scan_fwd_kernel<T, kSig, false, true>);
+    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, sms, 1.7, 3, st);
 }
 
 int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream) {

@@ -269,3 +269,22 @@ def test_offsets_past_32_bits(cuda_device):
     assert (final.double() - limit.to(final.device)).abs().max() <= allowed
     assert (y[0, -1].double() - limit.to(final.device)).abs().max() <= allowed + ref.half_step(BF16) * float(limit)
     assert torch.equal(y[0, -1], y[0, 1 << 20]) and torch.equal(y[0, (1 << 24) + 3], y[0, -1])
+
+
+def test_rows_far_apart(cuda_device):
+    # rows 2^24 elements apart: a tile's rows span more than 2^32 bytes
+    D, T, far = 40, 130, 1 << 24
+    for dtype in (BF16, F32):
+        g, x, dy, state, dfinal = draw(1, T, D, "sigmoid", dtype, 16)
+        buf = torch.zeros((T - 1) * far + D, dtype=dtype, device="cuda")
+        wide = buf.as_strided((1, T, D), (T * far, far, 1))
+        wide.copy_(x)
+        check(g, wide, dy, state, dfinal, "sigmoid", what="far rows")
+        del buf, wide
+
+
+def test_many_batch_entries(cuda_device):
+    # more than one axis of the grid takes
+    B, T, D = 65535 + 70, 2, 3
+    g, x, dy, state, dfinal = draw(B, T, D, "log", BF16, 17)
+    check(g, x, dy, state, dfinal, "log", what="many")
