@@ -1,0 +1,129 @@
+"""The operators together: the differentiable functions against torch's autograd in 64 bits, and the
+example's language model in training and generation."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from linear_attention_gb300.autograd import embedding, gated_scan, group_norm
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def example():
+    spec = importlib.util.spec_from_file_location("language_model", os.path.join(ROOT, "examples", "language_model.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def plain(ids, table, wg, wx, wz, state, weight, bias, lengths, groups):
+    """One layer in plain torch: embedding, three projections, recurrence, gated group norm."""
+    x = torch.where((ids >= 0)[..., None], table[ids.clamp(min=0)] * 3.0, 0.0)
+    g, v, z = x @ wg, x @ wx, x @ wz
+    a = torch.sigmoid(g)
+    h, hs = state, []
+    for t in range(ids.shape[1]):
+        live = (t < lengths)[:, None]
+        h = torch.where(live, a[:, t] * h + (1 - a[:, t]) * v[:, t], h)
+        hs.append(torch.where(live, h, 0.0))
+    y = torch.stack(hs, 1)
+    n = y.unflatten(-1, (groups, -1))
+    n = (n - n.mean(-1, keepdim=True)) / torch.sqrt(n.var(-1, unbiased=False, keepdim=True) + 1e-5)
+    return (n.flatten(-2) * weight + bias) * torch.nn.functional.silu(z), h
+
+
+def test_gradients_through_a_layer(cuda_device):
+    gen = torch.Generator().manual_seed(1)
+    B, T, D, V, groups = 3, 70, 48, 20, 3
+    rand = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    ids = torch.randint(0, V, (B, T), generator=gen)
+    lengths = torch.tensor([70, 33, 64])
+    ids[torch.arange(T)[None] >= lengths[:, None]] = -1
+    leaves = [rand(V, D), rand(D, D) / 7, rand(D, D) / 7, rand(D, D) / 7, rand(B, D), 1 + 0.1 * rand(D), 0.1 * rand(D)]
+    cot, cot_state = rand(B, T, D), rand(B, D)
+    ref = [t.clone().requires_grad_() for t in leaves]
+    y, h = plain(ids, *ref, lengths, groups)
+    ((y * cot).sum() + (h * cot_state).sum()).backward()
+    mine = [t.float().cuda().requires_grad_() for t in leaves]
+    table, wg, wx, wz, state, weight, bias = mine
+    x = embedding(ids.cuda(), table, 3.0)
+    s, final = gated_scan(x @ wg, x @ wx, state=state, lengths=lengths.to(torch.int32).cuda())
+    out = group_norm(s, groups, weight, bias, x @ wz)
+    ((out * cot.float().cuda()).sum() + (final * cot_state.float().cuda()).sum()).backward()
+    # float32 against float64 through some 70 dependent rows and two products of 48 terms: a few
+    # hundred roundings of 2^-24, relative to the largest gradient
+    for name, p, q in zip("table wg wx wz state weight bias".split(), mine, ref):
+        scale = q.grad.abs().max()
+        assert (p.grad.cpu().double() - q.grad).abs().max() <= 2e-4 * scale, name
+    assert (out.detach().cpu().double() - y.detach()).abs().max() <= 1e-4 * y.abs().max()
+
+
+def test_gradients_that_are_broadcast_or_absent(cuda_device):
+    g, x = (torch.randn(2, 30, 16, device="cuda", requires_grad=True) for _ in range(2))
+    y, final = gated_scan(g, x)
+    y.sum().backward()  # a gradient of stride 0 in every axis
+    by_sum = (g.grad.clone(), x.grad.clone())
+    g.grad = x.grad = None
+    y, final = gated_scan(g, x)
+    (y * torch.ones_like(y)).sum().backward()
+    assert torch.equal(by_sum[0], g.grad) and torch.equal(by_sum[1], x.grad)
+    g.grad = x.grad = None
+    y, final = gated_scan(g, x)
+    final.sum().backward()  # no gradient of y at all
+    assert torch.isfinite(g.grad).all() and (x.grad.abs().sum() > 0)
+    # a gate shared by all batch entries: autograd sums its gradient
+    one = torch.randn(1, 30, 16, device="cuda", requires_grad=True)
+    y, _ = gated_scan(one.expand(2, 30, 16), x.detach())
+    y.sum().backward()
+    assert one.grad.shape == (1, 30, 16)
+    w = torch.ones(16, device="cuda", requires_grad=True)
+    n = group_norm(x, 2, w, act="silu")
+    n.transpose(0, 1).sum().backward()
+    assert torch.isfinite(w.grad).all()
+    table = torch.randn(9, 16, device="cuda", requires_grad=True)
+    embedding(torch.tensor([[1, 2], [2, -1]], device="cuda"), table).sum().backward()
+    assert table.grad[2].eq(2).all() and table.grad[1].eq(1).all() and table.grad[0].eq(0).all()
+
+
+def test_nothing_is_kept_without_gradients(cuda_device):
+    g, x = (torch.randn(1, 20, 16, device="cuda") for _ in range(2))
+    y, final = gated_scan(g, x)
+    assert not y.requires_grad and not final.requires_grad
+
+
+def test_model_learns_and_generates(cuda_device):
+    m = example()
+    torch.manual_seed(0)
+    gen = torch.Generator().manual_seed(0)
+    model = m.Model()
+    losses = m.train(model, 60, gen)
+    assert losses[0] > 5.0 and sum(losses[-5:]) / 5 < 1.0, losses
+    # generation step by step is the greedy continuation that whole passes give
+    ids, lengths = m.batch(model.vocab, 5, 40, gen)
+    got = model.generate(ids, lengths, 8)
+    agree = 0
+    for b in range(5):
+        n = int(lengths[b])
+        text = torch.cat([ids[b, :n].long(), got[b]]).to(torch.int32)[None]
+        logits, _ = model.prefill(text, None)
+        agree += int((logits[0, n - 1:-1].argmax(-1) == got[b]).sum())
+    assert agree >= 38  # of 40: a bf16 rounding may tip a near tie
+
+
+def test_based_layers_score(cuda_device):
+    m = example()
+    torch.manual_seed(0)
+    model = m.Model(kinds=("based", "recurrence"))
+    ids, lengths = m.batch(model.vocab, 3, 70, torch.Generator().manual_seed(2))
+    logits, states = model.prefill(ids, lengths)
+    assert logits.shape == (3, 70, 512) and torch.isfinite(logits).all() and states[0] is None
+    # causal: later tokens change nothing before them
+    other = ids.clone()
+    other[:, 50:] = (other[:, 50:] + 1) % model.vocab
+    again, _ = model.prefill(other, lengths)
+    keep = int(min(50, int(lengths.min())))
+    assert torch.equal(logits[:, :keep], again[:, :keep])
