@@ -7,7 +7,8 @@
 // launch write the zeros of the gradient. The sorted order is cut into tiles, a CTA sums the runs of
 // equal ids in its tile, and runs that cross tiles are joined from float32 partial sums. The order
 // of every sum follows from the ids alone, so that results repeat bit for bit, and a token that
-// occurs thousands of times is spread over many CTAs.
+// occurs thousands of times is spread over many CTAs. A few tokens (up to 1024) take two launches:
+// each finds its place by counting the smaller ones, and a CTA sums a whole run.
 #include "ops_common.cuh"
 
 namespace based {
@@ -18,6 +19,7 @@ constexpr int kSortCluster = 8;
 constexpr int kSortRounds = 8;                             // keys that a thread holds, at most
 constexpr int kSortChunk = kSortThreads * kSortRounds;
 constexpr int kMaxBits = 9;                                // of a digit
+constexpr int kFewTokens = 1024, kFewVocab = 1 << 22;      // tokens that are ranked directly (ids of 22 bits)
 constexpr int kTileRows = 32;                              // sorted positions of a tile, at most
 
 struct EmbedParams {
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(256) based_embed_fwd_kernel(const EmbedParams 
 struct SortParams {
     const void *ids;
     int32_t *key0, *key1, *pos0, *pos1;  // pass i writes lists i & 1; the first reads ids
-    int N, V, ids64, passes, bits;
+    int N, V, ids64, few, passes, bits;
     void *out;                 // the gradient: `words` 16-byte words, then bytes up to `bytes`
     int64_t words, bytes;
 };
@@ -175,6 +177,31 @@ struct SortChunk {
     }
 };
 
+// Few tokens: a token's place is the number of smaller (id, position) pairs, and every pair fits one
+// word. Each CTA of the first cluster places an eighth of the tokens, 512 / (N / 8) threads a token.
+// 512 tokens: 2 us where two passes of the counting sort take 5.
+__device__ __forceinline__ void rank_few(const SortParams &p, uint32_t *all) {
+    const int tid = threadIdx.x, n4 = (p.N + 3) / 4;
+    for (int i = tid; i < n4 * 4; i += kSortThreads)
+        all[i] = i < p.N ? static_cast<uint32_t>(load_id(p.ids, p.ids64, i, p.V)) << 10 | i : ~0u;
+    __syncthreads();
+    const int per = (p.N + kSortCluster - 1) / kSortCluster;  // tokens of a CTA: at most 128
+    const int split = per <= 16 ? 32 : per <= 32 ? 16 : per <= 64 ? 8 : 4, part = tid % split, mine = tid / split;
+    const int i = static_cast<int>(blockIdx.x) * per + mine;
+    const bool on = mine < per && i < p.N;
+    const uint32_t me = on ? all[i] : 0;
+    int rank = 0;
+    for (int j = part; j < n4; j += split) {
+        const uint4 q = reinterpret_cast<const uint4 *>(all)[j];
+        rank += (q.x < me) + (q.y < me) + (q.z < me) + (q.w < me);
+    }
+    for (int d = split >> 1; d > 0; d >>= 1) rank += __shfl_xor_sync(~0u, rank, d);
+    if (on && part == 0) {
+        p.key0[rank] = static_cast<int>(me >> 10);
+        p.pos0[rank] = i;
+    }
+}
+
 // The first cluster sorts: each of its CTAs takes an eighth of the keys. Per pass and CTA: count the
 // digits; read the other CTAs' counts through distributed shared memory; move each key behind those
 // of smaller digits, then those of the same digit in earlier CTAs, warps, rounds and lanes. On one
@@ -203,6 +230,10 @@ __global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const
         }
         // the rest, or all of a table that starts off a 16-byte boundary, in the 2 bytes of the smallest type
         for (int64_t i = p.words * 8 + at; i < p.bytes / 2; i += step) static_cast<uint16_t *>(p.out)[i] = 0;
+        return;
+    }
+    if (p.few) {
+        rank_few(p, reinterpret_cast<uint32_t *>(raw));
         return;
     }
     const int rank = static_cast<int>(cluster_rank()), digits = 1 << p.bits;
@@ -369,6 +400,58 @@ __global__ void __launch_bounds__(256) based_embed_sum_kernel(const SumParams p)
     }
 }
 
+// Few tokens: the CTA of the sorted position where a run begins sums all of it. blockDim.x threads
+// along the columns, N channels each; blockDim.y share the rows.
+constexpr int kRunLanes = 8;
+template <typename T, typename G, int N>
+__global__ void __launch_bounds__(32 * kRunLanes) based_embed_run_kernel(const SumParams p) {
+    constexpr int kPer = sizeof(T) * N > 16 ? 16 / sizeof(T) : N, kWords = N / kPer, kAhead = 4;
+    using W = Pack<T, kPer>;
+    __shared__ float red[kRunLanes][N][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int first = blockIdx.x, lane = threadIdx.x, row = threadIdx.y, c = (blockIdx.y * 32 + lane) * N;
+    const int k = p.key[first];
+    if (k >= p.V || (first > 0 && p.key[first - 1] == k)) return;
+    int last = first;  // 32 positions at a time
+    for (unsigned same = ~0u; same == ~0u;) {
+        const int at = last + 1 + lane;
+        same = __ballot_sync(~0u, at < p.N && p.key[at < p.N ? at : 0] == k);
+        last += same == ~0u ? 32 : __ffs(~same) - 1;
+    }
+    float acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    const T *dy = static_cast<const T *>(p.dy) + (c < p.D ? c : 0);
+    for (int i0 = first + row; i0 <= last; i0 += kAhead * kRunLanes) {
+        W w[kAhead][kWords];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const T *src = dy + p.pos[min(i0 + a * kRunLanes, last)] * p.dy_sr;
+#pragma unroll
+            for (int q = 0; q < kWords; ++q) w[a][q] = *reinterpret_cast<const W *>(src + q * kPer);
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += i0 + a * kRunLanes <= last ? to_f32(w[a][j / kPer].v[j % kPer]) : 0.0f;
+        }
+    }
+    if (last > first) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) red[row][j][lane] = acc[j];
+        __syncthreads();
+        if (row == 0) {
+#pragma unroll
+            for (int r = 1; r < kRunLanes; ++r) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += red[r][j][lane];
+            }
+        }
+    }
+    if (row == 0 && c < p.D) store_row<G, N>(p, k, c, acc);
+}
+
 // Joins each run that crosses tiles: a warp looks at one tile and 32 N columns, and sums the run that begins
 // there and goes on after it; the CTA's warps share a run of more than kJoinAlone tiles.
 constexpr int kJoinWarps = 8, kJoinAlone = 8;
@@ -436,36 +519,42 @@ __global__ void __launch_bounds__(32 * kJoinWarps) based_embed_join_kernel(const
 
 // Where the parts of based_embed_bwd's workspace lie.
 struct EmbedPlan {
-    int passes, bits, rows, tiles;
+    int few, passes, bits, rows, tiles;
     size_t list, partial, bytes;  // two lists of keys, two of positions, the partial sums
 };
 bool embed_plan(int64_t N, int V, int D, EmbedPlan &e) {
     if (N < 1 || V < 1 || D < 1 || N >= (1ll << 30)) return false;
     int bits = 1;
     while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;  // V itself is the key of padding
-    e.passes = (bits + kMaxBits - 1) / kMaxBits;
+    e.few = N <= kFewTokens && V < kFewVocab;
+    e.passes = e.few ? 1 : (bits + kMaxBits - 1) / kMaxBits;
     e.bits = (bits + e.passes - 1) / e.passes;
     // few tokens: short tiles, so that more CTAs share them
     e.rows = N >= 4096 ? kTileRows : 8;
     e.tiles = static_cast<int>((N + e.rows - 1) / e.rows);
     e.list = (static_cast<size_t>(N) * 4 + 255) & ~static_cast<size_t>(255);
     e.partial = 4 * e.list;
-    e.bytes = e.partial + static_cast<size_t>(e.tiles) * 2 * D * 4;
+    e.bytes = e.partial + (e.few ? 0 : static_cast<size_t>(e.tiles) * 2 * D * 4);
     return true;
 }
 
 template <typename T, typename G, int N>
-int launch_sums(const SumParams &p, int tiles, cudaStream_t st) {
+int launch_sums(const SumParams &p, const EmbedPlan &e, cudaStream_t st) {
     const int need = (p.D + N - 1) / N, threads = need >= 256 ? 256 : (need + 31) / 32 * 32;
-    const dim3 grid(tiles, (need + threads - 1) / threads);
-    OPS_CUDA(launch_op(based_embed_sum_kernel<T, G, N>, grid, threads, 0, st, p));
-    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, dim3((tiles + kJoinWarps - 1) / kJoinWarps, (need + 31) / 32), 32 * kJoinWarps, 0, st, p));
+    const unsigned tiles = static_cast<unsigned>(e.tiles);
+    if (e.few) {
+        OPS_CUDA(launch_op(based_embed_run_kernel<T, G, N>, dim3(p.N, (need + 31) / 32), dim3(32, kRunLanes), 0, st, p));
+        return BASED_OK;
+    }
+    OPS_CUDA(launch_op(based_embed_sum_kernel<T, G, N>, dim3(tiles, (need + threads - 1) / threads), threads, 0, st, p));
+    OPS_CUDA(launch_op(based_embed_join_kernel<G, N>, dim3((tiles + kJoinWarps - 1) / kJoinWarps, (need + 31) / 32),
+                       32 * kJoinWarps, 0, st, p));
     return BASED_OK;
 }
 template <typename T>
-int launch_sums(const SumParams &p, int g_dtype, bool wide, int tiles, cudaStream_t st) {
-    if (g_dtype == BASED_F32) return wide ? launch_sums<T, float, 8>(p, tiles, st) : launch_sums<T, float, 1>(p, tiles, st);
-    return wide ? launch_sums<T, T, 8>(p, tiles, st) : launch_sums<T, T, 1>(p, tiles, st);
+int launch_sums(const SumParams &p, int g_dtype, bool wide, const EmbedPlan &e, cudaStream_t st) {
+    if (g_dtype == BASED_F32) return wide ? launch_sums<T, float, 8>(p, e, st) : launch_sums<T, float, 1>(p, e, st);
+    return wide ? launch_sums<T, T, 8>(p, e, st) : launch_sums<T, T, 1>(p, e, st);
 }
 
 template <typename T, int N>
@@ -474,16 +563,7 @@ int launch_embed(const EmbedParams &p, int sms, cudaStream_t st) {
     while (tx < 256 && tx * N < p.D) tx *= 2;
     const int ty = 256 / tx;
     const int64_t need = (p.N + ty - 1) / ty, most = sms * 8ll;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(need < most ? need : most));
-    cfg.blockDim = dim3(tx, ty);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    OPS_CUDA(cudaLaunchKernelEx(&cfg, based_embed_fwd_kernel<T, N>, p));
+    OPS_CUDA(launch_op(based_embed_fwd_kernel<T, N>, dim3(static_cast<unsigned>(need < most ? need : most)), dim3(tx, ty), 0, st, p));
     return BASED_OK;
 }
 
@@ -544,8 +624,8 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     int32_t *lists[4];
     for (int i = 0; i < 4; ++i) lists[i] = reinterpret_cast<int32_t *>(ws + i * e.list);
     const int64_t out_bytes = static_cast<int64_t>(V) * D * gs;
-    const SortParams s = {ids, lists[0], lists[1], lists[2], lists[3], static_cast<int>(N), V, ids64 ? 1 : 0, e.passes,
-                          e.bits, dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
+    const SortParams s = {ids, lists[0], lists[1], lists[2], lists[3], static_cast<int>(N), V, ids64 ? 1 : 0, e.few,
+                          e.passes, e.bits, dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
     // one cluster sorts; enough others write the zeros: the rest of the GPU, or 16 words a thread
     int64_t fill = (out_bytes / 16 + kSortCluster * kSortThreads * 16 - 1) / (kSortCluster * kSortThreads * 16);
     // no more clusters than are resident at once (a cluster's CTAs share a part of the GPU, which leaves some SMs over)
@@ -558,9 +638,9 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     const SumParams p = {lists[done], lists[2 + done], dy, dy_sr, static_cast<int>(N), V, D, e.rows, scale,
                          reinterpret_cast<float *>(ws + e.partial), dtable};
     const bool wide = D % 8 == 0 && aligned(dy, 16) && dy_sr * es % 16 == 0 && aligned(dtable, 16);
-    if (dtype == BASED_F32) return launch_sums<float>(p, g_dtype, wide, e.tiles, st);
-    if (dtype == BASED_BF16) return launch_sums<__nv_bfloat16>(p, g_dtype, wide, e.tiles, st);
-    return launch_sums<__half>(p, g_dtype, wide, e.tiles, st);
+    if (dtype == BASED_F32) return launch_sums<float>(p, g_dtype, wide, e, st);
+    if (dtype == BASED_BF16) return launch_sums<__nv_bfloat16>(p, g_dtype, wide, e, st);
+    return launch_sums<__half>(p, g_dtype, wide, e, st);
 }
 
 }  // extern "C"

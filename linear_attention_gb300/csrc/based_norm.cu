@@ -154,10 +154,11 @@ __device__ __forceinline__ void with_act(int act, F f) {
 }
 
 // Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
-// and dbias, 80: weight and bias wait in shared memory, four 16-byte reads a row. BIG ones may have
-// 512 threads.
+// and dbias, 80 (100 where x is float32): weight and bias wait in shared memory, four 16-byte reads a row. Channel by channel
+// (VEC false) they take 85 and 128. BIG ones may have 512 threads.
 template <typename TX, typename TY, bool VEC, bool GATED, bool BWD, bool BIG>
-__global__ void __launch_bounds__(BIG ? 512 : BWD ? 128 : 256, BIG ? 1 : BWD ? 6 : 4) based_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : VEC ? (BWD ? (sizeof(TX) == 4 ? 5 : 6) : 4) : (BWD ? 2 : 3))
+    based_norm_kernel(const NormParams p) {
     constexpr int P = kElems / 2;
     extern __shared__ float smem[];
     const int slot = threadIdx.x / p.tpg, l = threadIdx.x % p.tpg;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) based_norm_sum_kernel(const No
 struct NormShape {
     int tpg, gpb, rp, threads, grid_x, grid_y;
 };
-NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd) {
+NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd, bool vec, bool x32) {
     NormShape s;
     const int per = (C / G + kElems - 1) / kElems;
     for (s.tpg = 1; s.tpg < per;) s.tpg *= 2;
@@ -372,14 +373,14 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd) {
         s.threads = s.tpg;
     } else {
         // columns in blocks of about equal width, rows side by side where one block is narrow
-        const int limit = bwd ? 128 : 256, blocks = (G * s.tpg + limit - 1) / limit;
+        const int limit = bwd && vec ? 128 : 256, blocks = (G * s.tpg + limit - 1) / limit;
         s.gpb = (G + blocks - 1) / blocks;
         s.rp = limit / (s.gpb * s.tpg);
         s.threads = (s.gpb * s.rp * s.tpg + 31) / 32 * 32;
     }
     s.grid_y = (G + s.gpb - 1) / s.gpb;
     // as many CTAs as are resident at once, in whole turns over the column blocks
-    const int resident = sms * ((bwd ? 768 : 1024) / s.threads);
+    const int held = vec ? (bwd ? (x32 ? 640 : 768) : 1024) : (bwd ? 512 : 768), resident = sms * (held / s.threads > 1 ? held / s.threads : 1);
     const int64_t turns = (R + s.rp - 1) / s.rp, most = resident / s.grid_y > 1 ? resident / s.grid_y : 1;
     s.grid_x = static_cast<int>(turns < most ? turns : most);
     return s;
@@ -420,18 +421,15 @@ int check_norm(const NormParams &p, int x_dtype, int dtype, bool bwd, const void
 }
 
 template <typename TX, typename TY, bool BWD>
-int launch_norm(const NormParams &p, const NormShape &s, cudaStream_t st) {
-    const size_t xs = sizeof(TX), es = sizeof(TY);
-    auto wide = [](const void *q, int64_t sr, size_t e) { return aligned(q, 16) && sr * e % 16 == 0; };
-    // 16-byte words where every group of every row starts on one
-    const bool vec = p.Cg % kElems == 0 && wide(p.x, p.x_sr, xs) && wide(p.gate, p.gate_sr, es) &&
-                     wide(p.dy, p.dy_sr, es) && aligned(p.y, 16) && aligned(p.dx, 16) && aligned(p.dgate, 16);
+int launch_norm(const NormParams &p, const NormShape &s, bool vec, cudaStream_t st) {
     const dim3 grid(s.grid_x, s.grid_y);
     // the sums' 64 floats, weight and bias, and where rows lie side by side their dweight and dbias
     const size_t smem = (64 + (BWD && s.rp > 1 ? 4 : 2) * kElems * s.gpb * s.tpg) * sizeof(float);
     void (*kernel)(NormParams);
-    if (!vec)
+    if (!vec && s.tpg > 32)
         kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, true> : based_norm_kernel<TX, TY, false, false, BWD, true>;
+    else if (!vec)
+        kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, false> : based_norm_kernel<TX, TY, false, false, BWD, false>;
     else if (s.tpg > 32)
         kernel = p.gate ? based_norm_kernel<TX, TY, true, true, BWD, true> : based_norm_kernel<TX, TY, true, false, BWD, true>;
     else
@@ -441,15 +439,15 @@ int launch_norm(const NormParams &p, const NormShape &s, cudaStream_t st) {
 }
 
 template <bool BWD>
-int dispatch_norm(const NormParams &p, const NormShape &s, int x_dtype, int dtype, cudaStream_t st) {
+int dispatch_norm(const NormParams &p, const NormShape &s, bool vec, int x_dtype, int dtype, cudaStream_t st) {
     using bf = __nv_bfloat16;
     if (x_dtype == BASED_F32) {
-        if (dtype == BASED_F32) return launch_norm<float, float, BWD>(p, s, st);
-        if (dtype == BASED_BF16) return launch_norm<float, bf, BWD>(p, s, st);
-        return launch_norm<float, __half, BWD>(p, s, st);
+        if (dtype == BASED_F32) return launch_norm<float, float, BWD>(p, s, vec, st);
+        if (dtype == BASED_BF16) return launch_norm<float, bf, BWD>(p, s, vec, st);
+        return launch_norm<float, __half, BWD>(p, s, vec, st);
     }
-    if (dtype == BASED_BF16) return launch_norm<bf, bf, BWD>(p, s, st);
-    return launch_norm<__half, __half, BWD>(p, s, st);
+    if (dtype == BASED_BF16) return launch_norm<bf, bf, BWD>(p, s, vec, st);
+    return launch_norm<__half, __half, BWD>(p, s, vec, st);
 }
 
 NormParams norm_params(const void *x, int64_t x_sr, const void *gate, int64_t gate_sr, const void *weight,
@@ -459,6 +457,14 @@ NormParams norm_params(const void *x, int64_t x_sr, const void *gate, int64_t ga
     p.weight = weight, p.bias = bias, p.p_dtype = p_dtype;
     p.R = R, p.C = C, p.G = G, p.eps = eps, p.act = act;
     return p;
+}
+
+// 16-byte words where every group of every row starts on one
+bool vector_rows(const NormParams &p, int x_dtype, int dtype) {
+    auto wide = [](const void *q, int64_t sr, size_t e) { return aligned(q, 16) && sr * e % 16 == 0; };
+    const size_t xs = elem_size(x_dtype), es = elem_size(dtype);
+    return p.C / p.G % kElems == 0 && wide(p.x, p.x_sr, xs) && wide(p.gate, p.gate_sr, es) && wide(p.dy, p.dy_sr, es) &&
+           aligned(p.y, 16) && aligned(p.dx, 16) && aligned(p.dgate, 16);
 }
 
 void place(NormParams &p, const NormShape &s) {
@@ -479,16 +485,23 @@ int based_norm_fwd(const void *x, int64_t x_sr, int x_dtype, const void *gate, i
     p.y = y;
     int sms, rc = check_norm(p, x_dtype, dtype, false, nullptr, nullptr);
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
-    const NormShape s = norm_shape(R, C, G, sms, false);
+    const bool vec = vector_rows(p, x_dtype, dtype);
+    const NormShape s = norm_shape(R, C, G, sms, false, vec, x_dtype == BASED_F32);
     place(p, s);
-    return dispatch_norm<false>(p, s, x_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
+    return dispatch_norm<false>(p, s, vec, x_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t based_norm_bwd_workspace_size(int64_t R, int C, int G) {
     int sms;
     if (R < 1 || C < 1 || G < 1 || C % G != 0 || C / G > based::kMaxGroup || based::host_device(&sms) != BASED_OK)
         return 0;
-    return static_cast<size_t>(based::norm_shape(R, C, G, sms, true).grid_x) * 2 * C * sizeof(float);
+    // the most that any alignment and type takes
+    int parts = 0;
+    for (int k = 0; k < 4; ++k) {
+        const int n = based::norm_shape(R, C, G, sms, true, k & 1, k & 2).grid_x;
+        parts = n > parts ? n : parts;
+    }
+    return static_cast<size_t>(parts) * 2 * C * sizeof(float);
 }
 
 int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, int x_dtype, const void *gate,
@@ -500,7 +513,8 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
     p.dy = dy, p.dy_sr = dy_sr, p.dx = dx, p.dgate = dgate;
     int sms, rc = check_norm(p, x_dtype, dtype, true, dweight, dbias);
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
-    const NormShape s = norm_shape(R, C, G, sms, true);
+    const bool vec = vector_rows(p, x_dtype, dtype);
+    const NormShape s = norm_shape(R, C, G, sms, true, vec, x_dtype == BASED_F32);
     place(p, s);
     const bool sums = dweight || dbias;
     if (sums) {
@@ -509,7 +523,7 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
         p.partial = static_cast<float *>(workspace);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((rc = dispatch_norm<true>(p, s, x_dtype, dtype, st)) != BASED_OK || !sums) return rc;
+    if ((rc = dispatch_norm<true>(p, s, vec, x_dtype, dtype, st)) != BASED_OK || !sums) return rc;
     const NormSumParams q = {p.partial, s.grid_x, C, p_dtype, dweight, dbias};
     OPS_CUDA(launch_op(based_norm_sum_kernel, dim3((2 * C + 31) / 32), 32 * kSumWarps, 0, st, q));
     return BASED_OK;

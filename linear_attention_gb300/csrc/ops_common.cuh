@@ -45,11 +45,11 @@ inline bool overlap(const Span &x, const Span &y) { return x.a < y.b && y.a < x.
 // it in the stream: its CTAs may start while that kernel finishes, and every thread that touches
 // memory first waits for it (griddep_wait). cluster: CTAs per cluster along x.
 template <typename P>
-cudaError_t launch_op(void (*kernel)(P), dim3 grid, int block, size_t smem, cudaStream_t st, const P &arg,
+cudaError_t launch_op(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P &arg,
                       int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

@@ -162,3 +162,29 @@ def test_offsets_past_32_bits(cuda_device):
     grad = based_embed_bwd(ids, dy, V, dtype=BF16)
     assert (grad[V - 1] == 5).all() and (grad[0] == 2).all() and (grad[1 << 20] == 8).all()
     assert int((grad != 0).sum()) == 3 * D
+
+
+@pytest.mark.parametrize("filler", [1200, 6000])
+def test_runs_at_every_place_of_a_tile_among_many_tokens(filler, cuda_device):
+    # enough tokens for the counting sort, with short and with long tiles
+    gen = torch.Generator().manual_seed(3)
+    for first in (0, 1, 5, 8, 13, 31, 32, 40, 63, 64, 69):
+        counts = [first, 1, 2, 40, 31, 32, 33, 64, 1, 97, 0, filler, 3, 400]
+        ids = torch.repeat_interleave(torch.arange(14), torch.tensor(counts))
+        ids[torch.rand(len(ids), generator=gen) < 0.02] = -1
+        ids = ids[torch.randperm(len(ids), generator=gen)].to(torch.int32).cuda()
+        dy = torch.randn(len(ids), 16, generator=gen).cuda()
+        check_bwd(ids, dy, 15, 1.0, F32)
+
+
+@pytest.mark.parametrize("N", [1, 7, 8, 127, 128, 129, 250, 512, 513, 1000, 1023, 1024, 1025, 1030])
+def test_token_counts_around_the_direct_ranking(N, cuda_device):
+    for V in (5, 900, 2 ** 22 - 1, 2 ** 22, 2 ** 22 + 5):
+        gen = torch.Generator().manual_seed(N + V)
+        ids = torch.randint(0, V, (N,), generator=gen)
+        ids[: N // 3] = V - 1
+        ids[N // 2: N // 2 + 2] = -1
+        dy = torch.randn(N, 2, generator=gen)
+        got = based_embed_bwd(ids.to(torch.int32).cuda(), dy.cuda(), V)
+        val, bound = ref.embed_grad(ids, dy, V, 1.0, F32)
+        ref.assert_within(got, val, bound, (N, V))
