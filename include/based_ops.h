@@ -59,7 +59,7 @@ enum { BASED_ACT_NONE = 0, BASED_ACT_SILU = 1, BASED_ACT_SIGMOID = 2 };
  *   saved        (B, ceil(T / BASED_SCAN_SAVE_ROWS), D) float32 or NULL: the states before rows
  *                0, 64, 128, ..., which based_scan_bwd reads
  * Errors: BASED_ERR_NULL_POINTER, BASED_ERR_UNSUPPORTED_TYPE, BASED_ERR_BAD_ARGUMENT (mode),
- * BASED_ERR_BAD_SIZE (B, T or D < 1, T > 2^30, D > 2^22 or B D >= 2^30), BASED_ERR_BAD_STRIDE, BASED_ERR_MISALIGNED,
+ * BASED_ERR_BAD_SIZE (B, T or D < 1, T > 2^30, D > 2^20 or B D >= 2^30), BASED_ERR_BAD_STRIDE, BASED_ERR_MISALIGNED,
  * BASED_ERR_ALIASING, BASED_ERR_CUDA, BASED_ERR_NO_DEVICE.
  */
 BASED_API int based_scan_fwd(const void *gate, int64_t gate_sb, int64_t gate_st, const void *x, int64_t x_sb,

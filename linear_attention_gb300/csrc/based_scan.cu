@@ -10,6 +10,7 @@
 // the state in front of them. So each input is read once and each output written once, however
 // few channels there are, and no CTA waits for one that may not be resident.
 #include <cstddef>
+#include <mutex>
 #include <type_traits>
 
 #include "ops_common.cuh"
@@ -21,14 +22,14 @@ constexpr int kSave = BASED_SCAN_SAVE_ROWS;
 constexpr int kTile = kSave;       // rows of a tile: one saved state each
 constexpr int kRowBytes = 128;     // a tile's row: 64 channels of 16 bits or 32 of 32
 constexpr int kMaxCluster = 16;
-constexpr int kMaxGridY = 65535;   // batch entries along y, then z
-constexpr int kMaxD = 1 << 22;     // channels: a tile of an output spans less than 2^32 bytes
+constexpr int kMaxGrid = 65535;    // blocks along y and z
+constexpr int kMaxD = 1 << 20;     // channels: blocks of them along y; a tile of an output spans less than 2^32 bytes
 
 struct ScanParams {
     const void *gate, *x, *dy;
     int64_t gate_sb, gate_st, x_sb, x_st, dy_sb, dy_st;
-    int B, T, D, slabs;
-    int cluster, log2_cluster;  // CTAs of a cluster, a power of two
+    int B, T, D, b0;      // b0: the launch's first batch entry
+    int cluster, steps;   // CTAs of a cluster; tiles that each of them takes, at most
     int word;             // bytes of a copy to shared memory that every row's start allows: 16 or 4; 0: neither
     int pair;             // two 16-bit outputs can be stored as one word
     const float *state;   // forward: h_{-1}; backward: dfinal
@@ -237,14 +238,14 @@ __device__ __forceinline__ void zero_rows(T *to, const ScanParams &p, int row0, 
 template <typename T>
 struct Place {
     static constexpr int N = 4 / sizeof(T);  // channels of a lane: one 32-bit word
-    int lane, warp, rank, b, c0, c, n, cols, tiles, steps;
+    int lane, warp, rank, b, c0, c, n, cols, tiles;
     __device__ __forceinline__ explicit Place(const ScanParams &p) {
         lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        rank = static_cast<int>(blockIdx.x) & (p.cluster - 1);
-        b = static_cast<int>(blockIdx.z * kMaxGridY + blockIdx.y);
-        c0 = static_cast<int>(blockIdx.x >> p.log2_cluster) * 32 * N, c = c0 + lane * N;
+        // the grid: the CTAs of a cluster, the channel blocks, the batch entries
+        rank = static_cast<int>(blockIdx.x), b = p.b0 + static_cast<int>(blockIdx.z);
+        c0 = static_cast<int>(blockIdx.y) * 32 * N, c = c0 + lane * N;
         n = min(max(p.D - c, 0), N), cols = min(p.D - c0, 32 * N);
-        tiles = (p.T + kTile - 1) / kTile, steps = (tiles + p.cluster - 1) >> p.log2_cluster;
+        tiles = (p.T + kTile - 1) / kTile;
     }
 };
 
@@ -269,7 +270,6 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
-    if (at.b >= p.B) return;
     if (cs > 1) {
         if (threadIdx.x == 0) sm.ex.init();
         cluster_sync();  // every CTA's mbarriers are there before another CTA counts on them
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     for (int k = 0; k < kFwdStages; ++k) fetch(k);
     cp_async_wait<kFwdStages - 1>();
     __syncthreads();
-    for (int step = 0; step < at.steps; ++step) {
+    for (int step = 0; step < p.steps; ++step) {
         const int tile = step * cs + at.rank, row0 = tile * kTile + warp * R;
         const bool live = !RAGGED || step * cs * kTile < len;  // some row of the cluster's tiles is no padding
         const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
@@ -400,7 +400,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
     BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
-    if (at.b >= p.B) return;
     if (cs > 1) {
         if (threadIdx.x == 0) sm.ex.init();
         cluster_sync();
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
     };
     if (warp == 0) fetch_state(0);
     fetch(0);
-    for (int step = 0; step < at.steps; ++step) {
+    for (int step = 0; step < p.steps; ++step) {
         const int tile = tile_of(step), row0 = tile * kTile + warp * R;
         const bool live = !RAGGED || (at.tiles - (step + 1) * cs) * kTile < len;  // some row of the cluster's tiles is no padding
         cp_async_wait<0>();
@@ -626,45 +625,127 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
     return BASED_OK;
 }
 
-// CTAs of a cluster: those whose estimated time is least. A step of a CTA takes `step_us` by its
-// own latencies, or longer where the resident CTAs' copies exceed the memory's rate; a CTA has two steps'
-// worth of start and end besides its share of the tiles. smem(cs): shared memory of a CTA, which
-// decides with the registers (four CTAs) how many an SM holds.
+// What a kernel's steps take, measured: `us` by a CTA's own latencies where the GPU is not full, `bytes` of copies
+// and stores at `rate` bytes per us where it is, and `us_rank` more for each CTA of a cluster.
+struct StepCost {
+    double us, bytes, rate, us_rank;
+};
+
+// How many clusters of each size the device holds at once: a cluster lies within one of the parts that
+// its SMs form, and those are not all equal. Asked once per kernel and device.
+struct ClusterSlots {
+    int64_t clusters[kMaxCluster + 1];
+};
 template <typename F>
-int choose_cluster(int64_t blocks, int64_t tiles, int sms, F smem, double step_us, double step_bytes) {
-    auto step = [&](int64_t resident) {
-        const double us = resident * step_bytes / 6.4e6;  // bytes per us that the memory gives a kernel
-        return us > step_us ? us : step_us;
+int cluster_slots(void (*kernel)(ScanParams), int threads, F smem, const ClusterSlots **out) {
+    struct Entry {
+        void (*kernel)(ScanParams);
+        int dev;
+        ClusterSlots slots;
     };
+    static std::mutex m;
+    static Entry table[256];
+    int dev;
+    OPS_CUDA(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(m);
+    Entry *e = table;
+    for (; e < table + 255 && e->kernel; ++e) {
+        if (e->kernel == kernel && e->dev == dev) {
+            *out = &e->slots;
+            return BASED_OK;
+        }
+    }
+    for (int cs = 1; cs <= kMaxCluster; ++cs) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cs);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem(cs);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cs;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        OPS_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
+        e->slots.clusters[cs] = n;
+    }
+    e->dev = dev;
+    e->kernel = kernel;
+    *out = &e->slots;
+    return BASED_OK;
+}
+
+// CTAs of a cluster: those whose estimated time is least, a CTA having two steps' worth of start and end besides
+// its share of the tiles. Of sequences with padding a little more than half is taken to be alive. Against the best
+// of all sizes on eleven shapes the choice costs up to 6 % (8 x 3000 x 1536: 1, 2, 3, 4 CTAs take
+// 54, 42, 38, 49 us, and 3 are chosen).
+int choose_cluster(int64_t blocks, int64_t tiles, const ClusterSlots &slots, const StepCost &c, bool ragged) {
     int best = 1;
     double least = 0.0;
-    for (int cs = 1; cs <= kMaxCluster && (cs == 1 || cs / 2 < tiles); cs *= 2) {
-        const int64_t per_sm = 228 * 1024 / (static_cast<int64_t>(smem(cs)) + 1024), slots = sms * (per_sm < 4 ? per_sm : 4);
-        const int64_t n = blocks * cs, waves = n / slots, rest = n % slots;
-        const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots) + (rest ? step(rest) : 0.0));
-        // a larger cluster for a clear gain alone: its exchange costs what the estimate leaves out
-        if (cs == 1 || us < 0.9 * least) best = cs, least = us;
+    for (int cs = 1; cs <= kMaxCluster && (cs == 1 || cs / 2 < tiles); ++cs) {
+        if (slots.clusters[cs] < 1) continue;
+        auto step = [&](int64_t resident) {
+            const double us = resident * cs * c.bytes * (ragged ? 0.6 : 1.0) / c.rate;
+            return (us > c.us ? us : c.us) + c.us_rank * cs;
+        };
+        const int64_t waves = blocks / slots.clusters[cs], rest = blocks % slots.clusters[cs];
+        const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots.clusters[cs]) + (rest ? step(rest) : 0.0));
+        if (cs == 1 || us < 0.98 * least) best = cs, least = us;
     }
     return best;
 }
 
+// The cluster size of a call, from a per-thread cache of the last few shapes: a call repeats the
+// shapes of the calls before it far more often than not.
+template <typename F>
+int recent_cluster(ScanParams &p, void (*kernel)(ScanParams), F choose) {
+    struct Entry {
+        void (*kernel)(ScanParams);
+        int dev, B, T, D, cluster;
+    };
+    constexpr int kEntries = 8;
+    static thread_local Entry recent[kEntries];
+    static thread_local int next = 0;
+    int dev;
+    OPS_CUDA(cudaGetDevice(&dev));
+    for (const Entry &e : recent) {
+        if (e.kernel == kernel && e.dev == dev && e.B == p.B && e.T == p.T && e.D == p.D) {
+            p.cluster = e.cluster;
+            return BASED_OK;
+        }
+    }
+    const int rc = choose(&p.cluster);
+    if (rc != BASED_OK) return rc;
+    recent[next] = {kernel, dev, p.B, p.T, p.D, p.cluster};
+    next = (next + 1) % kEntries;
+    return BASED_OK;
+}
+
 template <typename T, typename Smem>
-int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms, double step_us, int tensors,
-                cudaStream_t st) {
-    p.slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
-    const int64_t blocks = static_cast<int64_t>(p.slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
-    p.cluster = choose_cluster(blocks, tiles, sms, Smem::bytes, step_us, static_cast<double>(tensors) * kTile * kRowBytes);
-    for (p.log2_cluster = 0; 1 << p.log2_cluster < p.cluster;) ++p.log2_cluster;
-    // CTAs that are all resident at once spread evenly where no SM can take more than its share: each asks for
-    // that share of the shared memory (8 x 3000 x 1536 backward: 84 us with up to four on an SM, 69 us with three)
+int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms, const StepCost &cost, cudaStream_t st) {
+    const int slabs = (p.D + 32 * Place<T>::N - 1) / (32 * Place<T>::N);
+    const int64_t blocks = static_cast<int64_t>(slabs) * p.B, tiles = (p.T + kTile - 1) / kTile;
     constexpr int64_t kMost = 227 * 1024;
-    // One more with clusters of 16, which have to find their SMs within a part of the GPU.
-    const int64_t per_sm = (blocks * p.cluster + sms - 1) / sms + (p.cluster == kMaxCluster ? 1 : 0), share = per_sm < 4 ? 228 * 1024 / per_sm - 1024 : 0;
+    const int rc = recent_cluster(p, kernel, [&](int *cluster) -> int {
+        OPS_CUDA(allow(kernel, kMost));
+        const ClusterSlots *slots;
+        const int rc = cluster_slots(kernel, threads, Smem::bytes, &slots);
+        if (rc == BASED_OK) *cluster = choose_cluster(blocks, tiles, *slots, cost, p.lengths != nullptr);
+        return rc;
+    });
+    if (rc != BASED_OK) return rc;
+    p.steps = static_cast<int>((tiles + p.cluster - 1) / p.cluster);
+    // CTAs that are all resident at once spread evenly where no SM can take more than its share: each asks for
+    // that share of the shared memory (8 x 3000 x 1536 backward: 84 us with up to four on an SM, 69 us with three).
+    // One more with large clusters, which have to find their SMs within a part of the GPU.
+    const int64_t per_sm = (blocks * p.cluster + sms - 1) / sms + (p.cluster > 8 ? 1 : 0), share = per_sm < 4 ? 228 * 1024 / per_sm - 1024 : 0;
     size_t smem = Smem::bytes(p.cluster);
     if (share > static_cast<int64_t>(smem)) smem = static_cast<size_t>(share < kMost ? share : kMost);
-    OPS_CUDA(allow(kernel, kMost));
-    const dim3 grid(static_cast<unsigned>(p.slabs) * p.cluster, p.B < kMaxGridY ? p.B : kMaxGridY, (p.B + kMaxGridY - 1) / kMaxGridY);
-    OPS_CUDA(launch_op(kernel, grid, threads, smem, st, p, p.cluster));
+    for (p.b0 = 0; p.b0 < p.B; p.b0 += kMaxGrid) {
+        const dim3 grid(p.cluster, slabs, p.B - p.b0 < kMaxGrid ? p.B - p.b0 : kMaxGrid);
+        OPS_CUDA(launch_op(kernel, grid, threads, smem, st, p, p.cluster));
+    }
     return BASED_OK;
 }
 template <typename T>
@@ -676,13 +757,15 @@ int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
             !fast    ? (log ? based_scan_bwd_kernel<T, kLog, true, false> : based_scan_bwd_kernel<T, kSig, true, false>)
             : ragged ? (log ? based_scan_bwd_kernel<T, kLog, true, true> : based_scan_bwd_kernel<T, kSig, true, true>)
                      : (log ? based_scan_bwd_kernel<T, kLog, false, true> : based_scan_bwd_kernel<T, kSig, false, true>);
-        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, sms, 2.4, 5, st);
+        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, sms,
+                                                     {2.6, 5.0 * kTile * kRowBytes, 6.6e6, 0.03}, st);
     }
     void (*const k)(ScanParams) =
         !fast    ? (log ? based_scan_fwd_kernel<T, kLog, true, false> : based_scan_fwd_kernel<T, kSig, true, false>)
         : ragged ? (log ? based_scan_fwd_kernel<T, kLog, true, true> : based_scan_fwd_kernel<T, kSig, true, true>)
                  : (log ? based_scan_fwd_kernel<T, kLog, false, true> : based_scan_fwd_kernel<T, kSig, false, true>);
-    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, sms, 1.7, 3, st);
+    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, sms,
+                                                 {1.6, 3.0 * kTile * kRowBytes, 6.7e6, 0.02}, st);
 }
 
 int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream) {

@@ -90,7 +90,7 @@ REFUSALS = [
     (scan_fwd, dict(dtype=3), TYPE), (scan_fwd, dict(dtype=-1), TYPE), (scan_fwd, dict(mode=2), ARG),
     (scan_fwd, dict(B=0), SIZE), (scan_fwd, dict(T=0), SIZE), (scan_fwd, dict(D=-1), SIZE),
     (scan_fwd, dict(B=1 << 16, D=1 << 15), SIZE), (scan_fwd, dict(T=(1 << 30) + 1), SIZE),
-    (scan_fwd, dict(gst=-64), STRIDE), (scan_fwd, dict(xsb=-1), STRIDE),
+    (scan_fwd, dict(B=1, D=(1 << 20) + 1), SIZE), (scan_fwd, dict(gst=-64), STRIDE), (scan_fwd, dict(xsb=-1), STRIDE),
     (scan_fwd, dict(x=at(1) + 1), ALIGN), (scan_fwd, dict(state=at(2) + 2), ALIGN), (scan_fwd, dict(lengths=at(3) + 2), ALIGN),
     (scan_fwd, dict(y=at(0)), ALIAS), (scan_fwd, dict(y=at(1) + 2 * 1279), ALIAS), (scan_fwd, dict(final=at(4)), ALIAS),
     (scan_fwd, dict(saved=at(5) + 256), ALIAS), (scan_fwd, dict(final=at(2) + 4), ALIAS), (scan_fwd, dict(y=at(3)), ALIAS),
