@@ -629,7 +629,7 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     // one cluster sorts; enough others write the zeros: the rest of the GPU, or 16 words a thread
     int64_t fill = (out_bytes / 16 + kSortCluster * kSortThreads * 16 - 1) / (kSortCluster * kSortThreads * 16);
     // no more clusters than are resident at once (a cluster's CTAs share a part of the GPU, which leaves some SMs over)
-    const int64_t most = 2 * sms / kSortCluster * 4 / 5;
+    const int64_t most = 2 * sms / kSortCluster * 9 / 10;
     fill = fill < 1 ? 1 : fill < most ? fill : most;
     OPS_CUDA(allow(based_embed_sort_kernel, sizeof(SortSmem)));
     OPS_CUDA(launch_op(based_embed_sort_kernel, dim3(static_cast<unsigned>((fill + 1) * kSortCluster)), kSortThreads,
