@@ -52,11 +52,13 @@ struct Row<T, true> {
 #pragma unroll
         for (int k = 0; k < 4 * kQuads; ++k) w[k] = 0;
     }
+    // ONCE: the data is not kept in L2 over what others read again
+    template <bool ONCE>
     __device__ __forceinline__ void load(const T *p, int n, int) {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
             if (n <= 0) continue;
-            const uint4 q = reinterpret_cast<const uint4 *>(p)[k];
+            const uint4 *at = reinterpret_cast<const uint4 *>(p) + k, q = ONCE ? __ldcs(at) : *at;
             w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
         }
     }
@@ -85,6 +87,7 @@ struct Row<T, false> {
 #pragma unroll
         for (int k = 0; k < kElems; ++k) w[k] = from_f32<T>(0.0f);
     }
+    template <bool ONCE>
     __device__ __forceinline__ void load(const T *p, int n, int step) {
 #pragma unroll
         for (int k = 0; k < kElems; ++k)
@@ -204,9 +207,11 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
     // past the last row the registers keep an earlier one
     auto fetch = [&] {
         const int m = row < p.R ? n : 0;
-        nx.load(px, m, step);
-        if (GATED) nz.load(pz, m, step);
-        if (BWD) nd.load(pd, m, step);
+        // streaming loads forward (16384 x 1024, float32 in: 23.3 to 18.7 us), ordinary ones backward (they
+        // take 67 us there, streaming ones 69)
+        nx.template load<!BWD>(px, m, step);
+        if (GATED) nz.template load<!BWD>(pz, m, step);
+        if (BWD) nd.template load<!BWD>(pd, m, step);
     };
     fetch();
     __syncthreads();
