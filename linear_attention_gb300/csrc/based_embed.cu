@@ -209,7 +209,7 @@ __device__ __forceinline__ void rank_few(const SortParams &p, uint32_t *all) {
 // cluster a pass costs barriers of a few hundred nanoseconds where launches of their own cost
 // microseconds. Up to 32768 tokens every key is loaded once a pass; more go through twice, in chunks.
 __global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const SortParams p) {
-    extern __shared__ int raw[];
+    extern __shared__ __align__(128) int raw[];
     SortSmem &sm = *reinterpret_cast<SortSmem *>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
     griddep_wait();
@@ -610,6 +610,9 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     if (overlap(so, span(ids, N - 1, is)) || overlap(so, span(dy, (N - 1) * dy_sr + D - 1, es)))
         return BASED_ERR_ALIASING;
     if (!workspace || !aligned(workspace, 16) || ws_bytes < e.bytes) return BASED_ERR_WORKSPACE;
+    const Span sw = span(workspace, static_cast<int64_t>(e.bytes) - 1, 1);
+    if (overlap(sw, so) || overlap(sw, span(ids, N - 1, is)) || overlap(sw, span(dy, (N - 1) * dy_sr + D - 1, es)))
+        return BASED_ERR_ALIASING;
     int sms;
     const int rc = host_device(&sms);
     if (rc != BASED_OK) return rc;

@@ -529,6 +529,15 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
     if (sums) {
         if (!workspace || !aligned(workspace, 16) || ws_bytes < static_cast<size_t>(s.grid_x) * 2 * C * sizeof(float))
             return BASED_ERR_WORKSPACE;
+        const size_t xs = elem_size(x_dtype), es = elem_size(dtype), ps = elem_size(p_dtype);
+        const Span sw = span(workspace, static_cast<int64_t>(s.grid_x) * 2 * C - 1, sizeof(float));
+        const Span all[] = {span(x, (R - 1) * x_sr + C - 1, xs),   span(gate, (R - 1) * p.gate_sr + C - 1, es),
+                            span(dy, (R - 1) * dy_sr + C - 1, es), span(dx, R * C - 1, xs),
+                            span(dgate, R * C - 1, es),            span(weight, C - 1, ps),
+                            span(bias, C - 1, ps),                 span(dweight, C - 1, ps),
+                            span(dbias, C - 1, ps)};
+        for (const Span &t : all)
+            if (overlap(sw, t)) return BASED_ERR_ALIASING;
         p.partial = static_cast<float *>(workspace);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -104,8 +104,9 @@ __device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t st
         copy_words<THREADS, 4>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
     } else {
         // Rows that start on an odd 16-bit element (no asynchronous copy is that narrow), or far apart:
-        // element by element through registers, the loads of four words at a time under way together.
-        constexpr int kPer = 4 / es, kStep = THREADS / 32, kAhead = 4;
+        // element by element through registers, the loads of eight words at a time under way together
+        // (three CTAs an SM, for the registers).
+        constexpr int kPer = 4 / es, kStep = THREADS / 32, kAhead = 8;
         const int col = static_cast<int>(threadIdx.x & 31) * kPer, row0 = threadIdx.x >> 5;
         const T *from = src + row0 * stride + col;
 #pragma unroll 1
@@ -268,7 +269,7 @@ struct FwdSmem {
 };
 
 template <typename T, int MODE, bool RAGGED, bool FAST>
-__global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
     FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
@@ -287,8 +288,13 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
     const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = p.pair && at.n == N;
-    Vec<N> carry;  // warp 0's: the state in front of the cluster's tiles
-    load_state(p.state ? p.state + plane : nullptr, at.n, carry);
+    Vec<N> carry = splat<N>(0.0f);  // warp 0's: the state in front of the cluster's tiles
+    if (warp == 0) {
+        load_state(p.state ? p.state + plane : nullptr, at.n, carry);
+        // The store needs the loaded value: this CTA has read the state before it sends its first map, and so before
+        // any CTA of the cluster can have the last state, which may be written to the same place.
+        sm.start[lane] = carry;
+    }
     bool waiting = true;
     auto fetch = [&](int step) {
         const int row = (step * cs + at.rank) * kTile, rows = min(len - row, kTile);
@@ -399,7 +405,7 @@ struct BwdSmem {
 };
 
 template <typename T, int MODE, bool RAGGED, bool FAST>
-__global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
     extern __shared__ __align__(128) uint8_t raw[];
     BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
@@ -420,8 +426,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 4) based_scan_bwd_kernel(const
     T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D;
     const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = p.pair && at.n == N;
-    Vec<N> carry;  // warp 1's: mu behind the cluster's tiles
-    load_state(p.state ? p.state + plane : nullptr, at.n, carry);
+    Vec<N> carry = splat<N>(0.0f);  // warp 1's: mu behind the cluster's tiles
+    if (warp == 1) load_state(p.state ? p.state + plane : nullptr, at.n, carry);
     bool waiting = true;
     int exchanges = 0;
     auto tile_of = [&](int step) { return at.tiles - 1 - (step * cs + at.rank); };
@@ -624,7 +630,8 @@ int check_scan(const ScanParams &p, int dtype, int mode, bool bwd) {
                         bwd ? Span{0, 0} : span(p.saved, saved, 4)};
     for (int i = 0; i < 4; ++i) {
         for (const Span &s : in)
-            if (overlap(out[i], s) && !(p.state && p.final_state == p.state && i == 2 && s.a == in[4].a && s.b == in[4].b))
+            // the last state may take the place of the first
+            if (overlap(out[i], s) && !(!bwd && p.state && p.final_state == p.state && i == 2 && s.a == in[4].a && s.b == in[4].b))
                 return BASED_ERR_ALIASING;
         for (int k = 0; k < i; ++k)
             if (overlap(out[i], out[k])) return BASED_ERR_ALIASING;

@@ -96,7 +96,7 @@ REFUSALS = [
     (scan_fwd, dict(saved=at(5) + 256), ALIAS), (scan_fwd, dict(final=at(2) + 4), ALIAS), (scan_fwd, dict(y=at(3)), ALIAS),
     (scan_bwd, dict(dy=None), NULL), (scan_bwd, dict(saved=None), NULL), (scan_bwd, dict(dx=None), NULL),
     (scan_bwd, dict(dgate=at(0)), ALIAS), (scan_bwd, dict(dx=at(6)), ALIAS), (scan_bwd, dict(dstate=at(3)), ALIAS),
-    (scan_bwd, dict(dst=-1), STRIDE), (scan_bwd, dict(dy=at(2) + 1), ALIGN), (scan_bwd, dict(dtype=7), TYPE),
+    (scan_bwd, dict(dstate=at(4)), ALIAS), (scan_bwd, dict(dst=-1), STRIDE), (scan_bwd, dict(dy=at(2) + 1), ALIGN), (scan_bwd, dict(dtype=7), TYPE),
     (step, dict(pool=None), NULL), (step, dict(N=0), SIZE), (step, dict(slots=None, N=6), SIZE), (step, dict(S=0), SIZE),
     (step, dict(gs=-1), STRIDE), (step, dict(pool=at(2) + 2), ALIGN), (step, dict(y=at(2)), ALIAS),
     (step, dict(pool=at(0)), ALIAS), (step, dict(mode=-1), ARG), (step, dict(dtype=9), TYPE),
@@ -115,7 +115,7 @@ REFUSALS = [
     (embed_bwd, dict(out=None), NULL), (embed_bwd, dict(dt=1, gt=2), TYPE), (embed_bwd, dict(N=1 << 30), SIZE),
     (embed_bwd, dict(D=0), SIZE), (embed_bwd, dict(ds=-2), STRIDE), (embed_bwd, dict(out=at(2) + 2), ALIGN),
     (embed_bwd, dict(out=at(1)), ALIAS), (embed_bwd, dict(ws=None), WS), (embed_bwd, dict(n=64), WS),
-    (embed_bwd, dict(ws=at(3) + 8), WS),
+    (embed_bwd, dict(ws=at(3) + 8), WS), (embed_bwd, dict(ws=at(1)), ALIAS), (embed_bwd, dict(ws=at(2) + 256), ALIAS),
 ]
 
 
