@@ -15,7 +15,7 @@ namespace based {
 namespace {
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;  // two CTAs an SM
-constexpr int kSortCluster = 8;
+constexpr int kSortCluster = 8, kWideCluster = 16;         // CTAs that sort
 constexpr int kSortRounds = 8;                             // keys that a thread holds, at most
 constexpr int kSortChunk = kSortThreads * kSortRounds;
 constexpr int kMaxBits = 9;                                // of a digit
@@ -203,28 +203,29 @@ __device__ __forceinline__ void rank_few(const SortParams &p, uint32_t *all) {
     }
 }
 
-// The first cluster sorts: each of its CTAs takes an eighth of the keys. Per pass and CTA: count the
+// The first cluster sorts: each of its CTAs takes an equal part of the keys. Per pass and CTA: count the
 // digits; read the other CTAs' counts through distributed shared memory; move each key behind those
 // of smaller digits, then those of the same digit in earlier CTAs, warps, rounds and lanes. On one
 // cluster a pass costs barriers of a few hundred nanoseconds where launches of their own cost
-// microseconds. Up to 32768 tokens every key is loaded once a pass; more go through twice, in chunks.
+// microseconds. Up to 4096 tokens a CTA every key is loaded once a pass; more go through twice, in chunks.
+template <int CLUSTER>
 __global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const SortParams p) {
     extern __shared__ __align__(128) int raw[];
     SortSmem &sm = *reinterpret_cast<SortSmem *>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
     griddep_wait();
     griddep_launch_dependents();
-    if (blockIdx.x >= kSortCluster) {
-        const int64_t step = static_cast<int64_t>(gridDim.x - kSortCluster) * kSortThreads;
-        const int64_t at = static_cast<int64_t>(blockIdx.x - kSortCluster) * kSortThreads + tid;
+    if (blockIdx.x >= CLUSTER) {
+        const int64_t step = static_cast<int64_t>(gridDim.x - CLUSTER) * kSortThreads;
+        const int64_t at = static_cast<int64_t>(blockIdx.x - CLUSTER) * kSortThreads + tid;
         // bulk copies of zeros from shared memory, by one thread
         for (int i = tid; i < kFillBytes / 16; i += kSortThreads) reinterpret_cast<uint4 *>(raw)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncthreads();
         if (tid == 0) {
             const int64_t n = p.words * 16;
-            for (int64_t i = static_cast<int64_t>(blockIdx.x - kSortCluster) * kFillBytes; i < n;
-                 i += static_cast<int64_t>(gridDim.x - kSortCluster) * kFillBytes)
+            for (int64_t i = static_cast<int64_t>(blockIdx.x - CLUSTER) * kFillBytes; i < n;
+                 i += static_cast<int64_t>(gridDim.x - CLUSTER) * kFillBytes)
                 bulk_store(static_cast<uint8_t *>(p.out) + i, smem_u32(raw), static_cast<int>(min(n - i, static_cast<int64_t>(kFillBytes))));
             bulk_commit_group();
             bulk_wait_group_all();
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const
         return;
     }
     const int rank = static_cast<int>(cluster_rank()), digits = 1 << p.bits;
-    const int64_t begin = static_cast<int64_t>(p.N) * rank / kSortCluster;
-    const int64_t end = static_cast<int64_t>(p.N) * (rank + 1) / kSortCluster;
+    const int64_t begin = static_cast<int64_t>(p.N) * rank / CLUSTER;
+    const int64_t end = static_cast<int64_t>(p.N) * (rank + 1) / CLUSTER;
     const bool once = end - begin <= kSortChunk;
     SortChunk ch;
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -266,11 +267,11 @@ __global__ void __launch_bounds__(kSortThreads, 2) based_embed_sort_kernel(const
         cluster_sync();
         int total = 0, before = 0;
         if (tid < digits) {
-            int v[kSortCluster];
+            int v[CLUSTER];
 #pragma unroll
-            for (int r = 0; r < kSortCluster; ++r) v[r] = load_remote(&sm.hist[tid], r);
+            for (int r = 0; r < CLUSTER; ++r) v[r] = load_remote(&sm.hist[tid], r);
 #pragma unroll
-            for (int r = 0; r < kSortCluster; ++r) {
+            for (int r = 0; r < CLUSTER; ++r) {
                 total += v[r];
                 before += r < rank ? v[r] : 0;
             }
@@ -614,7 +615,7 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     if (overlap(sw, so) || overlap(sw, span(ids, N - 1, is)) || overlap(sw, span(dy, (N - 1) * dy_sr + D - 1, es)))
         return BASED_ERR_ALIASING;
     int sms;
-    const int rc = host_device(&sms);
+    int rc = host_device(&sms);
     if (rc != BASED_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -623,14 +624,22 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     const int64_t out_bytes = static_cast<int64_t>(V) * D * gs;
     const SortParams s = {ids, lists[0], lists[1], lists[2], lists[3], static_cast<int>(N), V, ids64 ? 1 : 0, e.few,
                           e.passes, e.bits, dtable, aligned(dtable, 16) ? out_bytes / 16 : 0, out_bytes};
-    // one cluster sorts; enough others write the zeros: the rest of the GPU, or 16 words a thread
-    int64_t fill = (out_bytes / 16 + kSortCluster * kSortThreads * 16 - 1) / (kSortCluster * kSortThreads * 16);
-    // no more clusters than are resident at once (a cluster's CTAs share a part of the GPU, which leaves some SMs over)
-    const int64_t most = 2 * sms / kSortCluster * 9 / 10;
+    // one cluster sorts; enough others write the zeros: the rest of what is resident at once, or 16 words a thread
+    // Sixteen CTAs sort where the sort would take longer than the zeros (some 0.7 ns a token with eight CTAs), or where
+    // eight cannot hold the tokens: 32768 tokens, 50000 x 64: 26 us, 31 with eight; 65536 tokens, 50000 x 1024: 83 and
+    // 105. Their clusters leave more of the GPU unused for the zeros (32768 tokens, 50000 x 1024: 66 us, 61 with eight).
+    const bool wider = N > kSortCluster * kSortChunk || (N > 8192 && out_bytes < 4480 * N);
+    const int cluster = wider ? kWideCluster : kSortCluster;
+    void (*const sort)(SortParams) =
+        cluster == kWideCluster ? based_embed_sort_kernel<kWideCluster> : based_embed_sort_kernel<kSortCluster>;
+    OPS_CUDA(allow(sort, sizeof(SortSmem)));
+    int resident;
+    if ((rc = resident_clusters(reinterpret_cast<const void *>(sort), kSortThreads, sizeof(SortSmem), cluster, &resident)) != BASED_OK)
+        return rc;
+    int64_t fill = (out_bytes / 16 + cluster * kSortThreads * 16 - 1) / (cluster * kSortThreads * 16);
+    const int64_t most = resident > 2 ? resident - 1 : 1;
     fill = fill < 1 ? 1 : fill < most ? fill : most;
-    OPS_CUDA(allow(based_embed_sort_kernel, sizeof(SortSmem)));
-    OPS_CUDA(launch_op(based_embed_sort_kernel, dim3(static_cast<unsigned>((fill + 1) * kSortCluster)), kSortThreads,
-                       sizeof(SortSmem), st, s, kSortCluster));
+    OPS_CUDA(launch_op(sort, dim3(static_cast<unsigned>((fill + 1) * cluster)), kSortThreads, sizeof(SortSmem), st, s, cluster));
     const int done = (e.passes - 1) & 1;
     const SumParams p = {lists[done], lists[2 + done], dy, dy_sr, static_cast<int>(N), V, D, e.rows, scale,
                          reinterpret_cast<float *>(ws + e.partial), dtable};

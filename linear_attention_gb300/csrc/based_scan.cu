@@ -10,7 +10,6 @@
 // the state in front of them. So each input is read once and each output written once, however
 // few channels there are, and no CTA waits for one that may not be resident.
 #include <cstddef>
-#include <mutex>
 #include <type_traits>
 
 #include "ops_common.cuh"
@@ -645,66 +644,22 @@ struct StepCost {
     double us, bytes, rate, us_rank;
 };
 
-// How many clusters of each size the device holds at once: a cluster lies within one of the parts that
-// its SMs form, and those are not all equal. Asked once per kernel and device.
-struct ClusterSlots {
-    int64_t clusters[kMaxCluster + 1];
-};
-template <typename F>
-int cluster_slots(void (*kernel)(ScanParams), int threads, F smem, const ClusterSlots **out) {
-    struct Entry {
-        void (*kernel)(ScanParams);
-        int dev;
-        ClusterSlots slots;
-    };
-    static std::mutex m;
-    static Entry table[256];
-    int dev;
-    OPS_CUDA(cudaGetDevice(&dev));
-    std::lock_guard<std::mutex> lk(m);
-    Entry *e = table;
-    for (; e < table + 255 && e->kernel; ++e) {
-        if (e->kernel == kernel && e->dev == dev) {
-            *out = &e->slots;
-            return BASED_OK;
-        }
-    }
-    for (int cs = 1; cs <= kMaxCluster; ++cs) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(cs);
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem(cs);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cs;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        OPS_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
-        e->slots.clusters[cs] = n;
-    }
-    e->dev = dev;
-    e->kernel = kernel;
-    *out = &e->slots;
-    return BASED_OK;
-}
-
 // CTAs of a cluster: those whose estimated time is least, a CTA having two steps' worth of start and end besides
 // its share of the tiles. Of sequences with padding a little more than half is taken to be alive. Against the best
 // of all sizes on eleven shapes the choice costs up to 6 % (8 x 3000 x 1536: 1, 2, 3, 4 CTAs take
 // 54, 42, 38, 49 us, and 3 are chosen).
-int choose_cluster(int64_t blocks, int64_t tiles, const ClusterSlots &slots, const StepCost &c, bool ragged) {
+// slots[cs]: clusters of cs CTAs that the device holds at once.
+int choose_cluster(int64_t blocks, int64_t tiles, const int (&slots)[kMaxCluster + 1], const StepCost &c, bool ragged) {
     int best = 1;
     double least = 0.0;
     for (int cs = 1; cs <= kMaxCluster && (cs == 1 || cs / 2 < tiles); ++cs) {
-        if (slots.clusters[cs] < 1) continue;
+        if (slots[cs] < 1) continue;
         auto step = [&](int64_t resident) {
             const double us = resident * cs * c.bytes * (ragged ? 0.6 : 1.0) / c.rate;
             return (us > c.us ? us : c.us) + c.us_rank * cs;
         };
-        const int64_t waves = blocks / slots.clusters[cs], rest = blocks % slots.clusters[cs];
-        const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots.clusters[cs]) + (rest ? step(rest) : 0.0));
+        const int64_t waves = blocks / slots[cs], rest = blocks % slots[cs];
+        const double us = ((tiles + cs - 1) / cs + 2) * (waves * step(slots[cs]) + (rest ? step(rest) : 0.0));
         if (cs == 1 || us < 0.98 * least) best = cs, least = us;
     }
     return best;
@@ -743,10 +698,13 @@ int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms,
     constexpr int64_t kMost = 227 * 1024;
     const int rc = recent_cluster(p, kernel, [&](int *cluster) -> int {
         OPS_CUDA(allow(kernel, kMost));
-        const ClusterSlots *slots;
-        const int rc = cluster_slots(kernel, threads, Smem::bytes, &slots);
-        if (rc == BASED_OK) *cluster = choose_cluster(blocks, tiles, *slots, cost, p.lengths != nullptr);
-        return rc;
+        int slots[kMaxCluster + 1];
+        for (int cs = 1; cs <= kMaxCluster; ++cs) {
+            const int rc = resident_clusters(reinterpret_cast<const void *>(kernel), threads, Smem::bytes(cs), cs, &slots[cs]);
+            if (rc != BASED_OK) return rc;
+        }
+        *cluster = choose_cluster(blocks, tiles, slots, cost, p.lengths != nullptr);
+        return BASED_OK;
     });
     if (rc != BASED_OK) return rc;
     p.steps = static_cast<int>((tiles + p.cluster - 1) / p.cluster);

@@ -86,6 +86,43 @@ cudaError_t allow(K *kernel, size_t smem) {
     return e;
 }
 
+// How many clusters of `cluster` CTAs of a kernel the current device holds at once: a cluster lies within
+// one of the parts that the SMs form, and those are not all equal. Asked once per kernel, device and size.
+inline int resident_clusters(const void *kernel, int threads, size_t smem, int cluster, int *out) {
+    struct Entry {
+        const void *kernel;
+        int dev, cluster, n;
+    };
+    static std::mutex m;
+    static Entry table[1024];
+    static int used = 0;
+    int dev;
+    OPS_CUDA(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lk(m);
+    for (int i = 0; i < used; ++i) {
+        const Entry &e = table[i];
+        if (e.kernel == kernel && e.dev == dev && e.cluster == cluster) {
+            *out = e.n;
+            return BASED_OK;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    OPS_CUDA(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
+    if (used < 1024) table[used++] = {kernel, dev, cluster, n};
+    *out = n;
+    return BASED_OK;
+}
+
 // ------------------------------------------------------------------------------------------------
 // Device: clusters
 // ------------------------------------------------------------------------------------------------
