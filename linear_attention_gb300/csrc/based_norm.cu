@@ -160,13 +160,13 @@ __device__ __forceinline__ void with_act(int act, F f) {
 }
 
 // Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
-// and dbias, 80 (100 where x is float32): weight and bias wait in shared memory, four 16-byte reads a row. Channel by channel
-// (VEC false) they take 85 and 128. BIG ones may have 512 threads.
+// and dbias, 80 (100 where x is float32): weight and bias wait in shared memory, four 16-byte reads a
+// row. Channel by channel (VEC false) they take 85 and 128. BIG ones may have 512 threads.
 template <typename TX, typename TY, bool VEC, bool GATED, bool BWD, bool BIG>
 __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : VEC ? (BWD ? (sizeof(TX) == 4 ? 5 : 6) : 4) : (BWD ? 2 : 3))
     based_norm_kernel(const NormParams p) {
     constexpr int P = kElems / 2;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];
     const int slot = threadIdx.x / p.tpg, l = threadIdx.x % p.tpg;
     const int r = slot / p.gpb, g = blockIdx.y * p.gpb + slot % p.gpb;
     const int first = VEC ? l * kElems : l, step = p.tpg, per = p.gpb * p.tpg;
