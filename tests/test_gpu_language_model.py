@@ -127,3 +127,65 @@ def test_based_layers_score(cuda_device):
     again, _ = model.prefill(other, lengths)
     keep = int(min(50, int(lengths.min())))
     assert torch.equal(logits[:, :keep], again[:, :keep])
+
+
+FIRST_CALLS = """
+import torch
+from linear_attention_gb300 import ops
+dev = "cuda"
+g, x, dy = (torch.randn(2, 200, 96, device=dev).bfloat16() for _ in range(3))
+w = torch.ones(96, device=dev)
+ids = torch.randint(0, 50, (3000,), device=dev, dtype=torch.int32)
+table, de = torch.randn(50, 64, device=dev), torch.randn(3000, 64, device=dev)
+pool = torch.randn(2, 96, device=dev)
+kept = pool.clone()
+
+def calls():
+    y, final, saved = ops.based_scan_fwd(g, x, save=True)
+    return (y, final, *ops.based_scan_bwd(g, x, dy, saved), ops.based_scan_step(g[:, 0], x[:, 0], pool),
+            ops.based_norm_fwd(x, 2, w, w, g), *ops.based_norm_bwd(dy, x, 2, w, w, g),
+            ops.based_embed_fwd(ids, table), ops.based_embed_bwd(ids, de, 50))
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+captured = [t.clone() for t in captured]
+pool.copy_(kept)
+for a, b in zip(captured, calls()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured(cuda_device):
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
+
+
+def test_two_threads_call_at_once(cuda_device):
+    import threading
+
+    from linear_attention_gb300 import ops
+    inputs = [tuple(torch.randn(2, 100 + 70 * i, 64, device="cuda").bfloat16() for _ in range(2)) for i in range(4)]
+    want = [ops.based_scan_fwd(g, x)[0] for g, x in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        for _ in range(50):
+            y = ops.based_scan_fwd(*inputs[i], stream=stream)[0]
+            stream.synchronize()
+            if not torch.equal(y, want[i]):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
