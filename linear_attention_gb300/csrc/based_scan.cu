@@ -29,7 +29,7 @@ struct ScanParams {
     int64_t gate_sb, gate_st, x_sb, x_st, dy_sb, dy_st;
     int B, T, D, b0;      // b0: the launch's first batch entry
     int cluster, steps;   // CTAs of a cluster; tiles that each of them takes, at most
-    int word;             // bytes of a copy to shared memory that every row's start allows: 16 or 4; 0: neither
+    int fast;             // every row of every input starts on 16 bytes, a tile's rows within 2^32 bytes
     int pair;             // two 16-bit outputs can be stored as one word
     const float *state;   // forward: h_{-1}; backward: dfinal
     const int32_t *lengths;
@@ -57,12 +57,8 @@ __device__ __forceinline__ Vec<N> increment(const Vec<N> &rest, const Vec<N> &x)
 // ------------------------------------------------------------------------------------------------
 // Copies of a tile's rows into shared memory
 // ------------------------------------------------------------------------------------------------
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -73,56 +69,118 @@ __device__ __forceinline__ void cp_async_wait() {
 // Rows [0, rows) of the first `cols` bytes of rows at src, `stride` bytes apart, into the tile at dst, by
 // all THREADS threads of the CTA. The other places keep what they held; nothing that is stored depends
 // on it. src is the same for all threads and their offsets from it fit 32 bits: one addition a copy.
-template <int THREADS, int BYTES>
-__device__ __forceinline__ void copy_words(uint8_t *dst, const uint8_t *src, uint32_t stride, int rows, int cols) {
-    constexpr int kWords = kRowBytes / BYTES, kStep = THREADS / kWords;
+template <int THREADS>
+__device__ __forceinline__ void copy_aligned(uint8_t *dst, const uint8_t *src, uint32_t stride, int rows, int cols) {
+    constexpr int kWords = kRowBytes / 16, kStep = THREADS / kWords;
     const int col = static_cast<int>(threadIdx.x) % kWords, row0 = static_cast<int>(threadIdx.x) / kWords;
-    if (col * BYTES >= cols) return;
-    uint32_t off = row0 * stride + col * BYTES;
-    const uint32_t to = smem_u32(dst) + row0 * kRowBytes + col * BYTES;
+    if (col * 16 >= cols) return;
+    uint32_t off = row0 * stride + col * 16;
+    const uint32_t to = smem_u32(dst) + row0 * kRowBytes + col * 16;
     if (rows == kTile) {
 #pragma unroll
         for (int k = 0; k < kTile / kStep; ++k) {
-            cp_async<BYTES>(to + k * kStep * kRowBytes, src + off);
+            cp_async_16(to + k * kStep * kRowBytes, src + off);
             off += kStep * stride;
         }
     } else {
         for (int k = 0; k < kTile / kStep && row0 + k * kStep < rows; ++k) {
-            cp_async<BYTES>(to + k * kStep * kRowBytes, src + off);
+            cp_async_16(to + k * kStep * kRowBytes, src + off);
             off += kStep * stride;
         }
     }
 }
-// T: the element; stride in elements, cols in channels. FAST: some word can be copied asynchronously.
-template <typename T, int THREADS, bool FAST>
-__device__ __forceinline__ void copy_tile(uint8_t *dst, const T *src, int64_t stride, int rows, int cols, int word) {
-    constexpr int es = sizeof(T);
-    if (FAST && word == 16) {
-        copy_words<THREADS, 16>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
-    } else if (FAST) {
-        copy_words<THREADS, 4>(dst, reinterpret_cast<const uint8_t *>(src), static_cast<uint32_t>(stride) * es, rows, cols * es);
-    } else {
-        // Rows that start on an odd 16-bit element (no asynchronous copy is that narrow), or far apart:
-        // element by element through registers, the loads of eight words at a time under way together
-        // (three CTAs an SM, for the registers).
-        constexpr int kPer = 4 / es, kStep = THREADS / 32, kAhead = 8;
-        const int col = static_cast<int>(threadIdx.x & 31) * kPer, row0 = threadIdx.x >> 5;
-        const T *from = src + row0 * stride + col;
-#pragma unroll 1
-        for (int k = 0; k < kTile / kStep; k += kAhead) {
-            Pack<T, kPer> w[kAhead];
+
+// Rows that start anywhere: a row's 16-byte words from the one its first element lies in, nine at most, at the
+// row's place in a tile with room for them. Words that reach past the tensor [first, end) are
+// copied element by element: nothing outside it is read.
+constexpr int kWideRow = kRowBytes + 16;
+template <typename T, int THREADS>
+__device__ __forceinline__ void copy_anywhere(uint8_t *dst, const T *src, int64_t stride, int rows, int cols,
+                                              const T *first, const T *end) {
+    constexpr int kWords = kRowBytes / 16, kStep = THREADS / kWords;
+    static_assert(THREADS >= kTile && kTile % kStep == 0, "a thread for each row's ninth word");
+    static_assert(kStep * sizeof(T) % 16 == 0, "a thread's rows start alike");
+    const uintptr_t at = reinterpret_cast<uintptr_t>(src);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(first), hi = reinterpret_cast<uintptr_t>(end);
+    const uint32_t bytes = cols * static_cast<uint32_t>(sizeof(T)), low = static_cast<uint32_t>(at);
+    const uintptr_t begin = at & ~static_cast<uintptr_t>(15), stop = at + (rows - 1) * stride * sizeof(T) + bytes + 15;
+    const int word = static_cast<int>(threadIdx.x) % kWords, row0 = static_cast<int>(threadIdx.x) / kWords;
+    if (stride < (1 << 24) && begin >= lo && (stop & ~static_cast<uintptr_t>(15)) <= hi) {
+        const uint32_t pitch = static_cast<uint32_t>(stride) * sizeof(T);
+        const uint8_t *const from = reinterpret_cast<const uint8_t *>(begin);
+        uint32_t off = (low & 15) + row0 * pitch, to = smem_u32(dst) + row0 * kWideRow + word * 16;
+        if (word * 16 < (off & 15) + bytes) {
+            off = (off & ~15u) + word * 16;
+            if (rows == kTile) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    if (row0 + (k + i) * kStep < rows && col + j < cols) w[i].v[j] = from[(k + i) * (kStep * stride) + j];
+                for (int k = 0; k < kTile / kStep; ++k) {
+                    cp_async_16(to + k * kStep * kWideRow, from + off);
+                    off += kStep * pitch;
+                }
+            } else {
+                for (int row = row0; row < rows; row += kStep) {
+                    cp_async_16(to, from + off);
+                    to += kStep * kWideRow, off += kStep * pitch;
+                }
             }
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                *reinterpret_cast<Pack<T, kPer> *>(dst + (row0 + (k + i) * kStep) * kRowBytes + col * es) = w[i];
+        }
+        const uint32_t ninth = threadIdx.x, last = (low & 15) + ninth * pitch;
+        if (ninth < static_cast<uint32_t>(rows) && kRowBytes < (last & 15) + bytes)
+            cp_async_16(smem_u32(dst) + ninth * kWideRow + kRowBytes, from + ((last & ~15u) + kRowBytes));
+    } else {
+#pragma unroll 1
+        for (int i = threadIdx.x; i < rows * (kWords + 1); i += THREADS) {
+            const int row = i % rows, k = i / rows;
+            const uintptr_t start = at + row * stride * sizeof(T), part = (start & ~static_cast<uintptr_t>(15)) + k * 16;
+            uint8_t *to = dst + row * kWideRow + k * 16;
+            if (part >= lo && part + 16 <= hi && part < start + bytes)
+                cp_async_16(smem_u32(to), reinterpret_cast<const void *>(part));
+            else
+                for (uintptr_t e = k ? part : start; e < part + 16 && e < start + bytes; e += sizeof(T))
+                    *reinterpret_cast<T *>(to + (e - part)) = *reinterpret_cast<const T *>(e);
         }
     }
 }
+
+// One of the kernels' inputs: what a CTA needs to copy its tiles and to read them. FAST: the rows start on 16 bytes.
+template <typename T, int THREADS, bool FAST>
+struct Input {
+    const T *at;      // row 0, first channel of the CTA
+    int64_t stride;
+    const T *first, *end;  // the tensor
+    __device__ __forceinline__ Input(const void *p, int64_t sb, int64_t st, int b, int c0, const ScanParams &s)
+        : at(static_cast<const T *>(p) + b * sb + c0), stride(st), first(static_cast<const T *>(p)),
+          end(first + (s.B - 1) * sb + (s.T - 1) * st + s.D) {}
+    __device__ __forceinline__ void copy(uint8_t *dst, int row, int rows, int cols) const {
+        if (FAST)
+            copy_aligned<THREADS>(dst, reinterpret_cast<const uint8_t *>(at + row * stride),
+                                  static_cast<uint32_t>(stride) * sizeof(T), rows, cols * static_cast<int>(sizeof(T)));
+        else
+            copy_anywhere<T, THREADS>(dst, at + row * stride, stride, rows, cols, first, end);
+    }
+    // A lane's word of the i-th of a warp's rows, which are at `rows`. How far from a word of 16 bytes a row starts
+    // is the same for every warp and tile, as those begin sixteen rows apart: uniform registers hold it.
+    __device__ __forceinline__ uint32_t word(const uint8_t *rows, int i, int lane) const {
+        if (FAST) return reinterpret_cast<const uint32_t *>(rows + i * kRowBytes)[lane];
+        const uint32_t begin = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) +
+                               i * static_cast<uint32_t>(stride) * static_cast<uint32_t>(sizeof(T));
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(rows + i * kWideRow + (begin & 12)) + lane;
+        return sizeof(T) == 4 ? from[0] : __funnelshift_r(from[0], from[1], (begin & 2) * 8);
+    }
+    // A warp's R rows moved to where aligned rows have them.
+    template <int R>
+    __device__ __forceinline__ void realign(uint8_t *rows, int lane) const {
+        static_assert(R * sizeof(T) % 16 == 0, "rows of other warps and tiles start alike");
+        if constexpr (!FAST) {
+            uint32_t w[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) w[i] = word(rows, i, lane);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < R; ++i) reinterpret_cast<uint32_t *>(rows + i * kWideRow)[lane] = w[i];
+        }
+    }
+};
 
 // ------------------------------------------------------------------------------------------------
 // Maps h -> a h + b of N channels, and their exchange in a cluster
@@ -204,6 +262,29 @@ __device__ __forceinline__ void store_some(T *dst, const Vec<N> &v, int n) {
     for (int j = 0; j < N; ++j)
         if (j < n) dst[j] = from_f32<T>(v.v[j]);
 }
+// A row's values, one lane's at `to` each, the whole warp together. FAST: whole words on their places, and no
+// lane without its own. Otherwise 16-bit rows that start between two words are stored one element further
+// on, each lane's first with the last of the lane before it (8 x 4096 x 2047: 128 us forward and 263 backward
+// with these stores and copy_anywhere(), 199 and 341 element by element).
+template <typename T, bool FAST, int N>
+__device__ __forceinline__ void store_row(uint8_t *to, const Vec<N> &v, int lane, int n, int cols) {
+    const uint32_t w = pack<T>(v);
+    if (FAST || N == 1) {
+        if (FAST || n) *reinterpret_cast<uint32_t *>(to) = w;
+    } else if ((reinterpret_cast<uintptr_t>(to) & 2) == 0) {
+        if (n == 2)
+            *reinterpret_cast<uint32_t *>(to) = w;
+        else if (n)
+            *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(w);
+    } else {
+        const uint32_t before = __shfl_up_sync(~0u, w, 1);
+        if (n && lane)
+            *reinterpret_cast<uint32_t *>(to - 2) = __funnelshift_l(before, w, 16);
+        else if (n)
+            *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(w);
+        if (n == 2 && 2 * lane + 2 >= cols) *reinterpret_cast<uint16_t *>(to + 2) = static_cast<uint16_t>(w >> 16);
+    }
+}
 template <int N>
 __device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
 #pragma unroll
@@ -213,8 +294,8 @@ __device__ __forceinline__ void load_state(const float *src, int n, Vec<N> &v) {
 // The rows of sequence b before its padding. The loops over the tiles run to T all the same, and steps in
 // the padding skip their work between the barriers: a bound that comes from memory makes the loop one
 // of threads that might diverge, which costs a third more time. Kernels without lengths (RAGGED
-// false) and those whose rows need the slow copy (FAST false, which take lengths or none) are
-// instances of their own, as both cost the others registers.
+// false) and those whose rows start anywhere (FAST false, which take lengths or none) are instances
+// of their own, as both cost the others registers.
 template <bool RAGGED>
 __device__ __forceinline__ int sequence_length(const ScanParams &p, int b) {
     return RAGGED && p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
@@ -258,9 +339,9 @@ struct Place {
 // size. Where few channels leave each CTA many steps, a step's own latencies bound it, 1.6 us: the pass over the rows,
 // the exchange and the second pass, one after the other.
 constexpr int kFwdWarps = 4, kFwdStages = 2;
-template <int N>
+template <int N, int PITCH>  // PITCH: bytes of a tile's row
 struct FwdSmem {
-    uint8_t tile[kFwdStages][2][kTile * kRowBytes];
+    uint8_t tile[kFwdStages][2][kTile * PITCH];
     Map<N> warp[kFwdWarps][32];  // each warp's rows; then the tile's rows in front of them
     Vec<N> start[32];            // the state in front of the tile
     Exchange<N> ex;
@@ -268,10 +349,10 @@ struct FwdSmem {
 };
 
 template <typename T, int MODE, bool RAGGED, bool FAST>
-__global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_kernel(const ScanParams p) {
-    constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps;
+__global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
+    constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps, P = FAST ? kRowBytes : kWideRow;
     extern __shared__ __align__(128) uint8_t raw[];
-    FwdSmem<N> &sm = *reinterpret_cast<FwdSmem<N> *>(raw);
+    FwdSmem<N, P> &sm = *reinterpret_cast<FwdSmem<N, P> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
     if (cs > 1) {
@@ -282,11 +363,11 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
     griddep_launch_dependents();
     const int len = sequence_length<RAGGED>(p, at.b);
     const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
-    const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
-    const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
+    const Input<T, kThreads, FAST> gate(p.gate, p.gate_sb, p.gate_st, at.b, at.c0, p);
+    const Input<T, kThreads, FAST> x(p.x, p.x_sb, p.x_st, at.b, at.c0, p);
     T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
     const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
-    const bool wide = p.pair && at.n == N;
+    const bool wide = !FAST || (p.pair && at.n == N);  // store_row() takes rows that are whole in time
     Vec<N> carry = splat<N>(0.0f);  // warp 0's: the state in front of the cluster's tiles
     if (warp == 0) {
         load_state(p.state ? p.state + plane : nullptr, at.n, carry);
@@ -298,8 +379,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
     auto fetch = [&](int step) {
         const int row = (step * cs + at.rank) * kTile, rows = min(len - row, kTile);
         if (rows > 0) {
-            copy_tile<T, kThreads, FAST>(sm.tile[step % kFwdStages][0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads, FAST>(sm.tile[step % kFwdStages][1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
+            gate.copy(sm.tile[step % kFwdStages][0], row, rows, at.cols);
+            x.copy(sm.tile[step % kFwdStages][1], row, rows, at.cols);
         }
         cp_async_commit();
     };
@@ -310,8 +391,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
     for (int step = 0; step < p.steps; ++step) {
         const int tile = step * cs + at.rank, row0 = tile * kTile + warp * R;
         const bool live = !RAGGED || step * cs * kTile < len;  // some row of the cluster's tiles is no padding
-        const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * kRowBytes + lane * 4;
-        const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * kRowBytes + lane * 4;
+        const uint8_t *sg = sm.tile[step % kFwdStages][0] + warp * R * P;
+        const uint8_t *sx = sm.tile[step % kFwdStages][1] + warp * R * P;
         Vec<N> a[R], u[R];
         const bool full = row0 + R <= len;
         Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
@@ -319,8 +400,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<N> rest;
-                decay<MODE>(unpack<T>(*reinterpret_cast<const uint32_t *>(sg + i * kRowBytes)), a[i], rest);
-                u[i] = increment<MODE>(rest, unpack<T>(*reinterpret_cast<const uint32_t *>(sx + i * kRowBytes)));
+                decay<MODE>(unpack<T>(gate.word(sg, i, lane)), a[i], rest);
+                u[i] = increment<MODE>(rest, unpack<T>(x.word(sx, i, lane)));
                 if (!decltype(all_live)::value && row0 + i >= len) a[i] = splat<N>(1.0f), u[i] = splat<N>(0.0f);
                 m = compose(Map<N>{a[i], u[i]}, m);
             }
@@ -362,7 +443,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
-                *reinterpret_cast<uint32_t *>(to + off) = pack<T>(h);
+                store_row<T, FAST>(to + off, h, lane, at.n, at.cols);
                 off += off_row;
             }
         } else if (row0 < len) {
@@ -393,9 +474,9 @@ __global__ void __launch_bounds__(32 * kFwdWarps, FAST ? 4 : 3) based_scan_fwd_k
 // reads and writes its own words alone). Eight rows a thread and twice the warps took 489 us where this takes
 // 437 (8 x 16384 x 2048, log decays, 92 % of the floor).
 constexpr int kBwdWarps = 4, kBwdStages = 2;
-template <int N>
+template <int N, int PITCH>
 struct BwdSmem {
-    uint8_t tile[kBwdStages][3][kTile * kRowBytes];
+    uint8_t tile[kBwdStages][3][kTile * PITCH];
     Map<N> warp[kBwdWarps][32];
     Vec<N> rev[kBwdWarps][32];   // the reversed map's increment
     Vec<N> start[32], mu[32];    // the state in front of the tile, mu behind it
@@ -405,9 +486,9 @@ struct BwdSmem {
 
 template <typename T, int MODE, bool RAGGED, bool FAST>
 __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_kernel(const ScanParams p) {
-    constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps;
+    constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps, P = FAST ? kRowBytes : kWideRow;
     extern __shared__ __align__(128) uint8_t raw[];
-    BwdSmem<N> &sm = *reinterpret_cast<BwdSmem<N> *>(raw);
+    BwdSmem<N, P> &sm = *reinterpret_cast<BwdSmem<N, P> *>(raw);
     const Place<T> at(p);
     const int lane = at.lane, warp = at.warp, cs = p.cluster;
     if (cs > 1) {
@@ -418,13 +499,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
     griddep_launch_dependents();
     const int len = sequence_length<RAGGED>(p, at.b);
     const int64_t plane = static_cast<int64_t>(at.b) * p.D + at.c;
-    const T *gate = static_cast<const T *>(p.gate) + at.b * p.gate_sb + at.c0;
-    const T *x = static_cast<const T *>(p.x) + at.b * p.x_sb + at.c0;
-    const T *dy = static_cast<const T *>(p.dy) + at.b * p.dy_sb + at.c0;
+    const Input<T, kThreads, FAST> gate(p.gate, p.gate_sb, p.gate_st, at.b, at.c0, p);
+    const Input<T, kThreads, FAST> x(p.x, p.x_sb, p.x_st, at.b, at.c0, p);
+    const Input<T, kThreads, FAST> dy(p.dy, p.dy_sb, p.dy_st, at.b, at.c0, p);
     T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
     T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D;
     const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
-    const bool wide = p.pair && at.n == N;
+    const bool wide = !FAST || (p.pair && at.n == N);  // store_row() takes rows that are whole in time
     Vec<N> carry = splat<N>(0.0f);  // warp 1's: mu behind the cluster's tiles
     if (warp == 1) load_state(p.state ? p.state + plane : nullptr, at.n, carry);
     bool waiting = true;
@@ -433,10 +514,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
     auto fetch = [&](int step) {
         const int row = tile_of(step) * kTile, rows = min(len - row, kTile);
         if (row >= 0 && rows > 0) {
-            uint8_t(*to)[kTile * kRowBytes] = sm.tile[step % kBwdStages];
-            copy_tile<T, kThreads, FAST>(to[0], gate + row * p.gate_st, p.gate_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads, FAST>(to[1], x + row * p.x_st, p.x_st, rows, at.cols, p.word);
-            copy_tile<T, kThreads, FAST>(to[2], dy + row * p.dy_st, p.dy_st, rows, at.cols, p.word);
+            uint8_t(*to)[kTile * P] = sm.tile[step % kBwdStages];
+            gate.copy(to[0], row, rows, at.cols);
+            x.copy(to[1], row, rows, at.cols);
+            dy.copy(to[2], row, rows, at.cols);
         }
         cp_async_commit();
     };
@@ -453,9 +534,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
         cp_async_wait<0>();
         __syncthreads();  // the tile has landed, and the other stage is free
         fetch(step + 1);
-        uint8_t *sg = sm.tile[step % kBwdStages][0] + warp * R * kRowBytes + lane * 4;
-        uint8_t *sx = sg + kTile * kRowBytes, *sd = sx + kTile * kRowBytes;
-        auto word = [&](uint8_t *s, int i) -> uint32_t & { return *reinterpret_cast<uint32_t *>(s + i * kRowBytes); };
+        x.template realign<R>(sm.tile[step % kBwdStages][1] + warp * R * P, lane);
+        dy.template realign<R>(sm.tile[step % kBwdStages][2] + warp * R * P, lane);
+        uint8_t *sg = sm.tile[step % kBwdStages][0] + warp * R * P + lane * 4;
+        uint8_t *sx = sg + kTile * P, *sd = sx + kTile * P;
+        auto word = [&](uint8_t *s, int i) -> uint32_t & { return *reinterpret_cast<uint32_t *>(s + i * P); };
         const bool full = tile >= 0 && row0 + R <= len, some = tile >= 0 && row0 < len;
         Vec<N> a[R], other[R], rev = splat<N>(0.0f);  // other: 1 - a, or the states in front of the rows
         Map<N> m = {splat<N>(1.0f), splat<N>(0.0f)};
@@ -463,7 +546,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<N> rest;
-                decay<MODE>(unpack<T>(word(sg, i)), a[i], rest);
+                decay<MODE>(unpack<T>(gate.word(sg - lane * 4, i, lane)), a[i], rest);
                 if (!decltype(all_live)::value && row0 + i >= len) {
                     a[i] = splat<N>(1.0f), rest = splat<N>(0.0f);
                     word(sx, i) = word(sd, i) = 0;
@@ -543,8 +626,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
                         ox = vmul(other[i], lam);
                     }
                     if (decltype(all_live)::value) {
-                        *reinterpret_cast<uint32_t *>(to_g + off) = pack<T>(og);
-                        *reinterpret_cast<uint32_t *>(to_x + off) = pack<T>(ox);
+                        store_row<T, FAST>(to_g + off, og, lane, at.n, at.cols);
+                        store_row<T, FAST>(to_x + off, ox, lane, at.n, at.cols);
                     } else if (row0 + i < p.T) {
                         store_some(reinterpret_cast<T *>(to_g + off), row0 + i < len ? og : splat<N>(0.0f), at.n);
                         store_some(reinterpret_cast<T *>(to_x + off), row0 + i < len ? ox : splat<N>(0.0f), at.n);
@@ -723,36 +806,44 @@ int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms,
 template <typename T>
 int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
     constexpr int kLog = BASED_GATE_LOG, kSig = BASED_GATE_SIGMOID;
-    const bool log = mode == BASED_GATE_LOG, fast = p.word != 0, ragged = p.lengths;
+    const bool log = mode == BASED_GATE_LOG, fast = p.fast != 0, ragged = p.lengths;
+    const StepCost fwd_cost = {1.6, 3.0 * kTile * kRowBytes, 6.7e6, 0.02}, bwd_cost = {2.6, 5.0 * kTile * kRowBytes, 6.6e6, 0.03};
+    constexpr int N = Place<T>::N;
     if (bwd) {
+        if (!fast)
+            return launch_scan<T, BwdSmem<N, kWideRow>>(
+                p, log ? based_scan_bwd_kernel<T, kLog, true, false> : based_scan_bwd_kernel<T, kSig, true, false>,
+                32 * kBwdWarps, sms, bwd_cost, st);
         void (*const k)(ScanParams) =
-            !fast    ? (log ? based_scan_bwd_kernel<T, kLog, true, false> : based_scan_bwd_kernel<T, kSig, true, false>)
-            : ragged ? (log ? based_scan_bwd_kernel<T, kLog, true, true> : based_scan_bwd_kernel<T, kSig, true, true>)
-                     : (log ? based_scan_bwd_kernel<T, kLog, false, true> : based_scan_bwd_kernel<T, kSig, false, true>);
-        return launch_scan<T, BwdSmem<Place<T>::N>>(p, k, 32 * kBwdWarps, sms,
-                                                     {2.6, 5.0 * kTile * kRowBytes, 6.6e6, 0.03}, st);
+            ragged ? (log ? based_scan_bwd_kernel<T, kLog, true, true> : based_scan_bwd_kernel<T, kSig, true, true>)
+                   : (log ? based_scan_bwd_kernel<T, kLog, false, true> : based_scan_bwd_kernel<T, kSig, false, true>);
+        return launch_scan<T, BwdSmem<N, kRowBytes>>(p, k, 32 * kBwdWarps, sms, bwd_cost, st);
     }
+    if (!fast)
+        return launch_scan<T, FwdSmem<N, kWideRow>>(
+            p, log ? based_scan_fwd_kernel<T, kLog, true, false> : based_scan_fwd_kernel<T, kSig, true, false>,
+            32 * kFwdWarps, sms, fwd_cost, st);
     void (*const k)(ScanParams) =
-        !fast    ? (log ? based_scan_fwd_kernel<T, kLog, true, false> : based_scan_fwd_kernel<T, kSig, true, false>)
-        : ragged ? (log ? based_scan_fwd_kernel<T, kLog, true, true> : based_scan_fwd_kernel<T, kSig, true, true>)
-                 : (log ? based_scan_fwd_kernel<T, kLog, false, true> : based_scan_fwd_kernel<T, kSig, false, true>);
-    return launch_scan<T, FwdSmem<Place<T>::N>>(p, k, 32 * kFwdWarps, sms,
-                                                 {1.6, 3.0 * kTile * kRowBytes, 6.7e6, 0.02}, st);
+        ragged ? (log ? based_scan_fwd_kernel<T, kLog, true, true> : based_scan_fwd_kernel<T, kSig, true, true>)
+               : (log ? based_scan_fwd_kernel<T, kLog, false, true> : based_scan_fwd_kernel<T, kSig, false, true>);
+    return launch_scan<T, FwdSmem<N, kRowBytes>>(p, k, 32 * kFwdWarps, sms, fwd_cost, st);
 }
 
 int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream) {
     int rc = check_scan(p, dtype, mode, bwd), sms;
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    // the widest word that every row of every input starts on, and ends on
     const int64_t es = static_cast<int64_t>(elem_size(dtype));
     const int64_t bits = (p.D | p.gate_sb | p.gate_st | p.x_sb | p.x_st | p.dy_sb | p.dy_st) * es |
                          static_cast<int64_t>(reinterpret_cast<uintptr_t>(p.gate) | reinterpret_cast<uintptr_t>(p.x) |
                                               reinterpret_cast<uintptr_t>(p.dy));
-    // (8 x 3000 x 1536: 37 us forward and 62 us backward by words of 16 bytes, 50 and 92 by words of 4)
     const bool near = (p.gate_st | p.x_st | p.dy_st) < (1 << 24);  // a tile's rows within 2^32 bytes
-    p.word = !near ? 0 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
-    p.pair = p.D % 2 == 0 && aligned(p.y, 4) && aligned(p.dx, 4);
+    // (8 x 4096 x 2048 and 2047 bfloat16: 67 + 117 us forward and backward by aligned words, 128 + 263 by shifted ones, 199
+    // + 341 element by element. Rows of 4-byte words are copied as rows that start anywhere, too: by such words
+    // 2 x 2047 x 777 float32 takes 14.2 + 21.6 us, here 11.5 + 18.2, and 8 x 4096 x 1023 95 + 230, here 85 + 145;
+    // 2 x 4096 x 1022 bfloat16 alone would be faster, 19.4 + 35.6 where this takes 21.3 + 38.1.)
+    p.fast = bits % 16 == 0 && near;
+    p.pair = es == 4 || (p.D % 2 == 0 && aligned(p.y, 4) && aligned(p.dx, 4));
     if (dtype == BASED_F32) return launch_scan<float>(p, mode, bwd, sms, st);
     if (dtype == BASED_BF16) return launch_scan<__nv_bfloat16>(p, mode, bwd, sms, st);
     return launch_scan<__half>(p, mode, bwd, sms, st);

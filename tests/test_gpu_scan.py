@@ -271,6 +271,20 @@ def test_offsets_past_32_bits(cuda_device):
     assert torch.equal(y[0, -1], y[0, 1 << 20]) and torch.equal(y[0, (1 << 24) + 3], y[0, -1])
 
 
+@pytest.mark.parametrize("dtype,D", [(BF16, 34), (BF16, 35), (F32, 33), (F16, 31)])
+def test_many_rows_that_start_anywhere(dtype, D, cuda_device):
+    # as many tiles as fill the GPU, of rows that no 16-byte word starts on; between them, NaN
+    B, T = 320, 660
+    for mode in ("log", "sigmoid"):
+        g, x, dy, state, dfinal = draw(B, T, D, mode, dtype, 18)
+        lengths = torch.arange(B, dtype=torch.int32, device="cuda") * T // (B - 1)
+        for lens in (None, lengths):
+            check(g, x, dy, state, dfinal, mode, lens, what=(dtype, D, mode))
+        wide = torch.full((B, T, D + 5), float("nan"), dtype=dtype, device="cuda")
+        wide[:, :, 3:3 + D] = x
+        check(g, wide[:, :, 3:3 + D], dy, state, dfinal, mode, lengths, what=(dtype, D, mode, "inner"))
+
+
 def test_rows_far_apart(cuda_device):
     # rows 2^24 elements apart: a tile's rows span more than 2^32 bytes
     D, T, far = 40, 130, 1 << 24
