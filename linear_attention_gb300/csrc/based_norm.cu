@@ -39,13 +39,15 @@ __device__ __forceinline__ float load_param(const void *p, int dtype, int i, flo
     return to_f32(static_cast<const __half *>(p)[i]);
 }
 
-// Eight channels of a row. VEC: consecutive ones, loaded as 16-byte words; otherwise channels
-// l, l + tpg, ... of the group. n: the channels of the group from this thread's first on. A load
-// leaves what the thread does not hold as it is (zero from clear()).
-template <typename T, bool VEC>
+// Eight channels of a row, by what lies in a word. kOctets: consecutive ones, loaded as 16-byte words. kPairs:
+// pairs of neighbours, tpg pairs apart. kSingles: channels l, l + tpg, ... of the group.
+// `held`: a bit for each that the thread holds. A load leaves what the thread does not hold as it
+// is (zero from clear()).
+enum Words { kSingles, kPairs, kOctets };
+template <typename T, Words W>
 struct Row;
 template <typename T>
-struct Row<T, true> {
+struct Row<T, kOctets> {
     static constexpr int kQuads = sizeof(T) * kElems / 16;
     uint32_t w[kQuads * 4];
     __device__ __forceinline__ void clear() {
@@ -54,18 +56,86 @@ struct Row<T, true> {
     }
     // ONCE: the data is not kept in L2 over what others read again
     template <bool ONCE>
-    __device__ __forceinline__ void load(const T *p, int n, int) {
+    __device__ __forceinline__ void load(const T *p, unsigned held, int) {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
-            if (n <= 0) continue;
+            if (!held) continue;
             const uint4 *at = reinterpret_cast<const uint4 *>(p) + k, q = ONCE ? __ldcs(at) : *at;
             w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
         }
     }
-    __device__ __forceinline__ void store(T *p, int n, int) const {
+    __device__ __forceinline__ void store(T *p, unsigned held, int) const {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k)
-            if (n > 0) reinterpret_cast<uint4 *>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            if (held) reinterpret_cast<uint4 *>(p)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+    __device__ __forceinline__ void keep(unsigned) {}
+    __device__ __forceinline__ Vec<2> get(int k) const {
+        if constexpr (sizeof(T) == 4)
+            return {{__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])}};
+        else
+            return unpack<T>(w[k]);
+    }
+    __device__ __forceinline__ void set(int k, const Vec<2> &v) {
+        if constexpr (sizeof(T) == 4)
+            w[2 * k] = __float_as_uint(v.v[0]), w[2 * k + 1] = __float_as_uint(v.v[1]);
+        else
+            w[k] = pack<T>(v);
+    }
+};
+// A pair at the start or the end of a group may have one half in the next group. It is loaded whole, as the row goes
+// on there, and keep() clears the half; a store leaves it alone.
+template <typename T>
+struct Row<T, kPairs> {
+    static constexpr int kPairWords = sizeof(T) / 2;
+    uint32_t w[kElems / 2 * kPairWords];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kElems / 2 * kPairWords; ++k) w[k] = 0;
+    }
+    template <bool ONCE>
+    __device__ __forceinline__ void load(const T *p, unsigned held, int tpg) {
+#pragma unroll
+        for (int k = 0; k < kElems / 2; ++k) {
+            if (!(held >> (2 * k) & 3)) continue;
+            const T *from = p + k * 2 * tpg;
+            if constexpr (sizeof(T) == 4) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(from);
+                w[2 * k] = q.x, w[2 * k + 1] = q.y;
+            } else {
+                w[k] = *reinterpret_cast<const uint32_t *>(from);
+            }
+        }
+    }
+    __device__ __forceinline__ void keep(unsigned held) {
+#pragma unroll
+        for (int k = 0; k < kElems / 2; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                if (!(held >> (2 * k) & 1)) w[2 * k] = 0;
+                if (!(held >> (2 * k) & 2)) w[2 * k + 1] = 0;
+            } else {
+                if (!(held >> (2 * k) & 1)) w[k] &= 0xffff0000u;
+                if (!(held >> (2 * k) & 2)) w[k] &= 0xffffu;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *p, unsigned held, int tpg) const {
+#pragma unroll
+        for (int k = 0; k < kElems / 2; ++k) {
+            const unsigned both = held >> (2 * k) & 3;
+            T *to = p + k * 2 * tpg;
+            if constexpr (sizeof(T) == 4) {
+                if (both == 3)
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(w[2 * k], w[2 * k + 1]);
+                else if (both)
+                    *reinterpret_cast<uint32_t *>(to + (both >> 1)) = both & 1 ? w[2 * k] : w[2 * k + 1];
+            } else {
+                if (both == 3)
+                    *reinterpret_cast<uint32_t *>(to) = w[k];
+                else if (both)
+                    *reinterpret_cast<uint16_t *>(to + (both >> 1)) = static_cast<uint16_t>(both & 1 ? w[k] : w[k] >> 16);
+            }
+        }
     }
     __device__ __forceinline__ Vec<2> get(int k) const {
         if constexpr (sizeof(T) == 4)
@@ -81,22 +151,23 @@ struct Row<T, true> {
     }
 };
 template <typename T>
-struct Row<T, false> {
+struct Row<T, kSingles> {
     T w[kElems];
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int k = 0; k < kElems; ++k) w[k] = from_f32<T>(0.0f);
     }
     template <bool ONCE>
-    __device__ __forceinline__ void load(const T *p, int n, int step) {
+    __device__ __forceinline__ void load(const T *p, unsigned held, int tpg) {
 #pragma unroll
         for (int k = 0; k < kElems; ++k)
-            if (k * step < n) w[k] = p[k * step];
+            if (held >> k & 1) w[k] = p[k * tpg];
     }
-    __device__ __forceinline__ void store(T *p, int n, int step) const {
+    __device__ __forceinline__ void keep(unsigned) {}
+    __device__ __forceinline__ void store(T *p, unsigned held, int tpg) const {
 #pragma unroll
         for (int k = 0; k < kElems; ++k)
-            if (k * step < n) p[k * step] = w[k];
+            if (held >> k & 1) p[k * tpg] = w[k];
     }
     __device__ __forceinline__ Vec<2> get(int k) const { return {{to_f32(w[2 * k]), to_f32(w[2 * k + 1])}}; }
     __device__ __forceinline__ void set(int k, const Vec<2> &v) {
@@ -161,20 +232,26 @@ __device__ __forceinline__ void with_act(int act, F f) {
 
 // Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
 // and dbias, 80 (100 where x is float32): weight and bias wait in shared memory, four 16-byte reads a
-// row. Channel by channel (VEC false) they take 85 and 128. BIG ones may have 512 threads.
-template <typename TX, typename TY, bool VEC, bool GATED, bool BWD, bool BIG>
-__global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : VEC ? (BWD ? (sizeof(TX) == 4 ? 5 : 6) : 4) : (BWD ? 2 : 3))
+// row. By pairs and singles they take up to 85 and 128. BIG ones may have 512 threads.
+template <typename TX, typename TY, Words W, bool GATED, bool BWD, bool BIG>
+__global__ void __launch_bounds__(BIG ? 512 : W == kOctets && BWD ? 128 : 256, BIG ? 1 : W == kOctets ? (BWD ? (sizeof(TX) == 4 ? 5 : 6) : 4) : (BWD ? 2 : 3))
     based_norm_kernel(const NormParams p) {
     constexpr int P = kElems / 2;
+    constexpr bool VEC = W == kOctets;
     extern __shared__ __align__(16) float smem[];
     const int slot = threadIdx.x / p.tpg, l = threadIdx.x % p.tpg;
     const int r = slot / p.gpb, g = blockIdx.y * p.gpb + slot % p.gpb;
-    const int first = VEC ? l * kElems : l, step = p.tpg, per = p.gpb * p.tpg;
+    const int per = p.gpb * p.tpg;
     const bool on = r < p.rp && g < p.G;
-    const int n = on ? p.Cg - first : 0;  // > 0: this thread holds channels
+    // pairs start on even channels: in a group that starts on an odd one with the channel before it
+    const int first = W == kOctets ? l * kElems : W == kPairs ? 2 * l - (g * p.Cg & 1) : l;
+    auto place = [&](int i) { return W == kOctets ? i : W == kPairs ? i / 2 * 2 * p.tpg + i % 2 : i * p.tpg; };
+    unsigned held = 0;
+#pragma unroll
+    for (int i = 0; i < kElems; ++i)
+        if (on && first + place(i) >= 0 && first + place(i) < p.Cg) held |= 1u << i;
     const int64_t c = static_cast<int64_t>(g) * p.Cg + first;
     const float inv = 1.0f / p.Cg;
-    auto holds = [&](int i, int m) { return VEC ? m > 0 : i * step < m; };  // element i of a row with m channels
     griddep_wait();
     griddep_launch_dependents();
     // (4, per) quads: elements 0-3 and 4-7 of the weights, then of the biases, of a row's threads
@@ -186,8 +263,8 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
             float v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int i = (q & 1) * 4 + j, o = static_cast<int>(c) + (VEC ? i : i * step);
-                v[j] = holds(i, n) ? load_param(q < 2 ? p.weight : p.bias, p.p_dtype, o, q < 2 ? 1.0f : 0.0f) : 0.0f;
+                const int i = (q & 1) * 4 + j, o = static_cast<int>(c) + place(i);
+                v[j] = held >> i & 1 ? load_param(q < 2 ? p.weight : p.bias, p.p_dtype, o, q < 2 ? 1.0f : 0.0f) : 0.0f;
             }
             params[q * per + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
         }
@@ -196,8 +273,8 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
 #pragma unroll
     for (int k = 0; k < P; ++k) dw[k] = db[k] = splat<2>(0.0f);
     // the next row is loaded while a row is worked on
-    Row<TX, VEC> nx;
-    Row<TY, VEC> nz, nd;
+    Row<TX, W> nx;
+    Row<TY, W> nz, nd;
     nx.clear(), nz.clear(), nd.clear();
     const int64_t turn = static_cast<int64_t>(gridDim.x) * p.rp;
     int64_t row = static_cast<int64_t>(blockIdx.x) * p.rp + r;
@@ -206,26 +283,29 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
     int64_t out = row * p.C + c;
     // past the last row the registers keep an earlier one
     auto fetch = [&] {
-        const int m = row < p.R ? n : 0;
+        const unsigned m = row < p.R ? held : 0;
         // streaming loads forward (16384 x 1024, float32 in: 23.3 to 18.7 us), ordinary ones backward (they
         // take 67 us there, streaming ones 69)
-        nx.template load<!BWD>(px, m, step);
-        if (GATED) nz.template load<!BWD>(pz, m, step);
-        if (BWD) nd.template load<!BWD>(pd, m, step);
+        nx.template load<!BWD>(px, m, p.tpg);
+        if (GATED) nz.template load<!BWD>(pz, m, p.tpg);
+        if (BWD) nd.template load<!BWD>(pd, m, p.tpg);
     };
     fetch();
     __syncthreads();
     // every thread takes part in the sums of every turn: the bound is the CTA's first row
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * p.rp; base < p.R; base += turn) {
-        const Row<TX, VEC> rx = nx;
-        Row<TY, VEC> rz, rd;
+        Row<TX, W> rx = nx;
+        Row<TY, W> rz, rd;
         if (GATED) rz = nz;
         if (BWD) rd = nd;
-        const int mh = row < p.R ? n : 0;
+        const unsigned mh = row < p.R ? held : 0;
+        rx.keep(held);
+        if (GATED) rz.keep(held);
+        if (BWD) rd.keep(held);
         row += turn;
         px += turn * p.x_sr, pz += turn * p.gate_sr, pd += turn * p.dy_sr;
         fetch();
-        if (BWD && mh <= 0) rd.clear();  // adds nothing to dweight and dbias
+        if (BWD && !mh) rd.clear();  // adds nothing to dweight and dbias
         Vec<2> h[P], sq[P];
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = rx.get(k);
@@ -236,22 +316,22 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
         for (int k = 0; k < P; ++k) {
             h[k] = vadd(h[k], mean);
             if (!VEC) {
-                if (!holds(2 * k, mh)) h[k].v[0] = 0.0f;
-                if (!holds(2 * k + 1, mh)) h[k].v[1] = 0.0f;
+                if (!(mh >> (2 * k) & 1)) h[k].v[0] = 0.0f;
+                if (!(mh >> (2 * k) & 2)) h[k].v[1] = 0.0f;
             }
             sq[k] = vmul(h[k], h[k]);
         }
         float s2[1] = {total(sq)};
-        if (VEC && mh <= 0) s2[0] = 0.0f;
+        if (VEC && !mh) s2[0] = 0.0f;
         group_sum<1, BIG>(s2, p.tpg, smem + 16);
         // a thread without channels scales by 0, so that nothing it adds to a sum is NaN where eps is 0
-        const float rstd = mh > 0 ? rsqrtf(fmaf(s2[0], inv, p.eps)) : 0.0f;
+        const float rstd = mh ? rsqrtf(fmaf(s2[0], inv, p.eps)) : 0.0f;
         auto param = [&](int k, int which) {  // pair k of the weights (0) or biases (1)
             const float4 q = mine[(2 * which + k / 2) * per];
             return k % 2 ? Vec<2>{{q.z, q.w}} : Vec<2>{{q.x, q.y}};
         };
         if (!BWD) {
-            Row<TY, VEC> ry;
+            Row<TY, W> ry;
             with_act(p.act, [&](auto act) {
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
@@ -261,10 +341,10 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
                     ry.set(k, GATED ? vmul(v, f) : f);
                 }
             });
-            ry.store(static_cast<TY *>(p.y) + out, mh, step);
+            ry.store(static_cast<TY *>(p.y) + out, mh, p.tpg);
         } else {
-            Row<TY, VEC> oz;
-            Row<TX, VEC> ox;
+            Row<TY, W> oz;
+            Row<TX, W> ox;
             Vec<2> q[P], s0 = splat<2>(0.0f), sh = splat<2>(0.0f);
             with_act(p.act, [&](auto act) {
 #pragma unroll
@@ -282,13 +362,13 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
                     sh = vfma(q[k], h[k], sh);
                 }
             });
-            if (GATED) oz.store(static_cast<TY *>(p.dgate) + out, mh, step);
+            if (GATED) oz.store(static_cast<TY *>(p.dgate) + out, mh, p.tpg);
             float s[2] = {s0.v[0] + s0.v[1], sh.v[0] + sh.v[1]};
             group_sum<2, BIG>(s, p.tpg, smem + 32);
             const Vec<2> m0 = splat<2>(-s[0] * inv), m1 = splat<2>(-s[1] * inv), scale = splat<2>(rstd);
 #pragma unroll
             for (int k = 0; k < P; ++k) ox.set(k, vmul(scale, vfma(h[k], m1, vadd(q[k], m0))));
-            ox.store(static_cast<TX *>(p.dx) + out, mh, step);
+            ox.store(static_cast<TX *>(p.dx) + out, mh, p.tpg);
         }
         out += turn * p.C;
     }
@@ -317,8 +397,8 @@ __global__ void __launch_bounds__(BIG ? 512 : VEC && BWD ? 128 : 256, BIG ? 1 : 
         if (r == 0) {
 #pragma unroll
             for (int i = 0; i < kElems; ++i) {
-                const int o = VEC ? i : i * step;
-                if (holds(i, n)) {
+                const int o = place(i);
+                if (held >> i & 1) {
                     part[c + o] = dw[i / 2].v[i % 2];
                     part[p.C + c + o] = db[i / 2].v[i % 2];
                 }
@@ -428,34 +508,36 @@ int check_norm(const NormParams &p, int x_dtype, int dtype, bool bwd, const void
     return BASED_OK;
 }
 
-template <typename TX, typename TY, bool BWD>
-int launch_norm(const NormParams &p, const NormShape &s, bool vec, cudaStream_t st) {
+template <typename TX, typename TY, bool BWD, Words W>
+int launch_norm(const NormParams &p, const NormShape &s, cudaStream_t st) {
     const dim3 grid(s.grid_x, s.grid_y);
     // the sums' 64 floats, weight and bias, and where rows lie side by side their dweight and dbias
     const size_t smem = (64 + (BWD && s.rp > 1 ? 4 : 2) * kElems * s.gpb * s.tpg) * sizeof(float);
     void (*kernel)(NormParams);
-    if (!vec && s.tpg > 32)
-        kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, true> : based_norm_kernel<TX, TY, false, false, BWD, true>;
-    else if (!vec)
-        kernel = p.gate ? based_norm_kernel<TX, TY, false, true, BWD, false> : based_norm_kernel<TX, TY, false, false, BWD, false>;
-    else if (s.tpg > 32)
-        kernel = p.gate ? based_norm_kernel<TX, TY, true, true, BWD, true> : based_norm_kernel<TX, TY, true, false, BWD, true>;
+    if (s.tpg > 32)
+        kernel = p.gate ? based_norm_kernel<TX, TY, W, true, BWD, true> : based_norm_kernel<TX, TY, W, false, BWD, true>;
     else
-        kernel = p.gate ? based_norm_kernel<TX, TY, true, true, BWD, false> : based_norm_kernel<TX, TY, true, false, BWD, false>;
+        kernel = p.gate ? based_norm_kernel<TX, TY, W, true, BWD, false> : based_norm_kernel<TX, TY, W, false, BWD, false>;
     OPS_CUDA(launch_op(kernel, grid, s.threads, smem, st, p));
     return BASED_OK;
 }
+template <typename TX, typename TY, bool BWD>
+int launch_norm(const NormParams &p, const NormShape &s, Words w, cudaStream_t st) {
+    if (w == kOctets) return launch_norm<TX, TY, BWD, kOctets>(p, s, st);
+    if (w == kPairs) return launch_norm<TX, TY, BWD, kPairs>(p, s, st);
+    return launch_norm<TX, TY, BWD, kSingles>(p, s, st);
+}
 
 template <bool BWD>
-int dispatch_norm(const NormParams &p, const NormShape &s, bool vec, int x_dtype, int dtype, cudaStream_t st) {
+int dispatch_norm(const NormParams &p, const NormShape &s, Words w, int x_dtype, int dtype, cudaStream_t st) {
     using bf = __nv_bfloat16;
     if (x_dtype == BASED_F32) {
-        if (dtype == BASED_F32) return launch_norm<float, float, BWD>(p, s, vec, st);
-        if (dtype == BASED_BF16) return launch_norm<float, bf, BWD>(p, s, vec, st);
-        return launch_norm<float, __half, BWD>(p, s, vec, st);
+        if (dtype == BASED_F32) return launch_norm<float, float, BWD>(p, s, w, st);
+        if (dtype == BASED_BF16) return launch_norm<float, bf, BWD>(p, s, w, st);
+        return launch_norm<float, __half, BWD>(p, s, w, st);
     }
-    if (dtype == BASED_BF16) return launch_norm<bf, bf, BWD>(p, s, vec, st);
-    return launch_norm<__half, __half, BWD>(p, s, vec, st);
+    if (dtype == BASED_BF16) return launch_norm<bf, bf, BWD>(p, s, w, st);
+    return launch_norm<__half, __half, BWD>(p, s, w, st);
 }
 
 NormParams norm_params(const void *x, int64_t x_sr, const void *gate, int64_t gate_sr, const void *weight,
@@ -467,13 +549,17 @@ NormParams norm_params(const void *x, int64_t x_sr, const void *gate, int64_t ga
     return p;
 }
 
-// 16-byte words where every group of every row starts on one (24000 x 1536: 40 us forward and 66 us
-// backward, 63 and 117 channel by channel)
-bool vector_rows(const NormParams &p, int x_dtype, int dtype) {
-    auto wide = [](const void *q, int64_t sr, size_t e) { return aligned(q, 16) && sr * e % 16 == 0; };
+// The widest words on which every group of every row starts (pairs: on, or on the second half of one).
+// 24000 x 1536 in 12 groups takes 40 us forward and 66 us backward by octets, 63 and 117 by singles; 24000 x 1500,
+// whose groups of 125 start on even and odd channels, 57 and 105 by pairs, 65 and 119 by singles.
+Words row_words(const NormParams &p, int x_dtype, int dtype) {
     const size_t xs = elem_size(x_dtype), es = elem_size(dtype);
-    return p.C / p.G % kElems == 0 && wide(p.x, p.x_sr, xs) && wide(p.gate, p.gate_sr, es) && wide(p.dy, p.dy_sr, es) &&
-           aligned(p.y, 16) && aligned(p.dx, 16) && aligned(p.dgate, 16);
+    auto on = [&](size_t x_bytes, size_t bytes) {
+        auto row = [](const void *q, int64_t sr, size_t e, size_t b) { return !q || (aligned(q, b) && sr * e % b == 0); };
+        return row(p.x, p.x_sr, xs, x_bytes) && row(p.gate, p.gate_sr, es, bytes) && row(p.dy, p.dy_sr, es, bytes) &&
+               row(p.y, p.C, es, bytes) && row(p.dx, p.C, xs, x_bytes) && row(p.dgate, p.C, es, bytes);
+    };
+    return p.C / p.G % kElems == 0 && on(16, 16) ? kOctets : on(2 * xs, 2 * es) ? kPairs : kSingles;
 }
 
 void place(NormParams &p, const NormShape &s) {
@@ -494,10 +580,10 @@ int based_norm_fwd(const void *x, int64_t x_sr, int x_dtype, const void *gate, i
     p.y = y;
     int sms, rc = check_norm(p, x_dtype, dtype, false, nullptr, nullptr);
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
-    const bool vec = vector_rows(p, x_dtype, dtype);
-    const NormShape s = norm_shape(R, C, G, sms, false, vec, x_dtype == BASED_F32);
+    const Words w = row_words(p, x_dtype, dtype);
+    const NormShape s = norm_shape(R, C, G, sms, false, w == kOctets, x_dtype == BASED_F32);
     place(p, s);
-    return dispatch_norm<false>(p, s, vec, x_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
+    return dispatch_norm<false>(p, s, w, x_dtype, dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t based_norm_bwd_workspace_size(int64_t R, int C, int G) {
@@ -522,8 +608,8 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
     p.dy = dy, p.dy_sr = dy_sr, p.dx = dx, p.dgate = dgate;
     int sms, rc = check_norm(p, x_dtype, dtype, true, dweight, dbias);
     if (rc != BASED_OK || (rc = host_device(&sms)) != BASED_OK) return rc;
-    const bool vec = vector_rows(p, x_dtype, dtype);
-    const NormShape s = norm_shape(R, C, G, sms, true, vec, x_dtype == BASED_F32);
+    const Words w = row_words(p, x_dtype, dtype);
+    const NormShape s = norm_shape(R, C, G, sms, true, w == kOctets, x_dtype == BASED_F32);
     place(p, s);
     const bool sums = dweight || dbias;
     if (sums) {
@@ -541,7 +627,7 @@ int based_norm_bwd(const void *dy, int64_t dy_sr, const void *x, int64_t x_sr, i
         p.partial = static_cast<float *>(workspace);
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((rc = dispatch_norm<true>(p, s, vec, x_dtype, dtype, st)) != BASED_OK || !sums) return rc;
+    if ((rc = dispatch_norm<true>(p, s, w, x_dtype, dtype, st)) != BASED_OK || !sums) return rc;
     const NormSumParams q = {p.partial, s.grid_x, C, p_dtype, dweight, dbias};
     OPS_CUDA(launch_op(based_norm_sum_kernel, dim3((2 * C + 31) / 32), 32 * kSumWarps, 0, st, q));
     return BASED_OK;

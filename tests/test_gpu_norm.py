@@ -115,6 +115,35 @@ def test_extreme_gates_and_nan(cuda_device):
     assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("xt,yt", PAIRS, ids=[f"{str(a)[6:]}-{str(b)[6:]}" for a, b in PAIRS])
+def test_groups_that_end_inside_a_word(xt, yt, cuda_device):
+    # groups of odd size: what a neighbour's channels hold is in the same word and stays out
+    inf = float("inf")
+    for C, G in ((6, 2), (20, 4), (50, 2), (250, 2), (1000, 8), (1026, 2)):
+        n = C // G
+        x, gate, w, b, dy = draw(37, C, xt, yt, F32, True, C)
+        check(x, gate, w, b, dy, G, "silu", what=(C, G))
+        check(x[1:], gate[1:], w, b, dy[1:], G, "none", what=(C, G))
+        check(x, None, w, b, dy, G, "sigmoid", what=(C, G))
+        want = based_norm_fwd(x, G, w, b, gate), *based_norm_bwd(dy, x, G, w, b, gate)
+        bad = torch.zeros(C, dtype=torch.bool, device="cuda")
+        bad[n:2 * n] = True
+        for k, t in enumerate((x, gate, dy)):
+            t = t.clone()
+            t[3, n], t[3, 2 * n - 1], t[36, n:2 * n] = inf, float("nan"), float("nan")
+            args = [t if k == j else o for j, o in enumerate((x, gate, dy))]
+            got = based_norm_fwd(args[0], G, w, b, args[1]), *based_norm_bwd(args[2], args[0], G, w, b, args[1])
+            for p, q in zip(got, want):
+                assert torch.equal(p[..., ~bad], q[..., ~bad]), (C, G, k)
+        if xt == yt:
+            y = want[0]
+            assert torch.equal(based_norm_fwd(x, G, w, b, gate, out=gate.clone()), y)
+            for into in (x.clone(), gate.clone()):
+                first = into.data_ptr()
+                same = based_norm_fwd(into if torch.equal(into, x) else x, G, w, b, into if torch.equal(into, gate) else gate, out=into)
+                assert same.data_ptr() == first and torch.equal(same, y), (C, G)
+
+
 def test_determinism_streams_graphs_and_workspace(cuda_device):
     x, gate, w, b, dy = draw(3000, 512, BF16, BF16, BF16, True, 7)
     want = (based_norm_fwd(x, 8, w, b, gate), *based_norm_bwd(dy, x, 8, w, b, gate))
