@@ -2,8 +2,9 @@
 the error a float32 evaluation that rounds once to the output's type may have.
 
 Bounds: an output of type t may be off by half a step, eps(t) / 2 relative, plus the float32 error.
-exp is good to 2^-23 relative, the logistic function made of it (one addition, a reciprocal to
-2^-23, one product) to 2^-21, and every float32 operation adds 2^-24; DELTA = 2^-20 per row covers
+exp(x) is good to 2^-22 and |x| 2^-24 relative, the logistic function made of it (one addition, a
+reciprocal to 2^-23, one product) to 2^-21 where x is small and so a decay is far from 0, and
+every float32 operation adds 2^-24; DELTA = 2^-20 per row covers
 the decay, the increment, the row's own multiply-add and its share of the products that join
 stretches of rows. Sums over a group or over rows add at most their depth times 2^-24 relative to
 the sum of magnitudes.
