@@ -233,8 +233,12 @@ __device__ __forceinline__ void with_act(int act, F f) {
 // Registers: the forward kernel fits 64, the backward kernel, which also holds the sums for dweight
 // and dbias, 80 (100 where x is float32): weight and bias wait in shared memory, four 16-byte reads a
 // row. By pairs and singles they take up to 85 and 128. BIG ones may have 512 threads.
+constexpr int norm_threads(Words w, bool bwd, bool big) { return big ? 512 : w == kOctets && bwd ? 128 : 256; }
+constexpr int norm_ctas(Words w, bool bwd, bool big, bool x32) {
+    return big ? 1 : w == kOctets ? (bwd ? (x32 ? 5 : 6) : 4) : (bwd ? 2 : 3);
+}
 template <typename TX, typename TY, Words W, bool GATED, bool BWD, bool BIG>
-__global__ void __launch_bounds__(BIG ? 512 : W == kOctets && BWD ? 128 : 256, BIG ? 1 : W == kOctets ? (BWD ? (sizeof(TX) == 4 ? 5 : 6) : 4) : (BWD ? 2 : 3))
+__global__ void __launch_bounds__(norm_threads(W, BWD, BIG), norm_ctas(W, BWD, BIG, sizeof(TX) == 4))
     based_norm_kernel(const NormParams p) {
     constexpr int P = kElems / 2;
     constexpr bool VEC = W == kOctets;
@@ -279,7 +283,8 @@ __global__ void __launch_bounds__(BIG ? 512 : W == kOctets && BWD ? 128 : 256, B
     const int64_t turn = static_cast<int64_t>(gridDim.x) * p.rp;
     int64_t row = static_cast<int64_t>(blockIdx.x) * p.rp + r;
     const TX *px = static_cast<const TX *>(p.x) + row * p.x_sr + c;
-    const TY *pz = static_cast<const TY *>(p.gate) + row * p.gate_sr + c, *pd = static_cast<const TY *>(p.dy) + row * p.dy_sr + c;
+    const TY *pz = static_cast<const TY *>(p.gate) + row * p.gate_sr + c;
+    const TY *pd = static_cast<const TY *>(p.dy) + row * p.dy_sr + c;
     int64_t out = row * p.C + c;
     // past the last row the registers keep an earlier one
     auto fetch = [&] {
@@ -468,7 +473,8 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd, bool vec, bool 
     }
     s.grid_y = (G + s.gpb - 1) / s.gpb;
     // as many CTAs as are resident at once, in whole turns over the column blocks
-    const int held = vec ? (bwd ? (x32 ? 640 : 768) : 1024) : (bwd ? 512 : 768), resident = sms * (held / s.threads > 1 ? held / s.threads : 1);
+    const int held = vec ? (bwd ? (x32 ? 640 : 768) : 1024) : (bwd ? 512 : 768);
+    const int resident = sms * (held / s.threads > 1 ? held / s.threads : 1);
     const int64_t turns = (R + s.rp - 1) / s.rp, most = resident / s.grid_y > 1 ? resident / s.grid_y : 1;
     s.grid_x = static_cast<int>(turns < most ? turns : most);
     return s;

@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
     const Input<T, kThreads, FAST> gate(p.gate, p.gate_sb, p.gate_st, at.b, at.c0, p);
     const Input<T, kThreads, FAST> x(p.x, p.x_sb, p.x_st, at.b, at.c0, p);
     T *y = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
-    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = !FAST || (p.pair && at.n == N);  // store_row() takes rows that are whole in time
     Vec<N> carry = splat<N>(0.0f);  // warp 0's: the state in front of the cluster's tiles
     if (warp == 0) {
@@ -504,7 +505,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
     const Input<T, kThreads, FAST> dy(p.dy, p.dy_sb, p.dy_st, at.b, at.c0, p);
     T *dgate = static_cast<T *>(p.y) + static_cast<int64_t>(at.b) * p.T * p.D;
     T *dx = static_cast<T *>(p.dx) + static_cast<int64_t>(at.b) * p.T * p.D;
-    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T)), off_row = p.D * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off0 = (warp * R * p.D + at.c) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off_row = p.D * static_cast<uint32_t>(sizeof(T));
     const bool wide = !FAST || (p.pair && at.n == N);  // store_row() takes rows that are whole in time
     Vec<N> carry = splat<N>(0.0f);  // warp 1's: mu behind the cluster's tiles
     if (warp == 1) load_state(p.state ? p.state + plane : nullptr, at.n, carry);
@@ -794,7 +796,8 @@ int launch_scan(ScanParams &p, void (*kernel)(ScanParams), int threads, int sms,
     // CTAs that are all resident at once spread evenly where no SM can take more than its share: each asks for
     // that share of the shared memory (8 x 3000 x 1536 backward: 84 us with up to four on an SM, 69 us with three).
     // One more with large clusters, which have to find their SMs within a part of the GPU.
-    const int64_t per_sm = (blocks * p.cluster + sms - 1) / sms + (p.cluster > 8 ? 1 : 0), share = per_sm < 4 ? 228 * 1024 / per_sm - 1024 : 0;
+    const int64_t per_sm = (blocks * p.cluster + sms - 1) / sms + (p.cluster > 8 ? 1 : 0);
+    const int64_t share = per_sm < 4 ? 228 * 1024 / per_sm - 1024 : 0;
     size_t smem = Smem::bytes(p.cluster);
     if (share > static_cast<int64_t>(smem)) smem = static_cast<size_t>(share < kMost ? share : kMost);
     for (p.b0 = 0; p.b0 < p.B; p.b0 += kMaxGrid) {
@@ -807,7 +810,8 @@ template <typename T>
 int launch_scan(ScanParams &p, int mode, bool bwd, int sms, cudaStream_t st) {
     constexpr int kLog = BASED_GATE_LOG, kSig = BASED_GATE_SIGMOID;
     const bool log = mode == BASED_GATE_LOG, fast = p.fast != 0, ragged = p.lengths;
-    const StepCost fwd_cost = {1.6, 3.0 * kTile * kRowBytes, 6.7e6, 0.02}, bwd_cost = {2.6, 5.0 * kTile * kRowBytes, 6.6e6, 0.03};
+    const StepCost fwd_cost = {1.6, 3.0 * kTile * kRowBytes, 6.7e6, 0.02};
+    const StepCost bwd_cost = {2.6, 5.0 * kTile * kRowBytes, 6.6e6, 0.03};
     constexpr int N = Place<T>::N;
     if (bwd) {
         if (!fast)
