@@ -39,7 +39,16 @@ def _binding():
     return module
 
 
-_C = _binding()
+class _Unloaded:
+    """Stands for the binding until the first call, so that this module can be imported before build()."""
+
+    def __getattr__(self, name):
+        global _C
+        _C = _binding()
+        return getattr(_C, name)
+
+
+_C = _Unloaded()
 
 
 def library():

@@ -154,3 +154,30 @@ def test_binding_refuses_host_tensors_types_and_shapes():
         ops.based_embed_fwd(torch.zeros(3, dtype=torch.int32), g[0])
     with pytest.raises(ValueError):
         ops.based_embed_bwd(torch.zeros(3, dtype=torch.int32), g[0, :3], 10)
+
+
+def run_copy(tmp_path, code):
+    """Runs `code` beside a copy of the package's Python files: a checkout in which nothing is built."""
+    import shutil
+    import subprocess
+    import sys
+    shutil.copytree(os.path.join(ROOT, "linear_attention_gb300"), tmp_path / "linear_attention_gb300",
+                    ignore=shutil.ignore_patterns("_lib", "__pycache__"))
+    return subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True, timeout=300)
+
+
+def test_import_before_the_build_and_a_call_that_says_so(tmp_path):
+    out = run_copy(tmp_path, """
+import torch
+from linear_attention_gb300 import autograd, based, based_scan_fwd, ops
+assert ops.__file__.startswith(%r), ops.__file__
+for call in (lambda: based_scan_fwd(torch.zeros(1, 1, 1), torch.zeros(1, 1, 1)), ops.library):
+    try:
+        call()
+    except based.BasedError as e:
+        assert "not built" in str(e)
+    else:
+        raise SystemExit("no error")
+print("refused")
+""" % str(tmp_path))
+    assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr[-2000:]
