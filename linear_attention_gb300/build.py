@@ -14,7 +14,6 @@ SOURCES = [os.path.join(CSRC, f) for f in ("based_fwd.cu", "based_scan.cu", "bas
 DEPS = SOURCES + [os.path.join(CSRC, "based_kernels.cuh"), os.path.join(CSRC, "sm103_ptx.cuh"),
                   os.path.join(CSRC, "based_plan.h"), os.path.join(CSRC, "ops_common.cuh"),
                   os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]
-BINDING_PATH = os.path.join(LIB_DIR, "based_ops_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "ops_binding.cpp")
 BINDING_DEPS = [BINDING_SOURCE, os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
@@ -30,6 +29,15 @@ def nvcc() -> str:
 def _fresh(path: str, deps) -> bool:
     """Whether path exists and is not older than any of deps."""
     return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def binding_path() -> str:
+    """The operators' binding, named by the Python and torch whose interfaces it was compiled against:
+    one built for others is not loaded, and is built again."""
+    import torch
+
+    tag = "".join(c if c.isalnum() or c in ".+" else "_" for c in torch.__version__)
+    return os.path.join(LIB_DIR, f"based_ops_binding-torch{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _binding_commands(obj: str, out: str):
@@ -48,34 +56,45 @@ def _binding_commands(obj: str, out: str):
     return compile_ + ["-c", BINDING_SOURCE, "-o", obj], link
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the shared library, and the operators' binding to it, where they are missing or older
-    than any of their sources."""
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile the shared library where it is missing or older than any of its sources."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    obj = BINDING_PATH[:-3] + ".o"
-    compile_, link = _binding_commands(obj, BINDING_PATH + ".tmp")
-    compiler = None
-    if force or not _fresh(BINDING_PATH, BINDING_DEPS):
+    if force or not _fresh(LIB_PATH, DEPS):
+        tmp = LIB_PATH + ".tmp"
+        cmd = [nvcc()] + NVCC_FLAGS + SOURCES + ["-o", tmp]
         if verbose:
-            print(" ".join(compile_))
-        compiler = subprocess.Popen(compile_)  # beside nvcc
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB_PATH)
+    return LIB_PATH
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """build_library(), and the operators' binding to the library where it is missing or old. The
+    library is there even where the binding's compiler, Python's headers or torch are not."""
+    os.makedirs(LIB_DIR, exist_ok=True)
+    compiler = None
     try:
-        if force or not _fresh(LIB_PATH, DEPS):
-            tmp = LIB_PATH + ".tmp"
-            cmd = [nvcc()] + NVCC_FLAGS + SOURCES + ["-o", tmp]
+        path = binding_path()
+        obj = path[:-3] + ".o"
+        compile_, link = _binding_commands(obj, path + ".tmp")
+        if force or not _fresh(path, BINDING_DEPS):
             if verbose:
-                print(" ".join(cmd))
-            subprocess.run(cmd, check=True)
-            os.replace(tmp, LIB_PATH)
+                print(" ".join(compile_))
+            compiler = subprocess.Popen(compile_)  # beside nvcc
     finally:
-        failed = compiler is not None and compiler.wait() != 0
+        try:
+            build_library(force, verbose)
+        finally:
+            failed = compiler is not None and compiler.wait() != 0
     if failed:
         raise subprocess.CalledProcessError(compiler.returncode, compile_)
     if compiler is not None:
         if verbose:
             print(" ".join(link))
         subprocess.run(link, check=True)
-        os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        os.replace(path + ".tmp", path)
+        os.remove(obj)
     return LIB_PATH
 
 

@@ -22,17 +22,17 @@ from typing import Optional, Tuple
 import torch
 
 from . import based
-from .build import BINDING_PATH
+from .build import binding_path
 
 SAVE_ROWS = 64  # BASED_SCAN_SAVE_ROWS
 
 
 def _binding():
-    if not os.path.exists(BINDING_PATH):
-        raise based.BasedError(
-            f"binding not built: {BINDING_PATH} is missing (run linear_attention_gb300.build.build())")
+    path = binding_path()
+    if not os.path.exists(path):
+        raise based.BasedError(f"binding not built: {path} is missing (run linear_attention_gb300.build.build())")
     based.library()
-    spec = importlib.util.spec_from_file_location("based_ops_binding", BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("based_ops_binding", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.set_check(based._check)

@@ -181,3 +181,24 @@ for call in (lambda: based_scan_fwd(torch.zeros(1, 1, 1), torch.zeros(1, 1, 1)),
 print("refused")
 """ % str(tmp_path))
     assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr[-2000:]
+
+
+def test_a_binding_of_another_torch_is_not_taken(lib, monkeypatch):
+    path = lbuild.binding_path()
+    assert os.path.exists(path)
+    monkeypatch.setattr(torch, "__version__", "0.0.1/x")
+    other = lbuild.binding_path()
+    assert other != path and os.path.dirname(other) == os.path.dirname(path) and not os.path.exists(other)
+
+
+def test_the_library_is_built_where_the_binding_cannot_be(lib, monkeypatch):
+    built = []
+    monkeypatch.setattr(lbuild, "build_library", lambda *a: built.append(a))
+
+    def broken(*a):
+        raise RuntimeError("no headers")
+
+    monkeypatch.setattr(lbuild, "_binding_commands", broken)
+    with pytest.raises(RuntimeError):
+        lbuild.build()
+    assert built
