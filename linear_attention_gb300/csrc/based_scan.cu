@@ -571,16 +571,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
             fetch_state(step + 1);
         } else if (warp == 1 && live) {
             Vec<N> mu = carry;
-            if (cs > 1) {
-                Map<N> all = {sm.warp[kBwdWarps - 1][lane].a, sm.rev[kBwdWarps - 1][lane]};  // the tile's, in reversed time
+            // the tile's map in reversed time, composed for one CTA as for several: no bit depends on their number
+            Map<N> all = {sm.warp[kBwdWarps - 1][lane].a, sm.rev[kBwdWarps - 1][lane]};
 #pragma unroll
-                for (int w = kBwdWarps - 2; w >= 0; --w) all = compose(Map<N>{sm.warp[w][lane].a, sm.rev[w][lane]}, all);
+            for (int w = kBwdWarps - 2; w >= 0; --w) all = compose(Map<N>{sm.warp[w][lane].a, sm.rev[w][lane]}, all);
+            if (cs > 1) {
                 if (waiting) waiting = sm.ex.swap(exchanges, cs, at.rank, lane, all);
                 sm.ex.fold(exchanges, cs, at.rank, lane, mu, carry);
                 ++exchanges;
             } else {
-#pragma unroll
-                for (int w = kBwdWarps - 1; w >= 0; --w) carry = vfma(sm.warp[w][lane].a, carry, sm.rev[w][lane]);
+                carry = apply(all, carry);
             }
             sm.mu[lane] = mu;
         }
@@ -751,27 +751,28 @@ int choose_cluster(int64_t blocks, int64_t tiles, const int (&slots)[kMaxCluster
 }
 
 // The cluster size of a call, from a per-thread cache of the last few shapes: a call repeats the
-// shapes of the calls before it far more often than not.
+// shapes of the calls before it far more often than not. All that `choose` looks at is in the key.
 template <typename F>
 int recent_cluster(ScanParams &p, void (*kernel)(ScanParams), F choose) {
     struct Entry {
         void (*kernel)(ScanParams);
-        int dev, B, T, D, cluster;
+        int dev, B, T, D, ragged, cluster;
     };
     constexpr int kEntries = 8;
     static thread_local Entry recent[kEntries];
     static thread_local int next = 0;
     int dev;
     OPS_CUDA(cudaGetDevice(&dev));
+    const int ragged = p.lengths != nullptr;
     for (const Entry &e : recent) {
-        if (e.kernel == kernel && e.dev == dev && e.B == p.B && e.T == p.T && e.D == p.D) {
+        if (e.kernel == kernel && e.dev == dev && e.B == p.B && e.T == p.T && e.D == p.D && e.ragged == ragged) {
             p.cluster = e.cluster;
             return BASED_OK;
         }
     }
     const int rc = choose(&p.cluster);
     if (rc != BASED_OK) return rc;
-    recent[next] = {kernel, dev, p.B, p.T, p.D, p.cluster};
+    recent[next] = {kernel, dev, p.B, p.T, p.D, ragged, p.cluster};
     next = (next + 1) % kEntries;
     return BASED_OK;
 }

@@ -302,3 +302,36 @@ def test_many_batch_entries(cuda_device):
     B, T, D = 65535 + 70, 2, 3
     g, x, dy, state, dfinal = draw(B, T, D, "log", BF16, 17)
     check(g, x, dy, state, dfinal, "log", what="many")
+
+
+def in_a_new_thread(work):
+    """What work() returns in a thread of its own, which remembers no shapes of earlier calls."""
+    import threading
+    got = []
+    thread = threading.Thread(target=lambda: got.append(work()))
+    thread.start()
+    thread.join()
+    return got[0]
+
+
+@pytest.mark.parametrize("B,T,D", [(240, 831, 31), (304, 1535, 31)])
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+def test_bits_do_not_depend_on_the_calls_before(B, T, D, mode, cuda_device):
+    # shapes for which another number of CTAs is best with padding than without; decays near 1, so that
+    # what the tiles in front pass on is not lost in rounding
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    g, x, dy = (torch.randn(B, T, D, generator=gen, device="cuda") for _ in range(3))
+    g = g + 6 if mode == "sigmoid" else -0.01 * g.abs()
+    lengths = torch.randint(0, T + 1, (B,), generator=gen, device="cuda").to(torch.int32)
+
+    def grads(lens):
+        y, final, saved = based_scan_fwd(g, x, mode=mode, lengths=lens, save=True)
+        return y, final, saved, *based_scan_bwd(g, x, dy, saved, mode=mode, lengths=lens)
+
+    for lens, other in ((lengths, None), (None, lengths)):
+        want = in_a_new_thread(lambda: grads(lens))
+        got = in_a_new_thread(lambda: (grads(other), grads(lens))[1])
+        assert all(torch.equal(p, q) for p, q in zip(want, got))
+    # as many rows as there are, told by lengths or not: other CTAs, the same bits
+    full = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    assert all(torch.equal(p, q) for p, q in zip(in_a_new_thread(lambda: grads(full)), in_a_new_thread(lambda: grads(None))))
