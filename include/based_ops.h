@@ -35,7 +35,7 @@ enum { BASED_F32 = 0, BASED_BF16 = 1, BASED_F16 = 2 };
 
 /* How the recurrence turns its gate g and input x into a decay a and an increment u. */
 enum {
-    BASED_GATE_LOG = 0,    /* a = exp(g), u = x: g is the log decay (g = -inf clears the state) */
+    BASED_GATE_LOG = 0,    /* a = exp(g), u = x: g is the log decay (g = -inf clears the state; g > 0 makes it grow) */
     BASED_GATE_SIGMOID = 1 /* a = 1 / (1 + exp(-g)), u = (1 - a) x: g is the forget-gate logit */
 };
 
@@ -49,6 +49,10 @@ enum { BASED_ACT_NONE = 0, BASED_ACT_SILU = 1, BASED_ACT_SIGMOID = 2 };
  * based_scan_fwd: the gated linear recurrence
  *     h_t = a_t h_{t-1} + u_t,   t = 0 .. T-1, independently for each batch entry and channel,
  * with a and u from the gate and input by `mode`, computed and carried in float32.
+ * States may be anything that float32 holds, row by row, with one exception: where log gates add up
+ * to more than 88 within sixteen rows (0-15, 16-31, ...), a state of 0 in front of them stays 0,
+ * and one that is not 0 becomes infinite, however small it is. A state that is infinite stays so,
+ * or is NaN.
  *   gate, x      (B,T,D) of `dtype`, strides (gate_sb, gate_st, 1) and (x_sb, x_st, 1)
  *   state        (B,D) float32: h_{-1}; NULL is zero
  *   lengths      (B) int32 or NULL: rows t >= lengths[b] are padding: they leave the state as it

@@ -198,6 +198,70 @@ __device__ __forceinline__ Map<N> compose(const Map<N> &m, const Map<N> &in) {
     return {vmul(m.a, in.a), vfma(m.a, in.b, m.b)};
 }
 
+// Where decays grow (positive log gates), the product over a tile can pass float32 although every row of the recurrence
+// is finite: the state in front of it may be 0, or small. Such a map holds the negative cube root of its product
+// (past 2^300 any state but 0 overflows: the root stays at 2^100). Sixteen rows alone are one product in float32:
+// where that is infinite, a state of 0 stays 0 and any other becomes infinite. And where a product underflows, an
+// infinite state in front of it stays infinite, as it does row by row. The functions named far do that. They are
+// for tiles in which a warp's map is not plain(), which a barrier's vote tells, and for steps through the cluster's maps
+// that meet such a map or an infinite state. There they are made of selections: with branches on which the lanes of a
+// warp differ the loops over the tiles take longer (8 x 4096 x 2047 bf16, log decays, forward: 139 us, 129 here, 124
+// without any of this; 1 x 16384 x 2048 40.9 and 39.9 us).
+template <int N>
+__device__ __forceinline__ bool finite(const Vec<N> &v) {
+    return fabsf(v.v[0]) + (N == 2 ? fabsf(v.v[N - 1]) : 0.0f) < INFINITY;
+}
+// Whether this map and three more of its kind compose in float32.
+template <int N>
+__device__ __forceinline__ bool plain(const Vec<N> &a, const Vec<N> &b) {
+    return a.v[0] < 0x1p31f && a.v[N - 1] < 0x1p31f && finite(b);
+}
+// a h + b of one channel, as fmaf() has it for maps of the common kind
+__device__ __forceinline__ float far_apply(float a, float b, float h) {
+    const bool root = a < 0.0f, stays = (a == 0.0f && isinf(h)) || (a == INFINITY && h == 0.0f);
+    return fmaf(stays ? 1.0f : fabsf(a), root ? a * (a * h) : h, b);
+}
+__device__ __forceinline__ float far_product(float a, float b) {
+    if (a == 0.0f || b == 0.0f) return 0.0f;
+    if (a > 0.0f && b > 0.0f && a * b < INFINITY) return a * b;
+    const float root = (a < 0.0f ? -a : cbrtf(a)) * (b < 0.0f ? -b : cbrtf(b));
+    return root > 0x1p100f ? -0x1p100f : -root;  // NaN stays NaN
+}
+template <int N>
+__device__ __forceinline__ Vec<N> far_apply(const Map<N> &m, const Vec<N> &h) {
+    Vec<N> r;
+#pragma unroll
+    for (int j = 0; j < N; ++j) r.v[j] = far_apply(m.a.v[j], m.b.v[j], h.v[j]);
+    return r;
+}
+// A product that overflowed before a decay of 0 is NaN; its increment is not, as it is where a gate was.
+template <int N>
+__device__ __forceinline__ Map<N> far_clear(Map<N> m) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) m.a.v[j] = isnan(m.a.v[j]) && !isnan(m.b.v[j]) ? 0.0f : m.a.v[j];
+    return m;
+}
+
+// The warps' maps composed, the first first: to[i] is the map of the first i + 1. far: some lane's map is not plain().
+template <int COUNT, int N, typename F>
+__device__ __forceinline__ void in_order(F map, Map<N> (&to)[COUNT], bool far) {
+    to[0] = map(0);
+#pragma unroll
+    for (int i = 1; i < COUNT; ++i) to[i] = compose(map(i), to[i - 1]);
+    if (far) {
+        to[0] = far_clear(to[0]);
+#pragma unroll
+        for (int i = 1; i < COUNT; ++i) {
+            const Map<N> m = far_clear(map(i));
+#pragma unroll
+            for (int j = 0; j < N; ++j) to[i].a.v[j] = far_product(m.a.v[j], to[i - 1].a.v[j]);
+            to[i].b = far_apply(m, to[i - 1].b);
+        }
+    }
+}
+// What a kernel looks at in its steps through the cluster's maps: nothing; results; results and the maps' signs.
+enum Far { kNever, kInfinite, kGrowing };
+
 __device__ unsigned int g_scan_status;  // bit 0: a wait on the cluster's maps gave up
 constexpr uint64_t kScanWaitNs = 1000000000ull;
 
@@ -244,14 +308,59 @@ struct Exchange {
             }
         return true;
     }
-    // `at`: the value in front of tile `rank`; `carry` becomes the one behind the last tile
-    __device__ __forceinline__ void fold(int step, int cluster, int rank, int lane, Vec<N> &at, Vec<N> &carry) {
+    // `at`: the value in front of tile `rank`; `carry` becomes the one behind the last tile. signs: of the maps' products
+    __device__ __forceinline__ void fold(int step, int cluster, int rank, int lane, Vec<N> &at, Vec<N> &carry, uint32_t &signs) {
         const Map<N>(*set)[32] = maps + (step & 1) * cluster;
         at = carry;
 #pragma unroll 4
         for (int r = 0; r < cluster; ++r) {
-            carry = apply(set[r][lane], carry);
+            const Map<N> m = set[r][lane];
+#pragma unroll
+            for (int j = 0; j < N; ++j) signs |= __float_as_uint(m.a.v[j]);
+            carry = apply(m, carry);
             if (r + 1 == rank) at = carry;
+        }
+    }
+    __device__ __forceinline__ void far_fold(int step, int cluster, int rank, int lane, Vec<N> &at, Vec<N> &carry) {
+        const Map<N>(*set)[32] = maps + (step & 1) * cluster;
+        at = carry;
+#pragma unroll 1
+        for (int r = 0; r < cluster; ++r) {
+            carry = far_apply(set[r][lane], carry);
+            if (r + 1 == rank) at = carry;
+        }
+    }
+    // From the maps of a CTA's COUNT stretches, composed, what is in front of each of them, through the exchange where
+    // there are several CTAs (waiting: no wait has given up); `carry` moves on.
+    template <Far FAR, int COUNT>
+    __device__ __forceinline__ void advance(const Map<N> (&to)[COUNT], int step, int cluster, int rank, int lane, bool &waiting,
+                                            Vec<N> &carry, Vec<N> (&front)[COUNT]) {
+        const Vec<N> before = carry;
+        uint32_t signs = 0;
+        front[0] = carry;
+        if (cluster > 1) {
+            if (waiting) waiting = swap(step, cluster, rank, lane, to[COUNT - 1]);
+            fold(step, cluster, rank, lane, front[0], carry, signs);
+        } else {
+            carry = apply(to[COUNT - 1], carry);
+#pragma unroll
+            for (int j = 0; j < N; ++j) signs |= __float_as_uint(to[COUNT - 1].a.v[j]);
+        }
+#pragma unroll
+        for (int i = 1; i < COUNT; ++i) {
+            front[i] = apply(to[i - 1], front[0]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) signs |= __float_as_uint(to[i - 1].a.v[j]);
+        }
+        if (FAR == kNever) return;
+        if (__any_sync(~0u, (FAR == kGrowing && static_cast<int32_t>(signs) < 0) || !finite(carry))) {
+            carry = front[0] = before;
+            if (cluster > 1)
+                far_fold(step, cluster, rank, lane, front[0], carry);
+            else
+                carry = far_apply(to[COUNT - 1], carry);
+#pragma unroll
+            for (int i = 1; i < COUNT; ++i) front[i] = far_apply(to[i - 1], front[0]);
         }
     }
 };
@@ -342,8 +451,7 @@ constexpr int kFwdWarps = 4, kFwdStages = 2;
 template <int N, int PITCH>  // PITCH: bytes of a tile's row
 struct FwdSmem {
     uint8_t tile[kFwdStages][2][kTile * PITCH];
-    Map<N> warp[kFwdWarps][32];  // each warp's rows; then the tile's rows in front of them
-    Vec<N> start[32];            // the state in front of the tile
+    Map<N> warp[kFwdWarps][32];  // each warp's rows; then in b the state in front of them
     Exchange<N> ex;
     static constexpr size_t bytes(int cluster) { return offsetof(FwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
@@ -351,6 +459,7 @@ struct FwdSmem {
 template <typename T, int MODE, bool RAGGED, bool FAST>
 __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kFwdWarps, kThreads = 32 * kFwdWarps, P = FAST ? kRowBytes : kWideRow;
+    constexpr Far kFar = MODE == BASED_GATE_LOG ? kGrowing : kInfinite;
     extern __shared__ __align__(128) uint8_t raw[];
     FwdSmem<N, P> &sm = *reinterpret_cast<FwdSmem<N, P> *>(raw);
     const Place<T> at(p);
@@ -374,7 +483,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         load_state(p.state ? p.state + plane : nullptr, at.n, carry);
         // The store needs the loaded value: this CTA has read the state before it sends its first map, and so before
         // any CTA of the cluster can have the last state, which may be written to the same place.
-        sm.start[lane] = carry;
+        sm.warp[0][lane].b = carry;
     }
     bool waiting = true;
     auto fetch = [&](int step) {
@@ -412,25 +521,18 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         else if (row0 < len)
             rows(std::false_type());
         sm.warp[warp][lane] = m;
-        __syncthreads();  // the maps are there, and this step's stage is free
+        const bool far = __syncthreads_or(!plain(m.a, m.b));  // the maps are there, and this step's stage is free
         fetch(step + kFwdStages);
         if (warp == 0) {
             Vec<N> h = carry;
             if (live) {
-                Map<N> all = {splat<N>(1.0f), splat<N>(0.0f)};
+                Map<N> to[kFwdWarps];
+                Vec<N> front[kFwdWarps];
+                in_order<kFwdWarps, N>([&](int w) { return sm.warp[w][lane]; }, to, far);
+                sm.ex.template advance<kFar>(to, step, cs, at.rank, lane, waiting, carry, front);
 #pragma unroll
-                for (int w = 0; w < kFwdWarps; ++w) {
-                    const Map<N> o = sm.warp[w][lane];
-                    sm.warp[w][lane] = all;
-                    all = compose(o, all);
-                }
-                if (cs > 1) {
-                    if (waiting) waiting = sm.ex.swap(step, cs, at.rank, lane, all);
-                    sm.ex.fold(step, cs, at.rank, lane, h, carry);
-                } else {
-                    carry = apply(all, carry);
-                }
-                sm.start[lane] = h;
+                for (int w = 0; w < kFwdWarps; ++w) sm.warp[w][lane].b = front[w];
+                h = front[0];
             }
             if (p.saved && tile < at.tiles)
                 store_some(p.saved + (static_cast<int64_t>(at.b) * at.tiles + tile) * p.D + at.c, h, at.n);
@@ -440,7 +542,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
         uint8_t *to = reinterpret_cast<uint8_t *>(y + static_cast<int64_t>(tile) * kTile * p.D);
         uint32_t off = off0;
         if (full && wide) {
-            Vec<N> h = apply(sm.warp[warp][lane], sm.start[lane]);
+            Vec<N> h = sm.warp[warp][lane].b;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
@@ -448,7 +550,7 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 4) based_scan_fwd_kernel(const
                 off += off_row;
             }
         } else if (row0 < len) {
-            Vec<N> h = apply(sm.warp[warp][lane], sm.start[lane]);
+            Vec<N> h = sm.warp[warp][lane].b;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 h = vfma(a[i], h, u[i]);
@@ -478,9 +580,8 @@ constexpr int kBwdWarps = 4, kBwdStages = 2;
 template <int N, int PITCH>
 struct BwdSmem {
     uint8_t tile[kBwdStages][3][kTile * PITCH];
-    Map<N> warp[kBwdWarps][32];
-    Vec<N> rev[kBwdWarps][32];   // the reversed map's increment
-    Vec<N> start[32], mu[32];    // the state in front of the tile, mu behind it
+    Map<N> warp[kBwdWarps][32];  // each warp's rows; then in b the state in front of them
+    Vec<N> rev[kBwdWarps][32];   // the reversed map's increment; then mu behind the warp's rows
     Exchange<N> ex;
     static constexpr size_t bytes(int cluster) { return offsetof(BwdSmem, ex) + (cluster > 1 ? Exchange<N>::bytes(cluster) : 0); }
 };
@@ -488,6 +589,7 @@ struct BwdSmem {
 template <typename T, int MODE, bool RAGGED, bool FAST>
 __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_kernel(const ScanParams p) {
     constexpr int N = Place<T>::N, R = kTile / kBwdWarps, kThreads = 32 * kBwdWarps, P = FAST ? kRowBytes : kWideRow;
+    constexpr Far kFar = MODE == BASED_GATE_LOG ? kGrowing : kNever;
     extern __shared__ __align__(128) uint8_t raw[];
     BwdSmem<N, P> &sm = *reinterpret_cast<BwdSmem<N, P> *>(raw);
     const Place<T> at(p);
@@ -565,36 +667,38 @@ __global__ void __launch_bounds__(32 * kBwdWarps, FAST ? 4 : 3) based_scan_bwd_k
             rows(std::false_type());
         sm.warp[warp][lane] = m;
         sm.rev[warp][lane] = rev;
-        __syncthreads();  // the maps are there
+        bool far = false;
+        if (kFar != kNever)
+            far = __syncthreads_or(!plain(m.a, m.b) || !finite(rev));  // the maps are there
+        else
+            __syncthreads();
         if (warp == 0) {
-            sm.start[lane] = saved;
+            Map<N> m[kBwdWarps];
+            Vec<N> h[kBwdWarps];
+            h[0] = saved;
+#pragma unroll
+            for (int w = 1; w < kBwdWarps; ++w) m[w] = sm.warp[w - 1][lane], h[w] = apply(m[w], h[w - 1]);
+            if (far) {
+#pragma unroll
+                for (int w = 1; w < kBwdWarps; ++w) h[w] = far_apply(far_clear(m[w]), h[w - 1]);
+            }
+#pragma unroll
+            for (int w = 0; w < kBwdWarps; ++w) sm.warp[w][lane].b = h[w];
             fetch_state(step + 1);
         } else if (warp == 1 && live) {
-            Vec<N> mu = carry;
             // the tile's map in reversed time, composed for one CTA as for several: no bit depends on their number
-            Map<N> all = {sm.warp[kBwdWarps - 1][lane].a, sm.rev[kBwdWarps - 1][lane]};
+            Map<N> to[kBwdWarps];
+            Vec<N> front[kBwdWarps];
+            in_order<kBwdWarps, N>([&](int i) { return Map<N>{sm.warp[kBwdWarps - 1 - i][lane].a, sm.rev[kBwdWarps - 1 - i][lane]}; }, to, far);
+            sm.ex.template advance<kFar>(to, exchanges++, cs, at.rank, lane, waiting, carry, front);
 #pragma unroll
-            for (int w = kBwdWarps - 2; w >= 0; --w) all = compose(Map<N>{sm.warp[w][lane].a, sm.rev[w][lane]}, all);
-            if (cs > 1) {
-                if (waiting) waiting = sm.ex.swap(exchanges, cs, at.rank, lane, all);
-                sm.ex.fold(exchanges, cs, at.rank, lane, mu, carry);
-                ++exchanges;
-            } else {
-                carry = apply(all, carry);
-            }
-            sm.mu[lane] = mu;
+            for (int w = 0; w < kBwdWarps; ++w) sm.rev[kBwdWarps - 1 - w][lane] = front[w];
         }
         __syncthreads();  // the starts are there
         uint8_t *const to_g = reinterpret_cast<uint8_t *>(dgate + static_cast<int64_t>(tile) * kTile * p.D);
         uint8_t *const to_x = reinterpret_cast<uint8_t *>(dx + static_cast<int64_t>(tile) * kTile * p.D);
         if (some) {
-            // through the tile's rows in front of this warp's, and those behind it
-            Vec<N> h = sm.start[lane], mu = sm.mu[lane];
-#pragma unroll
-            for (int w = 0; w < kBwdWarps; ++w) {
-                if (w < warp) h = apply(sm.warp[w][lane], h);
-                if (kBwdWarps - 1 - w > warp) mu = vfma(sm.warp[kBwdWarps - 1 - w][lane].a, mu, sm.rev[kBwdWarps - 1 - w][lane]);
-            }
+            Vec<N> h = sm.warp[warp][lane].b, mu = sm.rev[warp][lane];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const Vec<N> v = unpack<T>(word(sx, i));

@@ -335,3 +335,68 @@ def test_bits_do_not_depend_on_the_calls_before(B, T, D, mode, cuda_device):
     # as many rows as there are, told by lengths or not: other CTAs, the same bits
     full = torch.full((B,), T, dtype=torch.int32, device="cuda")
     assert all(torch.equal(p, q) for p, q in zip(in_a_new_thread(lambda: grads(full)), in_a_new_thread(lambda: grads(None))))
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (F32, 33), (BF16, 64), (BF16, 35), (F16, 35)])
+def test_growing_log_gates(dtype, D, cuda_device):
+    # exp of the gates' sum over a tile, or over sixteen rows, passes float32; what the rows make of it does not:
+    # the inputs are zero but for the last few rows, the gradients but for the first few
+    for gates, rows in (((3.0, 40.0), (10, 2)), ((0.7, 2.0), (100, 30))):
+        g, x, dy, state, dfinal = draw(2, 200, D, "log", dtype, 21)
+        for b in range(2):
+            n = rows[b] if dtype != F16 else min(rows[b], 2)  # float16 ends at 65504
+            g[b], x[b, :-n], dy[b, n:] = gates[b] if dtype != F16 else min(gates[b], 9.0), 0, 0
+        check(g, x, dy, 0 * state, 0 * dfinal, "log", what=gates)
+    # a channel that grows leaves its neighbours' bits alone
+    g, x, dy, state, dfinal = draw(2, 200, D, "log", dtype, 22)
+    want = based_scan_fwd(g, x, mode="log", state=state, save=True)
+    want = *want, *based_scan_bwd(g, x, dy, want[2], mode="log", dfinal=dfinal)
+    g2 = g.clone()
+    g2[:, :, 4] = 30.0
+    got = based_scan_fwd(g2, x, mode="log", state=state, save=True)
+    got = *got, *based_scan_bwd(g2, x, dy, got[2], mode="log", dfinal=dfinal)
+    rest = torch.arange(D, device="cuda") != 4
+    assert all(torch.equal(p[..., rest], q[..., rest]) for p, q in zip(want, got))
+
+
+@pytest.mark.parametrize("T", [90, 3000])
+def test_growth_of_a_small_state(T, cuda_device):
+    # from 1e-30 by a factor of e^1.5 a row, for 80 rows wherever they lie: e^120 in all
+    g, x, dy, state, dfinal = draw(3, T, 40, "log", F32, 23)
+    g[:], x[:], dy[:] = 0, 0, 0
+    for b, first in enumerate((0, 7, T - 80)):
+        g[b, first:first + 80] = 1.5
+    check(g, x, dy, state * 1e-30, dfinal * 1e-30, "log", what=T)
+    g[:, :] = -1.5
+    g[1, 0], g[2] = 100.0, 1.4  # e^100 is infinite: a state of zero times it is NaN, in any order
+    y, final, _ = based_scan_fwd(g, x, mode="log", state=0 * state)
+    assert (y[0] == 0).all() and torch.isnan(y[1]).all() and (y[2] == 0).all() and (final[2] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 33), (BF16, 64)])
+def test_growth_that_is_cleared(dtype, D, cuda_device):
+    # products over a warp's rows that overflow before a decay of exactly 0, of a state of zero; beside them ordinary
+    # channels, and NaN gates that stay NaN
+    for at in (3, 9, 70, 150):
+        g, x, dy, state, dfinal = draw(2, 200, D, "log", dtype, at)
+        g[:, at:at + 6, 1::2], x[:, :at + 6, 1::2], dy[:, at:, 1::2] = 30.0, 0, 0
+        g[:, at + 6, 1::2] = -float("inf")
+        state[:, 1::2], dfinal[:, 1::2] = 0, 0
+        check(g, x, dy, state, dfinal, "log", what=at)
+        g[:, at + 8, 0] = float("nan")
+        y, final, _ = based_scan_fwd(g, x, mode="log", state=state)
+        assert torch.isnan(y[:, at + 8:, 0]).all() and torch.isnan(final[:, 0]).all() and torch.isfinite(y[:, :, 1:]).all()
+
+
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+def test_an_infinite_state_stays_infinite(mode, cuda_device):
+    # the decays' product over some rows underflows, and 0 times infinity is NaN: no row alone does that
+    for dtype, D in ((F32, 64), (BF16, 33), (BF16, 64)):
+        g, x, _, state, _ = draw(1, 700, D, mode, dtype, 24)
+        want, _, _ = based_scan_fwd(g, x, mode=mode, state=state)
+        g[0, :, 3] = -3.0
+        x[0, 5, 3] = float("inf")
+        got, final, _ = based_scan_fwd(g, x, mode=mode, state=state)
+        assert (got[0, 5:, 3] == float("inf")).all() and final[0, 3] == float("inf")
+        rest = torch.arange(D, device="cuda") != 3
+        assert torch.equal(got[..., rest], want[..., rest])
