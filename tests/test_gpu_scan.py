@@ -400,3 +400,17 @@ def test_an_infinite_state_stays_infinite(mode, cuda_device):
         assert (got[0, 5:, 3] == float("inf")).all() and final[0, 3] == float("inf")
         rest = torch.arange(D, device="cuda") != 3
         assert torch.equal(got[..., rest], want[..., rest])
+
+
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+def test_float32_decays_over_their_range(mode, cuda_device):
+    # one row from a state of 1 and an input of 0 shows the decay itself. expf is off by 2^-22 at most, the addition by
+    # 2^-24, the reciprocal by 2^-23, the multiply-add by 2^-24: 2^-21 in all
+    g = torch.linspace(-20, 0 if mode == "log" else 20, 8192, device="cuda").view(8, 1, 1024)
+    zero, one = torch.zeros_like(g), torch.ones(8, 1024, device="cuda")
+    want = torch.exp(g.double()) if mode == "log" else torch.sigmoid(g.double())
+    y, final, _ = based_scan_fwd(g, zero, mode=mode, state=one)
+    pool = one.clone()
+    z = based_scan_step(g[:, 0], zero[:, 0], pool, mode=mode)
+    for got in (y[:, 0], final, z, pool):
+        assert ((got.double() - want[:, 0]) / want[:, 0]).abs().max() <= 2.0 ** -21
