@@ -206,13 +206,13 @@ __device__ __forceinline__ float total(const Vec<2> (&v)[kElems / 2]) {
 
 // act(v) and act'(v)
 template <int ACT>
-__device__ __forceinline__ void activate(const Vec<2> &v, Vec<2> &f, Vec<2> &df) {
+__device__ __forceinline__ void activate(Vec<2> v, Vec<2> &f, Vec<2> &df) {
     if (ACT == BASED_ACT_NONE) {
         f = v, df = splat<2>(1.0f);
         return;
     }
     Vec<2> s, t;
-    vsigmoid(v, s, t);
+    vsigmoid(v, s, t);  // v is -87 at least: a type's lowest value times the smallest sigma is far from 0
     if (ACT == BASED_ACT_SIGMOID)
         f = s, df = vmul(s, t);
     else

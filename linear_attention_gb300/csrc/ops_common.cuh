@@ -276,10 +276,10 @@ __device__ __forceinline__ Vec<N> vexp(const Vec<N> &x) {
     return t;
 }
 // p = sigma(g), q = sigma(-g) = 1 - p, each with its own relative accuracy (q = e^-g p, not 1 - p). Below
-// g = -87, where p is under 2e-38, g counts as -87, so that e^-g stays finite; NaN stays NaN. A single element's p
+// g = -87, where p is under 2e-38, g becomes -87, so that e^-g stays finite and g p near 0; NaN stays NaN. A single element's p
 // above 1/2 is 1 - q, as close to 1 as float32 has it: the reciprocal's error would add up over a recurrence's rows.
 template <int N>
-__device__ __forceinline__ void vsigmoid(Vec<N> g, Vec<N> &p, Vec<N> &q) {
+__device__ __forceinline__ void vsigmoid(Vec<N> &g, Vec<N> &p, Vec<N> &q) {
 #pragma unroll
     for (int j = 0; j < N; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(g.v[j]) : "f"(g.v[j]), "f"(-87.0f));
     Vec<N> e;

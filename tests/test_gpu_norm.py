@@ -207,3 +207,25 @@ def test_offsets_past_32_bits(cuda_device):
     y = based_norm_fwd(big, 8, act="silu")
     want = based_norm_fwd(x, 8, act="silu")
     assert torch.equal(y[-3:], want[[(R - 3) % 8, (R - 2) % 8, (R - 1) % 8]]) and torch.equal(y[:8], want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gates_of_the_lowest_value(dtype, act, cuda_device):
+    # what masks a gate: its activation and its slope are 0 for every type, and nothing else of the row changes
+    for C in (128, 50):
+        x, gate, w, b, dy = draw(6, C, dtype, dtype, F32, True, C)
+        low = torch.rand(6, C, generator=torch.Generator().manual_seed(C)).cuda() < 0.3
+        for value in (torch.finfo(dtype).min, -1e4):
+            gate[low] = value
+            y = based_norm_fwd(x, 2, w, b, gate, act)
+            dx, dgate, dw, db = based_norm_bwd(dy, x, 2, w, b, gate, act)
+            assert y[low].abs().max() <= 1e-30 and dgate[low].abs().max() <= 1e-30
+            far = gate.clone()
+            far[low] = -120.0
+            want = based_norm_fwd(x, 2, w, b, far, act), *based_norm_bwd(dy, x, 2, w, b, far, act)
+            for p, q in zip((y, dx, dgate, dw, db), want):
+                assert torch.equal(torch.where(p.abs() > 1e-30, p, 0), torch.where(q.abs() > 1e-30, q, 0))
+        # without a gate, v itself: a bias of the lowest value
+        bias = torch.full((C,), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+        assert based_norm_fwd(x, 2, None, bias, act=act).abs().max() <= 1e-30
