@@ -310,7 +310,10 @@ __global__ void __launch_bounds__(norm_threads(W, BWD, BIG), norm_ctas(W, BWD, B
         row += turn;
         px += turn * p.x_sr, pz += turn * p.gate_sr, pd += turn * p.dy_sr;
         fetch();
-        if (BWD && !mh) rd.clear();  // adds nothing to dweight and dbias
+        if (BWD && !mh) {  // adds nothing to dweight and dbias, whatever the earlier row's gate was
+            rd.clear();
+            if (GATED) rz.clear();
+        }
         Vec<2> h[P], sq[P];
 #pragma unroll
         for (int k = 0; k < P; ++k) h[k] = rx.get(k);

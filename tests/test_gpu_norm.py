@@ -229,3 +229,16 @@ def test_gates_of_the_lowest_value(dtype, act, cuda_device):
         # without a gate, v itself: a bias of the lowest value
         bias = torch.full((C,), torch.finfo(dtype).min, dtype=dtype, device="cuda")
         assert based_norm_fwd(x, 2, None, bias, act=act).abs().max() <= 1e-30
+
+
+def test_infinite_gates_in_sums_over_rows(cuda_device):
+    # rows that do not come out even over the CTAs: threads without a row in the last turn keep an earlier one's values
+    inf = float("inf")
+    for R, C, G in ((5003, 192, 3), (3, 192, 3), (2999, 50, 2), (700, 512, 1)):
+        x, gate, w, b, dy = draw(R, C, BF16, BF16, F32, True, R)
+        gate[:, 7], dy[:, 7], gate[:, 9], dy[:, 9] = inf, 1, -inf, 1
+        for act, want in (("silu", (inf, 0)), ("none", (inf, -inf)), ("sigmoid", (R, 0))):
+            _, _, dw, db = based_norm_bwd(dy, x, G, w, b, gate, act)
+            assert float(db[7]) == want[0] and (abs(float(db[9])) <= 1e-30 if want[1] == 0 else float(db[9]) == want[1])
+            rest = torch.tensor([c not in (7, 9) for c in range(C)], device="cuda")
+            assert torch.isfinite(dw[rest]).all() and torch.isfinite(db[rest]).all()
