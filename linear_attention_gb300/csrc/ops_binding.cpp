@@ -93,7 +93,7 @@ void input(const Tensor &t, const char *name, Sizes shape, ScalarType type, int 
         refuse(PyExc_ValueError, std::string(name) + " must have shape " + shape_of(shape) + ", got " + shape_of(t.sizes()));
     if (t.scalar_type() != type)
         refuse(PyExc_TypeError, std::string(name) + " must be " + name_of(type) + ", got " + name_of(t.scalar_type()));
-    if (t.stride(-1) != 1 && t.size(-1) != 1)
+    if (t.stride(-1) != 1 && t.size(-1) != 1 && t.numel() != 0)
         refuse(PyExc_ValueError, "the last axis of " + std::string(name) + " must have stride 1");
 }
 // The address of a contiguous tensor of this shape and type; NULL for none.
@@ -115,7 +115,7 @@ struct Rows {
             if (size != 1) {
                 if (!any)
                     stride = t.stride(i);
-                else if (t.stride(i) != stride * n && size > 0)
+                else if (t.stride(i) != stride * n && t.numel() != 0)
                     refuse(PyExc_ValueError, "the leading axes of " + std::string(name) + " must have one common stride");
                 any = true;
             }
@@ -178,6 +178,14 @@ void check(int rc, const char *what) {
     throw Refusal();
 }
 
+// The value of an output that no row or token adds to: `from`, or zero.
+void settle(const Tensor &to, const Tensor *from) {
+    if (!from)
+        to.zero_();
+    else if (from->data_ptr() != to.data_ptr())
+        to.copy_(*from);
+}
+
 PyObject *wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject *none() { return Py_NewRef(Py_None); }
 PyObject *wrap_or_none(Tensor t) { return t.defined() ? wrap(std::move(t)) : none(); }
@@ -212,6 +220,10 @@ PyObject *scan_fwd(PyObject *const *a) {
     const Tensor y = at.output(a[6], "out", shape, type), last = at.output(a[7], "final_state", {B, D}, kF32);
     Tensor saved;
     if (save) saved = at.empty({B, saved_rows(T), D}, kF32);
+    if ((B == 0 || T == 0) && D > 0) {  // the C functions take at least one row
+        settle(last, optional_tensor(a[3], "state"));
+        return tuple(wrap(y), wrap(last), wrap_or_none(saved));
+    }
     check(based_scan_fwd(gate.data_ptr(), gate.stride(0), gate.stride(1), x.data_ptr(), x.stride(0), x.stride(1), small(B),
                          small(T), small(D), code, mode, static_cast<float *>(state), static_cast<int32_t *>(lengths),
                          y.data_ptr(), static_cast<float *>(last.data_ptr()),
@@ -237,6 +249,10 @@ PyObject *scan_bwd(PyObject *const *a) {
     void *dfinal = whole(optional_tensor(a[5], "dfinal"), "dfinal", {B, D}, kF32, at.dev);
     void *lengths = whole(optional_tensor(a[6], "lengths"), "lengths", {B}, ScalarType::Int, at.dev);
     const Tensor dgate = at.empty(shape, type), dx = at.empty(shape, type), dstate = at.empty({B, D}, kF32);
+    if ((B == 0 || T == 0) && D > 0) {
+        settle(dstate, optional_tensor(a[5], "dfinal"));
+        return tuple(wrap(dgate), wrap(dx), wrap(dstate));
+    }
     check(based_scan_bwd(gate.data_ptr(), gate.stride(0), gate.stride(1), x.data_ptr(), x.stride(0), x.stride(1),
                          dy.data_ptr(), dy.stride(0), dy.stride(1), static_cast<float *>(saved), small(B), small(T), small(D),
                          code, mode, static_cast<float *>(dfinal), static_cast<int32_t *>(lengths), dgate.data_ptr(),
@@ -259,6 +275,7 @@ PyObject *scan_step(PyObject *const *a) {
     void *states = whole(&pool, "pool", {S, D}, kF32, at.dev);
     void *slots = whole(optional_tensor(a[4], "slots"), "slots", {N}, ScalarType::Int, at.dev);
     const Tensor y = at.output(a[5], "out", shape, type);
+    if (N == 0 && D > 0) return wrap(y);
     check(based_scan_step(gate.data_ptr(), gate.stride(0), x.data_ptr(), x.stride(0), small(N), small(D), small(S), code, mode,
                           static_cast<float *>(states), static_cast<int32_t *>(slots), y.data_ptr(), at.raw()),
           "based_scan_step");
@@ -296,6 +313,7 @@ PyObject *norm_fwd(PyObject *const *a) {
     const Rows rx(x, "x"), rg(gate ? *gate : x, "gate");
     const NormParams par(a[2], a[3], C, type, at.dev);
     const Tensor y = at.output(a[8], "out", x.sizes(), type);
+    if (rx.n == 0 && C > 0) return wrap(y);
     check(based_norm_fwd(x.data_ptr(), rx.stride, xcode, gate ? gate->data_ptr() : nullptr, rg.stride, par.weight, par.bias,
                          par.code, rx.n, small(C), small(groups), eps, act, y.data_ptr(), code, at.raw()),
           "based_norm_fwd");
@@ -331,6 +349,11 @@ PyObject *norm_bwd(PyObject *const *a) {
     if (gate) dgate = at.empty(shape, type);
     if (par.w) dweight = at.empty({C}, par.w->scalar_type());
     if (par.b) dbias = at.empty({C}, par.b->scalar_type());
+    if (rx.n == 0 && C > 0) {
+        if (par.w) settle(dweight, nullptr);
+        if (par.b) settle(dbias, nullptr);
+        return tuple(wrap(dx), wrap_or_none(dgate), wrap_or_none(dweight), wrap_or_none(dbias));
+    }
     const bool sums = par.w || par.b;
     if (sums) ws = workspace(a[8], a[8] == Py_None ? based_norm_bwd_workspace_size(rx.n, small(C), small(groups)) : 0, at);
     check(based_norm_bwd(dy.data_ptr(), rd.stride, x.data_ptr(), rx.stride, xcode, gate ? gate->data_ptr() : nullptr, rg.stride,
@@ -371,6 +394,7 @@ PyObject *embed_fwd(PyObject *const *a) {
     ids_place(ids, at.dev);
     input(table, "table", table.sizes(), type, at.dev);
     const Tensor y = at.output(a[3], "out", with_channels(ids, D), type);
+    if (ids.numel() == 0 && V > 0 && D > 0) return wrap(y);
     check(based_embed_fwd(ids.data_ptr(), wide, table.data_ptr(), table.stride(0), ids.numel(), small(V), small(D), code, scale,
                           y.data_ptr(), at.raw()),
           "based_embed_fwd");
@@ -391,6 +415,10 @@ PyObject *embed_bwd(PyObject *const *a) {
     const Rows rd(dy, "dy");
     if (V < 0) refuse(PyExc_ValueError, "rows must not be negative");
     const Tensor dtable = at.output(a[5], "out", {V, D}, type);
+    if (N == 0 && V > 0 && D > 0) {
+        settle(dtable, nullptr);
+        return wrap(dtable);
+    }
     const Tensor ws = workspace(a[6], a[6] == Py_None ? based_embed_bwd_workspace_size(N, small(V), small(D)) : 0, at);
     check(based_embed_bwd(ids.data_ptr(), wide, dy.data_ptr(), rd.stride, N, small(V), small(D), code, scale, dtable.data_ptr(),
                           gcode, ws.data_ptr(), ws.nbytes(), at.raw()),

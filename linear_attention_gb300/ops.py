@@ -10,7 +10,9 @@ TypeError, and what the C functions refuse raises BasedError.
 All functions launch on ``stream`` (default: the current stream of the inputs' device). What they
 allocate (outputs that are not passed in, workspaces) comes from that stream's pool, so a call on a
 side stream needs ordering only for its inputs and for the use of its results. Inputs may be
-strided as long as their last axis has stride 1; outputs are contiguous.
+strided as long as their last axis has stride 1; outputs are contiguous. Batches without rows, tokens
+or sequences, which the C functions refuse, give empty outputs, the state they were given and
+gradients of zero.
 """
 from __future__ import annotations
 

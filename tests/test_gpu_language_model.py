@@ -189,3 +189,51 @@ def test_two_threads_call_at_once(cuda_device):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def test_empty_batches(cuda_device):
+    from linear_attention_gb300 import ops
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    state = torch.randn(3, 8, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        for B, T in ((0, 5), (3, 0), (0, 0)):
+            s = state[:B]
+            y, final, saved = ops.based_scan_fwd(z(B, T, 8), z(B, T, 8), state=s, save=True, stream=stream)
+            grads = ops.based_scan_bwd(z(B, T, 8), z(B, T, 8), z(B, T, 8), saved, dfinal=s, stream=stream)
+            none = ops.based_scan_fwd(z(B, T, 8), z(B, T, 8), stream=stream)
+            torch.cuda.synchronize()
+            assert y.shape == grads[0].shape == grads[1].shape == (B, T, 8) and saved.shape == (B, (T + 63) // 64, 8)
+            assert torch.equal(final, s) and torch.equal(grads[2], s) and final.data_ptr() != s.data_ptr() or B == 0
+            assert none[1].shape == (B, 8) and (none[1] == 0).all()
+        carry = state.clone()
+        assert ops.based_scan_fwd(z(3, 0, 8), z(3, 0, 8), state=carry, final_state=carry, stream=stream)[1].data_ptr() == carry.data_ptr()
+        torch.cuda.synchronize()
+        assert torch.equal(carry, state)
+        pool = state.clone()
+        slots = torch.zeros(0, dtype=torch.int32, device="cuda")
+        assert ops.based_scan_step(z(0, 8), z(0, 8), pool, slots=slots, stream=stream).shape == (0, 8) and torch.equal(pool, state)
+        w = torch.ones(8, device="cuda")
+        for shape in ((0, 8), (4, 0, 8)):
+            assert ops.based_norm_fwd(z(*shape), 2, w, w, z(*shape), stream=stream).shape == shape
+            dx, dgate, dw, db = ops.based_norm_bwd(z(*shape), z(*shape), 2, w, w, z(*shape), stream=stream)
+            torch.cuda.synchronize()
+            assert dx.shape == dgate.shape == shape and (dw == 0).all() and (db == 0).all() and dw.shape == db.shape == (8,)
+        for shape in ((0,), (2, 0)):
+            ids = torch.zeros(*shape, dtype=torch.int32, device="cuda")
+            assert ops.based_embed_fwd(ids, state, stream=stream).shape == (*shape, 8)
+            grad = ops.based_embed_bwd(ids, z(*shape, 8), 3, out=torch.ones(3, 8, device="cuda"), stream=stream)
+            torch.cuda.synchronize()
+            assert (grad == 0).all()
+    # through autograd
+    leaves = [t.requires_grad_() for t in (z(2, 0, 8), z(2, 0, 8), state[:2].clone(), w.clone(), state.clone())]
+    y, final = gated_scan(leaves[0], leaves[1], state=leaves[2])
+    x = embedding(torch.zeros(2, 0, dtype=torch.int64, device="cuda"), leaves[4])
+    (group_norm(y + x, 2, leaves[3]).sum() + final.sum()).backward()
+    assert (leaves[2].grad == 1).all() and (leaves[3].grad == 0).all() and (leaves[4].grad == 0).all()
+    # a width of zero is still no width, and a table without rows no table
+    from linear_attention_gb300.based import BasedError
+    for call in (lambda: ops.based_scan_fwd(z(2, 3, 0), z(2, 3, 0)), lambda: ops.based_norm_fwd(z(2, 0), 1),
+                 lambda: ops.based_embed_fwd(slots, z(0, 8))):
+        with pytest.raises(BasedError):
+            call()
