@@ -83,7 +83,7 @@ class Model(torch.nn.Module):
 
     def loss(self, ids, lengths):
         """Mean loss of predicting each token from those before it; ids (B,T) hold -1 past the lengths."""
-        x = embedding(ids[:, :-1].contiguous(), self.table, self.scale)
+        x = embedding(ids[:, :-1], self.table, self.scale)
         for layer in self.layers:
             x = layer.train_forward(x, (lengths - 1).clamp(min=0).to(torch.int32))
         return F.cross_entropy(self.logits(x, group_norm).flatten(0, 1), ids[:, 1:].flatten().long(), ignore_index=-1)

@@ -1,7 +1,7 @@
 """The operators of ``linear_attention_gb300.ops`` as differentiable torch functions.
 
 Each function runs the forward kernel, keeps what the backward kernel needs, and gives its gradients
-to torch's autograd. Forward and backward passes run on the stream that is current at the forward
+to torch's autograd. Inputs may have any strides: those that the kernels do not read are copied first. Forward and backward passes run on the stream that is current at the forward
 call (autograd replays it). Gradients of gradients are not defined.
 
 Capturing a training step into a CUDA graph follows torch's rules: run a few steps on the capturing
@@ -19,12 +19,15 @@ from . import ops
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:
-    """A gradient that the kernels can read: sums and broadcasts give ones whose last axis is not."""
-    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+    """t as the kernels can read it: transposes, and gradients of sums and broadcasts, have a last axis of another
+    stride than 1."""
+    return t if t.dim() == 0 or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
-    """... and whose leading axes have one common stride."""
+    """... and with one common stride of its leading axes."""
+    if t.dim() == 0:
+        return t
     try:
         t.view(-1, t.shape[-1])
     except RuntimeError:
@@ -36,6 +39,8 @@ class _Scan(Function):
     @staticmethod
     def forward(ctx, gate, x, state, lengths, mode):
         needed = any(ctx.needs_input_grad[:3])
+        gate, x = _dense(gate), _dense(x)
+        state, lengths = (t if t is None else t.contiguous() for t in (state, lengths))
         y, final, saved = ops.based_scan_fwd(gate, x, mode=mode, state=state, lengths=lengths, save=needed)
         ctx.save_for_backward(gate, x, saved, lengths)
         ctx.mode = mode
@@ -57,6 +62,8 @@ class _Scan(Function):
 class _Norm(Function):
     @staticmethod
     def forward(ctx, x, weight, bias, gate, groups, act, eps, out_dtype):
+        x, gate = _rows(x), gate if gate is None else _rows(gate)
+        weight, bias = (t if t is None else t.contiguous() for t in (weight, bias))
         ctx.save_for_backward(x, weight, bias, gate)
         ctx.args = dict(groups=groups, act=act, eps=eps)
         return ops.based_norm_fwd(x, weight=weight, bias=bias, gate=gate, out_dtype=out_dtype, **ctx.args)
@@ -72,6 +79,7 @@ class _Norm(Function):
 class _Embed(Function):
     @staticmethod
     def forward(ctx, ids, table, scale):
+        table = _dense(table)
         ctx.save_for_backward(ids)
         ctx.args = (table.shape[0], scale, table.dtype)
         return ops.based_embed_fwd(ids, table, scale)

@@ -371,9 +371,11 @@ int ids_type(const Tensor &ids) {
         refuse(PyExc_TypeError, std::string("ids must be int32 or int64, got ") + name_of(ids.scalar_type()));
     return ids.scalar_type() == ScalarType::Long;
 }
-void ids_place(const Tensor &ids, int dev) {
-    if (!ids.is_cuda() || ids.get_device() != dev || !ids.is_contiguous())
-        refuse(PyExc_ValueError, "ids must be a contiguous CUDA tensor on the device of the other inputs");
+// ids in order, as a copy where they are strided (ids[:, :-1] of a batch)
+Tensor ids_in_order(const Tensor &ids, int dev) {
+    if (!ids.is_cuda() || ids.get_device() != dev)
+        refuse(PyExc_ValueError, "ids must be a CUDA tensor on the device of the other inputs");
+    return ids.contiguous();
 }
 // the shape of ids with one more axis
 c10::SmallVector<int64_t, 6> with_channels(const Tensor &ids, int64_t D) {
@@ -384,14 +386,14 @@ c10::SmallVector<int64_t, 6> with_channels(const Tensor &ids, int64_t D) {
 
 // ids, table, scale, out, stream
 PyObject *embed_fwd(PyObject *const *a) {
-    const Tensor &ids = tensor(a[0], "ids"), &table = tensor(a[1], "table");
+    const Tensor &given = tensor(a[0], "ids"), &table = tensor(a[1], "table");
     if (table.dim() != 2) refuse(PyExc_ValueError, "expected a table of shape (V,D)");
     const ScalarType type = table.scalar_type();
-    const int code = type_code(type, "table"), wide = ids_type(ids);
+    const int code = type_code(type, "table"), wide = ids_type(given);
     const float scale = static_cast<float>(float_arg(a[2]));
     const Place at(table, "table", a[4]);
     const int64_t V = table.size(0), D = table.size(1);
-    ids_place(ids, at.dev);
+    const Tensor ids = ids_in_order(given, at.dev);
     input(table, "table", table.sizes(), type, at.dev);
     const Tensor y = at.output(a[3], "out", with_channels(ids, D), type);
     if (ids.numel() == 0 && V > 0 && D > 0) return wrap(y);
@@ -403,14 +405,14 @@ PyObject *embed_fwd(PyObject *const *a) {
 
 // ids, dy, rows, scale, dtype, out, workspace, stream
 PyObject *embed_bwd(PyObject *const *a) {
-    const Tensor &ids = tensor(a[0], "ids"), &dy = tensor(a[1], "dy");
+    const Tensor &given = tensor(a[0], "ids"), &dy = tensor(a[1], "dy");
     if (dy.dim() < 1) refuse(PyExc_ValueError, "expected dy of shape (..., D)");
     const ScalarType type = dtype_arg(a[4]);
-    const int code = type_code(dy.scalar_type(), "dy"), gcode = type_code(type, "the gradient"), wide = ids_type(ids);
-    const int64_t V = int_arg(a[2]), D = dy.size(-1), N = ids.numel();
+    const int code = type_code(dy.scalar_type(), "dy"), gcode = type_code(type, "the gradient"), wide = ids_type(given);
+    const int64_t V = int_arg(a[2]), D = dy.size(-1), N = given.numel();
     const float scale = static_cast<float>(float_arg(a[3]));
     const Place at(dy, "dy", a[7]);
-    ids_place(ids, at.dev);
+    const Tensor ids = ids_in_order(given, at.dev);
     input(dy, "dy", with_channels(ids, D), dy.scalar_type(), at.dev);
     const Rows rd(dy, "dy");
     if (V < 0) refuse(PyExc_ValueError, "rows must not be negative");

@@ -10,7 +10,9 @@ TypeError, and what the C functions refuse raises BasedError.
 All functions launch on ``stream`` (default: the current stream of the inputs' device). What they
 allocate (outputs that are not passed in, workspaces) comes from that stream's pool, so a call on a
 side stream needs ordering only for its inputs and for the use of its results. Inputs may be
-strided as long as their last axis has stride 1; outputs are contiguous. Batches without rows, tokens
+strided as long as their last axis has stride 1; the leading axes of the norm's inputs and of the
+embedding's dy need one common stride (rows at equal distances), states, lengths, slots, weights and
+biases are contiguous, and ids may have any strides. Outputs are contiguous. Batches without rows, tokens
 or sequences, which the C functions refuse, give empty outputs, the state they were given and
 gradients of zero.
 """

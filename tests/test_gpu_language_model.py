@@ -237,3 +237,41 @@ def test_empty_batches(cuda_device):
                  lambda: ops.based_embed_fwd(slots, z(0, 8))):
         with pytest.raises(BasedError):
             call()
+
+
+def test_inputs_of_any_strides(cuda_device):
+    # the same bits as from contiguous copies, forward and backward
+    from linear_attention_gb300 import ops
+    gen = torch.Generator().manual_seed(5)
+    rand = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+
+    def results(f, tensors):
+        leaves = [t.detach().clone(memory_format=torch.preserve_format).requires_grad_() for t in tensors]
+        outs = f(*leaves)
+        outs = outs if isinstance(outs, tuple) else (outs,)
+        sum((o * torch.arange(o.numel(), device="cuda").view(o.shape).cos()).sum() for o in outs).backward()
+        return *outs, *(t.grad for t in leaves)
+
+    def same(f, view, tensors):
+        got = results(lambda *t: f(*map(view, t)), tensors)
+        want = results(lambda *t: f(*(view(v).contiguous() for v in t)), tensors)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+    for view in (lambda t: t[:, :-1], lambda t: t.transpose(0, 1), lambda t: t.transpose(1, 2), lambda t: t[..., ::2],
+                 lambda t: t[:, ::3], lambda t: t[:1].expand_as(t), lambda t: t[..., :1].expand_as(t)):
+        same(lambda g, x: gated_scan(g, x), view, (rand(4, 12, 16), rand(4, 12, 16)))
+        same(lambda x, z: group_norm(x, 2, gate=z), view, (rand(4, 12, 16), rand(4, 12, 16)))
+        same(lambda x: group_norm(x, 1, act="none"), view, (rand(4, 12, 16),))
+    x, both = rand(4, 12, 16), rand(32, 2)
+    same(lambda w, b: group_norm(x, 2, w[:16], b[16:]), lambda t: t[:, 0], (both, both))
+    same(lambda s: gated_scan(x, x, state=s), lambda t: t.t(), (rand(16, 4),))
+    lengths = torch.tensor([[3, 0], [12, 0], [7, 1], [0, 9]], device="cuda").to(torch.int32)
+    assert torch.equal(gated_scan(x, x, lengths=lengths[:, 0])[0], gated_scan(x, x, lengths=lengths[:, 0].contiguous())[0])
+    ids = torch.randint(-1, 9, (4, 13), generator=gen).cuda()
+    for idt in (torch.int32, torch.int64):
+        for part in (ids.to(idt)[:, :-1], ids.to(idt).t(), ids.to(idt)[::2, 1:]):
+            same(lambda t: embedding(part, t, 2.0), lambda t: t.t(), (rand(16, 9),))
+            dy = rand(*part.shape, 16)
+            assert torch.equal(ops.based_embed_bwd(part, dy, 9), ops.based_embed_bwd(part.contiguous(), dy, 9))
+            table = rand(9, 16)
+            assert torch.equal(ops.based_embed_fwd(part, table), ops.based_embed_fwd(part.contiguous(), table))
