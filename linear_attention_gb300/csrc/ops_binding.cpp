@@ -99,7 +99,9 @@ void input(const Tensor &t, const char *name, Sizes shape, ScalarType type, int 
 // The address of a contiguous tensor of this shape and type; NULL for none.
 void *whole(const Tensor *t, const char *name, Sizes shape, ScalarType type, int dev) {
     if (!t) return nullptr;
-    if (!t->is_cuda() || t->get_device() != dev || t->scalar_type() != type || t->sizes() != shape || !t->is_contiguous())
+    if (t->scalar_type() != type)
+        refuse(PyExc_TypeError, std::string(name) + " must be " + name_of(type) + ", got " + name_of(t->scalar_type()));
+    if (!t->is_cuda() || t->get_device() != dev || t->sizes() != shape || !t->is_contiguous())
         refuse(PyExc_ValueError, std::string(name) + " must be a contiguous " + name_of(type) + " CUDA tensor of shape " + shape_of(shape));
     return t->data_ptr();
 }

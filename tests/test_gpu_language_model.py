@@ -275,3 +275,34 @@ def test_inputs_of_any_strides(cuda_device):
             assert torch.equal(ops.based_embed_bwd(part, dy, 9), ops.based_embed_bwd(part.contiguous(), dy, 9))
             table = rand(9, 16)
             assert torch.equal(ops.based_embed_fwd(part, table), ops.based_embed_fwd(part.contiguous(), table))
+
+
+def test_wrong_types_raise_type_error_and_wrong_shapes_value_error(cuda_device):
+    from linear_attention_gb300 import ops
+    x, s = torch.zeros(2, 5, 8, device="cuda"), torch.zeros(2, 8, device="cuda")
+    w, ids = torch.ones(8, device="cuda"), torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    saved = ops.based_scan_fwd(x, x, save=True)[2]
+    calls = [  # a call of one argument, that argument right, of a wrong type, of a wrong shape
+        (lambda t: ops.based_scan_fwd(x, x, state=t), s, s.half(), s[:1]),
+        (lambda t: ops.based_scan_fwd(x, x, lengths=t), n, n.long(), n[:1]),
+        (lambda t: ops.based_scan_fwd(x, x, out=t), x.clone(), x.half(), x[:, :4].clone()),
+        (lambda t: ops.based_scan_fwd(x, x, final_state=t), s.clone(), s.double(), s.t().contiguous()),
+        (lambda t: ops.based_scan_fwd(t, x), x, x.half(), x[:1]),
+        (lambda t: ops.based_scan_bwd(x, x, x, t), saved, saved.half(), saved[:, :0]),
+        (lambda t: ops.based_scan_bwd(x, x, x, saved, dfinal=t), s, s.half(), s[:1]),
+        (lambda t: ops.based_scan_step(s, s, t), s.clone(), s.half(), s[:, :4].clone()),
+        (lambda t: ops.based_scan_step(s, s, s.clone(), slots=t), n, n.long(), n[:1]),
+        (lambda t: ops.based_norm_fwd(x, 2, w, t), w, w.half(), w[:4]),
+        (lambda t: ops.based_norm_fwd(x, 2, out=t), x.clone(), x.half(), x[:1].clone()),
+        (lambda t: ops.based_norm_bwd(t, x, 2, gate=x), x, x.half(), x[:1]),
+        (lambda t: ops.based_embed_fwd(ids, s, out=t), x.clone(), x.half(), x[:1].clone()),
+        (lambda t: ops.based_embed_bwd(t, x, 2), ids, ids.float(), ids[:1]),
+        (lambda t: ops.based_embed_bwd(ids, x, 2, out=t), s.clone(), s.half(), s[:1].clone()),
+    ]
+    for call, right, type_, shape in calls:
+        call(right)
+        with pytest.raises(TypeError):
+            call(type_)
+        with pytest.raises(ValueError):
+            call(shape)
