@@ -516,7 +516,7 @@ struct EmbedPlan {
     size_t list, partial, bytes;  // two lists of keys, two of positions, the partial sums
 };
 bool embed_plan(int64_t N, int V, int D, EmbedPlan &e) {
-    if (N < 1 || V < 1 || D < 1 || N >= (1ll << 30)) return false;
+    if (N < 1 || V < 1 || D < 1 || N >= (1ll << 30) || D > (1 << 20)) return false;
     int bits = 1;
     while ((static_cast<int64_t>(V) >> bits) != 0) ++bits;  // V itself is the key of padding
     e.few = N <= kFewTokens && V < kFewVocab;
@@ -603,7 +603,7 @@ int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_t dy_sr, i
     if (!type_ok(dtype) || !type_ok(g_dtype) || (g_dtype != BASED_F32 && g_dtype != dtype))
         return BASED_ERR_UNSUPPORTED_TYPE;
     EmbedPlan e;
-    if (!embed_plan(N, V, D, e) || D > (1 << 20)) return BASED_ERR_BAD_SIZE;
+    if (!embed_plan(N, V, D, e)) return BASED_ERR_BAD_SIZE;
     if (dy_sr < 0) return BASED_ERR_BAD_STRIDE;
     const size_t es = elem_size(dtype), gs = elem_size(g_dtype), is = ids64 ? 8 : 4;
     if (!aligned(ids, is) || !aligned(dy, es) || !aligned(dtable, gs)) return BASED_ERR_MISALIGNED;

@@ -483,15 +483,17 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd, bool vec, bool 
     return s;
 }
 
+bool norm_sizes_ok(int64_t R, int C, int G) {
+    return R >= 1 && R < (1ll << 40) && C >= 1 && C <= (1 << 20) && G >= 1 && C % G == 0 && C / G <= kMaxGroup;
+}
+
 int check_norm(const NormParams &p, int x_dtype, int dtype, bool bwd, const void *dweight, const void *dbias) {
     if (!p.x || (bwd ? (!p.dy || !p.dx || !p.dgate != !p.gate) : !p.y)) return BASED_ERR_NULL_POINTER;
     if (!type_ok(x_dtype) || !type_ok(dtype) || !type_ok(p.p_dtype) || (x_dtype != BASED_F32 && x_dtype != dtype))
         return BASED_ERR_UNSUPPORTED_TYPE;
     if (p.act != BASED_ACT_NONE && p.act != BASED_ACT_SILU && p.act != BASED_ACT_SIGMOID) return BASED_ERR_BAD_ARGUMENT;
     if (!(p.eps >= 0.0f)) return BASED_ERR_BAD_ARGUMENT;
-    if (p.R < 1 || p.C < 1 || p.G < 1 || p.C % p.G != 0 || p.C / p.G > kMaxGroup || p.C > (1 << 20) ||
-        p.R >= (1ll << 40))
-        return BASED_ERR_BAD_SIZE;
+    if (!norm_sizes_ok(p.R, p.C, p.G)) return BASED_ERR_BAD_SIZE;
     if (p.x_sr < 0 || p.gate_sr < 0 || p.dy_sr < 0) return BASED_ERR_BAD_STRIDE;
     const size_t xs = elem_size(x_dtype), es = elem_size(dtype), ps = elem_size(p.p_dtype);
     if (!aligned(p.x, xs) || !aligned(p.dx, xs) || !aligned(p.gate, es) || !aligned(p.dy, es) || !aligned(p.y, es) ||
@@ -597,8 +599,7 @@ int based_norm_fwd(const void *x, int64_t x_sr, int x_dtype, const void *gate, i
 
 size_t based_norm_bwd_workspace_size(int64_t R, int C, int G) {
     int sms;
-    if (R < 1 || C < 1 || G < 1 || C % G != 0 || C / G > based::kMaxGroup || based::host_device(&sms) != BASED_OK)
-        return 0;
+    if (!based::norm_sizes_ok(R, C, G) || based::host_device(&sms) != BASED_OK) return 0;
     // the most that any alignment and type takes
     int parts = 0;
     for (int k = 0; k < 4; ++k) {

@@ -242,3 +242,11 @@ def test_infinite_gates_in_sums_over_rows(cuda_device):
             assert float(db[7]) == want[0] and (abs(float(db[9])) <= 1e-30 if want[1] == 0 else float(db[9]) == want[1])
             rest = torch.tensor([c not in (7, 9) for c in range(C)], device="cuda")
             assert torch.isfinite(dw[rest]).all() and torch.isfinite(db[rest]).all()
+
+
+def test_workspace_sizes_at_the_limits(cuda_device):
+    big = 1 << 20
+    for R, C, G in ((4, 2 * big, big), (1 << 40, 64, 4), (4, 8192, 1), (0, 64, 4), (4, 64, 5)):
+        assert norm_bwd_workspace_size(R, C, G) == 0, (R, C, G)
+    for R, C, G in ((4, big, big), ((1 << 40) - 1, 64, 4), (4, 4096, 1)):
+        assert norm_bwd_workspace_size(R, C, G) > 0, (R, C, G)

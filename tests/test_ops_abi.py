@@ -202,3 +202,15 @@ def test_the_library_is_built_where_the_binding_cannot_be(lib, monkeypatch):
     with pytest.raises(RuntimeError):
         lbuild.build()
     assert built
+
+
+def test_workspace_sizes_at_the_limits(lib):
+    """The sizes are 0 exactly where the calls refuse theirs."""
+    big = 1 << 20
+    for N, V, D in ((9, 100, big), (9, 100, big + 1), ((1 << 30) - 1, 5, 1), (1 << 30, 5, 1), (9, 100, -1), (9, -1, 4)):
+        refused = embed_bwd(lib, N=N, V=V, D=D, ds=max(D, 0), n=64) == SIZE
+        assert (lib.based_embed_bwd_workspace_size(N, V, D) == 0) == refused, (N, V, D)
+    # (the norm's sizes depend on the GPU; without one all are 0)
+    for R, C, G in ((4, 2 * big, big), (1 << 40, 64, 4), (4, 8192, 1), (0, 64, 4), (4, 64, -4)):
+        assert norm_bwd(lib, R=R, C=C, G=G, xs=C, ds=C, gs=C) == SIZE
+        assert lib.based_norm_bwd_workspace_size(R, C, G) == 0
