@@ -430,7 +430,9 @@ __global__ void __launch_bounds__(32 * kSumWarps) based_norm_sum_kernel(const No
     griddep_wait();
     griddep_launch_dependents();
     float s = 0.0f;
-    constexpr int kAhead = 20;  // loads under way at once: the sums of 640 CTAs, the most there are, in one go
+    // loads under way at once: the sums of 640 CTAs in one go (608 at 24000 x 1536); others, up to eight CTAs an SM of
+    // 96 threads, take two
+    constexpr int kAhead = 20;
     for (int k0 = warp; k0 < p.parts && c < 2 * p.C; k0 += kAhead * kSumWarps) {
         float v[kAhead];
 #pragma unroll
