@@ -188,3 +188,43 @@ def test_token_counts_around_the_direct_ranking(N, cuda_device):
         got = based_embed_bwd(ids.to(torch.int32).cuda(), dy.cuda(), V)
         val, bound = ref.embed_grad(ids, dy, V, 1.0, F32)
         ref.assert_within(got, val, bound, (N, V))
+
+
+def check_exactly(ids, V, D, seed):
+    """Gradients of small whole numbers: every float32 sum below 2^24 is exact, and one missing row shows."""
+    dy = torch.randint(-8, 9, (ids.numel(), D), generator=torch.Generator().manual_seed(seed))
+    live = (ids >= 0) & (ids < V)
+    want = torch.zeros(V, D, dtype=torch.int64).index_add(0, ids[live].long(), dy[live])
+    for dtype in (F32, BF16, F16):
+        got = based_embed_bwd(ids.cuda(), dy.to(dtype).cuda(), V)
+        assert torch.equal(got.cpu().long(), want) and torch.equal(got.cpu(), want.float())
+
+
+@pytest.mark.parametrize("N", [8192, 8193, 40000, 300_000])
+def test_one_token_everywhere_exactly(N, cuda_device):
+    # tiles of 32 rows: from one run over all of them to runs that begin and end around them
+    check_exactly(torch.full((N,), 3, dtype=torch.int32), 5, 40, N)
+    ids = torch.full((N,), 3, dtype=torch.int32)
+    ids[::5], ids[7], ids[N // 2] = 1, -1, 4
+    check_exactly(ids, 5, 9, N + 1)
+
+
+def test_runs_at_every_place_of_a_long_tile(cuda_device):
+    # 8192 tokens and more: tiles of 32 rows, more tokens than one chunk of eight CTAs
+    gen = torch.Generator().manual_seed(4)
+    for first in (0, 1, 5, 13, 30, 31, 32, 33, 40, 63, 64, 69):
+        counts = [first, 1, 2, 40, 31, 32, 33, 64, 1, 97, 0, 9000, 3, 400, 290]
+        ids = torch.repeat_interleave(torch.arange(15), torch.tensor(counts))
+        ids[torch.rand(len(ids), generator=gen) < 0.02] = -1
+        check_exactly(ids[torch.randperm(len(ids), generator=gen)].to(torch.int32), 16, 16, first)
+
+
+@pytest.mark.parametrize("N,V,D", [(8193, 45_000, 256), (9000, 45_000, 256), (20_000, 90_001, 256), (32_768, 150_000, 256),
+                                   (32_769, 150_000, 256), (70_000, 3_000, 24)])
+def test_sorts_of_eight_and_sixteen_ctas(N, V, D, cuda_device):
+    # eight sort up to 32768 tokens where the gradient has at least 4480 bytes a token
+    gen = torch.Generator().manual_seed(N)
+    ids = torch.randint(0, V, (N,), generator=gen)
+    ids[: N // 3] = torch.randint(0, 50, (N // 3,), generator=gen)
+    ids[torch.rand(N, generator=gen) < 0.05] = -1
+    check_exactly(ids[torch.randperm(N, generator=gen)].to(torch.int32), V, D, N)
