@@ -12,7 +12,9 @@
  *     of 0 broadcasts, negative ones are refused); outputs are contiguous. Offsets are computed
  *     in 64 bits.
  *   - Pointers must be aligned to their element size. 16-byte aligned pointers with strides and
- *     sizes that keep rows 16-byte aligned take wider loads; nothing else depends on alignment.
+ *     sizes that keep rows 16-byte aligned take wider loads. In the norm the order in which sums are
+ *     taken follows the loads, so that the same values at other strides or alignments can give
+ *     other bits; in the other operators nothing but time depends on alignment.
  *   - Inputs are read-only. Outputs must not overlap inputs, except where stated.
  *   - Calls are asynchronous on `stream`, never synchronise and never allocate. Scratch, where an
  *     operator needs some, is a caller's workspace (16-byte aligned; contents ignored on entry,
@@ -132,7 +134,7 @@ BASED_API int based_norm_fwd(const void *x, int64_t x_sr, int x_dtype, const voi
  *   dx       (R,C) of x_dtype, contiguous
  *   dgate    (R,C) of dtype, contiguous; needed if and only if there is a gate
  *   dweight, dbias  (C) of p_dtype; each may be NULL. Sums over rows are taken in float32, in an
- *            order that depends on the sizes alone.
+ *            order that depends on the sizes, types, strides, alignment and the GPU's number of SMs alone.
  *   workspace  based_norm_bwd_workspace_size() bytes (0 where dweight and dbias are NULL)
  * The statistics are recomputed from x. The rest as for based_norm_fwd.
  */

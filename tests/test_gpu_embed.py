@@ -228,3 +228,12 @@ def test_sorts_of_eight_and_sixteen_ctas(N, V, D, cuda_device):
     ids[: N // 3] = torch.randint(0, 50, (N // 3,), generator=gen)
     ids[torch.rand(N, generator=gen) < 0.05] = -1
     check_exactly(ids[torch.randperm(N, generator=gen)].to(torch.int32), V, D, N)
+
+
+def test_bits_do_not_depend_on_strides_and_alignment(cuda_device):
+    for N, V in ((700, 90), (3000, 90), (9000, 300)):
+        ids, _, dy = draw(N, V, 72, BF16, N)
+        wide = torch.zeros(N, 81, dtype=BF16, device="cuda")
+        for off in (1, 8):
+            wide[:, off:off + 72] = dy
+            assert torch.equal(based_embed_bwd(ids, wide[:, off:off + 72], V), based_embed_bwd(ids, dy, V))

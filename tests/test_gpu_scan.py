@@ -414,3 +414,23 @@ def test_float32_decays_over_their_range(mode, cuda_device):
     z = based_scan_step(g[:, 0], zero[:, 0], pool, mode=mode)
     for got in (y[:, 0], final, z, pool):
         assert ((got.double() - want[:, 0]) / want[:, 0]).abs().max() <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+def test_bits_do_not_depend_on_strides_and_alignment(dtype, mode, cuda_device):
+    for B, T, D in ((2, 700, 64), (40, 130, 136)):
+        g, x, dy, state, dfinal = draw(B, T, D, mode, dtype, 25)
+        lengths = torch.arange(B, dtype=torch.int32, device="cuda") * T // B
+
+        def run(g, x, dy, lens):
+            y, final, saved = based_scan_fwd(g, x, mode=mode, state=state, lengths=lens, save=True)
+            return y, final, saved, *based_scan_bwd(g, x, dy, saved, mode=mode, dfinal=dfinal, lengths=lens)
+
+        for lens in (None, lengths):
+            want = run(g, x, dy, lens)
+            wide = torch.zeros(B, T, 3 * D + 3, dtype=dtype, device="cuda")
+            parts = [wide[..., k * (D + 1):][..., 1:D + 1] for k in range(3)]
+            for p, t in zip(parts, (g, x, dy)):
+                p.copy_(t)
+            assert all(torch.equal(p, q) for p, q in zip(want, run(*parts, lens)))
