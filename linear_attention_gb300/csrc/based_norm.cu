@@ -477,7 +477,9 @@ NormShape norm_shape(int64_t R, int C, int G, int sms, bool bwd, bool vec, bool 
         s.threads = (s.gpb * s.rp * s.tpg + 31) / 32 * 32;
     }
     s.grid_y = (G + s.gpb - 1) / s.gpb;
-    // as many CTAs as are resident at once, in whole turns over the column blocks
+    // as many CTAs as are resident at once, in whole turns over the column blocks, by what groups of up to 256
+    // channels hold. Larger groups' kernels take up to 128 registers, and a half-empty last wave (16384 x 2048 in one
+    // group: 32 us forward and 86 us backward, of 20 and 30 at the memory's rate).
     const int held = vec ? (bwd ? (x32 ? 640 : 768) : 1024) : (bwd ? 512 : 768);
     const int resident = sms * (held / s.threads > 1 ? held / s.threads : 1);
     const int64_t turns = (R + s.rp - 1) / s.rp, most = resident / s.grid_y > 1 ? resident / s.grid_y : 1;
