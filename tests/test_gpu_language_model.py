@@ -306,3 +306,63 @@ def test_wrong_types_raise_type_error_and_wrong_shapes_value_error(cuda_device):
             call(type_)
         with pytest.raises(ValueError):
             call(shape)
+
+
+CAPTURED_STEPS = """
+import sys
+import torch
+sys.path[:0] = [".", "tests"]
+from test_gpu_language_model import example
+
+m = example()
+ids, lengths = m.batch(64, 4, 40, torch.Generator().manual_seed(1))
+
+
+def steps(model, count, capture):
+    opt = torch.optim.SGD(model.parameters(), lr=0.05)
+
+    def step():
+        opt.zero_grad(set_to_none=True)
+        loss = model.loss(ids, lengths)
+        loss.backward()
+        opt.step()
+        return loss.detach()
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        losses = [step().clone() for _ in range(3)]  # their graphs are gone when the capture begins
+    torch.cuda.current_stream().wait_stream(stream)
+    if not capture:
+        return losses + [step().clone() for _ in range(count)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        loss = step()
+    for _ in range(count):
+        graph.replay()
+        losses.append(loss.clone())
+    return losses
+
+
+def run(capture):
+    torch.manual_seed(0)
+    model = m.Model(vocab=64, width=64, heads=2, dtype=torch.float32)
+    losses = torch.stack(steps(model, 5, capture))
+    return losses, [p.detach() for p in model.parameters()]
+
+
+eager, captured = run(False), run(True)
+assert torch.allclose(eager[0], captured[0], rtol=1e-4), (eager[0], captured[0])
+for a, b in zip(eager[1], captured[1]):
+    assert (a - b).abs().max() <= 1e-3 * a.abs().max()
+assert eager[0][-1] < eager[0][0]
+print("same")
+"""
+
+
+def test_training_steps_can_be_captured(cuda_device):
+    # forward, backward and update as one graph, against the same steps without (products may choose other kernels)
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", CAPTURED_STEPS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
