@@ -951,8 +951,9 @@ int run_scan(ScanParams &p, int dtype, int mode, bool bwd, based_stream_t stream
     const bool near = (p.gate_st | p.x_st | p.dy_st) < (1 << 24);  // a tile's rows within 2^32 bytes
     // (8 x 4096 x 2048 and 2047 bfloat16: 67 + 117 us forward and backward by aligned words, 128 + 263 by shifted ones, 199
     // + 341 element by element. Rows of 4-byte words are copied as rows that start anywhere, too: by such words
-    // 2 x 2047 x 777 float32 takes 14.2 + 21.6 us, here 11.5 + 18.2, and 8 x 4096 x 1023 95 + 230, here 85 + 145;
-    // 2 x 4096 x 1022 bfloat16 alone would be faster, 19.4 + 35.6 where this takes 21.3 + 38.1.)
+    // 2 x 2047 x 777 float32 took 14.2 + 21.6 us where this took 11.5 + 18.2, and 8 x 4096 x 1023 95 + 230, this 85 + 145,
+    // both before float32 decays took expf(), 0.6 us of 12; 2 x 4096 x 1022 bfloat16 alone would be faster, 19.4 + 35.6
+    // where this takes 21.3 + 38.1.)
     p.fast = bits % 16 == 0 && near;
     p.pair = es == 4 || (p.D % 2 == 0 && aligned(p.y, 4) && aligned(p.dx, 4));
     if (dtype == BASED_F32) return launch_scan<float>(p, mode, bwd, sms, st);
