@@ -51,9 +51,10 @@ enum { BASED_ACT_NONE = 0, BASED_ACT_SILU = 1, BASED_ACT_SIGMOID = 2 };
  * based_scan_fwd: the gated linear recurrence
  *     h_t = a_t h_{t-1} + u_t,   t = 0 .. T-1, independently for each batch entry and channel,
  * with a and u from the gate and input by `mode`, computed and carried in float32.
- * States may be anything that float32 holds, row by row, with one exception: where log gates add up
+ * States may be anything that float32 holds, row by row, with two exceptions. Where log gates add up
  * to more than 88 within sixteen rows (0-15, 16-31, ...), a state of 0 in front of them stays 0,
- * and one that is not 0 becomes infinite, however small it is. A state that is infinite stays so,
+ * and one that is not 0 becomes infinite, however small it is. And what a tile of 64 rows or sixteen
+ * of its rows would make of a state of 0 has to fit float32 too. A state that is infinite stays so,
  * or is NaN.
  *   gate, x      (B,T,D) of `dtype`, strides (gate_sb, gate_st, 1) and (x_sb, x_st, 1)
  *   state        (B,D) float32: h_{-1}; NULL is zero
