@@ -175,6 +175,79 @@ BASED_API int based_embed_bwd(const void *ids, int ids64, const void *dy, int64_
 /* Bytes of workspace based_embed_bwd() needs for these sizes (0 for sizes it refuses). */
 BASED_API size_t based_embed_bwd_workspace_size(int64_t N, int V, int D);
 
+/*
+ * based_delta_fwd: the gated delta rule, a linear attention whose state (K,V) decays and corrects what it
+ * has stored: per batch entry and head, for t = 0 .. T-1,
+ *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),   S_t = a_t S_{t-1} + k_t u_t^T,   o_t = scale S_t^T q_t,
+ * with a = exp(gate), or 1 without gates. Head h of the values uses head h / (H / HK) of queries and keys.
+ * Products go through float16 pairs: as accurate as float32's relative to the largest magnitude of a
+ * row of the state's columns or of 64 rows of keys or queries; magnitudes below 2^-84 count as 0 there.
+ * Gates are meant to be <= 0 (-inf clears the state, gates below -1e5 count as -inf). Positive ones let the state grow and
+ * work as long as no 64 of them add up to more than 88. A state with an infinity or NaN has NaN from
+ * there on. Keys are taken as they are; the rule is stable where beta |k|^2 is at most 2.
+ *   q, k         (B,T,HK,K) of `dtype`, strides (sb, st, sh, 1)
+ *   v            (B,T,H,V) of `dtype`, strides (sb, st, sh, 1)
+ *   beta, gate   (B,T,H) of `dtype`, strides (sb, st, 1); gate may be NULL
+ *   scale        <= 0 selects K^-0.5
+ *   state        (B,H,K,V) float32: S_{-1}; NULL is zero
+ *   lengths      (B) int32 or NULL: rows t >= lengths[b] are padding: they leave the state as it is, their
+ *                inputs are not read and their outputs are zero. Values are clamped to [0, T].
+ *   o            (B,T,H,V) of `dtype`, contiguous
+ *   final_state  (B,H,K,V) float32 or NULL: S_{T-1}; may be `state` itself
+ *   states       (B, ceil(T / BASED_DELTA_ROWS), H, K, V) float32, the states in front of rows 0, 64, ..., and
+ *   errors       (B,T,H,V) float32, v_t - a_t S_{t-1}^T k_t: what based_delta_bwd reads (16-byte aligned; both or
+ *                neither NULL; unspecified in chunks and rows of padding)
+ *   workspace    based_delta_workspace_size(..., 0) bytes
+ * H must be a multiple of HK, K at most 128, V at most 65536.
+ * Errors: as based_scan_fwd, BASED_ERR_WORKSPACE, BASED_ERR_BAD_ARGUMENT (a scale that is NaN).
+ */
+#define BASED_DELTA_ROWS 64
+BASED_API int based_delta_fwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, const void *k, int64_t k_sb,
+                              int64_t k_st, int64_t k_sh, const void *v, int64_t v_sb, int64_t v_st, int64_t v_sh,
+                              const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate, int64_t gate_sb,
+                              int64_t gate_st, int B, int T, int H, int HK, int K, int V, int dtype, float scale,
+                              const float *state, const int32_t *lengths, void *o, float *final_state, float *states,
+                              float *errors, void *workspace, size_t ws_bytes, based_stream_t stream);
+
+/*
+ * based_delta_bwd: gradients of based_delta_fwd for the gradients dout (B,T,H,V) of o and dfinal of final_state.
+ * Queries' and keys' gradients are summed over the heads that share them, in a fixed order.
+ *   q .. gate, scale, lengths  as given to based_delta_fwd
+ *   dout         (B,T,H,V) of `dtype`, strides (do_sb, do_st, do_sh, 1); not read in padding rows
+ *   states, errors  what based_delta_fwd wrote
+ *   dfinal       (B,H,K,V) float32 or NULL (zero)
+ *   dq, dk       (B,T,HK,K), dv (B,T,H,V), dbeta, dgate (B,T,H) of `dtype`, contiguous, zero in padding rows;
+ *                dgate if and only if there are gates; dq and dk aligned to two elements
+ *   dstate       (B,H,K,V) float32 or NULL
+ *   workspace    based_delta_workspace_size(..., 1) bytes
+ * Errors: as based_delta_fwd.
+ */
+BASED_API int based_delta_bwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, const void *k, int64_t k_sb,
+                              int64_t k_st, int64_t k_sh, const void *v, int64_t v_sb, int64_t v_st, int64_t v_sh,
+                              const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate, int64_t gate_sb,
+                              int64_t gate_st, const void *dout, int64_t do_sb, int64_t do_st, int64_t do_sh,
+                              const float *states, const float *errors, int B, int T, int H, int HK, int K, int V,
+                              int dtype, float scale, const float *dfinal, const int32_t *lengths, void *dq, void *dk,
+                              void *dv, void *dbeta, void *dgate, float *dstate, void *workspace, size_t ws_bytes,
+                              based_stream_t stream);
+
+/* Bytes of workspace based_delta_fwd() (backward 0) or based_delta_bwd() needs for these sizes (0 for sizes they refuse). */
+BASED_API size_t based_delta_workspace_size(int B, int T, int H, int HK, int K, int V, int dtype, int backward);
+
+/*
+ * based_delta_step: one row of the delta rule for N sequences whose states lie in a pool:
+ *     S = a pool[s],  u = beta (v - S^T k),  pool[s] = S + k u^T,  o_i = scale pool[s]^T q,   s = slots[i] (or i).
+ *   q, k (N,HK,K) and v (N,H,V) of `dtype`, strides (sn, sh, 1); beta, gate (N,H), strides (sn, 1); gate may be NULL
+ *   pool     (S,H,K,V) float32, contiguous, updated in place
+ *   slots    as for based_scan_step
+ *   o        (N,H,V) of `dtype`, contiguous
+ * Errors: as based_delta_fwd.
+ */
+BASED_API int based_delta_step(const void *q, int64_t q_sn, int64_t q_sh, const void *k, int64_t k_sn, int64_t k_sh,
+                               const void *v, int64_t v_sn, int64_t v_sh, const void *beta, int64_t beta_sn,
+                               const void *gate, int64_t gate_sn, int N, int H, int HK, int K, int V, int S, int dtype,
+                               float scale, float *pool, const int32_t *slots, void *o, based_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

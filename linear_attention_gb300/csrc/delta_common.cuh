@@ -1,0 +1,248 @@
+// delta_common.cuh: what the kernels of the gated delta rule share: parameters, the layout of a chunk's records,
+// float16 pairs and the matrix instructions on them.
+//
+// The kernels multiply on tensor cores and keep float32's accuracy. A float32 operand x goes in as two
+// float16 terms, hi = x s and lo = x s - hi with a power of two s that brings the largest |x| of a row or tile
+// to 2^12: together 22 bits, off by 2^-23 of that largest where bfloat16 pairs would be off by 2^-17. A product
+// of two pairs is three matrix products (lo lo, 2^-22 of the result, is left out); 16-bit inputs are one term.
+// Sums are float32. Per multiprocessor and cycle mma.sync makes 1019 float16 products (measured), a quarter of what
+// tcgen05.mma does, but its accumulators are registers: a chunk's chain of products runs
+// in one warp, which hands its results to itself without a barrier or a trip through memory.
+#pragma once
+#include "ops_common.cuh"
+
+namespace based {
+
+constexpr int kChunk = 64;         // rows of a chunk
+constexpr int kMaxKeys = 128;      // channels of a key
+constexpr int kDeltaMaxV = 1 << 16;
+
+struct DeltaParams {
+    const void *q, *k, *v, *beta, *gate, *dout;
+    int64_t q_sb, q_st, q_sh, k_sb, k_st, k_sh, v_sb, v_st, v_sh, do_sb, do_st, do_sh, beta_sb, beta_st, gate_sb, gate_st;
+    int B, T, H, HK, K, V, chunks;
+    int qk_vec, v_vec, do_vec, o_vec;  // rows can be read (written) as 16-byte words
+    float scale;
+    const int32_t *lengths;
+    const float *state;       // forward: the first state; backward: dfinal
+    float *final_state;       // forward: the last state; backward: dstate
+    float *states, *errors;   // (B,chunks,H,K,V) states in front of the chunks; (B,T,H,V) v - a S^T k
+    void *out;                // forward: o; backward: dv
+    void *dq, *dk, *dbeta, *dgate;
+    uint8_t *qk_rec, *g_rec;  // the records of the chunks
+    float *dr, *dstates;      // backward: dbeta-free gradients (B,T,H,V) of what the rows write; of the states behind the chunks
+};
+
+// The terms of an operand. Inputs of 16 bits are one float16 term (bfloat16 fits one after its scaling: 8 bits). Results that are
+// rounded to bfloat16 (2^-9) take one term, 2^-12, of what is computed; other outputs, and all that goes into a state, two.
+template <typename T>
+struct Terms {
+    static constexpr int in = 1, out = 2;
+};
+template <>
+struct Terms<__nv_bfloat16> {
+    static constexpr int in = 1, out = 1;
+};
+template <>
+struct Terms<float> {
+    static constexpr int in = 2, out = 2;
+};
+
+// A chunk's records in the workspace: images of shared memory, copied as they are.
+//   of a key head: the scaled keys and queries, TERMS x 64 x KP float16 each
+//   of a value head: the inverse (two terms), the masked scores (forward: Terms::out, backward: two), 64 x 64 float16 each, and
+//   float32 numbers: per row grow = exp(b), rest = exp(b_last - b), beta, b in two parts (b: the sum of log decays up to the row),
+//   then the scales' inverses.
+constexpr int kSquare = kChunk * kChunk * 2;  // bytes
+enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_INV = 320, F_P, F_WHOLE, F_K, F_Q, F_COUNT = 336 };
+template <typename T, int KP>
+struct Rec {
+    static constexpr int term = kChunk * KP * 2, img = Terms<T>::in * term, qk = 2 * img;
+    __host__ __device__ static constexpr int scores(bool bwd) { return bwd ? 2 : Terms<T>::out; }
+    __host__ __device__ static constexpr int g(bool bwd) { return (2 + scores(bwd)) * kSquare + F_COUNT * 4; }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Images: rows of COLS float16, their 16-byte words exchanged by the row so that eight rows of one column of
+// words lie in different banks
+// ------------------------------------------------------------------------------------------------
+template <int COLS>
+__device__ __forceinline__ uint32_t word_at(int row, int word) {
+    return row * (COLS * 2) + ((word ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+// Operands of a 16 x 8 x 16 product from an image X. The second operand's register pairs {r0, r1} and {r2, r3} are two blocks of
+// eight columns n:
+//   left:    A[m][k] = X[row + m][col + k]
+//   left_t:  A[m][k] = X[row + k][col + m]
+//   right:   B[k][n] = X[row + n][col + k]     (16 n)
+//   right_t: B[k][n] = X[row + k][col + n]     (16 n)
+// row and col are multiples of 16.
+template <int COLS>
+__device__ __forceinline__ void left(uint32_t (&r)[4], uint32_t img, int row, int col, int lane) {
+    ldsm(r, img + word_at<COLS>(row + (lane & 15), (col >> 3) + (lane >> 4)));
+}
+template <int COLS>
+__device__ __forceinline__ void left_t(uint32_t (&r)[4], uint32_t img, int row, int col, int lane) {
+    ldsm_t(r, img + word_at<COLS>(row + (lane & 7) + ((lane >> 4) << 3), (col >> 3) + ((lane >> 3) & 1)));
+}
+template <int COLS>
+__device__ __forceinline__ void right(uint32_t (&r)[4], uint32_t img, int row, int col, int lane) {
+    ldsm(r, img + word_at<COLS>(row + (lane & 7) + ((lane >> 4) << 3), (col >> 3) + ((lane >> 3) & 1)));
+}
+template <int COLS>
+__device__ __forceinline__ void right_t(uint32_t (&r)[4], uint32_t img, int row, int col, int lane) {
+    ldsm_t(r, img + word_at<COLS>(row + (lane & 15), (col >> 3) + (lane >> 4)));
+}
+
+using Acc = float[4];  // a 16 x 8 block: rows lane / 4 and + 8, columns 2 (lane % 4) and + 1
+
+__device__ __forceinline__ void mma(Acc &d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ------------------------------------------------------------------------------------------------
+// float16 pairs
+// ------------------------------------------------------------------------------------------------
+// The power of two that brings `most` (finite, >= 0) to [2^12, 2^13): between 2^-100 and 2^60, so that a
+// product of two inverses is a float32 number unless the product of the values is none.
+__device__ __forceinline__ float scale_for(float most) {
+    int e = 266 - static_cast<int>(__float_as_uint(most) >> 23);
+    e = e < 27 ? 27 : e > 187 ? 187 : e;
+    return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+__device__ __forceinline__ float inverse_of(float pow2) { return __uint_as_float((254u << 23) - __float_as_uint(pow2)); }
+
+__device__ __forceinline__ uint32_t half2_of(float x, float y) { return pack<__half>(Vec<2>{{x, y}}); }
+// hi and lo terms of two elements
+__device__ __forceinline__ void split(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = half2_of(x, y);
+    const Vec<2> h = unpack<__half>(hi);
+    lo = half2_of(x - h.v[0], y - h.v[1]);
+}
+template <int TERMS>
+__device__ __forceinline__ void terms(float x, float y, uint32_t (&w)[TERMS]) {
+    if constexpr (TERMS == 2)
+        split(x, y, w[0], w[1]);
+    else
+        w[0] = half2_of(x, y);
+}
+// The left operand made of two neighbouring accumulator blocks, rows scaled by s0 (lane / 4) and s1 (+ 8)
+template <int TERMS>
+__device__ __forceinline__ void left_of(uint32_t (&a)[TERMS][4], const Acc &x, const Acc &y, float s0, float s1) {
+    uint32_t w[TERMS];
+    terms<TERMS>(x[0] * s0, x[1] * s0, w);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) a[i][0] = w[i];
+    terms<TERMS>(x[2] * s1, x[3] * s1, w);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) a[i][1] = w[i];
+    terms<TERMS>(y[0] * s0, y[1] * s0, w);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) a[i][2] = w[i];
+    terms<TERMS>(y[2] * s1, y[3] * s1, w);
+#pragma unroll
+    for (int i = 0; i < TERMS; ++i) a[i][3] = w[i];
+}
+// The scales of an accumulator row over N blocks, the same in the four lanes of a row
+template <int N>
+__device__ __forceinline__ void row_scales(const Acc (&x)[N], float &s0, float &s1) {
+    float m0 = 0.0f, m1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        m0 = fmaxf(m0, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
+        m1 = fmaxf(m1, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+    }
+    s0 = scale_for(m0), s1 = scale_for(m1);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Copies
+// ------------------------------------------------------------------------------------------------
+// 16 bytes, of which the first `bytes` are read and the others become zero
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes = 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Eight elements at p, of which the first n exist; the others are zero. vec: p is on 16 bytes and n is 8, or in float32 4 or 8.
+template <typename T>
+__device__ __forceinline__ void load8(float (&x)[8], const T *p, int n, bool vec) {
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 2) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Vec<2> f = unpack<T>(u[i]);
+                x[2 * i] = f.v[0], x[2 * i + 1] = f.v[1];
+            }
+        } else {
+            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f32(p[i]) : 0.0f;
+    }
+}
+// The terms of eight scaled elements as a word of each term's image
+template <int TERMS>
+__device__ __forceinline__ void words_of(uint4 (&w)[TERMS], const float (&x)[8], float s) {
+    uint32_t t[4][TERMS];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) terms<TERMS>(x[2 * i] * s, x[2 * i + 1] * s, t[i]);
+#pragma unroll
+    for (int j = 0; j < TERMS; ++j) w[j] = make_uint4(t[0][j], t[1][j], t[2][j], t[3][j]);
+}
+__device__ __forceinline__ float most8(float m, const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    return m;
+}
+// The largest of the CTA's m >= 0; at: WARPS places that nothing else uses between the barriers in front and behind
+template <int WARPS>
+__device__ __forceinline__ float cta_most(float m, float *at) {
+    const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = __uint_as_float(w);
+    __syncthreads();
+    float r = at[0];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) r = fmaxf(r, at[i]);
+    __syncthreads();
+    return r;
+}
+
+// The rows of batch entry b that exist.
+__device__ __forceinline__ int live_rows(const DeltaParams &p, int b) {
+    if (!p.lengths) return p.T;
+    const int n = p.lengths[b];
+    return n < 0 ? 0 : n > p.T ? p.T : n;
+}
+
+}  // namespace based

@@ -430,6 +430,126 @@ PyObject *embed_bwd(PyObject *const *a) {
     return wrap(dtable);
 }
 
+// q, k (..., HK, K) and v (..., H, V) of one type, beta and gate (..., H)
+struct DeltaInputs {
+    const Tensor &q, &k, &v, &beta, *gate;
+    int code;
+    ScalarType type;
+    int64_t H, HK, K, V;
+    DeltaInputs(PyObject *const *a, int dims)
+        : q(tensor(a[0], "q")), k(tensor(a[1], "k")), v(tensor(a[2], "v")), beta(tensor(a[3], "beta")), gate(optional_tensor(a[4], "gate")) {
+        if (q.dim() != dims || v.dim() != dims)
+            refuse(PyExc_ValueError, dims == 4 ? "expected q and k of shape (B,T,HK,K) and v of shape (B,T,H,V)"
+                                               : "expected q and k of shape (N,HK,K) and v of shape (N,H,V)");
+        type = v.scalar_type(), code = type_code(type, "v");
+        H = v.size(dims - 2), V = v.size(dims - 1), HK = q.size(dims - 2), K = q.size(dims - 1);
+    }
+    void check(int dev) const {
+        c10::SmallVector<int64_t, 4> keys(v.sizes().begin(), v.sizes().end()), heads(v.sizes().begin(), v.sizes().end() - 1);
+        keys[keys.size() - 2] = HK, keys[keys.size() - 1] = K;
+        input(v, "v", v.sizes(), type, dev);
+        input(q, "q", keys, type, dev);
+        input(k, "k", keys, type, dev);
+        input(beta, "beta", heads, type, dev);
+        if (gate) input(*gate, "gate", heads, type, dev);
+    }
+    const void *gate_data() const { return gate ? gate->data_ptr() : nullptr; }
+    int64_t gate_stride(int i) const { return gate ? gate->stride(i) : 0; }
+};
+// a scale; None selects the default
+float scale_arg(PyObject *o) { return o == Py_None ? 0.0f : static_cast<float>(float_arg(o)); }
+int64_t delta_chunks(int64_t T) { return (T + BASED_DELTA_ROWS - 1) / BASED_DELTA_ROWS; }
+
+// q, k, v, beta, gate, scale, state, lengths, save, out, final_state, workspace, stream
+PyObject *delta_fwd(PyObject *const *a) {
+    const DeltaInputs in(a, 4);
+    const float scale = scale_arg(a[5]);
+    const Place at(in.v, "v", a[12]);
+    in.check(at.dev);
+    const int64_t B = in.v.size(0), T = in.v.size(1), H = in.H, K = in.K, V = in.V;
+    const int save = PyObject_IsTrue(a[8]);
+    if (save < 0) throw Refusal();
+    void *state = whole(optional_tensor(a[6], "state"), "state", {B, H, K, V}, kF32, at.dev);
+    void *lengths = whole(optional_tensor(a[7], "lengths"), "lengths", {B}, ScalarType::Int, at.dev);
+    const Tensor o = at.output(a[9], "out", in.v.sizes(), in.type), last = at.output(a[10], "final_state", {B, H, K, V}, kF32);
+    Tensor states, errors;
+    if (save) states = at.empty({B, delta_chunks(T), H, K, V}, kF32), errors = at.empty({B, T, H, V}, kF32);
+    const auto result = [&] {
+        return tuple(wrap(o), wrap(last), save ? tuple(wrap(states), wrap(errors)) : none());
+    };
+    if ((B == 0 || T == 0) && H > 0 && K > 0 && V > 0) {
+        settle(last, optional_tensor(a[6], "state"));
+        return result();
+    }
+    const Tensor ws = workspace(a[11], a[11] == Py_None ? based_delta_workspace_size(small(B), small(T), small(H), small(in.HK), small(K), small(V), in.code, 0) : 0, at);
+    check(based_delta_fwd(in.q.data_ptr(), in.q.stride(0), in.q.stride(1), in.q.stride(2), in.k.data_ptr(), in.k.stride(0), in.k.stride(1),
+                          in.k.stride(2), in.v.data_ptr(), in.v.stride(0), in.v.stride(1), in.v.stride(2), in.beta.data_ptr(),
+                          in.beta.stride(0), in.beta.stride(1), in.gate_data(), in.gate_stride(0), in.gate_stride(1), small(B), small(T),
+                          small(H), small(in.HK), small(K), small(V), in.code, scale, static_cast<float *>(state),
+                          static_cast<int32_t *>(lengths), o.data_ptr(), static_cast<float *>(last.data_ptr()),
+                          save ? static_cast<float *>(states.data_ptr()) : nullptr, save ? static_cast<float *>(errors.data_ptr()) : nullptr,
+                          ws.data_ptr(), ws.nbytes(), at.raw()),
+          "based_delta_fwd");
+    return result();
+}
+
+// q, k, v, beta, gate, dout, saved, scale, dfinal, lengths, workspace, stream
+PyObject *delta_bwd(PyObject *const *a) {
+    const DeltaInputs in(a, 4);
+    const Tensor &dout = tensor(a[5], "dout");
+    const float scale = scale_arg(a[7]);
+    const Place at(in.v, "v", a[11]);
+    in.check(at.dev);
+    input(dout, "dout", in.v.sizes(), in.type, at.dev);
+    const int64_t B = in.v.size(0), T = in.v.size(1), H = in.H, K = in.K, V = in.V;
+    if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2)
+        refuse(PyExc_ValueError, "based_delta_bwd needs what based_delta_fwd(..., save=True) saved");
+    void *states = whole(&tensor(PyTuple_GET_ITEM(a[6], 0), "saved"), "saved states", {B, delta_chunks(T), H, K, V}, kF32, at.dev);
+    void *errors = whole(&tensor(PyTuple_GET_ITEM(a[6], 1), "saved"), "saved errors", {B, T, H, V}, kF32, at.dev);
+    void *dfinal = whole(optional_tensor(a[8], "dfinal"), "dfinal", {B, H, K, V}, kF32, at.dev);
+    void *lengths = whole(optional_tensor(a[9], "lengths"), "lengths", {B}, ScalarType::Int, at.dev);
+    const Tensor dq = at.empty(in.q.sizes(), in.type), dk = at.empty(in.q.sizes(), in.type), dv = at.empty(in.v.sizes(), in.type),
+                 dbeta = at.empty({B, T, H}, in.type), dstate = at.empty({B, H, K, V}, kF32);
+    Tensor dgate;
+    if (in.gate) dgate = at.empty({B, T, H}, in.type);
+    const auto result = [&] { return tuple(wrap(dq), wrap(dk), wrap(dv), wrap(dbeta), wrap_or_none(dgate), wrap(dstate)); };
+    if ((B == 0 || T == 0) && H > 0 && K > 0 && V > 0) {
+        settle(dstate, optional_tensor(a[8], "dfinal"));
+        return result();
+    }
+    const Tensor ws = workspace(a[10], a[10] == Py_None ? based_delta_workspace_size(small(B), small(T), small(H), small(in.HK), small(K), small(V), in.code, 1) : 0, at);
+    check(based_delta_bwd(in.q.data_ptr(), in.q.stride(0), in.q.stride(1), in.q.stride(2), in.k.data_ptr(), in.k.stride(0), in.k.stride(1),
+                          in.k.stride(2), in.v.data_ptr(), in.v.stride(0), in.v.stride(1), in.v.stride(2), in.beta.data_ptr(),
+                          in.beta.stride(0), in.beta.stride(1), in.gate_data(), in.gate_stride(0), in.gate_stride(1), dout.data_ptr(),
+                          dout.stride(0), dout.stride(1), dout.stride(2), static_cast<float *>(states), static_cast<float *>(errors),
+                          small(B), small(T), small(H), small(in.HK), small(K), small(V), in.code, scale, static_cast<float *>(dfinal),
+                          static_cast<int32_t *>(lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dbeta.data_ptr(),
+                          in.gate ? dgate.data_ptr() : nullptr, static_cast<float *>(dstate.data_ptr()), ws.data_ptr(), ws.nbytes(), at.raw()),
+          "based_delta_bwd");
+    return result();
+}
+
+// q, k, v, beta, gate, pool, scale, slots, out, stream
+PyObject *delta_step(PyObject *const *a) {
+    const DeltaInputs in(a, 3);
+    const Tensor &pool = tensor(a[5], "pool");
+    if (pool.dim() != 4) refuse(PyExc_ValueError, "expected pool of shape (S,H,K,V)");
+    const float scale = scale_arg(a[6]);
+    const Place at(in.v, "v", a[9]);
+    in.check(at.dev);
+    const int64_t N = in.v.size(0), S = pool.size(0);
+    void *states = whole(&pool, "pool", {S, in.H, in.K, in.V}, kF32, at.dev);
+    void *slots = whole(optional_tensor(a[7], "slots"), "slots", {N}, ScalarType::Int, at.dev);
+    const Tensor o = at.output(a[8], "out", in.v.sizes(), in.type);
+    if (N == 0 && in.H > 0 && in.K > 0 && in.V > 0) return wrap(o);
+    check(based_delta_step(in.q.data_ptr(), in.q.stride(0), in.q.stride(1), in.k.data_ptr(), in.k.stride(0), in.k.stride(1), in.v.data_ptr(),
+                           in.v.stride(0), in.v.stride(1), in.beta.data_ptr(), in.beta.stride(0), in.gate_data(), in.gate_stride(0),
+                           small(N), small(in.H), small(in.HK), small(in.K), small(in.V), small(S), in.code, scale,
+                           static_cast<float *>(states), static_cast<int32_t *>(slots), o.data_ptr(), at.raw()),
+          "based_delta_step");
+    return wrap(o);
+}
+
 // A Python function of COUNT positional arguments. Nothing is thrown past it: torch's errors (such
 // as memory that cannot be had) become Python's.
 template <PyObject *(*F)(PyObject *const *), int COUNT>
@@ -463,6 +583,9 @@ PyMethodDef g_methods[] = {method<scan_fwd, 9>("scan_fwd"),
                            method<norm_bwd, 10>("norm_bwd"),
                            method<embed_fwd, 5>("embed_fwd"),
                            method<embed_bwd, 8>("embed_bwd"),
+                           method<delta_fwd, 13>("delta_fwd"),
+                           method<delta_bwd, 12>("delta_bwd"),
+                           method<delta_step, 10>("delta_step"),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "based_ops_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

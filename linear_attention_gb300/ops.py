@@ -68,7 +68,15 @@ def library():
     L.based_embed_fwd.argtypes = [p, i, p, l, l, i, i, i, f, p, p]
     L.based_embed_bwd.argtypes = [p, i, p, l, l, i, i, i, f, p, i, p, z, p]
     L.based_embed_bwd_workspace_size.argtypes = [l, i, i]
-    for name in ("scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd", "embed_fwd", "embed_bwd"):
+    heads = [l, l, l]
+    L.based_delta_fwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, i, i, i, i, i, i, i, f, p, p, p, p, p, p, p, z, p]
+    L.based_delta_bwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, p, *heads, p, p, i, i, i, i, i, i, i, f, p, p,
+                                  p, p, p, p, p, p, p, z, p]
+    L.based_delta_step.argtypes = [p, l, l, p, l, l, p, l, l, p, l, p, l, i, i, i, i, i, i, i, f, p, p, p, p]
+    L.based_delta_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    L.based_delta_workspace_size.restype = z
+    for name in ("scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd", "embed_fwd", "embed_bwd", "delta_fwd", "delta_bwd",
+                 "delta_step"):
         getattr(L, "based_" + name).restype = i
     L.based_norm_bwd_workspace_size.restype = z
     L.based_embed_bwd_workspace_size.restype = z
@@ -174,3 +182,50 @@ def based_embed_bwd(ids: torch.Tensor, dy: torch.Tensor, rows: int, scale: float
 def embed_bwd_workspace_size(n: int, rows: int, channels: int) -> int:
     """Bytes of workspace based_embed_bwd takes for n tokens and a table of these sizes."""
     return library().based_embed_bwd_workspace_size(n, rows, channels)
+
+
+# ------------------------------------------------------------------------------------------------
+# Gated delta rule
+# ------------------------------------------------------------------------------------------------
+Saved = Tuple[torch.Tensor, torch.Tensor]
+
+
+def based_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                    scale: Optional[float] = None, state: Optional[torch.Tensor] = None,
+                    lengths: Optional[torch.Tensor] = None, save: bool = False, out: Optional[torch.Tensor] = None,
+                    final_state: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, Optional[Saved]]:
+    """S_t = a_t S_{t-1} + k_t u_t^T with u_t = beta_t (v_t - a_t S_{t-1}^T k_t), o_t = scale S_t^T q_t along axis 1 of
+    q, k (B,T,HK,K) and v (B,T,H,V); a = exp(gate), or 1 without a gate; beta and gate (B,T,H) have the type of v.
+
+    Heads of v share the HK heads of q and k in consecutive groups. ``scale`` defaults to K^-0.5. ``state`` (B,H,K,V)
+    float32 is S before the first row (default zero); ``lengths`` (B) int32 marks rows t >= lengths[b] as padding
+    (zero output, state kept). Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the pair of
+    float32 tensors that based_delta_bwd needs, or None without ``save``). ``final_state`` may be ``state``, to update
+    it in place. ``workspace``: a CUDA byte tensor of at least delta_workspace_size(...) bytes (default: one is allocated).
+    """
+    return _C.delta_fwd(q, k, v, beta, gate, scale, state, lengths, save, out, final_state, workspace, stream)
+
+
+def based_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor],
+                    dout: torch.Tensor, saved: Saved, scale: Optional[float] = None, dfinal: Optional[torch.Tensor] = None,
+                    lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of based_delta_fwd for the gradients dout (B,T,H,V) of its output and dfinal (B,H,K,V) float32 of its
+    last state: (dq, dk, dv, dbeta, dgate, dstate), dgate None without a gate. ``saved`` is what the forward call returned."""
+    return _C.delta_bwd(q, k, v, beta, gate, dout, saved, scale, dfinal, lengths, workspace, stream)
+
+
+def based_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor],
+                     pool: torch.Tensor, scale: Optional[float] = None, slots: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One row of the delta rule for q, k (N,HK,K), v (N,H,V), beta and gate (N,H): ``pool`` (S,H,K,V) float32 holds the
+    states and is updated in place; slots as in based_scan_step. Returns o (N,H,V)."""
+    return _C.delta_step(q, k, v, beta, gate, pool, scale, slots, out, stream)
+
+
+def delta_workspace_size(batch: int, rows: int, heads: int, key_heads: int, key_size: int, value_size: int,
+                         dtype: torch.dtype = torch.bfloat16, backward: bool = False) -> int:
+    """Bytes of workspace based_delta_fwd or based_delta_bwd takes for these sizes."""
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    return library().based_delta_workspace_size(batch, rows, heads, key_heads, key_size, value_size, code, int(backward))
