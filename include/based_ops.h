@@ -248,6 +248,64 @@ BASED_API int based_delta_step(const void *q, int64_t q_sn, int64_t q_sh, const 
                                const void *gate, int64_t gate_sn, int N, int H, int HK, int K, int V, int S, int dtype,
                                float scale, float *pool, const int32_t *slots, void *o, based_stream_t stream);
 
+/*
+ * based_rms_fwd: root-mean-square norm of a residual stream, with the addition in front of it:
+ *     s = x + residual, rounded to s_dtype (or s = x),   y = s / sqrt(mean(s^2) + eps) * weight,
+ * the mean over the C channels of a row. The norm is that of the s that is written.
+ *   x         (R,C) of dtype, row stride x_sr
+ *   residual  (R,C) of s_dtype (dtype or BASED_F32), row stride res_sr, or NULL
+ *   weight    (C) of p_dtype (dtype or BASED_F32), or NULL (1)
+ *   sum       (R,C) of s_dtype, contiguous: s; NULL if and only if there is no residual; may be `residual` where that is contiguous
+ *   y         (R,C) contiguous, of dtype; or, where scales are given, e4m3 bytes (one an element):
+ *             y = y8 * scales[row] with scales[row] = max|y| / 448 (1 for a row of zeros), rounded to nearest even
+ *   scales    (R) float32 or NULL
+ * C is at most 16384. Errors: as based_scan_fwd.
+ */
+BASED_API int based_rms_fwd(const void *x, int64_t x_sr, const void *residual, int64_t res_sr, int s_dtype,
+                            const void *weight, int p_dtype, int64_t R, int C, float eps, void *sum, void *y, int dtype,
+                            float *scales, based_stream_t stream);
+
+/*
+ * based_rms_bwd: gradients of based_rms_fwd (its output of dtype).
+ *   dy       (R,C) of dtype, row stride dy_sr
+ *   s        the sum that based_rms_fwd wrote (without a residual its x), (R,C) of s_dtype, row stride s_sr
+ *   dsum     (R,C) of s_dtype, row stride dsum_sr: what comes back along the stream, added to ds; or NULL
+ *   ds       (R,C) of s_dtype, contiguous: the gradient of the residual (and of x); may be `dsum` where that is contiguous
+ *   dx       (R,C) of dtype, contiguous: ds in the type of x; NULL if and only if s_dtype is dtype
+ *   dweight  (C) of p_dtype or NULL; summed in float32 in an order that the sizes fix
+ *   workspace  based_rms_bwd_workspace_size() bytes (none where dweight is NULL)
+ * Errors: as based_rms_fwd, BASED_ERR_WORKSPACE.
+ */
+BASED_API int based_rms_bwd(const void *dy, int64_t dy_sr, const void *s, int64_t s_sr, int s_dtype, const void *weight,
+                            int p_dtype, const void *dsum, int64_t dsum_sr, int64_t R, int C, float eps, void *ds,
+                            void *dx, void *dweight, int dtype, void *workspace, size_t ws_bytes,
+                            based_stream_t stream);
+
+/* Bytes of workspace based_rms_bwd() needs for these sizes, with dweight (0 for sizes it refuses). */
+BASED_API size_t based_rms_bwd_workspace_size(int64_t R, int C);
+
+/*
+ * based_sample: the next token of each row of logits, from given random numbers. Tokens are ordered by falling logits, equal ones
+ * by rising index; with p_i the softmax of logits / temperature, a row keeps
+ *     the first top_k of the order; of these the fewest of the first whose p reach the share top_p of theirs;
+ *     and of these the ones with p_i >= min_p max(p),
+ * and takes, in the order of indices, the first whose kept p sum up to more than u times the sum of all kept ones.
+ *   logits       (N,V) of dtype, row stride `stride`. -inf is never taken, NaN counts as -inf. A row of -inf gives token -1 and
+ *                probability 0; a row with +inf its first +inf.
+ *   u            (N) float32 in [0, 1)
+ *   temperature, top_k, top_p, min_p  (N) float32 (top_k int32), one for each row, or NULL: then the value behind it holds for all rows.
+ *                temperature <= 0 takes the first of the order; top_k <= 0, top_p >= 1 and min_p <= 0 keep all; top_p <= 0 keeps the first; NaN keeps all
+ *                (as a temperature: the first).
+ *   tokens       (N) int32
+ *   probs        (N) float32 or NULL: the token's share of what its row keeps
+ * Probabilities are computed in float32 (to 2^-21) and summed as whole multiples of 2^-40 of the largest: tokens below that have none.
+ * V is at most 2^22, N at most 2^26. Errors: as based_scan_fwd.
+ */
+BASED_API int based_sample(const void *logits, int64_t stride, int dtype, int N, int V, const float *u,
+                           const float *temperature, float temperature_all, const int32_t *top_k, int top_k_all,
+                           const float *top_p, float top_p_all, const float *min_p, float min_p_all, int32_t *tokens,
+                           float *probs, based_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,8 @@ embedding; ``include/based_ops.h``) are bound by ``linear_attention_gb300.ops``.
 import importlib
 
 _OPS = ("based_scan_fwd", "based_scan_bwd", "based_scan_step", "based_norm_fwd", "based_norm_bwd",
-        "based_embed_fwd", "based_embed_bwd", "based_delta_fwd", "based_delta_bwd", "based_delta_step")
+        "based_embed_fwd", "based_embed_bwd", "based_delta_fwd", "based_delta_bwd", "based_delta_step",
+        "based_rms_fwd", "based_rms_bwd", "based_sample")
 __all__ = ["based_fwd", "based_fwd_host", *_OPS]
 
 

@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libbased_gb300.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("based_fwd.cu", "based_scan.cu", "based_norm.cu", "based_embed.cu",
-                                              "based_delta.cu")]
+                                              "based_delta.cu", "based_rms.cu", "based_sample.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, "based_kernels.cuh"), os.path.join(CSRC, "sm103_ptx.cuh"),
                   os.path.join(CSRC, "based_plan.h"), os.path.join(CSRC, "ops_common.cuh"), os.path.join(CSRC, "delta_common.cuh"),
                   os.path.join(ROOT, "include", "based.h"), os.path.join(ROOT, "include", "based_ops.h")]

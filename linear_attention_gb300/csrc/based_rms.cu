@@ -1,0 +1,397 @@
+// based_rms.cu: the root-mean-square norm of a residual stream (declared in include/based_ops.h).
+//
+//     s = x + residual (rounded to the stream's type),   y = s r w,   r = 1 / sqrt(mean(s^2) + eps)
+//     ds = r (d - s r mean(d s r)) + dsum with d = dy w,   dw = sum over rows of dy s r
+//
+// A row lies in the registers of THREADS threads, up to four packs of eight channels each, so one reading of it serves the
+// sum of squares, the largest magnitude of an 8-bit output and the result. Bound by memory. Rows of 8 to 128 packs take a part of
+// a warp or a warp; longer ones several warps, which meet once (8 bits: twice) in shared memory. CTAs walk over the rows with the weights in
+// registers; backward the weights' gradients add up there too, in an order that the sizes fix.
+#include <type_traits>
+
+#include "ops_common.cuh"
+
+namespace based {
+namespace {
+
+constexpr int kPack = 8, kMostPacks = 4, kMostThreads = 512;
+constexpr int kRmsMaxC = kPack * kMostPacks * kMostThreads;
+constexpr int kRmsCtas = 608;  // partial sums of the weights' gradient: four CTAs on each of 152 SMs
+
+struct RmsParams {
+    const void *x, *residual, *weight, *dy, *dsum;
+    int64_t x_sr, res_sr, dy_sr, dsum_sr;
+    int64_t R;
+    int C, p_dtype, ctas;
+    float eps;
+    void *sum, *y, *ds, *dx, *dweight;
+    float *scales, *partial;
+};
+
+// Channel e of pack j of a thread. Packs that are words lie side by side; single channels are dealt out one to a thread, so that either way
+// neighbouring threads read neighbouring addresses.
+template <bool WORDS>
+__device__ __forceinline__ int channel(int t, int threads, int j, int e) {
+    return WORDS ? (t + threads * j) * kPack + e : t + threads * (j * kPack + e);
+}
+template <bool WORDS, typename T>
+__device__ __forceinline__ void load_pack(float (&x)[kPack], const T *p, int t, int threads, int j, int C) {
+    if constexpr (WORDS) {
+        const int c = channel<true>(t, threads, j, 0);
+        if (c < C) {
+            const Pack<T, kPack> w = *reinterpret_cast<const Pack<T, kPack> *>(p + c);
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) x[e] = to_f32(w.v[e]);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < kPack; ++e) x[e] = 0.0f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPack; ++e) {
+            const int c = channel<false>(t, threads, j, e);
+            x[e] = c < C ? to_f32(p[c]) : 0.0f;
+        }
+    }
+}
+template <bool WORDS, typename T>
+__device__ __forceinline__ void store_pack(T *p, const float (&x)[kPack], int t, int threads, int j, int C) {
+    if constexpr (WORDS) {
+        const int c = channel<true>(t, threads, j, 0);
+        if (c < C) {
+            Pack<T, kPack> w;
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) w.v[e] = from_f32<T>(x[e]);
+            *reinterpret_cast<Pack<T, kPack> *>(p + c) = w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPack; ++e) {
+            const int c = channel<false>(t, threads, j, e);
+            if (c < C) p[c] = from_f32<T>(x[e]);
+        }
+    }
+}
+// Two elements in e4m3, to nearest even; beyond 448 they become 448
+__device__ __forceinline__ uint32_t e4m3_pair(float x, float y) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+    return r;
+}
+template <bool WORDS>
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[kPack], int t, int threads, int j, int C) {
+    if constexpr (WORDS) {
+        const int c = channel<true>(t, threads, j, 0);
+        if (c < C)
+            *reinterpret_cast<uint2 *>(p + c) = make_uint2(e4m3_pair(x[0], x[1]) | e4m3_pair(x[2], x[3]) << 16,
+                                                           e4m3_pair(x[4], x[5]) | e4m3_pair(x[6], x[7]) << 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPack; ++e) {
+            const int c = channel<false>(t, threads, j, e);
+            if (c < C) p[c] = static_cast<uint8_t>(e4m3_pair(x[e], 0.0f));
+        }
+    }
+}
+template <typename T, bool WORDS>
+__device__ __forceinline__ void load_weight(float (&w)[kPack], const RmsParams &p, int t, int threads, int j) {
+    if (!p.weight) {
+#pragma unroll
+        for (int e = 0; e < kPack; ++e) w[e] = channel<WORDS>(t, threads, j, e) < p.C ? 1.0f : 0.0f;
+    } else if (p.p_dtype == BASED_F32) {
+        load_pack<WORDS>(w, static_cast<const float *>(p.weight), t, threads, j, p.C);
+    } else {
+        load_pack<WORDS>(w, static_cast<const T *>(p.weight), t, threads, j, p.C);
+    }
+}
+
+// The sum or the largest of v over the THREADS threads of a row; red: 32 floats of the CTA, two rows of them used in turn
+template <int THREADS, bool MOST>
+__device__ __forceinline__ float over_row(float v, float *red, int &turn) {
+    constexpr int kLanes = THREADS < 32 ? THREADS : 32, kWarps = THREADS / 32;
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = MOST ? fmaxf(v, o) : v + o;
+    }
+    if constexpr (kWarps > 1) {
+        float *const at = red + turn * 32 + threadIdx.x / THREADS * kWarps;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) at[threadIdx.x % THREADS / 32] = v;
+        __syncthreads();
+        v = at[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) v = MOST ? fmaxf(v, at[i]) : v + at[i];
+    }
+    return v;
+}
+
+__host__ __device__ constexpr int cta_of(int threads) { return threads < 256 ? 256 : threads; }
+
+template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
+__global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParams p) {
+    constexpr int kRows = cta_of(THREADS) / THREADS;
+    __shared__ float red[64];
+    int turn = 0;
+    const int t = threadIdx.x % THREADS, slot = threadIdx.x / THREADS;
+    griddep_wait();
+    float w[PACKS][kPack];
+#pragma unroll
+    for (int j = 0; j < PACKS; ++j) load_weight<T, WORDS>(w[j], p, t, THREADS, j);
+    const float mean = 1.0f / p.C;
+    // all threads of the CTA go round equally often: rows behind the last are computed as zeros and not stored
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.R; first += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t row = first + slot;
+        const bool there = row < p.R;
+        const int C = there ? p.C : 0;
+        float s[PACKS][kPack], sq = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) load_pack<WORDS>(s[j], static_cast<const T *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+        if (p.residual) {
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j) {
+                float r[kPack];
+                load_pack<WORDS>(r, static_cast<const S *>(p.residual) + row * p.res_sr, t, THREADS, j, C);
+#pragma unroll
+                for (int e = 0; e < kPack; ++e) s[j][e] = to_f32(from_f32<S>(s[j][e] + r[e]));  // what is written is what is normed
+            }
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j) store_pack<WORDS>(static_cast<S *>(p.sum) + row * p.C, s[j], t, THREADS, j, C);
+        }
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) sq = fmaf(s[j][e], s[j][e], sq);
+        const float r = rsqrtf(over_row<THREADS, false>(sq, red, turn) * mean + p.eps);
+        float most = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) {
+                s[j][e] = s[j][e] * r * w[j][e];
+                asm("max.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(most), "f"(fabsf(s[j][e])));
+            }
+        if (p.scales) {
+            most = over_row<THREADS, true>(most, red, turn);
+            const float scale = most > 0.0f ? fmaxf(most / 448.0f, 1.17549435e-38f) : 1.0f, inverse = 1.0f / scale;
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j) {
+#pragma unroll
+                for (int e = 0; e < kPack; ++e) s[j][e] *= inverse;
+                store_e4m3<WORDS>(static_cast<uint8_t *>(p.y) + row * p.C, s[j], t, THREADS, j, C);
+            }
+            if (t == 0 && there) p.scales[row] = scale;
+        } else {
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j) store_pack<WORDS>(static_cast<T *>(p.y) + row * p.C, s[j], t, THREADS, j, C);
+        }
+    }
+}
+
+template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
+__global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParams p) {
+    constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
+    __shared__ float red[64];
+    extern __shared__ float sums[];  // rows' threads' sums of the weights' gradient, where a CTA takes several rows
+    int turn = 0;
+    const int t = threadIdx.x % THREADS, slot = threadIdx.x / THREADS;
+    griddep_wait();
+    float w[PACKS][kPack], dw[PACKS][kPack] = {};
+#pragma unroll
+    for (int j = 0; j < PACKS; ++j) load_weight<T, WORDS>(w[j], p, t, THREADS, j);
+    const float mean = 1.0f / p.C;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.R; first += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t row = first + slot;
+        const int C = row < p.R ? p.C : 0;
+        float s[PACKS][kPack], d[PACKS][kPack], sq = 0.0f, ds = 0.0f;
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) {
+            load_pack<WORDS>(s[j], static_cast<const S *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+            load_pack<WORDS>(d[j], static_cast<const T *>(p.dy) + row * p.dy_sr, t, THREADS, j, C);
+        }
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) sq = fmaf(s[j][e], s[j][e], sq), ds = fmaf(d[j][e] * w[j][e], s[j][e], ds);
+        const float r = rsqrtf(over_row<THREADS, false>(sq, red, turn) * mean + p.eps);
+        const float back = over_row<THREADS, false>(ds, red, turn) * mean * r * r;  // mean(d s) r^2
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) {
+            float g[kPack];
+            if (p.dsum)
+                load_pack<WORDS>(g, static_cast<const S *>(p.dsum) + row * p.dsum_sr, t, THREADS, j, C);
+            else
+#pragma unroll
+                for (int e = 0; e < kPack; ++e) g[e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) {
+                dw[j][e] = fmaf(d[j][e], s[j][e] * r, dw[j][e]);
+                g[e] += r * (d[j][e] * w[j][e] - s[j][e] * back);
+            }
+            store_pack<WORDS>(static_cast<S *>(p.ds) + row * p.C, g, t, THREADS, j, C);
+            if constexpr (!std::is_same<T, S>::value) store_pack<WORDS>(static_cast<T *>(p.dx) + row * p.C, g, t, THREADS, j, C);
+        }
+    }
+    if (!p.dweight) return;
+    float *const out = p.partial + static_cast<int64_t>(blockIdx.x) * p.C;
+    if constexpr (kRows == 1) {
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) store_pack<WORDS>(out, dw[j], t, THREADS, j, p.C);
+    } else {
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+            for (int e = 0; e < kPack; ++e) {
+                const int c = channel<WORDS>(t, THREADS, j, e);
+                if (c < p.C) sums[slot * p.C + c] = dw[j][e];
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.C; c += kCta) {
+            float v = sums[c];
+            for (int i = 1; i < kRows; ++i) v += sums[i * p.C + c];
+            out[c] = v;
+        }
+    }
+}
+
+// dweight from the CTAs' sums: 32 channels a CTA, its 32 warps take every 32nd sum
+template <typename P>
+__global__ void __launch_bounds__(1024) based_rms_sum_kernel(RmsParams p) {
+    __shared__ float part[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    griddep_wait();
+    float v = 0.0f;
+    if (c < p.C) {
+#pragma unroll 4
+        for (int i = warp; i < p.ctas; i += 32) v += p.partial[static_cast<int64_t>(i) * p.C + c];
+    }
+    part[warp][lane] = v;
+    __syncthreads();
+    v = part[lane][warp];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+    const int to = blockIdx.x * 32 + warp;
+    if (lane == 0 && to < p.C) static_cast<P *>(p.dweight)[to] = from_f32<P>(v);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Host
+// ------------------------------------------------------------------------------------------------
+template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
+int launch_rms(RmsParams &p, bool bwd, int sms, cudaStream_t st) {
+    constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
+    const int64_t groups = (p.R + kRows - 1) / kRows;
+    if (!bwd) {
+        void (*const fwd)(RmsParams) = based_rms_fwd_kernel<T, S, THREADS, PACKS, WORDS>;
+        int per_sm = 0;
+        if (const int rc = resident_clusters(reinterpret_cast<const void *>(fwd), kCta, 0, 1, &per_sm)) return rc;
+        const int64_t most = per_sm > 0 ? per_sm : sms;  // CTAs of the device
+        OPS_CUDA(launch_op(fwd, static_cast<unsigned>(groups < most ? groups : most), kCta, 0, st, p));
+        return BASED_OK;
+    }
+    p.ctas = static_cast<int>(groups < kRmsCtas ? groups : kRmsCtas);
+    const size_t smem = kRows > 1 ? static_cast<size_t>(kRows) * p.C * 4 : 0;
+    OPS_CUDA(launch_op(based_rms_bwd_kernel<T, S, THREADS, PACKS, WORDS>, p.ctas, kCta, smem, st, p));
+    if (p.dweight) {
+        void (*const sum)(RmsParams) = p.p_dtype == BASED_F32 ? based_rms_sum_kernel<float> : based_rms_sum_kernel<T>;
+        OPS_CUDA(launch_op(sum, (p.C + 31) / 32, 1024, 0, st, p));
+    }
+    return BASED_OK;
+}
+// Threads for a row: as few as hold it in four packs each, so that a warp or a part of one serves short rows and sums stay in it
+template <typename T, typename S>
+int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
+    const int packs = (p.C + kPack - 1) / kPack;
+    if (!words) {
+        if (packs <= 128) return launch_rms<T, S, 32, 4, false>(p, bwd, sms, st);
+        if (packs <= 512) return launch_rms<T, S, 128, 4, false>(p, bwd, sms, st);
+        return launch_rms<T, S, 512, 4, false>(p, bwd, sms, st);
+    }
+    if (packs <= 8) return launch_rms<T, S, 8, 1, true>(p, bwd, sms, st);
+    if (packs <= 32) return launch_rms<T, S, 16, 2, true>(p, bwd, sms, st);
+    if (packs <= 64) return launch_rms<T, S, 32, 2, true>(p, bwd, sms, st);
+    if (packs <= 128) return launch_rms<T, S, 32, 4, true>(p, bwd, sms, st);
+    if (packs <= 256) return launch_rms<T, S, 64, 4, true>(p, bwd, sms, st);
+    if (packs <= 512) return launch_rms<T, S, 128, 4, true>(p, bwd, sms, st);
+    if (packs <= 1024) return launch_rms<T, S, 256, 4, true>(p, bwd, sms, st);
+    return launch_rms<T, S, 512, 4, true>(p, bwd, sms, st);
+}
+
+int run_rms(RmsParams &p, int dtype, int s_dtype, bool bwd, void *workspace, size_t ws_bytes, based_stream_t stream) {
+    if (!type_ok(dtype) || !type_ok(s_dtype) || (s_dtype != dtype && s_dtype != BASED_F32)) return BASED_ERR_UNSUPPORTED_TYPE;
+    if (p.weight && p.p_dtype != dtype && p.p_dtype != BASED_F32) return BASED_ERR_UNSUPPORTED_TYPE;
+    if (!(p.eps >= 0.0f)) return BASED_ERR_BAD_ARGUMENT;
+    if (p.R < 1 || p.C < 1 || p.C > kRmsMaxC || p.R > (static_cast<int64_t>(1) << 46) / p.C) return BASED_ERR_BAD_SIZE;
+    if (p.x_sr < 0 || p.res_sr < 0 || p.dy_sr < 0 || p.dsum_sr < 0) return BASED_ERR_BAD_STRIDE;
+    const int64_t R = p.R, C = p.C;
+    const size_t es = elem_size(dtype), ss = elem_size(s_dtype), ps = elem_size(p.p_dtype), xs = bwd ? ss : es;
+    if (!aligned(p.x, xs) || !aligned(p.residual, ss) || !aligned(p.weight, ps) || !aligned(p.dy, es) || !aligned(p.dsum, ss) ||
+        !aligned(p.sum, ss) || (!p.scales && !aligned(p.y, es)) || !aligned(p.scales, 4) || !aligned(p.ds, ss) || !aligned(p.dx, es) ||
+        !aligned(p.dweight, ps))
+        return BASED_ERR_MISALIGNED;
+    const Span x = span(p.x, (R - 1) * p.x_sr + C - 1, xs), res = span(p.residual, (R - 1) * p.res_sr + C - 1, ss),
+               w = span(p.weight, C - 1, ps), dy = span(p.dy, (R - 1) * p.dy_sr + C - 1, es), dsum = span(p.dsum, (R - 1) * p.dsum_sr + C - 1, ss);
+    size_t need = 0;
+    if (bwd && p.dweight) {
+        need = static_cast<size_t>(R < kRmsCtas ? R : kRmsCtas) * C * 4;
+        if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return BASED_ERR_WORKSPACE;
+        p.partial = static_cast<float *>(workspace);
+    }
+    const Span in[] = {x, res, w, dy, dsum};
+    const Span out[] = {span(p.sum, R * C - 1, ss), span(p.y, R * C - 1, p.scales ? 1 : es), span(p.scales, R - 1, 4), span(p.ds, R * C - 1, ss),
+                        span(p.dx, R * C - 1, es), span(p.dweight, C - 1, ps), span(p.partial, static_cast<int64_t>(need / 4) - 1, 4)};
+    for (int i = 0; i < 7; ++i) {
+        for (int j = 0; j < 5; ++j) {
+            // the sum may replace the residual, and the gradient of the sum the one that is added to it
+            const bool place = (i == 0 && j == 1 && p.sum == p.residual && p.res_sr == C) || (i == 3 && j == 4 && p.ds == p.dsum && p.dsum_sr == C);
+            if (!place && overlap(out[i], in[j])) return BASED_ERR_ALIASING;
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return BASED_ERR_ALIASING;
+    }
+    int sms;
+    if (const int rc = host_device(&sms)) return rc;
+    const auto words = [&](const void *q, int64_t stride, size_t size) {
+        return !q || (aligned(q, size * kPack < 16 ? size * kPack : 16) && (stride * static_cast<int64_t>(size)) % 16 == 0);
+    };
+    const bool wide = C % kPack == 0 && words(p.x, p.x_sr, xs) && words(p.residual, p.res_sr, ss) && words(p.weight, 0, ps) &&
+                      words(p.dy, p.dy_sr, es) && words(p.dsum, p.dsum_sr, ss) && words(p.sum, 0, ss) && words(p.y, 0, p.scales ? 1 : es) &&
+                      words(p.ds, 0, ss) && words(p.dx, 0, es);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == BASED_F32) return launch_rms<float, float>(p, wide, bwd, sms, st);
+    if (dtype == BASED_BF16)
+        return s_dtype == BASED_F32 ? launch_rms<__nv_bfloat16, float>(p, wide, bwd, sms, st)
+                                    : launch_rms<__nv_bfloat16, __nv_bfloat16>(p, wide, bwd, sms, st);
+    return s_dtype == BASED_F32 ? launch_rms<__half, float>(p, wide, bwd, sms, st) : launch_rms<__half, __half>(p, wide, bwd, sms, st);
+}
+
+}  // namespace
+}  // namespace based
+
+extern "C" {
+
+int based_rms_fwd(const void *x, int64_t x_sr, const void *residual, int64_t res_sr, int s_dtype, const void *weight, int p_dtype, int64_t R,
+                  int C, float eps, void *sum, void *y, int dtype, float *scales, based_stream_t stream) {
+    if (!x || !y || !residual != !sum) return BASED_ERR_NULL_POINTER;
+    based::RmsParams p = {};
+    p.x = x, p.x_sr = x_sr, p.residual = residual, p.res_sr = res_sr, p.weight = weight, p.p_dtype = weight ? p_dtype : dtype;
+    p.R = R, p.C = C, p.eps = eps, p.sum = sum, p.y = y, p.scales = scales;
+    return based::run_rms(p, dtype, residual ? s_dtype : dtype, false, nullptr, 0, stream);
+}
+
+int based_rms_bwd(const void *dy, int64_t dy_sr, const void *s, int64_t s_sr, int s_dtype, const void *weight, int p_dtype, const void *dsum,
+                  int64_t dsum_sr, int64_t R, int C, float eps, void *ds, void *dx, void *dweight, int dtype, void *workspace, size_t ws_bytes,
+                  based_stream_t stream) {
+    if (!dy || !s || !ds || (s_dtype == dtype) != !dx || (dweight && !weight)) return BASED_ERR_NULL_POINTER;
+    based::RmsParams p = {};
+    p.dy = dy, p.dy_sr = dy_sr, p.x = s, p.x_sr = s_sr, p.weight = weight, p.p_dtype = weight ? p_dtype : dtype, p.dsum = dsum, p.dsum_sr = dsum_sr;
+    p.R = R, p.C = C, p.eps = eps, p.ds = ds, p.dx = dx, p.dweight = dweight;
+    return based::run_rms(p, dtype, s_dtype, true, workspace, ws_bytes, stream);
+}
+
+size_t based_rms_bwd_workspace_size(int64_t R, int C) {
+    if (R < 1 || C < 1 || C > based::kRmsMaxC || R > (static_cast<int64_t>(1) << 46) / C) return 0;
+    return static_cast<size_t>(R < based::kRmsCtas ? R : based::kRmsCtas) * C * 4;
+}
+
+}  // extern "C"

@@ -1,0 +1,495 @@
+// based_sample.cu: the choice of a next token (declared in include/based_ops.h).
+//
+// With w_i = exp((x_i - max) / temperature), each of top-k, top-p and min-p keeps a prefix of the tokens in the order of falling
+// logits (equal ones by rising index), so what is kept is one comparison with a cut: the order itself is never needed. A row lies
+// in the shared memory of a cluster. One pass over it counts tokens and masses in 2048 bins of x's distance from the largest; the cut's bin
+// follows from the bins' sums and the cut from the few tokens of that bin. A last pass sums the kept masses by warps, and the warp in which
+// the random number falls finds the token. Masses are whole numbers, w 2^40 in 64 bits: their sums do not depend on an order, so
+// the same call gives the same token. Bound by reading the logits once, for few rows by the barriers between the passes.
+#include "ops_common.cuh"
+
+namespace based {
+namespace {
+
+constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
+constexpr int kBins = 2048, kFew = 1024;  // bins; tokens of one bin that are compared with one another
+constexpr float kReach = 46.0f;           // the last bin begins at w = 2^-46
+constexpr float kMass = 1099511627776.0f; // 2^40
+constexpr int kSampleCluster = 16;
+constexpr int kSampleMostV = 1 << 22;     // whose masses' sum is below 2^63
+
+struct SampleParams {
+    const void *logits;
+    int64_t stride;
+    int V, slice, cluster, resident;  // tokens of a CTA, a multiple of eight; whether they lie in shared memory
+    int words;                        // rows can be read as 16-byte words
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all;
+    int32_t *tokens;
+    float *probs;
+};
+
+using u64 = unsigned long long;
+
+struct SampleShared {
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    u64 few_at[kFew], few_mass[kFew];
+    u64 slots[2][3];        // what this CTA hands to the others, two sets in turn
+    u64 warp[3][kSampleWarps];
+    u64 found[3];
+    uint32_t few;
+};
+
+static_assert(sizeof(SampleShared) % 16 == 0, "the tokens lie behind it");
+
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+// A token's place in the order: larger is earlier
+__device__ __forceinline__ u64 place_of(float x, int index) { return static_cast<u64>(ordered(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(index)); }
+
+// The same variable in the shared memory of another CTA of the cluster
+template <typename P>
+__device__ __forceinline__ uint32_t peer(P *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ u64 peer_load(uint32_t at) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t peer_load32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void peer_store(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
+__device__ __forceinline__ uint32_t peer_add(uint32_t at, uint32_t v) {
+    uint32_t r;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(at), "r"(v) : "memory");
+    return r;
+}
+
+template <bool MOST>
+__device__ __forceinline__ u64 over_warp(u64 v) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const u64 o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = MOST ? (o > v ? o : v) : v + o;
+    }
+    return v;
+}
+
+template <typename T>
+struct Sampler {
+    const SampleParams &p;
+    SampleShared &sh;
+    const T *row;    // this CTA's tokens, in shared memory or the row itself
+    int first, len;  // their indices
+    uint32_t rank;
+    int turn = 0;
+    int tid = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    __device__ __forceinline__ void meet() {
+        if (p.cluster > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    }
+    // Sums (or largest) over all threads of the cluster of up to three numbers, and the sums of the CTAs in front of this one. All
+    // threads get them.
+    template <int N, bool MOST = false>
+    __device__ __forceinline__ void total(u64 (&v)[N], u64 (&before)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = over_warp<MOST>(v[i]);
+            if (lane == 0) sh.warp[i][warp] = v[i];
+        }
+        __syncthreads();
+        if (tid < N) {
+            u64 s = 0;
+            for (int w = 0; w < kSampleWarps; ++w) s = MOST ? (sh.warp[tid][w] > s ? sh.warp[tid][w] : s) : s + sh.warp[tid][w];
+            sh.slots[turn][tid] = s;
+        }
+        meet();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = before[i] = 0;
+            for (uint32_t r = 0; r < static_cast<uint32_t>(p.cluster); ++r) {
+                const u64 o = p.cluster > 1 ? peer_load(peer(&sh.slots[turn][i], r)) : sh.slots[turn][i];
+                if (r < rank) before[i] += o;
+                v[i] = MOST ? (o > v[i] ? o : v[i]) : v[i] + o;
+            }
+        }
+        turn ^= 1;
+        // (the next call writes the other set; sh.warp is read before meet())
+    }
+    template <int N, bool MOST = false>
+    __device__ __forceinline__ void total(u64 (&v)[N]) {
+        u64 before[N];
+        total<N, MOST>(v, before);
+    }
+
+    // f(x, index in the slice) for this thread's tokens, in the order of their indices within a warp's rounds
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        const int per = (len + kSampleWarps * 8 - 1) / (kSampleWarps * 8) * 8, from = warp * per, to = min(len, from + per);
+        for (int i = from + 8 * lane; i < to; i += 256) eight(i, to, f);
+    }
+    template <typename F>
+    __device__ __forceinline__ void eight(int i, int to, F f) {
+        if (i + 8 <= to && p.resident) {
+            const Pack<T, 8> w = *reinterpret_cast<const Pack<T, 8> *>(row + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f(to_f32(w.v[e]), i + e);
+        } else {
+            for (int e = 0; e < 8 && i + e < to; ++e) {
+                const float x = to_f32(row[i + e]);
+                f(x == x ? x : -INFINITY, i + e);
+            }
+        }
+    }
+};
+
+// w = 2^-t, t = (most - x) log2(e) / temperature, with the product's rounding made good
+struct Weigh {
+    float most, hi, lo;
+    __device__ __forceinline__ float distance(float x) const { return x == most ? 0.0f : most - x; }
+    __device__ __forceinline__ float bits(float x) const { return distance(x) * hi; }
+    __device__ __forceinline__ float weight(float x) const {
+        const float d = distance(x), t = d * hi, r = fmaf(d, hi, -t) + d * lo;
+        const float w = ex2(-t);
+        return t < 120.0f ? fmaf(w, -0.6931471806f * r, w) : 0.0f;
+    }
+    __device__ __forceinline__ u64 mass(float x) const { return static_cast<u64>(__float2ull_rn(weight(x) * kMass)); }
+    __device__ __forceinline__ int bin(float x) const {
+        const float b = bits(x) * (kBins / kReach);
+        return b < kBins - 1 ? static_cast<int>(b) : kBins - 1;
+    }
+};
+
+// The place of the last token that is kept: with `by_mass` the first in the order at which the masses reach `target`, otherwise the
+// target'th. kept: the mass up to it. The bins' sums are there, merged: `count` and `mass` of the CTA's own part.
+template <typename T>
+__device__ u64 find_cut(Sampler<T> &s, const Weigh &w, bool by_mass, double target, u64 &kept) {
+    SampleShared &sh = s.sh;
+    const SampleParams &p = s.p;
+    // the bin: a CTA looks through its part, kBins / cluster bins, by warp 0
+    const int part = kBins / p.cluster;
+    u64 sums[2] = {0, 0}, before[2];
+    for (int i = s.tid; i < part; i += kSampleThreads) sums[0] += sh.count[s.rank * part + i], sums[1] += sh.mass[s.rank * part + i];
+    s.template total<2>(sums, before);
+    if (s.tid == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
+    __syncthreads();
+    if (s.warp == 0) {
+        u64 c = before[0], m = before[1];
+        for (int i0 = 0; i0 < part; i0 += 32) {
+            const int i = i0 + s.lane, at = s.rank * part + i;
+            const u64 ci = i < part ? sh.count[at] : 0, mi = i < part ? sh.mass[at] : 0;
+            u64 cs = ci, ms = mi;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const u64 a = __shfl_up_sync(0xffffffffu, cs, d), b = __shfl_up_sync(0xffffffffu, ms, d);
+                if (s.lane >= d) cs += a, ms += b;
+            }
+            const u64 c0 = c + cs - ci, m0 = m + ms - mi;
+            const bool here = by_mass ? static_cast<double>(m0) < target && static_cast<double>(m0 + mi) >= target
+                                      : static_cast<double>(c0) < target && static_cast<double>(c0 + ci) >= target;
+            if (here && i < part) sh.found[0] = at + 1, sh.found[1] = c0, sh.found[2] = m0;
+            c += __shfl_sync(0xffffffffu, cs, 31), m += __shfl_sync(0xffffffffu, ms, 31);
+        }
+    }
+    __syncthreads();
+    u64 at[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) at[i] = s.tid == 0 ? sh.found[i] : 0;
+    s.template total<3>(at);
+    if (at[0] == 0) {  // fewer tokens than asked for
+        kept = sums[1];
+        return 0;
+    }
+    const int bin = static_cast<int>(at[0]) - 1;
+    // its tokens, in the first CTA
+    if (s.tid == 0) sh.few = 0;
+    s.meet();
+    s.each([&](float x, int i) {
+        if (x == -INFINITY || w.bin(x) != bin) return;
+        const uint32_t n = p.cluster > 1 ? peer_add(peer(&sh.few, 0), 1) : atomicAdd(&sh.few, 1u);
+        if (n >= kFew) return;
+        const u64 pl = place_of(x, s.first + i), m = w.mass(x);
+        if (p.cluster > 1)
+            peer_store(peer(&sh.few_at[n], 0), pl), peer_store(peer(&sh.few_mass[n], 0), m);
+        else
+            sh.few_at[n] = pl, sh.few_mass[n] = m;
+    });
+    s.meet();
+    u64 few[1] = {s.rank == 0 && s.tid == 0 ? sh.few : 0u};
+    s.template total<1>(few);
+    if (few[0] <= kFew) {
+        const int n = static_cast<int>(few[0]);
+        if (s.tid == 0) sh.found[0] = sh.found[1] = 0;
+        __syncthreads();
+        if (s.rank == 0) {
+            for (int i = s.tid; i < n; i += kSampleThreads) {
+                const u64 me = sh.few_at[i], mine = sh.few_mass[i];
+                u64 c = at[1], m = at[2];
+                for (int j = 0; j < n; ++j)
+                    if (sh.few_at[j] > me) ++c, m += sh.few_mass[j];
+                const bool here = by_mass ? static_cast<double>(m) < target && static_cast<double>(m + mine) >= target
+                                          : static_cast<double>(c + 1) == target;
+                if (here) sh.found[0] = me, sh.found[1] = m + mine;
+            }
+        }
+        __syncthreads();
+        u64 cut[2] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0};
+        s.template total<2>(cut);
+        kept = cut[1];
+        return cut[0];
+    }
+    // Many tokens lie close together (equal logits, a high temperature): the cut bit by bit, the largest place with enough at or above it
+    u64 cut = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+        const u64 trial = cut | 1ull << bit;
+        u64 v[2] = {0, 0};
+        s.each([&](float x, int i) {
+            if (x != -INFINITY && place_of(x, s.first + i) >= trial) ++v[0], v[1] += by_mass ? w.mass(x) : 0;
+        });
+        s.template total<2>(v);
+        if (static_cast<double>(by_mass ? v[1] : v[0]) >= target) cut = trial;
+    }
+    u64 v[1] = {0};
+    s.each([&](float x, int i) {
+        if (x != -INFINITY && place_of(x, s.first + i) >= cut) v[0] += w.mass(x);
+    });
+    s.template total<1>(v);
+    kept = v[0];
+    return cut;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SampleParams p) {
+    extern __shared__ __align__(16) uint8_t memory[];
+    SampleShared &sh = *reinterpret_cast<SampleShared *>(memory);
+    T *const tokens = reinterpret_cast<T *>(memory + sizeof(SampleShared));
+    const int64_t n = blockIdx.x / p.cluster;
+    const uint32_t rank = p.cluster > 1 ? cluster_rank() : 0;
+    const int first = static_cast<int>(rank) * p.slice, len = max(0, min(p.slice, p.V - first));
+    griddep_wait();
+    const T *const src = static_cast<const T *>(p.logits) + n * p.stride + first;
+    Sampler<T> s = {p, sh, p.resident ? tokens : src, first, len, rank};
+    u64 best[1] = {0};
+    const auto look = [&](float x, int i) {
+        const u64 pl = place_of(x, first + i);
+        if (pl > best[0]) best[0] = pl;
+    };
+    if (p.resident && p.words) {
+        constexpr int kEl = 16 / sizeof(T);
+        const int words = (len + kEl - 1) / kEl;  // the row's last word is whole: p.words has V a multiple of it
+#pragma unroll 4
+        for (int i = threadIdx.x; i < words; i += kSampleThreads) {
+            Pack<T, kEl> w = *reinterpret_cast<const Pack<T, kEl> *>(src + i * kEl);
+#pragma unroll
+            for (int e = 0; e < kEl; ++e) {
+                float x = to_f32(w.v[e]);
+                if (!(x == x)) x = -INFINITY, w.v[e] = from_f32<T>(x);
+                look(x, i * kEl + e);
+            }
+            *reinterpret_cast<Pack<T, kEl> *>(tokens + i * kEl) = w;
+        }
+        __syncthreads();
+    } else if (p.resident) {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < len; i += kSampleThreads) {
+            float x = to_f32(src[i]);
+            if (!(x == x)) x = -INFINITY;
+            tokens[i] = from_f32<T>(x);
+            look(x, i);
+        }
+        __syncthreads();
+    } else {
+        s.each(look);
+    }
+    s.template total<1, true>(best);
+    const float most = unordered(static_cast<uint32_t>(best[0] >> 32));
+    const float temperature = p.temperature ? p.temperature[n] : p.temperature_all;
+    const bool none = !(most > -INFINITY);
+    if (none || !(temperature > 0.0f) || most == INFINITY) {
+        if (rank == 0 && threadIdx.x == 0) {
+            p.tokens[n] = none ? -1 : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(best[0]));
+            if (p.probs) p.probs[n] = none ? 0.0f : 1.0f;
+        }
+        s.meet();  // shared memory stays until the others have read it
+        return;
+    }
+    const double factor = 1.4426950408889634 / temperature;
+    Weigh w;
+    w.most = most, w.hi = static_cast<float>(factor), w.lo = static_cast<float>(factor - w.hi);
+    if (!(w.hi < 3e38f)) w.hi = 3e38f, w.lo = 0.0f;
+    int k = p.top_k ? p.top_k[n] : p.top_k_all;
+    float top_p = p.top_p ? p.top_p[n] : p.top_p_all;
+    float min_p = p.min_p ? p.min_p[n] : p.min_p_all;
+    min_p = min_p > 0.0f ? fminf(min_p, 1.0f) : 0.0f;
+    if (k <= 0 || k > p.V) k = p.V;
+    if (!(top_p < 1.0f)) top_p = 1.0f;
+    if (top_p <= 0.0f) k = 1, top_p = 1.0f;
+    u64 cut = 0;
+    if (k < p.V || top_p < 1.0f) {
+        for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.mass[i] = 0, sh.count[i] = 0;
+        __syncthreads();
+        u64 last_mass = 0, last_count = 0;  // the last bin's tokens, which may be most, without atomics
+        s.each([&](float x, int) {
+            if (x == -INFINITY) return;
+            const int bin = w.bin(x);
+            const u64 m = w.mass(x);
+            if (bin == kBins - 1) {
+                last_mass += m, ++last_count;
+            } else {
+                atomicAdd(&sh.count[bin], 1u);
+                atomicAdd(&sh.mass[bin], m);
+            }
+        });
+        last_mass = over_warp<false>(last_mass), last_count = over_warp<false>(last_count);
+        if (s.lane == 0 && last_count) atomicAdd(&sh.count[kBins - 1], static_cast<uint32_t>(last_count)), atomicAdd(&sh.mass[kBins - 1], last_mass);
+        s.meet();
+        if (p.cluster > 1) {  // this CTA's part of the bins over all CTAs, in registers until all have read
+            const int part = kBins / p.cluster;
+            u64 m[kBins / kSampleThreads];
+            uint32_t c[kBins / kSampleThreads];
+#pragma unroll
+            for (int j = 0; j < kBins / kSampleThreads; ++j) {
+                const int i = threadIdx.x + j * kSampleThreads;
+                m[j] = c[j] = 0;
+                if (i < part)
+                    for (int r = 0; r < p.cluster; ++r)
+                        m[j] += peer_load(peer(&sh.mass[rank * part + i], r)), c[j] += peer_load32(peer(&sh.count[rank * part + i], r));
+            }
+            cluster_sync();
+#pragma unroll
+            for (int j = 0; j < kBins / kSampleThreads; ++j) {
+                const int i = threadIdx.x + j * kSampleThreads;
+                if (i < part) sh.mass[rank * part + i] = m[j], sh.count[rank * part + i] = c[j];
+            }
+            __syncthreads();
+        }
+        u64 kept = 0;
+        if (k < p.V) {
+            cut = find_cut(s, w, false, static_cast<double>(k), kept);
+        } else {
+            u64 all[1] = {0};
+            const int part = kBins / p.cluster;
+            for (int i = threadIdx.x; i < part; i += kSampleThreads) all[0] += sh.mass[rank * part + i];
+            s.template total<1>(all);
+            kept = all[0];
+        }
+        if (top_p < 1.0f) {
+            u64 mass;
+            const u64 by_p = find_cut(s, w, true, static_cast<double>(top_p) * static_cast<double>(kept), mass);
+            if (by_p > cut) cut = by_p;
+        }
+    }
+    const auto mass_of = [&](float x, int i) -> u64 {
+        if (x == -INFINITY || place_of(x, first + i) < cut) return 0;
+        const float v = w.weight(x);
+        return v >= min_p ? static_cast<u64>(__float2ull_rn(v * kMass)) : 0;
+    };
+    u64 sum[1] = {0}, before[1];
+    s.each([&](float x, int i) { sum[0] += mass_of(x, i); });
+    s.template total<1>(sum, before);  // leaves the warps' sums in sh.warp
+    double target = static_cast<double>(p.u[n]) * static_cast<double>(sum[0]);
+    const double end = static_cast<double>(sum[0]) - 0.5;
+    if (!(target < end)) target = end;
+    if (!(target >= 0.0)) target = 0.0;
+    // the warp at which the sum passes the target, then its round, lane and token
+    u64 at = before[0];
+    for (int i = 0; i < s.warp; ++i) at += sh.warp[0][i];
+    if (static_cast<double>(at) <= target && static_cast<double>(at + sh.warp[0][s.warp]) > target) {
+        const int per = (len + kSampleWarps * 8 - 1) / (kSampleWarps * 8) * 8, from = s.warp * per, to = min(len, from + per);
+        for (int i0 = from; i0 < to; i0 += 256) {
+            const int i = i0 + 8 * s.lane;
+            u64 m = 0;
+            if (i < to) s.eight(i, to, [&](float x, int e) { m += mass_of(x, e); });
+            u64 up = m;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const u64 o = __shfl_up_sync(0xffffffffu, up, d);
+                if (s.lane >= d) up += o;
+            }
+            const u64 mine = at + up - m;
+            if (m && static_cast<double>(mine) <= target && static_cast<double>(mine + m) > target) {
+                u64 now = mine;
+                s.eight(i, to, [&](float x, int e) {
+                    const u64 v = mass_of(x, e);
+                    if (v && static_cast<double>(now) <= target && static_cast<double>(now + v) > target) {
+                        p.tokens[n] = first + e;
+                        if (p.probs) p.probs[n] = static_cast<float>(static_cast<double>(w.weight(x)) * kMass / static_cast<double>(sum[0]));
+                    }
+                    now += v;
+                });
+            }
+            at += __shfl_sync(0xffffffffu, up, 31);
+            if (static_cast<double>(at) > target) break;
+        }
+    }
+    s.meet();
+}
+
+// ------------------------------------------------------------------------------------------------
+// Host
+// ------------------------------------------------------------------------------------------------
+template <typename T>
+int launch_sample(SampleParams &p, int N, int sms, cudaStream_t st) {
+    constexpr int64_t kRoom = 226 * 1024 - static_cast<int64_t>(sizeof(SampleShared));
+    constexpr int64_t kShare = kRoom / 2 - 24 * 1024;  // two CTAs on an SM
+    const auto bytes = [&](int cluster) {
+        return ((static_cast<int64_t>(p.V) + cluster - 1) / cluster + 7) / 8 * 8 * static_cast<int64_t>(sizeof(T));
+    };
+    // As many CTAs to a row as leave no more than the SMs', and as its tokens need to lie in shared memory
+    int cluster = 1;
+    while (cluster < kSampleCluster && (bytes(cluster) > kShare || static_cast<int64_t>(N) * cluster * 2 <= sms) && p.V / (2 * cluster) >= 1024) cluster *= 2;
+    p.cluster = cluster, p.slice = static_cast<int>(bytes(cluster) / sizeof(T)), p.resident = bytes(cluster) <= kRoom;
+    const size_t smem = sizeof(SampleShared) + (p.resident ? bytes(cluster) : 0);
+    OPS_CUDA(allow(based_sample_kernel<T>, 227 * 1024));
+    OPS_CUDA(launch_op(based_sample_kernel<T>, dim3(static_cast<unsigned>(N) * cluster), kSampleThreads, smem, st, p, cluster));
+    return BASED_OK;
+}
+
+}  // namespace
+}  // namespace based
+
+extern "C" int based_sample(const void *logits, int64_t stride, int dtype, int N, int V, const float *u, const float *temperature,
+                            float temperature_all, const int32_t *top_k, int top_k_all, const float *top_p, float top_p_all, const float *min_p,
+                            float min_p_all, int32_t *tokens, float *probs, based_stream_t stream) {
+    using namespace based;
+    if (!logits || !u || !tokens) return BASED_ERR_NULL_POINTER;
+    if (!type_ok(dtype)) return BASED_ERR_UNSUPPORTED_TYPE;
+    if (N < 1 || V < 1 || N > (1 << 26) || V > kSampleMostV) return BASED_ERR_BAD_SIZE;
+    if (stride < 0) return BASED_ERR_BAD_STRIDE;
+    const size_t es = elem_size(dtype);
+    if (!aligned(logits, es) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) ||
+        !aligned(tokens, 4) || !aligned(probs, 4))
+        return BASED_ERR_MISALIGNED;
+    const Span in[] = {span(logits, (N - 1) * stride + V - 1, es), span(u, N - 1, 4), span(temperature, N - 1, 4), span(top_k, N - 1, 4),
+                       span(top_p, N - 1, 4), span(min_p, N - 1, 4)};
+    const Span st = span(tokens, N - 1, 4), sp = span(probs, N - 1, 4);
+    for (const Span &s : in)
+        if (overlap(s, st) || overlap(s, sp)) return BASED_ERR_ALIASING;
+    if (overlap(st, sp)) return BASED_ERR_ALIASING;
+    int sms;
+    if (const int rc = host_device(&sms)) return rc;
+    SampleParams p = {};
+    p.logits = logits, p.stride = stride, p.V = V, p.u = u;
+    p.temperature = temperature, p.temperature_all = temperature_all, p.top_k = top_k, p.top_k_all = top_k_all;
+    p.top_p = top_p, p.top_p_all = top_p_all, p.min_p = min_p, p.min_p_all = min_p_all, p.tokens = tokens, p.probs = probs;
+    p.words = aligned(logits, 16) && stride * static_cast<int64_t>(es) % 16 == 0 && V * es % 16 == 0;
+    cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == BASED_F32) return launch_sample<float>(p, N, sms, stm);
+    if (dtype == BASED_BF16) return launch_sample<__nv_bfloat16>(p, N, sms, stm);
+    return launch_sample<__half>(p, N, sms, stm);
+}

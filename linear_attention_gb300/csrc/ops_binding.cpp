@@ -550,6 +550,104 @@ PyObject *delta_step(PyObject *const *a) {
     return wrap(o);
 }
 
+// x, weight, residual, eps, quantize, out, sum_out, stream
+PyObject *rms_fwd(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x"), *weight = optional_tensor(a[1], "weight"), *residual = optional_tensor(a[2], "residual");
+    if (x.dim() < 1) refuse(PyExc_ValueError, "expected x of shape (..., C)");
+    const ScalarType type = x.scalar_type(), stype = residual ? residual->scalar_type() : type, ptype = weight ? weight->scalar_type() : type;
+    const int code = type_code(type, "x"), scode = type_code(stype, "residual"), pcode = type_code(ptype, "weight");
+    const int quantize = PyObject_IsTrue(a[4]);
+    if (quantize < 0) throw Refusal();
+    const int64_t C = x.size(-1);
+    const float eps = static_cast<float>(float_arg(a[3]));
+    const Place at(x, "x", a[7]);
+    const Sizes shape = x.sizes();
+    input(x, "x", shape, type, at.dev);
+    if (residual) input(*residual, "residual", shape, stype, at.dev);
+    void *w = whole(weight, "weight", {C}, ptype, at.dev);
+    const Rows rx(x, "x"), rr(residual ? *residual : x, "residual");
+    const Tensor y = at.output(a[5], "out", shape, quantize ? ScalarType::Float8_e4m3fn : type);
+    Tensor sum, scales;
+    if (residual) sum = at.output(a[6], "sum_out", shape, stype);
+    if (!residual && a[6] != Py_None) refuse(PyExc_ValueError, "sum_out needs a residual");
+    if (quantize) scales = at.empty(shape.slice(0, shape.size() - 1), kF32);
+    if (rx.n > 0 || C == 0)
+        check(based_rms_fwd(x.data_ptr(), rx.stride, residual ? residual->data_ptr() : nullptr, rr.stride, scode, w, pcode, rx.n, small(C), eps,
+                            residual ? sum.data_ptr() : nullptr, y.data_ptr(), code, quantize ? static_cast<float *>(scales.data_ptr()) : nullptr,
+                            at.raw()),
+              "based_rms_fwd");
+    PyObject *const total = residual ? wrap(sum) : Py_NewRef(a[0]);
+    return tuple(wrap(y), total, wrap_or_none(scales));
+}
+
+// dy, s, weight, dsum, eps, workspace, stream
+PyObject *rms_bwd(PyObject *const *a) {
+    const Tensor &dy = tensor(a[0], "dy"), &s = tensor(a[1], "s"), *weight = optional_tensor(a[2], "weight"), *dsum = optional_tensor(a[3], "dsum");
+    if (s.dim() < 1) refuse(PyExc_ValueError, "expected s of shape (..., C)");
+    const ScalarType type = dy.scalar_type(), stype = s.scalar_type(), ptype = weight ? weight->scalar_type() : type;
+    const int code = type_code(type, "dy"), scode = type_code(stype, "s"), pcode = type_code(ptype, "weight");
+    const int64_t C = s.size(-1);
+    const float eps = static_cast<float>(float_arg(a[4]));
+    const Place at(s, "s", a[6]);
+    const Sizes shape = s.sizes();
+    input(s, "s", shape, stype, at.dev);
+    input(dy, "dy", shape, type, at.dev);
+    if (dsum) input(*dsum, "dsum", shape, stype, at.dev);
+    void *w = whole(weight, "weight", {C}, ptype, at.dev);
+    const Rows rs(s, "s"), rd(dy, "dy"), rg(dsum ? *dsum : s, "dsum");
+    const Tensor ds = at.empty(shape, stype);
+    Tensor dx, dweight, ws;
+    if (type != stype) dx = at.empty(shape, type);
+    if (weight) dweight = at.empty({C}, ptype);
+    if (rs.n == 0 && C > 0) {
+        if (weight) settle(dweight, nullptr);
+    } else {
+        if (weight) ws = workspace(a[5], a[5] == Py_None ? based_rms_bwd_workspace_size(rs.n, small(C)) : 0, at);
+        check(based_rms_bwd(dy.data_ptr(), rd.stride, s.data_ptr(), rs.stride, scode, w, pcode, dsum ? dsum->data_ptr() : nullptr, rg.stride, rs.n,
+                            small(C), eps, ds.data_ptr(), dx.defined() ? dx.data_ptr() : nullptr, weight ? dweight.data_ptr() : nullptr, code,
+                            weight ? ws.data_ptr() : nullptr, weight ? ws.nbytes() : 0, at.raw()),
+              "based_rms_bwd");
+    }
+    PyObject *const first = wrap(ds);
+    return tuple(first, dx.defined() ? wrap(dx) : Py_NewRef(first), wrap_or_none(dweight));
+}
+
+// A number for all rows, or a tensor with one for each
+struct PerRow {
+    void *data = nullptr;
+    double all = 0;
+    PerRow(PyObject *o, const char *name, double none, int64_t N, ScalarType type, int dev) : all(none) {
+        if (THPVariable_Check(o))
+            data = whole(&THPVariable_Unpack(o), name, {N}, type, dev);
+        else if (o != Py_None)
+            all = float_arg(o);
+    }
+};
+
+// logits, u, temperature, top_k, top_p, min_p, out, stream
+PyObject *sample(PyObject *const *a) {
+    const Tensor &logits = tensor(a[0], "logits"), &u = tensor(a[1], "u");
+    if (logits.dim() != 2) refuse(PyExc_ValueError, "expected logits of shape (N,V)");
+    const ScalarType type = logits.scalar_type();
+    const int code = type_code(type, "logits");
+    const int64_t N = logits.size(0), V = logits.size(1);
+    const Place at(logits, "logits", a[7]);
+    input(logits, "logits", logits.sizes(), type, at.dev);
+    void *const random = whole(&u, "u", {N}, kF32, at.dev);
+    const PerRow temperature(a[2], "temperature", 1.0, N, kF32, at.dev), top_k(a[3], "top_k", 0.0, N, ScalarType::Int, at.dev),
+        top_p(a[4], "top_p", 1.0, N, kF32, at.dev), min_p(a[5], "min_p", 0.0, N, kF32, at.dev);
+    if (!(top_k.all >= INT32_MIN && top_k.all <= INT32_MAX) || top_k.all != static_cast<int>(top_k.all)) refuse(PyExc_ValueError, "top_k must be a whole number");
+    const Tensor tokens = at.output(a[6], "out", {N}, ScalarType::Int), probs = at.empty({N}, kF32);
+    if (N > 0 || V == 0)
+        check(based_sample(logits.data_ptr(), logits.stride(0), code, small(N), small(V), static_cast<float *>(random),
+                           static_cast<float *>(temperature.data), static_cast<float>(temperature.all), static_cast<int32_t *>(top_k.data),
+                           static_cast<int>(top_k.all), static_cast<float *>(top_p.data), static_cast<float>(top_p.all),
+                           static_cast<float *>(min_p.data), static_cast<float>(min_p.all), static_cast<int32_t *>(tokens.data_ptr()),
+                           static_cast<float *>(probs.data_ptr()), at.raw()),
+              "based_sample");
+    return tuple(wrap(tokens), wrap(probs));
+}
+
 // A Python function of COUNT positional arguments. Nothing is thrown past it: torch's errors (such
 // as memory that cannot be had) become Python's.
 template <PyObject *(*F)(PyObject *const *), int COUNT>
@@ -586,6 +684,9 @@ PyMethodDef g_methods[] = {method<scan_fwd, 9>("scan_fwd"),
                            method<delta_fwd, 13>("delta_fwd"),
                            method<delta_bwd, 12>("delta_bwd"),
                            method<delta_step, 10>("delta_step"),
+                           method<rms_fwd, 8>("rms_fwd"),
+                           method<rms_bwd, 7>("rms_bwd"),
+                           method<sample, 8>("sample"),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "based_ops_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -21,7 +21,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -75,8 +75,13 @@ def library():
     L.based_delta_step.argtypes = [p, l, l, p, l, l, p, l, l, p, l, p, l, i, i, i, i, i, i, i, f, p, p, p, p]
     L.based_delta_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
     L.based_delta_workspace_size.restype = z
+    L.based_rms_fwd.argtypes = [p, l, p, l, i, p, i, l, i, f, p, p, i, p, p]
+    L.based_rms_bwd.argtypes = [p, l, p, l, i, p, i, p, l, l, i, f, p, p, p, i, p, z, p]
+    L.based_rms_bwd_workspace_size.argtypes = [l, i]
+    L.based_rms_bwd_workspace_size.restype = z
+    L.based_sample.argtypes = [p, l, i, i, i, p, p, f, p, i, p, f, p, f, p, p, p]
     for name in ("scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd", "embed_fwd", "embed_bwd", "delta_fwd", "delta_bwd",
-                 "delta_step"):
+                 "delta_step", "rms_fwd", "rms_bwd", "sample"):
         getattr(L, "based_" + name).restype = i
     L.based_norm_bwd_workspace_size.restype = z
     L.based_embed_bwd_workspace_size.restype = z
@@ -229,3 +234,55 @@ def delta_workspace_size(batch: int, rows: int, heads: int, key_heads: int, key_
     """Bytes of workspace based_delta_fwd or based_delta_bwd takes for these sizes."""
     code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
     return library().based_delta_workspace_size(batch, rows, heads, key_heads, key_size, value_size, code, int(backward))
+
+
+# ------------------------------------------------------------------------------------------------
+# Root-mean-square norm of a residual stream
+# ------------------------------------------------------------------------------------------------
+def based_rms_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, quantize: bool = False, out: Optional[torch.Tensor] = None,
+                  sum_out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
+    """(y, s, scales): s = x + residual (..., C) in the type of ``residual`` (that of x, or float32), x itself without one, and
+    y = s / sqrt(mean(s^2) + eps) * weight in the type of x. The norm is that of the s that is written.
+
+    ``quantize``: y is float8_e4m3fn, with scales (...) float32 so that y * scales is the norm and each row's largest is 448;
+    else scales is None. weight (C) has the type of x or float32. ``sum_out`` may be ``residual``, to add in place.
+    """
+    return _C.rms_fwd(x, weight, residual, eps, quantize, out, sum_out, stream)
+
+
+def based_rms_bwd(dy: torch.Tensor, s: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  dsum: Optional[torch.Tensor] = None, eps: float = 1e-6, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of based_rms_fwd for the gradients dy of y and dsum of s: (ds, dx, dweight). ds is that of the residual, in the
+    type of s, dx that of x: the same values in the type of dy, the same tensor where the types are. ``s`` is what the
+    forward call returned. ``workspace``: a CUDA byte tensor of at least rms_bwd_workspace_size(...) bytes (default: one
+    is allocated)."""
+    return _C.rms_bwd(dy, s, weight, dsum, eps, workspace, stream)
+
+
+def rms_bwd_workspace_size(rows: int, channels: int) -> int:
+    """Bytes of workspace based_rms_bwd takes for these sizes."""
+    return library().based_rms_bwd_workspace_size(rows, channels)
+
+
+# ------------------------------------------------------------------------------------------------
+# Sampling
+# ------------------------------------------------------------------------------------------------
+PerRow = Union[float, torch.Tensor, None]
+
+
+def based_sample(logits: torch.Tensor, u: torch.Tensor, temperature: PerRow = 1.0, top_k: PerRow = None, top_p: PerRow = None,
+                 min_p: PerRow = None, out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The next token of each row of logits (N,V) from random numbers u (N) float32 in [0, 1): (tokens (N) int32, their
+    probabilities (N) float32 among what their rows keep).
+
+    A row keeps the top_k largest logits (of equal ones the first), of these the fewest of the largest whose probabilities
+    reach top_p of theirs, and of these the ones of at least min_p times the largest's; the token is the first, in the order
+    of indices, at which the kept probabilities exceed u. Each limit is a number, a tensor (N) (float32; top_k
+    int32) or None. temperature <= 0 takes the largest logit. -inf is never taken, NaN counts as -inf, and a row
+    with nothing else gives token -1.
+    """
+    return _C.sample(logits, u, temperature, top_k, top_p, min_p, out, stream)
