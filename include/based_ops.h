@@ -194,27 +194,25 @@ BASED_API size_t based_embed_bwd_workspace_size(int64_t N, int V, int D);
  *                inputs are not read and their outputs are zero. Values are clamped to [0, T].
  *   o            (B,T,H,V) of `dtype`, contiguous
  *   final_state  (B,H,K,V) float32 or NULL: S_{T-1}; may be `state` itself
- *   states       (B, ceil(T / BASED_DELTA_ROWS), H, K, V) float32, the states in front of rows 0, 64, ..., and
- *   errors       (B,T,H,V) float32, v_t - a_t S_{t-1}^T k_t: what based_delta_bwd reads (16-byte aligned; both or
- *                neither NULL; unspecified in chunks and rows of padding)
+ *   saved        based_delta_saved_size() bytes, 16-byte aligned, or NULL: what based_delta_bwd reads (the states in front of rows 0, 64, ...
+ *                and the rows' v_t - a_t S_{t-1}^T k_t, in the kernels' own order and types)
  *   workspace    based_delta_workspace_size(..., 0) bytes
  * H must be a multiple of HK, K at most 128, V at most 65536.
  * Errors: as based_scan_fwd, BASED_ERR_WORKSPACE, BASED_ERR_BAD_ARGUMENT (a scale that is NaN).
  */
-#define BASED_DELTA_ROWS 64
 BASED_API int based_delta_fwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, const void *k, int64_t k_sb,
                               int64_t k_st, int64_t k_sh, const void *v, int64_t v_sb, int64_t v_st, int64_t v_sh,
                               const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate, int64_t gate_sb,
                               int64_t gate_st, int B, int T, int H, int HK, int K, int V, int dtype, float scale,
-                              const float *state, const int32_t *lengths, void *o, float *final_state, float *states,
-                              float *errors, void *workspace, size_t ws_bytes, based_stream_t stream);
+                              const float *state, const int32_t *lengths, void *o, float *final_state, void *saved,
+                              void *workspace, size_t ws_bytes, based_stream_t stream);
 
 /*
  * based_delta_bwd: gradients of based_delta_fwd for the gradients dout (B,T,H,V) of o and dfinal of final_state.
  * Queries' and keys' gradients are summed over the heads that share them, in a fixed order.
  *   q .. gate, scale, lengths  as given to based_delta_fwd
  *   dout         (B,T,H,V) of `dtype`, strides (do_sb, do_st, do_sh, 1); not read in padding rows
- *   states, errors  what based_delta_fwd wrote
+ *   saved        what based_delta_fwd wrote
  *   dfinal       (B,H,K,V) float32 or NULL (zero)
  *   dq, dk       (B,T,HK,K), dv (B,T,H,V), dbeta, dgate (B,T,H) of `dtype`, contiguous, zero in padding rows;
  *                dgate if and only if there are gates; dq and dk aligned to two elements
@@ -226,13 +224,16 @@ BASED_API int based_delta_bwd(const void *q, int64_t q_sb, int64_t q_st, int64_t
                               int64_t k_st, int64_t k_sh, const void *v, int64_t v_sb, int64_t v_st, int64_t v_sh,
                               const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate, int64_t gate_sb,
                               int64_t gate_st, const void *dout, int64_t do_sb, int64_t do_st, int64_t do_sh,
-                              const float *states, const float *errors, int B, int T, int H, int HK, int K, int V,
-                              int dtype, float scale, const float *dfinal, const int32_t *lengths, void *dq, void *dk,
+                              const void *saved, int B, int T, int H, int HK, int K, int V, int dtype,
+                              float scale, const float *dfinal, const int32_t *lengths, void *dq, void *dk,
                               void *dv, void *dbeta, void *dgate, float *dstate, void *workspace, size_t ws_bytes,
                               based_stream_t stream);
 
 /* Bytes of workspace based_delta_fwd() (backward 0) or based_delta_bwd() needs for these sizes (0 for sizes they refuse). */
 BASED_API size_t based_delta_workspace_size(int B, int T, int H, int HK, int K, int V, int dtype, int backward);
+
+/* Bytes that based_delta_fwd() saves for based_delta_bwd() (0 for sizes they refuse). */
+BASED_API size_t based_delta_saved_size(int B, int T, int H, int K, int V, int dtype);
 
 /*
  * based_delta_step: one row of the delta rule for N sequences whose states lie in a pool:

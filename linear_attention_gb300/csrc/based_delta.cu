@@ -6,12 +6,13 @@
 // the chunk, D_ij = exp(b_i - b_j) for j <= i, S0 the state in front, grow_i = exp(b_i) and rest_i = exp(b_last - b_i):
 //     X = V - grow K S0,   E = (1 + L)^-1 X with L_ij = D_ij (k_i k_j) beta_j below the diagonal,   U = beta E,
 //     O = scale grow Q S0 + P U with P_ij = scale D_ij (q_i k_j),   S = grow_last S0 + (rest K)^T U.
-// delta_prep_kernel has all that does not depend on the state (the inverse and P), for all chunks at once;
-// delta_fwd_kernel runs through the chunks. Backward, with G the gradient of the state behind the chunk and A_ij = beta_i D_ij (k_i k_j):
+// based_delta_prep_kernel has all that does not depend on the state (the inverse and P), for all chunks at once;
+// based_delta_fwd_kernel runs through the chunks. Backward, with G the gradient of the state behind the chunk and
+// A_ij = beta_i D_ij (k_i k_j) below the diagonal:
 //     dU = P^T dO + rest K G,   dR = (1 + A)^-T dU,   dV = beta dR,
 //     G' = grow_last G + scale (grow Q)^T dO - (beta grow K)^T dR
-// runs through the chunks from the last (delta_bwd_kernel), and what is left is again for all chunks at once
-// (delta_grad_kernel, where its formulas are).
+// runs through the chunks from the last (based_delta_bwd_kernel), and what is left is again for all chunks at once
+// (based_delta_grad_kernel, where its formulas are).
 #include "delta_common.cuh"
 
 namespace based {
@@ -25,53 +26,47 @@ constexpr int kLd = 68;  // floats in a row of the square matrices in shared mem
 
 template <typename T, int KP>
 struct PrepSmem {
-    static constexpr int squares = kChunk * kLd * 4;
-    static constexpr int images = Rec<T, KP>::qk, work = 2 * squares + 32 * 36 * 4;
+    static constexpr int images = Rec<T, KP>::qk, work = (2 * kChunk * kLd + 32 * 36) * 4;
     static constexpr int shared = images > work ? images : work;  // the images, then the inverse's work in their place
-    static constexpr int bytes = shared + 2 * squares + (3 * kChunk + 16) * 4;
+    static constexpr int bytes = shared + (3 * kChunk + 16) * 4;
 };
 
 // Rows of q or k into their images, in shared memory and in the record; returns the scale's inverse.
+__host__ __device__ constexpr int prep_words(int KP) { return kChunk * KP / 8 / (32 * kPrepWarps); }  // of a thread
 template <typename T, int KP>
-__device__ __forceinline__ float make_image(const T *src, int64_t stride, int rows, int K, bool vec, uint8_t *img, uint8_t *rec, float *red) {
-    constexpr int kWords = KP / 8, kEach = kChunk * kWords / (32 * kPrepWarps), kStep = 32 * kPrepWarps / kWords;
+__device__ __forceinline__ void read_rows(Raw<T> (&raw)[prep_words(KP)], const T *src, int64_t stride, int rows, int K, bool words) {
+    constexpr int kWords = KP / 8, kStep = 32 * kPrepWarps / kWords;
     const int word = threadIdx.x % kWords, row0 = threadIdx.x / kWords;
-    float x[kEach][8], most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < prep_words(KP); ++i) {
         const int row = row0 + i * kStep;
-        load8(x[i], src + row * stride + word * 8, row < rows ? K - word * 8 : 0, vec);
-        most = most8(most, x[i]);
+        raw[i].load(src + row * stride + word * 8, row < rows ? K - word * 8 : 0, words);
+    }
+}
+template <typename T, int KP>
+__device__ __forceinline__ float make_image(const Raw<T> (&raw)[prep_words(KP)], uint8_t *img, uint8_t *rec, float *red) {
+    constexpr int kWords = KP / 8, kStep = 32 * kPrepWarps / kWords;
+    const int word = threadIdx.x % kWords, row0 = threadIdx.x / kWords;
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < prep_words(KP); ++i) {
+        float x[8];
+        raw[i].get(x);
+        most = most8(most, x);
     }
     const float s = scale_for(cta_most<kPrepWarps>(most, red));
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < prep_words(KP); ++i) {
+        float x[8];
+        raw[i].get(x);
         uint4 w[Terms<T>::in];
-        words_of<Terms<T>::in>(w, x[i], s);
+        words_of<Terms<T>::in>(w, x, s);
         const uint32_t at = word_at<KP>(row0 + i * kStep, word);
 #pragma unroll
         for (int j = 0; j < Terms<T>::in; ++j) {
             *reinterpret_cast<uint4 *>(img + j * Rec<T, KP>::term + at) = w[j];
             *reinterpret_cast<uint4 *>(rec + j * Rec<T, KP>::term + at) = w[j];
         }
-    }
-    return inverse_of(s);
-}
-
-// The terms of a 64 x 64 matrix, held in x as rows (threadIdx.x / 8) + 16 r and words threadIdx.x % 8, into the record
-template <int TERMS>
-__device__ __forceinline__ float put_square(const float (&x)[4][8], uint8_t *rec, float *red) {
-    float most = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) most = most8(most, x[r]);
-    const float s = scale_for(cta_most<kPrepWarps>(most, red));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        uint4 w[TERMS];
-        words_of<TERMS>(w, x[r], s);
-        const uint32_t at = word_at<kChunk>(threadIdx.x / 8 + 16 * r, threadIdx.x % 8);
-#pragma unroll
-        for (int j = 0; j < TERMS; ++j) *reinterpret_cast<uint4 *>(rec + j * kSquare + at) = w[j];
     }
     return inverse_of(s);
 }
@@ -126,13 +121,13 @@ __device__ __forceinline__ void invert(float *h, const float *m, float *w) {
 
 // One chunk of one key head, and all value heads that share it.
 template <typename T, int KP, bool BWD>
-__global__ void __launch_bounds__(32 * kPrepWarps) based_delta_prep_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(DeltaParams p) {
     using R = Rec<T, KP>;
     using Sm = PrepSmem<T, KP>;
+    constexpr int NI = Terms<T>::in, NP = R::scores(BWD);
     extern __shared__ __align__(128) uint8_t smem[];
-    float *const gk = reinterpret_cast<float *>(smem + Sm::shared), *const gq = gk + kChunk * kLd;
     float *const m = reinterpret_cast<float *>(smem), *const h = m + kChunk * kLd, *const w = h + kChunk * kLd;
-    float *const bhi = gq + kChunk * kLd, *const blo = bhi + kChunk, *const beta = blo + kChunk, *const red = beta + kChunk;
+    float *const bhi = reinterpret_cast<float *>(smem + Sm::shared), *const blo = bhi + kChunk, *const beta = blo + kChunk, *const red = beta + kChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK;
     griddep_wait();
@@ -144,52 +139,50 @@ __global__ void __launch_bounds__(32 * kPrepWarps) based_delta_prep_kernel(Delta
         const T *const ks = static_cast<const T *>(p.k) + b * p.k_sb + t0 * p.k_st + hk * p.k_sh;
         const T *const qs = static_cast<const T *>(p.q) + b * p.q_sb + t0 * p.q_st + hk * p.q_sh;
         __syncthreads();  // the batch entry before
-        const float ik = make_image<T, KP>(ks, p.k_st, rows, p.K, p.qk_vec, smem, rec, red);
-        const float iq = make_image<T, KP>(qs, p.q_st, rows, p.K, p.qk_vec, smem + R::img, rec + R::img, red);
+        float ik, iq;
+        if constexpr (sizeof(T) == 2) {  // (registers for both only in 16 bits)
+            Raw<T> rk[prep_words(KP)], rq[prep_words(KP)];
+            read_rows<T, KP>(rk, ks, p.k_st, rows, p.K, p.qk_vec);
+            read_rows<T, KP>(rq, qs, p.q_st, rows, p.K, p.qk_vec);
+            ik = make_image<T, KP>(rk, smem, rec, red);
+            iq = make_image<T, KP>(rq, smem + R::img, rec + R::img, red);
+        } else {
+            Raw<T> raw[prep_words(KP)];
+            read_rows<T, KP>(raw, ks, p.k_st, rows, p.K, p.qk_vec);
+            ik = make_image<T, KP>(raw, smem, rec, red);
+            read_rows<T, KP>(raw, qs, p.q_st, rows, p.K, p.qk_vec);
+            iq = make_image<T, KP>(raw, smem + R::img, rec + R::img, red);
+        }
         __syncthreads();
-        {  // the products of keys with keys and queries: rows 16 warp .. + 15, columns up to the diagonal
-            Acc sk[8] = {}, sq[8] = {};
+        // the products of keys with keys and queries: rows 16 warp .. + 15, columns up to the diagonal
+        Acc sk[8], sq[8];
+        clear(sk), clear(sq);
+        {
             const uint32_t kimg = smem_u32(smem), qimg = kimg + R::img;
-            constexpr int NT = Terms<T>::in;
 #pragma unroll
             for (int kk = 0; kk < KP / 16; ++kk) {
-                uint32_t a[NT][4], c[NT][4];
+                uint32_t a[NI][4], c[NI][4];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
+                for (int j = 0; j < NI; ++j) {
                     left<KP>(a[j], kimg + j * R::term, 16 * warp, 16 * kk, lane);
                     left<KP>(c[j], qimg + j * R::term, 16 * warp, 16 * kk, lane);
                 }
 #pragma unroll
                 for (int np = 0; np < 4; ++np) {
                     if (np > warp) continue;
-                    uint32_t x[NT][4];
+                    uint32_t x[NI][4];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) right<KP>(x[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int i = 0; i + j < NT; ++i)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                mma(sk[2 * np + e], a[i], x[j][2 * e], x[j][2 * e + 1]);
-                                mma(sq[2 * np + e], c[i], x[j][2 * e], x[j][2 * e + 1]);
-                            }
+                    for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
+                    products<NI, NI>(sk[2 * np], sk[2 * np + 1], a, x);
+                    products<NI, NI>(sq[2 * np], sq[2 * np + 1], c, x);
                 }
             }
-            const float fk = ik * ik, fq = iq * ik * p.scale;
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt) {
-                const int at = (16 * warp + lane / 4) * kLd + 8 * nt + 2 * (lane % 4);
-                *reinterpret_cast<float2 *>(gk + at) = make_float2(sk[nt][0] * fk, sk[nt][1] * fk);
-                *reinterpret_cast<float2 *>(gk + at + 8 * kLd) = make_float2(sk[nt][2] * fk, sk[nt][3] * fk);
-                *reinterpret_cast<float2 *>(gq + at) = make_float2(sq[nt][0] * fq, sq[nt][1] * fq);
-                *reinterpret_cast<float2 *>(gq + at + 8 * kLd) = make_float2(sq[nt][2] * fq, sq[nt][3] * fq);
-            }
         }
+        const float fk = ik * ik, fq = iq * ik * p.scale;
         for (int hh = 0; hh < group; ++hh) {
             const int head = hk * group + hh;
             uint8_t *const g = p.g_rec + ((static_cast<int64_t>(b) * p.H + head) * p.chunks + n) * R::g(BWD);
-            float *const f = reinterpret_cast<float *>(g + (2 + R::scores(BWD)) * kSquare);
+            float *const f = reinterpret_cast<float *>(g + (2 + NP) * kSquare);
             if (warp == 0) {
                 // Sums of log decays in 64 bits, kept as two floats: differences of neighbours then have float32's relative
                 // accuracy however much has decayed before. -1e5 stands for anything below it, -inf among it: its decay is 0.
@@ -223,224 +216,246 @@ __global__ void __launch_bounds__(32 * kPrepWarps) based_delta_prep_kernel(Delta
                 }
                 if (lane == 0) f[F_WHOLE] = expf(static_cast<float>(last)), f[F_K] = ik, f[F_Q] = iq;
             }
+            for (int i = tid; i < kChunk * kLd / 4; i += 32 * kPrepWarps)
+                if (hh) reinterpret_cast<float4 *>(h)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             __syncthreads();  // the sums, and the images are done with
+            if (!hh)
+                for (int i = tid; i < kChunk * kLd / 4; i += 32 * kPrepWarps) reinterpret_cast<float4 *>(h)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            Acc pv[8];
+            float most = 0.0f;
+            {
+                const int r0 = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
+                const float hi[2] = {bhi[r0], bhi[r0 + 8]}, lo[2] = {blo[r0], blo[r0 + 8]}, bi[2] = {beta[r0], beta[r0 + 8]};
+#pragma unroll
+                for (int nt = 0; nt < 8; ++nt) {
+                    if (nt > 2 * warp + 1) {  // above the diagonal
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pv[nt][e] = 0.0f;
+                        continue;
+                    }
+                    const float2 jh = *reinterpret_cast<const float2 *>(bhi + 8 * nt + c0), jl = *reinterpret_cast<const float2 *>(blo + 8 * nt + c0),
+                                 jb = *reinterpret_cast<const float2 *>(beta + 8 * nt + c0);
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = r0 + 8 * (e / 2), j = 8 * nt + c0 + e % 2;
+                        const float d = j <= i ? expf((hi[e / 2] - (e % 2 ? jh.y : jh.x)) + (lo[e / 2] - (e % 2 ? jl.y : jl.x))) : 0.0f;
+                        const float bj = e % 2 ? jb.y : jb.x;
+                        pv[nt][e] = j <= i ? d * (sq[nt][e] * fq) * (BWD ? 1.0f : bj) : 0.0f;
+                        y[e] = j < i ? d * (sk[nt][e] * fk) * (BWD ? bi[e / 2] : bj) : 0.0f;
+                        most = fmaxf(most, fabsf(pv[nt][e]));
+                    }
+                    float *const to = m + r0 * kLd + 8 * nt + c0;
+                    *reinterpret_cast<float2 *>(to) = make_float2(y[0], y[1]);
+                    *reinterpret_cast<float2 *>(to + 8 * kLd) = make_float2(y[2], y[3]);
+                }
+            }
+            const float sp = scale_for(cta_most<kPrepWarps>(most, red));  // with a barrier
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t x[NP];
+                    terms<NP>(pv[nt][2 * e] * sp, pv[nt][2 * e + 1] * sp, x);
+                    const uint32_t at = word_at<kChunk>(16 * warp + (lane >> 2) + 8 * e, nt) + 4 * (lane & 3);
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) *reinterpret_cast<uint32_t *>(g + (2 + j) * kSquare + at) = x[j];
+                }
+            invert(h, m, w);
             float x[4][8];
+            most = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int i = tid / 8 + 16 * r, j0 = tid % 8 * 8;
-                float k8[8], q8[8], y[8];
-                load8(k8, gk + i * kLd + j0, 8, true), load8(q8, gq + i * kLd + j0, 8, true);
-                const float hi = bhi[i], lo = blo[i], bi = beta[i];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = j0 + e;
-                    const float d = j <= i ? expf((hi - bhi[j]) + (lo - blo[j])) : 0.0f;
-                    x[r][e] = j <= i ? d * q8[e] : 0.0f;
-                    y[e] = j < i ? d * k8[e] * (BWD ? bi : beta[j]) : 0.0f;
-                }
-                float4 *const to = reinterpret_cast<float4 *>(m + i * kLd + j0), *const zero = reinterpret_cast<float4 *>(h + i * kLd + j0);
-                to[0] = make_float4(y[0], y[1], y[2], y[3]), to[1] = make_float4(y[4], y[5], y[6], y[7]);
-                zero[0] = zero[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float4 *const from = reinterpret_cast<const float4 *>(h + (tid / 8 + 16 * r) * kLd + tid % 8 * 8);
+                const float4 u = from[0], v = from[1];
+                x[r][0] = u.x, x[r][1] = u.y, x[r][2] = u.z, x[r][3] = u.w, x[r][4] = v.x, x[r][5] = v.y, x[r][6] = v.z, x[r][7] = v.w;
+                most = most8(most, x[r]);
             }
-            const float ip = put_square<R::scores(BWD)>(x, g + 2 * kSquare, red);  // with a barrier
-            invert(h, m, w);
+            const float sh = scale_for(cta_most<kPrepWarps>(most, red));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) load8(x[r], h + (tid / 8 + 16 * r) * kLd + tid % 8 * 8, 8, true);
-            const float ih = put_square<2>(x, g, red);
-            if (tid == 0) f[F_INV] = ih, f[F_P] = ip;
+            for (int r = 0; r < 4; ++r) {
+                uint4 z[2];
+                words_of<2>(z, x[r], sh);
+                const uint32_t at = word_at<kChunk>(tid / 8 + 16 * r, tid % 8);
+                *reinterpret_cast<uint4 *>(g + at) = z[0], *reinterpret_cast<uint4 *>(g + kSquare + at) = z[1];
+            }
+            if (tid == 0) f[F_INV] = inverse_of(sh), f[F_P] = inverse_of(sp);
         }
     }
 }
 
 // ------------------------------------------------------------------------------------------------
-// Through the chunks. A warp owns 16 channels of the values: the state's transpose, 16 x KP, lies in its accumulators, so every
-// product's left operand comes from the warp's own registers, and the records in shared memory serve all warps of the CTA.
+// Through the chunks. Four warps own 16 channels of the values, a slice. The state's transpose lies in their accumulators, a quarter of the keys'
+// channels each, so what a state's product needs of the state is never stored in float32 and read back; a chunk's rows are shared out too, 16 to each
+// warp. Three times a chunk the warps hand one another left operands: the state's, X's and E's (backward: the gradient's, dU's and dR's).
+// A chunk's records in shared memory serve all slices of a CTA.
 // ------------------------------------------------------------------------------------------------
-constexpr int kSlice = 16;
-constexpr int kMostWarps = 8;
+constexpr int kQuad = 128;  // threads of a slice
 
 template <typename T, int KP>
 struct SeqSmem {
     static constexpr int row = sizeof(T) == 2 ? 32 : 80;  // bytes of a row of 16 values: 32-bit ones lie apart so that four rows' banks differ
-    static constexpr int tile = kChunk * row;
-    // of float32 with 128 channels of keys, two chunks' records leave room for the tiles of two warps
-    static constexpr int warps = sizeof(T) == 4 && KP == 128 ? 2 : kMostWarps;
+    static constexpr int tile = 16 * row;                 // of a warp: its rows of the values
     __host__ __device__ static constexpr int stage(bool bwd) { return Rec<T, KP>::qk + Rec<T, KP>::g(bwd); }
-    static constexpr int bytes(bool bwd, int warps) { return 2 * stage(bwd) + 2 * warps * tile; }
+    // left operands, 512 bytes a term of a 16 x 16 block: the state's; E's or dO's; what is added to the state (backward: two); X's or dU's
+    // (backward in the place of the state's, which all warps are done with by then)
+    static constexpr int state = 0, e = state + KP / 16 * 1024, e_block = (Terms<T>::in > Terms<T>::out ? Terms<T>::in : Terms<T>::out) * 512, u = e + 4 * e_block,
+                         w = u + 4096;
+    __host__ __device__ static constexpr int x(bool bwd) { return bwd ? state : w; }
+    static constexpr int scales = w + 4096, slice = scales + 128 + 8 * tile;
+    static constexpr int bytes(bool bwd, int slices) { return 2 * stage(bwd) + slices * slice; }
+    // Slices of a CTA, at most: 512 threads, and what shared memory holds
+    static constexpr int most(bool bwd) { return bytes(bwd, 4) <= 227 * 1024 ? 4 : bytes(bwd, 3) <= 227 * 1024 ? 3 : bytes(bwd, 2) <= 227 * 1024 ? 2 : 1; }
 };
 
-// A warp's 64 x 16 tile of v, dout or an output: where its words lie
+// A warp's 16 rows by 16 channels of v, dout or an output: where its words lie
 template <typename T>
 __device__ __forceinline__ uint32_t tile_word(int row, int word) {
     if constexpr (sizeof(T) == 2) return row * 32 + ((word ^ (row >> 2 & 1)) << 4);
     return row * 80 + (word << 4);
 }
-// Rows [0, rows) of the channels [0, cols) at src; zeros elsewhere. By one warp.
+// Rows [0, rows) of the channels [0, cols) at src; zeros elsewhere
 template <typename T>
-__device__ __forceinline__ void load_tile(uint8_t *tile, const T *src, int64_t stride, int rows, int cols, bool vec, int lane) {
+__device__ __forceinline__ void load_tile(uint8_t *tile, const T *src, int64_t stride, int rows, int cols, bool words, int lane) {
     constexpr int kWords = sizeof(T), kEl = 16 / sizeof(T);  // two words of eight, or four of four elements a row
-    if (vec) {
+    if (words) {
 #pragma unroll
-        for (int i = 0; i < 2 * kWords; ++i) {
+        for (int i = 0; i < kWords / 2; ++i) {
             const int row = (lane + 32 * i) / kWords, word = (lane + 32 * i) % kWords;
             const bool there = row < rows && word * kEl < cols;
             copy16(smem_u32(tile) + tile_word<T>(row, word), there ? src + row * stride + word * kEl : src, there ? 16 : 0);
         }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = (lane >> 4) + 2 * i, c = lane & 15;
+            const bool there = row < rows && c < cols;
+            copy4(smem_u32(tile) + row * 80 + c * 4, there ? src + row * stride + c : src, there ? 4 : 0);
+        }
     } else {
-#pragma unroll 4
-        for (int i = lane; i < kChunk * kSlice; i += 32) {
-            const int row = i / kSlice, c = i % kSlice;
-            T v = from_f32<T>(0.0f);
-            if (row < rows && c < cols) v = src[row * stride + c];
-            *reinterpret_cast<T *>(tile + tile_word<T>(row, c / kEl) + c % kEl * sizeof(T)) = v;
+        T x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = (lane >> 4) + 2 * i, c = lane & 15;
+            x[i] = from_f32<T>(0.0f);
+            if (row < rows && c < cols) x[i] = src[row * stride + c];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = (lane >> 4) + 2 * i, c = lane & 15;
+            *reinterpret_cast<T *>(tile + tile_word<T>(row, c / kEl) + c % kEl * sizeof(T)) = x[i];
         }
     }
 }
-// The tile's transpose as accumulator blocks: rows are channels, columns the chunk's rows
+// The tile's transpose as two accumulator blocks: rows are channels, columns the warp's 16 rows
 template <typename T>
-__device__ __forceinline__ void read_tile(Acc (&x)[8], const uint8_t *tile, int lane) {
+__device__ __forceinline__ void read_tile(Acc (&x)[2], const uint8_t *tile, int lane) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t r[4];
+        ldsm_t(r, smem_u32(tile) + tile_word<T>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-        if constexpr (sizeof(T) == 2) {
-            uint32_t r[4];
-            ldsm_t(r, smem_u32(tile) + tile_word<T>(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Vec<2> f = unpack<T>(r[i]);
-                x[2 * np + i / 2][2 * (i % 2)] = f.v[0], x[2 * np + i / 2][2 * (i % 2) + 1] = f.v[1];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 16 * np + 8 * (e / 4) + 2 * (lane & 3) + e % 2, c = (lane >> 2) + 8 * (e / 2 % 2);
-                x[2 * np + e / 4][e % 4] = *reinterpret_cast<const float *>(tile + row * 80 + c * 4);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const Vec<2> f = unpack<T>(r[i]);
+            x[i / 2][2 * (i % 2)] = f.v[0], x[i / 2][2 * (i % 2) + 1] = f.v[1];
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e / 4][e % 4] = *reinterpret_cast<const float *>(tile + (8 * (e / 4) + 2 * (lane & 3) + e % 2) * 80 + ((lane >> 2) + 8 * (e / 2 % 2)) * 4);
     }
 }
 template <typename T>
-__device__ __forceinline__ void write_tile(uint8_t *tile, const Acc (&x)[8], int lane) {
+__device__ __forceinline__ void write_tile(uint8_t *tile, const Acc (&x)[2], int lane) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t r[4];
 #pragma unroll
-    for (int np = 0; np < 4; ++np) {
-        if constexpr (sizeof(T) == 2) {
-            uint32_t r[4];
+        for (int i = 0; i < 4; ++i) r[i] = pack<T>(Vec<2>{{x[i / 2][2 * (i % 2)], x[i / 2][2 * (i % 2) + 1]}});
+        stsm_t(smem_u32(tile) + tile_word<T>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), r[0], r[1], r[2], r[3]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r[i] = pack<T>(Vec<2>{{x[2 * np + i / 2][2 * (i % 2)], x[2 * np + i / 2][2 * (i % 2) + 1]}});
-            stsm_t(smem_u32(tile) + tile_word<T>(16 * np + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1), r[0], r[1], r[2], r[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 16 * np + 8 * (e / 4) + 2 * (lane & 3) + e % 2, c = (lane >> 2) + 8 * (e / 2 % 2);
-                *reinterpret_cast<float *>(tile + row * 80 + c * 4) = x[2 * np + e / 4][e % 4];
-            }
-        }
+        for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float *>(tile + (8 * (e / 4) + 2 * (lane & 3) + e % 2) * 80 + ((lane >> 2) + 8 * (e / 2 % 2)) * 4) = x[e / 4][e % 4];
     }
 }
 // Rows [0, rows) of the tile, and zeros up to row `all`, to dst
 template <typename T>
-__device__ __forceinline__ void store_tile(T *dst, int64_t stride, const uint8_t *tile, int rows, int all, int cols, bool vec, int lane) {
+__device__ __forceinline__ void store_tile(T *dst, int64_t stride, const uint8_t *tile, int rows, int all, int cols, bool words, int lane) {
     constexpr int kWords = sizeof(T), kEl = 16 / sizeof(T);
-    if (vec) {
+    if (words) {
 #pragma unroll
-        for (int i = 0; i < 2 * kWords; ++i) {
+        for (int i = 0; i < kWords / 2; ++i) {
             const int row = (lane + 32 * i) / kWords, word = (lane + 32 * i) % kWords;
             if (row < all && word * kEl < cols)
                 *reinterpret_cast<uint4 *>(dst + row * stride + word * kEl) =
                     row < rows ? *reinterpret_cast<const uint4 *>(tile + tile_word<T>(row, word)) : make_uint4(0, 0, 0, 0);
         }
     } else {
-#pragma unroll 4
-        for (int i = lane; i < kChunk * kSlice; i += 32) {
-            const int row = i / kSlice, c = i % kSlice;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int row = (lane >> 4) + 2 * i, c = lane & 15;
             if (row < all && c < cols)
                 dst[row * stride + c] =
                     row < rows ? *reinterpret_cast<const T *>(tile + tile_word<T>(row, c / kEl) + c % kEl * sizeof(T)) : from_f32<T>(0.0f);
         }
     }
 }
-// A state (K,V) at p, or its transpose in the accumulators
-template <int KP>
-__device__ __forceinline__ void read_state(Acc (&s)[KP / 8], const float *p, int K, int V, int v0, int lane) {
+// A quarter (N blocks) of a state (K,V)'s transpose
+template <int N>
+__device__ __forceinline__ void read_state(Acc (&s)[N], const float *p, int k0, int K, int V, int v0, int lane) {
 #pragma unroll
-    for (int j = 0; j < KP / 8; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int k = 8 * j + 2 * (lane & 3) + e % 2, v = v0 + (lane >> 2) + 8 * (e / 2);
-            s[j][e] = p && k < K && v < V ? p[static_cast<int64_t>(k) * V + v] : 0.0f;
+            const int k = k0 + 8 * j + 2 * (lane & 3) + e % 2, v = v0 + (lane >> 2) + 8 * (e / 2);
+            s[j][e] = 0.0f;
+            if (p && k < K && v < V) s[j][e] = p[static_cast<int64_t>(k) * V + v];
         }
 }
-template <int KP>
-__device__ __forceinline__ void write_state(float *p, const Acc (&s)[KP / 8], int K, int V, int v0, int lane) {
+template <int N>
+__device__ __forceinline__ void write_state(float *p, const Acc (&s)[N], int k0, int K, int V, int v0, int lane) {
 #pragma unroll
-    for (int j = 0; j < KP / 8; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int k = 8 * j + 2 * (lane & 3) + e % 2, v = v0 + (lane >> 2) + 8 * (e / 2);
+            const int k = k0 + 8 * j + 2 * (lane & 3) + e % 2, v = v0 + (lane >> 2) + 8 * (e / 2);
             if (k < K && v < V) p[static_cast<int64_t>(k) * V + v] = s[j][e];
         }
 }
-// The transpose of rows of 32-bit values, (rows) x (V), as they lie in the accumulators
-__device__ __forceinline__ void write_rows(float *p, int64_t stride, const Acc (&x)[8], int rows, int V, int v0, int lane) {
+// Columns of two blocks times f[column]
+__device__ __forceinline__ void by_columns(Acc (&x)[2], const float *f, float c, int lane) {
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = 8 * nt + 2 * (lane & 3) + e % 2, v = v0 + (lane >> 2) + 8 * (e / 2);
-            if (row < rows && v < V) p[row * stride + v] = x[nt][e];
-        }
-}
-// Elements of columns of x times f[column] and by rows times c0 or c1
-__device__ __forceinline__ void by_columns(Acc (&x)[8], const float *f, float c0, float c1, int lane) {
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-        const float2 y = *reinterpret_cast<const float2 *>(f + 8 * nt + 2 * (lane & 3));
-        x[nt][0] *= y.x * c0, x[nt][1] *= y.y * c0, x[nt][2] *= y.x * c1, x[nt][3] *= y.y * c1;
+    for (int i = 0; i < 2; ++i) {
+        const float2 y = *reinterpret_cast<const float2 *>(f + 8 * i + 2 * (lane & 3));
+        x[i][0] *= y.x * c, x[i][1] *= y.y * c, x[i][2] *= y.x * c, x[i][3] *= y.y * c;
     }
-}
-__device__ __forceinline__ void by_rows(Acc (&x)[8], float c0, float c1) {
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt) x[nt][0] *= c0, x[nt][1] *= c0, x[nt][2] *= c1, x[nt][3] *= c1;
 }
 template <int N>
-__device__ __forceinline__ void clear(Acc (&x)[N]) {
+__device__ __forceinline__ void add(Acc (&x)[N], const Acc (&t)[N], float c) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[i][e] = fmaf(t[i][e], c, x[i][e]);
 }
-// Two 16 x 8 blocks += the left operand's LT terms times the RT terms of a right operand
-template <int LT, int RT>
-__device__ __forceinline__ void products(Acc &x, Acc &y, const uint32_t (&a)[LT][4], const uint32_t (&b)[RT][4]) {
+// Left operands, handed over through shared memory or left in a record
+template <int TERMS>
+__device__ __forceinline__ void give(uint8_t *to, const uint32_t (&a)[TERMS][4], int lane) {
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int i = 0; i < LT; ++i)
-            if (i + j < 2) {
-                mma(x, a[i], b[j][0], b[j][1]);
-                mma(y, a[i], b[j][2], b[j][3]);
-            }
+    for (int j = 0; j < TERMS; ++j) *reinterpret_cast<uint4 *>(to + j * 512 + lane * 16) = make_uint4(a[j][0], a[j][1], a[j][2], a[j][3]);
 }
-
-// x = M^T or M of the record (a lower triangular 64 x 64 image of RT terms) applied to y along its columns:
-// TURN false: x[.][i] = sum over j <= i of y[.][j] M[i][j]; true: x[.][j] = sum over i >= j of y[.][i] M[i][j]
-template <bool TURN, int LT, int RT>
-__device__ __forceinline__ void triangle(Acc (&x)[8], const Acc (&y)[8], float s0, float s1, uint32_t img, int lane) {
-    clear(x);
+template <int TERMS>
+__device__ __forceinline__ void take(uint32_t (&a)[TERMS][4], const uint8_t *from, int lane) {
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
-        uint32_t a[LT][4];
-        left_of<LT>(a, y[2 * kb], y[2 * kb + 1], s0, s1);
-#pragma unroll
-        for (int np = TURN ? 0 : kb; np < (TURN ? kb + 1 : 4); ++np) {
-            uint32_t b[RT][4];
-#pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                if (TURN)
-                    right_t<kChunk>(b[j], img + j * kSquare, 16 * kb, 16 * np, lane);
-                else
-                    right<kChunk>(b[j], img + j * kSquare, 16 * np, 16 * kb, lane);
-            }
-            products<LT, RT>(x[2 * np], x[2 * np + 1], a, b);
-        }
+    for (int j = 0; j < TERMS; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(from + j * 512 + lane * 16);
+        a[j][0] = x.x, a[j][1] = x.y, a[j][2] = x.z, a[j][3] = x.w;
     }
+}
+template <int TERMS, int N>
+__device__ __forceinline__ void leave(uint8_t *to, int term, const uint32_t (&a)[N][4], int lane) {
+#pragma unroll
+    for (int j = 0; j < TERMS; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) *reinterpret_cast<uint32_t *>(to + j * term + r * 128 + lane * 4) = a[j][r];
 }
 
 // The records of a chunk, by all threads of the CTA
@@ -450,242 +465,361 @@ __device__ __forceinline__ void copy_records(uint8_t *to, const uint8_t *qk, int
     for (int i = threadIdx.x * 16; i < g_bytes; i += blockDim.x * 16) copy16(at + qk_bytes + i, g + i);
 }
 
-template <typename T, int KP>
-__global__ void __launch_bounds__(32 * kMostWarps, 1) based_delta_fwd_kernel(DeltaParams p) {
+// What both directions have in common: this warp's place, and the parts of shared memory
+template <typename T, int KP, bool BWD>
+struct Seq {
     using R = Rec<T, KP>;
     using Sm = SeqSmem<T, KP>;
-    constexpr int NI = Terms<T>::in, NO = Terms<T>::out, kStage = Sm::stage(false);
+    static constexpr int NI = Terms<T>::in, NO = Terms<T>::out, kSteps = KP / 64, kStage = Sm::stage(BWD);  // steps: of 16 of the keys' channels
+    const DeltaParams &p;
+    uint8_t *smem, *mine;  // the records; the slice's
+    int lane, w, slice, head, hk, v0, cols;
+    float *sc;  // scales' inverses: of the state's quarters, then of 16 rows of x, e, u, w
+    uint8_t *tiles;
+
+    __device__ __forceinline__ Seq(const DeltaParams &p_, uint8_t *smem_) : p(p_), smem(smem_) {
+        const int quad = threadIdx.x / kQuad, quads = blockDim.x / kQuad;
+        lane = threadIdx.x & 31, w = threadIdx.x >> 5 & 3;
+        head = blockIdx.y, hk = head / (p.H / p.HK);
+        slice = blockIdx.x * quads + quad, v0 = slice * kSlice, cols = p.V - v0;
+        mine = smem + 2 * kStage + quad * Sm::slice;
+        sc = reinterpret_cast<float *>(mine + Sm::scales);
+        tiles = mine + Sm::scales + 128 + 2 * w * Sm::tile;
+    }
+    __device__ __forceinline__ void meet() const { named_bar_sync(1 + threadIdx.x / kQuad, kQuad); }
+    // The quarter's left operands and their scale, for the others and for the record
+    __device__ __forceinline__ void hand_over(const Acc (&s)[2 * kSteps], uint8_t *rec, float *rec_scales) const {
+        const float f = warp_scale(s);
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            uint32_t a[2][4];
+            left_of<2>(a, s[2 * i], s[2 * i + 1], f);
+            give<2>(mine + Sm::state + (w * kSteps + i) * 1024, a, lane);
+            if (rec) leave<NO>(rec + (w * kSteps + i) * 512, SliceRec<T, KP>::state_term, a, lane);
+        }
+        if (lane == 0) {
+            sc[w] = inverse_of(f);
+            if (rec) rec_scales[w] = inverse_of(f);
+        }
+    }
+};
+
+template <typename T, int KP>
+__global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) {
+    using R = Rec<T, KP>;
+    using Sm = SeqSmem<T, KP>;
+    using SR = SliceRec<T, KP>;
+    using Q = Seq<T, KP, false>;
+    constexpr int NI = Q::NI, NO = Q::NO, kSteps = Q::kSteps, kStage = Q::kStage;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int head = blockIdx.y, hk = head / (p.H / p.HK), v0 = (blockIdx.x * warps + warp) * kSlice;
-    uint8_t *const tiles = smem + 2 * kStage + 2 * warp * Sm::tile;
-    const int cols = p.V - v0;  // of this warp; may be none
+    const Q q(p, smem);
+    const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int live = live_rows(p, b), count = (live + kChunk - 1) / kChunk;
-        const int64_t st = static_cast<int64_t>(b) * p.H + head, first = static_cast<int64_t>(b) * p.T;
-        const uint8_t *const qk = p.qk_rec + (static_cast<int64_t>(b) * p.HK + hk) * p.chunks * R::qk;
-        const uint8_t *const g = p.g_rec + st * p.chunks * R::g(false);
+        const int64_t st = static_cast<int64_t>(b) * p.H + head, first = static_cast<int64_t>(b) * p.T, row_o = static_cast<int64_t>(p.H) * p.V;
+        const uint8_t *const qk = p.qk_rec + (static_cast<int64_t>(b) * p.HK + q.hk) * p.chunks * R::qk, *const g = p.g_rec + st * p.chunks * R::g(false);
         const T *const v = static_cast<const T *>(p.v) + b * p.v_sb + head * p.v_sh + v0;
         T *const o = static_cast<T *>(p.out) + (first * p.H + head) * p.V + v0;
-        const int64_t row_o = static_cast<int64_t>(p.H) * p.V;
+        const auto record = [&](int n) { return p.saved ? p.saved + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::fwd : nullptr; };
         const auto fetch = [&](int n) {
             copy_records(smem + (n & 1) * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, g + static_cast<int64_t>(n) * R::g(false), R::g(false));
-            if (cols > 0)
-                load_tile(tiles + (n & 1) * Sm::tile, v + static_cast<int64_t>(n) * kChunk * p.v_st, p.v_st, live - n * kChunk, cols, p.v_vec, lane);
+            const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
+            if (cols > 0) load_tile(q.tiles + (n & 1) * Sm::tile, t < live ? v + t * p.v_st : v, p.v_st, static_cast<int>(live - t), cols, p.v_vec, lane);
             copies_commit();
         };
-        Acc s[KP / 8];
-        read_state<KP>(s, p.state ? p.state + st * p.K * p.V : nullptr, p.K, p.V, v0, lane);
+        Acc s[2 * kSteps];
+        read_state(s, p.state ? p.state + st * p.K * p.V : nullptr, w * (KP / 4), p.K, p.V, v0, lane);
         __syncthreads();  // the batch entry before
-        if (count > 0) fetch(0);
+        if (count > 0) {
+            fetch(0);
+            uint8_t *const rec = cols > 0 ? record(0) : nullptr;
+            q.hand_over(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
+        }
         for (int n = 0; n < count; ++n) {
-            copies_wait();
-            __syncthreads();  // chunk n is there, and chunk n - 1 done with
+            copies_wait<0>();
+            __syncthreads();  // chunk n and the state's operands are there, and chunk n - 1 is done with
             if (n + 1 < count) fetch(n + 1);
-            if (cols <= 0) continue;
-            const int rows = live - n * kChunk < kChunk ? live - n * kChunk : kChunk;
-            const int64_t t0 = static_cast<int64_t>(n) * kChunk;
-            uint8_t *const tile = tiles + (n & 1) * Sm::tile;
-            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk;
+            if (cols <= 0) continue;  // the same for the slice's warps
+            const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;  // this warp's first row
+            uint8_t *const tile = q.tiles + (n & 1) * Sm::tile;
+            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
             const float *const f = reinterpret_cast<const float *>(smem + (n & 1) * kStage + R::qk + (2 + NO) * kSquare);
-            if (p.states) write_state<KP>(p.states + ((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * p.K * p.V, s, p.K, p.V, v0, lane);
-            float s0, s1;
-            row_scales(s, s0, s1);
-            Acc x[8], y[8], z[8];
+            uint8_t *const rec = record(n);
+            Acc x[2], z[2], y[2];  // S0^T K^T, S0^T Q^T
             clear(x), clear(z);
 #pragma unroll
-            for (int kk = 0; kk < KP / 16; ++kk) {  // x = S0^T K^T, z = S0^T Q^T
-                uint32_t a[2][4];
-                left_of<2>(a, s[2 * kk], s[2 * kk + 1], s0, s1);
+            for (int c = 0; c < 4; ++c) {
+                Acc tx[2], tz[2];
+                clear(tx), clear(tz);
 #pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    uint32_t r[NI][4];
+                for (int i = 0; i < kSteps; ++i) {
+                    const int kk = c * kSteps + i;
+                    uint32_t a[2][4], r[NI][4];
+                    take<2>(a, q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
-                    products<2, NI>(x[2 * np], x[2 * np + 1], a, r);
+                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
+                    products<2, NI>(tx[0], tx[1], a, r);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * np, 16 * kk, lane);
-                    products<NO, NI>(z[2 * np], z[2 * np + 1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
+                    for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * w, 16 * kk, lane);
+                    products<NO, NI>(tz[0], tz[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
                 }
+                add(x, tx, q.sc[c]), add(z, tz, q.sc[c]);
             }
-            s0 = inverse_of(s0), s1 = inverse_of(s1);
-            by_columns(x, f + F_GROW, s0 * f[F_K], s1 * f[F_K], lane);
-            by_columns(z, f + F_GROW, s0 * f[F_Q] * p.scale, s1 * f[F_Q] * p.scale, lane);
+            by_columns(x, f + F_GROW + 16 * w, f[F_K], lane);
+            by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale, lane);
             read_tile<T>(y, tile, lane);
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[nt][e] = y[nt][e] - x[nt][e];
-            row_scales(x, s0, s1);
-            triangle<false, 2, 2>(y, x, s0, s1, inv, lane);
-            by_rows(y, inverse_of(s0) * f[F_INV], inverse_of(s1) * f[F_INV]);  // E
-            if (p.errors) write_rows(p.errors + ((first + t0) * p.H + head) * p.V, row_o, y, rows, p.V, v0, lane);
-            by_columns(y, f + F_BETA, 1.0f, 1.0f, lane);  // U
-            row_scales(y, s0, s1);
-            triangle<false, NO, NO>(x, y, s0, s1, inv + 2 * kSquare, lane);
-            by_rows(x, inverse_of(s0) * f[F_P], inverse_of(s1) * f[F_P]);
+                for (int e = 0; e < 4; ++e) x[i][e] = y[i][e] - x[i][e];
+            {
+                const float sx = warp_scale(x);
+                uint32_t a[2][4];
+                left_of<2>(a, x[0], x[1], sx);
+                give<2>(q.mine + Sm::x(false) + w * 1024, a, lane);
+                if (lane == 0) q.sc[4 + w] = inverse_of(sx);
+            }
+            q.meet();
+            clear(y);  // E
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[nt][e] += x[nt][e];
-            __syncwarp();  // the tile is read
-            write_tile<T>(tile, z, lane);
-            __syncwarp();
-            store_tile<T>(o + t0 * row_o, row_o, tile, rows, static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk), cols, p.o_vec, lane);
-            by_columns(y, f + F_REST, 1.0f, 1.0f, lane);
-            row_scales(y, s0, s1);
-            uint32_t a[4][2][4];
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) left_of<2>(a[kb], y[2 * kb], y[2 * kb + 1], s0, s1);
-            s0 = inverse_of(s0) * f[F_K], s1 = inverse_of(s1) * f[F_K];
-            const float whole = f[F_WHOLE];
-#pragma unroll
-            for (int jp = 0; jp < KP / 32; ++jp) {  // S = whole S0 + K^T U, 32 keys' channels at a time
-                Acc t[4];
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb > w) continue;
+                Acc t[2];
                 clear(t);
-#pragma unroll
-                for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t r[NI][4];
-#pragma unroll
-                        for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, 32 * jp + 16 * e, lane);
-                        products<2, NI>(t[2 * e], t[2 * e + 1], a[kb], r);
-                    }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    Acc &w = s[4 * jp + i];
-                    w[0] = fmaf(t[i][0], s0, w[0] * whole), w[1] = fmaf(t[i][1], s0, w[1] * whole);
-                    w[2] = fmaf(t[i][2], s1, w[2] * whole), w[3] = fmaf(t[i][3], s1, w[3] * whole);
+                uint32_t a[2][4], r[2][4];
+                take<2>(a, q.mine + Sm::x(false) + kb * 1024, lane);
+                right<kChunk>(r[0], inv, 16 * w, 16 * kb, lane), right<kChunk>(r[1], inv + kSquare, 16 * w, 16 * kb, lane);
+                products<2, 2>(t[0], t[1], a, r);
+                add(y, t, q.sc[4 + kb] * f[F_INV]);
+            }
+            {
+                const float se = warp_scale(y);
+                uint32_t a[NO][4];
+                left_of<NO>(a, y[0], y[1], se);
+                give<NO>(q.mine + Sm::e + w * Sm::e_block, a, lane);
+                if (rec) leave<NO>(rec + SR::e + w * 512, kRowsTerm, a, lane);
+                by_columns(y, f + F_BETA + 16 * w, 1.0f, lane);
+                by_columns(y, f + F_REST + 16 * w, 1.0f, lane);
+                const float su = warp_scale(y);
+                uint32_t c[2][4];
+                left_of<2>(c, y[0], y[1], su);
+                give<2>(q.mine + Sm::u + w * 1024, c, lane);
+                if (lane == 0) {
+                    q.sc[8 + w] = inverse_of(se), q.sc[12 + w] = inverse_of(su);
+                    if (rec) reinterpret_cast<float *>(rec + SR::fwd_scales)[4 + w] = inverse_of(se);
                 }
+            }
+            q.meet();
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb > w) continue;
+                Acc t[2];
+                clear(t);
+                uint32_t a[NO][4], r[NO][4];
+                take<NO>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
+#pragma unroll
+                for (int j = 0; j < NO; ++j) right<kChunk>(r[j], pimg + j * kSquare, 16 * w, 16 * kb, lane);
+                products<NO, NO>(t[0], t[1], a, r);
+                add(z, t, q.sc[8 + kb] * f[F_P]);
+            }
+            // S = whole S0 + K^T U, this warp's quarter
+            const float whole = f[F_WHOLE], ik = f[F_K];
+#pragma unroll
+            for (int j = 0; j < 2 * kSteps; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] *= whole;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                Acc t[2 * kSteps];
+                clear(t);
+                uint32_t a[2][4];
+                take<2>(a, q.mine + Sm::u + kb * 1024, lane);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    uint32_t r[NI][4];
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
+                    products<2, NI>(t[2 * i], t[2 * i + 1], a, r);
+                }
+                add(s, t, q.sc[12 + kb] * ik);
+            }
+            if (n + 1 < count) {
+                uint8_t *const next = record(n + 1);
+                q.hand_over(s, next, reinterpret_cast<float *>(next + SR::fwd_scales));
+            }
+            if (t0 < p.T) {
+                write_tile<T>(tile, z, lane);
+                __syncwarp();
+                store_tile<T>(o + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
             }
         }
         if (cols > 0) {
-            for (int n = count; n < p.chunks; ++n) {
-                const int64_t t0 = static_cast<int64_t>(n) * kChunk;
-                store_tile<T>(o + t0 * row_o, row_o, tiles, 0, static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk), cols, p.o_vec, lane);
-            }
-            if (p.final_state) write_state<KP>(p.final_state + st * p.K * p.V, s, p.K, p.V, v0, lane);
+            for (int64_t t = static_cast<int64_t>(count) * kChunk + 16 * w; t < p.T; t += kChunk)
+                store_tile<T>(o + t * row_o, row_o, q.tiles, 0, static_cast<int>(p.T - t), cols, p.o_vec, lane);
+            if (p.final_state) write_state(p.final_state + st * p.K * p.V, s, w * (KP / 4), p.K, p.V, v0, lane);
         }
     }
 }
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(32 * kMostWarps, 1) based_delta_bwd_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) {
     using R = Rec<T, KP>;
     using Sm = SeqSmem<T, KP>;
-    constexpr int NI = Terms<T>::in, kStage = Sm::stage(true);
+    using SR = SliceRec<T, KP>;
+    using Q = Seq<T, KP, true>;
+    constexpr int NI = Q::NI, NO = Q::NO, kSteps = Q::kSteps, kStage = Q::kStage;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int head = blockIdx.y, hk = head / (p.H / p.HK), v0 = (blockIdx.x * warps + warp) * kSlice;
-    uint8_t *const tiles = smem + 2 * kStage + 2 * warp * Sm::tile;
-    const int cols = p.V - v0;
+    const Q q(p, smem);
+    const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int live = live_rows(p, b), count = (live + kChunk - 1) / kChunk;
-        const int64_t st = static_cast<int64_t>(b) * p.H + head, first = static_cast<int64_t>(b) * p.T;
-        const uint8_t *const qk = p.qk_rec + (static_cast<int64_t>(b) * p.HK + hk) * p.chunks * R::qk;
-        const uint8_t *const grec = p.g_rec + st * p.chunks * R::g(true);
+        const int64_t st = static_cast<int64_t>(b) * p.H + head, first = static_cast<int64_t>(b) * p.T, row_o = static_cast<int64_t>(p.H) * p.V;
+        const uint8_t *const qk = p.qk_rec + (static_cast<int64_t>(b) * p.HK + q.hk) * p.chunks * R::qk, *const grec = p.g_rec + st * p.chunks * R::g(true);
         const T *const dout = static_cast<const T *>(p.dout) + b * p.do_sb + head * p.do_sh + v0;
         T *const dv = static_cast<T *>(p.out) + (first * p.H + head) * p.V + v0;
-        const int64_t row_o = static_cast<int64_t>(p.H) * p.V;
+        const auto record = [&](int n) { return p.slice_rec + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::bwd; };
         const auto fetch = [&](int n) {
             copy_records(smem + (n & 1) * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, grec + static_cast<int64_t>(n) * R::g(true), R::g(true));
-            if (cols > 0)
-                load_tile(tiles + (n & 1) * Sm::tile, dout + static_cast<int64_t>(n) * kChunk * p.do_st, p.do_st, live - n * kChunk, cols, p.do_vec, lane);
+            const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
+            if (cols > 0) load_tile(q.tiles + (n & 1) * Sm::tile, t < live ? dout + t * p.do_st : dout, p.do_st, static_cast<int>(live - t), cols, p.do_vec, lane);
             copies_commit();
         };
-        Acc g[KP / 8];
-        read_state<KP>(g, p.state ? p.state + st * p.K * p.V : nullptr, p.K, p.V, v0, lane);
+        Acc g[2 * kSteps];
+        read_state(g, p.state ? p.state + st * p.K * p.V : nullptr, w * (KP / 4), p.K, p.V, v0, lane);
         __syncthreads();
-        if (count > 0) fetch(count - 1);
+        if (count > 0) {
+            fetch(count - 1);
+            if (cols > 0) q.hand_over(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
+        }
         for (int n = count - 1; n >= 0; --n) {
-            copies_wait();
+            copies_wait<0>();
             __syncthreads();
             if (n > 0) fetch(n - 1);
             if (cols <= 0) continue;
-            const int rows = live - n * kChunk < kChunk ? live - n * kChunk : kChunk;
-            const int64_t t0 = static_cast<int64_t>(n) * kChunk;
-            uint8_t *const tile = tiles + (n & 1) * Sm::tile;
-            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk;
+            const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;
+            uint8_t *const tile = q.tiles + (n & 1) * Sm::tile;
+            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
             const float *const f = reinterpret_cast<const float *>(smem + (n & 1) * kStage + R::qk + 4 * kSquare);
-            write_state<KP>(p.dstates + ((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * p.K * p.V, g, p.K, p.V, v0, lane);
-            float s0, s1;
-            row_scales(g, s0, s1);
-            Acc x[8], y[8], z[8];
-            clear(x);
-#pragma unroll
-            for (int kk = 0; kk < KP / 16; ++kk) {  // x = G^T K^T
-                uint32_t a[2][4];
-                left_of<2>(a, g[2 * kk], g[2 * kk + 1], s0, s1);
-#pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    uint32_t r[NI][4];
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
-                    products<2, NI>(x[2 * np], x[2 * np + 1], a, r);
-                }
+            uint8_t *const rec = record(n);
+            float *const rec_scales = reinterpret_cast<float *>(rec + SR::bwd_scales);
+            Acc x[2], y[2];
+            read_tile<T>(y, tile, lane);  // dO
+            {
+                const float so = warp_scale(y);
+                uint32_t a[NI][4];
+                left_of<NI>(a, y[0], y[1], so);
+                give<NI>(q.mine + Sm::e + w * Sm::e_block, a, lane);
+                leave<NI>(rec + SR::dout + w * 512, kRowsTerm, a, lane);
+                by_columns(y, f + F_GROW + 16 * w, p.scale, lane);
+                const float su = warp_scale(y);
+                uint32_t c[2][4];
+                left_of<2>(c, y[0], y[1], su);
+                give<2>(q.mine + Sm::u + w * 1024, c, lane);
+                if (lane == 0) q.sc[8 + w] = inverse_of(so), q.sc[12 + w] = inverse_of(su), rec_scales[8 + w] = inverse_of(so);
             }
-            by_columns(x, f + F_REST, inverse_of(s0) * f[F_K], inverse_of(s1) * f[F_K], lane);
-            read_tile<T>(z, tile, lane);  // dO
-            row_scales(z, s0, s1);
-            triangle<true, NI, 2>(y, z, s0, s1, inv + 2 * kSquare, lane);
-            s0 = inverse_of(s0) * f[F_P], s1 = inverse_of(s1) * f[F_P];
+            clear(x);  // dU
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int c = 0; c < 4; ++c) {
+                Acc t[2];
+                clear(t);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(y[nt][e], e < 2 ? s0 : s1, x[nt][e]);  // dU
-            row_scales(x, s0, s1);
-            triangle<true, 2, 2>(y, x, s0, s1, inv, lane);
-            by_rows(y, inverse_of(s0) * f[F_INV], inverse_of(s1) * f[F_INV]);  // dR
-            write_rows(p.dr + ((first + t0) * p.H + head) * p.V, row_o, y, rows, p.V, v0, lane);
-            by_columns(y, f + F_BETA, 1.0f, 1.0f, lane);  // dV
-            __syncwarp();
-            write_tile<T>(tile, y, lane);
-            __syncwarp();
-            store_tile<T>(dv + t0 * row_o, row_o, tile, rows, static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk), cols, p.o_vec, lane);
-            by_columns(y, f + F_GROW, -1.0f, -1.0f, lane);
-            by_columns(z, f + F_GROW, p.scale, p.scale, lane);
-            uint32_t a[4][2][4], c[4][2][4];
-            float u0, u1;
-            row_scales(y, s0, s1), row_scales(z, u0, u1);
+                for (int i = 0; i < kSteps; ++i) {
+                    const int kk = c * kSteps + i;
+                    uint32_t a[2][4], r[NI][4];
+                    take<2>(a, q.mine + Sm::state + kk * 1024, lane);
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
+                    products<2, NI>(t[0], t[1], a, r);
+                }
+                add(x, t, q.sc[c]);
+            }
+            by_columns(x, f + F_REST + 16 * w, f[F_K], lane);
+            q.meet();
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
-                left_of<2>(a[kb], y[2 * kb], y[2 * kb + 1], s0, s1);
-                left_of<2>(c[kb], z[2 * kb], z[2 * kb + 1], u0, u1);
+                if (kb < w) continue;
+                Acc t[2];
+                clear(t);
+                uint32_t a[NI][4], r[2][4];
+                take<NI>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
+                right_t<kChunk>(r[0], pimg, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], pimg + kSquare, 16 * kb, 16 * w, lane);
+                products<NI, 2>(t[0], t[1], a, r);
+                add(x, t, q.sc[8 + kb] * f[F_P]);
             }
-            s0 = inverse_of(s0) * f[F_K], s1 = inverse_of(s1) * f[F_K];
-            u0 = inverse_of(u0) * f[F_Q], u1 = inverse_of(u1) * f[F_Q];
-            const float whole = f[F_WHOLE];
+            {
+                const float sx = warp_scale(x);
+                uint32_t a[2][4];
+                left_of<2>(a, x[0], x[1], sx);
+                give<2>(q.mine + Sm::x(true) + w * 1024, a, lane);
+                if (lane == 0) q.sc[4 + w] = inverse_of(sx);
+            }
+            q.meet();
+            clear(y);  // dR
 #pragma unroll
-            for (int jp = 0; jp < KP / 16; ++jp) {
-                Acc t[2], w[2];
-                clear(t), clear(w);
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb < w) continue;
+                Acc t[2];
+                clear(t);
+                uint32_t a[2][4], r[2][4];
+                take<2>(a, q.mine + Sm::x(true) + kb * 1024, lane);
+                right_t<kChunk>(r[0], inv, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], inv + kSquare, 16 * kb, 16 * w, lane);
+                products<2, 2>(t[0], t[1], a, r);
+                add(y, t, q.sc[4 + kb] * f[F_INV]);
+            }
+            {
+                const float sr = warp_scale(y);
+                uint32_t a[NO][4];
+                left_of<NO>(a, y[0], y[1], sr);
+                leave<NO>(rec + SR::dr + w * 512, kRowsTerm, a, lane);
+                by_columns(y, f + F_BETA + 16 * w, 1.0f, lane);
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][e] = y[i][e];  // dV
+                by_columns(y, f + F_GROW + 16 * w, -1.0f, lane);
+                const float sw = warp_scale(y);
+                uint32_t c[2][4];
+                left_of<2>(c, y[0], y[1], sw);
+                give<2>(q.mine + Sm::w + w * 1024, c, lane);
+                if (lane == 0) q.sc[16 + w] = inverse_of(sw), rec_scales[4 + w] = inverse_of(sr);
+            }
+            q.meet();
+            const float whole = f[F_WHOLE], ik = f[F_K], iq = f[F_Q];
+#pragma unroll
+            for (int j = 0; j < 2 * kSteps; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[j][e] *= whole;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                Acc t[2 * kSteps], u[2 * kSteps];
+                clear(t), clear(u);
+                uint32_t a[2][4], c[2][4];
+                take<2>(a, q.mine + Sm::u + kb * 1024, lane), take<2>(c, q.mine + Sm::w + kb * 1024, lane);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
                     uint32_t r[NI][4];
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, 16 * jp, lane);
-                    products<2, NI>(t[0], t[1], a[kb], r);
+                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], qimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
+                    products<2, NI>(t[2 * i], t[2 * i + 1], a, r);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], qimg + j * R::term, 16 * kb, 16 * jp, lane);
-                    products<2, NI>(w[0], w[1], c[kb], r);
+                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
+                    products<2, NI>(u[2 * i], u[2 * i + 1], c, r);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    Acc &d = g[2 * jp + i];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = fmaf(t[i][e], e < 2 ? s0 : s1, fmaf(w[i][e], e < 2 ? u0 : u1, d[e] * whole));
-                }
+                add(g, t, q.sc[12 + kb] * iq), add(g, u, q.sc[16 + kb] * ik);
+            }
+            if (n > 0) q.hand_over(g, record(n - 1), reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
+            if (t0 < p.T) {
+                write_tile<T>(tile, x, lane);
+                __syncwarp();
+                store_tile<T>(dv + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
             }
         }
         if (cols > 0) {
-            for (int n = count; n < p.chunks; ++n) {
-                const int64_t t0 = static_cast<int64_t>(n) * kChunk;
-                store_tile<T>(dv + t0 * row_o, row_o, tiles, 0, static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk), cols, p.o_vec, lane);
-            }
-            if (p.final_state) write_state<KP>(p.final_state + st * p.K * p.V, g, p.K, p.V, v0, lane);
+            for (int64_t t = static_cast<int64_t>(count) * kChunk + 16 * w; t < p.T; t += kChunk)
+                store_tile<T>(dv + t * row_o, row_o, q.tiles, 0, static_cast<int>(p.T - t), cols, p.o_vec, lane);
+            if (p.final_state) write_state(p.final_state + st * p.K * p.V, g, w * (KP / 4), p.K, p.V, v0, lane);
         }
     }
 }
@@ -694,37 +828,24 @@ __global__ void __launch_bounds__(32 * kMostWarps, 1) based_delta_bwd_kernel(Del
 // Gradients that need no order. With dP = dO U^T and dA = -dR U^T (below the diagonal),
 //     dQ = scale grow dO S0^T + (scale D dP) K,
 //     dK = rest U G^T - beta grow dR S0^T + (scale D dP)^T Q + (beta D dA) K + (beta D dA)^T K,
-//     dbeta = rows of dR E,
+//     dbeta = the diagonal of dR E^T,
 // and the gradient of b_i, the sum of log decays up to row i, is what row i reads minus what it has written:
 //     db_i = q_i (scale grow dO S0^T)_i - k_i (beta grow dR S0^T + rest U G^T)_i + sum_j (N_ij - N_ji),  N = dP P + dA A,
 // with grow_last <S0, G> + sum_i k_i (rest U G^T)_i more at the last row; dgate_i is the sum of db from i on.
-// A CTA takes one chunk of one key head and adds up the value heads that share it, so that nothing is added by atomics.
+// A CTA takes one chunk of one key head and adds up the value heads that share it, so that nothing is added by atomics. Its 16 warps share out
+// the products' results, 16 rows and a quarter of the columns each; the slices' records come in by a ring of stages and are used as they lie.
 // ------------------------------------------------------------------------------------------------
-constexpr int kGradWarps = 8;
-constexpr int kTileV = 64;
+constexpr int kGradWarps = 16;
 
 template <typename T, int KP>
 struct GradSmem {
-    static constexpr int NO = Terms<T>::out;
-    static constexpr int f = Rec<T, KP>::qk, dout = f + F_COUNT * 4, u = dout + NO * kSquare, dr = u + NO * kSquare, s = dr + NO * kSquare,
-                         g = s + NO * KP * kTileV * 2, inv = g + NO * KP * kTileV * 2;  // the images' rows' inverse scales
-    static constexpr int part = inv + (3 * kChunk + 2 * KP) * 4;                        // sums: rows 2 x 64, next 2 x 64, columns 4 x 64, dbeta 64
-    static constexpr int red = part + 9 * kChunk * 4, bytes = red + 64;
+    using SR = SliceRec<T, KP>;
+    static constexpr int stages = Terms<T>::out == 1 ? 4 : 3, stage = SR::fwd + SR::bwd;
+    static constexpr int f = Rec<T, KP>::qk, ring = f + F_COUNT * 4, dp = ring + stages * stage, da = dp + Terms<T>::out * kSquare,
+                         part = da + Terms<T>::out * kSquare;  // sums: rows 4 x 64, next 4 x 64, columns 4 x 64, dbeta 64
+    static constexpr int red = part + 13 * kChunk * 4, bytes = red + 2 * kGradWarps * 4;
 };
 
-// Rows of eight words into an image of 64 columns, each row with its own scale. x: the word that this thread holds
-template <int NO>
-__device__ __forceinline__ void put_row(uint8_t *img, int term, float *inv, int row, int word, const float (&x)[8]) {
-    float m = most8(0.0f, x);
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float s = scale_for(m);
-    uint4 w[NO];
-    words_of<NO>(w, x, s);
-#pragma unroll
-    for (int j = 0; j < NO; ++j) *reinterpret_cast<uint4 *>(img + j * term + word_at<kTileV>(row, word)) = w[j];
-    if (word == 0) inv[row] = inverse_of(s);
-}
 // Two neighbouring elements of an image of key or query rows
 template <typename T, int KP>
 __device__ __forceinline__ float2 image_pair(const uint8_t *img, int row, int col, float inv) {
@@ -747,212 +868,205 @@ __device__ __forceinline__ void store_pair(T *p, int col, int K, bool pair, floa
         if (col + 1 < K) p[col + 1] = from_f32<T>(y);
     }
 }
+// A left operand's transpose, 16 of the chunk's rows by a slice's channels, and a right operand, a slice's channels by 16 columns, from the
+// blocks of a record
+__device__ __forceinline__ void left_blocks(uint32_t (&r)[4], uint32_t at, int lane) {
+    ldsm_t(r, at + ((lane >> 4) + 2 * (lane >> 3 & 1)) * 128 + (lane & 7) * 16);
+}
+__device__ __forceinline__ void right_blocks(uint32_t (&r)[4], uint32_t at, int lane) { ldsm_t(r, at + lane * 16); }
+
+// Slices differ in their scales. Their products are brought to the largest's by a power of two on one operand: what that takes from the last
+// bits of a slice is below the sum's. The exponent of a power of two, and 2^e for e <= 0 as two halves
+__device__ __forceinline__ int exponent(float pow2) { return static_cast<int>(__float_as_uint(pow2) >> 23) - 127; }
+__device__ __forceinline__ uint32_t halves(int e) {
+    const uint32_t h = e >= -14 ? static_cast<uint32_t>(15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+    return h | h << 16;
+}
+template <int TERMS>
+__device__ __forceinline__ void times(uint32_t (&to)[TERMS][4], const uint32_t (&a)[TERMS][4], int e) {
+    const uint32_t f = halves(e);
+#pragma unroll
+    for (int j = 0; j < TERMS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(to[j][i]) : "r"(a[j][i]), "r"(f));
+}
 
 template <typename T, int KP>
-__global__ void __launch_bounds__(32 * kGradWarps) based_delta_grad_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(DeltaParams p) {
     using R = Rec<T, KP>;
+    using SR = SliceRec<T, KP>;
     using Sm = GradSmem<T, KP>;
-    constexpr int NI = Terms<T>::in, NO = Terms<T>::out, NB = KP / 16;  // a warp's blocks of keys' channels
-    constexpr int kStateTerm = KP * kTileV * 2;
+    constexpr int NI = Terms<T>::in, NO = Terms<T>::out, NQ = KP / 64, kThreads = 32 * kGradWarps;  // NQ: 16 columns of a warp's quarter
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp & 3, wn = warp >> 2;
-    const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK;
-    const int r0 = 16 * wm + (lane >> 2), r1 = r0 + 8, col0 = wn * (KP / 2) + 2 * (lane & 3);  // this thread's accumulators
+    const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK, slices = (p.V + kSlice - 1) / kSlice;
+    const int r0 = 16 * wm + (lane >> 2), r1 = r0 + 8, col0 = wn * (KP / 4) + 2 * (lane & 3);  // this thread's accumulators
     float *const f = reinterpret_cast<float *>(smem + Sm::f);
-    float *const inv_do = reinterpret_cast<float *>(smem + Sm::inv), *const inv_u = inv_do + kChunk, *const inv_dr = inv_u + kChunk,
-                *const inv_s = inv_dr + kChunk, *const inv_g = inv_s + KP;
-    float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 2 * kChunk,
-                *const part_col = part_next + 2 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
-    const uint32_t base = smem_u32(smem), kimg = base, qimg = base + R::img, i_do = base + Sm::dout, i_u = base + Sm::u, i_dr = base + Sm::dr,
-                   i_s = base + Sm::s, i_g = base + Sm::g;
-    const bool vec32 = p.V % 4 == 0, pair = p.K % 2 == 0;
+    float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 4 * kChunk,
+                *const part_col = part_next + 4 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
+    const uint32_t base = smem_u32(smem), kimg = base, qimg = base + R::img;
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int64_t t0 = static_cast<int64_t>(n) * kChunk, first = static_cast<int64_t>(b) * p.T + t0;
         const int rows = min(kChunk, live_rows(p, b) - n * kChunk), all = static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk);
         T *const dq = static_cast<T *>(p.dq) + (first * p.HK + hk) * p.K, *const dk = static_cast<T *>(p.dk) + (first * p.HK + hk) * p.K;
         const int64_t row_k = static_cast<int64_t>(p.HK) * p.K;
-        // padding
-        for (int i = tid; i < (all - (rows < 0 ? 0 : rows)) * p.K; i += 32 * kGradWarps) {
-            const int row = (rows < 0 ? 0 : rows) + i / p.K, c = i % p.K;
-            dq[row * row_k + c] = dk[row * row_k + c] = from_f32<T>(0.0f);
+        const int from = rows < 0 ? 0 : rows;  // padding
+        for (int i = tid; i < (all - from) * p.K; i += kThreads) {
+            const int64_t at = (from + i / p.K) * row_k + i % p.K;
+            dq[at] = dk[at] = from_f32<T>(0.0f);
         }
-        for (int i = tid; i < (all - (rows < 0 ? 0 : rows)) * group; i += 32 * kGradWarps) {
-            const int64_t at = (first + (rows < 0 ? 0 : rows) + i / group) * p.H + hk * group + i % group;
+        for (int i = tid; i < (all - from) * group; i += kThreads) {
+            const int64_t at = (first + from + i / group) * p.H + hk * group + i % group;
             static_cast<T *>(p.dbeta)[at] = from_f32<T>(0.0f);
             if (p.dgate) static_cast<T *>(p.dgate)[at] = from_f32<T>(0.0f);
         }
         if (rows <= 0) continue;
         __syncthreads();  // the batch entry before
         copy_records(smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
-        copies_commit();
-        Acc aq[NB], ak[NB];
+        Acc aq[2 * NQ], ak[2 * NQ];
         clear(aq), clear(ak);
         for (int hh = 0; hh < group; ++hh) {
             const int head = hk * group + hh;
             const uint8_t *const rec = p.g_rec + ((static_cast<int64_t>(b) * p.H + head) * p.chunks + n) * R::g(true) + 4 * kSquare;
+            const int64_t at0 = ((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices;
+            const uint8_t *const fwd = p.saved + at0 * SR::fwd, *const bwd = p.slice_rec + at0 * SR::bwd;
+            const auto fetch = [&](int sl) {
+                if (sl < slices)
+                    copy_records(smem + Sm::ring + sl % Sm::stages * Sm::stage, fwd + static_cast<int64_t>(sl) * SR::fwd, SR::fwd,
+                                 bwd + static_cast<int64_t>(sl) * SR::bwd, SR::bwd);
+                copies_commit();
+            };
             __syncthreads();  // the head before
-            for (int i = tid; i < F_COUNT; i += 32 * kGradWarps) f[i] = reinterpret_cast<const float *>(rec)[i];
-            if (tid < kChunk) part_beta[tid] = 0.0f;
-            copies_wait();
-            __syncthreads();
-            const float ik = f[F_K], iq = f[F_Q];
-            float row0 = 0.0f, row1 = 0.0f, next0 = 0.0f, next1 = 0.0f, dot = 0.0f;
-            Acc dp[4], da[4];
-            clear(dp), clear(da);
-            const T *const dout = static_cast<const T *>(p.dout) + b * p.do_sb + t0 * p.do_st + head * p.do_sh;
-            const int64_t val = (first * p.H + head) * p.V, row_v = static_cast<int64_t>(p.H) * p.V;
-            const int64_t st = ((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * p.K * p.V;
-            for (int v0 = 0; v0 < p.V; v0 += kTileV) {
-                const int word = tid & 7, c = v0 + 8 * word;
-                if (v0) __syncthreads();  // the tiles before
+            for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = (tid >> 3) + 32 * i, there = row < rows ? p.V - c : 0;
-                    float x[8], e[8];
-                    load8(x, dout + row * p.do_st + c, there, p.do_vec);
-                    put_row<NO>(smem + Sm::dout, kSquare, inv_do, row, word, x);
-                    load8(e, p.errors + val + row * row_v + c, there, vec32);
-                    load8(x, p.dr + val + row * row_v + c, there, vec32);
+            for (int i = 0; i < Sm::stages - 1; ++i) fetch(i);
+            // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, dO E, dR E
+            int top[5] = {-1000, -1000, -1000, -1000, -1000};
+            for (int sl = lane; sl < slices; sl += 32) {
+                const float *const x = reinterpret_cast<const float *>(fwd + static_cast<int64_t>(sl) * SR::fwd + SR::fwd_scales),
+                                   *const y = reinterpret_cast<const float *>(bwd + static_cast<int64_t>(sl) * SR::bwd + SR::bwd_scales);
+                const int s = exponent(x[wn]), em = exponent(x[4 + wm]), en = exponent(x[4 + wn]), g = exponent(y[wn]), r = exponent(y[4 + wm]), o = exponent(y[8 + wm]);
+                top[0] = max(top[0], o + s), top[1] = max(top[1], r + s), top[2] = max(top[2], em + g), top[3] = max(top[3], o + en), top[4] = max(top[4], r + en);
+            }
+#pragma unroll
+            for (int i = 0; i < 5; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+            Acc aos[2 * NQ], ars[2 * NQ], aeg[2 * NQ], dp[2], da[2];
+            clear(aos), clear(ars), clear(aeg), clear(dp), clear(da);
+            float dot = 0.0f;
+            for (int sl = 0; sl < slices; ++sl) {
+                copies_wait<Sm::stages - 2>();
+                __syncthreads();  // the slice is there, and the one whose place comes next is done with
+                fetch(sl + Sm::stages - 1);
+                const uint8_t *const x = smem + Sm::ring + sl % Sm::stages * Sm::stage, *const y = x + SR::fwd;
+                const float *const xs = reinterpret_cast<const float *>(x + SR::fwd_scales), *const ys = reinterpret_cast<const float *>(y + SR::bwd_scales);
+                const int s = exponent(xs[wn]), em = exponent(xs[4 + wm]), en = exponent(xs[4 + wn]), g = exponent(ys[wn]), r = exponent(ys[4 + wm]), o = exponent(ys[8 + wm]);
+                const uint32_t xa = smem_u32(x), ya = smem_u32(y);
+                uint32_t lo[NI][4], lr[NO][4], le[NO][4], c[NO][4], d[NI][4], v[NO][4];
+#pragma unroll
+                for (int j = 0; j < NI; ++j) left_blocks(lo[j], ya + SR::dout + j * kRowsTerm + wm * 512, lane);
+#pragma unroll
+                for (int j = 0; j < NO; ++j) left_blocks(lr[j], ya + SR::dr + j * kRowsTerm + wm * 512, lane), left_blocks(le[j], xa + SR::e + j * kRowsTerm + wm * 512, lane);
+                if (wn <= wm) {
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + wn * 512, lane);
+                    times<NI>(d, lo, o + en - top[3]);
+                    products<NI, NO>(dp[0], dp[1], d, v);
+                    times<NO>(c, lr, r + en - top[4]);
+                    products<NO, NO>(da[0], da[1], c, v);
+                }
+                times<NI>(d, lo, o + s - top[0]), times<NO>(c, lr, r + s - top[1]), times<NO>(le, le, em + g - top[2]);
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + j * SR::state_term + (wn * NQ + i) * 512, lane);
+                    products<NI, NO>(aos[2 * i], aos[2 * i + 1], d, v);
+                    products<NO, NO>(ars[2 * i], ars[2 * i + 1], c, v);
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) right_blocks(v[j], ya + j * SR::state_term + (wn * NQ + i) * 512, lane);
+                    products<NO, NO>(aeg[2 * i], aeg[2 * i + 1], le, v);
+                }
+                // <S0, G>: words of eight elements
+                for (int i = tid; i < SR::state_term / 16; i += kThreads) {
+                    const int quarter = i / (SR::state_term / 64);
                     float sum = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(x[j], e[j], sum), e[j] *= f[F_BETA + row];
-                    put_row<NO>(smem + Sm::u, kSquare, inv_u, row, word, e);
-                    put_row<NO>(smem + Sm::dr, kSquare, inv_dr, row, word, x);
-#pragma unroll
-                    for (int d = 1; d < 8; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    if (word == 0) part_beta[row] += sum;
-                }
-#pragma unroll
-                for (int i = 0; i < KP / 32; ++i) {
-                    const int row = (tid >> 3) + 32 * i, there = row < p.K ? p.V - c : 0;
-                    float x[8], y[8];
-                    load8(x, p.states + st + static_cast<int64_t>(row) * p.V + c, there, vec32);
-                    load8(y, p.dstates + st + static_cast<int64_t>(row) * p.V + c, there, vec32);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
-                    put_row<NO>(smem + Sm::s, kStateTerm, inv_s, row, word, x);
-                    put_row<NO>(smem + Sm::g, kStateTerm, inv_g, row, word, y);
-                }
-                __syncthreads();
-                // the left operand's rows 16 wm .. + 15 by the rows of a state's image
-                const auto by_state = [&](Acc(&t)[NB], uint32_t l, uint32_t r) {
-                    clear(t);
-#pragma unroll
-                    for (int kk = 0; kk < kTileV / 16; ++kk) {
-                        uint32_t a[NO][4];
-#pragma unroll
-                        for (int j = 0; j < NO; ++j) left<kTileV>(a[j], l + j * kSquare, 16 * wm, 16 * kk, lane);
-#pragma unroll
-                        for (int jp = 0; jp < NB / 2; ++jp) {
-                            uint32_t x[NO][4];
-#pragma unroll
-                            for (int j = 0; j < NO; ++j) right<kTileV>(x[j], r + j * kStateTerm, wn * (KP / 2) + 16 * jp, 16 * kk, lane);
-                            products<NO, NO>(t[2 * jp], t[2 * jp + 1], a, x);
-                        }
-                    }
-                };
-                // to += t by rows' and columns' factors; returns its rows' products with the image's
-                const auto add = [&](Acc(&to)[NB], const Acc(&t)[NB], float c0, float c1, const float *cols, const uint8_t *img, float inv, float &d0, float &d1) {
-                    d0 = d1 = 0.0f;
-#pragma unroll
-                    for (int nt = 0; nt < NB; ++nt) {
-                        const int col = col0 + 8 * nt;
-                        const float2 y = *reinterpret_cast<const float2 *>(cols + col);
-                        const float2 x0 = image_pair<T, KP>(img, r0, col, inv), x1 = image_pair<T, KP>(img, r1, col, inv);
-                        const float z[4] = {t[nt][0] * (c0 * y.x), t[nt][1] * (c0 * y.y), t[nt][2] * (c1 * y.x), t[nt][3] * (c1 * y.y)};
-                        d0 = fmaf(z[0], x0.x, fmaf(z[1], x0.y, d0)), d1 = fmaf(z[2], x1.x, fmaf(z[3], x1.y, d1));
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) to[nt][e] += z[e];
-                    }
-                };
-                {
-                    Acc t[NB];
-                    float d0, d1;
-                    by_state(t, i_do, i_s);
-                    add(aq, t, p.scale * f[F_GROW + r0] * inv_do[r0], p.scale * f[F_GROW + r1] * inv_do[r1], inv_s, smem + R::img, iq, d0, d1);
-                    row0 += d0, row1 += d1;
-                    by_state(t, i_dr, i_s);
-                    add(ak, t, -f[F_BETA + r0] * f[F_GROW + r0] * inv_dr[r0], -f[F_BETA + r1] * f[F_GROW + r1] * inv_dr[r1], inv_s, smem, ik, d0, d1);
-                    row0 += d0, row1 += d1;
-                    by_state(t, i_u, i_g);
-                    add(ak, t, f[F_REST + r0] * inv_u[r0], f[F_REST + r1] * inv_u[r1], inv_g, smem, ik, d0, d1);
-                    next0 += d0, next1 += d1;
-                }
-                // dP and -dA: 32 columns of this warp
-                Acc tp[4], ta[4];
-                clear(tp), clear(ta);
-#pragma unroll
-                for (int kk = 0; kk < kTileV / 16; ++kk) {
-                    uint32_t a[NO][4], c4[NO][4];
+                    float a[8] = {}, e[8] = {};
 #pragma unroll
                     for (int j = 0; j < NO; ++j) {
-                        left<kTileV>(a[j], i_do + j * kSquare, 16 * wm, 16 * kk, lane);
-                        left<kTileV>(c4[j], i_dr + j * kSquare, 16 * wm, 16 * kk, lane);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(x + j * SR::state_term + i * 16), z = *reinterpret_cast<const uint4 *>(y + j * SR::state_term + i * 16);
+                        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int l = 0; l < 4; ++l) {
+                            const Vec<2> h = unpack<__half>(uw[l]), k = unpack<__half>(zw[l]);
+                            a[2 * l] += h.v[0], a[2 * l + 1] += h.v[1], e[2 * l] += k.v[0], e[2 * l + 1] += k.v[1];
+                        }
                     }
 #pragma unroll
-                    for (int jp = 0; jp < 2; ++jp) {
-                        if (2 * wn + jp > wm) continue;
-                        uint32_t x[NO][4];
-#pragma unroll
-                        for (int j = 0; j < NO; ++j) right<kTileV>(x[j], i_u + j * kSquare, 32 * wn + 16 * jp, 16 * kk, lane);
-                        products<NO, NO>(tp[2 * jp], tp[2 * jp + 1], a, x);
-                        products<NO, NO>(ta[2 * jp], ta[2 * jp + 1], c4, x);
-                    }
+                    for (int l = 0; l < 8; ++l) sum = fmaf(a[l], e[l], sum);
+                    dot = fmaf(sum * xs[quarter], ys[quarter], dot);
                 }
+            }
+            // rows' and columns' factors, and the rows' products with queries and keys
+            const float ik = f[F_K], iq = f[F_Q], c0 = f[F_GROW + r0], c1 = f[F_GROW + r1], b0 = f[F_BETA + r0], b1 = f[F_BETA + r1];
+            float row0 = 0.0f, row1 = 0.0f, next0 = 0.0f, next1 = 0.0f;
+            {
+                const float so = ldexpf(p.scale, top[0]), sr = ldexpf(-1.0f, top[1]), se = ldexpf(1.0f, top[2]);
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const float2 y = *reinterpret_cast<const float2 *>(inv_u + 32 * wn + 8 * nt + 2 * (lane & 3));
+                for (int i = 0; i < 2 * NQ; ++i) {
+                    const int col = col0 + 8 * i;
+                    const float2 q0 = image_pair<T, KP>(smem + R::img, r0, col, iq), q1 = image_pair<T, KP>(smem + R::img, r1, col, iq);
+                    const float2 k0 = image_pair<T, KP>(smem, r0, col, ik), k1 = image_pair<T, KP>(smem, r1, col, ik);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float w = e % 2 ? y.y : y.x;
-                        dp[nt][e] = fmaf(tp[nt][e], w * inv_do[e < 2 ? r0 : r1], dp[nt][e]);
-                        da[nt][e] = fmaf(ta[nt][e], -w * inv_dr[e < 2 ? r0 : r1], da[nt][e]);
+                        const float c = e < 2 ? c0 : c1, be = e < 2 ? b0 : b1, re = f[F_REST + (e < 2 ? r0 : r1)];
+                        const float x = aos[i][e] * so * c, y = ars[i][e] * sr * (be * c), z = aeg[i][e] * se * (re * be);
+                        const float qv = e == 0 ? q0.x : e == 1 ? q0.y : e == 2 ? q1.x : q1.y, kv = e == 0 ? k0.x : e == 1 ? k0.y : e == 2 ? k1.x : k1.y;
+                        (e < 2 ? row0 : row1) += x * qv + y * kv;
+                        (e < 2 ? next0 : next1) += z * kv;
+                        aq[i][e] += x, ak[i][e] += y + z;
                     }
                 }
             }
             // the products of queries and keys with keys, and with them the pairs' sums and the factors of dQ and dK
-            float pair0 = 0.0f, pair1 = 0.0f;
-            {
-                Acc sq[4], sk[4];
+            row0 -= next0, row1 -= next1;
+            float col[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, mp = 0.0f, ma = 0.0f;
+            if (wn <= wm) {
+                Acc sq[2], sk[2];
                 clear(sq), clear(sk);
 #pragma unroll
                 for (int kk = 0; kk < KP / 16; ++kk) {
-                    uint32_t a[NI][4], c4[NI][4];
+                    uint32_t a[NI][4], c4[NI][4], x[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) {
                         left<KP>(a[j], qimg + j * R::term, 16 * wm, 16 * kk, lane);
                         left<KP>(c4[j], kimg + j * R::term, 16 * wm, 16 * kk, lane);
+                        right<KP>(x[j], kimg + j * R::term, 16 * wn, 16 * kk, lane);
                     }
-#pragma unroll
-                    for (int jp = 0; jp < 2; ++jp) {
-                        if (2 * wn + jp > wm) continue;
-                        uint32_t x[NI][4];
-#pragma unroll
-                        for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 32 * wn + 16 * jp, 16 * kk, lane);
-                        products<NI, NI>(sq[2 * jp], sq[2 * jp + 1], a, x);
-                        products<NI, NI>(sk[2 * jp], sk[2 * jp + 1], c4, x);
-                    }
+                    products<NI, NI>(sq[0], sq[1], a, x);
+                    products<NI, NI>(sk[0], sk[1], c4, x);
                 }
+                const float sp = ldexpf(1.0f, top[3]), sa = ldexpf(-1.0f, top[4]);
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    float col[2] = {0.0f, 0.0f};
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = e < 2 ? r0 : r1, j = 32 * wn + 8 * nt + 2 * (lane & 3) + e % 2;
-                        const float d = j <= i ? expf((f[F_BHI + i] - f[F_BHI + j]) + (f[F_BLO + i] - f[F_BLO + j])) : 0.0f;
-                        const float dq_ = j <= i ? d * p.scale : 0.0f, dk_ = j < i ? d * f[F_BETA + i] : 0.0f;
-                        dp[nt][e] = j <= i ? dp[nt][e] * dq_ : 0.0f, da[nt][e] = j < i ? da[nt][e] * dk_ : 0.0f;
-                        const float sum = j <= i ? dp[nt][e] * sq[nt][e] * (iq * ik) + da[nt][e] * sk[nt][e] * (ik * ik) : 0.0f;
-                        (e < 2 ? pair0 : pair1) += sum;
-                        col[e % 2] += sum;
+                        const int i = e < 2 ? r0 : r1, j = 16 * wn + 8 * nt + 2 * (lane & 3) + e % 2;
+                        if (i == j) part_beta[i] = -da[nt][e] * sa;
+                        const float d = j <= i ? expf((f[F_BHI + i] - f[F_BHI + j]) + (f[F_BLO + i] - f[F_BLO + j])) : 0.0f, bj = f[F_BETA + j];
+                        dp[nt][e] = j <= i ? dp[nt][e] * sp * bj * (d * p.scale) : 0.0f;
+                        da[nt][e] = j < i ? da[nt][e] * sa * bj * (d * f[F_BETA + i]) : 0.0f;
+                        const float sum = j <= i ? dp[nt][e] * (sq[nt][e] * (iq * ik)) + da[nt][e] * (sk[nt][e] * (ik * ik)) : 0.0f;
+                        (e < 2 ? row0 : row1) += sum;
+                        col[nt][e % 2] += sum;
+                        mp = fmaxf(mp, fabsf(dp[nt][e])), ma = fmaxf(ma, fabsf(da[nt][e]));
                     }
-#pragma unroll
-                    for (int d = 4; d < 32; d *= 2) col[0] += __shfl_xor_sync(0xffffffffu, col[0], d), col[1] += __shfl_xor_sync(0xffffffffu, col[1], d);
-                    if (lane < 4) part_col[wm * kChunk + 32 * wn + 8 * nt + 2 * lane] = col[0], part_col[wm * kChunk + 32 * wn + 8 * nt + 2 * lane + 1] = col[1];
-                }
             }
-            row0 += pair0 - next0, row1 += pair1 - next1;
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) col[nt][0] += __shfl_xor_sync(0xffffffffu, col[nt][0], d), col[nt][1] += __shfl_xor_sync(0xffffffffu, col[nt][1], d);
+                if (lane < 4) *reinterpret_cast<float2 *>(part_col + wm * kChunk + 16 * wn + 8 * nt + 2 * lane) = make_float2(col[nt][0], col[nt][1]);
+            }
 #pragma unroll
             for (int d = 1; d < 4; d *= 2) {
                 row0 += __shfl_xor_sync(0xffffffffu, row0, d), row1 += __shfl_xor_sync(0xffffffffu, row1, d);
@@ -964,39 +1078,39 @@ __global__ void __launch_bounds__(32 * kGradWarps) based_delta_grad_kernel(Delta
             }
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-            float mp = 0.0f, ma = 0.0f;
+            if (lane == 0) red[kGradWarps + warp] = dot;
+            mp = scale_for(cta_most<kGradWarps>(mp, red)), ma = scale_for(cta_most<kGradWarps>(ma, red));
+            if (wn <= wm) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+                for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mp = fmaxf(mp, fabsf(dp[nt][e])), ma = fmaxf(ma, fabsf(da[nt][e]));
-            mp = scale_for(cta_most<kGradWarps>(mp, red)), ma = scale_for(cta_most<kGradWarps>(ma, red));  // with barriers: the tiles are done with
-            if (lane == 0) red[warp] = dot;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t at = word_at<kChunk>(e ? r1 : r0, 2 * wn + nt) + 4 * (lane & 3);
+                        uint32_t w[NO];
+                        terms<NO>(dp[nt][2 * e] * mp, dp[nt][2 * e + 1] * mp, w);
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+                        for (int j = 0; j < NO; ++j) *reinterpret_cast<uint32_t *>(smem + Sm::dp + j * kSquare + at) = w[j];
+                        terms<NO>(da[nt][2 * e] * ma, da[nt][2 * e + 1] * ma, w);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t at = word_at<kChunk>(e ? r1 : r0, 4 * wn + nt) + 4 * (lane & 3);
-                    uint32_t w[NO];
-                    terms<NO>(dp[nt][2 * e] * mp, dp[nt][2 * e + 1] * mp, w);
-#pragma unroll
-                    for (int j = 0; j < NO; ++j) *reinterpret_cast<uint32_t *>(smem + Sm::dout + j * kSquare + at) = w[j];
-                    terms<NO>(da[nt][2 * e] * ma, da[nt][2 * e + 1] * ma, w);
-#pragma unroll
-                    for (int j = 0; j < NO; ++j) *reinterpret_cast<uint32_t *>(smem + Sm::dr + j * kSquare + at) = w[j];
-                }
+                        for (int j = 0; j < NO; ++j) *reinterpret_cast<uint32_t *>(smem + Sm::da + j * kSquare + at) = w[j];
+                    }
+            }
             __syncthreads();
             if (warp == 0) {
                 float dots = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kGradWarps; ++i) dots += red[i];
+                for (int i = 0; i < kGradWarps; ++i) dots += red[kGradWarps + i];
                 float x[2], nx[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = 2 * lane + e;
+                    x[e] = nx[e] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[e] += part_row[j * kChunk + i], nx[e] += part_next[j * kChunk + i];
                     float c = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) c += part_col[j * kChunk + i];
-                    x[e] = part_row[i] + part_row[kChunk + i] - c, nx[e] = part_next[i] + part_next[kChunk + i];
+                    x[e] -= c;
                 }
                 float end = nx[0] + nx[1];
 #pragma unroll
@@ -1008,78 +1122,61 @@ __global__ void __launch_bounds__(32 * kGradWarps) based_delta_grad_kernel(Delta
                     const float o = __shfl_down_sync(0xffffffffu, sum, d);
                     if (lane + d < 32) sum += o;
                 }
-                const float behind = sum - (x[0] + x[1]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int i = 2 * lane + e;
-                    const float from = e ? behind + x[1] : behind + x[1] + x[0];
                     if (i < rows) {
                         const int64_t at = (first + i) * p.H + head;
                         static_cast<T *>(p.dbeta)[at] = from_f32<T>(part_beta[i]);
-                        if (p.dgate) static_cast<T *>(p.dgate)[at] = from_f32<T>(from + end);
+                        if (p.dgate) static_cast<T *>(p.dgate)[at] = from_f32<T>(sum - (e ? x[0] : 0.0f) + end);
                     }
                 }
             }
             {
-                const auto rank = [&](Acc(&to)[NB], uint32_t l, uint32_t r, float c) {  // to += c times the lower triangle (TURN: its transpose) of l by the rows of r
-                    Acc t[NB];
-                    clear(t);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        if (kb > wm) continue;
-                        uint32_t a[NO][4];
-#pragma unroll
-                        for (int j = 0; j < NO; ++j) left<kChunk>(a[j], l + j * kSquare, 16 * wm, 16 * kb, lane);
-#pragma unroll
-                        for (int jp = 0; jp < NB / 2; ++jp) {
-                            uint32_t x[NI][4];
-#pragma unroll
-                            for (int j = 0; j < NI; ++j) right_t<KP>(x[j], r + j * R::term, 16 * kb, wn * (KP / 2) + 16 * jp, lane);
-                            products<NO, NI>(t[2 * jp], t[2 * jp + 1], a, x);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NB; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) to[nt][e] = fmaf(t[nt][e], c, to[nt][e]);
-                };
-                const auto rank_t = [&](Acc(&to)[NB], uint32_t l, uint32_t r, float c) {
-                    Acc t[NB];
-                    clear(t);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        if (kb < wm) continue;
-                        uint32_t a[NO][4];
-#pragma unroll
-                        for (int j = 0; j < NO; ++j) left_t<kChunk>(a[j], l + j * kSquare, 16 * kb, 16 * wm, lane);
-#pragma unroll
-                        for (int jp = 0; jp < NB / 2; ++jp) {
-                            uint32_t x[NI][4];
-#pragma unroll
-                            for (int j = 0; j < NI; ++j) right_t<KP>(x[j], r + j * R::term, 16 * kb, wn * (KP / 2) + 16 * jp, lane);
-                            products<NO, NI>(t[2 * jp], t[2 * jp + 1], a, x);
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NB; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) to[nt][e] = fmaf(t[nt][e], c, to[nt][e]);
-                };
+                const uint32_t i_dp = base + Sm::dp, i_da = base + Sm::da;
                 mp = inverse_of(mp), ma = inverse_of(ma) * ik;
-                rank(aq, i_do, kimg, mp * ik);
-                rank_t(ak, i_do, qimg, mp * iq);
-                rank(ak, i_dr, kimg, ma);
-                rank_t(ak, i_dr, kimg, ma);
+                Acc tq[2 * NQ], tk[2 * NQ], ta[2 * NQ];
+                clear(tq), clear(tk), clear(ta);
+#pragma unroll
+                for (int kb = 0; kb < 4; ++kb) {
+                    uint32_t a[NO][4], c[NO][4], e[NO][4];
+                    if (kb <= wm) {  // the triangles' rows
+#pragma unroll
+                        for (int j = 0; j < NO; ++j)
+                            left<kChunk>(a[j], i_dp + j * kSquare, 16 * wm, 16 * kb, lane), left<kChunk>(c[j], i_da + j * kSquare, 16 * wm, 16 * kb, lane);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) {
+                        uint32_t x[NI][4];
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) right_t<KP>(x[j], kimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
+                        if (kb <= wm) {
+                            products<NO, NI>(tq[2 * i], tq[2 * i + 1], a, x);
+                            products<NO, NI>(ta[2 * i], ta[2 * i + 1], c, x);
+                        }
+                        if (kb >= wm) {  // their columns
+#pragma unroll
+                            for (int j = 0; j < NO; ++j) left_t<kChunk>(e[j], i_da + j * kSquare, 16 * kb, 16 * wm, lane);
+                            products<NO, NI>(ta[2 * i], ta[2 * i + 1], e, x);
+#pragma unroll
+                            for (int j = 0; j < NO; ++j) left_t<kChunk>(e[j], i_dp + j * kSquare, 16 * kb, 16 * wm, lane);
+#pragma unroll
+                            for (int j = 0; j < NI; ++j) right_t<KP>(x[j], qimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
+                            products<NO, NI>(tk[2 * i], tk[2 * i + 1], e, x);
+                        }
+                    }
+                }
+                add(aq, tq, mp * ik), add(ak, tk, mp * iq), add(ak, ta, ma);
             }
         }
 #pragma unroll
-        for (int nt = 0; nt < NB; ++nt)
+        for (int i = 0; i < 2 * NQ; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = e ? r1 : r0, col = col0 + 8 * nt;
+                const int row = e ? r1 : r0, c = col0 + 8 * i;
                 if (row >= rows) continue;
-                store_pair(dq + row * row_k, col, p.K, pair, aq[nt][2 * e], aq[nt][2 * e + 1]);
-                store_pair(dk + row * row_k, col, p.K, pair, ak[nt][2 * e], ak[nt][2 * e + 1]);
+                store_pair(dq + row * row_k, c, p.K, p.K % 2 == 0, aq[i][2 * e], aq[i][2 * e + 1]);
+                store_pair(dk + row * row_k, c, p.K, p.K % 2 == 0, ak[i][2 * e], ak[i][2 * e + 1]);
             }
     }
 }
@@ -1183,29 +1280,28 @@ __global__ void __launch_bounds__(32 * kStepWarps) based_delta_step_kernel(Delta
 // ------------------------------------------------------------------------------------------------
 constexpr int kMostGrid = 65535;
 
-// The parts of a workspace, each on 256 bytes
+// The parts of a workspace, each on 256 bytes, and the bytes that the forward pass saves
 struct DeltaSpace {
-    size_t qk, g, dr, dstates, total;
+    size_t qk, g, slices, total, saved;
 };
 inline int padded_keys(int K) { return K <= 64 ? 64 : 128; }
 template <typename T, int KP>
-DeltaSpace delta_space(int B, int T_, int H, int HK, int K, int V, bool bwd) {
-    const size_t chunks = (static_cast<size_t>(T_) + kChunk - 1) / kChunk, up = 255;
+DeltaSpace delta_space(int B, int T_, int H, int HK, int V, bool bwd) {
+    const size_t chunks = (static_cast<size_t>(T_) + kChunk - 1) / kChunk, up = 255, slices = chunks * B * H * ((V + kSlice - 1) / kSlice);
     DeltaSpace s;
     s.qk = 0;
     s.g = (s.qk + chunks * B * HK * Rec<T, KP>::qk + up) & ~up;
-    s.dr = (s.g + chunks * B * H * Rec<T, KP>::g(bwd) + up) & ~up;
-    s.dstates = bwd ? (s.dr + static_cast<size_t>(B) * T_ * H * V * 4 + up) & ~up : s.dr;
-    s.total = bwd ? (s.dstates + chunks * B * H * K * V * 4 + up) & ~up : s.dr;
+    s.slices = (s.g + chunks * B * H * Rec<T, KP>::g(bwd) + up) & ~up;
+    s.total = bwd ? (s.slices + slices * SliceRec<T, KP>::bwd + up) & ~up : s.slices;
+    s.saved = slices * SliceRec<T, KP>::fwd;
     return s;
 }
 DeltaSpace delta_space(int B, int T, int H, int HK, int K, int V, int dtype, bool bwd) {
     const bool wide = padded_keys(K) == 128;
-    // (the records of bfloat16 and float16 differ in the terms of the scores)
-    if (dtype == BASED_F32) return wide ? delta_space<float, 128>(B, T, H, HK, K, V, bwd) : delta_space<float, 64>(B, T, H, HK, K, V, bwd);
+    if (dtype == BASED_F32) return wide ? delta_space<float, 128>(B, T, H, HK, V, bwd) : delta_space<float, 64>(B, T, H, HK, V, bwd);
     if (dtype == BASED_BF16)
-        return wide ? delta_space<__nv_bfloat16, 128>(B, T, H, HK, K, V, bwd) : delta_space<__nv_bfloat16, 64>(B, T, H, HK, K, V, bwd);
-    return wide ? delta_space<__half, 128>(B, T, H, HK, K, V, bwd) : delta_space<__half, 64>(B, T, H, HK, K, V, bwd);
+        return wide ? delta_space<__nv_bfloat16, 128>(B, T, H, HK, V, bwd) : delta_space<__nv_bfloat16, 64>(B, T, H, HK, V, bwd);
+    return wide ? delta_space<__half, 128>(B, T, H, HK, V, bwd) : delta_space<__half, 64>(B, T, H, HK, V, bwd);
 }
 
 int check_delta_sizes(int64_t B, int64_t T, int H, int HK, int K, int V) {
@@ -1218,18 +1314,24 @@ int check_delta_sizes(int64_t B, int64_t T, int H, int HK, int K, int V) {
 template <typename T, int KP>
 int launch_delta(DeltaParams &p, bool bwd, int sms, cudaStream_t st) {
     using Sm = SeqSmem<T, KP>;
+    static_assert(Sm::bytes(true, Sm::most(true)) <= 227 * 1024 && Sm::bytes(false, Sm::most(false)) <= 227 * 1024 && GradSmem<T, KP>::bytes <= 227 * 1024,
+                  "shared memory of a CTA");
     const int slices = (p.V + kSlice - 1) / kSlice;
     const unsigned z = p.B < kMostGrid ? p.B : kMostGrid;
     void (*const prep)(DeltaParams) = bwd ? based_delta_prep_kernel<T, KP, true> : based_delta_prep_kernel<T, KP, false>;
     OPS_CUDA(allow(prep, PrepSmem<T, KP>::bytes));
     OPS_CUDA(launch_op(prep, dim3(p.chunks, p.HK, z), 32 * kPrepWarps, PrepSmem<T, KP>::bytes, st, p));
-    // As many warps to a CTA (they share its records) as leave a CTA for every SM
-    static_assert(Sm::bytes(true, Sm::warps) <= 227 * 1024 && GradSmem<T, KP>::bytes <= 227 * 1024, "shared memory of a CTA");
-    int warps = Sm::warps;
-    while (warps > 1 && (warps / 2 >= slices || static_cast<int64_t>(p.B) * p.H * ((slices + warps - 1) / warps) < sms)) warps /= 2;
+    // A CTA's slices share its records but also its SM: as many as give the fewest rounds of CTAs, each counted by what it takes
+    int per = 1;
+    const auto cost = [&](int n) {
+        const int64_t ctas = static_cast<int64_t>(p.B) * p.H * ((slices + n - 1) / n);
+        return static_cast<double>((ctas + sms - 1) / sms) * (1.0 + 0.45 * (n - 1));
+    };
+    for (int n = 2; n <= Sm::most(bwd) && n <= slices; ++n)
+        if (cost(n) <= cost(per)) per = n;
     void (*const seq)(DeltaParams) = bwd ? based_delta_bwd_kernel<T, KP> : based_delta_fwd_kernel<T, KP>;
-    OPS_CUDA(allow(seq, Sm::bytes(bwd, Sm::warps)));
-    OPS_CUDA(launch_op(seq, dim3((slices + warps - 1) / warps, p.H, z), 32 * warps, Sm::bytes(bwd, warps), st, p));
+    OPS_CUDA(allow(seq, Sm::bytes(bwd, Sm::most(bwd))));
+    OPS_CUDA(launch_op(seq, dim3((slices + per - 1) / per, p.H, z), kQuad * per, Sm::bytes(bwd, per), st, p));
     if (bwd) {
         void (*const grad)(DeltaParams) = based_delta_grad_kernel<T, KP>;
         OPS_CUDA(allow(grad, GradSmem<T, KP>::bytes));
@@ -1257,8 +1359,7 @@ bool clash(const Region (&r)[N]) {
 
 int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_bytes, based_stream_t stream) {
     if (!p.q || !p.k || !p.v || !p.beta || !p.out) return BASED_ERR_NULL_POINTER;
-    if (bwd && (!p.dout || !p.states || !p.errors || !p.dq || !p.dk || !p.dbeta || !p.gate != !p.dgate)) return BASED_ERR_NULL_POINTER;
-    if (!bwd && !p.states != !p.errors) return BASED_ERR_NULL_POINTER;
+    if (bwd && (!p.dout || !p.saved || !p.dq || !p.dk || !p.dbeta || !p.gate != !p.dgate)) return BASED_ERR_NULL_POINTER;
     if (!type_ok(dtype)) return BASED_ERR_UNSUPPORTED_TYPE;
     if (!(p.scale == p.scale)) return BASED_ERR_BAD_ARGUMENT;
     const int B = p.B, T = p.T, H = p.H, HK = p.HK, K = p.K, V = p.V;
@@ -1275,7 +1376,7 @@ int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_by
     const void *const typed[] = {p.q, p.k, p.v, p.beta, p.gate, p.dout, p.out, p.dq, p.dk, p.dbeta, p.dgate};
     for (const void *t : typed)
         if (!aligned(t, es)) return BASED_ERR_MISALIGNED;
-    if (!aligned(p.lengths, 4) || !aligned(p.state, 4) || !aligned(p.final_state, 4) || !aligned(p.states, 16) || !aligned(p.errors, 16) ||
+    if (!aligned(p.lengths, 4) || !aligned(p.state, 4) || !aligned(p.final_state, 4) || !aligned(p.saved, 16) ||
         !aligned(p.dq, 2 * es) || !aligned(p.dk, 2 * es))
         return BASED_ERR_MISALIGNED;
     const DeltaSpace space = delta_space(B, T, H, HK, K, V, dtype, bwd);
@@ -1290,7 +1391,7 @@ int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_by
         {three(p.beta, p.beta_sb, p.beta_st, 1, H, 1), false}, {three(p.gate, p.gate_sb, p.gate_st, 1, H, 1), false},
         {span(p.lengths, B - 1, 4), false},
         {p.state == p.final_state ? Span{0, 0} : span(p.state, states - 1, 4), false},  // may be replaced in place
-        {span(p.states, states * p.chunks - 1, 4), !bwd}, {span(p.errors, bth * V - 1, 4), !bwd},
+        {span(p.saved, static_cast<int64_t>(space.saved) - 1, 1), !bwd},
         {span(p.out, bth * V - 1, es), true}, {span(p.final_state, states - 1, 4), true},
         {span(p.dq, static_cast<int64_t>(B) * T * HK * K - 1, es), true}, {span(p.dk, static_cast<int64_t>(B) * T * HK * K - 1, es), true},
         {span(p.dbeta, bth - 1, es), true}, {span(p.dgate, bth - 1, es), true}, {span(workspace, static_cast<int64_t>(space.total) - 1, 1), true}};
@@ -1298,8 +1399,7 @@ int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_by
     int sms;
     if (const int rc = host_device(&sms)) return rc;
     uint8_t *const ws = static_cast<uint8_t *>(workspace);
-    p.qk_rec = ws + space.qk, p.g_rec = ws + space.g;
-    if (bwd) p.dr = reinterpret_cast<float *>(ws + space.dr), p.dstates = reinterpret_cast<float *>(ws + space.dstates);
+    p.qk_rec = ws + space.qk, p.g_rec = ws + space.g, p.slice_rec = ws + space.slices;
     const int64_t e = static_cast<int64_t>(es);
     const auto words = [&](const void *t, int64_t sb, int64_t s1, int64_t sh, int c) {
         return (sb | s1 | sh | c) * e % 16 == 0 && aligned(t, 16);
@@ -1332,21 +1432,20 @@ extern "C" {
 int based_delta_fwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, const void *k, int64_t k_sb, int64_t k_st, int64_t k_sh, const void *v,
                     int64_t v_sb, int64_t v_st, int64_t v_sh, const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate,
                     int64_t gate_sb, int64_t gate_st, int B, int T, int H, int HK, int K, int V, int dtype, float scale, const float *state,
-                    const int32_t *lengths, void *o, float *final_state, float *states, float *errors, void *workspace, size_t ws_bytes,
+                    const int32_t *lengths, void *o, float *final_state, void *saved, void *workspace, size_t ws_bytes,
                     based_stream_t stream) {
     based::DeltaParams p = {};
     p.q = q, p.q_sb = q_sb, p.q_st = q_st, p.q_sh = q_sh, p.k = k, p.k_sb = k_sb, p.k_st = k_st, p.k_sh = k_sh;
     p.v = v, p.v_sb = v_sb, p.v_st = v_st, p.v_sh = v_sh, p.beta = beta, p.beta_sb = beta_sb, p.beta_st = beta_st;
     p.gate = gate, p.gate_sb = gate_sb, p.gate_st = gate_st;
     p.B = B, p.T = T, p.H = H, p.HK = HK, p.K = K, p.V = V, p.scale = based::delta_scale(scale, K);
-    p.state = state, p.lengths = lengths, p.out = o, p.final_state = final_state, p.states = states, p.errors = errors;
+    p.state = state, p.lengths = lengths, p.out = o, p.final_state = final_state, p.saved = static_cast<uint8_t *>(saved);
     return based::run_delta(p, dtype, false, workspace, ws_bytes, stream);
 }
 
 int based_delta_bwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, const void *k, int64_t k_sb, int64_t k_st, int64_t k_sh, const void *v,
                     int64_t v_sb, int64_t v_st, int64_t v_sh, const void *beta, int64_t beta_sb, int64_t beta_st, const void *gate,
-                    int64_t gate_sb, int64_t gate_st, const void *dout, int64_t do_sb, int64_t do_st, int64_t do_sh, const float *states,
-                    const float *errors, int B, int T, int H, int HK, int K, int V, int dtype, float scale, const float *dfinal,
+                    int64_t gate_sb, int64_t gate_st, const void *dout, int64_t do_sb, int64_t do_st, int64_t do_sh, const void *saved, int B, int T, int H, int HK, int K, int V, int dtype, float scale, const float *dfinal,
                     const int32_t *lengths, void *dq, void *dk, void *dv, void *dbeta, void *dgate, float *dstate, void *workspace,
                     size_t ws_bytes, based_stream_t stream) {
     based::DeltaParams p = {};
@@ -1355,13 +1454,18 @@ int based_delta_bwd(const void *q, int64_t q_sb, int64_t q_st, int64_t q_sh, con
     p.gate = gate, p.gate_sb = gate_sb, p.gate_st = gate_st, p.dout = dout, p.do_sb = do_sb, p.do_st = do_st, p.do_sh = do_sh;
     p.B = B, p.T = T, p.H = H, p.HK = HK, p.K = K, p.V = V, p.scale = based::delta_scale(scale, K);
     p.state = dfinal, p.lengths = lengths, p.out = dv, p.dq = dq, p.dk = dk, p.dbeta = dbeta, p.dgate = dgate, p.final_state = dstate;
-    p.states = const_cast<float *>(states), p.errors = const_cast<float *>(errors);
+    p.saved = static_cast<uint8_t *>(const_cast<void *>(saved));
     return based::run_delta(p, dtype, true, workspace, ws_bytes, stream);
 }
 
 size_t based_delta_workspace_size(int B, int T, int H, int HK, int K, int V, int dtype, int backward) {
     if (based::check_delta_sizes(B, T, H, HK, K, V) != BASED_OK || !based::type_ok(dtype)) return 0;
     return based::delta_space(B, T, H, HK, K, V, dtype, backward != 0).total;
+}
+
+size_t based_delta_saved_size(int B, int T, int H, int K, int V, int dtype) {
+    if (based::check_delta_sizes(B, T, H, 1, K, V) != BASED_OK || !based::type_ok(dtype)) return 0;
+    return based::delta_space(B, T, H, 1, K, V, dtype, false).saved;
 }
 
 int based_delta_step(const void *q, int64_t q_sn, int64_t q_sh, const void *k, int64_t k_sn, int64_t k_sh, const void *v, int64_t v_sn, int64_t v_sh,

@@ -9,6 +9,8 @@
 // tcgen05.mma does, but its accumulators are registers: a chunk's chain of products runs
 // in one warp, which hands its results to itself without a barrier or a trip through memory.
 #pragma once
+#include <cstring>
+
 #include "ops_common.cuh"
 
 namespace based {
@@ -26,11 +28,11 @@ struct DeltaParams {
     const int32_t *lengths;
     const float *state;       // forward: the first state; backward: dfinal
     float *final_state;       // forward: the last state; backward: dstate
-    float *states, *errors;   // (B,chunks,H,K,V) states in front of the chunks; (B,T,H,V) v - a S^T k
+    uint8_t *saved;           // forward's records of the slices (SliceRec), or NULL
     void *out;                // forward: o; backward: dv
     void *dq, *dk, *dbeta, *dgate;
     uint8_t *qk_rec, *g_rec;  // the records of the chunks
-    float *dr, *dstates;      // backward: dbeta-free gradients (B,T,H,V) of what the rows write; of the states behind the chunks
+    uint8_t *slice_rec;       // backward's records of the slices
 };
 
 // The terms of an operand. Inputs of 16 bits are one float16 term (bfloat16 fits one after its scaling: 8 bits). Results that are
@@ -50,9 +52,9 @@ struct Terms<float> {
 
 // A chunk's records in the workspace: images of shared memory, copied as they are.
 //   of a key head: the scaled keys and queries, TERMS x 64 x KP float16 each
-//   of a value head: the inverse (two terms), the masked scores (forward: Terms::out, backward: two), 64 x 64 float16 each, and
-//   float32 numbers: per row grow = exp(b), rest = exp(b_last - b), beta, b in two parts (b: the sum of log decays up to the row),
-//   then the scales' inverses.
+//   of a value head: the inverse (two terms), the masked scores (forward: Terms::out, times beta of their columns; backward: two),
+//   64 x 64 float16 each, and float32 numbers: per row grow = exp(b), rest = exp(b_last - b), beta, b in two parts (b: the
+//   sum of log decays up to the row), then the scales' inverses.
 constexpr int kSquare = kChunk * kChunk * 2;  // bytes
 enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_INV = 320, F_P, F_WHOLE, F_K, F_Q, F_COUNT = 336 };
 template <typename T, int KP>
@@ -60,6 +62,21 @@ struct Rec {
     static constexpr int term = kChunk * KP * 2, img = Terms<T>::in * term, qk = 2 * img;
     __host__ __device__ static constexpr int scores(bool bwd) { return bwd ? 2 : Terms<T>::out; }
     __host__ __device__ static constexpr int g(bool bwd) { return (2 + scores(bwd)) * kSquare + F_COUNT * 4; }
+};
+
+// What the passes through the chunks leave for the gradients, per chunk, value head and slice of 16 channels of the values: float16 terms
+// in the order of left operands, 16 x 16 blocks of four 8 x 8 blocks (rows 0-7 and 8-15 of columns 0-7, the same of columns 8-15) of 128
+// bytes, rows the slice's channels; behind them the scales' inverses, one for each quarter of the keys' channels or 16 of the chunk's rows.
+constexpr int kSlice = 16;
+constexpr int kRowsTerm = kSlice * kChunk * 2;
+template <typename T, int KP>
+struct SliceRec {
+    static constexpr int in = Terms<T>::in, out = Terms<T>::out;
+    static constexpr int state_term = kSlice * KP * 2, states = out * state_term;
+    // forward: the state in front of the chunk, E
+    static constexpr int e = states, fwd_scales = e + out * kRowsTerm, fwd = fwd_scales + 32;
+    // backward: the gradient of the state behind the chunk, dR, dO
+    static constexpr int dr = states, dout = dr + out * kRowsTerm, bwd_scales = dout + in * kRowsTerm, bwd = bwd_scales + 48;
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -114,10 +131,28 @@ __device__ __forceinline__ void right_t(uint32_t (&r)[4], uint32_t img, int row,
 using Acc = float[4];  // a 16 x 8 block: rows lane / 4 and + 8, columns 2 (lane % 4) and + 1
 
 __device__ __forceinline__ void mma(Acc &d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int N>
+__device__ __forceinline__ void clear(Acc (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
+}
+// Two 16 x 8 blocks += the left operand's LT terms times the RT terms of a right operand
+template <int LT, int RT>
+__device__ __forceinline__ void products(Acc &x, Acc &y, const uint32_t (&a)[LT][4], const uint32_t (&b)[RT][4]) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < LT; ++i)
+            if (i + j < 2) {
+                mma(x, a[i], b[j][0], b[j][1]);
+                mma(y, a[i], b[j][2], b[j][3]);
+            }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -146,38 +181,30 @@ __device__ __forceinline__ void terms(float x, float y, uint32_t (&w)[TERMS]) {
     else
         w[0] = half2_of(x, y);
 }
-// The left operand made of two neighbouring accumulator blocks, rows scaled by s0 (lane / 4) and s1 (+ 8)
+// The left operand made of two neighbouring accumulator blocks
 template <int TERMS>
-__device__ __forceinline__ void left_of(uint32_t (&a)[TERMS][4], const Acc &x, const Acc &y, float s0, float s1) {
+__device__ __forceinline__ void left_of(uint32_t (&a)[TERMS][4], const Acc &x, const Acc &y, float s) {
     uint32_t w[TERMS];
-    terms<TERMS>(x[0] * s0, x[1] * s0, w);
+    terms<TERMS>(x[0] * s, x[1] * s, w);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) a[i][0] = w[i];
-    terms<TERMS>(x[2] * s1, x[3] * s1, w);
+    terms<TERMS>(x[2] * s, x[3] * s, w);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) a[i][1] = w[i];
-    terms<TERMS>(y[0] * s0, y[1] * s0, w);
+    terms<TERMS>(y[0] * s, y[1] * s, w);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) a[i][2] = w[i];
-    terms<TERMS>(y[2] * s1, y[3] * s1, w);
+    terms<TERMS>(y[2] * s, y[3] * s, w);
 #pragma unroll
     for (int i = 0; i < TERMS; ++i) a[i][3] = w[i];
 }
-// The scales of an accumulator row over N blocks, the same in the four lanes of a row
+// The scale of the warp's N blocks
 template <int N>
-__device__ __forceinline__ void row_scales(const Acc (&x)[N], float &s0, float &s1) {
-    float m0 = 0.0f, m1 = 0.0f;
+__device__ __forceinline__ float warp_scale(const Acc (&x)[N]) {
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        m0 = fmaxf(m0, fmaxf(fabsf(x[i][0]), fabsf(x[i][1])));
-        m1 = fmaxf(m1, fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
-    }
-#pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
-        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, d));
-        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, d));
-    }
-    s0 = scale_for(m0), s1 = scale_for(m1);
+    for (int i = 0; i < N; ++i) m = fmaxf(fmaxf(m, fmaxf(fabsf(x[i][0]), fabsf(x[i][1]))), fmaxf(fabsf(x[i][2]), fabsf(x[i][3])));
+    return scale_for(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -188,29 +215,49 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 4 bytes
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 
-// Eight elements at p, of which the first n exist; the others are zero. vec: p is on 16 bytes and n is 8, or in float32 4 or 8.
+// Eight elements at p as they lie there, of which the first n exist; the others are zero. words: p is on 16 bytes and n is at least 8, or 0 or less (in
+// float32 also 4). The loads of several calls go out together; the conversion comes after.
 template <typename T>
-__device__ __forceinline__ void load8(float (&x)[8], const T *p, int n, bool vec) {
-    if (vec && n >= 8) {
-        if constexpr (sizeof(T) == 2) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T *p, int n, bool words) {
+        constexpr int kEl = 16 / sizeof(T);
+        if (words) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Vec<2> f = unpack<T>(u[i]);
-                x[2 * i] = f.v[0], x[2 * i + 1] = f.v[1];
+            for (int i = 0; i < 8 / kEl; ++i) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (i * kEl < n) x = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
             }
         } else {
-            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-        }
-    } else {
+            T x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f32(p[i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+                x[i] = from_f32<T>(0.0f);
+                if (i < n) x[i] = p[i];
+            }
+            memcpy(w, x, sizeof(w));
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        constexpr int kEach = 4 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 8 / kEach; ++i) {
+            const Vec<kEach> f = unpack<T>(w[i]);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) x[i * kEach + e] = f.v[e];
+        }
+    }
+};
 // The terms of eight scaled elements as a word of each term's image
 template <int TERMS>
 __device__ __forceinline__ void words_of(uint4 (&w)[TERMS], const float (&x)[8], float s) {

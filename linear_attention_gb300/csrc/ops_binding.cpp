@@ -458,7 +458,6 @@ struct DeltaInputs {
 };
 // a scale; None selects the default
 float scale_arg(PyObject *o) { return o == Py_None ? 0.0f : static_cast<float>(float_arg(o)); }
-int64_t delta_chunks(int64_t T) { return (T + BASED_DELTA_ROWS - 1) / BASED_DELTA_ROWS; }
 
 // q, k, v, beta, gate, scale, state, lengths, save, out, final_state, workspace, stream
 PyObject *delta_fwd(PyObject *const *a) {
@@ -472,10 +471,10 @@ PyObject *delta_fwd(PyObject *const *a) {
     void *state = whole(optional_tensor(a[6], "state"), "state", {B, H, K, V}, kF32, at.dev);
     void *lengths = whole(optional_tensor(a[7], "lengths"), "lengths", {B}, ScalarType::Int, at.dev);
     const Tensor o = at.output(a[9], "out", in.v.sizes(), in.type), last = at.output(a[10], "final_state", {B, H, K, V}, kF32);
-    Tensor states, errors;
-    if (save) states = at.empty({B, delta_chunks(T), H, K, V}, kF32), errors = at.empty({B, T, H, V}, kF32);
+    Tensor saved;
+    if (save) saved = at.empty({static_cast<int64_t>(based_delta_saved_size(small(B), small(T), small(H), small(K), small(V), in.code))}, ScalarType::Byte);
     const auto result = [&] {
-        return tuple(wrap(o), wrap(last), save ? tuple(wrap(states), wrap(errors)) : none());
+        return tuple(wrap(o), wrap(last), wrap_or_none(saved));
     };
     if ((B == 0 || T == 0) && H > 0 && K > 0 && V > 0) {
         settle(last, optional_tensor(a[6], "state"));
@@ -487,8 +486,7 @@ PyObject *delta_fwd(PyObject *const *a) {
                           in.beta.stride(0), in.beta.stride(1), in.gate_data(), in.gate_stride(0), in.gate_stride(1), small(B), small(T),
                           small(H), small(in.HK), small(K), small(V), in.code, scale, static_cast<float *>(state),
                           static_cast<int32_t *>(lengths), o.data_ptr(), static_cast<float *>(last.data_ptr()),
-                          save ? static_cast<float *>(states.data_ptr()) : nullptr, save ? static_cast<float *>(errors.data_ptr()) : nullptr,
-                          ws.data_ptr(), ws.nbytes(), at.raw()),
+                          save ? saved.data_ptr() : nullptr, ws.data_ptr(), ws.nbytes(), at.raw()),
           "based_delta_fwd");
     return result();
 }
@@ -502,10 +500,9 @@ PyObject *delta_bwd(PyObject *const *a) {
     in.check(at.dev);
     input(dout, "dout", in.v.sizes(), in.type, at.dev);
     const int64_t B = in.v.size(0), T = in.v.size(1), H = in.H, K = in.K, V = in.V;
-    if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2)
-        refuse(PyExc_ValueError, "based_delta_bwd needs what based_delta_fwd(..., save=True) saved");
-    void *states = whole(&tensor(PyTuple_GET_ITEM(a[6], 0), "saved"), "saved states", {B, delta_chunks(T), H, K, V}, kF32, at.dev);
-    void *errors = whole(&tensor(PyTuple_GET_ITEM(a[6], 1), "saved"), "saved errors", {B, T, H, V}, kF32, at.dev);
+    if (a[6] == Py_None) refuse(PyExc_ValueError, "based_delta_bwd needs what based_delta_fwd(..., save=True) saved");
+    void *saved = whole(&tensor(a[6], "saved"), "saved", {static_cast<int64_t>(based_delta_saved_size(small(B), small(T), small(H), small(K), small(V), in.code))},
+                        ScalarType::Byte, at.dev);
     void *dfinal = whole(optional_tensor(a[8], "dfinal"), "dfinal", {B, H, K, V}, kF32, at.dev);
     void *lengths = whole(optional_tensor(a[9], "lengths"), "lengths", {B}, ScalarType::Int, at.dev);
     const Tensor dq = at.empty(in.q.sizes(), in.type), dk = at.empty(in.q.sizes(), in.type), dv = at.empty(in.v.sizes(), in.type),
@@ -521,8 +518,7 @@ PyObject *delta_bwd(PyObject *const *a) {
     check(based_delta_bwd(in.q.data_ptr(), in.q.stride(0), in.q.stride(1), in.q.stride(2), in.k.data_ptr(), in.k.stride(0), in.k.stride(1),
                           in.k.stride(2), in.v.data_ptr(), in.v.stride(0), in.v.stride(1), in.v.stride(2), in.beta.data_ptr(),
                           in.beta.stride(0), in.beta.stride(1), in.gate_data(), in.gate_stride(0), in.gate_stride(1), dout.data_ptr(),
-                          dout.stride(0), dout.stride(1), dout.stride(2), static_cast<float *>(states), static_cast<float *>(errors),
-                          small(B), small(T), small(H), small(in.HK), small(K), small(V), in.code, scale, static_cast<float *>(dfinal),
+                          dout.stride(0), dout.stride(1), dout.stride(2), saved, small(B), small(T), small(H), small(in.HK), small(K), small(V), in.code, scale, static_cast<float *>(dfinal),
                           static_cast<int32_t *>(lengths), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dbeta.data_ptr(),
                           in.gate ? dgate.data_ptr() : nullptr, static_cast<float *>(dstate.data_ptr()), ws.data_ptr(), ws.nbytes(), at.raw()),
           "based_delta_bwd");

@@ -69,12 +69,14 @@ def library():
     L.based_embed_bwd.argtypes = [p, i, p, l, l, i, i, i, f, p, i, p, z, p]
     L.based_embed_bwd_workspace_size.argtypes = [l, i, i]
     heads = [l, l, l]
-    L.based_delta_fwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, i, i, i, i, i, i, i, f, p, p, p, p, p, p, p, z, p]
-    L.based_delta_bwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, p, *heads, p, p, i, i, i, i, i, i, i, f, p, p,
+    L.based_delta_fwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, i, i, i, i, i, i, i, f, p, p, p, p, p, p, z, p]
+    L.based_delta_bwd.argtypes = [p, *heads, p, *heads, p, *heads, p, l, l, p, l, l, p, *heads, p, i, i, i, i, i, i, i, f, p, p,
                                   p, p, p, p, p, p, p, z, p]
     L.based_delta_step.argtypes = [p, l, l, p, l, l, p, l, l, p, l, p, l, i, i, i, i, i, i, i, f, p, p, p, p]
     L.based_delta_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
     L.based_delta_workspace_size.restype = z
+    L.based_delta_saved_size.argtypes = [i, i, i, i, i, i]
+    L.based_delta_saved_size.restype = z
     L.based_rms_fwd.argtypes = [p, l, p, l, i, p, i, l, i, f, p, p, i, p, p]
     L.based_rms_bwd.argtypes = [p, l, p, l, i, p, i, p, l, l, i, f, p, p, p, i, p, z, p]
     L.based_rms_bwd_workspace_size.argtypes = [l, i]
@@ -192,28 +194,25 @@ def embed_bwd_workspace_size(n: int, rows: int, channels: int) -> int:
 # ------------------------------------------------------------------------------------------------
 # Gated delta rule
 # ------------------------------------------------------------------------------------------------
-Saved = Tuple[torch.Tensor, torch.Tensor]
-
-
 def based_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor] = None,
                     scale: Optional[float] = None, state: Optional[torch.Tensor] = None,
                     lengths: Optional[torch.Tensor] = None, save: bool = False, out: Optional[torch.Tensor] = None,
                     final_state: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, Optional[Saved]]:
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
     """S_t = a_t S_{t-1} + k_t u_t^T with u_t = beta_t (v_t - a_t S_{t-1}^T k_t), o_t = scale S_t^T q_t along axis 1 of
     q, k (B,T,HK,K) and v (B,T,H,V); a = exp(gate), or 1 without a gate; beta and gate (B,T,H) have the type of v.
 
     Heads of v share the HK heads of q and k in consecutive groups. ``scale`` defaults to K^-0.5. ``state`` (B,H,K,V)
     float32 is S before the first row (default zero); ``lengths`` (B) int32 marks rows t >= lengths[b] as padding
-    (zero output, state kept). Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the pair of
-    float32 tensors that based_delta_bwd needs, or None without ``save``). ``final_state`` may be ``state``, to update
+    (zero output, state kept). Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the bytes
+    that based_delta_bwd needs, or None without ``save``). ``final_state`` may be ``state``, to update
     it in place. ``workspace``: a CUDA byte tensor of at least delta_workspace_size(...) bytes (default: one is allocated).
     """
     return _C.delta_fwd(q, k, v, beta, gate, scale, state, lengths, save, out, final_state, workspace, stream)
 
 
 def based_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor],
-                    dout: torch.Tensor, saved: Saved, scale: Optional[float] = None, dfinal: Optional[torch.Tensor] = None,
+                    dout: torch.Tensor, saved: torch.Tensor, scale: Optional[float] = None, dfinal: Optional[torch.Tensor] = None,
                     lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                     stream: Optional[torch.cuda.Stream] = None):
     """Gradients of based_delta_fwd for the gradients dout (B,T,H,V) of its output and dfinal (B,H,K,V) float32 of its
