@@ -138,17 +138,60 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
         uint8_t *const rec = p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk;
         const T *const ks = static_cast<const T *>(p.k) + b * p.k_sb + t0 * p.k_st + hk * p.k_sh;
         const T *const qs = static_cast<const T *>(p.q) + b * p.q_sb + t0 * p.q_st + hk * p.q_sh;
+        const auto record = [&](int head) { return p.g_rec + ((static_cast<int64_t>(b) * p.H + head) * p.chunks + n) * R::g(BWD); };
+        const auto scan = [&](int head) {
+            if (warp != 0) return;
+            float *const f = reinterpret_cast<float *>(record(head) + (2 + NP) * kSquare);
+            // Sums of log decays in 64 bits, kept as two floats: differences of neighbours then have float32's relative
+            // accuracy however much has decayed before. -1e5 stands for anything below it, -inf among it: its decay is 0.
+            double x[2], be[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                float v = 0.0f, y = 0.0f;
+                if (i < rows) {
+                    if (p.gate) v = to_f32(static_cast<const T *>(p.gate)[b * p.gate_sb + (t0 + i) * p.gate_st + head]);
+                    y = to_f32(static_cast<const T *>(p.beta)[b * p.beta_sb + (t0 + i) * p.beta_st + head]);
+                }
+                x[e] = v < -1e5f ? -1e5 : static_cast<double>(v), be[e] = y;
+            }
+            x[1] += x[0];
+            double sum = x[1];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const double o = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            const double before = sum - x[1];
+            const double last = __shfl_sync(0xffffffffu, sum, 31);
+            float most = 0.0f, grow_most = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * lane + e;
+                const double v = before + x[e];
+                const float grow = expf(static_cast<float>(v)), rest = expf(static_cast<float>(last - v)), y = static_cast<float>(be[e]);
+                bhi[i] = static_cast<float>(v), blo[i] = static_cast<float>(v - bhi[i]), beta[i] = y;
+                f[F_GROW + i] = grow, f[F_REST + i] = rest, f[F_BETA + i] = y, f[F_BHI + i] = bhi[i], f[F_BLO + i] = blo[i];
+                f[F_BF + i] = y * (BWD ? grow : rest);
+                most = fmaxf(most, fabsf(y * (BWD ? grow : rest))), grow_most = fmaxf(grow_most, grow);
+            }
+            most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+            grow_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(grow_most)));
+            if (lane == 0) f[F_WHOLE] = expf(static_cast<float>(last)), f[F_BFMOST] = most, f[F_GROWMOST] = grow_most;
+        };
         __syncthreads();  // the batch entry before
         float ik, iq;
         if constexpr (sizeof(T) == 2) {  // (registers for both only in 16 bits)
             Raw<T> rk[prep_words(KP)], rq[prep_words(KP)];
             read_rows<T, KP>(rk, ks, p.k_st, rows, p.K, p.qk_vec);
             read_rows<T, KP>(rq, qs, p.q_st, rows, p.K, p.qk_vec);
+            scan(hk * group);  // while the rows are on their way
             ik = make_image<T, KP>(rk, smem, rec, red);
             iq = make_image<T, KP>(rq, smem + R::img, rec + R::img, red);
         } else {
             Raw<T> raw[prep_words(KP)];
             read_rows<T, KP>(raw, ks, p.k_st, rows, p.K, p.qk_vec);
+            scan(hk * group);
             ik = make_image<T, KP>(raw, smem, rec, red);
             read_rows<T, KP>(raw, qs, p.q_st, rows, p.K, p.qk_vec);
             iq = make_image<T, KP>(raw, smem + R::img, rec + R::img, red);
@@ -181,41 +224,9 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
         const float fk = ik * ik, fq = iq * ik * p.scale;
         for (int hh = 0; hh < group; ++hh) {
             const int head = hk * group + hh;
-            uint8_t *const g = p.g_rec + ((static_cast<int64_t>(b) * p.H + head) * p.chunks + n) * R::g(BWD);
+            uint8_t *const g = record(head);
             float *const f = reinterpret_cast<float *>(g + (2 + NP) * kSquare);
-            if (warp == 0) {
-                // Sums of log decays in 64 bits, kept as two floats: differences of neighbours then have float32's relative
-                // accuracy however much has decayed before. -1e5 stands for anything below it, -inf among it: its decay is 0.
-                double x[2], be[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 2 * lane + e;
-                    float v = 0.0f, y = 0.0f;
-                    if (i < rows) {
-                        if (p.gate) v = to_f32(static_cast<const T *>(p.gate)[b * p.gate_sb + (t0 + i) * p.gate_st + head]);
-                        y = to_f32(static_cast<const T *>(p.beta)[b * p.beta_sb + (t0 + i) * p.beta_st + head]);
-                    }
-                    x[e] = v < -1e5f ? -1e5 : static_cast<double>(v), be[e] = y;
-                }
-                x[1] += x[0];
-                double sum = x[1];
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const double o = __shfl_up_sync(0xffffffffu, sum, d);
-                    if (lane >= d) sum += o;
-                }
-                const double before = sum - x[1];
-                const double last = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 2 * lane + e;
-                    const double v = before + x[e];
-                    bhi[i] = static_cast<float>(v), blo[i] = static_cast<float>(v - bhi[i]), beta[i] = static_cast<float>(be[e]);
-                    f[F_GROW + i] = expf(static_cast<float>(v)), f[F_REST + i] = expf(static_cast<float>(last - v));
-                    f[F_BETA + i] = beta[i], f[F_BHI + i] = bhi[i], f[F_BLO + i] = blo[i];
-                }
-                if (lane == 0) f[F_WHOLE] = expf(static_cast<float>(last)), f[F_K] = ik, f[F_Q] = iq;
-            }
+            if (hh) scan(head);
             for (int i = tid; i < kChunk * kLd / 4; i += 32 * kPrepWarps)
                 if (hh) reinterpret_cast<float4 *>(h)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             __syncthreads();  // the sums, and the images are done with
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
                 const uint32_t at = word_at<kChunk>(tid / 8 + 16 * r, tid % 8);
                 *reinterpret_cast<uint4 *>(g + at) = z[0], *reinterpret_cast<uint4 *>(g + kSquare + at) = z[1];
             }
-            if (tid == 0) f[F_INV] = inverse_of(sh), f[F_P] = inverse_of(sp);
+            if (tid == 0) f[F_INV] = inverse_of(sh), f[F_P] = inverse_of(sp), f[F_K] = ik, f[F_Q] = iq;
         }
     }
 }
@@ -474,7 +485,7 @@ struct Seq {
     const DeltaParams &p;
     uint8_t *smem, *mine;  // the records; the slice's
     int lane, w, slice, head, hk, v0, cols;
-    float *sc;  // scales' inverses: of the state's quarters, then of 16 rows of x, e, u, w
+    float *sc;  // the state's quarters' largest as inverse scales; the inverse scale of its operands; of 16 rows of x, and of e backward
     uint8_t *tiles;
 
     __device__ __forceinline__ Seq(const DeltaParams &p_, uint8_t *smem_) : p(p_), smem(smem_) {
@@ -487,9 +498,11 @@ struct Seq {
         tiles = mine + Sm::scales + 128 + 2 * w * Sm::tile;
     }
     __device__ __forceinline__ void meet() const { named_bar_sync(1 + threadIdx.x / kQuad, kQuad); }
-    // The quarter's left operands and their scale, for the others and for the record
-    __device__ __forceinline__ void hand_over(const Acc (&s)[2 * kSteps], uint8_t *rec, float *rec_scales) const {
-        const float f = warp_scale(s);
+    // A bound on the state's magnitudes, from its warps' largest
+    __device__ __forceinline__ float state_most() const { return kTop * fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])); }
+    // The quarter's left operands, scaled for magnitudes up to `most`, for the others and for the record; and its own largest
+    __device__ __forceinline__ void hand_over(const Acc (&s)[2 * kSteps], float most, uint8_t *rec, float *rec_scales) const {
+        const float f = scale_for(most), own = inverse_of(warp_scale(s));
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             uint32_t a[2][4];
@@ -498,9 +511,19 @@ struct Seq {
             if (rec) leave<NO>(rec + (w * kSteps + i) * 512, SliceRec<T, KP>::state_term, a, lane);
         }
         if (lane == 0) {
-            sc[w] = inverse_of(f);
+            sc[w] = own;
+            if (w == 0) sc[4] = inverse_of(f);
             if (rec) rec_scales[w] = inverse_of(f);
         }
+    }
+    // The first state: its largest is found first
+    __device__ __forceinline__ void begin(const Acc (&s)[2 * kSteps], uint8_t *rec, float *rec_scales) const {
+        const float own = inverse_of(warp_scale(s));
+        if (lane == 0) sc[w] = own;
+        meet();
+        const float most = state_most();
+        meet();
+        hand_over(s, most, rec, rec_scales);
     }
 };
 
@@ -534,7 +557,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
         if (count > 0) {
             fetch(0);
             uint8_t *const rec = cols > 0 ? record(0) : nullptr;
-            q.hand_over(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
+            q.begin(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
         }
         for (int n = 0; n < count; ++n) {
             copies_wait<0>();
@@ -548,26 +571,20 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             uint8_t *const rec = record(n);
             Acc x[2], z[2], y[2];  // S0^T K^T, S0^T Q^T
             clear(x), clear(z);
+            const float is = q.sc[4], before = q.state_most();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                Acc tx[2], tz[2];
-                clear(tx), clear(tz);
+            for (int kk = 0; kk < KP / 16; ++kk) {
+                uint32_t a[2][4], r[NI][4];
+                take<2>(a, q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int kk = c * kSteps + i;
-                    uint32_t a[2][4], r[NI][4];
-                    take<2>(a, q.mine + Sm::state + kk * 1024, lane);
+                for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
+                products<2, NI>(x[0], x[1], a, r);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                    products<2, NI>(tx[0], tx[1], a, r);
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * w, 16 * kk, lane);
-                    products<NO, NI>(tz[0], tz[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
-                }
-                add(x, tx, q.sc[c]), add(z, tz, q.sc[c]);
+                for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * w, 16 * kk, lane);
+                products<NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
             }
-            by_columns(x, f + F_GROW + 16 * w, f[F_K], lane);
-            by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale, lane);
+            by_columns(x, f + F_GROW + 16 * w, f[F_K] * is, lane);
+            by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale * is, lane);
             read_tile<T>(y, tile, lane);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 uint32_t a[2][4];
                 left_of<2>(a, x[0], x[1], sx);
                 give<2>(q.mine + Sm::x(false) + w * 1024, a, lane);
-                if (lane == 0) q.sc[4 + w] = inverse_of(sx);
+                if (lane == 0) q.sc[8 + w] = inverse_of(sx);
             }
             q.meet();
             clear(y);  // E
@@ -591,48 +608,39 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 take<2>(a, q.mine + Sm::x(false) + kb * 1024, lane);
                 right<kChunk>(r[0], inv, 16 * w, 16 * kb, lane), right<kChunk>(r[1], inv + kSquare, 16 * w, 16 * kb, lane);
                 products<2, 2>(t[0], t[1], a, r);
-                add(y, t, q.sc[4 + kb] * f[F_INV]);
+                add(y, t, q.sc[8 + kb] * f[F_INV]);
             }
+            // All warps scale E and U for the same bounds, from X's and the inverse's largest, so that sums run over all rows
+            const float e_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
+            const float se = scale_for(e_most), u_most = e_most * f[F_BFMOST], su = scale_for(u_most);
             {
-                const float se = warp_scale(y);
-                uint32_t a[NO][4];
+                uint32_t a[NO][4], c[2][4];
                 left_of<NO>(a, y[0], y[1], se);
                 give<NO>(q.mine + Sm::e + w * Sm::e_block, a, lane);
                 if (rec) leave<NO>(rec + SR::e + w * 512, kRowsTerm, a, lane);
-                by_columns(y, f + F_BETA + 16 * w, 1.0f, lane);
-                by_columns(y, f + F_REST + 16 * w, 1.0f, lane);
-                const float su = warp_scale(y);
-                uint32_t c[2][4];
+                by_columns(y, f + F_BF + 16 * w, 1.0f, lane);
                 left_of<2>(c, y[0], y[1], su);
                 give<2>(q.mine + Sm::u + w * 1024, c, lane);
-                if (lane == 0) {
-                    q.sc[8 + w] = inverse_of(se), q.sc[12 + w] = inverse_of(su);
-                    if (rec) reinterpret_cast<float *>(rec + SR::fwd_scales)[4 + w] = inverse_of(se);
-                }
+                if (rec && lane == 0) reinterpret_cast<float *>(rec + SR::fwd_scales)[4 + w] = inverse_of(se);
             }
             q.meet();
+            clear(x);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
                 if (kb > w) continue;
-                Acc t[2];
-                clear(t);
                 uint32_t a[NO][4], r[NO][4];
                 take<NO>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
 #pragma unroll
                 for (int j = 0; j < NO; ++j) right<kChunk>(r[j], pimg + j * kSquare, 16 * w, 16 * kb, lane);
-                products<NO, NO>(t[0], t[1], a, r);
-                add(z, t, q.sc[8 + kb] * f[F_P]);
+                products<NO, NO>(x[0], x[1], a, r);
             }
+            add(z, x, inverse_of(se) * f[F_P]);
             // S = whole S0 + K^T U, this warp's quarter
-            const float whole = f[F_WHOLE], ik = f[F_K];
-#pragma unroll
-            for (int j = 0; j < 2 * kSteps; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] *= whole;
+            const float whole = f[F_WHOLE], ik = f[F_K], iu = inverse_of(su) * ik;
+            Acc t[2 * kSteps];
+            clear(t);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
-                Acc t[2 * kSteps];
-                clear(t);
                 uint32_t a[2][4];
                 take<2>(a, q.mine + Sm::u + kb * 1024, lane);
 #pragma unroll
@@ -642,11 +650,14 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
                     products<2, NI>(t[2 * i], t[2 * i + 1], a, r);
                 }
-                add(s, t, q.sc[12 + kb] * ik);
             }
+#pragma unroll
+            for (int j = 0; j < 2 * kSteps; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] = fmaf(t[j][e], iu, s[j][e] * whole);
             if (n + 1 < count) {
                 uint8_t *const next = record(n + 1);
-                q.hand_over(s, next, reinterpret_cast<float *>(next + SR::fwd_scales));
+                q.hand_over(s, fmaf(before, whole, 64.0f * (kTop * ik) * u_most), next, reinterpret_cast<float *>(next + SR::fwd_scales));
             }
             if (t0 < p.T) {
                 write_tile<T>(tile, z, lane);
@@ -691,7 +702,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
         __syncthreads();
         if (count > 0) {
             fetch(count - 1);
-            if (cols > 0) q.hand_over(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
+            if (cols > 0) q.begin(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
         }
         for (int n = count - 1; n >= 0; --n) {
             copies_wait<0>();
@@ -712,30 +723,19 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 left_of<NI>(a, y[0], y[1], so);
                 give<NI>(q.mine + Sm::e + w * Sm::e_block, a, lane);
                 leave<NI>(rec + SR::dout + w * 512, kRowsTerm, a, lane);
-                by_columns(y, f + F_GROW + 16 * w, p.scale, lane);
-                const float su = warp_scale(y);
-                uint32_t c[2][4];
-                left_of<2>(c, y[0], y[1], su);
-                give<2>(q.mine + Sm::u + w * 1024, c, lane);
-                if (lane == 0) q.sc[8 + w] = inverse_of(so), q.sc[12 + w] = inverse_of(su), rec_scales[8 + w] = inverse_of(so);
+                if (lane == 0) q.sc[12 + w] = inverse_of(so), rec_scales[8 + w] = inverse_of(so);
             }
             clear(x);  // dU
+            const float is = q.sc[4], behind = q.state_most();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                Acc t[2];
-                clear(t);
+            for (int kk = 0; kk < KP / 16; ++kk) {
+                uint32_t a[2][4], r[NI][4];
+                take<2>(a, q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int kk = c * kSteps + i;
-                    uint32_t a[2][4], r[NI][4];
-                    take<2>(a, q.mine + Sm::state + kk * 1024, lane);
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                    products<2, NI>(t[0], t[1], a, r);
-                }
-                add(x, t, q.sc[c]);
+                for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
+                products<2, NI>(x[0], x[1], a, r);
             }
-            by_columns(x, f + F_REST + 16 * w, f[F_K], lane);
+            by_columns(x, f + F_REST + 16 * w, f[F_K] * is, lane);
             q.meet();
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
@@ -746,14 +746,22 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 take<NI>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
                 right_t<kChunk>(r[0], pimg, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], pimg + kSquare, 16 * kb, 16 * w, lane);
                 products<NI, 2>(t[0], t[1], a, r);
-                add(x, t, q.sc[8 + kb] * f[F_P]);
+                add(x, t, q.sc[12 + kb] * f[F_P]);
             }
             {
                 const float sx = warp_scale(x);
                 uint32_t a[2][4];
                 left_of<2>(a, x[0], x[1], sx);
                 give<2>(q.mine + Sm::x(true) + w * 1024, a, lane);
-                if (lane == 0) q.sc[4 + w] = inverse_of(sx);
+                if (lane == 0) q.sc[8 + w] = inverse_of(sx);
+            }
+            // scale grow dO, all warps for the same bound
+            const float u_most = kTop * fmaxf(fmaxf(q.sc[12], q.sc[13]), fmaxf(q.sc[14], q.sc[15])) * f[F_GROWMOST] * fabsf(p.scale), su = scale_for(u_most);
+            {
+                uint32_t c[2][4];
+                by_columns(y, f + F_GROW + 16 * w, p.scale, lane);
+                left_of<2>(c, y[0], y[1], su);
+                give<2>(q.mine + Sm::u + w * 1024, c, lane);
             }
             q.meet();
             clear(y);  // dR
@@ -766,35 +774,32 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 take<2>(a, q.mine + Sm::x(true) + kb * 1024, lane);
                 right_t<kChunk>(r[0], inv, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], inv + kSquare, 16 * kb, 16 * w, lane);
                 products<2, 2>(t[0], t[1], a, r);
-                add(y, t, q.sc[4 + kb] * f[F_INV]);
+                add(y, t, q.sc[8 + kb] * f[F_INV]);
             }
+            // beta grow dR likewise, from dU's and the inverse's largest
+            const float r_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
+            const float sr = scale_for(r_most), w_most = r_most * f[F_BFMOST], sw = scale_for(w_most);
             {
-                const float sr = warp_scale(y);
                 uint32_t a[NO][4];
                 left_of<NO>(a, y[0], y[1], sr);
                 leave<NO>(rec + SR::dr + w * 512, kRowsTerm, a, lane);
-                by_columns(y, f + F_BETA + 16 * w, 1.0f, lane);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = y[i][e];  // dV
-                by_columns(y, f + F_GROW + 16 * w, -1.0f, lane);
-                const float sw = warp_scale(y);
+                    for (int e = 0; e < 4; ++e) x[i][e] = y[i][e];
+                by_columns(x, f + F_BETA + 16 * w, 1.0f, lane);  // dV
+                by_columns(y, f + F_BF + 16 * w, -1.0f, lane);
                 uint32_t c[2][4];
                 left_of<2>(c, y[0], y[1], sw);
                 give<2>(q.mine + Sm::w + w * 1024, c, lane);
-                if (lane == 0) q.sc[16 + w] = inverse_of(sw), rec_scales[4 + w] = inverse_of(sr);
+                if (lane == 0) rec_scales[4 + w] = inverse_of(sr);
             }
             q.meet();
-            const float whole = f[F_WHOLE], ik = f[F_K], iq = f[F_Q];
-#pragma unroll
-            for (int j = 0; j < 2 * kSteps; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[j][e] *= whole;
+            const float whole = f[F_WHOLE], ik = f[F_K], iq = f[F_Q], iu = inverse_of(su) * iq, iw = inverse_of(sw) * ik;
+            Acc t[2 * kSteps], u[2 * kSteps];
+            clear(t), clear(u);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {
-                Acc t[2 * kSteps], u[2 * kSteps];
-                clear(t), clear(u);
                 uint32_t a[2][4], c[2][4];
                 take<2>(a, q.mine + Sm::u + kb * 1024, lane), take<2>(c, q.mine + Sm::w + kb * 1024, lane);
 #pragma unroll
@@ -807,9 +812,14 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
                     products<2, NI>(u[2 * i], u[2 * i + 1], c, r);
                 }
-                add(g, t, q.sc[12 + kb] * iq), add(g, u, q.sc[16 + kb] * ik);
             }
-            if (n > 0) q.hand_over(g, record(n - 1), reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
+#pragma unroll
+            for (int j = 0; j < 2 * kSteps; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[j][e] = fmaf(t[j][e], iu, fmaf(u[j][e], iw, g[j][e] * whole));
+            if (n > 0)
+                q.hand_over(g, fmaf(behind, whole, 64.0f * ((kTop * iq) * u_most + (kTop * ik) * w_most)), record(n - 1),
+                            reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
             if (t0 < p.T) {
                 write_tile<T>(tile, x, lane);
                 __syncwarp();
@@ -883,8 +893,7 @@ __device__ __forceinline__ uint32_t halves(int e) {
     return h | h << 16;
 }
 template <int TERMS>
-__device__ __forceinline__ void times(uint32_t (&to)[TERMS][4], const uint32_t (&a)[TERMS][4], int e) {
-    const uint32_t f = halves(e);
+__device__ __forceinline__ void times(uint32_t (&to)[TERMS][4], const uint32_t (&a)[TERMS][4], uint32_t f) {
 #pragma unroll
     for (int j = 0; j < TERMS; ++j)
 #pragma unroll
@@ -901,6 +910,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp & 3, wn = warp >> 2;
     const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK, slices = (p.V + kSlice - 1) / kSlice;
     const int r0 = 16 * wm + (lane >> 2), r1 = r0 + 8, col0 = wn * (KP / 4) + 2 * (lane & 3);  // this thread's accumulators
+    const bool traces = warp < KP / 8;
+    const int trace = traces ? warp >> 1 : 0, half = warp & 1;
     float *const f = reinterpret_cast<float *>(smem + Sm::f);
     float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 4 * kChunk,
                 *const part_col = part_next + 4 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
@@ -941,26 +952,41 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
 #pragma unroll
             for (int i = 0; i < Sm::stages - 1; ++i) fetch(i);
-            // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, dO E, dR E
-            int top[5] = {-1000, -1000, -1000, -1000, -1000};
+            // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, dO E, dR E, S0 G
+            int top[6] = {-1000, -1000, -1000, -1000, -1000, -1000};
+            const auto exponents = [&](int (&x)[6], int sl) {
+                const float *const a = reinterpret_cast<const float *>(fwd + static_cast<int64_t>(sl) * SR::fwd + SR::fwd_scales),
+                                   *const c = reinterpret_cast<const float *>(bwd + static_cast<int64_t>(sl) * SR::bwd + SR::bwd_scales);
+                const int s = exponent(a[wn]), em = exponent(a[4 + wm]), en = exponent(a[4 + wn]), g = exponent(c[wn]), r = exponent(c[4 + wm]), o = exponent(c[8 + wm]);
+                x[0] = o + s, x[1] = r + s, x[2] = em + g, x[3] = o + en, x[4] = r + en;
+                x[5] = exponent(a[trace / NQ]) + exponent(c[trace / NQ]);
+            };
+            uint32_t by[6];  // lane i: the factors of slice i (of 32)
             for (int sl = lane; sl < slices; sl += 32) {
-                const float *const x = reinterpret_cast<const float *>(fwd + static_cast<int64_t>(sl) * SR::fwd + SR::fwd_scales),
-                                   *const y = reinterpret_cast<const float *>(bwd + static_cast<int64_t>(sl) * SR::bwd + SR::bwd_scales);
-                const int s = exponent(x[wn]), em = exponent(x[4 + wm]), en = exponent(x[4 + wn]), g = exponent(y[wn]), r = exponent(y[4 + wm]), o = exponent(y[8 + wm]);
-                top[0] = max(top[0], o + s), top[1] = max(top[1], r + s), top[2] = max(top[2], em + g), top[3] = max(top[3], o + en), top[4] = max(top[4], r + en);
+                int x[6];
+                exponents(x, sl);
+#pragma unroll
+                for (int i = 0; i < 6; ++i) top[i] = max(top[i], x[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 5; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+            for (int i = 0; i < 6; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
             Acc aos[2 * NQ], ars[2 * NQ], aeg[2 * NQ], dp[2], da[2];
-            clear(aos), clear(ars), clear(aeg), clear(dp), clear(da);
-            float dot = 0.0f;
+            Acc diagonal[1];
+            clear(aos), clear(ars), clear(aeg), clear(dp), clear(da), clear(diagonal);
             for (int sl = 0; sl < slices; ++sl) {
                 copies_wait<Sm::stages - 2>();
                 __syncthreads();  // the slice is there, and the one whose place comes next is done with
                 fetch(sl + Sm::stages - 1);
                 const uint8_t *const x = smem + Sm::ring + sl % Sm::stages * Sm::stage, *const y = x + SR::fwd;
-                const float *const xs = reinterpret_cast<const float *>(x + SR::fwd_scales), *const ys = reinterpret_cast<const float *>(y + SR::bwd_scales);
-                const int s = exponent(xs[wn]), em = exponent(xs[4 + wm]), en = exponent(xs[4 + wn]), g = exponent(ys[wn]), r = exponent(ys[4 + wm]), o = exponent(ys[8 + wm]);
+                if (sl % 32 == 0) {
+                    int e[6] = {};
+                    if (sl + lane < slices) exponents(e, sl + lane);
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) by[i] = halves(e[i] - top[i]);
+                }
+                uint32_t factor[6];
+#pragma unroll
+                for (int i = 0; i < 6; ++i) factor[i] = __shfl_sync(0xffffffffu, by[i], sl % 32);
                 const uint32_t xa = smem_u32(x), ya = smem_u32(y);
                 uint32_t lo[NI][4], lr[NO][4], le[NO][4], c[NO][4], d[NI][4], v[NO][4];
 #pragma unroll
@@ -970,12 +996,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 if (wn <= wm) {
 #pragma unroll
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + wn * 512, lane);
-                    times<NI>(d, lo, o + en - top[3]);
+                    times<NI>(d, lo, factor[3]);
                     products<NI, NO>(dp[0], dp[1], d, v);
-                    times<NO>(c, lr, r + en - top[4]);
+                    times<NO>(c, lr, factor[4]);
                     products<NO, NO>(da[0], da[1], c, v);
                 }
-                times<NI>(d, lo, o + s - top[0]), times<NO>(c, lr, r + s - top[1]), times<NO>(le, le, em + g - top[2]);
+                times<NI>(d, lo, factor[0]), times<NO>(c, lr, factor[1]), times<NO>(le, le, factor[2]);
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
 #pragma unroll
@@ -986,26 +1012,22 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], ya + j * SR::state_term + (wn * NQ + i) * 512, lane);
                     products<NO, NO>(aeg[2 * i], aeg[2 * i + 1], le, v);
                 }
-                // <S0, G>: words of eight elements
-                for (int i = tid; i < SR::state_term / 16; i += kThreads) {
-                    const int quarter = i / (SR::state_term / 64);
-                    float sum = 0.0f;
-                    float a[8] = {}, e[8] = {};
+                // <S0, G>: the diagonal of S0^T G, a block of eight channels to a warp
+                if (traces) {
 #pragma unroll
-                    for (int j = 0; j < NO; ++j) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(x + j * SR::state_term + i * 16), z = *reinterpret_cast<const uint4 *>(y + j * SR::state_term + i * 16);
-                        const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, zw[4] = {z.x, z.y, z.z, z.w};
+                    for (int j = 0; j < NO; ++j) left_blocks(c[j], xa + j * SR::state_term + trace * 512, lane), right_blocks(v[j], ya + j * SR::state_term + trace * 512, lane);
+                    times<NO>(c, c, factor[5]);
 #pragma unroll
-                        for (int l = 0; l < 4; ++l) {
-                            const Vec<2> h = unpack<__half>(uw[l]), k = unpack<__half>(zw[l]);
-                            a[2 * l] += h.v[0], a[2 * l + 1] += h.v[1], e[2 * l] += k.v[0], e[2 * l + 1] += k.v[1];
-                        }
-                    }
+                    for (int j = 0; j < NO; ++j)
 #pragma unroll
-                    for (int l = 0; l < 8; ++l) sum = fmaf(a[l], e[l], sum);
-                    dot = fmaf(sum * xs[quarter], ys[quarter], dot);
+                        for (int i = 0; i + j < NO; ++i) mma(diagonal[0], c[i], half ? v[j][2] : v[j][0], half ? v[j][3] : v[j][1]);
                 }
             }
+            float dot = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (traces && 2 * (lane & 3) + e == lane >> 2) dot += half ? diagonal[0][2 + e] : diagonal[0][e];
+            dot = ldexpf(dot, top[5]);
             // rows' and columns' factors, and the rows' products with queries and keys
             const float ik = f[F_K], iq = f[F_Q], c0 = f[F_GROW + r0], c1 = f[F_GROW + r1], b0 = f[F_BETA + r0], b1 = f[F_BETA + r1];
             float row0 = 0.0f, row1 = 0.0f, next0 = 0.0f, next1 = 0.0f;

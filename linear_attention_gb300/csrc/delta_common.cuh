@@ -54,9 +54,10 @@ struct Terms<float> {
 //   of a key head: the scaled keys and queries, TERMS x 64 x KP float16 each
 //   of a value head: the inverse (two terms), the masked scores (forward: Terms::out, times beta of their columns; backward: two),
 //   64 x 64 float16 each, and float32 numbers: per row grow = exp(b), rest = exp(b_last - b), beta, b in two parts (b: the
-//   sum of log decays up to the row), then the scales' inverses.
+//   sum of log decays up to the row), beta rest (backward: beta grow), then the scales' inverses, the largest |beta rest| (backward: |beta
+//   grow|) and the largest grow.
 constexpr int kSquare = kChunk * kChunk * 2;  // bytes
-enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_INV = 320, F_P, F_WHOLE, F_K, F_Q, F_COUNT = 336 };
+enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_BF = 320, F_INV = 384, F_P, F_WHOLE, F_K, F_Q, F_BFMOST, F_GROWMOST, F_COUNT = 400 };
 template <typename T, int KP>
 struct Rec {
     static constexpr int term = kChunk * KP * 2, img = Terms<T>::in * term, qk = 2 * img;
@@ -165,6 +166,7 @@ __device__ __forceinline__ float scale_for(float most) {
     e = e < 27 ? 27 : e > 187 ? 187 : e;
     return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
+constexpr float kTop = 8192.0f;  // what scaled magnitudes stay below: |x| < kTop * inverse
 __device__ __forceinline__ float inverse_of(float pow2) { return __uint_as_float((254u << 23) - __float_as_uint(pow2)); }
 
 __device__ __forceinline__ uint32_t half2_of(float x, float y) { return pack<__half>(Vec<2>{{x, y}}); }
