@@ -34,26 +34,30 @@ template <bool WORDS>
 __device__ __forceinline__ int channel(int t, int threads, int j, int e) {
     return WORDS ? (t + threads * j) * kPack + e : t + threads * (j * kPack + e);
 }
+// A pack as it lies in memory: the loads of several packs go out together, the conversion comes after
 template <bool WORDS, typename T>
-__device__ __forceinline__ void load_pack(float (&x)[kPack], const T *p, int t, int threads, int j, int C) {
-    if constexpr (WORDS) {
-        const int c = channel<true>(t, threads, j, 0);
-        if (c < C) {
-            const Pack<T, kPack> w = *reinterpret_cast<const Pack<T, kPack> *>(p + c);
+struct Raw {
+    Pack<T, kPack> p;
+    __device__ __forceinline__ void load(const T *from, int t, int threads, int j, int C) {
+        if constexpr (WORDS) {
+            const int c = channel<true>(t, threads, j, 0);
+            uint4 *const w = reinterpret_cast<uint4 *>(&p);
 #pragma unroll
-            for (int e = 0; e < kPack; ++e) x[e] = to_f32(w.v[e]);
-            return;
-        }
+            for (int i = 0; i < static_cast<int>(sizeof(p)) / 16; ++i) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (c < C) w[i] = __ldcs(reinterpret_cast<const uint4 *>(from + c) + i);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < kPack; ++e) x[e] = 0.0f;
-    } else {
-#pragma unroll
-        for (int e = 0; e < kPack; ++e) {
-            const int c = channel<false>(t, threads, j, e);
-            x[e] = c < C ? to_f32(p[c]) : 0.0f;
+            for (int e = 0; e < kPack; ++e) {
+                const int c = channel<false>(t, threads, j, e);
+                p.v[e] = from_f32<T>(0.0f);
+                if (c < C) p.v[e] = from[c];
+            }
         }
     }
-}
+    __device__ __forceinline__ float operator[](int e) const { return to_f32(p.v[e]); }
+};
 template <bool WORDS, typename T>
 __device__ __forceinline__ void store_pack(T *p, const float (&x)[kPack], int t, int threads, int j, int C) {
     if constexpr (WORDS) {
@@ -95,14 +99,14 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&x)[kPack], 
 }
 template <typename T, bool WORDS>
 __device__ __forceinline__ void load_weight(float (&w)[kPack], const RmsParams &p, int t, int threads, int j) {
-    if (!p.weight) {
+    Raw<WORDS, T> a;
+    Raw<WORDS, float> b;
+    if (p.weight && p.p_dtype == BASED_F32)
+        b.load(static_cast<const float *>(p.weight), t, threads, j, p.C);
+    else if (p.weight)
+        a.load(static_cast<const T *>(p.weight), t, threads, j, p.C);
 #pragma unroll
-        for (int e = 0; e < kPack; ++e) w[e] = channel<WORDS>(t, threads, j, e) < p.C ? 1.0f : 0.0f;
-    } else if (p.p_dtype == BASED_F32) {
-        load_pack<WORDS>(w, static_cast<const float *>(p.weight), t, threads, j, p.C);
-    } else {
-        load_pack<WORDS>(w, static_cast<const T *>(p.weight), t, threads, j, p.C);
-    }
+    for (int e = 0; e < kPack; ++e) w[e] = !p.weight ? 1.0f : p.p_dtype == BASED_F32 ? b[e] : a[e];
 }
 
 // The sum or the largest of v over the THREADS threads of a row; red: 32 floats of the CTA, two rows of them used in turn
@@ -126,12 +130,30 @@ __device__ __forceinline__ float over_row(float v, float *red, int &turn) {
     return v;
 }
 
+// Two sums at once
+template <int THREADS>
+__device__ __forceinline__ void over_row2(float &a, float &b, float *red, int &turn) {
+    constexpr int kLanes = THREADS < 32 ? THREADS : 32, kWarps = THREADS / 32;
+#pragma unroll
+    for (int d = 1; d < kLanes; d *= 2) a += __shfl_xor_sync(0xffffffffu, a, d), b += __shfl_xor_sync(0xffffffffu, b, d);
+    if constexpr (kWarps > 1) {
+        float2 *const at = reinterpret_cast<float2 *>(red) + turn * 16 + threadIdx.x / THREADS * kWarps;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) at[threadIdx.x % THREADS / 32] = make_float2(a, b);
+        __syncthreads();
+        float2 v = at[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) v.x += at[i].x, v.y += at[i].y;
+        a = v.x, b = v.y;
+    }
+}
+
 __host__ __device__ constexpr int cta_of(int threads) { return threads < 256 ? 256 : threads; }
 
 template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
 __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParams p) {
     constexpr int kRows = cta_of(THREADS) / THREADS;
-    __shared__ float red[64];
+    __shared__ __align__(8) float red[64];
     int turn = 0;
     const int t = threadIdx.x % THREADS, slot = threadIdx.x / THREADS;
     griddep_wait();
@@ -145,16 +167,24 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
         const bool there = row < p.R;
         const int C = there ? p.C : 0;
         float s[PACKS][kPack], sq = 0.0f;
+        Raw<WORDS, T> x[PACKS];
 #pragma unroll
-        for (int j = 0; j < PACKS; ++j) load_pack<WORDS>(s[j], static_cast<const T *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+        for (int j = 0; j < PACKS; ++j) x[j].load(static_cast<const T *>(p.x) + row * p.x_sr, t, THREADS, j, C);
         if (p.residual) {
+            Raw<WORDS, S> r[PACKS];
 #pragma unroll
-            for (int j = 0; j < PACKS; ++j) {
-                float r[kPack];
-                load_pack<WORDS>(r, static_cast<const S *>(p.residual) + row * p.res_sr, t, THREADS, j, C);
+            for (int j = 0; j < PACKS; ++j) r[j].load(static_cast<const S *>(p.residual) + row * p.res_sr, t, THREADS, j, C);
 #pragma unroll
-                for (int e = 0; e < kPack; ++e) s[j][e] = to_f32(from_f32<S>(s[j][e] + r[e]));  // what is written is what is normed
-            }
+            for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+                for (int e = 0; e < kPack; ++e) s[j][e] = to_f32(from_f32<S>(x[j][e] + r[j][e]));  // what is written is what is normed
+        } else {
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j)
+#pragma unroll
+                for (int e = 0; e < kPack; ++e) s[j][e] = x[j][e];
+        }
+        if (p.residual) {
 #pragma unroll
             for (int j = 0; j < PACKS; ++j) store_pack<WORDS>(static_cast<S *>(p.sum) + row * p.C, s[j], t, THREADS, j, C);
         }
@@ -191,7 +221,7 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
 template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
 __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParams p) {
     constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
-    __shared__ float red[64];
+    __shared__ __align__(8) float red[64];
     extern __shared__ float sums[];  // rows' threads' sums of the weights' gradient, where a CTA takes several rows
     int turn = 0;
     const int t = threadIdx.x % THREADS, slot = threadIdx.x / THREADS;
@@ -203,33 +233,32 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParam
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.R; first += static_cast<int64_t>(gridDim.x) * kRows) {
         const int64_t row = first + slot;
         const int C = row < p.R ? p.C : 0;
-        float s[PACKS][kPack], d[PACKS][kPack], sq = 0.0f, ds = 0.0f;
+        Raw<WORDS, S> s[PACKS], g[PACKS];
+        Raw<WORDS, T> d[PACKS];
+        float sq = 0.0f, ds = 0.0f;
 #pragma unroll
         for (int j = 0; j < PACKS; ++j) {
-            load_pack<WORDS>(s[j], static_cast<const S *>(p.x) + row * p.x_sr, t, THREADS, j, C);
-            load_pack<WORDS>(d[j], static_cast<const T *>(p.dy) + row * p.dy_sr, t, THREADS, j, C);
+            s[j].load(static_cast<const S *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+            d[j].load(static_cast<const T *>(p.dy) + row * p.dy_sr, t, THREADS, j, C);
         }
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) g[j].load(static_cast<const S *>(p.dsum) + row * p.dsum_sr, t, THREADS, j, p.dsum ? C : 0);
 #pragma unroll
         for (int j = 0; j < PACKS; ++j)
 #pragma unroll
             for (int e = 0; e < kPack; ++e) sq = fmaf(s[j][e], s[j][e], sq), ds = fmaf(d[j][e] * w[j][e], s[j][e], ds);
-        const float r = rsqrtf(over_row<THREADS, false>(sq, red, turn) * mean + p.eps);
-        const float back = over_row<THREADS, false>(ds, red, turn) * mean * r * r;  // mean(d s) r^2
+        over_row2<THREADS>(sq, ds, red, turn);
+        const float r = rsqrtf(sq * mean + p.eps), back = ds * mean * r * r;  // mean(d s) r^2
 #pragma unroll
         for (int j = 0; j < PACKS; ++j) {
-            float g[kPack];
-            if (p.dsum)
-                load_pack<WORDS>(g, static_cast<const S *>(p.dsum) + row * p.dsum_sr, t, THREADS, j, C);
-            else
-#pragma unroll
-                for (int e = 0; e < kPack; ++e) g[e] = 0.0f;
+            float x[kPack];
 #pragma unroll
             for (int e = 0; e < kPack; ++e) {
                 dw[j][e] = fmaf(d[j][e], s[j][e] * r, dw[j][e]);
-                g[e] += r * (d[j][e] * w[j][e] - s[j][e] * back);
+                x[e] = fmaf(r, d[j][e] * w[j][e] - s[j][e] * back, g[j][e]);
             }
-            store_pack<WORDS>(static_cast<S *>(p.ds) + row * p.C, g, t, THREADS, j, C);
-            if constexpr (!std::is_same<T, S>::value) store_pack<WORDS>(static_cast<T *>(p.dx) + row * p.C, g, t, THREADS, j, C);
+            store_pack<WORDS>(static_cast<S *>(p.ds) + row * p.C, x, t, THREADS, j, C);
+            if constexpr (!std::is_same<T, S>::value) store_pack<WORDS>(static_cast<T *>(p.dx) + row * p.C, x, t, THREADS, j, C);
         }
     }
     if (!p.dweight) return;

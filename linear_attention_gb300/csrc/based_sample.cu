@@ -1,18 +1,19 @@
 // based_sample.cu: the choice of a next token (declared in include/based_ops.h).
 //
 // With w_i = exp((x_i - max) / temperature), each of top-k, top-p and min-p keeps a prefix of the tokens in the order of falling
-// logits (equal ones by rising index), so what is kept is one comparison with a cut: the order itself is never needed. A row lies
-// in the shared memory of a cluster. One pass over it counts tokens and masses in 2048 bins of x's distance from the largest; the cut's bin
-// follows from the bins' sums and the cut from the few tokens of that bin. A last pass sums the kept masses by warps, and the warp in which
-// the random number falls finds the token. Masses are whole numbers, w 2^40 in 64 bits: their sums do not depend on an order, so
-// the same call gives the same token. Bound by reading the logits once, for few rows by the barriers between the passes.
+// logits (equal ones by rising index), so what is kept is one comparison with a cut: the whole order is never needed. A row lies in the
+// shared memory of a cluster. One pass over it counts tokens (or sums masses) in 2048 bins of x's distance from the largest; the bin of the cut follows
+// from the bins' sums, and the cut from the tokens of that bin, or of all bins up to it, which one CTA sorts. A last pass sums the kept masses by
+// warps, and the warp in which the random number falls finds the token. Masses are whole numbers, w 2^40 in 64 bits: their sums
+// do not depend on an order, so the same call gives the same token. Bound by the passes' instructions where there are many rows, by the
+// barriers between them where there are few.
 #include "ops_common.cuh"
 
 namespace based {
 namespace {
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
-constexpr int kBins = 2048, kFew = 1024;  // bins; tokens of one bin that are compared with one another
+constexpr int kBins = 2048, kFew = 2048;  // bins; tokens that one CTA sorts
 constexpr float kReach = 46.0f;           // the last bin begins at w = 2^-46
 constexpr float kMass = 1099511627776.0f; // 2^40
 constexpr int kSampleCluster = 16;
@@ -34,15 +35,13 @@ struct SampleParams {
 using u64 = unsigned long long;
 
 struct SampleShared {
-    u64 mass[kBins];
-    uint32_t count[kBins];
-    u64 few_at[kFew], few_mass[kFew];
-    u64 slots[2][3];        // what this CTA hands to the others, two sets in turn
-    u64 warp[3][kSampleWarps];
-    u64 found[3];
-    uint32_t few;
+    u64 bins[kBins];
+    u64 place[kFew], mass[kFew];  // the tokens to sort
+    u64 slots[2][4];              // what this CTA hands to the others, two sets in turn
+    u64 warp[4][kSampleWarps];
+    u64 found[4];
+    uint32_t few, pad[3];
 };
-
 static_assert(sizeof(SampleShared) % 16 == 0, "the tokens lie behind it");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -63,11 +62,6 @@ __device__ __forceinline__ uint32_t peer(P *p, uint32_t rank) {
 __device__ __forceinline__ u64 peer_load(uint32_t at) {
     u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t peer_load32(uint32_t at) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ void peer_store(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
@@ -175,102 +169,172 @@ struct Weigh {
     }
 };
 
-// The place of the last token that is kept: with `by_mass` the first in the order at which the masses reach `target`, otherwise the
-// target'th. kept: the mass up to it. The bins' sums are there, merged: `count` and `mass` of the CTA's own part.
+// Prefix sums over the CTA, in the order of threads; all: the sum
+__device__ __forceinline__ u64 cta_prefix(u64 v, u64 *by_warp, u64 &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 up = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const u64 o = __shfl_up_sync(0xffffffffu, up, d);
+        if (lane >= d) up += o;
+    }
+    if (lane == 31) by_warp[warp] = up;
+    __syncthreads();
+    u64 before = up - v;
+    all = 0;
+    for (int w = 0; w < kSampleWarps; ++w) {
+        const u64 o = by_warp[w];
+        if (w < warp) before += o;
+        all += o;
+    }
+    __syncthreads();
+    return before;
+}
+// The tokens to sort, into falling places
+__device__ __forceinline__ void sort_few(SampleShared &sh, int n) {
+    int size = 2;
+    while (size < n) size *= 2;
+    for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sh.place[i] = sh.mass[i] = 0;
+    for (int k = 2; k <= size; k *= 2)
+        for (int d = k / 2; d > 0; d /= 2) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < size / 2; i += kSampleThreads) {
+                const int a = 2 * i - (i & (d - 1)), b = a + d;
+                const u64 x = sh.place[a], y = sh.place[b];
+                if (((a & k) == 0) == (x < y)) {
+                    const u64 m = sh.mass[a];
+                    sh.place[a] = y, sh.place[b] = x, sh.mass[a] = sh.mass[b], sh.mass[b] = m;
+                }
+            }
+        }
+    __syncthreads();
+}
+
+// Moves the cut up: by count to the k'th token of those at or above it and, where `share` is below 1 and all of them could be sorted, on to the first
+// at which the masses reach that share of theirs (returns true); by mass (k is 0) to the latter.
 template <typename T>
-__device__ u64 find_cut(Sampler<T> &s, const Weigh &w, bool by_mass, double target, u64 &kept) {
+__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64 &cut) {
     SampleShared &sh = s.sh;
     const SampleParams &p = s.p;
-    // the bin: a CTA looks through its part, kBins / cluster bins, by warp 0
-    const int part = kBins / p.cluster;
-    u64 sums[2] = {0, 0}, before[2];
-    for (int i = s.tid; i < part; i += kSampleThreads) sums[0] += sh.count[s.rank * part + i], sums[1] += sh.mass[s.rank * part + i];
-    s.template total<2>(sums, before);
-    if (s.tid == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
-    __syncthreads();
-    if (s.warp == 0) {
-        u64 c = before[0], m = before[1];
-        for (int i0 = 0; i0 < part; i0 += 32) {
-            const int i = i0 + s.lane, at = s.rank * part + i;
-            const u64 ci = i < part ? sh.count[at] : 0, mi = i < part ? sh.mass[at] : 0;
-            u64 cs = ci, ms = mi;
+    const bool by_mass = k == 0;
+    u64 last = 0;  // the last bin's tokens, which may be most, without atomics
+    s.each([&](float x, int i) {
+        if (x == -INFINITY || place_of(x, s.first + i) < cut) return;
+        const int bin = w.bin(x);
+        const u64 v = by_mass ? w.mass(x) : 1;
+        if (bin == kBins - 1)
+            last += v;
+        else if (v)
+            atomicAdd(&sh.bins[bin], v);
+    });
+    last = over_warp<false>(last);
+    if (s.lane == 0 && last) atomicAdd(&sh.bins[kBins - 1], last);
+    s.meet();
+    // this CTA's part of the bins over all CTAs: up to four neighbouring bins a thread
+    constexpr int kMost = kBins / kSampleThreads;
+    const int part = kBins / p.cluster, per = part < kSampleThreads ? 1 : part / kSampleThreads, mine = threadIdx.x * per;
+    u64 v[kMost], sum = 0;
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const u64 a = __shfl_up_sync(0xffffffffu, cs, d), b = __shfl_up_sync(0xffffffffu, ms, d);
-                if (s.lane >= d) cs += a, ms += b;
-            }
-            const u64 c0 = c + cs - ci, m0 = m + ms - mi;
-            const bool here = by_mass ? static_cast<double>(m0) < target && static_cast<double>(m0 + mi) >= target
-                                      : static_cast<double>(c0) < target && static_cast<double>(c0 + ci) >= target;
-            if (here && i < part) sh.found[0] = at + 1, sh.found[1] = c0, sh.found[2] = m0;
-            c += __shfl_sync(0xffffffffu, cs, 31), m += __shfl_sync(0xffffffffu, ms, 31);
+    for (int j = 0; j < kMost; ++j) {
+        v[j] = 0;
+        if (j < per && mine + j < part) {
+            const int at = s.rank * part + mine + j;
+            if (p.cluster > 1)
+                for (int r = 0; r < p.cluster; ++r) v[j] += peer_load(peer(&sh.bins[at], r));
+            else
+                v[j] = sh.bins[at];
         }
+        sum += v[j];
+    }
+    u64 all[1], others[1], in_cta;
+    u64 before = cta_prefix(sum, sh.warp[3], in_cta);
+    all[0] = threadIdx.x == 0 ? in_cta : 0;
+    if (threadIdx.x == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
+    s.template total<1>(all, others);
+    before += others[0];
+    const double target = by_mass ? share * static_cast<double>(all[0]) : static_cast<double>(k);
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        if (static_cast<double>(before) < target && static_cast<double>(before + v[j]) >= target)
+            sh.found[0] = s.rank * part + mine + j + 1, sh.found[1] = before, sh.found[2] = before + v[j];
+        before += v[j];
     }
     __syncthreads();
     u64 at[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) at[i] = s.tid == 0 ? sh.found[i] : 0;
     s.template total<3>(at);
-    if (at[0] == 0) {  // fewer tokens than asked for
-        kept = sums[1];
-        return 0;
-    }
-    const int bin = static_cast<int>(at[0]) - 1;
-    // its tokens, in the first CTA
-    if (s.tid == 0) sh.few = 0;
-    s.meet();
+    // fewer tokens than k: all are kept, and sorted where they are few
+    const bool enough = at[0] != 0, whole = !by_mass && (enough ? at[2] : all[0]) <= kFew;
+    if (!enough && !whole) return false;
+    const int bin = enough ? static_cast<int>(at[0]) - 1 : kBins - 1, low = whole ? 0 : bin;
     s.each([&](float x, int i) {
-        if (x == -INFINITY || w.bin(x) != bin) return;
+        if (x == -INFINITY) return;
+        const u64 pl = place_of(x, s.first + i);
+        const int b = w.bin(x);
+        if (b > bin || b < low || pl < cut) return;
         const uint32_t n = p.cluster > 1 ? peer_add(peer(&sh.few, 0), 1) : atomicAdd(&sh.few, 1u);
         if (n >= kFew) return;
-        const u64 pl = place_of(x, s.first + i), m = w.mass(x);
+        const u64 m = w.mass(x);
         if (p.cluster > 1)
-            peer_store(peer(&sh.few_at[n], 0), pl), peer_store(peer(&sh.few_mass[n], 0), m);
+            peer_store(peer(&sh.place[n], 0), pl), peer_store(peer(&sh.mass[n], 0), m);
         else
-            sh.few_at[n] = pl, sh.few_mass[n] = m;
+            sh.place[n] = pl, sh.mass[n] = m;
     });
     s.meet();
-    u64 few[1] = {s.rank == 0 && s.tid == 0 ? sh.few : 0u};
-    s.template total<1>(few);
-    if (few[0] <= kFew) {
-        const int n = static_cast<int>(few[0]);
-        if (s.tid == 0) sh.found[0] = sh.found[1] = 0;
-        __syncthreads();
-        if (s.rank == 0) {
-            for (int i = s.tid; i < n; i += kSampleThreads) {
-                const u64 me = sh.few_at[i], mine = sh.few_mass[i];
-                u64 c = at[1], m = at[2];
-                for (int j = 0; j < n; ++j)
-                    if (sh.few_at[j] > me) ++c, m += sh.few_mass[j];
-                const bool here = by_mass ? static_cast<double>(m) < target && static_cast<double>(m + mine) >= target
-                                          : static_cast<double>(c + 1) == target;
-                if (here) sh.found[0] = me, sh.found[1] = m + mine;
+    if (s.tid == 0) sh.found[0] = sh.found[1] = 0;
+    const uint32_t few = s.rank == 0 ? sh.few : 0;
+    __syncthreads();
+    if (s.rank == 0) {
+        if (s.tid == 0) sh.few = 0, sh.found[1] = few > kFew;
+        const int n = static_cast<int>(few);
+        if (n > 0 && n <= kFew) {
+            sort_few(sh, n);
+            // the k'th of all, or what is behind the bins in front
+            const u64 base = whole ? 0 : at[1];
+            const int nth = by_mass || !enough ? n : static_cast<int>(static_cast<u64>(k) - base);
+            if (share < 1.0 && (by_mass || whole)) {
+                u64 m[kFew / kSampleThreads], sums = 0, up_to;
+#pragma unroll
+                for (int j = 0; j < kFew / kSampleThreads; ++j) {
+                    const int i = threadIdx.x * (kFew / kSampleThreads) + j;
+                    m[j] = i < nth ? sh.mass[i] : 0;
+                    sums += m[j];
+                }
+                u64 now = (by_mass ? base : 0) + cta_prefix(sums, sh.warp[3], up_to);
+                const double reach = by_mass ? target : share * static_cast<double>(up_to);
+#pragma unroll
+                for (int j = 0; j < kFew / kSampleThreads; ++j) {
+                    if (static_cast<double>(now) < reach && static_cast<double>(now + m[j]) >= reach)
+                        sh.found[0] = sh.place[threadIdx.x * (kFew / kSampleThreads) + j];
+                    now += m[j];
+                }
+            } else if (s.tid == 0) {
+                sh.found[0] = sh.place[nth - 1];
             }
         }
-        __syncthreads();
-        u64 cut[2] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0};
-        s.template total<2>(cut);
-        kept = cut[1];
-        return cut[0];
+    }
+    __syncthreads();
+    u64 result[2] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0};
+    s.template total<2>(result);
+    if (!result[1]) {
+        if (result[0] > cut) cut = result[0];
+        return whole;
     }
     // Many tokens lie close together (equal logits, a high temperature): the cut bit by bit, the largest place with enough at or above it
-    u64 cut = 0;
+    u64 found = 0;
     for (int bit = 63; bit >= 0; --bit) {
-        const u64 trial = cut | 1ull << bit;
-        u64 v[2] = {0, 0};
+        const u64 trial = found | 1ull << bit;
+        u64 c[1] = {0};
         s.each([&](float x, int i) {
-            if (x != -INFINITY && place_of(x, s.first + i) >= trial) ++v[0], v[1] += by_mass ? w.mass(x) : 0;
+            const u64 pl = place_of(x, s.first + i);
+            if (x != -INFINITY && pl >= trial && pl >= cut) c[0] += by_mass ? w.mass(x) : 1;
         });
-        s.template total<2>(v);
-        if (static_cast<double>(by_mass ? v[1] : v[0]) >= target) cut = trial;
+        s.template total<1>(c);
+        if (static_cast<double>(c[0]) >= target) found = trial;
     }
-    u64 v[1] = {0};
-    s.each([&](float x, int i) {
-        if (x != -INFINITY && place_of(x, s.first + i) >= cut) v[0] += w.mass(x);
-    });
-    s.template total<1>(v);
-    kept = v[0];
-    return cut;
+    if (found > cut) cut = found;
+    return false;
 }
 
 template <typename T>
@@ -284,6 +348,8 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     griddep_wait();
     const T *const src = static_cast<const T *>(p.logits) + n * p.stride + first;
     Sampler<T> s = {p, sh, p.resident ? tokens : src, first, len, rank};
+    for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.bins[i] = 0;
+    if (threadIdx.x == 0) sh.few = 0;
     u64 best[1] = {0};
     const auto look = [&](float x, int i) {
         const u64 pl = place_of(x, first + i);
@@ -340,59 +406,14 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     if (!(top_p < 1.0f)) top_p = 1.0f;
     if (top_p <= 0.0f) k = 1, top_p = 1.0f;
     u64 cut = 0;
-    if (k < p.V || top_p < 1.0f) {
-        for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.mass[i] = 0, sh.count[i] = 0;
-        __syncthreads();
-        u64 last_mass = 0, last_count = 0;  // the last bin's tokens, which may be most, without atomics
-        s.each([&](float x, int) {
-            if (x == -INFINITY) return;
-            const int bin = w.bin(x);
-            const u64 m = w.mass(x);
-            if (bin == kBins - 1) {
-                last_mass += m, ++last_count;
-            } else {
-                atomicAdd(&sh.count[bin], 1u);
-                atomicAdd(&sh.mass[bin], m);
-            }
-        });
-        last_mass = over_warp<false>(last_mass), last_count = over_warp<false>(last_count);
-        if (s.lane == 0 && last_count) atomicAdd(&sh.count[kBins - 1], static_cast<uint32_t>(last_count)), atomicAdd(&sh.mass[kBins - 1], last_mass);
-        s.meet();
-        if (p.cluster > 1) {  // this CTA's part of the bins over all CTAs, in registers until all have read
-            const int part = kBins / p.cluster;
-            u64 m[kBins / kSampleThreads];
-            uint32_t c[kBins / kSampleThreads];
-#pragma unroll
-            for (int j = 0; j < kBins / kSampleThreads; ++j) {
-                const int i = threadIdx.x + j * kSampleThreads;
-                m[j] = c[j] = 0;
-                if (i < part)
-                    for (int r = 0; r < p.cluster; ++r)
-                        m[j] += peer_load(peer(&sh.mass[rank * part + i], r)), c[j] += peer_load32(peer(&sh.count[rank * part + i], r));
-            }
-            cluster_sync();
-#pragma unroll
-            for (int j = 0; j < kBins / kSampleThreads; ++j) {
-                const int i = threadIdx.x + j * kSampleThreads;
-                if (i < part) sh.mass[rank * part + i] = m[j], sh.count[rank * part + i] = c[j];
-            }
+    bool done = top_p >= 1.0f;
+    if (k < p.V) done |= move_cut(s, w, k, static_cast<double>(top_p), cut);
+    if (!done) {
+        if (k < p.V) {  // the bins again
+            for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.bins[i] = 0;
             __syncthreads();
         }
-        u64 kept = 0;
-        if (k < p.V) {
-            cut = find_cut(s, w, false, static_cast<double>(k), kept);
-        } else {
-            u64 all[1] = {0};
-            const int part = kBins / p.cluster;
-            for (int i = threadIdx.x; i < part; i += kSampleThreads) all[0] += sh.mass[rank * part + i];
-            s.template total<1>(all);
-            kept = all[0];
-        }
-        if (top_p < 1.0f) {
-            u64 mass;
-            const u64 by_p = find_cut(s, w, true, static_cast<double>(top_p) * static_cast<double>(kept), mass);
-            if (by_p > cut) cut = by_p;
-        }
+        move_cut(s, w, 0, static_cast<double>(top_p), cut);
     }
     const auto mass_of = [&](float x, int i) -> u64 {
         if (x == -INFINITY || place_of(x, first + i) < cut) return 0;
