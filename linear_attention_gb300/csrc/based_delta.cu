@@ -1218,7 +1218,7 @@ struct DeltaStepParams {
     void *o;
 };
 template <typename T, int VEC>
-__global__ void __launch_bounds__(32 * kStepWarps) based_delta_step_kernel(DeltaStepParams p) {
+__global__ void __launch_bounds__(32 * kStepWarps, 5) based_delta_step_kernel(DeltaStepParams p) {
     constexpr int kLanes = 32 / VEC, kRows = 32 / kLanes * kStepWarps, kEach = kMaxKeys / kRows;  // a row's lanes, rows of a pass, passes
     __shared__ float sk[kMaxKeys], sq[kMaxKeys], red[3][kStepWarps][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y, hk = head / (p.H / p.HK);

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kPack = 8, kMostPacks = 4, kMostThreads = 512;
 constexpr int kRmsMaxC = kPack * kMostPacks * kMostThreads;
-constexpr int kRmsCtas = 608;  // partial sums of the weights' gradient: four CTAs on each of 152 SMs
+constexpr int kRmsCtas = 304;  // partial sums of the weights' gradient: two CTAs on each of 152 SMs
 
 struct RmsParams {
     const void *x, *residual, *weight, *dy, *dsum;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(1024) based_rms_sum_kernel(RmsParams p) {
     griddep_wait();
     float v = 0.0f;
     if (c < p.C) {
-#pragma unroll 4
+#pragma unroll 10
         for (int i = warp; i < p.ctas; i += 32) v += p.partial[static_cast<int64_t>(i) * p.C + c];
     }
     part[warp][lane] = v;
@@ -307,17 +307,20 @@ __global__ void __launch_bounds__(1024) based_rms_sum_kernel(RmsParams p) {
 // Host
 // ------------------------------------------------------------------------------------------------
 template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
-int launch_rms(RmsParams &p, bool bwd, int sms, cudaStream_t st) {
+int launch_fwd(RmsParams &p, int sms, cudaStream_t st) {
     constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
     const int64_t groups = (p.R + kRows - 1) / kRows;
-    if (!bwd) {
-        void (*const fwd)(RmsParams) = based_rms_fwd_kernel<T, S, THREADS, PACKS, WORDS>;
-        int per_sm = 0;
-        if (const int rc = resident_clusters(reinterpret_cast<const void *>(fwd), kCta, 0, 1, &per_sm)) return rc;
-        const int64_t most = per_sm > 0 ? per_sm : sms;  // CTAs of the device
-        OPS_CUDA(launch_op(fwd, static_cast<unsigned>(groups < most ? groups : most), kCta, 0, st, p));
-        return BASED_OK;
-    }
+    void (*const fwd)(RmsParams) = based_rms_fwd_kernel<T, S, THREADS, PACKS, WORDS>;
+    int resident = 0;
+    if (const int rc = resident_clusters(reinterpret_cast<const void *>(fwd), kCta, 0, 1, &resident)) return rc;
+    const int64_t most = resident > 0 ? resident : sms;
+    OPS_CUDA(launch_op(fwd, static_cast<unsigned>(groups < most ? groups : most), kCta, 0, st, p));
+    return BASED_OK;
+}
+template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
+int launch_bwd(RmsParams &p, cudaStream_t st) {
+    constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
+    const int64_t groups = (p.R + kRows - 1) / kRows;
     p.ctas = static_cast<int>(groups < kRmsCtas ? groups : kRmsCtas);
     const size_t smem = kRows > 1 ? static_cast<size_t>(kRows) * p.C * 4 : 0;
     OPS_CUDA(launch_op(based_rms_bwd_kernel<T, S, THREADS, PACKS, WORDS>, p.ctas, kCta, smem, st, p));
@@ -327,23 +330,42 @@ int launch_rms(RmsParams &p, bool bwd, int sms, cudaStream_t st) {
     }
     return BASED_OK;
 }
-// Threads for a row: as few as hold it in four packs each, so that a warp or a part of one serves short rows and sums stay in it
+// Threads for a row: as few as hold it in four packs each (three where that fits better), so that a warp or a part of one serves short rows and
+// sums stay in it. Backward, with three inputs and the weights' gradients in registers, two packs: 24000 x 1536 takes FIGURE.
 template <typename T, typename S>
 int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
     const int packs = (p.C + kPack - 1) / kPack;
-    if (!words) {
-        if (packs <= 128) return launch_rms<T, S, 32, 4, false>(p, bwd, sms, st);
-        if (packs <= 512) return launch_rms<T, S, 128, 4, false>(p, bwd, sms, st);
-        return launch_rms<T, S, 512, 4, false>(p, bwd, sms, st);
+    if (bwd) {
+        if (!words) {
+            if (packs <= 64) return launch_bwd<T, S, 32, 2, false>(p, st);
+            if (packs <= 512) return launch_bwd<T, S, 256, 2, false>(p, st);
+            return launch_bwd<T, S, 512, 4, false>(p, st);
+        }
+        if (packs <= 8) return launch_bwd<T, S, 8, 1, true>(p, st);
+        if (packs <= 32) return launch_bwd<T, S, 16, 2, true>(p, st);
+        if (packs <= 64) return launch_bwd<T, S, 32, 2, true>(p, st);
+        if (packs <= 128) return launch_bwd<T, S, 64, 2, true>(p, st);
+        if (packs <= 256) return launch_bwd<T, S, 128, 2, true>(p, st);
+        if (packs <= 512) return launch_bwd<T, S, 256, 2, true>(p, st);
+        if (packs <= 1024) return launch_bwd<T, S, 512, 2, true>(p, st);
+        return launch_bwd<T, S, 512, 4, true>(p, st);
     }
-    if (packs <= 8) return launch_rms<T, S, 8, 1, true>(p, bwd, sms, st);
-    if (packs <= 32) return launch_rms<T, S, 16, 2, true>(p, bwd, sms, st);
-    if (packs <= 64) return launch_rms<T, S, 32, 2, true>(p, bwd, sms, st);
-    if (packs <= 128) return launch_rms<T, S, 32, 4, true>(p, bwd, sms, st);
-    if (packs <= 256) return launch_rms<T, S, 64, 4, true>(p, bwd, sms, st);
-    if (packs <= 512) return launch_rms<T, S, 128, 4, true>(p, bwd, sms, st);
-    if (packs <= 1024) return launch_rms<T, S, 256, 4, true>(p, bwd, sms, st);
-    return launch_rms<T, S, 512, 4, true>(p, bwd, sms, st);
+    if (!words) {
+        if (packs <= 128) return launch_fwd<T, S, 32, 4, false>(p, sms, st);
+        if (packs <= 512) return launch_fwd<T, S, 128, 4, false>(p, sms, st);
+        return launch_fwd<T, S, 512, 4, false>(p, sms, st);
+    }
+    if (packs <= 8) return launch_fwd<T, S, 8, 1, true>(p, sms, st);
+    if (packs <= 32) return launch_fwd<T, S, 16, 2, true>(p, sms, st);
+    if (packs <= 64) return launch_fwd<T, S, 32, 2, true>(p, sms, st);
+    if (packs <= 128) return launch_fwd<T, S, 32, 4, true>(p, sms, st);
+    if (packs <= 192) return launch_fwd<T, S, 64, 3, true>(p, sms, st);
+    if (packs <= 256) return launch_fwd<T, S, 64, 4, true>(p, sms, st);
+    if (packs <= 384) return launch_fwd<T, S, 128, 3, true>(p, sms, st);
+    if (packs <= 512) return launch_fwd<T, S, 128, 4, true>(p, sms, st);
+    if (packs <= 768) return launch_fwd<T, S, 256, 3, true>(p, sms, st);
+    if (packs <= 1024) return launch_fwd<T, S, 256, 4, true>(p, sms, st);
+    return launch_fwd<T, S, 512, 4, true>(p, sms, st);
 }
 
 int run_rms(RmsParams &p, int dtype, int s_dtype, bool bwd, void *workspace, size_t ws_bytes, based_stream_t stream) {

@@ -45,13 +45,25 @@ struct SampleShared {
 static_assert(sizeof(SampleShared) % 16 == 0, "the tokens lie behind it");
 
 __device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.0f);  // -0 and 0 are equal
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+// Where the kept tokens end in the order: the last one. (Of none -inf is kept.)
+struct Cut {
+    float x = -INFINITY;
+    int index = -1;
+    __device__ __forceinline__ bool keeps(float v, int i) const { return v > x || (v == x && i <= index); }
+};
 // A token's place in the order: larger is earlier
 __device__ __forceinline__ u64 place_of(float x, int index) { return static_cast<u64>(ordered(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(index)); }
 
+// Moves the cut up to a place
+__device__ __forceinline__ void raise(Cut &cut, u64 place) {
+    const float x = unordered(static_cast<uint32_t>(place >> 32));
+    const int i = static_cast<int>(0xffffffffu - static_cast<uint32_t>(place));
+    if (place && (x > cut.x || (x == cut.x && i < cut.index))) cut.x = x, cut.index = i;
+}
 // The same variable in the shared memory of another CTA of the cluster
 template <typename P>
 __device__ __forceinline__ uint32_t peer(P *p, uint32_t rank) {
@@ -115,12 +127,10 @@ struct Sampler {
         meet();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            v[i] = before[i] = 0;
-            for (uint32_t r = 0; r < static_cast<uint32_t>(p.cluster); ++r) {
-                const u64 o = p.cluster > 1 ? peer_load(peer(&sh.slots[turn][i], r)) : sh.slots[turn][i];
-                if (r < rank) before[i] += o;
-                v[i] = MOST ? (o > v[i] ? o : v[i]) : v[i] + o;
-            }
+            u64 o = 0;  // lane r: what CTA r handed over
+            if (lane < p.cluster) o = p.cluster > 1 ? peer_load(peer(&sh.slots[turn][i], lane)) : sh.slots[turn][i];
+            v[i] = over_warp<MOST>(o);
+            before[i] = over_warp<false>(lane < static_cast<int>(rank) ? o : 0);
         }
         turn ^= 1;
         // (the next call writes the other set; sh.warp is read before meet())
@@ -155,17 +165,16 @@ struct Sampler {
 // w = 2^-t, t = (most - x) log2(e) / temperature, with the product's rounding made good
 struct Weigh {
     float most, hi, lo;
-    __device__ __forceinline__ float distance(float x) const { return x == most ? 0.0f : most - x; }
-    __device__ __forceinline__ float bits(float x) const { return distance(x) * hi; }
+    // the bin, as a number whose whole part it is
+    __device__ __forceinline__ float place(float x) const { return (most - x) * hi * (kBins / kReach); }
     __device__ __forceinline__ float weight(float x) const {
-        const float d = distance(x), t = d * hi, r = fmaf(d, hi, -t) + d * lo;
+        const float d = most - x, t = d * hi, r = fmaf(d, hi, -t) + d * lo;
         const float w = ex2(-t);
         return t < 120.0f ? fmaf(w, -0.6931471806f * r, w) : 0.0f;
     }
     __device__ __forceinline__ u64 mass(float x) const { return static_cast<u64>(__float2ull_rn(weight(x) * kMass)); }
     __device__ __forceinline__ int bin(float x) const {
-        const float b = bits(x) * (kBins / kReach);
-        return b < kBins - 1 ? static_cast<int>(b) : kBins - 1;
+        return static_cast<int>(fminf(place(x), kBins - 1.0f));
     }
 };
 
@@ -213,13 +222,13 @@ __device__ __forceinline__ void sort_few(SampleShared &sh, int n) {
 // Moves the cut up: by count to the k'th token of those at or above it and, where `share` is below 1 and all of them could be sorted, on to the first
 // at which the masses reach that share of theirs (returns true); by mass (k is 0) to the latter.
 template <typename T>
-__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64 &cut) {
+__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut &cut) {
     SampleShared &sh = s.sh;
     const SampleParams &p = s.p;
     const bool by_mass = k == 0;
     u64 last = 0;  // the last bin's tokens, which may be most, without atomics
     s.each([&](float x, int i) {
-        if (x == -INFINITY || place_of(x, s.first + i) < cut) return;
+        if (!cut.keeps(x, s.first + i)) return;
         const int bin = w.bin(x);
         const u64 v = by_mass ? w.mass(x) : 1;
         if (bin == kBins - 1)
@@ -239,10 +248,13 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64
         v[j] = 0;
         if (j < per && mine + j < part) {
             const int at = s.rank * part + mine + j;
-            if (p.cluster > 1)
-                for (int r = 0; r < p.cluster; ++r) v[j] += peer_load(peer(&sh.bins[at], r));
-            else
+            if (p.cluster > 1) {
+#pragma unroll
+                for (int r = 0; r < kSampleCluster; ++r)
+                    if (r < p.cluster) v[j] += peer_load(peer(&sh.bins[at], r));
+            } else {
                 v[j] = sh.bins[at];
+            }
         }
         sum += v[j];
     }
@@ -268,11 +280,11 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64
     const bool enough = at[0] != 0, whole = !by_mass && (enough ? at[2] : all[0]) <= kFew;
     if (!enough && !whole) return false;
     const int bin = enough ? static_cast<int>(at[0]) - 1 : kBins - 1, low = whole ? 0 : bin;
+    const float from = static_cast<float>(low), to = bin == kBins - 1 ? INFINITY : static_cast<float>(bin + 1);
     s.each([&](float x, int i) {
-        if (x == -INFINITY) return;
+        const float b = w.place(x);
+        if (!(b < to && (b >= from || from == 0.0f)) || !cut.keeps(x, s.first + i)) return;
         const u64 pl = place_of(x, s.first + i);
-        const int b = w.bin(x);
-        if (b > bin || b < low || pl < cut) return;
         const uint32_t n = p.cluster > 1 ? peer_add(peer(&sh.few, 0), 1) : atomicAdd(&sh.few, 1u);
         if (n >= kFew) return;
         const u64 m = w.mass(x);
@@ -318,7 +330,7 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64
     u64 result[2] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0};
     s.template total<2>(result);
     if (!result[1]) {
-        if (result[0] > cut) cut = result[0];
+        raise(cut, result[0]);
         return whole;
     }
     // Many tokens lie close together (equal logits, a high temperature): the cut bit by bit, the largest place with enough at or above it
@@ -327,13 +339,12 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, u64
         const u64 trial = found | 1ull << bit;
         u64 c[1] = {0};
         s.each([&](float x, int i) {
-            const u64 pl = place_of(x, s.first + i);
-            if (x != -INFINITY && pl >= trial && pl >= cut) c[0] += by_mass ? w.mass(x) : 1;
+            if (cut.keeps(x, s.first + i) && place_of(x, s.first + i) >= trial) c[0] += by_mass ? w.mass(x) : 1;
         });
         s.template total<1>(c);
         if (static_cast<double>(c[0]) >= target) found = trial;
     }
-    if (found > cut) cut = found;
+    raise(cut, found);
     return false;
 }
 
@@ -350,10 +361,10 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     Sampler<T> s = {p, sh, p.resident ? tokens : src, first, len, rank};
     for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.bins[i] = 0;
     if (threadIdx.x == 0) sh.few = 0;
-    u64 best[1] = {0};
+    float top = -INFINITY;
+    int top_at = 0;
     const auto look = [&](float x, int i) {
-        const u64 pl = place_of(x, first + i);
-        if (pl > best[0]) best[0] = pl;
+        if (x > top) top = x, top_at = i;  // indices rise: the first of equals
     };
     if (p.resident && p.words) {
         constexpr int kEl = 16 / sizeof(T);
@@ -382,6 +393,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     } else {
         s.each(look);
     }
+    u64 best[1] = {place_of(top, first + top_at)};
     s.template total<1, true>(best);
     const float most = unordered(static_cast<uint32_t>(best[0] >> 32));
     const float temperature = p.temperature ? p.temperature[n] : p.temperature_all;
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     if (k <= 0 || k > p.V) k = p.V;
     if (!(top_p < 1.0f)) top_p = 1.0f;
     if (top_p <= 0.0f) k = 1, top_p = 1.0f;
-    u64 cut = 0;
+    Cut cut;
     bool done = top_p >= 1.0f;
     if (k < p.V) done |= move_cut(s, w, k, static_cast<double>(top_p), cut);
     if (!done) {
@@ -416,7 +428,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
         move_cut(s, w, 0, static_cast<double>(top_p), cut);
     }
     const auto mass_of = [&](float x, int i) -> u64 {
-        if (x == -INFINITY || place_of(x, first + i) < cut) return 0;
+        if (!cut.keeps(x, first + i)) return 0;
         const float v = w.weight(x);
         return v >= min_p ? static_cast<u64>(__float2ull_rn(v * kMass)) : 0;
     };
