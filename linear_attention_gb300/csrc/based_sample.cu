@@ -35,12 +35,16 @@ struct SampleParams {
 using u64 = unsigned long long;
 
 struct SampleShared {
-    u64 bins[kBins];
-    u64 place[kFew], mass[kFew];  // the tokens to sort
-    u64 slots[2][4];              // what this CTA hands to the others, two sets in turn
+    union {
+        uint32_t bins[3][kBins];  // counts; or masses, 14 bits of them in each (64-bit atomics on shared memory are loops)
+        struct {
+            u64 place[kFew], mass[kFew];
+        } few;  // the tokens to sort: in the first CTA, once all have read its bins
+    };
+    u64 slots[2][4];  // what this CTA hands to the others, two sets in turn
     u64 warp[4][kSampleWarps];
     u64 found[4];
-    uint32_t few, pad[3];
+    uint32_t count, pad[3];
 };
 static_assert(sizeof(SampleShared) % 16 == 0, "the tokens lie behind it");
 
@@ -74,6 +78,11 @@ __device__ __forceinline__ uint32_t peer(P *p, uint32_t rank) {
 __device__ __forceinline__ u64 peer_load(uint32_t at) {
     u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t peer_load32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ void peer_store(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
@@ -144,8 +153,16 @@ struct Sampler {
     // f(x, index in the slice) for this thread's tokens, in the order of their indices within a warp's rounds
     template <typename F>
     __device__ __forceinline__ void each(F f) {
+        each(f, [](int) {});
+    }
+    // ... and g(index of the first) after every eight
+    template <typename F, typename G>
+    __device__ __forceinline__ void each(F f, G g) {
         const int per = (len + kSampleWarps * 8 - 1) / (kSampleWarps * 8) * 8, from = warp * per, to = min(len, from + per);
-        for (int i = from + 8 * lane; i < to; i += 256) eight(i, to, f);
+        for (int i = from + 8 * lane; i < to; i += 256) {
+            eight(i, to, f);
+            g(i);
+        }
     }
     template <typename F>
     __device__ __forceinline__ void eight(int i, int to, F f) {
@@ -154,6 +171,7 @@ struct Sampler {
 #pragma unroll
             for (int e = 0; e < 8; ++e) f(to_f32(w.v[e]), i + e);
         } else {
+#pragma unroll 1
             for (int e = 0; e < 8 && i + e < to; ++e) {
                 const float x = to_f32(row[i + e]);
                 f(x == x ? x : -INFINITY, i + e);
@@ -203,26 +221,44 @@ __device__ __forceinline__ u64 cta_prefix(u64 v, u64 *by_warp, u64 &all) {
 __device__ __forceinline__ void sort_few(SampleShared &sh, int n) {
     int size = 2;
     while (size < n) size *= 2;
-    for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sh.place[i] = sh.mass[i] = 0;
+    for (int i = n + threadIdx.x; i < size; i += kSampleThreads) sh.few.place[i] = sh.few.mass[i] = 0;
     for (int k = 2; k <= size; k *= 2)
         for (int d = k / 2; d > 0; d /= 2) {
             __syncthreads();
             for (int i = threadIdx.x; i < size / 2; i += kSampleThreads) {
                 const int a = 2 * i - (i & (d - 1)), b = a + d;
-                const u64 x = sh.place[a], y = sh.place[b];
+                const u64 x = sh.few.place[a], y = sh.few.place[b];
                 if (((a & k) == 0) == (x < y)) {
-                    const u64 m = sh.mass[a];
-                    sh.place[a] = y, sh.place[b] = x, sh.mass[a] = sh.mass[b], sh.mass[b] = m;
+                    const u64 m = sh.few.mass[a];
+                    sh.few.place[a] = y, sh.few.place[b] = x, sh.few.mass[a] = sh.few.mass[b], sh.few.mass[b] = m;
                 }
             }
         }
     __syncthreads();
 }
 
+// (up to 2^18 of at most 2^40, or their sums: the highest part takes what is above)
+__device__ __forceinline__ void add_mass(SampleShared &sh, int bin, u64 v) {
+    atomicAdd(&sh.bins[0][bin], static_cast<uint32_t>(v) & 0x3fffu);
+    atomicAdd(&sh.bins[1][bin], static_cast<uint32_t>(v >> 14) & 0x3fffu);
+    atomicAdd(&sh.bins[2][bin], static_cast<uint32_t>(v >> 28));
+}
+
+// share * total, rounded up (UP) or down to a whole number; share in (0, 1)
+template <bool UP>
+__device__ __forceinline__ u64 share_of(float share, u64 total) {
+    const uint32_t b = __float_as_uint(share), e = b >> 23, m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const uint32_t shift = 150 - (e ? e : 1);  // share = m 2^-shift, shift from 24 on
+    const u64 low = total * m, high = __umul64hi(total, m);
+    if (shift >= 128) return UP && (low | high) ? 1 : 0;
+    if (shift >= 64) return (shift == 64 ? high : high >> (shift - 64)) + (UP && (low | (shift == 64 ? 0 : high << (128 - shift))) ? 1 : 0);
+    return (high << (64 - shift) | low >> shift) + (UP && low << (64 - shift) ? 1 : 0);
+}
+
 // Moves the cut up: by count to the k'th token of those at or above it and, where `share` is below 1 and all of them could be sorted, on to the first
 // at which the masses reach that share of theirs (returns true); by mass (k is 0) to the latter.
 template <typename T>
-__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut &cut) {
+__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut &cut) {
     SampleShared &sh = s.sh;
     const SampleParams &p = s.p;
     const bool by_mass = k == 0;
@@ -230,14 +266,20 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut
     s.each([&](float x, int i) {
         if (!cut.keeps(x, s.first + i)) return;
         const int bin = w.bin(x);
-        const u64 v = by_mass ? w.mass(x) : 1;
-        if (bin == kBins - 1)
-            last += v;
-        else if (v)
-            atomicAdd(&sh.bins[bin], v);
+        if (by_mass) {
+            const u64 v = w.mass(x);
+            if (bin == kBins - 1)
+                last += v;
+            else
+                add_mass(sh, bin, v);
+        } else if (bin == kBins - 1) {
+            ++last;
+        } else {
+            atomicAdd(&sh.bins[0][bin], 1u);
+        }
     });
     last = over_warp<false>(last);
-    if (s.lane == 0 && last) atomicAdd(&sh.bins[kBins - 1], last);
+    if (s.lane == 0 && last) by_mass ? add_mass(sh, kBins - 1, last) : static_cast<void>(atomicAdd(&sh.bins[0][kBins - 1], static_cast<uint32_t>(last)));
     s.meet();
     // this CTA's part of the bins over all CTAs: up to four neighbouring bins a thread
     constexpr int kMost = kBins / kSampleThreads;
@@ -248,12 +290,18 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut
         v[j] = 0;
         if (j < per && mine + j < part) {
             const int at = s.rank * part + mine + j;
-            if (p.cluster > 1) {
 #pragma unroll
-                for (int r = 0; r < kSampleCluster; ++r)
-                    if (r < p.cluster) v[j] += peer_load(peer(&sh.bins[at], r));
-            } else {
-                v[j] = sh.bins[at];
+            for (int c = 0; c < 3; ++c) {
+                if (c && !by_mass) continue;
+                u64 all_of = 0;
+                if (p.cluster > 1) {
+#pragma unroll
+                    for (int r = 0; r < kSampleCluster; ++r)
+                        if (r < p.cluster) all_of += peer_load32(peer(&sh.bins[c][at], r));
+                } else {
+                    all_of = sh.bins[c][at];
+                }
+                v[j] += all_of << (14 * c);
             }
         }
         sum += v[j];
@@ -264,10 +312,10 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut
     if (threadIdx.x == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
     s.template total<1>(all, others);
     before += others[0];
-    const double target = by_mass ? share * static_cast<double>(all[0]) : static_cast<double>(k);
+    const u64 target = by_mass ? share_of<true>(share, all[0]) : static_cast<u64>(k);  // (whole numbers: 64-bit floats are slow here)
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
-        if (static_cast<double>(before) < target && static_cast<double>(before + v[j]) >= target)
+        if (before < target && before + v[j] >= target)
             sh.found[0] = s.rank * part + mine + j + 1, sh.found[1] = before, sh.found[2] = before + v[j];
         before += v[j];
     }
@@ -281,48 +329,54 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut
     if (!enough && !whole) return false;
     const int bin = enough ? static_cast<int>(at[0]) - 1 : kBins - 1, low = whole ? 0 : bin;
     const float from = static_cast<float>(low), to = bin == kBins - 1 ? INFINITY : static_cast<float>(bin + 1);
+    uint32_t hits = 0;  // of eight tokens: what follows is needed for few, so it is there once
     s.each([&](float x, int i) {
         const float b = w.place(x);
-        if (!(b < to && (b >= from || from == 0.0f)) || !cut.keeps(x, s.first + i)) return;
-        const u64 pl = place_of(x, s.first + i);
-        const uint32_t n = p.cluster > 1 ? peer_add(peer(&sh.few, 0), 1) : atomicAdd(&sh.few, 1u);
-        if (n >= kFew) return;
-        const u64 m = w.mass(x);
-        if (p.cluster > 1)
-            peer_store(peer(&sh.place[n], 0), pl), peer_store(peer(&sh.mass[n], 0), m);
-        else
-            sh.place[n] = pl, sh.mass[n] = m;
+        if (b < to && (b >= from || from == 0.0f) && cut.keeps(x, s.first + i)) hits |= 1u << (i & 7);
+    }, [&](int i0) {
+        while (hits) {
+            const int i = i0 + __ffs(hits) - 1;
+            hits &= hits - 1;
+            const float x = to_f32(s.row[i]);
+            const uint32_t n = p.cluster > 1 ? peer_add(peer(&sh.count, 0), 1) : atomicAdd(&sh.count, 1u);
+            if (n >= kFew) continue;
+            const u64 pl = place_of(x, s.first + i), m = w.mass(x);
+            if (p.cluster > 1)
+                peer_store(peer(&sh.few.place[n], 0), pl), peer_store(peer(&sh.few.mass[n], 0), m);
+            else
+                sh.few.place[n] = pl, sh.few.mass[n] = m;
+        }
     });
     s.meet();
     if (s.tid == 0) sh.found[0] = sh.found[1] = 0;
-    const uint32_t few = s.rank == 0 ? sh.few : 0;
+    const uint32_t few = s.rank == 0 ? sh.count : 0;
     __syncthreads();
     if (s.rank == 0) {
-        if (s.tid == 0) sh.few = 0, sh.found[1] = few > kFew;
+        if (s.tid == 0) sh.count = 0, sh.found[1] = few > kFew;
         const int n = static_cast<int>(few);
         if (n > 0 && n <= kFew) {
             sort_few(sh, n);
             // the k'th of all, or what is behind the bins in front
             const u64 base = whole ? 0 : at[1];
             const int nth = by_mass || !enough ? n : static_cast<int>(static_cast<u64>(k) - base);
-            if (share < 1.0 && (by_mass || whole)) {
+            if (share < 1.0f && (by_mass || whole)) {
                 u64 m[kFew / kSampleThreads], sums = 0, up_to;
 #pragma unroll
                 for (int j = 0; j < kFew / kSampleThreads; ++j) {
                     const int i = threadIdx.x * (kFew / kSampleThreads) + j;
-                    m[j] = i < nth ? sh.mass[i] : 0;
+                    m[j] = i < nth ? sh.few.mass[i] : 0;
                     sums += m[j];
                 }
                 u64 now = (by_mass ? base : 0) + cta_prefix(sums, sh.warp[3], up_to);
-                const double reach = by_mass ? target : share * static_cast<double>(up_to);
+                const u64 reach = by_mass ? target : share_of<true>(share, up_to);
 #pragma unroll
                 for (int j = 0; j < kFew / kSampleThreads; ++j) {
-                    if (static_cast<double>(now) < reach && static_cast<double>(now + m[j]) >= reach)
-                        sh.found[0] = sh.place[threadIdx.x * (kFew / kSampleThreads) + j];
+                    if (now < reach && now + m[j] >= reach)
+                        sh.found[0] = sh.few.place[threadIdx.x * (kFew / kSampleThreads) + j];
                     now += m[j];
                 }
             } else if (s.tid == 0) {
-                sh.found[0] = sh.place[nth - 1];
+                sh.found[0] = sh.few.place[nth - 1];
             }
         }
     }
@@ -342,7 +396,7 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, double share, Cut
             if (cut.keeps(x, s.first + i) && place_of(x, s.first + i) >= trial) c[0] += by_mass ? w.mass(x) : 1;
         });
         s.template total<1>(c);
-        if (static_cast<double>(c[0]) >= target) found = trial;
+        if (c[0] >= target) found = trial;
     }
     raise(cut, found);
     return false;
@@ -359,8 +413,8 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     griddep_wait();
     const T *const src = static_cast<const T *>(p.logits) + n * p.stride + first;
     Sampler<T> s = {p, sh, p.resident ? tokens : src, first, len, rank};
-    for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.bins[i] = 0;
-    if (threadIdx.x == 0) sh.few = 0;
+    for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) sh.bins[0][i] = 0;
+    if (threadIdx.x == 0) sh.count = 0;
     float top = -INFINITY;
     int top_at = 0;
     const auto look = [&](float x, int i) {
@@ -406,9 +460,8 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
         s.meet();  // shared memory stays until the others have read it
         return;
     }
-    const double factor = 1.4426950408889634 / temperature;
     Weigh w;
-    w.most = most, w.hi = static_cast<float>(factor), w.lo = static_cast<float>(factor - w.hi);
+    w.most = most, w.hi = 1.44269502f / temperature, w.lo = (fmaf(-w.hi, temperature, 1.44269502f) + 1.92596303e-8f) / temperature;
     if (!(w.hi < 3e38f)) w.hi = 3e38f, w.lo = 0.0f;
     int k = p.top_k ? p.top_k[n] : p.top_k_all;
     float top_p = p.top_p ? p.top_p[n] : p.top_p_all;
@@ -419,35 +472,39 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     if (top_p <= 0.0f) k = 1, top_p = 1.0f;
     Cut cut;
     bool done = top_p >= 1.0f;
-    if (k < p.V) done |= move_cut(s, w, k, static_cast<double>(top_p), cut);
+    if (k < p.V) done |= move_cut(s, w, k, top_p, cut);
     if (!done) {
         if (k < p.V) {  // the bins again
-            for (int i = threadIdx.x; i < kBins; i += kSampleThreads) sh.bins[i] = 0;
+            for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) sh.bins[0][i] = 0;
             __syncthreads();
         }
-        move_cut(s, w, 0, static_cast<double>(top_p), cut);
+        move_cut(s, w, 0, top_p, cut);
     }
-    const auto mass_of = [&](float x, int i) -> u64 {
-        if (!cut.keeps(x, first + i)) return 0;
+    const auto kept = [&](float x, int i) -> float {
+        if (!cut.keeps(x, first + i)) return 0.0f;
         const float v = w.weight(x);
-        return v >= min_p ? static_cast<u64>(__float2ull_rn(v * kMass)) : 0;
+        return v >= min_p ? v : 0.0f;
     };
+    // the mass of eight tokens: the same in both passes
+    const auto mass_of = [&](int i, int to) -> u64 {
+        float sum = 0.0f;
+        s.eight(i, to, [&](float x, int e) { sum += kept(x, e); });
+        return static_cast<u64>(__float2ull_rn(sum * kMass));
+    };
+    const int per = (len + kSampleWarps * 8 - 1) / (kSampleWarps * 8) * 8, begin = s.warp * per, to = min(len, begin + per);
     u64 sum[1] = {0}, before[1];
-    s.each([&](float x, int i) { sum[0] += mass_of(x, i); });
+    for (int i = begin + 8 * s.lane; i < to; i += 256) sum[0] += mass_of(i, to);
     s.template total<1>(sum, before);  // leaves the warps' sums in sh.warp
-    double target = static_cast<double>(p.u[n]) * static_cast<double>(sum[0]);
-    const double end = static_cast<double>(sum[0]) - 0.5;
-    if (!(target < end)) target = end;
-    if (!(target >= 0.0)) target = 0.0;
+    const float u = p.u[n];
+    u64 target = u > 0.0f ? u < 1.0f ? share_of<false>(u, sum[0]) : sum[0] : 0;
+    if (target >= sum[0]) target = sum[0] - 1;
     // the warp at which the sum passes the target, then its round, lane and token
     u64 at = before[0];
     for (int i = 0; i < s.warp; ++i) at += sh.warp[0][i];
-    if (static_cast<double>(at) <= target && static_cast<double>(at + sh.warp[0][s.warp]) > target) {
-        const int per = (len + kSampleWarps * 8 - 1) / (kSampleWarps * 8) * 8, from = s.warp * per, to = min(len, from + per);
-        for (int i0 = from; i0 < to; i0 += 256) {
+    if (at <= target && at + sh.warp[0][s.warp] > target) {
+        for (int i0 = begin; i0 < to; i0 += 256) {
             const int i = i0 + 8 * s.lane;
-            u64 m = 0;
-            if (i < to) s.eight(i, to, [&](float x, int e) { m += mass_of(x, e); });
+            const u64 m = i < to ? mass_of(i, to) : 0;
             u64 up = m;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -455,19 +512,22 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
                 if (s.lane >= d) up += o;
             }
             const u64 mine = at + up - m;
-            if (m && static_cast<double>(mine) <= target && static_cast<double>(mine + m) > target) {
-                u64 now = mine;
+            if (m && mine <= target && mine + m > target) {
+                // the token in the eight: the first at which their sum passes what is left, or the last that is kept
+                const float left = static_cast<float>(target - mine) / kMass;
+                float now = 0.0f, weight = 0.0f;
+                int token = -1;
+                bool passed = false;
                 s.eight(i, to, [&](float x, int e) {
-                    const u64 v = mass_of(x, e);
-                    if (v && static_cast<double>(now) <= target && static_cast<double>(now + v) > target) {
-                        p.tokens[n] = first + e;
-                        if (p.probs) p.probs[n] = static_cast<float>(static_cast<double>(w.weight(x)) * kMass / static_cast<double>(sum[0]));
-                    }
+                    const float v = kept(x, e);
                     now += v;
+                    if (v > 0.0f && !passed) token = first + e, weight = v, passed = now > left;
                 });
+                p.tokens[n] = token;
+                if (p.probs) p.probs[n] = static_cast<float>(static_cast<double>(weight) * kMass / static_cast<double>(sum[0]));
             }
             at += __shfl_sync(0xffffffffu, up, 31);
-            if (static_cast<double>(at) > target) break;
+            if (at > target) break;
         }
     }
     s.meet();
@@ -479,7 +539,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
 template <typename T>
 int launch_sample(SampleParams &p, int N, int sms, cudaStream_t st) {
     constexpr int64_t kRoom = 226 * 1024 - static_cast<int64_t>(sizeof(SampleShared));
-    constexpr int64_t kShare = kRoom / 2 - 24 * 1024;  // two CTAs on an SM
+    constexpr int64_t kShare = 113 * 1024 - static_cast<int64_t>(sizeof(SampleShared));  // two CTAs on an SM
     const auto bytes = [&](int cluster) {
         return ((static_cast<int64_t>(p.V) + cluster - 1) / cluster + 7) / 8 * 8 * static_cast<int64_t>(sizeof(T));
     };
