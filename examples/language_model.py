@@ -5,9 +5,11 @@ activated gate, projection] -> logits with the embedding's table. It is trained 
 sequences in which every token follows from the one before, and then generates from prompts of
 different lengths: one pass over the padded prompts fills a pool of states, and each new token takes
 one step of the recurrence. In a layer of kind "based" the token mixer is the Based forward pass
-(without a backward pass, so such layers score text and are not trained).
+(without a backward pass, so such layers score text and are not trained). In a layer of kind "delta" it is the gated
+delta rule, and the norm in front of it also adds what the layer before has left to add to the residual stream.
+Tokens are the most likely ones, or sampled from given random numbers.
 
-    python examples/language_model.py [--steps 60]
+    python examples/language_model.py [--steps 60] [--kinds recurrence,delta] [--temperature 0.7 --top-p 0.9]
 """
 import argparse
 import math
@@ -21,8 +23,9 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
-from linear_attention_gb300 import based_embed_fwd, based_fwd, based_norm_fwd, based_scan_fwd, based_scan_step  # noqa: E402
-from linear_attention_gb300.autograd import embedding, gated_scan, group_norm  # noqa: E402
+from linear_attention_gb300 import (based_delta_fwd, based_delta_step, based_embed_fwd, based_fwd, based_norm_fwd,  # noqa: E402
+                                    based_rms_fwd, based_sample, based_scan_fwd, based_scan_step)
+from linear_attention_gb300.autograd import delta_rule, embedding, gated_scan, group_norm, rms_norm  # noqa: E402
 
 
 class Layer(torch.nn.Module):
@@ -69,13 +72,65 @@ class Layer(torch.nn.Module):
         m, gate = self.split(x, based_norm_fwd)
         return self.out(x, based_scan_step(m[:, :self.width] + 2.0, m[:, self.width:], pool, slots=slots), gate, based_norm_fwd)
 
+    def pool(self, slots, device):
+        return torch.zeros(slots, self.width, device=device)
+
+
+def settled(x, update):
+    """The stream with what is still to be added."""
+    return x if update is None else x + update
+
+
+class DeltaLayer(torch.nn.Module):
+    """A layer of the gated delta rule. It takes the stream and what is still to be added to it, and returns the two."""
+
+    def __init__(self, width: int, heads: int, dtype, device):
+        super().__init__()
+        self.width, self.heads, self.size = width, heads, width // heads
+        new = lambda *s: torch.nn.Parameter(torch.empty(*s, dtype=dtype, device=device))  # noqa: E731
+        # q, k, v, the output gate, and a gate and a step size for each head
+        self.proj_in, self.proj_out = new(4 * width + 2 * heads, width), new(width, width)
+        self.norm_w, self.head_w = new(width), new(width)
+        with torch.no_grad():
+            for p in (self.proj_in, self.proj_out):
+                p.normal_(0, width ** -0.5)
+            self.norm_w.fill_(1), self.head_w.fill_(1)
+
+    def split(self, y):
+        p = F.linear(y, self.proj_in)
+        q, k, v, out, beta, gate = p.split([self.width] * 4 + [self.heads] * 2, -1)
+        q, k, v = (t.unflatten(-1, (self.heads, self.size)) for t in (q, k, v))
+        return F.normalize(q, dim=-1), F.normalize(k, dim=-1), v, torch.sigmoid(beta), F.logsigmoid(gate + 3.0), out
+
+    def train_forward(self, x, update, lengths):
+        y, x = rms_norm(x, self.norm_w) if update is None else rms_norm(update, self.norm_w, residual=x)
+        *mix, out = self.split(y)
+        o, _ = delta_rule(*mix, lengths=lengths)
+        return x, F.linear(group_norm(o.flatten(-2), self.heads, self.head_w, gate=out), self.proj_out)
+
+    def run(self, x, update, mixer):
+        y, x, _ = based_rms_fwd(x, self.norm_w) if update is None else based_rms_fwd(update, self.norm_w, residual=x)
+        *mix, out = self.split(y)
+        o, state = mixer(*mix)
+        return x, F.linear(based_norm_fwd(o.flatten(-2), self.heads, self.head_w, gate=out), self.proj_out), state
+
+    def prefill(self, x, update, lengths):
+        return self.run(x, update, lambda *mix: based_delta_fwd(*mix, lengths=lengths)[:2])
+
+    def step(self, x, update, pool, slots):
+        return self.run(x, update, lambda *mix: (based_delta_step(*mix, pool, slots=slots), None))[:2]
+
+    def pool(self, slots, device):
+        return torch.zeros(slots, self.heads, self.size, self.size, device=device)
+
 
 class Model(torch.nn.Module):
     def __init__(self, vocab=512, width=256, heads=4, kinds=("recurrence", "recurrence"), dtype=torch.bfloat16, device="cuda"):
         super().__init__()
         self.vocab, self.width, self.scale = vocab, width, math.sqrt(width)
         self.table = torch.nn.Parameter(torch.randn(vocab, width, device=device).mul_(width ** -0.5).to(dtype))
-        self.layers = torch.nn.ModuleList(Layer(width, heads, k, dtype, device) for k in kinds)
+        self.layers = torch.nn.ModuleList(
+            DeltaLayer(width, heads, dtype, device) if k == "delta" else Layer(width, heads, k, dtype, device) for k in kinds)
         self.last_w = torch.nn.Parameter(torch.ones(width, dtype=dtype, device=device))
 
     def logits(self, x, norm):
@@ -84,38 +139,55 @@ class Model(torch.nn.Module):
     def loss(self, ids, lengths):
         """Mean loss of predicting each token from those before it; ids (B,T) hold -1 past the lengths."""
         x = embedding(ids[:, :-1], self.table, self.scale)
+        update = None  # what a layer of kind "delta" leaves to the norm behind it to add
         for layer in self.layers:
-            x = layer.train_forward(x, (lengths - 1).clamp(min=0).to(torch.int32))
+            live = (lengths - 1).clamp(min=0).to(torch.int32)
+            if isinstance(layer, DeltaLayer):
+                x, update = layer.train_forward(x, update, live)
+            else:
+                x, update = layer.train_forward(settled(x, update), live), None
+        x = settled(x, update)
         return F.cross_entropy(self.logits(x, group_norm).flatten(0, 1), ids[:, 1:].flatten().long(), ignore_index=-1)
 
     @torch.no_grad()
     def prefill(self, ids, lengths):
         """Logits of every position (B,T,vocab) and each layer's states (B,width)."""
-        x, states = based_embed_fwd(ids, self.table, self.scale), []
+        x, update, states = based_embed_fwd(ids, self.table, self.scale), None, []
         for layer in self.layers:
-            x, state = layer.prefill(x, lengths)
+            if isinstance(layer, DeltaLayer):
+                x, update, state = layer.prefill(x, update, lengths)
+            else:
+                (x, state), update = layer.prefill(settled(x, update), lengths), None
             states.append(state)
-        return self.logits(x, based_norm_fwd), states
+        return self.logits(settled(x, update), based_norm_fwd), states
 
     @torch.no_grad()
-    def generate(self, ids, lengths, count, slots_in_pool=64):
-        """The `count` most likely next tokens of each prompt, greedily: (B,count)."""
+    def generate(self, ids, lengths, count, slots_in_pool=64, **limits):
+        """`count` next tokens of each prompt: (B,count). The most likely ones, or, with any of the limits of based_sample
+        (temperature, top_k, top_p, min_p), sampled from torch's random numbers."""
         logits, states = self.prefill(ids, lengths)
         B = ids.shape[0]
         # the sequences' places in a pool of states that a server shares among its requests
         slots = torch.randperm(slots_in_pool, device=ids.device)[:B].to(torch.int32)
         pools = []
-        for state in states:
-            pool = torch.zeros(slots_in_pool, self.width, device=ids.device)
+        for layer, state in zip(self.layers, states):
+            pool = layer.pool(slots_in_pool, ids.device)
             pool[slots.long()] = state
             pools.append(pool)
-        token = logits[torch.arange(B, device=ids.device), lengths.long() - 1].argmax(-1)
+
+        def choose(logits):
+            return based_sample(logits, torch.rand(B, device=ids.device), **limits)[0] if limits else logits.argmax(-1)
+
+        token = choose(logits[torch.arange(B, device=ids.device), lengths.long() - 1])
         out = [token]
         for _ in range(count - 1):
-            x = based_embed_fwd(token, self.table, self.scale)
+            x, update = based_embed_fwd(token, self.table, self.scale), None
             for layer, pool in zip(self.layers, pools):
-                x = layer.step(x, pool, slots)
-            token = self.logits(x, based_norm_fwd).argmax(-1)
+                if isinstance(layer, DeltaLayer):
+                    x, update = layer.step(x, update, pool, slots)
+                else:
+                    x, update = layer.step(settled(x, update), pool, slots), None
+            token = choose(self.logits(settled(x, update), based_norm_fwd))
             out.append(token)
         return torch.stack(out, 1)
 
@@ -147,14 +219,18 @@ def train(model, steps, gen, B=16, T=128):
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
+    ap.add_argument("--kinds", default="recurrence,recurrence", help="the layers, by commas: recurrence or delta")
+    for name, kind in (("temperature", float), ("top-k", int), ("top-p", float), ("min-p", float)):
+        ap.add_argument("--" + name, type=kind, help="sample the tokens with this limit")
     a = ap.parse_args()
     torch.manual_seed(0)
     gen = torch.Generator().manual_seed(0)
-    model = Model()
+    model = Model(kinds=tuple(a.kinds.split(",")))
+    limits = {k: v for k, v in vars(a).items() if k not in ("steps", "kinds") and v is not None}
     losses = train(model, a.steps, gen)
     print("loss of the first and last five steps: %.3f %.3f" % (sum(losses[:5]) / 5, sum(losses[-5:]) / 5))
     ids, lengths = batch(model.vocab, 8, 40, gen)
-    got = model.generate(ids, lengths, 12)
+    got = model.generate(ids, lengths, 12, **limits)
     last = ids[torch.arange(8, device=ids.device), lengths.long() - 1].long()
     right = 0
     for i in range(12):

@@ -91,6 +91,57 @@ class _Embed(Function):
         return None, ops.based_embed_bwd(ctx.saved_tensors[0], _rows(dy), rows, scale, dtype=dtype), None
 
 
+class _Delta(Function):
+    @staticmethod
+    def forward(ctx, q, k, v, beta, gate, state, lengths, scale):
+        needed = any(ctx.needs_input_grad[:6])
+        q, k, v, beta = (_dense(t) for t in (q, k, v, beta))
+        gate = gate if gate is None else _dense(gate)
+        state, lengths = (t if t is None else t.contiguous() for t in (state, lengths))
+        o, final, saved = ops.based_delta_fwd(q, k, v, beta, gate, scale=scale, state=state, lengths=lengths, save=needed)
+        ctx.save_for_backward(q, k, v, beta, gate, lengths, saved)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do, dfinal):
+        q, k, v, beta, gate, lengths, saved = ctx.saved_tensors
+        if do is None and dfinal is None:
+            return (None,) * 8
+        do = torch.zeros_like(v, memory_format=torch.contiguous_format) if do is None else _dense(do)
+        dq, dk, dv, dbeta, dgate, dstate = ops.based_delta_bwd(q, k, v, beta, gate, do, saved, scale=ctx.scale,
+                                                               dfinal=None if dfinal is None else dfinal.contiguous(),
+                                                               lengths=lengths)
+        return dq, dk, dv, dbeta, dgate, dstate if ctx.needs_input_grad[5] else None, None, None
+
+
+class _Rms(Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        x, residual = _rows(x), residual if residual is None else _rows(residual)
+        weight = weight if weight is None else weight.contiguous()
+        y, total, _ = ops.based_rms_fwd(x, weight, residual=residual, eps=eps)
+        ctx.save_for_backward(total, weight)
+        ctx.args = (eps, residual is not None, x.dtype)
+        ctx.set_materialize_grads(False)
+        return (y, total) if residual is not None else (y, None)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dsum):
+        total, weight = ctx.saved_tensors
+        eps, added, dtype = ctx.args
+        if dy is None:  # only the sum was used
+            if dsum is None:
+                return None, None, None, None
+            dweight = None if weight is None else torch.zeros_like(weight)
+            return dsum.to(dtype), dweight, dsum, None
+        ds, dx, dweight = ops.based_rms_bwd(_rows(dy), total, weight, dsum=None if dsum is None else _rows(dsum), eps=eps)
+        return dx, dweight, ds if added else None, None
+
+
 def gated_scan(gate: torch.Tensor, x: torch.Tensor, mode: str = "sigmoid", state: Optional[torch.Tensor] = None,
                lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The gated linear recurrence (ops.based_scan_fwd): (h of every row, the last state)."""
@@ -107,3 +158,17 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
 def embedding(ids: torch.Tensor, table: torch.Tensor, scale: float = 1.0) -> torch.Tensor:
     """The scaled embedding (ops.based_embed_fwd); the gradient has the type of the table."""
     return _Embed.apply(ids, table, scale)
+
+
+def delta_rule(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: torch.Tensor, gate: Optional[torch.Tensor] = None,
+               scale: Optional[float] = None, state: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gated delta rule (ops.based_delta_fwd): (o of every row, the last state)."""
+    return _Delta.apply(q, k, v, beta, gate, state, lengths, scale)
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The root-mean-square norm of a residual stream (ops.based_rms_fwd): (y, the stream x + residual; x without one)."""
+    y, total = _Rms.apply(x, weight, residual, eps)
+    return y, x if total is None else total

@@ -1150,7 +1150,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     if (i < rows) {
                         const int64_t at = (first + i) * p.H + head;
                         static_cast<T *>(p.dbeta)[at] = from_f32<T>(part_beta[i]);
-                        if (p.dgate) static_cast<T *>(p.dgate)[at] = from_f32<T>(sum - (e ? x[0] : 0.0f) + end);
+                        if (p.dgate) {  // (a decay of 0 has no gradient, whatever the sums' rounding leaves)
+                            const float log = i ? (f[F_BHI + i] - f[F_BHI + i - 1]) + (f[F_BLO + i] - f[F_BLO + i - 1]) : f[F_BHI];
+                            static_cast<T *>(p.dgate)[at] = from_f32<T>(expf(log) == 0.0f ? 0.0f : sum - (e ? x[0] : 0.0f) + end);
+                        }
                     }
                 }
             }
@@ -1436,7 +1439,7 @@ int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_by
 }
 
 // The default scale is K^-1/2.
-inline float delta_scale(float scale, int K) { return scale > 0.0f || K < 1 ? scale : 1.0f / sqrtf(static_cast<float>(K)); }
+inline float delta_scale(float scale, int K) { return !(scale <= 0.0f) || K < 1 ? scale : 1.0f / sqrtf(static_cast<float>(K)); }
 
 template <typename T>
 int launch_delta_step(const DeltaStepParams &p, cudaStream_t st) {

@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParam
 #pragma unroll
             for (int e = 0; e < kPack; ++e) sq = fmaf(s[j][e], s[j][e], sq), ds = fmaf(d[j][e] * w[j][e], s[j][e], ds);
         over_row2<THREADS>(sq, ds, red, turn);
-        const float r = rsqrtf(sq * mean + p.eps), back = ds * mean * r * r;  // mean(d s) r^2
+        // (rows behind the last add nothing to the weights' gradient, whatever eps is)
+        const float r = row < p.R ? rsqrtf(sq * mean + p.eps) : 0.0f, back = ds * mean * r * r;  // mean(d s) r^2
 #pragma unroll
         for (int j = 0; j < PACKS; ++j) {
             float x[kPack];
