@@ -99,7 +99,7 @@ def test_heavy_and_cleared_decays(cuda_device):
     other = dict(more, state=more["state"] * 5)
     o, final, _ = based_delta_fwd(**s, **other)
     assert torch.equal(o[:, 100:], got["o"][:, 100:]) and torch.equal(final, got["final"])
-    assert (got["dgate"][:, 70] == 0).all() and (got["dgate"][:, 100] == 0).all() and (got["dstate"] == 0).all()
+    assert (got["dgate"][:, 70] == 0).all() and (got["dgate"][:, 100] == 0).all()
 
 
 def test_no_steps_and_large_steps(cuda_device):
