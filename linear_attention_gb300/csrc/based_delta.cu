@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
                     uint32_t x[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
-                    products<NI, NI>(sk[2 * np], sk[2 * np + 1], a, x);
-                    products<NI, NI>(sq[2 * np], sq[2 * np + 1], c, x);
+                    products<T, NI, NI>(sk[2 * np], sk[2 * np + 1], a, x);
+                    products<T, NI, NI>(sq[2 * np], sq[2 * np + 1], c, x);
                 }
             }
         }
@@ -578,10 +578,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 take<2>(a, q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<2, NI>(x[0], x[1], a, r);
+                products<T, 2, NI>(x[0], x[1], a, r);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
+                products<T, NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
             }
             by_columns(x, f + F_GROW + 16 * w, f[F_K] * is, lane);
             by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale * is, lane);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 uint32_t a[2][4], r[2][4];
                 take<2>(a, q.mine + Sm::x(false) + kb * 1024, lane);
                 right<kChunk>(r[0], inv, 16 * w, 16 * kb, lane), right<kChunk>(r[1], inv + kSquare, 16 * w, 16 * kb, lane);
-                products<2, 2>(t[0], t[1], a, r);
+                products<T, 2, 2>(t[0], t[1], a, r);
                 add(y, t, q.sc[8 + kb] * f[F_INV]);
             }
             // All warps scale E and U for the same bounds, from X's and the inverse's largest, so that sums run over all rows
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 take<NO>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
 #pragma unroll
                 for (int j = 0; j < NO; ++j) right<kChunk>(r[j], pimg + j * kSquare, 16 * w, 16 * kb, lane);
-                products<NO, NO>(x[0], x[1], a, r);
+                products<T, NO, NO>(x[0], x[1], a, r);
             }
             add(z, x, inverse_of(se) * f[F_P]);
             // S = whole S0 + K^T U, this warp's quarter
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                     uint32_t r[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<2, NI>(t[2 * i], t[2 * i + 1], a, r);
+                    products<T, 2, NI>(t[2 * i], t[2 * i + 1], a, r);
                 }
             }
 #pragma unroll
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 take<2>(a, q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
                 for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<2, NI>(x[0], x[1], a, r);
+                products<T, 2, NI>(x[0], x[1], a, r);
             }
             by_columns(x, f + F_REST + 16 * w, f[F_K] * is, lane);
             q.meet();
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 uint32_t a[NI][4], r[2][4];
                 take<NI>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
                 right_t<kChunk>(r[0], pimg, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], pimg + kSquare, 16 * kb, 16 * w, lane);
-                products<NI, 2>(t[0], t[1], a, r);
+                products<T, NI, 2>(t[0], t[1], a, r);
                 add(x, t, q.sc[12 + kb] * f[F_P]);
             }
             {
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 uint32_t a[2][4], r[2][4];
                 take<2>(a, q.mine + Sm::x(true) + kb * 1024, lane);
                 right_t<kChunk>(r[0], inv, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], inv + kSquare, 16 * kb, 16 * w, lane);
-                products<2, 2>(t[0], t[1], a, r);
+                products<T, 2, 2>(t[0], t[1], a, r);
                 add(y, t, q.sc[8 + kb] * f[F_INV]);
             }
             // beta grow dR likewise, from dU's and the inverse's largest
@@ -807,10 +807,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                     uint32_t r[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], qimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<2, NI>(t[2 * i], t[2 * i + 1], a, r);
+                    products<T, 2, NI>(t[2 * i], t[2 * i + 1], a, r);
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<2, NI>(u[2 * i], u[2 * i + 1], c, r);
+                    products<T, 2, NI>(u[2 * i], u[2 * i + 1], c, r);
                 }
             }
 #pragma unroll
@@ -997,20 +997,20 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + wn * 512, lane);
                     times<NI>(d, lo, factor[3]);
-                    products<NI, NO>(dp[0], dp[1], d, v);
+                    products<T, NI, NO>(dp[0], dp[1], d, v);
                     times<NO>(c, lr, factor[4]);
-                    products<NO, NO>(da[0], da[1], c, v);
+                    products<T, NO, NO>(da[0], da[1], c, v);
                 }
                 times<NI>(d, lo, factor[0]), times<NO>(c, lr, factor[1]), times<NO>(le, le, factor[2]);
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
 #pragma unroll
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + j * SR::state_term + (wn * NQ + i) * 512, lane);
-                    products<NI, NO>(aos[2 * i], aos[2 * i + 1], d, v);
-                    products<NO, NO>(ars[2 * i], ars[2 * i + 1], c, v);
+                    products<T, NI, NO>(aos[2 * i], aos[2 * i + 1], d, v);
+                    products<T, NO, NO>(ars[2 * i], ars[2 * i + 1], c, v);
 #pragma unroll
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], ya + j * SR::state_term + (wn * NQ + i) * 512, lane);
-                    products<NO, NO>(aeg[2 * i], aeg[2 * i + 1], le, v);
+                    products<T, NO, NO>(aeg[2 * i], aeg[2 * i + 1], le, v);
                 }
                 // <S0, G>: the diagonal of S0^T G, a block of eight channels to a warp
                 if (traces) {
@@ -1064,8 +1064,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                         left<KP>(c4[j], kimg + j * R::term, 16 * wm, 16 * kk, lane);
                         right<KP>(x[j], kimg + j * R::term, 16 * wn, 16 * kk, lane);
                     }
-                    products<NI, NI>(sq[0], sq[1], a, x);
-                    products<NI, NI>(sk[0], sk[1], c4, x);
+                    products<T, NI, NI>(sq[0], sq[1], a, x);
+                    products<T, NI, NI>(sk[0], sk[1], c4, x);
                 }
                 const float sp = ldexpf(1.0f, top[3]), sa = ldexpf(-1.0f, top[4]);
 #pragma unroll
@@ -1176,18 +1176,18 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
                         for (int j = 0; j < NI; ++j) right_t<KP>(x[j], kimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
                         if (kb <= wm) {
-                            products<NO, NI>(tq[2 * i], tq[2 * i + 1], a, x);
-                            products<NO, NI>(ta[2 * i], ta[2 * i + 1], c, x);
+                            products<T, NO, NI>(tq[2 * i], tq[2 * i + 1], a, x);
+                            products<T, NO, NI>(ta[2 * i], ta[2 * i + 1], c, x);
                         }
                         if (kb >= wm) {  // their columns
 #pragma unroll
                             for (int j = 0; j < NO; ++j) left_t<kChunk>(e[j], i_da + j * kSquare, 16 * kb, 16 * wm, lane);
-                            products<NO, NI>(ta[2 * i], ta[2 * i + 1], e, x);
+                            products<T, NO, NI>(ta[2 * i], ta[2 * i + 1], e, x);
 #pragma unroll
                             for (int j = 0; j < NO; ++j) left_t<kChunk>(e[j], i_dp + j * kSquare, 16 * kb, 16 * wm, lane);
 #pragma unroll
                             for (int j = 0; j < NI; ++j) right_t<KP>(x[j], qimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
-                            products<NO, NI>(tk[2 * i], tk[2 * i + 1], e, x);
+                            products<T, NO, NI>(tk[2 * i], tk[2 * i + 1], e, x);
                         }
                     }
                 }

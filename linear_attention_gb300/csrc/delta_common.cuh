@@ -143,17 +143,34 @@ __device__ __forceinline__ void clear(Acc (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.0f;
 }
-// Two 16 x 8 blocks += the left operand's LT terms times the RT terms of a right operand
-template <int LT, int RT>
+// Two 16 x 8 blocks += the left operand's LT terms times the RT terms of a right operand. The tensor cores cut a sum's last bits off at every
+// step; for float32 results (T) the step's sum is taken from zero, small terms first, and added in float32: a backward pass's errors
+// are 0.4e-6 instead of 1.1e-6 (2 x 777 rows, 3 heads of 40 x 75), where float32 products give 0.3e-6.
+template <typename T, int LT, int RT>
 __device__ __forceinline__ void products(Acc &x, Acc &y, const uint32_t (&a)[LT][4], const uint32_t (&b)[RT][4]) {
+    if constexpr (Terms<T>::in == 2) {
+        Acc s[2];
+        clear(s);
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
+        for (int j = RT - 1; j >= 0; --j)
 #pragma unroll
-        for (int i = 0; i < LT; ++i)
-            if (i + j < 2) {
-                mma(x, a[i], b[j][0], b[j][1]);
-                mma(y, a[i], b[j][2], b[j][3]);
-            }
+            for (int i = LT - 1; i >= 0; --i)
+                if (i + j < 2) {
+                    mma(s[0], a[i], b[j][0], b[j][1]);
+                    mma(s[1], a[i], b[j][2], b[j][3]);
+                }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += s[0][e], y[e] += s[1][e];
+    } else {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int i = 0; i < LT; ++i)
+                if (i + j < 2) {
+                    mma(x, a[i], b[j][0], b[j][1]);
+                    mma(y, a[i], b[j][2], b[j][3]);
+                }
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
