@@ -21,14 +21,14 @@ namespace {
 // ------------------------------------------------------------------------------------------------
 // What does not depend on the state
 // ------------------------------------------------------------------------------------------------
-constexpr int kPrepWarps = 4;
+constexpr int kPrepWarps = 8;
 constexpr int kLd = 68;  // floats in a row of the square matrices in shared memory
 
 template <typename T, int KP>
 struct PrepSmem {
     static constexpr int images = Rec<T, KP>::qk, work = (2 * kChunk * kLd + 32 * 36) * 4;
     static constexpr int shared = images > work ? images : work;  // the images, then the inverse's work in their place
-    static constexpr int bytes = shared + (3 * kChunk + 16) * 4;
+    static constexpr int bytes = shared + (8 * kChunk + 16) * 4;
 };
 
 // Rows of q or k into their images, in shared memory and in the record; returns the scale's inverse.
@@ -71,19 +71,22 @@ __device__ __forceinline__ float make_image(const Raw<T> (&raw)[prep_words(KP)],
     return inverse_of(s);
 }
 
-// C = sign A B for N x N blocks in shared memory, by `count` threads of which this is number i
+// C = sign A B for N x N blocks in shared memory, by `count` threads of which this is number i. A thread holds a column of B and takes rows of A that
+// its neighbours take too: a word of A serves a warp at once, where four results to a thread took five times the wavefronts.
 template <int N>
 __device__ __forceinline__ void small_product(float *c, int ldc, const float *a, int lda, const float *b, int ldb, float sign, int i, int count) {
-    for (int e = i * 4; e < N * N; e += count * 4) {
-        const int row = e / N, col = e % N;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int m = 0; m < N; ++m) {
-            const float x = a[row * lda + m];
-            const float4 y = *reinterpret_cast<const float4 *>(b + m * ldb + col);
-            s.x = fmaf(x, y.x, s.x), s.y = fmaf(x, y.y, s.y), s.z = fmaf(x, y.z, s.z), s.w = fmaf(x, y.w, s.w);
+    const int col = i % N;
+    float x[N];
+#pragma unroll
+    for (int m = 0; m < N; ++m) x[m] = b[m * ldb + col];
+    for (int row = i / N; row < N; row += count / N) {
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int m = 0; m < N; m += 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(a + row * lda + m);
+            s[0] = fmaf(y.x, x[m], s[0]), s[1] = fmaf(y.y, x[m + 1], s[1]), s[0] = fmaf(y.z, x[m + 2], s[0]), s[1] = fmaf(y.w, x[m + 3], s[1]);
         }
-        *reinterpret_cast<float4 *>(c + row * ldc + col) = make_float4(sign * s.x, sign * s.y, sign * s.z, sign * s.w);
+        c[row * ldc + col] = sign * (s[0] + s[1]);
     }
 }
 
@@ -98,7 +101,13 @@ __device__ __forceinline__ void invert(float *h, const float *m, float *w) {
         for (int i = 0; i < 16; ++i) {
             float s = 0.0f;
 #pragma unroll
-            for (int l = 0; l < i; ++l) s = fmaf(m[(block + i) * kLd + block + l], x[l], s);
+            for (int l = 0; l < i; l += 4) {
+                const float4 y = *reinterpret_cast<const float4 *>(m + (block + i) * kLd + block + l);
+                s = fmaf(y.x, x[l], s);
+                if (l + 1 < i) s = fmaf(y.y, x[l + 1], s);
+                if (l + 2 < i) s = fmaf(y.z, x[l + 2], s);
+                if (l + 3 < i) s = fmaf(y.w, x[l + 3], s);
+            }
             x[i] = i == j ? 1.0f : i < j ? 0.0f : -s;
         }
 #pragma unroll
@@ -106,11 +115,11 @@ __device__ __forceinline__ void invert(float *h, const float *m, float *w) {
     }
     __syncthreads();
     {
-        const int pair = tid / 64, a = 32 * pair, b = a + 16;
+        const int pair = tid / 128, a = 32 * pair, b = a + 16;
         float *const t = w + pair * 16 * 36;
-        small_product<16>(t, 36, m + b * kLd + a, kLd, h + a * kLd + a, kLd, 1.0f, tid % 64, 64);
+        small_product<16>(t, 36, m + b * kLd + a, kLd, h + a * kLd + a, kLd, 1.0f, tid % 128, 128);
         __syncthreads();
-        small_product<16>(h + b * kLd + a, kLd, h + b * kLd + b, kLd, t, 36, -1.0f, tid % 64, 64);
+        small_product<16>(h + b * kLd + a, kLd, h + b * kLd + b, kLd, t, 36, -1.0f, tid % 128, 128);
     }
     __syncthreads();
     small_product<32>(w, 36, m + 32 * kLd, kLd, h, kLd, 1.0f, tid, 32 * kPrepWarps);
@@ -119,15 +128,25 @@ __device__ __forceinline__ void invert(float *h, const float *m, float *w) {
     __syncthreads();
 }
 
+// A number as a float and what it is off by
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two plus(const Two &a, const Two &b) {
+    const float s = a.hi + b.hi, v = s - a.hi, e = (a.hi - (s - v)) + (b.hi - v) + (a.lo + b.lo), h = s + e;
+    return {h, e - (h - s)};
+}
+
 // One chunk of one key head, and all value heads that share it.
 template <typename T, int KP, bool BWD>
-__global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(DeltaParams p) {
+__global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based_delta_prep_kernel(DeltaParams p) {
     using R = Rec<T, KP>;
     using Sm = PrepSmem<T, KP>;
     constexpr int NI = Terms<T>::in, NP = R::scores(BWD);
     extern __shared__ __align__(128) uint8_t smem[];
     float *const m = reinterpret_cast<float *>(smem), *const h = m + kChunk * kLd, *const w = h + kChunk * kLd;
-    float *const bhi = reinterpret_cast<float *>(smem + Sm::shared), *const blo = bhi + kChunk, *const beta = blo + kChunk, *const red = beta + kChunk;
+    float *const bhi = reinterpret_cast<float *>(smem + Sm::shared), *const blo = bhi + kChunk, *const beta = blo + kChunk, *const till = beta + kChunk,
+                *const since = till + kChunk, *const red = since + 4 * kChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK;
     griddep_wait();
@@ -142,42 +161,47 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
         const auto scan = [&](int head) {
             if (warp != 0) return;
             float *const f = reinterpret_cast<float *>(record(head) + (2 + NP) * kSquare);
-            // Sums of log decays in 64 bits, kept as two floats: differences of neighbours then have float32's relative
+            // Sums of log decays as two floats each (64-bit floats are slow here): differences of neighbours then have float32's relative
             // accuracy however much has decayed before. -1e5 stands for anything below it, -inf among it: its decay is 0.
-            double x[2], be[2];
+            Two x[2];
+            float be[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                float v = 0.0f, y = 0.0f;
+                float v = 0.0f;
+                be[e] = 0.0f;
                 if (i < rows) {
                     if (p.gate) v = to_f32(static_cast<const T *>(p.gate)[b * p.gate_sb + (t0 + i) * p.gate_st + head]);
-                    y = to_f32(static_cast<const T *>(p.beta)[b * p.beta_sb + (t0 + i) * p.beta_st + head]);
+                    be[e] = to_f32(static_cast<const T *>(p.beta)[b * p.beta_sb + (t0 + i) * p.beta_st + head]);
                 }
-                x[e] = v < -1e5f ? -1e5 : static_cast<double>(v), be[e] = y;
+                x[e] = {v < -1e5f ? -1e5f : v, 0.0f};
             }
-            x[1] += x[0];
-            double sum = x[1];
+            x[1] = plus(x[0], x[1]);
+            Two sum = x[1];
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
-                const double o = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += o;
+                const Two o = {__shfl_up_sync(0xffffffffu, sum.hi, d), __shfl_up_sync(0xffffffffu, sum.lo, d)};
+                if (lane >= d) sum = plus(o, sum);
             }
-            const double before = sum - x[1];
-            const double last = __shfl_sync(0xffffffffu, sum, 31);
+            Two before = {__shfl_up_sync(0xffffffffu, sum.hi, 1), __shfl_up_sync(0xffffffffu, sum.lo, 1)};
+            if (lane == 0) before = {0.0f, 0.0f};
+            const Two last = {__shfl_sync(0xffffffffu, sum.hi, 31), __shfl_sync(0xffffffffu, sum.lo, 31)};
+            // the sum up to the last of each 16 rows
+            const Two end = {__shfl_sync(0xffffffffu, sum.hi, lane | 7), __shfl_sync(0xffffffffu, sum.lo, lane | 7)};
             float most = 0.0f, grow_most = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = 2 * lane + e;
-                const double v = before + x[e];
-                const float grow = expf(static_cast<float>(v)), rest = expf(static_cast<float>(last - v)), y = static_cast<float>(be[e]);
-                bhi[i] = static_cast<float>(v), blo[i] = static_cast<float>(v - bhi[i]), beta[i] = y;
-                f[F_GROW + i] = grow, f[F_REST + i] = rest, f[F_BETA + i] = y, f[F_BHI + i] = bhi[i], f[F_BLO + i] = blo[i];
+                const Two v = plus(before, x[e]);
+                const float grow = expf(v.hi + v.lo), rest = expf((last.hi - v.hi) + (last.lo - v.lo)), y = be[e];
+                bhi[i] = v.hi, blo[i] = v.lo, beta[i] = y, till[i] = expf((end.hi - v.hi) + (end.lo - v.lo));
+                f[F_GROW + i] = grow, f[F_REST + i] = rest, f[F_BETA + i] = y, f[F_BHI + i] = v.hi, f[F_BLO + i] = v.lo;
                 f[F_BF + i] = y * (BWD ? grow : rest);
                 most = fmaxf(most, fabsf(y * (BWD ? grow : rest))), grow_most = fmaxf(grow_most, grow);
             }
             most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
             grow_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(grow_most)));
-            if (lane == 0) f[F_WHOLE] = expf(static_cast<float>(last)), f[F_BFMOST] = most, f[F_GROWMOST] = grow_most;
+            if (lane == 0) f[F_WHOLE] = expf(last.hi + last.lo), f[F_BFMOST] = most, f[F_GROWMOST] = grow_most;
         };
         __syncthreads();  // the batch entry before
         float ik, iq;
@@ -197,25 +221,27 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
             iq = make_image<T, KP>(raw, smem + R::img, rec + R::img, red);
         }
         __syncthreads();
-        // the products of keys with keys and queries: rows 16 warp .. + 15, columns up to the diagonal
-        Acc sk[8], sq[8];
+        // the products of keys with keys and queries: a warp has 16 rows and 32 columns, up to the diagonal
+        const int wm = warp & 3, wn = warp >> 2;
+        Acc sk[4], sq[4];
         clear(sk), clear(sq);
         {
             const uint32_t kimg = smem_u32(smem), qimg = kimg + R::img;
 #pragma unroll
             for (int kk = 0; kk < KP / 16; ++kk) {
+                if (2 * wn > wm) continue;
                 uint32_t a[NI][4], c[NI][4];
 #pragma unroll
                 for (int j = 0; j < NI; ++j) {
-                    left<KP>(a[j], kimg + j * R::term, 16 * warp, 16 * kk, lane);
-                    left<KP>(c[j], qimg + j * R::term, 16 * warp, 16 * kk, lane);
+                    left<KP>(a[j], kimg + j * R::term, 16 * wm, 16 * kk, lane);
+                    left<KP>(c[j], qimg + j * R::term, 16 * wm, 16 * kk, lane);
                 }
 #pragma unroll
-                for (int np = 0; np < 4; ++np) {
-                    if (np > warp) continue;
+                for (int np = 0; np < 2; ++np) {
+                    if (2 * wn + np > wm) continue;
                     uint32_t x[NI][4];
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 16 * np, 16 * kk, lane);
+                    for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 32 * wn + 16 * np, 16 * kk, lane);
                     products<T, NI, NI>(sk[2 * np], sk[2 * np + 1], a, x);
                     products<T, NI, NI>(sq[2 * np], sq[2 * np + 1], c, x);
                 }
@@ -232,62 +258,79 @@ __global__ void __launch_bounds__(32 * kPrepWarps, 4) based_delta_prep_kernel(De
             __syncthreads();  // the sums, and the images are done with
             if (!hh)
                 for (int i = tid; i < kChunk * kLd / 4; i += 32 * kPrepWarps) reinterpret_cast<float4 *>(h)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            Acc pv[8];
+            {  // decays since the last of each 16 rows
+                const int i = tid & 63, end = 16 * (tid >> 6) + 15;
+                since[tid] = expf((bhi[i] - bhi[end]) + (blo[i] - blo[end]));
+            }
+            __syncthreads();
+            Acc pv[4];
             float most = 0.0f;
             {
-                const int r0 = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);
+                const int r0 = 16 * wm + (lane >> 2), c0 = 32 * wn + 2 * (lane & 3);
                 const float hi[2] = {bhi[r0], bhi[r0 + 8]}, lo[2] = {blo[r0], blo[r0 + 8]}, bi[2] = {beta[r0], beta[r0 + 8]};
 #pragma unroll
-                for (int nt = 0; nt < 8; ++nt) {
-                    if (nt > 2 * warp + 1) {  // above the diagonal
+                for (int nt = 0; nt < 4; ++nt) {
+                    const int block = 2 * wn + nt / 2, c = c0 + 8 * nt;
+                    if (block > wm) {  // above the diagonal
 #pragma unroll
                         for (int e = 0; e < 4; ++e) pv[nt][e] = 0.0f;
                         continue;
                     }
-                    const float2 jh = *reinterpret_cast<const float2 *>(bhi + 8 * nt + c0), jl = *reinterpret_cast<const float2 *>(blo + 8 * nt + c0),
-                                 jb = *reinterpret_cast<const float2 *>(beta + 8 * nt + c0);
+                    const float2 jb = *reinterpret_cast<const float2 *>(beta + c);
+                    float d[4];
+                    if (block < wm) {  // D_ij by the last row of j's 16: two factors
+                        const float2 t = *reinterpret_cast<const float2 *>(till + c);
+                        const float s0 = since[64 * block + r0], s1 = since[64 * block + r0 + 8];
+                        d[0] = s0 * t.x, d[1] = s0 * t.y, d[2] = s1 * t.x, d[3] = s1 * t.y;
+                    } else {
+                        const float2 jh = *reinterpret_cast<const float2 *>(bhi + c), jl = *reinterpret_cast<const float2 *>(blo + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = (hi[e / 2] - (e % 2 ? jh.y : jh.x)) + (lo[e / 2] - (e % 2 ? jl.y : jl.x));
+                            d[e] = c + e % 2 <= r0 + 8 * (e / 2) ? expf(x) : 0.0f;
+                        }
+                    }
                     float y[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = r0 + 8 * (e / 2), j = 8 * nt + c0 + e % 2;
-                        const float d = j <= i ? expf((hi[e / 2] - (e % 2 ? jh.y : jh.x)) + (lo[e / 2] - (e % 2 ? jl.y : jl.x))) : 0.0f;
+                        const int i = r0 + 8 * (e / 2), j = c + e % 2;
                         const float bj = e % 2 ? jb.y : jb.x;
-                        pv[nt][e] = j <= i ? d * (sq[nt][e] * fq) * (BWD ? 1.0f : bj) : 0.0f;
-                        y[e] = j < i ? d * (sk[nt][e] * fk) * (BWD ? bi[e / 2] : bj) : 0.0f;
+                        pv[nt][e] = j <= i ? d[e] * (sq[nt][e] * fq) * (BWD ? 1.0f : bj) : 0.0f;
+                        y[e] = j < i ? d[e] * (sk[nt][e] * fk) * (BWD ? bi[e / 2] : bj) : 0.0f;
                         most = fmaxf(most, fabsf(pv[nt][e]));
                     }
-                    float *const to = m + r0 * kLd + 8 * nt + c0;
+                    float *const to = m + r0 * kLd + c;
                     *reinterpret_cast<float2 *>(to) = make_float2(y[0], y[1]);
                     *reinterpret_cast<float2 *>(to + 8 * kLd) = make_float2(y[2], y[3]);
                 }
             }
             const float sp = scale_for(cta_most<kPrepWarps>(most, red));  // with a barrier
 #pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
+            for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     uint32_t x[NP];
                     terms<NP>(pv[nt][2 * e] * sp, pv[nt][2 * e + 1] * sp, x);
-                    const uint32_t at = word_at<kChunk>(16 * warp + (lane >> 2) + 8 * e, nt) + 4 * (lane & 3);
+                    const uint32_t at = word_at<kChunk>(16 * wm + (lane >> 2) + 8 * e, 4 * wn + nt) + 4 * (lane & 3);
 #pragma unroll
                     for (int j = 0; j < NP; ++j) *reinterpret_cast<uint32_t *>(g + (2 + j) * kSquare + at) = x[j];
                 }
             invert(h, m, w);
-            float x[4][8];
+            float x[2][8];
             most = 0.0f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 *const from = reinterpret_cast<const float4 *>(h + (tid / 8 + 16 * r) * kLd + tid % 8 * 8);
+            for (int r = 0; r < 2; ++r) {
+                const float4 *const from = reinterpret_cast<const float4 *>(h + (tid / 8 + 32 * r) * kLd + tid % 8 * 8);
                 const float4 u = from[0], v = from[1];
                 x[r][0] = u.x, x[r][1] = u.y, x[r][2] = u.z, x[r][3] = u.w, x[r][4] = v.x, x[r][5] = v.y, x[r][6] = v.z, x[r][7] = v.w;
                 most = most8(most, x[r]);
             }
             const float sh = scale_for(cta_most<kPrepWarps>(most, red));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 uint4 z[2];
                 words_of<2>(z, x[r], sh);
-                const uint32_t at = word_at<kChunk>(tid / 8 + 16 * r, tid % 8);
+                const uint32_t at = word_at<kChunk>(tid / 8 + 32 * r, tid % 8);
                 *reinterpret_cast<uint4 *>(g + at) = z[0], *reinterpret_cast<uint4 *>(g + kSquare + at) = z[1];
             }
             if (tid == 0) f[F_INV] = inverse_of(sh), f[F_P] = inverse_of(sp), f[F_K] = ik, f[F_Q] = iq;
