@@ -357,7 +357,7 @@ struct SeqSmem {
                          w = u + 4096;
     __host__ __device__ static constexpr int x(bool bwd) { return bwd ? state : w; }
     static constexpr int scales = w + 4096, slice = scales + 128 + 8 * tile;
-    static constexpr int bytes(bool bwd, int slices) { return 2 * stage(bwd) + slices * slice; }
+    static constexpr int bytes(bool bwd, int slices) { return 2 * stage(bwd) + slices * slice + 16; }
     // Slices of a CTA, at most: 512 threads, and what shared memory holds
     static constexpr int most(bool bwd) { return bytes(bwd, 4) <= 227 * 1024 ? 4 : bytes(bwd, 3) <= 227 * 1024 ? 3 : bytes(bwd, 2) <= 227 * 1024 ? 2 : 1; }
 };
@@ -512,12 +512,53 @@ __device__ __forceinline__ void leave(uint8_t *to, int term, const uint32_t (&a)
         for (int r = 0; r < 4; ++r) *reinterpret_cast<uint32_t *>(to + j * term + r * 128 + lane * 4) = a[j][r];
 }
 
-// The records of a chunk, by all threads of the CTA
-__device__ __forceinline__ void copy_records(uint8_t *to, const uint8_t *qk, int qk_bytes, const uint8_t *g, int g_bytes) {
-    const uint32_t at = smem_u32(to);
-    for (int i = threadIdx.x * 16; i < qk_bytes; i += blockDim.x * 16) copy16(at + i, qk + i);
-    for (int i = threadIdx.x * 16; i < g_bytes; i += blockDim.x * 16) copy16(at + qk_bytes + i, g + i);
-}
+// Records come by bulk copies that one thread issues (as 16-byte copies of all threads they took 1250 of a chunk's 4200 cycles where one slice
+// has an SM to itself: 1 x 16384, 16 heads of 128 x 128). A barrier counts a stage's bytes, and all threads wait for it.
+__device__ unsigned int g_delta_status;  // bit 0: a wait for records gave up
+constexpr uint64_t kDeltaWaitNs = 1000000000ull;
+
+struct Stages {
+    uint32_t bars;  // one of eight bytes for each stage
+    uint32_t late = 0, parities = 0;  // stages whose copies were given up, and the phases they belong to
+
+    __device__ __forceinline__ void begin(uint8_t *at, int count) {
+        bars = smem_u32(at);
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < count; ++i) mbar_init(bars + 8 * i, 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    // Two records, one behind the other, by thread 0. Nobody reads the stage any more, and its last copy has been waited for.
+    __device__ __forceinline__ void copy(int stage, uint8_t *to, const uint8_t *a, int a_bytes, const uint8_t *b, int b_bytes) const {
+        if (threadIdx.x != 0) return;
+        const uint32_t bar = bars + 8 * stage, at = smem_u32(to);
+        mbar_arrive_expect_tx(bar, a_bytes + b_bytes);
+        bulk_copy(at, a, a_bytes, bar);
+        if (b_bytes) bulk_copy(at + a_bytes, b, b_bytes, bar);
+    }
+    // A wait that gives up (a second: the copy has not come) sets the status word; later ones look only once, so that the kernel ends.
+    __device__ __forceinline__ void wait(int stage, int parity) {
+        if (mbar_try_wait(bars + 8 * stage, parity)) return;
+        if (late || !come(stage, parity)) late |= 1u << stage, parities = (parities & ~(1u << stage)) | static_cast<uint32_t>(parity) << stage;
+    }
+    // Before the CTA ends: what was given up may still be on its way into its shared memory
+    __device__ __forceinline__ void end() const {
+        if (late)
+            for (int i = 0; i < 8; ++i)
+                if (late >> i & 1) come(i, parities >> i & 1);
+    }
+    __device__ __noinline__ bool come(int stage, int parity) const {
+        const uint64_t began = global_timer_ns();
+        while (!mbar_try_wait(bars + 8 * stage, parity)) {
+            if (global_timer_ns() - began > kDeltaWaitNs) {
+                atomicOr(&g_delta_status, 1u);
+                return false;
+            }
+        }
+        return true;
+    }
+};
 
 // What both directions have in common: this warp's place, and the parts of shared memory
 template <typename T, int KP, bool BWD>
@@ -580,6 +621,9 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
     extern __shared__ __align__(128) uint8_t smem[];
     const Q q(p, smem);
     const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
+    Stages stages;
+    stages.begin(smem + 2 * kStage + blockDim.x / kQuad * Sm::slice, 2);
+    int turn = 0;  // chunks up to this batch entry
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int live = live_rows(p, b), count = (live + kChunk - 1) / kChunk;
@@ -589,9 +633,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
         T *const o = static_cast<T *>(p.out) + (first * p.H + head) * p.V + v0;
         const auto record = [&](int n) { return p.saved ? p.saved + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::fwd : nullptr; };
         const auto fetch = [&](int n) {
-            copy_records(smem + (n & 1) * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, g + static_cast<int64_t>(n) * R::g(false), R::g(false));
+            const int at = turn + n & 1;
+            stages.copy(at, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, g + static_cast<int64_t>(n) * R::g(false), R::g(false));
             const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
-            if (cols > 0) load_tile(q.tiles + (n & 1) * Sm::tile, t < live ? v + t * p.v_st : v, p.v_st, static_cast<int>(live - t), cols, p.v_vec, lane);
+            if (cols > 0) load_tile(q.tiles + at * Sm::tile, t < live ? v + t * p.v_st : v, p.v_st, static_cast<int>(live - t), cols, p.v_vec, lane);
             copies_commit();
         };
         Acc s[2 * kSteps];
@@ -603,14 +648,16 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             q.begin(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
         }
         for (int n = 0; n < count; ++n) {
+            const int stage = turn + n & 1;
             copies_wait<0>();
+            stages.wait(stage, turn + n >> 1 & 1);
             __syncthreads();  // chunk n and the state's operands are there, and chunk n - 1 is done with
             if (n + 1 < count) fetch(n + 1);
             if (cols <= 0) continue;  // the same for the slice's warps
             const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;  // this warp's first row
-            uint8_t *const tile = q.tiles + (n & 1) * Sm::tile;
-            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
-            const float *const f = reinterpret_cast<const float *>(smem + (n & 1) * kStage + R::qk + (2 + NO) * kSquare);
+            uint8_t *const tile = q.tiles + stage * Sm::tile;
+            const uint32_t kimg = smem_u32(smem) + stage * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
+            const float *const f = reinterpret_cast<const float *>(smem + stage * kStage + R::qk + (2 + NO) * kSquare);
             uint8_t *const rec = record(n);
             Acc x[2], z[2], y[2];  // S0^T K^T, S0^T Q^T
             clear(x), clear(z);
@@ -708,12 +755,14 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 store_tile<T>(o + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
             }
         }
+        turn += count;
         if (cols > 0) {
             for (int64_t t = static_cast<int64_t>(count) * kChunk + 16 * w; t < p.T; t += kChunk)
                 store_tile<T>(o + t * row_o, row_o, q.tiles, 0, static_cast<int>(p.T - t), cols, p.o_vec, lane);
             if (p.final_state) write_state(p.final_state + st * p.K * p.V, s, w * (KP / 4), p.K, p.V, v0, lane);
         }
     }
+    stages.end();
 }
 
 template <typename T, int KP>
@@ -726,6 +775,9 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
     extern __shared__ __align__(128) uint8_t smem[];
     const Q q(p, smem);
     const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
+    Stages stages;
+    stages.begin(smem + 2 * kStage + blockDim.x / kQuad * Sm::slice, 2);
+    int turn = 0;  // chunks up to this batch entry
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int live = live_rows(p, b), count = (live + kChunk - 1) / kChunk;
@@ -735,9 +787,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
         T *const dv = static_cast<T *>(p.out) + (first * p.H + head) * p.V + v0;
         const auto record = [&](int n) { return p.slice_rec + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::bwd; };
         const auto fetch = [&](int n) {
-            copy_records(smem + (n & 1) * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, grec + static_cast<int64_t>(n) * R::g(true), R::g(true));
+            const int at = turn + count - 1 - n & 1;
+            stages.copy(at, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, grec + static_cast<int64_t>(n) * R::g(true), R::g(true));
             const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
-            if (cols > 0) load_tile(q.tiles + (n & 1) * Sm::tile, t < live ? dout + t * p.do_st : dout, p.do_st, static_cast<int>(live - t), cols, p.do_vec, lane);
+            if (cols > 0) load_tile(q.tiles + at * Sm::tile, t < live ? dout + t * p.do_st : dout, p.do_st, static_cast<int>(live - t), cols, p.do_vec, lane);
             copies_commit();
         };
         Acc g[2 * kSteps];
@@ -748,14 +801,16 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             if (cols > 0) q.begin(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
         }
         for (int n = count - 1; n >= 0; --n) {
+            const int stage = turn + count - 1 - n & 1;
             copies_wait<0>();
+            stages.wait(stage, turn + count - 1 - n >> 1 & 1);
             __syncthreads();
             if (n > 0) fetch(n - 1);
             if (cols <= 0) continue;
             const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;
-            uint8_t *const tile = q.tiles + (n & 1) * Sm::tile;
-            const uint32_t kimg = smem_u32(smem) + (n & 1) * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
-            const float *const f = reinterpret_cast<const float *>(smem + (n & 1) * kStage + R::qk + 4 * kSquare);
+            uint8_t *const tile = q.tiles + stage * Sm::tile;
+            const uint32_t kimg = smem_u32(smem) + stage * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
+            const float *const f = reinterpret_cast<const float *>(smem + stage * kStage + R::qk + 4 * kSquare);
             uint8_t *const rec = record(n);
             float *const rec_scales = reinterpret_cast<float *>(rec + SR::bwd_scales);
             Acc x[2], y[2];
@@ -869,12 +924,14 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 store_tile<T>(dv + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
             }
         }
+        turn += count;
         if (cols > 0) {
             for (int64_t t = static_cast<int64_t>(count) * kChunk + 16 * w; t < p.T; t += kChunk)
                 store_tile<T>(dv + t * row_o, row_o, q.tiles, 0, static_cast<int>(p.T - t), cols, p.o_vec, lane);
             if (p.final_state) write_state(p.final_state + st * p.K * p.V, g, w * (KP / 4), p.K, p.V, v0, lane);
         }
     }
+    stages.end();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -896,7 +953,7 @@ struct GradSmem {
     static constexpr int stages = Terms<T>::out == 1 ? 4 : 3, stage = SR::fwd + SR::bwd;
     static constexpr int f = Rec<T, KP>::qk, ring = f + F_COUNT * 4, dp = ring + stages * stage, da = dp + Terms<T>::out * kSquare,
                          part = da + Terms<T>::out * kSquare;  // sums: rows 4 x 64, next 4 x 64, columns 4 x 64, dbeta 64
-    static constexpr int red = part + 13 * kChunk * 4, bytes = red + 2 * kGradWarps * 4;
+    static constexpr int red = part + 13 * kChunk * 4, bars = red + 2 * kGradWarps * 4, bytes = bars + 8 * (stages + 1);
 };
 
 // Two neighbouring elements of an image of key or query rows
@@ -959,6 +1016,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
     float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 4 * kChunk,
                 *const part_col = part_next + 4 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
     const uint32_t base = smem_u32(smem), kimg = base, qimg = base + R::img;
+    constexpr int kKeysStage = Sm::stages;  // the stage of the queries' and keys' images
+    Stages stages;
+    stages.begin(smem + Sm::bars, Sm::stages + 1);
+    int turn = 0, entry = 0;  // slices and batch entries up to this one
     griddep_wait();
     for (int b = blockIdx.z; b < p.B; b += gridDim.z) {
         const int64_t t0 = static_cast<int64_t>(n) * kChunk, first = static_cast<int64_t>(b) * p.T + t0;
@@ -977,7 +1038,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
         }
         if (rows <= 0) continue;
         __syncthreads();  // the batch entry before
-        copy_records(smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
+        stages.copy(kKeysStage, smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
         Acc aq[2 * NQ], ak[2 * NQ];
         clear(aq), clear(ak);
         for (int hh = 0; hh < group; ++hh) {
@@ -986,10 +1047,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             const int64_t at0 = ((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices;
             const uint8_t *const fwd = p.saved + at0 * SR::fwd, *const bwd = p.slice_rec + at0 * SR::bwd;
             const auto fetch = [&](int sl) {
+                const int at = (turn + sl) % Sm::stages;
                 if (sl < slices)
-                    copy_records(smem + Sm::ring + sl % Sm::stages * Sm::stage, fwd + static_cast<int64_t>(sl) * SR::fwd, SR::fwd,
-                                 bwd + static_cast<int64_t>(sl) * SR::bwd, SR::bwd);
-                copies_commit();
+                    stages.copy(at, smem + Sm::ring + at * Sm::stage, fwd + static_cast<int64_t>(sl) * SR::fwd, SR::fwd,
+                                bwd + static_cast<int64_t>(sl) * SR::bwd, SR::bwd);
             };
             __syncthreads();  // the head before
             for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
@@ -1017,10 +1078,11 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             Acc diagonal[1];
             clear(aos), clear(ars), clear(aeg), clear(dp), clear(da), clear(diagonal);
             for (int sl = 0; sl < slices; ++sl) {
-                copies_wait<Sm::stages - 2>();
+                const int at = (turn + sl) % Sm::stages;
+                stages.wait(at, (turn + sl) / Sm::stages & 1);
                 __syncthreads();  // the slice is there, and the one whose place comes next is done with
                 fetch(sl + Sm::stages - 1);
-                const uint8_t *const x = smem + Sm::ring + sl % Sm::stages * Sm::stage, *const y = x + SR::fwd;
+                const uint8_t *const x = smem + Sm::ring + at * Sm::stage, *const y = x + SR::fwd;
                 if (sl % 32 == 0) {
                     int e[6] = {};
                     if (sl + lane < slices) exponents(e, sl + lane);
@@ -1066,6 +1128,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                         for (int i = 0; i + j < NO; ++i) mma(diagonal[0], c[i], half ? v[j][2] : v[j][0], half ? v[j][3] : v[j][1]);
                 }
             }
+            turn += slices;
+            if (hh == 0) stages.wait(kKeysStage, entry & 1);
             float dot = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -1237,6 +1301,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 add(aq, tq, mp * ik), add(ak, tk, mp * iq), add(ak, ta, ma);
             }
         }
+        ++entry;
 #pragma unroll
         for (int i = 0; i < 2 * NQ; ++i)
 #pragma unroll
@@ -1247,6 +1312,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 store_pair(dk + row * row_k, c, p.K, p.K % 2 == 0, ak[i][2 * e], ak[i][2 * e + 1]);
             }
     }
+    stages.end();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -1493,6 +1559,15 @@ int launch_delta_step(const DeltaStepParams &p, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t delta_status(unsigned int *status, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_delta_status, sizeof(unsigned int));
+    if (e == cudaSuccess && clear && *status) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_delta_status, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
 }  // namespace based
 
 extern "C" {

@@ -634,6 +634,9 @@ int based_device_status(int device, unsigned int *status, int clear) {
     unsigned int scan = 0;
     if (e == cudaSuccess) e = based::scan_status(&scan, clear != 0);
     if (e == cudaSuccess && scan && !*status) *status = 1u | (64u << 8);  // the recurrence's cluster exchange: site 64
+    unsigned int delta = 0;
+    if (e == cudaSuccess) e = based::delta_status(&delta, clear != 0);
+    if (e == cudaSuccess && delta && !*status) *status = 1u | (65u << 8);  // the delta rule's records: site 65
     if (device != prev) cudaSetDevice(prev);
     if (e != cudaSuccess) return cuda_fail(e, "status word");
     return BASED_OK;

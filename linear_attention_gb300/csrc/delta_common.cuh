@@ -243,6 +243,13 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// bytes (a multiple of 16, as both addresses are), counted on a barrier
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
 // Eight elements at p as they lie there, of which the first n exist; the others are zero. words: p is on 16 bytes and n is at least 8, or 0 or less (in
 // float32 also 4). The loads of several calls go out together; the conversion comes after.
 template <typename T>

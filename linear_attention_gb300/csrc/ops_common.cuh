@@ -17,6 +17,8 @@ int host_cuda_fail(cudaError_t e, const char *what);
 int host_device(int *sms);  // checks that the current device is an sm_103 GPU
 // defined in based_scan.cu: the current device's status word of the scan kernels
 cudaError_t scan_status(unsigned int *status, bool clear);
+// defined in based_delta.cu: that of the delta rule's kernels
+cudaError_t delta_status(unsigned int *status, bool clear);
 
 #define OPS_CUDA(call)                                            \
     do {                                                          \
