@@ -13,6 +13,8 @@
 //     G' = grow_last G + scale (grow Q)^T dO - (beta grow K)^T dR
 // runs through the chunks from the last (based_delta_bwd_kernel), and what is left is again for all chunks at once
 // (based_delta_grad_kernel, where its formulas are).
+#include <cmath>
+
 #include "delta_common.cuh"
 
 namespace based {
@@ -662,16 +664,21 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             Acc x[2], z[2], y[2];  // S0^T K^T, S0^T Q^T
             clear(x), clear(z);
             const float is = q.sc[4], before = q.state_most();
+            {
+                uint32_t a[2][2][4], r[2][NI][4], c[2][NI][4];
+                const auto load = [&](int kk) {
+                    take<2>(a[kk & 1], q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
-            for (int kk = 0; kk < KP / 16; ++kk) {
-                uint32_t a[2][4], r[NI][4];
-                take<2>(a, q.mine + Sm::state + kk * 1024, lane);
+                    for (int j = 0; j < NI; ++j)
+                        right<KP>(r[kk & 1][j], kimg + j * R::term, 16 * w, 16 * kk, lane), right<KP>(c[kk & 1][j], qimg + j * R::term, 16 * w, 16 * kk, lane);
+                };
+                load(0);
 #pragma unroll
-                for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<T, 2, NI>(x[0], x[1], a, r);
-#pragma unroll
-                for (int j = 0; j < NI; ++j) right<KP>(r[j], qimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<T, NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a), r);
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    if (kk + 1 < KP / 16) load(kk + 1);  // a step ahead: often a warp has its scheduler to itself
+                    products<T, 2, NI>(x[0], x[1], a[kk & 1], r[kk & 1]);
+                    products<T, NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a[kk & 1]), c[kk & 1]);
+                }
             }
             by_columns(x, f + F_GROW + 16 * w, f[F_K] * is, lane);
             by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale * is, lane);
@@ -689,16 +696,22 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             }
             q.meet();
             clear(y);  // E
+            {
+                uint32_t a[2][2][4], r[2][2][4];
+                const auto load = [&](int kb) {
+                    take<2>(a[kb & 1], q.mine + Sm::x(false) + kb * 1024, lane);
+                    right<kChunk>(r[kb & 1][0], inv, 16 * w, 16 * kb, lane), right<kChunk>(r[kb & 1][1], inv + kSquare, 16 * w, 16 * kb, lane);
+                };
+                load(0);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb > w) continue;
-                Acc t[2];
-                clear(t);
-                uint32_t a[2][4], r[2][4];
-                take<2>(a, q.mine + Sm::x(false) + kb * 1024, lane);
-                right<kChunk>(r[0], inv, 16 * w, 16 * kb, lane), right<kChunk>(r[1], inv + kSquare, 16 * w, 16 * kb, lane);
-                products<T, 2, 2>(t[0], t[1], a, r);
-                add(y, t, q.sc[8 + kb] * f[F_INV]);
+                for (int kb = 0; kb < 4; ++kb) {
+                    if (kb > w) break;
+                    if (kb < 3) load(kb + 1);  // (of the last one nothing comes)
+                    Acc t[2];
+                    clear(t);
+                    products<T, 2, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
+                    add(y, t, q.sc[8 + kb] * f[F_INV]);
+                }
             }
             // All warps scale E and U for the same bounds, from X's and the inverse's largest, so that sums run over all rows
             const float e_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
@@ -715,30 +728,41 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             }
             q.meet();
             clear(x);
+            {
+                uint32_t a[2][NO][4], r[2][NO][4];
+                const auto load = [&](int kb) {
+                    take<NO>(a[kb & 1], q.mine + Sm::e + kb * Sm::e_block, lane);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb > w) continue;
-                uint32_t a[NO][4], r[NO][4];
-                take<NO>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
+                    for (int j = 0; j < NO; ++j) right<kChunk>(r[kb & 1][j], pimg + j * kSquare, 16 * w, 16 * kb, lane);
+                };
+                load(0);
 #pragma unroll
-                for (int j = 0; j < NO; ++j) right<kChunk>(r[j], pimg + j * kSquare, 16 * w, 16 * kb, lane);
-                products<T, NO, NO>(x[0], x[1], a, r);
+                for (int kb = 0; kb < 4; ++kb) {
+                    if (kb > w) break;
+                    if (kb < 3) load(kb + 1);
+                    products<T, NO, NO>(x[0], x[1], a[kb & 1], r[kb & 1]);
+                }
             }
             add(z, x, inverse_of(se) * f[F_P]);
             // S = whole S0 + K^T U, this warp's quarter
             const float whole = f[F_WHOLE], ik = f[F_K], iu = inverse_of(su) * ik;
             Acc t[2 * kSteps];
             clear(t);
+            {
+                uint32_t a[2][2][4], r[2][kSteps][NI][4];
+                const auto load = [&](int kb) {
+                    take<2>(a[kb & 1], q.mine + Sm::u + kb * 1024, lane);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                uint32_t a[2][4];
-                take<2>(a, q.mine + Sm::u + kb * 1024, lane);
+                    for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    uint32_t r[NI][4];
+                        for (int j = 0; j < NI; ++j) right_t<KP>(r[kb & 1][i][j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
+                };
+                load(0);
 #pragma unroll
-                    for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<T, 2, NI>(t[2 * i], t[2 * i + 1], a, r);
+                for (int kb = 0; kb < 4; ++kb) {
+                    if (kb < 3) load(kb + 1);
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) products<T, 2, NI>(t[2 * i], t[2 * i + 1], a[kb & 1], r[kb & 1][i]);
                 }
             }
 #pragma unroll
@@ -825,26 +849,38 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             }
             clear(x);  // dU
             const float is = q.sc[4], behind = q.state_most();
+            {
+                uint32_t a[2][2][4], r[2][NI][4];
+                const auto load = [&](int kk) {
+                    take<2>(a[kk & 1], q.mine + Sm::state + kk * 1024, lane);
 #pragma unroll
-            for (int kk = 0; kk < KP / 16; ++kk) {
-                uint32_t a[2][4], r[NI][4];
-                take<2>(a, q.mine + Sm::state + kk * 1024, lane);
+                    for (int j = 0; j < NI; ++j) right<KP>(r[kk & 1][j], kimg + j * R::term, 16 * w, 16 * kk, lane);
+                };
+                load(0);
 #pragma unroll
-                for (int j = 0; j < NI; ++j) right<KP>(r[j], kimg + j * R::term, 16 * w, 16 * kk, lane);
-                products<T, 2, NI>(x[0], x[1], a, r);
+                for (int kk = 0; kk < KP / 16; ++kk) {
+                    if (kk + 1 < KP / 16) load(kk + 1);
+                    products<T, 2, NI>(x[0], x[1], a[kk & 1], r[kk & 1]);
+                }
             }
             by_columns(x, f + F_REST + 16 * w, f[F_K] * is, lane);
             q.meet();
+            {  // (from the last rows up: all warps have those)
+                uint32_t a[2][NI][4], r[2][2][4];
+                const auto load = [&](int kb) {
+                    take<NI>(a[kb & 1], q.mine + Sm::e + kb * Sm::e_block, lane);
+                    right_t<kChunk>(r[kb & 1][0], pimg, 16 * kb, 16 * w, lane), right_t<kChunk>(r[kb & 1][1], pimg + kSquare, 16 * kb, 16 * w, lane);
+                };
+                load(3);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb < w) continue;
-                Acc t[2];
-                clear(t);
-                uint32_t a[NI][4], r[2][4];
-                take<NI>(a, q.mine + Sm::e + kb * Sm::e_block, lane);
-                right_t<kChunk>(r[0], pimg, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], pimg + kSquare, 16 * kb, 16 * w, lane);
-                products<T, NI, 2>(t[0], t[1], a, r);
-                add(x, t, q.sc[12 + kb] * f[F_P]);
+                for (int kb = 3; kb >= 0; --kb) {
+                    if (kb < w) break;
+                    if (kb > 0) load(kb - 1);
+                    Acc t[2];
+                    clear(t);
+                    products<T, NI, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
+                    add(x, t, q.sc[12 + kb] * f[F_P]);
+                }
             }
             {
                 const float sx = warp_scale(x);
@@ -863,16 +899,22 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             }
             q.meet();
             clear(y);  // dR
+            {
+                uint32_t a[2][2][4], r[2][2][4];
+                const auto load = [&](int kb) {
+                    take<2>(a[kb & 1], q.mine + Sm::x(true) + kb * 1024, lane);
+                    right_t<kChunk>(r[kb & 1][0], inv, 16 * kb, 16 * w, lane), right_t<kChunk>(r[kb & 1][1], inv + kSquare, 16 * kb, 16 * w, lane);
+                };
+                load(3);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb < w) continue;
-                Acc t[2];
-                clear(t);
-                uint32_t a[2][4], r[2][4];
-                take<2>(a, q.mine + Sm::x(true) + kb * 1024, lane);
-                right_t<kChunk>(r[0], inv, 16 * kb, 16 * w, lane), right_t<kChunk>(r[1], inv + kSquare, 16 * kb, 16 * w, lane);
-                products<T, 2, 2>(t[0], t[1], a, r);
-                add(y, t, q.sc[8 + kb] * f[F_INV]);
+                for (int kb = 3; kb >= 0; --kb) {
+                    if (kb < w) break;
+                    if (kb > 0) load(kb - 1);
+                    Acc t[2];
+                    clear(t);
+                    products<T, 2, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
+                    add(y, t, q.sc[8 + kb] * f[F_INV]);
+                }
             }
             // beta grow dR likewise, from dU's and the inverse's largest
             const float r_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
@@ -897,7 +939,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             Acc t[2 * kSteps], u[2 * kSteps];
             clear(t), clear(u);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
+            for (int kb = 0; kb < 4; ++kb) {  // (a step ahead there would be registers for neither)
                 uint32_t a[2][4], c[2][4];
                 take<2>(a, q.mine + Sm::u + kb * 1024, lane), take<2>(c, q.mine + Sm::w + kb * 1024, lane);
 #pragma unroll
@@ -1455,11 +1497,13 @@ int launch_delta(DeltaParams &p, bool bwd, int sms, cudaStream_t st) {
     void (*const prep)(DeltaParams) = bwd ? based_delta_prep_kernel<T, KP, true> : based_delta_prep_kernel<T, KP, false>;
     OPS_CUDA(allow(prep, PrepSmem<T, KP>::bytes));
     OPS_CUDA(launch_op(prep, dim3(p.chunks, p.HK, z), 32 * kPrepWarps, PrepSmem<T, KP>::bytes, st, p));
-    // A CTA's slices share its records but also its SM: as many as give the fewest rounds of CTAs, each counted by what it takes
+    // A CTA's slices share its records but also its SM: as many as take the least time, which is the rounds of CTAs (those of equal lengths end together)
+    // by what a round takes: 1, 1.24, 1.53 and 2.1 with one to four slices (8 x 4096 rows, 16 heads of 128 x 128: 908, 673, 617 and 572 us).
+    constexpr double kRound[5] = {0.0, 1.0, 1.24, 1.53, 2.1};
     int per = 1;
     const auto cost = [&](int n) {
-        const int64_t ctas = static_cast<int64_t>(p.B) * p.H * ((slices + n - 1) / n);
-        return static_cast<double>((ctas + sms - 1) / sms) * (1.0 + 0.45 * (n - 1));
+        const double rounds = static_cast<double>(p.B) * p.H * ((slices + n - 1) / n) / sms;
+        return (p.lengths && rounds > 1.0 ? rounds : ceil(rounds)) * kRound[n];
     };
     for (int n = 2; n <= Sm::most(bwd) && n <= slices; ++n)
         if (cost(n) <= cost(per)) per = n;
