@@ -1068,6 +1068,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
         const int rows = min(kChunk, live_rows(p, b) - n * kChunk), all = static_cast<int>(p.T - t0 < kChunk ? p.T - t0 : kChunk);
         T *const dq = static_cast<T *>(p.dq) + (first * p.HK + hk) * p.K, *const dk = static_cast<T *>(p.dk) + (first * p.HK + hk) * p.K;
         const int64_t row_k = static_cast<int64_t>(p.HK) * p.K;
+        if (rows > 0) {
+            __syncthreads();  // the batch entry before
+            stages.copy(kKeysStage, smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
+        }
         const int from = rows < 0 ? 0 : rows;  // padding
         for (int i = tid; i < (all - from) * p.K; i += kThreads) {
             const int64_t at = (from + i / p.K) * row_k + i % p.K;
@@ -1079,8 +1083,6 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             if (p.dgate) static_cast<T *>(p.dgate)[at] = from_f32<T>(0.0f);
         }
         if (rows <= 0) continue;
-        __syncthreads();  // the batch entry before
-        stages.copy(kKeysStage, smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
         Acc aq[2 * NQ], ak[2 * NQ];
         clear(aq), clear(ak);
         for (int hh = 0; hh < group; ++hh) {
@@ -1095,9 +1097,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                                 bwd + static_cast<int64_t>(sl) * SR::bwd, SR::bwd);
             };
             __syncthreads();  // the head before
-            for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
 #pragma unroll
             for (int i = 0; i < Sm::stages - 1; ++i) fetch(i);
+            for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
             // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, dO E, dR E, S0 G
             int top[6] = {-1000, -1000, -1000, -1000, -1000, -1000};
             const auto exponents = [&](int (&x)[6], int sl) {
@@ -1206,6 +1208,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 clear(sq), clear(sk);
 #pragma unroll
                 for (int kk = 0; kk < KP / 16; ++kk) {
+                    if (!p.dgate) break;  // nobody asks for the pairs' sums
                     uint32_t a[NI][4], c4[NI][4], x[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) {
