@@ -359,7 +359,7 @@ struct SeqSmem {
                          w = u + 4096;
     __host__ __device__ static constexpr int x(bool bwd) { return bwd ? state : w; }
     static constexpr int scales = w + 4096, slice = scales + 128 + 8 * tile;
-    static constexpr int bytes(bool bwd, int slices) { return 2 * stage(bwd) + slices * slice + 16; }
+    static constexpr int bytes(bool bwd, int slices) { return 2 * stage(bwd) + slices * slice + 32; }
     // Slices of a CTA, at most: 512 threads, and what shared memory holds
     static constexpr int most(bool bwd) { return bytes(bwd, 4) <= 227 * 1024 ? 4 : bytes(bwd, 3) <= 227 * 1024 ? 3 : bytes(bwd, 2) <= 227 * 1024 ? 2 : 1; }
 };
@@ -515,26 +515,31 @@ __device__ __forceinline__ void leave(uint8_t *to, int term, const uint32_t (&a)
 }
 
 // Records come by bulk copies that one thread issues (as 16-byte copies of all threads they took 1250 of a chunk's 4200 cycles where one slice
-// has an SM to itself: 1 x 16384, 16 heads of 128 x 128). A barrier counts a stage's bytes, and all threads wait for it.
+// has an SM to itself: 1 x 16384, 16 heads of 128 x 128). A barrier counts a stage's bytes, and all threads wait for it; another counts the warps
+// that are done with the stage, and only the thread that fills it again waits for that: slices that share records need not keep step (8 x 4096
+// rows, 16 heads of 128 x 128: forward 572 to 511 us, backward 666 to 607).
 __device__ unsigned int g_delta_status;  // bit 0: a wait for records gave up
 constexpr uint64_t kDeltaWaitNs = 1000000000ull;
 
 struct Stages {
-    uint32_t bars;  // one of eight bytes for each stage
+    uint32_t bars, done;  // a barrier of eight bytes for each stage
     uint32_t late = 0, parities = 0;  // stages whose copies were given up, and the phases they belong to
 
+    static constexpr int bytes(int count) { return 16 * count; }
     __device__ __forceinline__ void begin(uint8_t *at, int count) {
-        bars = smem_u32(at);
+        bars = smem_u32(at), done = bars + 8 * count;
         if (threadIdx.x == 0) {
-            for (int i = 0; i < count; ++i) mbar_init(bars + 8 * i, 1);
+            for (int i = 0; i < count; ++i) mbar_init(bars + 8 * i, 1), mbar_init(done + 8 * i, blockDim.x / 32);
             fence_mbar_init();
         }
         __syncthreads();
     }
-    // Two records, one behind the other, by thread 0. Nobody reads the stage any more, and its last copy has been waited for.
-    __device__ __forceinline__ void copy(int stage, uint8_t *to, const uint8_t *a, int a_bytes, const uint8_t *b, int b_bytes) const {
+    // Two records, one behind the other, by thread 0, once all warps are done with what the stage held. use: how often it was filled before (0 where a barrier
+    // of the CTA has said so).
+    __device__ __forceinline__ void copy(int stage, int use, uint8_t *to, const uint8_t *a, int a_bytes, const uint8_t *b, int b_bytes) {
         if (threadIdx.x != 0) return;
         const uint32_t bar = bars + 8 * stage, at = smem_u32(to);
+        if (use > 0 && !mbar_try_wait(done + 8 * stage, use - 1 & 1) && (late || !come(done + 8 * stage, use - 1 & 1))) late |= 1u << 31;
         mbar_arrive_expect_tx(bar, a_bytes + b_bytes);
         bulk_copy(at, a, a_bytes, bar);
         if (b_bytes) bulk_copy(at + a_bytes, b, b_bytes, bar);
@@ -542,17 +547,22 @@ struct Stages {
     // A wait that gives up (a second: the copy has not come) sets the status word; later ones look only once, so that the kernel ends.
     __device__ __forceinline__ void wait(int stage, int parity) {
         if (mbar_try_wait(bars + 8 * stage, parity)) return;
-        if (late || !come(stage, parity)) late |= 1u << stage, parities = (parities & ~(1u << stage)) | static_cast<uint32_t>(parity) << stage;
+        if (late || !come(bars + 8 * stage, parity)) late |= 1u << stage, parities = (parities & ~(1u << stage)) | static_cast<uint32_t>(parity) << stage;
+    }
+    // The warp is done with the stage.
+    __device__ __forceinline__ void leave(int stage) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(done + 8 * stage);
     }
     // Before the CTA ends: what was given up may still be on its way into its shared memory
     __device__ __forceinline__ void end() const {
         if (late)
             for (int i = 0; i < 8; ++i)
-                if (late >> i & 1) come(i, parities >> i & 1);
+                if (late >> i & 1) come(bars + 8 * i, parities >> i & 1);
     }
-    __device__ __noinline__ bool come(int stage, int parity) const {
+    __device__ static __noinline__ bool come(uint32_t bar, int parity) {
         const uint64_t began = global_timer_ns();
-        while (!mbar_try_wait(bars + 8 * stage, parity)) {
+        while (!mbar_try_wait(bar, parity)) {
             if (global_timer_ns() - began > kDeltaWaitNs) {
                 atomicOr(&g_delta_status, 1u);
                 return false;
@@ -599,7 +609,7 @@ struct Seq {
         if (lane == 0) {
             sc[w] = own;
             if (w == 0) sc[4] = inverse_of(f);
-            if (rec) rec_scales[w] = inverse_of(f);
+            if (rec && w == 0) rec_scales[0] = inverse_of(f);
         }
     }
     // The first state: its largest is found first
@@ -623,6 +633,9 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
     extern __shared__ __align__(128) uint8_t smem[];
     const Q q(p, smem);
     const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
+    // The next chunk's records are asked for at once where a slice has the CTA to itself, else after a chunk's first products: other
+    // slices may still be in the chunk before.
+    const bool alone = blockDim.x == kQuad;
     Stages stages;
     stages.begin(smem + 2 * kStage + blockDim.x / kQuad * Sm::slice, 2);
     int turn = 0;  // chunks up to this batch entry
@@ -636,7 +649,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
         const auto record = [&](int n) { return p.saved ? p.saved + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::fwd : nullptr; };
         const auto fetch = [&](int n) {
             const int at = turn + n & 1;
-            stages.copy(at, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, g + static_cast<int64_t>(n) * R::g(false), R::g(false));
+            stages.copy(at, turn + n >> 1, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, g + static_cast<int64_t>(n) * R::g(false), R::g(false));
+        };
+        const auto values = [&](int n) {
+            const int at = turn + n & 1;
             const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
             if (cols > 0) load_tile(q.tiles + at * Sm::tile, t < live ? v + t * p.v_st : v, p.v_st, static_cast<int>(live - t), cols, p.v_vec, lane);
             copies_commit();
@@ -645,17 +661,21 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
         read_state(s, p.state ? p.state + st * p.K * p.V : nullptr, w * (KP / 4), p.K, p.V, v0, lane);
         __syncthreads();  // the batch entry before
         if (count > 0) {
-            fetch(0);
+            fetch(0), values(0);
             uint8_t *const rec = cols > 0 ? record(0) : nullptr;
             q.begin(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
         }
         for (int n = 0; n < count; ++n) {
             const int stage = turn + n & 1;
-            copies_wait<0>();
             stages.wait(stage, turn + n >> 1 & 1);
-            __syncthreads();  // chunk n and the state's operands are there, and chunk n - 1 is done with
-            if (n + 1 < count) fetch(n + 1);
-            if (cols <= 0) continue;  // the same for the slice's warps
+            if (cols <= 0) {  // the same for the slice's warps (the CTA's first slice has channels)
+                stages.leave(stage);
+                continue;
+            }
+            copies_wait<0>();
+            q.meet();  // chunk n's values and the state's operands are there
+            if (n + 1 < count) values(n + 1);
+            if (n + 1 < count && alone) fetch(n + 1);
             const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;  // this warp's first row
             uint8_t *const tile = q.tiles + stage * Sm::tile;
             const uint32_t kimg = smem_u32(smem) + stage * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
@@ -694,6 +714,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 give<2>(q.mine + Sm::x(false) + w * 1024, a, lane);
                 if (lane == 0) q.sc[8 + w] = inverse_of(sx);
             }
+            if (n + 1 < count && !alone) fetch(n + 1);
             q.meet();
             clear(y);  // E
             {
@@ -724,7 +745,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 by_columns(y, f + F_BF + 16 * w, 1.0f, lane);
                 left_of<2>(c, y[0], y[1], su);
                 give<2>(q.mine + Sm::u + w * 1024, c, lane);
-                if (rec && lane == 0) reinterpret_cast<float *>(rec + SR::fwd_scales)[4 + w] = inverse_of(se);
+                if (rec && lane == 0 && w == 0) reinterpret_cast<float *>(rec + SR::fwd_scales)[1] = inverse_of(se);
             }
             q.meet();
             clear(x);
@@ -769,6 +790,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             for (int j = 0; j < 2 * kSteps; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[j][e] = fmaf(t[j][e], iu, s[j][e] * whole);
+            stages.leave(stage);
             if (n + 1 < count) {
                 uint8_t *const next = record(n + 1);
                 q.hand_over(s, fmaf(before, whole, 64.0f * (kTop * ik) * u_most), next, reinterpret_cast<float *>(next + SR::fwd_scales));
@@ -799,6 +821,9 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
     extern __shared__ __align__(128) uint8_t smem[];
     const Q q(p, smem);
     const int lane = q.lane, w = q.w, head = q.head, v0 = q.v0, cols = q.cols, slices = (p.V + kSlice - 1) / kSlice;
+    // The next chunk's records are asked for at once where a slice has the CTA to itself, else after a chunk's first products: other
+    // slices may still be in the chunk before.
+    const bool alone = blockDim.x == kQuad;
     Stages stages;
     stages.begin(smem + 2 * kStage + blockDim.x / kQuad * Sm::slice, 2);
     int turn = 0;  // chunks up to this batch entry
@@ -812,7 +837,11 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
         const auto record = [&](int n) { return p.slice_rec + (((static_cast<int64_t>(b) * p.chunks + n) * p.H + head) * slices + q.slice) * SR::bwd; };
         const auto fetch = [&](int n) {
             const int at = turn + count - 1 - n & 1;
-            stages.copy(at, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk, grec + static_cast<int64_t>(n) * R::g(true), R::g(true));
+            stages.copy(at, turn + count - 1 - n >> 1, smem + at * kStage, qk + static_cast<int64_t>(n) * R::qk, R::qk,
+                        grec + static_cast<int64_t>(n) * R::g(true), R::g(true));
+        };
+        const auto values = [&](int n) {
+            const int at = turn + count - 1 - n & 1;
             const int64_t t = static_cast<int64_t>(n) * kChunk + 16 * w;
             if (cols > 0) load_tile(q.tiles + at * Sm::tile, t < live ? dout + t * p.do_st : dout, p.do_st, static_cast<int>(live - t), cols, p.do_vec, lane);
             copies_commit();
@@ -821,16 +850,20 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
         read_state(g, p.state ? p.state + st * p.K * p.V : nullptr, w * (KP / 4), p.K, p.V, v0, lane);
         __syncthreads();
         if (count > 0) {
-            fetch(count - 1);
+            fetch(count - 1), values(count - 1);
             if (cols > 0) q.begin(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
         }
         for (int n = count - 1; n >= 0; --n) {
             const int stage = turn + count - 1 - n & 1;
-            copies_wait<0>();
             stages.wait(stage, turn + count - 1 - n >> 1 & 1);
-            __syncthreads();
-            if (n > 0) fetch(n - 1);
-            if (cols <= 0) continue;
+            if (cols <= 0) {
+                stages.leave(stage);
+                continue;
+            }
+            copies_wait<0>();
+            q.meet();
+            if (n > 0) values(n - 1);
+            if (n > 0 && alone) fetch(n - 1);
             const int64_t t0 = static_cast<int64_t>(n) * kChunk + 16 * w;
             uint8_t *const tile = q.tiles + stage * Sm::tile;
             const uint32_t kimg = smem_u32(smem) + stage * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
@@ -845,7 +878,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 left_of<NI>(a, y[0], y[1], so);
                 give<NI>(q.mine + Sm::e + w * Sm::e_block, a, lane);
                 leave<NI>(rec + SR::dout + w * 512, kRowsTerm, a, lane);
-                if (lane == 0) q.sc[12 + w] = inverse_of(so), rec_scales[8 + w] = inverse_of(so);
+                if (lane == 0) q.sc[12 + w] = inverse_of(so), rec_scales[2 + w] = inverse_of(so);
             }
             clear(x);  // dU
             const float is = q.sc[4], behind = q.state_most();
@@ -864,6 +897,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 }
             }
             by_columns(x, f + F_REST + 16 * w, f[F_K] * is, lane);
+            if (n > 0 && !alone) fetch(n - 1);
             q.meet();
             {  // (from the last rows up: all warps have those)
                 uint32_t a[2][NI][4], r[2][2][4];
@@ -932,7 +966,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 uint32_t c[2][4];
                 left_of<2>(c, y[0], y[1], sw);
                 give<2>(q.mine + Sm::w + w * 1024, c, lane);
-                if (lane == 0) rec_scales[4 + w] = inverse_of(sr);
+                if (lane == 0 && w == 0) rec_scales[1] = inverse_of(sr);
             }
             q.meet();
             const float whole = f[F_WHOLE], ik = f[F_K], iq = f[F_Q], iu = inverse_of(su) * iq, iw = inverse_of(sw) * ik;
@@ -957,6 +991,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             for (int j = 0; j < 2 * kSteps; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) g[j][e] = fmaf(t[j][e], iu, fmaf(u[j][e], iw, g[j][e] * whole));
+            stages.leave(stage);
             if (n > 0)
                 q.hand_over(g, fmaf(behind, whole, 64.0f * ((kTop * iq) * u_most + (kTop * ik) * w_most)), record(n - 1),
                             reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
@@ -984,18 +1019,21 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
 // and the gradient of b_i, the sum of log decays up to row i, is what row i reads minus what it has written:
 //     db_i = q_i (scale grow dO S0^T)_i - k_i (beta grow dR S0^T + rest U G^T)_i + sum_j (N_ij - N_ji),  N = dP P + dA A,
 // with grow_last <S0, G> + sum_i k_i (rest U G^T)_i more at the last row; dgate_i is the sum of db from i on.
-// A CTA takes one chunk of one key head and adds up the value heads that share it, so that nothing is added by atomics. Its 16 warps share out
-// the products' results, 16 rows and a quarter of the columns each; the slices' records come in by a ring of stages and are used as they lie.
+// A CTA takes one chunk of one key head and adds up the value heads that share it, so that nothing is added by atomics. Its eight warps share out
+// the products' results, 16 rows and half of the columns each; the slices' records come in by a ring of stages and are used as they lie. With
+// 16 warps of a quarter of the columns left operands were read twice as often (8 x 4096 rows, 16 heads of 128 x 128: 782 us, now 753; without the
+// barrier of each slice 797). The pairs' sums N come from the products of queries and keys again, 16 % of a CTA's time: taken from q dq - k dk
+// they would be differences of rounded sums, and where decays are steep dgate would be what that rounding leaves.
 // ------------------------------------------------------------------------------------------------
-constexpr int kGradWarps = 16;
+constexpr int kGradWarps = 8;
 
 template <typename T, int KP>
 struct GradSmem {
     using SR = SliceRec<T, KP>;
     static constexpr int stages = Terms<T>::out == 1 ? 4 : 3, stage = SR::fwd + SR::bwd;
     static constexpr int f = Rec<T, KP>::qk, ring = f + F_COUNT * 4, dp = ring + stages * stage, da = dp + Terms<T>::out * kSquare,
-                         part = da + Terms<T>::out * kSquare;  // sums: rows 4 x 64, next 4 x 64, columns 4 x 64, dbeta 64
-    static constexpr int red = part + 13 * kChunk * 4, bars = red + 2 * kGradWarps * 4, bytes = bars + 8 * (stages + 1);
+                         part = da + Terms<T>::out * kSquare;  // sums: rows 2 x 64, next 2 x 64, columns 4 x 64, dbeta 64
+    static constexpr int red = part + 9 * kChunk * 4, bars = red + 2 * kGradWarps * 4, bytes = bars + Stages::bytes(stages + 1);
 };
 
 // Two neighbouring elements of an image of key or query rows
@@ -1047,16 +1085,15 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
     using R = Rec<T, KP>;
     using SR = SliceRec<T, KP>;
     using Sm = GradSmem<T, KP>;
-    constexpr int NI = Terms<T>::in, NO = Terms<T>::out, NQ = KP / 64, kThreads = 32 * kGradWarps;  // NQ: 16 columns of a warp's quarter
+    constexpr int NI = Terms<T>::in, NO = Terms<T>::out, NQ = KP / 32, kThreads = 32 * kGradWarps;  // NQ: 16 columns of a warp's half
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp & 3, wn = warp >> 2;
     const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK, slices = (p.V + kSlice - 1) / kSlice;
-    const int r0 = 16 * wm + (lane >> 2), r1 = r0 + 8, col0 = wn * (KP / 4) + 2 * (lane & 3);  // this thread's accumulators
-    const bool traces = warp < KP / 8;
-    const int trace = traces ? warp >> 1 : 0, half = warp & 1;
+    const int r0 = 16 * wm + (lane >> 2), r1 = r0 + 8, col0 = wn * (KP / 2) + 2 * (lane & 3);  // this thread's accumulators
+    const bool traces = warp < KP / 16;
     float *const f = reinterpret_cast<float *>(smem + Sm::f);
-    float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 4 * kChunk,
-                *const part_col = part_next + 4 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
+    float *const part_row = reinterpret_cast<float *>(smem + Sm::part), *const part_next = part_row + 2 * kChunk,
+                *const part_col = part_next + 2 * kChunk, *const part_beta = part_col + 4 * kChunk, *const red = reinterpret_cast<float *>(smem + Sm::red);
     const uint32_t base = smem_u32(smem), kimg = base, qimg = base + R::img;
     constexpr int kKeysStage = Sm::stages;  // the stage of the queries' and keys' images
     Stages stages;
@@ -1070,7 +1107,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
         const int64_t row_k = static_cast<int64_t>(p.HK) * p.K;
         if (rows > 0) {
             __syncthreads();  // the batch entry before
-            stages.copy(kKeysStage, smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
+            stages.copy(kKeysStage, 0, smem, p.qk_rec + ((static_cast<int64_t>(b) * p.HK + hk) * p.chunks + n) * R::qk, R::qk, nullptr, 0);
         }
         const int from = rows < 0 ? 0 : rows;  // padding
         for (int i = tid; i < (all - from) * p.K; i += kThreads) {
@@ -1093,7 +1130,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             const auto fetch = [&](int sl) {
                 const int at = (turn + sl) % Sm::stages;
                 if (sl < slices)
-                    stages.copy(at, smem + Sm::ring + at * Sm::stage, fwd + static_cast<int64_t>(sl) * SR::fwd, SR::fwd,
+                    stages.copy(at, 0, smem + Sm::ring + at * Sm::stage, fwd + static_cast<int64_t>(sl) * SR::fwd, SR::fwd,
                                 bwd + static_cast<int64_t>(sl) * SR::bwd, SR::bwd);
             };
             __syncthreads();  // the head before
@@ -1105,9 +1142,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             const auto exponents = [&](int (&x)[6], int sl) {
                 const float *const a = reinterpret_cast<const float *>(fwd + static_cast<int64_t>(sl) * SR::fwd + SR::fwd_scales),
                                    *const c = reinterpret_cast<const float *>(bwd + static_cast<int64_t>(sl) * SR::bwd + SR::bwd_scales);
-                const int s = exponent(a[wn]), em = exponent(a[4 + wm]), en = exponent(a[4 + wn]), g = exponent(c[wn]), r = exponent(c[4 + wm]), o = exponent(c[8 + wm]);
-                x[0] = o + s, x[1] = r + s, x[2] = em + g, x[3] = o + en, x[4] = r + en;
-                x[5] = exponent(a[trace / NQ]) + exponent(c[trace / NQ]);
+                const int s = exponent(a[0]), e = exponent(a[1]), g = exponent(c[0]), r = exponent(c[1]), o = exponent(c[2 + wm]);
+                x[0] = o + s, x[1] = r + s, x[2] = e + g, x[3] = o + e, x[4] = r + e, x[5] = s + g;
             };
             uint32_t by[6];  // lane i: the factors of slice i (of 32)
             for (int sl = lane; sl < slices; sl += 32) {
@@ -1118,8 +1154,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             }
 #pragma unroll
             for (int i = 0; i < 6; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
-            Acc aos[2 * NQ], ars[2 * NQ], aeg[2 * NQ], dp[2], da[2];
-            Acc diagonal[1];
+            Acc aos[2 * NQ], ars[2 * NQ], aeg[2 * NQ], dp[4], da[4];
+            Acc diagonal[2];
             clear(aos), clear(ars), clear(aeg), clear(dp), clear(da), clear(diagonal);
             for (int sl = 0; sl < slices; ++sl) {
                 const int at = (turn + sl) % Sm::stages;
@@ -1142,13 +1178,14 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 for (int j = 0; j < NI; ++j) left_blocks(lo[j], ya + SR::dout + j * kRowsTerm + wm * 512, lane);
 #pragma unroll
                 for (int j = 0; j < NO; ++j) left_blocks(lr[j], ya + SR::dr + j * kRowsTerm + wm * 512, lane), left_blocks(le[j], xa + SR::e + j * kRowsTerm + wm * 512, lane);
-                if (wn <= wm) {
+                times<NI>(d, lo, factor[3]), times<NO>(c, lr, factor[4]);
 #pragma unroll
-                    for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + wn * 512, lane);
-                    times<NI>(d, lo, factor[3]);
-                    products<T, NI, NO>(dp[0], dp[1], d, v);
-                    times<NO>(c, lr, factor[4]);
-                    products<T, NO, NO>(da[0], da[1], c, v);
+                for (int i = 0; i < 2; ++i) {
+                    if (2 * wn + i > wm) break;
+#pragma unroll
+                    for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + (2 * wn + i) * 512, lane);
+                    products<T, NI, NO>(dp[2 * i], dp[2 * i + 1], d, v);
+                    products<T, NO, NO>(da[2 * i], da[2 * i + 1], c, v);
                 }
                 times<NI>(d, lo, factor[0]), times<NO>(c, lr, factor[1]), times<NO>(le, le, factor[2]);
 #pragma unroll
@@ -1161,15 +1198,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], ya + j * SR::state_term + (wn * NQ + i) * 512, lane);
                     products<T, NO, NO>(aeg[2 * i], aeg[2 * i + 1], le, v);
                 }
-                // <S0, G>: the diagonal of S0^T G, a block of eight channels to a warp
+                // <S0, G>: the diagonal of S0^T G, 16 channels to a warp
                 if (traces) {
 #pragma unroll
-                    for (int j = 0; j < NO; ++j) left_blocks(c[j], xa + j * SR::state_term + trace * 512, lane), right_blocks(v[j], ya + j * SR::state_term + trace * 512, lane);
+                    for (int j = 0; j < NO; ++j) left_blocks(c[j], xa + j * SR::state_term + warp * 512, lane), right_blocks(v[j], ya + j * SR::state_term + warp * 512, lane);
                     times<NO>(c, c, factor[5]);
-#pragma unroll
-                    for (int j = 0; j < NO; ++j)
-#pragma unroll
-                        for (int i = 0; i + j < NO; ++i) mma(diagonal[0], c[i], half ? v[j][2] : v[j][0], half ? v[j][3] : v[j][1]);
+                    products<T, NO, NO>(diagonal[0], diagonal[1], c, v);
                 }
             }
             turn += slices;
@@ -1177,7 +1211,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             float dot = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (traces && 2 * (lane & 3) + e == lane >> 2) dot += half ? diagonal[0][2 + e] : diagonal[0][e];
+                if (traces && 2 * (lane & 3) + e == lane >> 2) dot += diagonal[0][e] + diagonal[1][2 + e];
             dot = ldexpf(dot, top[5]);
             // rows' and columns' factors, and the rows' products with queries and keys
             const float ik = f[F_K], iq = f[F_Q], c0 = f[F_GROW + r0], c1 = f[F_GROW + r1], b0 = f[F_BETA + r0], b1 = f[F_BETA + r1];
@@ -1202,9 +1236,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             }
             // the products of queries and keys with keys, and with them the pairs' sums and the factors of dQ and dK
             row0 -= next0, row1 -= next1;
-            float col[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, mp = 0.0f, ma = 0.0f;
-            if (wn <= wm) {
-                Acc sq[2], sk[2];
+            float col[4][2] = {}, mp = 0.0f, ma = 0.0f;
+            if (2 * wn <= wm) {
+                Acc sq[4], sk[4];
                 clear(sq), clear(sk);
 #pragma unroll
                 for (int kk = 0; kk < KP / 16; ++kk) {
@@ -1214,17 +1248,22 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     for (int j = 0; j < NI; ++j) {
                         left<KP>(a[j], qimg + j * R::term, 16 * wm, 16 * kk, lane);
                         left<KP>(c4[j], kimg + j * R::term, 16 * wm, 16 * kk, lane);
-                        right<KP>(x[j], kimg + j * R::term, 16 * wn, 16 * kk, lane);
                     }
-                    products<T, NI, NI>(sq[0], sq[1], a, x);
-                    products<T, NI, NI>(sk[0], sk[1], c4, x);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (2 * wn + i > wm) break;
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) right<KP>(x[j], kimg + j * R::term, 32 * wn + 16 * i, 16 * kk, lane);
+                        products<T, NI, NI>(sq[2 * i], sq[2 * i + 1], a, x);
+                        products<T, NI, NI>(sk[2 * i], sk[2 * i + 1], c4, x);
+                    }
                 }
                 const float sp = ldexpf(1.0f, top[3]), sa = ldexpf(-1.0f, top[4]);
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = e < 2 ? r0 : r1, j = 16 * wn + 8 * nt + 2 * (lane & 3) + e % 2;
+                        const int i = e < 2 ? r0 : r1, j = 32 * wn + 8 * nt + 2 * (lane & 3) + e % 2;
                         if (i == j) part_beta[i] = -da[nt][e] * sa;
                         const float d = j <= i ? expf((f[F_BHI + i] - f[F_BHI + j]) + (f[F_BLO + i] - f[F_BLO + j])) : 0.0f, bj = f[F_BETA + j];
                         dp[nt][e] = j <= i ? dp[nt][e] * sp * bj * (d * p.scale) : 0.0f;
@@ -1236,10 +1275,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) col[nt][0] += __shfl_xor_sync(0xffffffffu, col[nt][0], d), col[nt][1] += __shfl_xor_sync(0xffffffffu, col[nt][1], d);
-                if (lane < 4) *reinterpret_cast<float2 *>(part_col + wm * kChunk + 16 * wn + 8 * nt + 2 * lane) = make_float2(col[nt][0], col[nt][1]);
+                if (lane < 4) *reinterpret_cast<float2 *>(part_col + wm * kChunk + 32 * wn + 8 * nt + 2 * lane) = make_float2(col[nt][0], col[nt][1]);
             }
 #pragma unroll
             for (int d = 1; d < 4; d *= 2) {
@@ -1254,12 +1293,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
             for (int d = 1; d < 32; d *= 2) dot += __shfl_xor_sync(0xffffffffu, dot, d);
             if (lane == 0) red[kGradWarps + warp] = dot;
             mp = scale_for(cta_most<kGradWarps>(mp, red)), ma = scale_for(cta_most<kGradWarps>(ma, red));
-            if (wn <= wm) {
+            if (2 * wn <= wm) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t at = word_at<kChunk>(e ? r1 : r0, 2 * wn + nt) + 4 * (lane & 3);
+                        const uint32_t at = word_at<kChunk>(e ? r1 : r0, 4 * wn + nt) + 4 * (lane & 3);
                         uint32_t w[NO];
                         terms<NO>(dp[nt][2 * e] * mp, dp[nt][2 * e + 1] * mp, w);
 #pragma unroll
@@ -1280,7 +1319,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     const int i = 2 * lane + e;
                     x[e] = nx[e] = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[e] += part_row[j * kChunk + i], nx[e] += part_next[j * kChunk + i];
+                    for (int j = 0; j < 2; ++j) x[e] += part_row[j * kChunk + i], nx[e] += part_next[j * kChunk + i];
                     float c = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) c += part_col[j * kChunk + i];
@@ -1326,7 +1365,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                     for (int i = 0; i < NQ; ++i) {
                         uint32_t x[NI][4];
 #pragma unroll
-                        for (int j = 0; j < NI; ++j) right_t<KP>(x[j], kimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
+                        for (int j = 0; j < NI; ++j) right_t<KP>(x[j], kimg + j * R::term, 16 * kb, wn * (KP / 2) + 16 * i, lane);
                         if (kb <= wm) {
                             products<T, NO, NI>(tq[2 * i], tq[2 * i + 1], a, x);
                             products<T, NO, NI>(ta[2 * i], ta[2 * i + 1], c, x);
@@ -1338,7 +1377,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
                             for (int j = 0; j < NO; ++j) left_t<kChunk>(e[j], i_dp + j * kSquare, 16 * kb, 16 * wm, lane);
 #pragma unroll
-                            for (int j = 0; j < NI; ++j) right_t<KP>(x[j], qimg + j * R::term, 16 * kb, wn * (KP / 4) + 16 * i, lane);
+                            for (int j = 0; j < NI; ++j) right_t<KP>(x[j], qimg + j * R::term, 16 * kb, wn * (KP / 2) + 16 * i, lane);
                             products<T, NO, NI>(tk[2 * i], tk[2 * i + 1], e, x);
                         }
                     }
@@ -1501,8 +1540,8 @@ int launch_delta(DeltaParams &p, bool bwd, int sms, cudaStream_t st) {
     OPS_CUDA(allow(prep, PrepSmem<T, KP>::bytes));
     OPS_CUDA(launch_op(prep, dim3(p.chunks, p.HK, z), 32 * kPrepWarps, PrepSmem<T, KP>::bytes, st, p));
     // A CTA's slices share its records but also its SM: as many as take the least time, which is the rounds of CTAs (those of equal lengths end together)
-    // by what a round takes: 1, 1.24, 1.53 and 2.1 with one to four slices (8 x 4096 rows, 16 heads of 128 x 128: 908, 673, 617 and 572 us).
-    constexpr double kRound[5] = {0.0, 1.0, 1.24, 1.53, 2.1};
+    // by what a round takes: 1, 1.29, 1.57 and 2.09 with one to four slices (8 x 4096 rows, 16 heads of 128 x 128: 857, 632, 575 and 511 us).
+    constexpr double kRound[5] = {0.0, 1.0, 1.29, 1.57, 2.09};
     int per = 1;
     const auto cost = [&](int n) {
         const double rounds = static_cast<double>(p.B) * p.H * ((slices + n - 1) / n) / sms;
@@ -1548,11 +1587,8 @@ int run_delta(DeltaParams &p, int dtype, bool bwd, void *workspace, size_t ws_by
     p.chunks = (T + kChunk - 1) / kChunk;
     const int64_t strides[] = {p.q_sb, p.q_st, p.q_sh, p.k_sb, p.k_st, p.k_sh, p.v_sb, p.v_st, p.v_sh, p.do_sb, p.do_st, p.do_sh,
                                p.beta_sb, p.beta_st, p.gate_sb, p.gate_st};
-    int64_t bits = 0;
-    for (const int64_t s : strides) {
+    for (const int64_t s : strides)
         if (s < 0) return BASED_ERR_BAD_STRIDE;
-        bits |= s;
-    }
     const size_t es = elem_size(dtype);
     const void *const typed[] = {p.q, p.k, p.v, p.beta, p.gate, p.dout, p.out, p.dq, p.dk, p.dbeta, p.dgate};
     for (const void *t : typed)
@@ -1665,7 +1701,9 @@ int based_delta_step(const void *q, int64_t q_sn, int64_t q_sh, const void *k, i
     if (!q || !k || !v || !beta || !pool || !o) return BASED_ERR_NULL_POINTER;
     if (!type_ok(dtype)) return BASED_ERR_UNSUPPORTED_TYPE;
     if (!(scale == scale)) return BASED_ERR_BAD_ARGUMENT;
-    if (check_delta_sizes(N, 1, H, HK, K, V) != BASED_OK || S < 1 || (!slots && S < N)) return BASED_ERR_BAD_SIZE;
+    if (check_delta_sizes(N, 1, H, HK, K, V) != BASED_OK || S < 1 || (!slots && S < N) ||
+        S > (static_cast<int64_t>(1) << 56) / (static_cast<int64_t>(H) * K * V))
+        return BASED_ERR_BAD_SIZE;
     if (q_sn < 0 || q_sh < 0 || k_sn < 0 || k_sh < 0 || v_sn < 0 || v_sh < 0 || beta_sn < 0 || gate_sn < 0) return BASED_ERR_BAD_STRIDE;
     const size_t es = elem_size(dtype);
     const void *const typed[] = {q, k, v, beta, gate, o};

@@ -67,7 +67,7 @@ struct Rec {
 
 // What the passes through the chunks leave for the gradients, per chunk, value head and slice of 16 channels of the values: float16 terms
 // in the order of left operands, 16 x 16 blocks of four 8 x 8 blocks (rows 0-7 and 8-15 of columns 0-7, the same of columns 8-15) of 128
-// bytes, rows the slice's channels; behind them the scales' inverses, one for each quarter of the keys' channels or 16 of the chunk's rows.
+// bytes, rows the slice's channels; behind them the scales' inverses, one for the state, one for E or dR, and one for each 16 of the chunk's rows of dO.
 constexpr int kSlice = 16;
 constexpr int kRowsTerm = kSlice * kChunk * 2;
 template <typename T, int KP>
@@ -75,9 +75,9 @@ struct SliceRec {
     static constexpr int in = Terms<T>::in, out = Terms<T>::out;
     static constexpr int state_term = kSlice * KP * 2, states = out * state_term;
     // forward: the state in front of the chunk, E
-    static constexpr int e = states, fwd_scales = e + out * kRowsTerm, fwd = fwd_scales + 32;
+    static constexpr int e = states, fwd_scales = e + out * kRowsTerm, fwd = fwd_scales + 16;
     // backward: the gradient of the state behind the chunk, dR, dO
-    static constexpr int dr = states, dout = dr + out * kRowsTerm, bwd_scales = dout + in * kRowsTerm, bwd = bwd_scales + 48;
+    static constexpr int dr = states, dout = dr + out * kRowsTerm, bwd_scales = dout + in * kRowsTerm, bwd = bwd_scales + 32;
 };
 
 // ------------------------------------------------------------------------------------------------

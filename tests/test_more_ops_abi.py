@@ -89,7 +89,7 @@ REFUSALS = [
     (delta_bwd, dict(dk=at(9)), ALIAS), (delta_bwd, dict(dv=at(5)), ALIAS), (delta_bwd, dict(dstate=at(6)), ALIAS),
     (delta_bwd, dict(dgate=at(12)), ALIAS), (delta_bwd, dict(dh=-1), STRIDE), (delta_bwd, dict(dq=at(9) + 2), ALIGN),
     *[(delta_step, {n: None}, NULL) for n in ("q", "k", "v", "beta", "pool", "o")], (delta_step, dict(slots=None, N=6), SIZE),
-    (delta_step, dict(S=0), SIZE), (delta_step, dict(K=130), SIZE), (delta_step, dict(HK=3), SIZE), (delta_step, dict(vn=-1), STRIDE),
+    (delta_step, dict(S=0), SIZE), (delta_step, dict(S=1 << 20, H=65532, K=128, V=1 << 16), SIZE), (delta_step, dict(K=130), SIZE), (delta_step, dict(HK=3), SIZE), (delta_step, dict(vn=-1), STRIDE),
     (delta_step, dict(pool=at(5) + 2), ALIGN), (delta_step, dict(o=at(5)), ALIAS), (delta_step, dict(pool=at(1)), ALIAS),
     (delta_step, dict(dtype=-1), TYPE), (delta_step, dict(scale=f(NAN)), ARG),
     *[(rms_fwd, {n: None}, NULL) for n in ("x", "y", "res", "sum")], (rms_fwd, dict(st=2), TYPE), (rms_fwd, dict(dt=3), TYPE),
