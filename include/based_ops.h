@@ -180,11 +180,12 @@ BASED_API size_t based_embed_bwd_workspace_size(int64_t N, int V, int D);
  * has stored: per batch entry and head, for t = 0 .. T-1,
  *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),   S_t = a_t S_{t-1} + k_t u_t^T,   o_t = scale S_t^T q_t,
  * with a = exp(gate), or 1 without gates. Head h of the values uses head h / (H / HK) of queries and keys.
- * Products go through float16 pairs: as accurate as float32's relative to the largest magnitude of a
- * row of the state's columns or of 64 rows of keys or queries; magnitudes below 2^-84 count as 0 there.
+ * Products go through float16 pairs: as accurate as float32's relative to the largest magnitude of 16 value channels of the
+ * state, of 64 rows of keys or queries, or of 16 rows and channels of values; magnitudes below 2^-84 count as 0 there.
  * Gates are meant to be <= 0 (-inf clears the state, gates below -1e5 count as -inf). Positive ones let the state grow and
- * work as long as no 64 of them add up to more than 88. A state with an infinity or NaN has NaN from
- * there on. Keys are taken as they are; the rule is stable where beta |k|^2 is at most 2.
+ * work as long as no 64 of them add up to more than 88. Rows go by chunks of 64, from row 0: from the chunk on that has an
+ * infinity or NaN in an input or the state, a head's results are NaN where the formulas have them, and undefined elsewhere.
+ * Keys are taken as they are; the rule is stable where beta |k|^2 is at most 2.
  *   q, k         (B,T,HK,K) of `dtype`, strides (sb, st, sh, 1)
  *   v            (B,T,H,V) of `dtype`, strides (sb, st, sh, 1)
  *   beta, gate   (B,T,H) of `dtype`, strides (sb, st, 1); gate may be NULL

@@ -3,7 +3,7 @@
 The compute runs in hand-written sm_103a CUDA kernels behind a C-ABI shared library
 (``include/based.h``); ``linear_attention_gb300.based`` is a thin ctypes binding to it. The
 operators of a language model around it (gated linear recurrence, group norm with an activation,
-embedding; ``include/based_ops.h``) are bound by ``linear_attention_gb300.ops``.
+embedding, gated delta rule, root-mean-square norm, sampling; ``include/based_ops.h``) are bound by ``linear_attention_gb300.ops``.
 """
 import importlib
 

@@ -1,8 +1,10 @@
 """Python functions of the C ABI in ``include/based_ops.h``.
 
 The operators of a language model around the Based forward pass: the gated linear recurrence
-(``based_scan_*``), the per-token group norm with an activation (``based_norm_*``) and the scaled
-embedding with its gradient (``based_embed_*``). Every step runs in the CUDA kernels of
+(``based_scan_*``), the per-token group norm with an activation (``based_norm_*``), the scaled
+embedding with its gradient (``based_embed_*``), the gated delta rule (``based_delta_*``), the
+root-mean-square norm of a residual stream (``based_rms_*``) and the choice of a next token
+(``based_sample``). Every step runs in the CUDA kernels of
 ``libbased_gb300.so``; there is no fallback. Arguments are checked and passed on by the compiled
 binding ``csrc/ops_binding.cpp``: wrong shapes, strides and devices raise ValueError, wrong types
 TypeError, and what the C functions refuse raises BasedError.
@@ -204,7 +206,7 @@ def based_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
 
     Heads of v share the HK heads of q and k in consecutive groups. ``scale`` defaults to K^-0.5. ``state`` (B,H,K,V)
     float32 is S before the first row (default zero); ``lengths`` (B) int32 marks rows t >= lengths[b] as padding
-    (zero output, state kept). Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the bytes
+    (zero output, state kept). An infinity or NaN leaves a head undefined from its chunk of 64 rows on. Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the bytes
     that based_delta_bwd needs, or None without ``save``). ``final_state`` may be ``state``, to update
     it in place. ``workspace``: a CUDA byte tensor of at least delta_workspace_size(...) bytes (default: one is allocated).
     """
