@@ -2,7 +2,8 @@
 //
 // With w_i = exp((x_i - max) / temperature), each of top-k, top-p and min-p keeps a prefix of the tokens in the order of falling
 // logits (equal ones by rising index), so what is kept is one comparison with a cut: the whole order is never needed. A row lies in the
-// shared memory of a cluster. One pass over it counts tokens (or sums masses) in 2048 bins of x's distance from the largest; the bin of the cut follows
+// shared memory of a cluster. A small top-k is cut among the tokens above a bound that the threads' largest ones give, and what it keeps is
+// sorted and summed by one CTA. Else one pass over the row counts tokens (or sums masses) in 2048 bins of x's distance from the largest; the bin of the cut follows
 // from the bins' sums, and the cut from the tokens of that bin, or of all bins up to it, which one CTA sorts. A last pass sums the kept masses by
 // warps, and the warp in which the random number falls finds the token. Masses are whole numbers, w 2^40 in 64 bits: their sums
 // do not depend on an order, so the same call gives the same token. Bound by the passes' instructions where there are many rows, by the
@@ -14,6 +15,7 @@ namespace {
 
 constexpr int kSampleThreads = 512, kSampleWarps = kSampleThreads / 32;
 constexpr int kBins = 2048, kFew = 2048;  // bins; tokens that one CTA sorts
+constexpr uint32_t kListed = 256;
 constexpr float kReach = 46.0f;           // the last bin begins at w = 2^-46
 constexpr float kMass = 1099511627776.0f; // 2^40
 constexpr int kSampleCluster = 16;
@@ -255,15 +257,24 @@ __device__ __forceinline__ u64 share_of(float share, u64 total) {
     return (high << (64 - shift) | low >> shift) + (UP && low << (64 - shift) ? 1 : 0);
 }
 
-// Moves the cut up: by count to the k'th token of those at or above it and, where `share` is below 1 and all of them could be sorted, on to the first
-// at which the masses reach that share of theirs (returns true); by mass (k is 0) to the latter.
+// The mass in front of the token that a random number takes
+__device__ __forceinline__ u64 target_of(float u, u64 all) {
+    const u64 target = u > 0.0f ? u < 1.0f ? share_of<false>(u, all) : all : 0;
+    return target >= all ? all - 1 : target;
+}
+
+// Moves the cut up: by count to the k'th token of those at or above it and, where all of those could be sorted, on to the first at which the masses
+// reach `share` of theirs (DONE; LISTED: the first CTA has them in `few`, found[2] of them, at most kListed); by mass (k is 0) to the latter.
+// quick: only each thread's largest, `top`, is counted. The k'th of those bounds the k'th of all, and in a row of any order but few tokens lie above
+// it. Where they do not fit (MANY) nothing is moved.
+enum Moved { CUT, DONE, LISTED, MANY };
 template <typename T>
-__device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut &cut) {
+__device__ Moved move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut &cut, bool quick, float top) {
     SampleShared &sh = s.sh;
     const SampleParams &p = s.p;
     const bool by_mass = k == 0;
     u64 last = 0;  // the last bin's tokens, which may be most, without atomics
-    s.each([&](float x, int i) {
+    const auto count = [&](float x, int i) {
         if (!cut.keeps(x, s.first + i)) return;
         const int bin = w.bin(x);
         if (by_mass) {
@@ -277,7 +288,11 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut 
         } else {
             atomicAdd(&sh.bins[0][bin], 1u);
         }
-    });
+    };
+    if (quick)
+        count(top, 0);
+    else
+        s.each(count);
     last = over_warp<false>(last);
     if (s.lane == 0 && last) by_mass ? add_mass(sh, kBins - 1, last) : static_cast<void>(atomicAdd(&sh.bins[0][kBins - 1], static_cast<uint32_t>(last)));
     s.meet();
@@ -325,8 +340,8 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut 
     for (int i = 0; i < 3; ++i) at[i] = s.tid == 0 ? sh.found[i] : 0;
     s.template total<3>(at);
     // fewer tokens than k: all are kept, and sorted where they are few
-    const bool enough = at[0] != 0, whole = !by_mass && (enough ? at[2] : all[0]) <= kFew;
-    if (!enough && !whole) return false;
+    const bool enough = at[0] != 0, whole = !by_mass && (quick || (enough ? at[2] : all[0]) <= kFew);
+    if (quick ? at[0] == 0 || at[0] == kBins : !enough && !whole) return quick ? MANY : CUT;
     const int bin = enough ? static_cast<int>(at[0]) - 1 : kBins - 1, low = whole ? 0 : bin;
     const float from = static_cast<float>(low), to = bin == kBins - 1 ? INFINITY : static_cast<float>(bin + 1);
     uint32_t hits = 0;  // of eight tokens: what follows is needed for few, so it is there once
@@ -348,11 +363,11 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut 
         }
     });
     s.meet();
-    if (s.tid == 0) sh.found[0] = sh.found[1] = 0;
+    if (s.tid == 0) sh.found[0] = sh.found[1] = sh.found[2] = 0;
     const uint32_t few = s.rank == 0 ? sh.count : 0;
     __syncthreads();
     if (s.rank == 0) {
-        if (s.tid == 0) sh.count = 0, sh.found[1] = few > kFew;
+        if (s.tid == 0) sh.count = 0, sh.found[1] = few > kFew, sh.found[2] = few;
         const int n = static_cast<int>(few);
         if (n > 0 && n <= kFew) {
             sort_few(sh, n);
@@ -381,12 +396,13 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut 
         }
     }
     __syncthreads();
-    u64 result[2] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0};
-    s.template total<2>(result);
+    u64 result[3] = {s.tid == 0 ? sh.found[0] : 0, s.tid == 0 ? sh.found[1] : 0, s.tid == 0 ? sh.found[2] : 0};
+    s.template total<3>(result);
     if (!result[1]) {
         raise(cut, result[0]);
-        return whole;
+        return !whole ? CUT : result[2] <= kListed ? LISTED : DONE;
     }
+    if (quick) return MANY;
     // Many tokens lie close together (equal logits, a high temperature): the cut bit by bit, the largest place with enough at or above it
     u64 found = 0;
     for (int bit = 63; bit >= 0; --bit) {
@@ -399,7 +415,50 @@ __device__ bool move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut 
         if (c[0] >= target) found = trial;
     }
     raise(cut, found);
-    return false;
+    return CUT;
+}
+
+// The token, by the first CTA alone, where move_cut has left it all that are kept. It sorts them again, by indices; above kListed that takes as long
+// as the passes over the row which it saves.
+template <typename T>
+__device__ void take_listed(const Sampler<T> &s, const Weigh &w, const Cut &cut, float min_p, int64_t n, const T *logits) {
+    SampleShared &sh = s.sh;
+    constexpr int kEach = kFew / kSampleThreads;
+    const int count = static_cast<int>(sh.found[2]), mine = s.tid * kEach;
+    u64 v[kEach], m[kEach], kept = 0, all;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        v[j] = 0, m[j] = sh.few.mass[mine + j];
+        if (mine + j < count) {
+            const u64 place = sh.few.place[mine + j];
+            const float x = unordered(static_cast<uint32_t>(place >> 32));
+            if (cut.keeps(x, static_cast<int>(0xffffffffu - static_cast<uint32_t>(place))) && w.weight(x) >= min_p) v[j] = place & 0xffffffffu, ++kept;
+        }
+    }
+    u64 at = cta_prefix(kept, sh.warp[0], all);  // (with barriers)
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        if (v[j]) sh.few.place[at] = v[j], sh.few.mass[at++] = m[j];
+    const int keep = static_cast<int>(all);
+    __syncthreads();
+    sort_few(sh, keep);  // by rising indices
+    u64 sum = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        v[j] = mine + j < keep ? sh.few.mass[mine + j] : 0;
+        sum += v[j];
+    }
+    u64 now = cta_prefix(sum, sh.warp[0], all);
+    const u64 target = target_of(s.p.u[n], all);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        if (now <= target && now + v[j] > target) {
+            const int token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(sh.few.place[mine + j]));
+            s.p.tokens[n] = token;
+            if (s.p.probs) s.p.probs[n] = static_cast<float>(static_cast<double>(w.weight(to_f32(logits[token]))) * kMass / static_cast<double>(all));
+        }
+        now += v[j];
+    }
 }
 
 template <typename T>
@@ -471,15 +530,27 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     if (!(top_p < 1.0f)) top_p = 1.0f;
     if (top_p <= 0.0f) k = 1, top_p = 1.0f;
     Cut cut;
-    bool done = top_p >= 1.0f;
-    if (k < p.V) done |= move_cut(s, w, k, top_p, cut);
-    if (!done) {
-        if (k < p.V) {  // the bins again
-            for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) sh.bins[0][i] = 0;
-            __syncthreads();
+    const auto clear = [&] {
+        for (int i = threadIdx.x; i < 3 * kBins; i += kSampleThreads) sh.bins[0][i] = 0;
+        __syncthreads();
+    };
+    // (256 x 50000 bf16: top-k 50 by the threads' largest 54 us, by all tokens 73; 61 x 130000 float32: 46 and 60, but top-k 1000, where more lies above
+    // their bound and is sorted, 118 and 93)
+    Moved moved = MANY;
+    if (k < p.V) {
+        if (k <= static_cast<int>(kListed) && 2 * k <= p.cluster * kSampleThreads) moved = move_cut(s, w, k, top_p, cut, true, top);
+        if (moved == MANY) {
+            clear();
+            moved = move_cut(s, w, k, top_p, cut, false, top);
         }
-        move_cut(s, w, 0, top_p, cut);
+        if (moved == LISTED) {
+            s.meet();
+            if (rank == 0) take_listed(s, w, cut, min_p, n, src);
+            return;
+        }
+        if (moved == CUT && top_p < 1.0f) clear();
     }
+    if (moved != DONE && top_p < 1.0f) move_cut(s, w, 0, top_p, cut, false, top);
     const auto kept = [&](float x, int i) -> float {
         if (!cut.keeps(x, first + i)) return 0.0f;
         const float v = w.weight(x);
@@ -496,8 +567,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     for (int i = begin + 8 * s.lane; i < to; i += 256) sum[0] += mass_of(i, to);
     s.template total<1>(sum, before);  // leaves the warps' sums in sh.warp
     const float u = p.u[n];
-    u64 target = u > 0.0f ? u < 1.0f ? share_of<false>(u, sum[0]) : sum[0] : 0;
-    if (target >= sum[0]) target = sum[0] - 1;
+    const u64 target = target_of(u, sum[0]);
     // the warp at which the sum passes the target, then its round, lane and token
     u64 at = before[0];
     for (int i = 0; i < s.warp; ++i) at += sh.warp[0][i];

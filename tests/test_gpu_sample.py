@@ -164,3 +164,28 @@ def test_batches_give_what_rows_alone_give(cuda_device):
             t, p = based_sample(x[i:i + 1], u[i:i + 1], **limits)
             # (without a cut the sums of eight tokens' masses may fall on other eights: the border moves by 2^-22)
             assert t.item() == got[i].item() and abs(p.item() - probs[i].item()) <= 2.0 ** -22 * p.item()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_few_kept_tokens_in_rows_of_any_order(cuda_device, dtype):
+    """A small top_k is cut by the threads' largest tokens where those bound it well: rows that are in order, rows whose largest
+    tokens lie side by side or in one thread's reach, and rows with fewer tokens than it are cut by all of them."""
+    x = row(20000, F32, 3).sort()[0].to(dtype)
+    for y in (x, x.flip(0), torch.roll(x, 777)):
+        for k in (1, 2, 40, 255, 256, 257, 300, 511, 512, 513, 2047, 2049):
+            check(y, top_k=k)
+        check(y, top_k=64, top_p=0.9, min_p=0.02, temperature=0.7)
+    y = torch.full((20000,), -math.inf).to(dtype)
+    y[4096:4136] = row(40, dtype, 4)
+    y[9] = math.nan
+    for k in (1, 7, 39, 40, 41, 200):
+        check(y, top_k=k)
+        check(y, top_k=k, top_p=0.8)
+    z = row(20000, dtype, 5)
+    z[8000:8512] = z.max() + 1  # more equal ones than top_k
+    check(z, top_k=100)
+    check(z, top_k=100, top_p=0.5, min_p=0.5)
+    z[8000:8512] -= torch.arange(512).to(dtype) * 2.0 ** -6
+    check(z, top_k=100, top_p=0.9)
+    check(z, top_k=100, temperature=1e-3)
+    check(z, top_k=100, temperature=50.0)
