@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
     Weigh w;
     w.most = most, w.hi = 1.44269502f / temperature, w.lo = (fmaf(-w.hi, temperature, 1.44269502f) + 1.92596303e-8f) / temperature;
     if (!(w.hi < 3e38f)) w.hi = 3e38f, w.lo = 0.0f;
+    if (temperature == INFINITY) w.lo = 0.0f;  // (hi is 0: all alike)
     int k = p.top_k ? p.top_k[n] : p.top_k_all;
     float top_p = p.top_p ? p.top_p[n] : p.top_p_all;
     float min_p = p.min_p ? p.min_p[n] : p.min_p_all;

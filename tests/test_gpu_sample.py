@@ -189,3 +189,21 @@ def test_few_kept_tokens_in_rows_of_any_order(cuda_device, dtype):
     check(z, top_k=100, top_p=0.9)
     check(z, top_k=100, temperature=1e-3)
     check(z, top_k=100, temperature=50.0)
+
+
+def test_an_infinite_temperature_weighs_all_alike(cuda_device):
+    x = row(3000, F32)
+    x[:1000] = -math.inf
+    for limits in ({}, dict(top_k=9), dict(top_k=2500), dict(top_p=0.5001), dict(top_k=600, top_p=0.3003)):
+        check(x, temperature=math.inf, **limits)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+def test_rows_that_no_cluster_holds(cuda_device, dtype):
+    x = row(4000003, dtype, 6, 3.0)
+    for limits in (dict(top_k=60), dict(top_k=60, top_p=0.9, min_p=0.01), dict(top_k=300), dict(min_p=0.3), dict(temperature=0.0)):
+        if limits.get("temperature") == 0.0:
+            got, p = based_sample(x.cuda()[None], torch.full((1,), 0.3, device="cuda"), **limits)
+            assert got.item() == int(x.float().argmax()) and p.item() == 1
+        else:
+            check(x, **limits)
