@@ -292,3 +292,23 @@ def test_empty_batches(cuda_device):
         assert torch.equal(grads[-1], dfinal[cut]) and all(g.numel() == 0 for g in grads[:-1])
     none = {n: t[:0, 0] for n, t in s.items()}
     assert based_delta_step(**none, pool=more["state"]).shape == (0, 2, 8)
+
+
+def test_more_sequences_than_a_grid_holds(cuda_device):
+    """Above 65535 sequences a CTA goes through several, of different lengths: they give what a call of their own gives, bit for bit."""
+    B, T, H, K, V = 66000, 65, 1, 8, 70  # five slices: a CTA of four and one of one with three idle
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    q, k, v, do = rand(B, T, H, K), rand(B, T, H, K) * 0.3, rand(B, T, H, V), rand(B, T, H, V)
+    beta, gate = torch.rand(B, T, H, generator=gen, device="cuda").to(BF16), -torch.rand(B, T, H, generator=gen, device="cuda").to(BF16)
+    state = torch.randn(B, H, K, V, generator=gen, device="cuda")
+    lengths = torch.randint(-1, T + 2, (B,), generator=gen, device="cuda").to(torch.int32)
+
+    def run(at):
+        s = [t[at] for t in (q, k, v, beta, gate)]
+        o, final, saved = based_delta_fwd(*s, state=state[at], lengths=lengths[at], save=True)
+        return o, final, *based_delta_bwd(*s, do[at], saved, dfinal=state[at], lengths=lengths[at])
+
+    whole = run(slice(0, B))
+    for at in (slice(0, 600), slice(B - 65535 - 100, B - 65535 + 100), slice(B - 600, B)):
+        assert all(torch.equal(a[at], b) for a, b in zip(whole, run(at)))
