@@ -109,6 +109,16 @@ __device__ __forceinline__ void load_weight(float (&w)[kPack], const RmsParams &
     for (int e = 0; e < kPack; ++e) w[e] = !p.weight ? 1.0f : p.p_dtype == BASED_F32 ? b[e] : a[e];
 }
 
+__host__ __device__ constexpr int cta_of(int threads) { return threads < 256 ? 256 : threads; }
+
+// The threads of a row meet; the CTA's other rows go on.
+template <int THREADS>
+__device__ __forceinline__ void meet_row() {
+    if constexpr (THREADS < cta_of(THREADS))
+        named_bar_sync(1 + threadIdx.x / THREADS, THREADS);
+    else
+        __syncthreads();
+}
 // The sum or the largest of v over the THREADS threads of a row; red: 32 floats of the CTA, two rows of them used in turn
 template <int THREADS, bool MOST>
 __device__ __forceinline__ float over_row(float v, float *red, int &turn) {
@@ -122,7 +132,7 @@ __device__ __forceinline__ float over_row(float v, float *red, int &turn) {
         float *const at = red + turn * 32 + threadIdx.x / THREADS * kWarps;
         turn ^= 1;
         if ((threadIdx.x & 31) == 0) at[threadIdx.x % THREADS / 32] = v;
-        __syncthreads();
+        meet_row<THREADS>();
         v = at[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) v = MOST ? fmaxf(v, at[i]) : v + at[i];
@@ -140,15 +150,13 @@ __device__ __forceinline__ void over_row2(float &a, float &b, float *red, int &t
         float2 *const at = reinterpret_cast<float2 *>(red) + turn * 16 + threadIdx.x / THREADS * kWarps;
         turn ^= 1;
         if ((threadIdx.x & 31) == 0) at[threadIdx.x % THREADS / 32] = make_float2(a, b);
-        __syncthreads();
+        meet_row<THREADS>();
         float2 v = at[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) v.x += at[i].x, v.y += at[i].y;
         a = v.x, b = v.y;
     }
 }
-
-__host__ __device__ constexpr int cta_of(int threads) { return threads < 256 ? 256 : threads; }
 
 template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
 __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParams p) {
