@@ -169,19 +169,28 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
 #pragma unroll
     for (int j = 0; j < PACKS; ++j) load_weight<T, WORDS>(w[j], p, t, THREADS, j);
     const float mean = 1.0f / p.C;
+    // The next row's loads go out in front of a row's sums where registers hold both
+    constexpr bool kAhead = WORDS && PACKS * (sizeof(T) + sizeof(S)) <= 12;
+    Raw<WORDS, T> x[PACKS];
+    Raw<WORDS, S> r[PACKS];
+    const auto load = [&](int64_t row) {
+        const int C = row < p.R ? p.C : 0;
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) x[j].load(static_cast<const T *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+        if (p.residual) {
+#pragma unroll
+            for (int j = 0; j < PACKS; ++j) r[j].load(static_cast<const S *>(p.residual) + row * p.res_sr, t, THREADS, j, C);
+        }
+    };
+    if (kAhead) load(static_cast<int64_t>(blockIdx.x) * kRows + slot);
     // all threads of the CTA go round equally often: rows behind the last are computed as zeros and not stored
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.R; first += static_cast<int64_t>(gridDim.x) * kRows) {
         const int64_t row = first + slot;
         const bool there = row < p.R;
         const int C = there ? p.C : 0;
         float s[PACKS][kPack], sq = 0.0f;
-        Raw<WORDS, T> x[PACKS];
-#pragma unroll
-        for (int j = 0; j < PACKS; ++j) x[j].load(static_cast<const T *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+        if (!kAhead) load(row);
         if (p.residual) {
-            Raw<WORDS, S> r[PACKS];
-#pragma unroll
-            for (int j = 0; j < PACKS; ++j) r[j].load(static_cast<const S *>(p.residual) + row * p.res_sr, t, THREADS, j, C);
 #pragma unroll
             for (int j = 0; j < PACKS; ++j)
 #pragma unroll
@@ -192,6 +201,7 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
 #pragma unroll
                 for (int e = 0; e < kPack; ++e) s[j][e] = x[j][e];
         }
+        if (kAhead) load(row + static_cast<int64_t>(gridDim.x) * kRows);
         if (p.residual) {
 #pragma unroll
             for (int j = 0; j < PACKS; ++j) store_pack<WORDS>(static_cast<S *>(p.sum) + row * p.C, s[j], t, THREADS, j, C);
@@ -200,13 +210,13 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
         for (int j = 0; j < PACKS; ++j)
 #pragma unroll
             for (int e = 0; e < kPack; ++e) sq = fmaf(s[j][e], s[j][e], sq);
-        const float r = rsqrtf(over_row<THREADS, false>(sq, red, turn) * mean + p.eps);
+        const float norm = rsqrtf(over_row<THREADS, false>(sq, red, turn) * mean + p.eps);
         float most = 0.0f;
 #pragma unroll
         for (int j = 0; j < PACKS; ++j)
 #pragma unroll
             for (int e = 0; e < kPack; ++e) {
-                s[j][e] = s[j][e] * r * w[j][e];
+                s[j][e] = s[j][e] * norm * w[j][e];
                 asm("max.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(most), "f"(fabsf(s[j][e])));
             }
         if (p.scales) {
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_fwd_kernel(RmsParam
 }
 
 template <typename T, typename S, int THREADS, int PACKS, bool WORDS>
-__global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParams p) {
+__global__ void __launch_bounds__(cta_of(THREADS), cta_of(THREADS) == 256 ? 2 : 1) based_rms_bwd_kernel(RmsParams p) {
     constexpr int kCta = cta_of(THREADS), kRows = kCta / THREADS;
     __shared__ __align__(8) float red[64];
     extern __shared__ float sums[];  // rows' threads' sums of the weights' gradient, where a CTA takes several rows
@@ -238,19 +248,30 @@ __global__ void __launch_bounds__(cta_of(THREADS)) based_rms_bwd_kernel(RmsParam
 #pragma unroll
     for (int j = 0; j < PACKS; ++j) load_weight<T, WORDS>(w[j], p, t, THREADS, j);
     const float mean = 1.0f / p.C;
+    constexpr bool kAhead = WORDS && PACKS * (sizeof(T) + 2 * sizeof(S)) <= 12;  // as forward
+    Raw<WORDS, S> ns[PACKS], ng[PACKS];
+    Raw<WORDS, T> nd[PACKS];
+    const auto load = [&](int64_t row) {
+        const int C = row < p.R ? p.C : 0;
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) {
+            ns[j].load(static_cast<const S *>(p.x) + row * p.x_sr, t, THREADS, j, C);
+            nd[j].load(static_cast<const T *>(p.dy) + row * p.dy_sr, t, THREADS, j, C);
+        }
+#pragma unroll
+        for (int j = 0; j < PACKS; ++j) ng[j].load(static_cast<const S *>(p.dsum) + row * p.dsum_sr, t, THREADS, j, p.dsum ? C : 0);
+    };
+    if (kAhead) load(static_cast<int64_t>(blockIdx.x) * kRows + slot);
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.R; first += static_cast<int64_t>(gridDim.x) * kRows) {
         const int64_t row = first + slot;
         const int C = row < p.R ? p.C : 0;
         Raw<WORDS, S> s[PACKS], g[PACKS];
         Raw<WORDS, T> d[PACKS];
         float sq = 0.0f, ds = 0.0f;
+        if (!kAhead) load(row);
 #pragma unroll
-        for (int j = 0; j < PACKS; ++j) {
-            s[j].load(static_cast<const S *>(p.x) + row * p.x_sr, t, THREADS, j, C);
-            d[j].load(static_cast<const T *>(p.dy) + row * p.dy_sr, t, THREADS, j, C);
-        }
-#pragma unroll
-        for (int j = 0; j < PACKS; ++j) g[j].load(static_cast<const S *>(p.dsum) + row * p.dsum_sr, t, THREADS, j, p.dsum ? C : 0);
+        for (int j = 0; j < PACKS; ++j) s[j] = ns[j], g[j] = ng[j], d[j] = nd[j];
+        if (kAhead) load(row + static_cast<int64_t>(gridDim.x) * kRows);
 #pragma unroll
         for (int j = 0; j < PACKS; ++j)
 #pragma unroll
@@ -339,9 +360,10 @@ int launch_bwd(RmsParams &p, cudaStream_t st) {
     }
     return BASED_OK;
 }
-// Threads for a row: as few as hold it in four packs each (three where that fits better), so that a warp or a part of one serves short rows and
-// sums stay in it. Backward, with three inputs and the weights' gradients in registers, two packs: 24000 x 1536
-// takes 64 us, with four 79.
+// Threads for a row: as few as hold it in two packs each, which leaves registers for the next row's loads (three where that fits better and both
+// streams have 16 bits), so that a warp or a part of one serves short rows and sums stay in it. bf16, with the next row ahead and without: 29296 x 2048 75 us (four packs
+// 84), 7324 x 8192 81 (109), a float32 stream of 20000 x 3000 114 (134); only a float32 stream of 4096 channels does better in four packs without
+// it (14648 rows: 111 us instead of 122). Backward 24000 x 1536 51 us, without 64, with four packs 79. Single channels, not words, go by four or two packs.
 template <typename T, typename S>
 int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
     const int packs = (p.C + kPack - 1) / kPack;
@@ -368,13 +390,16 @@ int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
     if (packs <= 8) return launch_fwd<T, S, 8, 1, true>(p, sms, st);
     if (packs <= 32) return launch_fwd<T, S, 16, 2, true>(p, sms, st);
     if (packs <= 64) return launch_fwd<T, S, 32, 2, true>(p, sms, st);
-    if (packs <= 128) return launch_fwd<T, S, 32, 4, true>(p, sms, st);
-    if (packs <= 192) return launch_fwd<T, S, 64, 3, true>(p, sms, st);
-    if (packs <= 256) return launch_fwd<T, S, 64, 4, true>(p, sms, st);
-    if (packs <= 384) return launch_fwd<T, S, 128, 3, true>(p, sms, st);
-    if (packs <= 512) return launch_fwd<T, S, 128, 4, true>(p, sms, st);
-    if (packs <= 768) return launch_fwd<T, S, 256, 3, true>(p, sms, st);
-    if (packs <= 1024) return launch_fwd<T, S, 256, 4, true>(p, sms, st);
+    if (packs <= 128) return launch_fwd<T, S, 64, 2, true>(p, sms, st);
+    if constexpr (sizeof(S) == 2)
+        if (packs <= 192) return launch_fwd<T, S, 64, 3, true>(p, sms, st);
+    if (packs <= 256) return launch_fwd<T, S, 128, 2, true>(p, sms, st);
+    if constexpr (sizeof(S) == 2)
+        if (packs <= 384) return launch_fwd<T, S, 128, 3, true>(p, sms, st);
+    if constexpr (sizeof(S) == 4)
+        if (packs > 384 && packs <= 512) return launch_fwd<T, S, 128, 4, true>(p, sms, st);
+    if (packs <= 512) return launch_fwd<T, S, 256, 2, true>(p, sms, st);
+    if (packs <= 1024) return launch_fwd<T, S, 512, 2, true>(p, sms, st);
     return launch_fwd<T, S, 512, 4, true>(p, sms, st);
 }
 
