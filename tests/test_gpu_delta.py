@@ -168,7 +168,9 @@ def test_chunks_of_a_sequence_one_after_the_other(cuda_device):
 
 
 @pytest.mark.parametrize("N,S,H,HK,K,V,dtype", [(1, 1, 1, 1, 1, 1, F32), (3, 7, 4, 2, 128, 64, BF16), (5, 5, 2, 2, 37, 75, F16),
-                                              (2, 9, 3, 1, 128, 33, F32)])
+                                              (2, 9, 3, 1, 128, 33, F32), (3, 7, 4, 2, 32, 226, BF16), (2, 4, 2, 2, 20, 131, F32),
+                                              (4, 6, 2, 1, 64, 36, F16), (2, 3, 2, 1, 33, 130, F32), (3, 4, 2, 2, 32, 128, BF16),
+                                              (2, 5, 2, 1, 64, 97, F32)])
 def test_step(cuda_device, N, S, H, HK, K, V, dtype):
     s, _, _, _ = inputs(N, 1, H, HK, K, V, dtype, seed=N)
     gen = torch.Generator().manual_seed(1)
