@@ -185,17 +185,16 @@ struct Sampler {
 // w = 2^-t, t = (most - x) log2(e) / temperature, with the product's rounding made good
 struct Weigh {
     float most, hi, lo;
-    // the bin, as a number whose whole part it is
-    __device__ __forceinline__ float place(float x) const { return (most - x) * hi * (kBins / kReach); }
+    // The bin, as a number whose whole part it is. The last one takes all that is far below the largest, also where the product is beyond
+    // float32 (a type's lowest value as a mask, a small temperature) or no number (a difference beyond it, an infinite temperature).
+    __device__ __forceinline__ float place(float x) const { return fminf((most - x) * hi * (kBins / kReach), kBins - 1.0f); }
     __device__ __forceinline__ float weight(float x) const {
         const float d = most - x, t = d * hi, r = fmaf(d, hi, -t) + d * lo;
         const float w = ex2(-t);
         return t < 120.0f ? fmaf(w, -0.6931471806f * r, w) : 0.0f;
     }
     __device__ __forceinline__ u64 mass(float x) const { return static_cast<u64>(__float2ull_rn(weight(x) * kMass)); }
-    __device__ __forceinline__ int bin(float x) const {
-        return static_cast<int>(fminf(place(x), kBins - 1.0f));
-    }
+    __device__ __forceinline__ int bin(float x) const { return static_cast<int>(place(x)); }
 };
 
 // Prefix sums over the CTA, in the order of threads; all: the sum
@@ -343,11 +342,11 @@ __device__ Moved move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut
     const bool enough = at[0] != 0, whole = !by_mass && (quick || (enough ? at[2] : all[0]) <= kFew);
     if (quick ? at[0] == 0 || at[0] == kBins : !enough && !whole) return quick ? MANY : CUT;
     const int bin = enough ? static_cast<int>(at[0]) - 1 : kBins - 1, low = whole ? 0 : bin;
-    const float from = static_cast<float>(low), to = bin == kBins - 1 ? INFINITY : static_cast<float>(bin + 1);
+    const float from = static_cast<float>(low), to = static_cast<float>(bin + 1);
     uint32_t hits = 0;  // of eight tokens: what follows is needed for few, so it is there once
     s.each([&](float x, int i) {
         const float b = w.place(x);
-        if (b < to && (b >= from || from == 0.0f) && cut.keeps(x, s.first + i)) hits |= 1u << (i & 7);
+        if (b < to && b >= from && cut.keeps(x, s.first + i)) hits |= 1u << (i & 7);
     }, [&](int i0) {
         while (hits) {
             const int i = i0 + __ffs(hits) - 1;
@@ -371,9 +370,9 @@ __device__ Moved move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut
         const int n = static_cast<int>(few);
         if (n > 0 && n <= kFew) {
             sort_few(sh, n);
-            // the k'th of all, or what is behind the bins in front
+            // the k'th of all, or what is behind the bins in front: no more than are listed
             const u64 base = whole ? 0 : at[1];
-            const int nth = by_mass || !enough ? n : static_cast<int>(static_cast<u64>(k) - base);
+            const int nth = by_mass || !enough ? n : min(n, static_cast<int>(static_cast<u64>(k) - base));
             if (share < 1.0f && (by_mass || whole)) {
                 u64 m[kFew / kSampleThreads], sums = 0, up_to;
 #pragma unroll
