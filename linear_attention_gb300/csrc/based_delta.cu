@@ -6,6 +6,7 @@
 // the chunk, D_ij = exp(b_i - b_j) for j <= i, S0 the state in front, grow_i = exp(b_i) and rest_i = exp(b_last - b_i):
 //     X = V - grow K S0,   E = (1 + L)^-1 X with L_ij = D_ij (k_i k_j) beta_j below the diagonal,   U = beta E,
 //     O = scale grow Q S0 + P U with P_ij = scale D_ij (q_i k_j),   S = grow_last S0 + (rest K)^T U.
+// The inverse's diagonal of ones is left to the float32 registers that X lies in: its product is only what other rows add.
 // based_delta_prep_kernel has all that does not depend on the state (the inverse and P), for all chunks at once;
 // based_delta_fwd_kernel runs through the chunks. Backward, with G the gradient of the state behind the chunk and
 // A_ij = beta_i D_ij (k_i k_j) below the diagonal:
@@ -30,7 +31,7 @@ template <typename T, int KP>
 struct PrepSmem {
     static constexpr int images = Rec<T, KP>::qk, work = (2 * kChunk * kLd + 32 * 36) * 4;
     static constexpr int shared = images > work ? images : work;  // the images, then the inverse's work in their place
-    static constexpr int bytes = shared + (8 * kChunk + 16) * 4;
+    static constexpr int bytes = shared + (9 * kChunk + 16) * 4;
 };
 
 // Rows of q or k into their images, in shared memory and in the record; returns the scale's inverse.
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based
     extern __shared__ __align__(128) uint8_t smem[];
     float *const m = reinterpret_cast<float *>(smem), *const h = m + kChunk * kLd, *const w = h + kChunk * kLd;
     float *const bhi = reinterpret_cast<float *>(smem + Sm::shared), *const blo = bhi + kChunk, *const beta = blo + kChunk, *const till = beta + kChunk,
-                *const since = till + kChunk, *const red = since + 4 * kChunk;
+                *const over = till + kChunk, *const since = over + kChunk, *const red = since + 4 * kChunk;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = blockIdx.x, hk = blockIdx.y, group = p.H / p.HK;
     griddep_wait();
@@ -196,14 +197,17 @@ __global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based
                 const int i = 2 * lane + e;
                 const Two v = plus(before, x[e]);
                 const float grow = expf(v.hi + v.lo), rest = expf((last.hi - v.hi) + (last.lo - v.lo)), y = be[e];
-                bhi[i] = v.hi, blo[i] = v.lo, beta[i] = y, till[i] = expf((end.hi - v.hi) + (end.lo - v.lo));
-                f[F_GROW + i] = grow, f[F_REST + i] = rest, f[F_BETA + i] = y, f[F_BHI + i] = v.hi, f[F_BLO + i] = v.lo;
-                f[F_BF + i] = y * (BWD ? grow : rest);
-                most = fmaxf(most, fabsf(y * (BWD ? grow : rest))), grow_most = fmaxf(grow_most, grow);
+                const float step = BWD ? 1.0f : step_of(y), bf = BWD ? y * grow : y * inverse_of(step) * rest;
+                bhi[i] = v.hi, blo[i] = v.lo, beta[i] = y, over[i] = inverse_of(step), till[i] = expf((end.hi - v.hi) + (end.lo - v.lo));
+                f[F_GROW + i] = grow, f[F_REST + i] = BWD ? rest : grow * step, f[F_BETA + i] = BWD ? y : step;
+                f[F_BHI + i] = v.hi, f[F_BLO + i] = v.lo, f[F_BF + i] = bf;
+                most = fmaxf(most, fabsf(bf)), grow_most = fmaxf(grow_most, grow);
             }
-            most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-            grow_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(grow_most)));
-            if (lane == 0) f[F_WHOLE] = expf(last.hi + last.lo), f[F_BFMOST] = most, f[F_GROWMOST] = grow_most;
+#pragma unroll
+            for (int d = 1; d < 8; d *= 2)
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d)), grow_most = fmaxf(grow_most, __shfl_xor_sync(0xffffffffu, grow_most, d));
+            if (lane % 8 == 0) f[F_BFMOST + lane / 8] = most, f[F_GROWMOST + lane / 8] = grow_most;
+            if (lane == 0) f[F_WHOLE] = expf(last.hi + last.lo);
         };
         __syncthreads();  // the batch entry before
         float ik, iq;
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based
                         for (int e = 0; e < 4; ++e) pv[nt][e] = 0.0f;
                         continue;
                     }
-                    const float2 jb = *reinterpret_cast<const float2 *>(beta + c);
+                    const float2 jb = *reinterpret_cast<const float2 *>(beta + c), jo = *reinterpret_cast<const float2 *>(over + c);
                     float d[4];
                     if (block < wm) {  // D_ij by the last row of j's 16: two factors
                         const float2 t = *reinterpret_cast<const float2 *>(till + c);
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based
                     for (int e = 0; e < 4; ++e) {
                         const int i = r0 + 8 * (e / 2), j = c + e % 2;
                         const float bj = e % 2 ? jb.y : jb.x;
-                        pv[nt][e] = j <= i ? d[e] * (sq[nt][e] * fq) * (BWD ? 1.0f : bj) : 0.0f;
+                        pv[nt][e] = j <= i ? d[e] * (sq[nt][e] * fq) * (BWD ? 1.0f : bj * (e % 2 ? jo.y : jo.x)) : 0.0f;
                         y[e] = j < i ? d[e] * (sk[nt][e] * fk) * (BWD ? bi[e / 2] : bj) : 0.0f;
                         most = fmaxf(most, fabsf(pv[nt][e]));
                     }
@@ -325,6 +329,12 @@ __global__ void __launch_bounds__(32 * kPrepWarps, sizeof(T) == 2 ? 4 : 2) based
                 const float4 *const from = reinterpret_cast<const float4 *>(h + (tid / 8 + 32 * r) * kLd + tid % 8 * 8);
                 const float4 u = from[0], v = from[1];
                 x[r][0] = u.x, x[r][1] = u.y, x[r][2] = u.z, x[r][3] = u.w, x[r][4] = v.x, x[r][5] = v.y, x[r][6] = v.z, x[r][7] = v.w;
+                const float step = inverse_of(over[tid / 8 + 32 * r]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = tid % 8 * 8 + e;
+                    x[r][e] = j < tid / 8 + 32 * r ? x[r][e] * (BWD ? 1.0f : over[j] * step) : 0.0f;
+                }
                 most = most8(most, x[r]);
             }
             const float sh = scale_for(cta_most<kPrepWarps>(most, red));
@@ -477,20 +487,24 @@ __device__ __forceinline__ void write_state(float *p, const Acc (&s)[N], int k0,
             if (k < K && v < V) p[static_cast<int64_t>(k) * V + v] = s[j][e];
         }
 }
-// Columns of two blocks times f[column]
+// Columns of two blocks times f[column] (and c)
+__device__ __forceinline__ void by_columns(Acc (&x)[2], const float *f, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) by_pairs(x[i], *reinterpret_cast<const Vec<2> *>(f + 8 * i + 2 * (lane & 3)));
+}
 __device__ __forceinline__ void by_columns(Acc (&x)[2], const float *f, float c, int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 y = *reinterpret_cast<const float2 *>(f + 8 * i + 2 * (lane & 3));
-        x[i][0] *= y.x * c, x[i][1] *= y.y * c, x[i][2] *= y.x * c, x[i][3] *= y.y * c;
-    }
+    for (int i = 0; i < 2; ++i) by_pairs(x[i], vmul(*reinterpret_cast<const Vec<2> *>(f + 8 * i + 2 * (lane & 3)), splat<2>(c)));
+}
+template <int N>
+__device__ __forceinline__ void scale_all(Acc (&x)[N], float c) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) by_pairs(x[i], splat<2>(c));
 }
 template <int N>
 __device__ __forceinline__ void add(Acc (&x)[N], const Acc (&t)[N], float c) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][e] = fmaf(t[i][e], c, x[i][e]);
+    for (int i = 0; i < N; ++i) add_times(x[i], t[i], c);
 }
 // Left operands, handed over through shared memory or left in a record
 template <int TERMS>
@@ -572,6 +586,21 @@ struct Stages {
     }
 };
 
+// Operands of another scale than what they are added up with come to the largest's by a power of two: what that takes from their last bits
+// is below the sum's. The exponent of a power of two, and 2^e for e <= 0 as two halves
+__device__ __forceinline__ int exponent(float pow2) { return static_cast<int>(__float_as_uint(pow2) >> 23) - 127; }
+__device__ __forceinline__ uint32_t halves(int e) {
+    const uint32_t h = e >= -14 ? static_cast<uint32_t>(15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
+    return h | h << 16;
+}
+template <int TERMS>
+__device__ __forceinline__ void times(uint32_t (&to)[TERMS][4], const uint32_t (&a)[TERMS][4], uint32_t f) {
+#pragma unroll
+    for (int j = 0; j < TERMS; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(to[j][i]) : "r"(a[j][i]), "r"(f));
+}
+
 // What both directions have in common: this warp's place, and the parts of shared memory
 template <typename T, int KP, bool BWD>
 struct Seq {
@@ -581,7 +610,8 @@ struct Seq {
     const DeltaParams &p;
     uint8_t *smem, *mine;  // the records; the slice's
     int lane, w, slice, head, hk, v0, cols;
-    float *sc;  // the state's quarters' largest as inverse scales; the inverse scale of its operands; of 16 rows of x, and of e backward
+    float *sc;  // inverse scales of operands
+    enum { SC_QUARTER = 0, SC_X = 4, SC_E = 8, SC_U = 12, SC_W = 16, SC_STATE = 20 };  // of each quarter, of 16 rows of x, e, u and w each, of the state
     uint8_t *tiles;
 
     __device__ __forceinline__ Seq(const DeltaParams &p_, uint8_t *smem_) : p(p_), smem(smem_) {
@@ -594,11 +624,17 @@ struct Seq {
         tiles = mine + Sm::scales + 128 + 2 * w * Sm::tile;
     }
     __device__ __forceinline__ void meet() const { named_bar_sync(1 + threadIdx.x / kQuad, kQuad); }
-    // A bound on the state's magnitudes, from its warps' largest
-    __device__ __forceinline__ float state_most() const { return kTop * fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])); }
-    // The quarter's left operands, scaled for magnitudes up to `most`, for the others and for the record; and its own largest
-    __device__ __forceinline__ void hand_over(const Acc (&s)[2 * kSteps], float most, uint8_t *rec, float *rec_scales) const {
-        const float f = scale_for(most), own = inverse_of(warp_scale(s));
+    // The largest of this warp's quarter of the state, as an inverse scale; and, once all four are known, the quarter's left operands for the others and
+    // for the record. Operands are scaled by what they hold, not by bounds from what they are made of: the largest factors may belong to different rows
+    // (a token masked by beta 0, values in front of a cleared state). By such bounds 1 x 16384 rows of 16 heads of 128 x 128 took 581 us where this takes 627, and
+    // 8 x 4096 rows in training 2336 where this takes 2385, but a masked row 10^4 times the others cost the results behind it all but 11 bits.
+    __device__ __forceinline__ void measure(const Acc (&s)[2 * kSteps]) const {
+        const float own = inverse_of(warp_scale(s));
+        if (lane == 0) sc[SC_QUARTER + w] = own;
+    }
+    __device__ __forceinline__ void hand_over(const Acc (&s)[2 * kSteps], uint8_t *rec, float *rec_scale) const {
+        const float4 of = *reinterpret_cast<const float4 *>(sc + SC_QUARTER);
+        const float inverse = fmaxf(fmaxf(of.x, of.y), fmaxf(of.z, of.w)), f = inverse_of(inverse);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             uint32_t a[2][4];
@@ -606,20 +642,22 @@ struct Seq {
             give<2>(mine + Sm::state + (w * kSteps + i) * 1024, a, lane);
             if (rec) leave<NO>(rec + (w * kSteps + i) * 512, SliceRec<T, KP>::state_term, a, lane);
         }
-        if (lane == 0) {
-            sc[w] = own;
-            if (w == 0) sc[4] = inverse_of(f);
-            if (rec && w == 0) rec_scales[0] = inverse_of(f);
+        if (lane == 0 && w == 0) {
+            sc[SC_STATE] = inverse;
+            if (rec) *rec_scale = inverse;
         }
     }
-    // The first state: its largest is found first
-    __device__ __forceinline__ void begin(const Acc (&s)[2 * kSteps], uint8_t *rec, float *rec_scales) const {
-        const float own = inverse_of(warp_scale(s));
-        if (lane == 0) sc[w] = own;
-        meet();
-        const float most = state_most();
-        meet();
-        hand_over(s, most, rec, rec_scales);
+    // Rows' left operand, scaled by its own largest, for the others: at number `place` of sc, and of a record
+    template <int TERMS>
+    __device__ __forceinline__ void hand_rows(const Acc (&x)[2], float f, uint8_t *to, int place, uint8_t *rec = nullptr, float *rec_scale = nullptr) const {
+        uint32_t a[TERMS][4];
+        left_of<TERMS>(a, x[0], x[1], f);
+        if (to) give<TERMS>(to, a, lane);
+        if (rec) leave<TERMS>(rec, kRowsTerm, a, lane);
+        if (lane == 0) {
+            if (to) sc[place + w] = inverse_of(f);
+            if (rec) *rec_scale = inverse_of(f);
+        }
     }
 };
 
@@ -663,7 +701,9 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
         if (count > 0) {
             fetch(0), values(0);
             uint8_t *const rec = cols > 0 ? record(0) : nullptr;
-            q.begin(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
+            q.measure(s);
+            q.meet();
+            q.hand_over(s, rec, reinterpret_cast<float *>(rec + SR::fwd_scales));
         }
         for (int n = 0; n < count; ++n) {
             const int stage = turn + n & 1;
@@ -681,9 +721,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
             const uint32_t kimg = smem_u32(smem) + stage * kStage, qimg = kimg + R::img, inv = kimg + R::qk, pimg = inv + 2 * kSquare;
             const float *const f = reinterpret_cast<const float *>(smem + stage * kStage + R::qk + (2 + NO) * kSquare);
             uint8_t *const rec = record(n);
+            float *const rec_scales = reinterpret_cast<float *>(rec + SR::fwd_scales);
             Acc x[2], z[2], y[2];  // S0^T K^T, S0^T Q^T
             clear(x), clear(z);
-            const float is = q.sc[4], before = q.state_most();
+            const float is = q.sc[Q::SC_STATE];
             {
                 uint32_t a[2][2][4], r[2][NI][4], c[2][NI][4];
                 const auto load = [&](int kk) {
@@ -700,24 +741,18 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                     products<T, NO, NI>(z[0], z[1], reinterpret_cast<const uint32_t(&)[NO][4]>(a[kk & 1]), c[kk & 1]);
                 }
             }
-            by_columns(x, f + F_GROW + 16 * w, f[F_K] * is, lane);
+            by_columns(x, f + F_GROWSTEP + 16 * w, f[F_K] * is, lane);
             by_columns(z, f + F_GROW + 16 * w, f[F_Q] * p.scale * is, lane);
             read_tile<T>(y, tile, lane);
+            by_columns(y, f + F_STEP + 16 * w, lane);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[i][e] = y[i][e] - x[i][e];
-            {
-                const float sx = warp_scale(x);
-                uint32_t a[2][4];
-                left_of<2>(a, x[0], x[1], sx);
-                give<2>(q.mine + Sm::x(false) + w * 1024, a, lane);
-                if (lane == 0) q.sc[8 + w] = inverse_of(sx);
-            }
+            q.template hand_rows<2>(x, warp_scale(x), q.mine + Sm::x(false) + w * 1024, Q::SC_X);
             if (n + 1 < count && !alone) fetch(n + 1);
             q.meet();
-            clear(y);  // E
-            {
+            {  // E: X and what the rows in front have written. X and E are times their rows' steps from here on
                 uint32_t a[2][2][4], r[2][2][4];
                 const auto load = [&](int kb) {
                     take<2>(a[kb & 1], q.mine + Sm::x(false) + kb * 1024, lane);
@@ -728,27 +763,21 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 for (int kb = 0; kb < 4; ++kb) {
                     if (kb > w) break;
                     if (kb < 3) load(kb + 1);  // (of the last one nothing comes)
-                    Acc t[2];
-                    clear(t);
-                    products<T, 2, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
-                    add(y, t, q.sc[8 + kb] * f[F_INV]);
+                    products_by<2, 2>(x[0], x[1], a[kb & 1], r[kb & 1], q.sc[Q::SC_X + kb] * f[F_INV]);
                 }
             }
-            // All warps scale E and U for the same bounds, from X's and the inverse's largest, so that sums run over all rows
-            const float e_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
-            const float se = scale_for(e_most), u_most = e_most * f[F_BFMOST], su = scale_for(u_most);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i][e] = x[i][e];
+            by_columns(y, f + F_BF + 16 * w, lane);
             {
-                uint32_t a[NO][4], c[2][4];
-                left_of<NO>(a, y[0], y[1], se);
-                give<NO>(q.mine + Sm::e + w * Sm::e_block, a, lane);
-                if (rec) leave<NO>(rec + SR::e + w * 512, kRowsTerm, a, lane);
-                by_columns(y, f + F_BF + 16 * w, 1.0f, lane);
-                left_of<2>(c, y[0], y[1], su);
-                give<2>(q.mine + Sm::u + w * 1024, c, lane);
-                if (rec && lane == 0 && w == 0) reinterpret_cast<float *>(rec + SR::fwd_scales)[1] = inverse_of(se);
+                // (U is E times factors of up to F_BFMOST in these rows)
+                const float se = warp_scale(x), su = scale_for(kTop * inverse_of(se) * f[F_BFMOST + w]);
+                q.template hand_rows<2>(y, su, q.mine + Sm::u + w * 1024, Q::SC_U);
+                q.template hand_rows<NO>(x, se, q.mine + Sm::e + w * Sm::e_block, Q::SC_E, rec ? rec + SR::e + w * 512 : nullptr, rec_scales + 1 + w);
             }
             q.meet();
-            clear(x);
             {
                 uint32_t a[2][NO][4], r[2][NO][4];
                 const auto load = [&](int kb) {
@@ -761,14 +790,12 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
                 for (int kb = 0; kb < 4; ++kb) {
                     if (kb > w) break;
                     if (kb < 3) load(kb + 1);
-                    products<T, NO, NO>(x[0], x[1], a[kb & 1], r[kb & 1]);
+                    products_by<NO, NO>(z[0], z[1], a[kb & 1], r[kb & 1], q.sc[Q::SC_E + kb] * f[F_P]);
                 }
             }
-            add(z, x, inverse_of(se) * f[F_P]);
             // S = whole S0 + K^T U, this warp's quarter
-            const float whole = f[F_WHOLE], ik = f[F_K], iu = inverse_of(su) * ik;
-            Acc t[2 * kSteps];
-            clear(t);
+            const float ik = f[F_K];
+            scale_all(s, f[F_WHOLE]);
             {
                 uint32_t a[2][2][4], r[2][kSteps][NI][4];
                 const auto load = [&](int kb) {
@@ -782,23 +809,22 @@ __global__ void __launch_bounds__(512, 1) based_delta_fwd_kernel(DeltaParams p) 
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb) {
                     if (kb < 3) load(kb + 1);
+                    const float iu = q.sc[Q::SC_U + kb] * ik;
 #pragma unroll
-                    for (int i = 0; i < kSteps; ++i) products<T, 2, NI>(t[2 * i], t[2 * i + 1], a[kb & 1], r[kb & 1][i]);
+                    for (int i = 0; i < kSteps; ++i) products_by<2, NI>(s[2 * i], s[2 * i + 1], a[kb & 1], r[kb & 1][i], iu);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 2 * kSteps; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = fmaf(t[j][e], iu, s[j][e] * whole);
             stages.leave(stage);
-            if (n + 1 < count) {
-                uint8_t *const next = record(n + 1);
-                q.hand_over(s, fmaf(before, whole, 64.0f * (kTop * ik) * u_most), next, reinterpret_cast<float *>(next + SR::fwd_scales));
-            }
+            q.measure(s);
             if (t0 < p.T) {
                 write_tile<T>(tile, z, lane);
                 __syncwarp();
                 store_tile<T>(o + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
+            }
+            if (n + 1 < count) {
+                uint8_t *const next = record(n + 1);
+                q.meet();
+                q.hand_over(s, next, reinterpret_cast<float *>(next + SR::fwd_scales));
             }
         }
         turn += count;
@@ -851,7 +877,11 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
         __syncthreads();
         if (count > 0) {
             fetch(count - 1), values(count - 1);
-            if (cols > 0) q.begin(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
+            if (cols > 0) {
+                q.measure(g);
+                q.meet();
+                q.hand_over(g, record(count - 1), reinterpret_cast<float *>(record(count - 1) + SR::bwd_scales));
+            }
         }
         for (int n = count - 1; n >= 0; --n) {
             const int stage = turn + count - 1 - n & 1;
@@ -872,16 +902,10 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
             float *const rec_scales = reinterpret_cast<float *>(rec + SR::bwd_scales);
             Acc x[2], y[2];
             read_tile<T>(y, tile, lane);  // dO
-            {
-                const float so = warp_scale(y);
-                uint32_t a[NI][4];
-                left_of<NI>(a, y[0], y[1], so);
-                give<NI>(q.mine + Sm::e + w * Sm::e_block, a, lane);
-                leave<NI>(rec + SR::dout + w * 512, kRowsTerm, a, lane);
-                if (lane == 0) q.sc[12 + w] = inverse_of(so), rec_scales[2 + w] = inverse_of(so);
-            }
+            const float so = warp_scale(y);
+            q.template hand_rows<NI>(y, so, q.mine + Sm::e + w * Sm::e_block, Q::SC_E, rec + SR::dout + w * 512, rec_scales + 5 + w);
             clear(x);  // dU
-            const float is = q.sc[4], behind = q.state_most();
+            const float is = q.sc[Q::SC_STATE];
             {
                 uint32_t a[2][2][4], r[2][NI][4];
                 const auto load = [&](int kk) {
@@ -910,30 +934,21 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 for (int kb = 3; kb >= 0; --kb) {
                     if (kb < w) break;
                     if (kb > 0) load(kb - 1);
-                    Acc t[2];
-                    clear(t);
-                    products<T, NI, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
-                    add(x, t, q.sc[12 + kb] * f[F_P]);
+                    products_by<NI, 2>(x[0], x[1], a[kb & 1], r[kb & 1], q.sc[Q::SC_E + kb] * f[F_P]);
                 }
             }
+            by_columns(y, f + F_GROW + 16 * w, p.scale, lane);
             {
-                const float sx = warp_scale(x);
-                uint32_t a[2][4];
-                left_of<2>(a, x[0], x[1], sx);
-                give<2>(q.mine + Sm::x(true) + w * 1024, a, lane);
-                if (lane == 0) q.sc[8 + w] = inverse_of(sx);
-            }
-            // scale grow dO, all warps for the same bound
-            const float u_most = kTop * fmaxf(fmaxf(q.sc[12], q.sc[13]), fmaxf(q.sc[14], q.sc[15])) * f[F_GROWMOST] * fabsf(p.scale), su = scale_for(u_most);
-            {
-                uint32_t c[2][4];
-                by_columns(y, f + F_GROW + 16 * w, p.scale, lane);
-                left_of<2>(c, y[0], y[1], su);
-                give<2>(q.mine + Sm::u + w * 1024, c, lane);
+                const float sx = warp_scale(x), su = scale_for(kTop * inverse_of(so) * f[F_GROWMOST + w] * fabsf(p.scale));
+                q.template hand_rows<2>(x, sx, q.mine + Sm::x(true) + w * 1024, Q::SC_X);
+                q.template hand_rows<2>(y, su, q.mine + Sm::u + w * 1024, Q::SC_U);
             }
             q.meet();
-            clear(y);  // dR
-            {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[i][e] = x[i][e];
+            {  // dR: dU and what the rows behind take back
                 uint32_t a[2][2][4], r[2][2][4];
                 const auto load = [&](int kb) {
                     take<2>(a[kb & 1], q.mine + Sm::x(true) + kb * 1024, lane);
@@ -944,61 +959,49 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
                 for (int kb = 3; kb >= 0; --kb) {
                     if (kb < w) break;
                     if (kb > 0) load(kb - 1);
-                    Acc t[2];
-                    clear(t);
-                    products<T, 2, 2>(t[0], t[1], a[kb & 1], r[kb & 1]);
-                    add(y, t, q.sc[8 + kb] * f[F_INV]);
+                    products_by<2, 2>(y[0], y[1], a[kb & 1], r[kb & 1], q.sc[Q::SC_X + kb] * f[F_INV]);
                 }
             }
-            // beta grow dR likewise, from dU's and the inverse's largest
-            const float r_most = 64.0f * (kTop * f[F_INV]) * (kTop * fmaxf(fmaxf(q.sc[8], q.sc[9]), fmaxf(q.sc[10], q.sc[11])));
-            const float sr = scale_for(r_most), w_most = r_most * f[F_BFMOST], sw = scale_for(w_most);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][e] = y[i][e];
+            by_columns(y, f + F_BF + 16 * w, -1.0f, lane);
             {
-                uint32_t a[NO][4];
-                left_of<NO>(a, y[0], y[1], sr);
-                leave<NO>(rec + SR::dr + w * 512, kRowsTerm, a, lane);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = y[i][e];
-                by_columns(x, f + F_BETA + 16 * w, 1.0f, lane);  // dV
-                by_columns(y, f + F_BF + 16 * w, -1.0f, lane);
-                uint32_t c[2][4];
-                left_of<2>(c, y[0], y[1], sw);
-                give<2>(q.mine + Sm::w + w * 1024, c, lane);
-                if (lane == 0 && w == 0) rec_scales[1] = inverse_of(sr);
+                const float sr = warp_scale(x), sw = scale_for(kTop * inverse_of(sr) * f[F_BFMOST + w]);
+                q.template hand_rows<2>(y, sw, q.mine + Sm::w + w * 1024, Q::SC_W);
+                q.template hand_rows<NO>(x, sr, nullptr, 0, rec + SR::dr + w * 512, rec_scales + 1 + w);
             }
+            by_columns(x, f + F_BETA + 16 * w, lane);  // dV
             q.meet();
-            const float whole = f[F_WHOLE], ik = f[F_K], iq = f[F_Q], iu = inverse_of(su) * iq, iw = inverse_of(sw) * ik;
-            Acc t[2 * kSteps], u[2 * kSteps];
-            clear(t), clear(u);
+            const float ik = f[F_K], iq = f[F_Q];
+            scale_all(g, f[F_WHOLE]);
 #pragma unroll
             for (int kb = 0; kb < 4; ++kb) {  // (a step ahead there would be registers for neither)
                 uint32_t a[2][4], c[2][4];
                 take<2>(a, q.mine + Sm::u + kb * 1024, lane), take<2>(c, q.mine + Sm::w + kb * 1024, lane);
+                const float iu = q.sc[Q::SC_U + kb] * iq, iw = q.sc[Q::SC_W + kb] * ik;
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     uint32_t r[NI][4];
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], qimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<T, 2, NI>(t[2 * i], t[2 * i + 1], a, r);
+                    products_by<2, NI>(g[2 * i], g[2 * i + 1], a, r, iu);
 #pragma unroll
                     for (int j = 0; j < NI; ++j) right_t<KP>(r[j], kimg + j * R::term, 16 * kb, w * (KP / 4) + 16 * i, lane);
-                    products<T, 2, NI>(u[2 * i], u[2 * i + 1], c, r);
+                    products_by<2, NI>(g[2 * i], g[2 * i + 1], c, r, iw);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 2 * kSteps; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[j][e] = fmaf(t[j][e], iu, fmaf(u[j][e], iw, g[j][e] * whole));
             stages.leave(stage);
-            if (n > 0)
-                q.hand_over(g, fmaf(behind, whole, 64.0f * ((kTop * iq) * u_most + (kTop * ik) * w_most)), record(n - 1),
-                            reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
+            q.measure(g);
             if (t0 < p.T) {
                 write_tile<T>(tile, x, lane);
                 __syncwarp();
                 store_tile<T>(dv + t0 * row_o, row_o, tile, static_cast<int>(live - t0), static_cast<int>(p.T - t0), cols, p.o_vec, lane);
+            }
+            if (n > 0) {
+                q.meet();
+                q.hand_over(g, record(n - 1), reinterpret_cast<float *>(record(n - 1) + SR::bwd_scales));
             }
         }
         turn += count;
@@ -1065,21 +1068,7 @@ __device__ __forceinline__ void left_blocks(uint32_t (&r)[4], uint32_t at, int l
 }
 __device__ __forceinline__ void right_blocks(uint32_t (&r)[4], uint32_t at, int lane) { ldsm_t(r, at + lane * 16); }
 
-// Slices differ in their scales. Their products are brought to the largest's by a power of two on one operand: what that takes from the last
-// bits of a slice is below the sum's. The exponent of a power of two, and 2^e for e <= 0 as two halves
-__device__ __forceinline__ int exponent(float pow2) { return static_cast<int>(__float_as_uint(pow2) >> 23) - 127; }
-__device__ __forceinline__ uint32_t halves(int e) {
-    const uint32_t h = e >= -14 ? static_cast<uint32_t>(15 + e) << 10 : e >= -24 ? 1u << (24 + e) : 0u;
-    return h | h << 16;
-}
-template <int TERMS>
-__device__ __forceinline__ void times(uint32_t (&to)[TERMS][4], const uint32_t (&a)[TERMS][4], uint32_t f) {
-#pragma unroll
-    for (int j = 0; j < TERMS; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(to[j][i]) : "r"(a[j][i]), "r"(f));
-}
-
+// Slices differ in their scales: their products are brought to the largest's on one operand.
 template <typename T, int KP>
 __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(DeltaParams p) {
     using R = Rec<T, KP>;
@@ -1137,23 +1126,31 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
             for (int i = 0; i < Sm::stages - 1; ++i) fetch(i);
             for (int i = tid; i < F_COUNT; i += kThreads) f[i] = reinterpret_cast<const float *>(rec)[i];
-            // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, dO E, dR E, S0 G
-            int top[6] = {-1000, -1000, -1000, -1000, -1000, -1000};
-            const auto exponents = [&](int (&x)[6], int sl) {
+            // The largest exponents of the slices' products for this warp: dO S0, dR S0, E G, S0 G, and by 16 columns dO E, dR E
+            enum { OS, RS, EG, SG, OE, RE = OE + 2, kProducts = RE + 2 };
+            int top[kProducts];
+#pragma unroll
+            for (int i = 0; i < kProducts; ++i) top[i] = -1000;
+            const auto exponents = [&](int (&x)[kProducts], int sl) {
                 const float *const a = reinterpret_cast<const float *>(fwd + static_cast<int64_t>(sl) * SR::fwd + SR::fwd_scales),
                                    *const c = reinterpret_cast<const float *>(bwd + static_cast<int64_t>(sl) * SR::bwd + SR::bwd_scales);
-                const int s = exponent(a[0]), e = exponent(a[1]), g = exponent(c[0]), r = exponent(c[1]), o = exponent(c[2 + wm]);
-                x[0] = o + s, x[1] = r + s, x[2] = e + g, x[3] = o + e, x[4] = r + e, x[5] = s + g;
+                const int s = exponent(a[0]), g = exponent(c[0]), r = exponent(c[1 + wm]), o = exponent(c[5 + wm]);
+                x[OS] = o + s, x[RS] = r + s, x[EG] = exponent(a[1 + wm]) + g, x[SG] = s + g;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = exponent(a[1 + 2 * wn + i]);
+                    x[OE + i] = o + e, x[RE + i] = r + e;
+                }
             };
-            uint32_t by[6];  // lane i: the factors of slice i (of 32)
+            uint32_t by[kProducts];  // lane i: the factors of slice i (of 32)
             for (int sl = lane; sl < slices; sl += 32) {
-                int x[6];
+                int x[kProducts];
                 exponents(x, sl);
 #pragma unroll
-                for (int i = 0; i < 6; ++i) top[i] = max(top[i], x[i]);
+                for (int i = 0; i < kProducts; ++i) top[i] = max(top[i], x[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 6; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+            for (int i = 0; i < kProducts; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
             Acc aos[2 * NQ], ars[2 * NQ], aeg[2 * NQ], dp[4], da[4];
             Acc diagonal[2];
             clear(aos), clear(ars), clear(aeg), clear(dp), clear(da), clear(diagonal);
@@ -1164,30 +1161,30 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 fetch(sl + Sm::stages - 1);
                 const uint8_t *const x = smem + Sm::ring + at * Sm::stage, *const y = x + SR::fwd;
                 if (sl % 32 == 0) {
-                    int e[6] = {};
+                    int e[kProducts] = {};
                     if (sl + lane < slices) exponents(e, sl + lane);
 #pragma unroll
-                    for (int i = 0; i < 6; ++i) by[i] = halves(e[i] - top[i]);
+                    for (int i = 0; i < kProducts; ++i) by[i] = halves(e[i] - top[i]);
                 }
-                uint32_t factor[6];
+                uint32_t factor[kProducts];
 #pragma unroll
-                for (int i = 0; i < 6; ++i) factor[i] = __shfl_sync(0xffffffffu, by[i], sl % 32);
+                for (int i = 0; i < kProducts; ++i) factor[i] = __shfl_sync(0xffffffffu, by[i], sl % 32);
                 const uint32_t xa = smem_u32(x), ya = smem_u32(y);
                 uint32_t lo[NI][4], lr[NO][4], le[NO][4], c[NO][4], d[NI][4], v[NO][4];
 #pragma unroll
                 for (int j = 0; j < NI; ++j) left_blocks(lo[j], ya + SR::dout + j * kRowsTerm + wm * 512, lane);
 #pragma unroll
                 for (int j = 0; j < NO; ++j) left_blocks(lr[j], ya + SR::dr + j * kRowsTerm + wm * 512, lane), left_blocks(le[j], xa + SR::e + j * kRowsTerm + wm * 512, lane);
-                times<NI>(d, lo, factor[3]), times<NO>(c, lr, factor[4]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (2 * wn + i > wm) break;
+                    times<NI>(d, lo, factor[OE + i]), times<NO>(c, lr, factor[RE + i]);
 #pragma unroll
                     for (int j = 0; j < NO; ++j) right_blocks(v[j], xa + SR::e + j * kRowsTerm + (2 * wn + i) * 512, lane);
                     products<T, NI, NO>(dp[2 * i], dp[2 * i + 1], d, v);
                     products<T, NO, NO>(da[2 * i], da[2 * i + 1], c, v);
                 }
-                times<NI>(d, lo, factor[0]), times<NO>(c, lr, factor[1]), times<NO>(le, le, factor[2]);
+                times<NI>(d, lo, factor[OS]), times<NO>(c, lr, factor[RS]), times<NO>(le, le, factor[EG]);
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
 #pragma unroll
@@ -1202,7 +1199,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                 if (traces) {
 #pragma unroll
                     for (int j = 0; j < NO; ++j) left_blocks(c[j], xa + j * SR::state_term + warp * 512, lane), right_blocks(v[j], ya + j * SR::state_term + warp * 512, lane);
-                    times<NO>(c, c, factor[5]);
+                    times<NO>(c, c, factor[SG]);
                     products<T, NO, NO>(diagonal[0], diagonal[1], c, v);
                 }
             }
@@ -1212,12 +1209,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (traces && 2 * (lane & 3) + e == lane >> 2) dot += diagonal[0][e] + diagonal[1][2 + e];
-            dot = ldexpf(dot, top[5]);
+            dot = ldexpf(dot, top[SG]);
             // rows' and columns' factors, and the rows' products with queries and keys
             const float ik = f[F_K], iq = f[F_Q], c0 = f[F_GROW + r0], c1 = f[F_GROW + r1], b0 = f[F_BETA + r0], b1 = f[F_BETA + r1];
             float row0 = 0.0f, row1 = 0.0f, next0 = 0.0f, next1 = 0.0f;
             {
-                const float so = ldexpf(p.scale, top[0]), sr = ldexpf(-1.0f, top[1]), se = ldexpf(1.0f, top[2]);
+                const float so = ldexpf(p.scale, top[OS]), sr = ldexpf(-1.0f, top[RS]), se = ldexpf(1.0f, top[EG]);
+                const float n0 = b0 * inverse_of(step_of(b0)), n1 = b1 * inverse_of(step_of(b1));  // (E's rows are times their steps)
 #pragma unroll
                 for (int i = 0; i < 2 * NQ; ++i) {
                     const int col = col0 + 8 * i;
@@ -1226,7 +1224,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float c = e < 2 ? c0 : c1, be = e < 2 ? b0 : b1, re = f[F_REST + (e < 2 ? r0 : r1)];
-                        const float x = aos[i][e] * so * c, y = ars[i][e] * sr * (be * c), z = aeg[i][e] * se * (re * be);
+                        const float x = aos[i][e] * so * c, y = ars[i][e] * sr * (be * c), z = aeg[i][e] * se * (re * (e < 2 ? n0 : n1));
                         const float qv = e == 0 ? q0.x : e == 1 ? q0.y : e == 2 ? q1.x : q1.y, kv = e == 0 ? k0.x : e == 1 ? k0.y : e == 2 ? k1.x : k1.y;
                         (e < 2 ? row0 : row1) += x * qv + y * kv;
                         (e < 2 ? next0 : next1) += z * kv;
@@ -1258,14 +1256,15 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                         products<T, NI, NI>(sk[2 * i], sk[2 * i + 1], c4, x);
                     }
                 }
-                const float sp = ldexpf(1.0f, top[3]), sa = ldexpf(-1.0f, top[4]);
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt)
+                for (int nt = 0; nt < 4; ++nt) {
+                    const float sp = ldexpf(1.0f, top[OE + nt / 2]), sa = ldexpf(-1.0f, top[RE + nt / 2]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e < 2 ? r0 : r1, j = 32 * wn + 8 * nt + 2 * (lane & 3) + e % 2;
-                        if (i == j) part_beta[i] = -da[nt][e] * sa;
-                        const float d = j <= i ? expf((f[F_BHI + i] - f[F_BHI + j]) + (f[F_BLO + i] - f[F_BLO + j])) : 0.0f, bj = f[F_BETA + j];
+                        const float over = inverse_of(step_of(f[F_BETA + j])), bj = f[F_BETA + j] * over;
+                        if (i == j) part_beta[i] = -da[nt][e] * sa * over;
+                        const float d = j <= i ? expf((f[F_BHI + i] - f[F_BHI + j]) + (f[F_BLO + i] - f[F_BLO + j])) : 0.0f;
                         dp[nt][e] = j <= i ? dp[nt][e] * sp * bj * (d * p.scale) : 0.0f;
                         da[nt][e] = j < i ? da[nt][e] * sa * bj * (d * f[F_BETA + i]) : 0.0f;
                         const float sum = j <= i ? dp[nt][e] * (sq[nt][e] * (iq * ik)) + da[nt][e] * (sk[nt][e] * (ik * ik)) : 0.0f;
@@ -1273,6 +1272,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, 1) based_delta_grad_kernel(De
                         col[nt][e % 2] += sum;
                         mp = fmaxf(mp, fabsf(dp[nt][e])), ma = fmaxf(ma, fabsf(da[nt][e]));
                     }
+                }
             }
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {

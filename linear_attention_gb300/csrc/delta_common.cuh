@@ -3,7 +3,7 @@
 //
 // The kernels multiply on tensor cores and keep float32's accuracy. A float32 operand x goes in as two
 // float16 terms, hi = x s and lo = x s - hi with a power of two s that brings the largest |x| of a row or tile
-// to 2^12: together 22 bits, off by 2^-23 of that largest where bfloat16 pairs would be off by 2^-17. A product
+// to 2^14: together 22 bits, off by 2^-23 of that largest where bfloat16 pairs would be off by 2^-17. A product
 // of two pairs is three matrix products (lo lo, 2^-22 of the result, is left out); 16-bit inputs are one term.
 // Sums are float32. Per multiprocessor and cycle mma.sync makes 1019 float16 products (measured), a quarter of what
 // tcgen05.mma does, but its accumulators are registers: a chunk's chain of products runs
@@ -52,12 +52,14 @@ struct Terms<float> {
 
 // A chunk's records in the workspace: images of shared memory, copied as they are.
 //   of a key head: the scaled keys and queries, TERMS x 64 x KP float16 each
-//   of a value head: the inverse (two terms), the masked scores (forward: Terms::out, times beta of their columns; backward: two),
-//   64 x 64 float16 each, and float32 numbers: per row grow = exp(b), rest = exp(b_last - b), beta, b in two parts (b: the
-//   sum of log decays up to the row), beta rest (backward: beta grow), then the scales' inverses, the largest |beta rest| (backward: |beta
-//   grow|) and the largest grow.
+//   of a value head: the inverse below its diagonal of ones (two terms; forward: its rows times their steps, its columns over theirs), the
+//   masked scores (forward: Terms::out, times beta of their columns over their steps; backward: two), 64 x 64 float16 each, and float32
+//   numbers: per row grow = exp(b), rest = exp(b_last - b) (forward: grow times the row's step), beta (forward: the step), b in two parts (b: the sum
+//   of log decays up to the row), beta grow (forward: beta rest over the step), then the scales' inverses, and of each 16 rows the
+//   largest |beta grow| (forward: the largest |beta rest| over the step) and the largest grow.
 constexpr int kSquare = kChunk * kChunk * 2;  // bytes
-enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_BF = 320, F_INV = 384, F_P, F_WHOLE, F_K, F_Q, F_BFMOST, F_GROWMOST, F_COUNT = 400 };
+enum { F_GROW = 0, F_REST = 64, F_BETA = 128, F_BHI = 192, F_BLO = 256, F_BF = 320, F_INV = 384, F_P, F_WHOLE, F_K, F_Q, F_BFMOST = 392, F_GROWMOST = 396, F_COUNT = 400 };
+enum { F_GROWSTEP = F_REST, F_STEP = F_BETA };  // forward
 template <typename T, int KP>
 struct Rec {
     static constexpr int term = kChunk * KP * 2, img = Terms<T>::in * term, qk = 2 * img;
@@ -67,7 +69,8 @@ struct Rec {
 
 // What the passes through the chunks leave for the gradients, per chunk, value head and slice of 16 channels of the values: float16 terms
 // in the order of left operands, 16 x 16 blocks of four 8 x 8 blocks (rows 0-7 and 8-15 of columns 0-7, the same of columns 8-15) of 128
-// bytes, rows the slice's channels; behind them the scales' inverses, one for the state, one for E or dR, and one for each 16 of the chunk's rows of dO.
+// bytes, rows the slice's channels; behind them the scales' inverses, one for the state, and one for each 16 of the chunk's rows of E (whose rows are times
+// their steps), dR and dO.
 constexpr int kSlice = 16;
 constexpr int kRowsTerm = kSlice * kChunk * 2;
 template <typename T, int KP>
@@ -75,9 +78,9 @@ struct SliceRec {
     static constexpr int in = Terms<T>::in, out = Terms<T>::out;
     static constexpr int state_term = kSlice * KP * 2, states = out * state_term;
     // forward: the state in front of the chunk, E
-    static constexpr int e = states, fwd_scales = e + out * kRowsTerm, fwd = fwd_scales + 16;
+    static constexpr int e = states, fwd_scales = e + out * kRowsTerm, fwd = fwd_scales + 32;
     // backward: the gradient of the state behind the chunk, dR, dO
-    static constexpr int dr = states, dout = dr + out * kRowsTerm, bwd_scales = dout + in * kRowsTerm, bwd = bwd_scales + 32;
+    static constexpr int dr = states, dout = dr + out * kRowsTerm, bwd_scales = dout + in * kRowsTerm, bwd = bwd_scales + 48;
 };
 
 // ------------------------------------------------------------------------------------------------
@@ -173,18 +176,56 @@ __device__ __forceinline__ void products(Acc &x, Acc &y, const uint32_t (&a)[LT]
     }
 }
 
+// Pairs of a block's columns times y; x += t c
+__device__ __forceinline__ void by_pairs(Acc &x, const Vec<2> &y) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const Vec<2> r = vmul(Vec<2>{{x[e], x[e + 1]}}, y);
+        x[e] = r.v[0], x[e + 1] = r.v[1];
+    }
+}
+__device__ __forceinline__ void add_times(Acc &x, const Acc &t, float c) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const Vec<2> r = vfma(Vec<2>{{t[e], t[e + 1]}}, splat<2>(c), Vec<2>{{x[e], x[e + 1]}});
+        x[e] = r.v[0], x[e + 1] = r.v[1];
+    }
+}
+// ... times c: of several products whose left operands differ in their scales each is a sum of its own
+template <int LT, int RT>
+__device__ __forceinline__ void products_by(Acc &x, Acc &y, const uint32_t (&a)[LT][4], const uint32_t (&b)[RT][4], float c) {
+    Acc s[2];
+    clear(s);
+#pragma unroll
+    for (int j = RT - 1; j >= 0; --j)
+#pragma unroll
+        for (int i = LT - 1; i >= 0; --i)
+            if (i + j < 2) {
+                mma(s[0], a[i], b[j][0], b[j][1]);
+                mma(s[1], a[i], b[j][2], b[j][3]);
+            }
+    add_times(x, s[0], c), add_times(y, s[1], c);
+}
+
 // ------------------------------------------------------------------------------------------------
 // float16 pairs
 // ------------------------------------------------------------------------------------------------
-// The power of two that brings `most` (finite, >= 0) to [2^12, 2^13): between 2^-100 and 2^60, so that a
+// The power of two that brings `most` (finite, >= 0) to [2^14, 2^15): between 2^-100 and 2^60, so that a
 // product of two inverses is a float32 number unless the product of the values is none.
 __device__ __forceinline__ float scale_for(float most) {
-    int e = 266 - static_cast<int>(__float_as_uint(most) >> 23);
+    int e = 268 - static_cast<int>(__float_as_uint(most) >> 23);
     e = e < 27 ? 27 : e > 187 ? 187 : e;
     return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
-constexpr float kTop = 8192.0f;  // what scaled magnitudes stay below: |x| < kTop * inverse
+constexpr float kTop = 32768.0f;  // what scaled magnitudes stay below: |x| < kTop * inverse
 __device__ __forceinline__ float inverse_of(float pow2) { return __uint_as_float((254u << 23) - __float_as_uint(pow2)); }
+
+// A row's step: the power of two at or below |beta|, from 2^-12 to 1. What a row holds before it is times beta is an operand times its step,
+// and the other operand is over it: a row that hardly writes (beta 0: a masked token) takes no bits from the 16 that it is scaled with, whatever
+// its values are, and beta's own gradient still has them.
+__device__ __forceinline__ float step_of(float beta) {
+    return fminf(fmaxf(__uint_as_float(__float_as_uint(beta) & 0x7f800000u), 2.44140625e-4f), 1.0f);
+}
 
 __device__ __forceinline__ uint32_t half2_of(float x, float y) { return pack<__half>(Vec<2>{{x, y}}); }
 // hi and lo terms of two elements
