@@ -189,7 +189,7 @@ struct Weigh {
     // float32 (a type's lowest value as a mask, a small temperature) or no number (a difference beyond it, an infinite temperature).
     __device__ __forceinline__ float place(float x) const { return fminf((most - x) * hi * (kBins / kReach), kBins - 1.0f); }
     __device__ __forceinline__ float weight(float x) const {
-        const float d = most - x, t = d * hi, r = fmaf(d, hi, -t) + d * lo;
+        const float d = most - x, t = d * hi, r = fmaf(d, lo, fmaf(d, hi, -t));
         const float w = ex2(-t);
         return t < 120.0f ? fmaf(w, -0.6931471806f * r, w) : 0.0f;
     }
@@ -418,20 +418,22 @@ __device__ Moved move_cut(Sampler<T> &s, const Weigh &w, int k, float share, Cut
 }
 
 // The token, by the first CTA alone, where move_cut has left it all that are kept. It sorts them again, by indices; above kListed that takes as long
-// as the passes over the row which it saves.
+// as the passes over the row which it saves. Masses are rounded by eight neighbouring tokens, as in those passes: which way a call goes depends on its
+// number of rows and on alignment, and its tokens do not.
 template <typename T>
-__device__ void take_listed(const Sampler<T> &s, const Weigh &w, const Cut &cut, float min_p, int64_t n, const T *logits) {
+__device__ void take_listed(const Sampler<T> &s, const Weigh &w, const Cut &cut, float min_p, int64_t n) {
     SampleShared &sh = s.sh;
     constexpr int kEach = kFew / kSampleThreads;
     const int count = static_cast<int>(sh.found[2]), mine = s.tid * kEach;
     u64 v[kEach], m[kEach], kept = 0, all;
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        v[j] = 0, m[j] = sh.few.mass[mine + j];
+        v[j] = m[j] = 0;
         if (mine + j < count) {
             const u64 place = sh.few.place[mine + j];
-            const float x = unordered(static_cast<uint32_t>(place >> 32));
-            if (cut.keeps(x, static_cast<int>(0xffffffffu - static_cast<uint32_t>(place))) && w.weight(x) >= min_p) v[j] = place & 0xffffffffu, ++kept;
+            const float x = unordered(static_cast<uint32_t>(place >> 32)), weight = w.weight(x);
+            m[j] = __float_as_uint(weight);
+            if (cut.keeps(x, static_cast<int>(0xffffffffu - static_cast<uint32_t>(place))) && weight >= min_p) v[j] = place & 0xffffffffu, ++kept;
         }
     }
     u64 at = cta_prefix(kept, sh.warp[0], all);  // (with barriers)
@@ -441,20 +443,36 @@ __device__ void take_listed(const Sampler<T> &s, const Weigh &w, const Cut &cut,
     const int keep = static_cast<int>(all);
     __syncthreads();
     sort_few(sh, keep);  // by rising indices
+    const auto token = [&](int i) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(sh.few.place[i])); };
+    const auto weight = [&](int i) { return __uint_as_float(static_cast<uint32_t>(sh.few.mass[i])); };
     u64 sum = 0;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        v[j] = mine + j < keep ? sh.few.mass[mine + j] : 0;
+    for (int j = 0; j < kEach; ++j) {  // the first of its eight has their mass
+        const int i = mine + j;
+        v[j] = 0;
+        if (i < keep && (i == 0 || token(i - 1) >> 3 != token(i) >> 3)) {
+            float eight = 0.0f;
+            for (int l = i; l < keep && token(l) >> 3 == token(i) >> 3; ++l) eight += weight(l);
+            v[j] = static_cast<u64>(__float2ull_rn(eight * kMass));
+        }
         sum += v[j];
     }
     u64 now = cta_prefix(sum, sh.warp[0], all);
     const u64 target = target_of(s.p.u[n], all);
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        if (now <= target && now + v[j] > target) {
-            const int token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(sh.few.place[mine + j]));
-            s.p.tokens[n] = token;
-            if (s.p.probs) s.p.probs[n] = static_cast<float>(static_cast<double>(w.weight(to_f32(logits[token]))) * kMass / static_cast<double>(all));
+        if (now <= target && now + v[j] > target) {  // as in the passes
+            const int i = mine + j;
+            const float left = static_cast<float>(target - now) / kMass;
+            float up_to = 0.0f, taken = 0.0f;
+            int to = -1;
+            bool passed = false;
+            for (int l = i; l < keep && token(l) >> 3 == token(i) >> 3; ++l) {
+                up_to += weight(l);
+                if (weight(l) > 0.0f && !passed) to = token(l), taken = weight(l), passed = up_to > left;
+            }
+            s.p.tokens[n] = to;
+            if (s.p.probs) s.p.probs[n] = static_cast<float>(static_cast<double>(taken) * kMass / static_cast<double>(all));
         }
         now += v[j];
     }
@@ -545,7 +563,7 @@ __global__ void __launch_bounds__(kSampleThreads) based_sample_kernel(SamplePara
         }
         if (moved == LISTED) {
             s.meet();
-            if (rank == 0) take_listed(s, w, cut, min_p, n, src);
+            if (rank == 0) take_listed(s, w, cut, min_p, n);
             return;
         }
         if (moved == CUT && top_p < 1.0f) clear();
