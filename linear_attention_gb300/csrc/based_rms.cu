@@ -4,9 +4,9 @@
 //     ds = r (d - s r mean(d s r)) + dsum with d = dy w,   dw = sum over rows of dy s r
 //
 // A row lies in the registers of THREADS threads, up to four packs of eight channels each, so one reading of it serves the
-// sum of squares, the largest magnitude of an 8-bit output and the result. Bound by memory. Rows of 8 to 128 packs take a part of
-// a warp or a warp; longer ones several warps, which meet once (8 bits: twice) in shared memory. CTAs walk over the rows with the weights in
-// registers; backward the weights' gradients add up there too, in an order that the sizes fix.
+// sum of squares, the largest magnitude of an 8-bit output and the result. Bound by memory. Rows of up to 64 packs take a part of
+// a warp or a warp; longer ones two to sixteen warps, which meet once (8 bits: twice) in shared memory. CTAs walk over the rows with the weights in
+// registers; backward the weights' gradients add up there too, in an order that the sizes and the rows' alignment fix.
 #include <type_traits>
 
 #include "ops_common.cuh"
@@ -362,8 +362,10 @@ int launch_bwd(RmsParams &p, cudaStream_t st) {
 }
 // Threads for a row: as few as hold it in two packs each, which leaves registers for the next row's loads (three where that fits better and both
 // streams have 16 bits), so that a warp or a part of one serves short rows and sums stay in it. bf16, with the next row ahead and without: 29296 x 2048 75 us (four packs
-// 84), 7324 x 8192 81 (109), a float32 stream of 20000 x 3000 114 (134); only a float32 stream of 4096 channels does better in four packs without
-// it (14648 rows: 111 us instead of 122). Backward 24000 x 1536 51 us, without 64, with four packs 79. Single channels, not words, go by four or two packs.
+// 84), 7324 x 8192 81 (109), a float32 stream of 20000 x 3000 114 (134). 16-bit inputs beside a float32 stream of more than 3584 channels do better in four packs
+// without it: of 60 million elements 4096 channels take 115 us (e4m3 out: 111) instead of 126 (117), 3840 115 (112) instead of 126 (113), 3584 117 (115) and 124 (111),
+// 3200 124 (119) and 120 (111); float32 throughout 3200 to 4096 channels take 179 to 193 us in four packs and 158 to 169 in two.
+// Backward 24000 x 1536 51 us, without 64, with four packs 79. Single channels, not words, go by four or two packs.
 template <typename T, typename S>
 int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
     const int packs = (p.C + kPack - 1) / kPack;
@@ -396,8 +398,8 @@ int launch_rms(RmsParams &p, bool words, bool bwd, int sms, cudaStream_t st) {
     if (packs <= 256) return launch_fwd<T, S, 128, 2, true>(p, sms, st);
     if constexpr (sizeof(S) == 2)
         if (packs <= 384) return launch_fwd<T, S, 128, 3, true>(p, sms, st);
-    if constexpr (sizeof(S) == 4)
-        if (packs > 384 && packs <= 512) return launch_fwd<T, S, 128, 4, true>(p, sms, st);
+    if constexpr (sizeof(T) == 2 && sizeof(S) == 4)
+        if (packs > 448 && packs <= 512) return launch_fwd<T, S, 128, 4, true>(p, sms, st);
     if (packs <= 512) return launch_fwd<T, S, 256, 2, true>(p, sms, st);
     if (packs <= 1024) return launch_fwd<T, S, 512, 2, true>(p, sms, st);
     return launch_fwd<T, S, 512, 4, true>(p, sms, st);
