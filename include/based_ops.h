@@ -1,20 +1,21 @@
 /*
  * based_ops.h: C ABI of the language-model operators around the Based forward pass (based.h):
- * the gated linear recurrence, the per-token group norm with an activation, and the scaled
- * embedding with its gradient.
+ * the gated linear recurrence, the per-token group norm with an activation, the scaled
+ * embedding with its gradient, the gated delta rule, the root-mean-square norm of a residual
+ * stream and the choice of a next token.
  *
  * Conventions shared by every entry point (return codes, streams and error strings are those of
  * based.h):
  *   - Element types are given by a BASED_F32 / BASED_BF16 / BASED_F16 code. States, saved states
- *     and accumulations are float32 whatever the element type; each output element is rounded
- *     once, to nearest even.
+ *     and accumulations are float32 whatever the element type (based_delta_fwd says what it
+ *     saves); each output element is rounded once, to nearest even.
  *   - The channel axis has stride 1. Other strides of inputs are arguments, in elements (a stride
  *     of 0 broadcasts, negative ones are refused); outputs are contiguous. Offsets are computed
  *     in 64 bits.
  *   - Pointers must be aligned to their element size. 16-byte aligned pointers with strides and
- *     sizes that keep rows 16-byte aligned take wider loads. In the norm the order in which sums are
- *     taken follows the loads, so that the same values at other strides or alignments can give
- *     other bits; in the other operators nothing but time depends on alignment.
+ *     sizes that keep rows 16-byte aligned take wider loads. In both norms and in based_delta_step
+ *     the order in which sums are taken follows the loads, so that the same values at other strides
+ *     or alignments can give other bits; elsewhere nothing but time depends on alignment.
  *   - Inputs are read-only. Outputs must not overlap inputs, except where stated.
  *   - Calls are asynchronous on `stream`, never synchronise and never allocate. Scratch, where an
  *     operator needs some, is a caller's workspace (16-byte aligned; contents ignored on entry,
@@ -180,8 +181,12 @@ BASED_API size_t based_embed_bwd_workspace_size(int64_t N, int V, int D);
  * has stored: per batch entry and head, for t = 0 .. T-1,
  *     u_t = beta_t (v_t - a_t S_{t-1}^T k_t),   S_t = a_t S_{t-1} + k_t u_t^T,   o_t = scale S_t^T q_t,
  * with a = exp(gate), or 1 without gates. Head h of the values uses head h / (H / HK) of queries and keys.
- * Products go through float16 pairs: as accurate as float32's relative to the largest magnitude of 16 value channels of the
- * state, of 64 rows of keys or queries, or of 16 rows and channels of values; magnitudes below 2^-84 count as 0 there.
+ * Products go through pairs of float16 terms, scaled by the largest magnitude of 16 value channels of the state, of 64 rows of keys, of queries
+ * or of their products, and of 16 rows by 16 channels of values (a row counts times |beta|, or 2^-12 where that is less) and of their gradients: off
+ * by 2^-22 of a number down to 2^-17 of the largest that it shares its scale with, and by 2^-39 of that below. Sums are float32's.
+ * Where `dtype` is BASED_BF16, what is in outputs and gradients alone is one term, off by 2^-11 of a number where the result's rounding is off by
+ * 2^-8: the state as q reads it, scores and corrections, and backward also what `saved` holds. What goes into a state is a pair.
+ * Magnitudes below 2^-84 count as 0, and from 2^115 on as infinite.
  * Gates are meant to be <= 0 (-inf clears the state, gates below -1e5 count as -inf). Positive ones let the state grow and
  * work as long as no 64 of them add up to more than 88. Rows go by chunks of 64, from row 0: from the chunk on that has an
  * infinity or NaN in an input or the state, a head's results are NaN where the formulas have them, and undefined elsewhere.
@@ -196,7 +201,7 @@ BASED_API size_t based_embed_bwd_workspace_size(int64_t N, int V, int D);
  *   o            (B,T,H,V) of `dtype`, contiguous
  *   final_state  (B,H,K,V) float32 or NULL: S_{T-1}; may be `state` itself
  *   saved        based_delta_saved_size() bytes, 16-byte aligned, or NULL: what based_delta_bwd reads (the states in front of rows 0, 64, ...
- *                and the rows' v_t - a_t S_{t-1}^T k_t, in the kernels' own order and types)
+ *                and the rows' v_t - a_t S_{t-1}^T k_t, as float16 terms in the kernels' own order: two a number, one in bfloat16)
  *   workspace    based_delta_workspace_size(..., 0) bytes
  * H must be a multiple of HK, K at most 128, V at most 65536.
  * Errors: as based_scan_fwd, BASED_ERR_WORKSPACE, BASED_ERR_BAD_ARGUMENT (a scale that is NaN).
@@ -274,7 +279,7 @@ BASED_API int based_rms_fwd(const void *x, int64_t x_sr, const void *residual, i
  *   dsum     (R,C) of s_dtype, row stride dsum_sr: what comes back along the stream, added to ds; or NULL
  *   ds       (R,C) of s_dtype, contiguous: the gradient of the residual (and of x); may be `dsum` where that is contiguous
  *   dx       (R,C) of dtype, contiguous: ds in the type of x; NULL if and only if s_dtype is dtype
- *   dweight  (C) of p_dtype or NULL; summed in float32 in an order that the sizes fix
+ *   dweight  (C) of p_dtype or NULL; summed in float32 in an order that sizes and alignment fix
  *   workspace  based_rms_bwd_workspace_size() bytes (none where dweight is NULL)
  * Errors: as based_rms_fwd, BASED_ERR_WORKSPACE.
  */
@@ -300,7 +305,8 @@ BASED_API size_t based_rms_bwd_workspace_size(int64_t R, int C);
  *                (as a temperature: the first).
  *   tokens       (N) int32
  *   probs        (N) float32 or NULL: the token's share of what its row keeps
- * Probabilities are computed in float32 (to 2^-21) and summed as whole multiples of 2^-40 of the largest: tokens below that have none.
+ * Probabilities are computed in float32 (to 2^-21) and summed as whole multiples of 2^-40 of the largest, eight neighbours at a time: tokens below that
+ * have none. A row's token and probability depend on the row alone, not on the others of the call nor on alignment.
  * V is at most 2^22, N at most 2^26. Errors: as based_scan_fwd.
  */
 BASED_API int based_sample(const void *logits, int64_t stride, int dtype, int N, int V, const float *u,

@@ -1541,7 +1541,9 @@ int launch_delta(DeltaParams &p, bool bwd, int sms, cudaStream_t st) {
     OPS_CUDA(allow(prep, PrepSmem<T, KP>::bytes));
     OPS_CUDA(launch_op(prep, dim3(p.chunks, p.HK, z), 32 * kPrepWarps, PrepSmem<T, KP>::bytes, st, p));
     // A CTA's slices share its records but also its SM: as many as take the least time, which is the rounds of CTAs (those of equal lengths end together)
-    // by what a round takes: 1, 1.29, 1.57 and 2.09 with one to four slices (8 x 4096 rows, 16 heads of 128 x 128: 857, 632, 575 and 511 us).
+    // by what a round takes: 1, 1.29, 1.57 and 2.09 with one to four slices. 8 x 4096 rows, 16 heads, with one, two, three and four: 128 x 128 bf16 forward 935, 674, 602
+    // and 527 us, backward 1132, 816, 723 and 636; f16 1035, 750 and 682 (three fit), 1155, 837 and 746; 64 x 64 bf16 288, 281, 344 and 208, 546, 338, 421 and 253;
+    // 4 x 4096 float32 of 64 x 64 286, 184 and 232, 311, 202 and 258. It takes the fastest of each.
     constexpr double kRound[5] = {0.0, 1.0, 1.29, 1.57, 2.09};
     int per = 1;
     const auto cost = [&](int n) {

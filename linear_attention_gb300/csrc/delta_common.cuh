@@ -2,7 +2,7 @@
 // float16 pairs and the matrix instructions on them.
 //
 // The kernels multiply on tensor cores and keep float32's accuracy. A float32 operand x goes in as two
-// float16 terms, hi = x s and lo = x s - hi with a power of two s that brings the largest |x| of a row or tile
+// float16 terms, hi = x s and lo = x s - hi with a power of two s that brings the largest |x| of what shares it
 // to 2^14: together 22 bits, off by 2^-23 of that largest where bfloat16 pairs would be off by 2^-17. A product
 // of two pairs is three matrix products (lo lo, 2^-22 of the result, is left out); 16-bit inputs are one term.
 // Sums are float32. Per multiprocessor and cycle mma.sync makes 1019 float16 products (measured), a quarter of what
@@ -36,7 +36,9 @@ struct DeltaParams {
 };
 
 // The terms of an operand. Inputs of 16 bits are one float16 term (bfloat16 fits one after its scaling: 8 bits). Results that are
-// rounded to bfloat16 (2^-9) take one term, 2^-12, of what is computed; other outputs, and all that goes into a state, two.
+// rounded to bfloat16 (half a step is 2^-8) take one term, 2^-11, of what is computed; other outputs, and all that goes into a state, two. With two
+// 8 x 4096 rows of 16 heads of 128 x 128 took 3091 us in training where one took 2327, 1 x 16384 forward 638 and 579; off the 64-bit results are
+// 0.166 % with two (the rounding alone) and 0.168 % with one.
 template <typename T>
 struct Terms {
     static constexpr int in = 1, out = 2;

@@ -206,9 +206,11 @@ def based_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, beta: tor
 
     Heads of v share the HK heads of q and k in consecutive groups. ``scale`` defaults to K^-0.5. ``state`` (B,H,K,V)
     float32 is S before the first row (default zero); ``lengths`` (B) int32 marks rows t >= lengths[b] as padding
-    (zero output, state kept). An infinity or NaN leaves a head undefined from its chunk of 64 rows on. Returns (o (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the bytes
-    that based_delta_bwd needs, or None without ``save``). ``final_state`` may be ``state``, to update
-    it in place. ``workspace``: a CUDA byte tensor of at least delta_workspace_size(...) bytes (default: one is allocated).
+    (zero output, state kept). An infinity or NaN leaves a head undefined from its chunk of 64 rows on. Products are as accurate as
+    float32's; with bfloat16 what is in outputs and gradients alone has 11 bits (include/based_ops.h says which). Returns (o
+    (B,T,H,V) in the type of v, the last state (B,H,K,V) float32, the bytes that based_delta_bwd needs, or None without
+    ``save``). ``final_state`` may be ``state``, to update it in place. ``workspace``: a CUDA byte tensor of at
+    least delta_workspace_size(...) bytes (default: one is allocated).
     """
     return _C.delta_fwd(q, k, v, beta, gate, scale, state, lengths, save, out, final_state, workspace, stream)
 

@@ -123,3 +123,26 @@ def test_values_of_heavy_tails(cuda_device, dtype):
     for n in val:
         ref.assert_within(got[n], val[n], bound[n], n)
     near(got, val, dtype, ("o", "dq", "dk", "dv", "dgate"))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_steps_of_many_magnitudes(cuda_device, dtype):
+    """beta from 2^-20 to 2 and of either sign, on values that make what each row writes about as large; and 0."""
+    s, more, do, dfinal = inputs(2, 150, 4, 2, 64, 32, dtype, seed=16)
+    gen = torch.Generator().manual_seed(16)
+    e = -14.0 * torch.rand(2, 150, 4, generator=gen)
+    e = torch.where(torch.rand(2, 150, 4, generator=gen) < 0.3, e, -torch.rand(2, 150, 4, generator=gen))
+    sign = torch.where(torch.rand(2, 150, 4, generator=gen) < 0.1, -1.0, 1.0)
+    s["beta"] = (torch.exp2(e) * sign).to(dtype).cuda()
+    s["beta"][:, 10::40] = 0.0
+    s["beta"][:, 11::40] = 2.0
+    s["v"] = (s["v"].float() / torch.exp2(e)[..., None].cuda()).to(dtype)
+    got, val, bound = run(s, more, do, dfinal)
+    for n in val:
+        ref.assert_within(got[n], val[n], bound[n], n)
+    near(got, val, dtype, ("o", "dq", "dv", "dgate"))
+    if dtype == F32:
+        t = dict(s, beta=torch.where(torch.rand(2, 150, 4, generator=gen).cuda() < 0.2, 2.0 ** -20, s["beta"]))
+        got, val, bound = run(t, more, do, dfinal)
+        for n in val:
+            ref.assert_within(got[n], val[n], bound[n], n)
