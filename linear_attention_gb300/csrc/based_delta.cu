@@ -1024,7 +1024,7 @@ __global__ void __launch_bounds__(512, 1) based_delta_bwd_kernel(DeltaParams p) 
 // with grow_last <S0, G> + sum_i k_i (rest U G^T)_i more at the last row; dgate_i is the sum of db from i on.
 // A CTA takes one chunk of one key head and adds up the value heads that share it, so that nothing is added by atomics. Its eight warps share out
 // the products' results, 16 rows and half of the columns each; the slices' records come in by a ring of stages and are used as they lie. With
-// 16 warps of a quarter of the columns left operands were read twice as often (8 x 4096 rows, 16 heads of 128 x 128: 782 us, now 753; without the
+// 16 warps of a quarter of the columns left operands were read twice as often (8 x 4096 rows, 16 heads of 128 x 128: 782 us, now 756; without the
 // barrier of each slice 797). The pairs' sums N come from the products of queries and keys again, 16 % of a CTA's time: taken from q dq - k dk
 // they would be differences of rounded sums, and where decays are steep dgate would be what that rounding leaves.
 // ------------------------------------------------------------------------------------------------
