@@ -258,7 +258,8 @@ BASED_API int based_delta_step(const void *q, int64_t q_sn, int64_t q_sh, const 
 /*
  * based_rms_fwd: root-mean-square norm of a residual stream, with the addition in front of it:
  *     s = x + residual, rounded to s_dtype (or s = x),   y = s / sqrt(mean(s^2) + eps) * weight,
- * the mean over the C channels of a row. The norm is that of the s that is written.
+ * the mean over the C channels of a row. The norm is that of the s that is written. Squares are summed in float32: a row whose sum passes it
+ * (magnitudes of some 2^60) has an infinite size.
  *   x         (R,C) of dtype, row stride x_sr
  *   residual  (R,C) of s_dtype (dtype or BASED_F32), row stride res_sr, or NULL
  *   weight    (C) of p_dtype (dtype or BASED_F32), or NULL (1)
